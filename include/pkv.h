@@ -299,6 +299,125 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
                                   void *stream);
 
 /*
+ * A cache held in 4 bits
+ * ----------------------
+ * The same paged cache with each K and V row quantised: codes of 4 bits and a
+ * (scale, offset) pair for every group of group_size (32, 64 or 128) dims.
+ *   k_codes, v_codes    uint8 [num_blocks, H_kv, block_size, 64]: byte j of a row
+ *                       holds dim 2j in its low nibble and dim 2j + 1 in its high one
+ *   k_params, v_params  bf16 [num_blocks, H_kv, block_size, 128 / group_size, 2]
+ * A row takes 64 + 512 / group_size bytes (80, 72 or 68) instead of 256. All
+ * four arrays are 16-byte aligned and contiguous. Within a block the rows of a
+ * head are contiguous (not those of a token, as in the bf16 cache), which is how
+ * the decode kernel reads them; slots and block tables mean the same.
+ *
+ * Values. Code n of a group with (scale, offset) stands for
+ *   bf16(scale * (16 + n) + offset),  rounded once, to nearest even.
+ * Attention over the cache is attention over exactly these bf16 values.
+ * Quantisation of a group with smallest value lo and largest value hi, each
+ * operation rounded to the type it is written with:
+ *   scale  = bf16(fp32(hi - lo) * fp32(1/15)), or 0 if that product is below 2^-100
+ *   offset = bf16(lo - 16 scale)
+ *   n      = clamp(floor(fp32(x - offset) / scale + 1/2) - 16, 0, 15), or 0 if scale = 0
+ * A value comes back within half a scale, plus the roundings of the parameters
+ * and of the result. A group that holds a NaN or an infinity, or whose range
+ * makes the offset overflow, gets scale 0 and offset NaN: it reads back as NaN.
+ */
+
+/*
+ * Quantise the new tokens' K/V rows into their slots: pkv_kv_store for a 4-bit
+ * cache, with the same slot_mapping semantics and errors (-1 skips the token;
+ * another value outside the pool is skipped and raises PKV_DEVERR_SLOT; two
+ * tokens with the same slot race).
+ *   k, v  device bf16 [num_tokens, num_kv_heads, 128]
+ */
+pkv_status pkv_kv_store_q4(const void *k, const void *v, void *k_codes, void *k_params,
+                           void *v_codes, void *v_params, const int32_t *slot_mapping,
+                           int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t group_size, int32_t block_size, int64_t num_blocks,
+                           void *stream);
+
+/*
+ * Read rows back as bf16: k[t], v[t] = the values that the rows at slots[t]
+ * stand for. A slot may appear any number of times; the rows of slot -1, and of
+ * a slot outside the pool (which raises PKV_DEVERR_SLOT), become zeros.
+ *   slots device int32 [num_tokens]
+ *   k, v  device bf16 [num_tokens, num_kv_heads, 128], written
+ */
+pkv_status pkv_kv_load_q4(const void *k_codes, const void *k_params, const void *v_codes,
+                          const void *v_params, const int32_t *slots, void *k, void *v,
+                          int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+                          int32_t group_size, int32_t block_size, int64_t num_blocks,
+                          void *stream);
+
+/*
+ * Bytes of device workspace of pkv_paged_decode_attn_q4 (0 on invalid sizes or
+ * without a device). with_scores != 0: for calls with key_scores, which keep the
+ * logits of the call there (4 bytes per key and query head). A workspace serves
+ * every call with sizes no larger than these; it needs no initialisation; calls
+ * that share one must be ordered (same stream, or graphs that never overlap).
+ */
+size_t pkv_decode_q4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                    int32_t head_dim, int32_t max_context_len,
+                                    int32_t with_scores);
+
+/*
+ * pkv_paged_decode_attn over a 4-bit cache. Arguments, result, sliding window
+ * and device errors are that call's, except:
+ *   - H_q / H_kv may be 1, 2, 4 or 8, and num_seqs at most 65535;
+ *   - an invalid table entry raises PKV_DEVERR_BLOCK and its keys are left out;
+ *   - no wait inside the kernels can run out, so the call takes no notice of
+ *     PKV_DEVERR_TIMEOUT (like pkv_kv_store);
+ *   - key_scores, if not NULL, accumulates the attention weights:
+ *       key_scores[s * score_stride + p] += sum over query heads h of
+ *                                           exp(z_hp - lse[s, h])
+ *     for every key p that sequence s attended to (those in its window, if
+ *     any); other entries keep their values. float32, score_stride >=
+ *     max_context_len. The caller sets a sequence's row to zero when it admits
+ *     the sequence. The heads are summed in order: the same inputs give the
+ *     same bits.
+ */
+pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const void *k_params,
+                                    const void *v_codes, const void *v_params,
+                                    const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                    const int32_t *context_lens, int32_t max_context_len,
+                                    int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                    int32_t head_dim, int32_t group_size, int32_t block_size,
+                                    int64_t num_blocks, float scale, int32_t sliding_window,
+                                    void *out, float *lse, float *key_scores,
+                                    int64_t score_stride, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of device workspace of pkv_paged_prefill_attn_q4 (0 on invalid sizes):
+ * the call widens the batch's keys to bf16 there, 512 * num_kv_heads bytes per
+ * key, and up to 128 keys more per sequence. Conditions as above.
+ */
+size_t pkv_prefill_q4_workspace_size(int32_t num_seqs, int32_t total_k, int32_t max_seqlen_k,
+                                     int32_t num_kv_heads, int32_t head_dim);
+
+/*
+ * pkv_paged_prefill_attn over a 4-bit cache: the new tokens attend to the
+ * quantised values of the cached prefix and of themselves (store them first).
+ * Arguments, result, sliding window, errors and the skip after a timeout are
+ * that call's, except:
+ *   total_k    host int: an upper bound of cu_seqlens_k[num_seqs]; a segment
+ *              that ends past it raises PKV_DEVERR_SEQLENS and is not written
+ *   workspace  device, >= pkv_prefill_q4_workspace_size(...) bytes
+ * num_seqs is at most 65535.
+ */
+pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const void *k_params,
+                                     const void *v_codes, const void *v_params,
+                                     const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                     const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                     int32_t num_seqs, int32_t total_q, int32_t total_k,
+                                     int32_t max_seqlen_q, int32_t max_seqlen_k,
+                                     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                     int32_t group_size, int32_t block_size, int64_t num_blocks,
+                                     float scale, int32_t sliding_window, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronise `stream`, then return in *flags_out the OR of the device error
  * words of every kernel of this library on the current device, and clear
  * them. It blocks the host; it is also the only way to clear the words, and

@@ -16,8 +16,10 @@ Tensors (all CUDA, contiguous):
     context_lens   int32 [S]
     cu_seqlens_q/k int32 [S + 1]
 """
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -89,6 +91,22 @@ def lib():
     L.pkv_paged_prefill_attn.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32,
                                          i32, i32, i64, f32, i32, P, P, P, sz, P]
     L.pkv_paged_prefill_attn.restype = ctypes.c_int
+    q4 = [P, P, P, P]  # k_codes, k_params, v_codes, v_params
+    L.pkv_kv_store_q4.argtypes = [P, P] + q4 + [P, i32, i32, i32, i32, i32, i64, P]
+    L.pkv_kv_store_q4.restype = ctypes.c_int
+    L.pkv_kv_load_q4.argtypes = q4 + [P, P, P, i32, i32, i32, i32, i32, i64, P]
+    L.pkv_kv_load_q4.restype = ctypes.c_int
+    L.pkv_decode_q4_workspace_size.argtypes = [i32] * 6
+    L.pkv_decode_q4_workspace_size.restype = sz
+    L.pkv_paged_decode_attn_q4.argtypes = [P] + q4 + [P, i32, P, i32, i32, i32, i32, i32, i32, i32,
+                                                      i64, f32, i32, P, P, P, i64, P, sz, P]
+    L.pkv_paged_decode_attn_q4.restype = ctypes.c_int
+    L.pkv_prefill_q4_workspace_size.argtypes = [i32] * 5
+    L.pkv_prefill_q4_workspace_size.restype = sz
+    L.pkv_paged_prefill_attn_q4.argtypes = [P] + q4 + [P, P, P, i32, i32, i32, i32, i32, i32, i32,
+                                                       i32, i32, i32, i32, i64, f32, i32, P, P, P,
+                                                       sz, P]
+    L.pkv_paged_prefill_attn_q4.restype = ctypes.c_int
     L.pkv_check_device_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     L.pkv_check_device_errors.restype = ctypes.c_int
     L.pkv_read_device_errors_async.argtypes = [P, P]
@@ -329,6 +347,199 @@ def paged_prefill_attn(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_ta
         H_q, H_kv, D, bs, NB, float(scale), int(sliding_window), _ptr(out), _ptr(lse),
         _ptr(workspace), workspace.numel() if workspace is not None else 0, _stream(stream)),
         "pkv_paged_prefill_attn")
+    return out, lse
+
+
+class Q4Cache(NamedTuple):
+    """K or V of a paged cache held in 4 bits (pkv.h, "A cache held in 4 bits").
+    The calls also take a plain (codes, params) pair."""
+    codes: torch.Tensor   # uint8 [num_blocks, H_kv, block_size, 64]
+    params: torch.Tensor  # bf16 [num_blocks, H_kv, block_size, 128 / group_size, 2]
+
+
+def new_q4_cache(num_blocks, block_size, num_kv_heads, group_size=32, device="cuda") -> Q4Cache:
+    """A 4-bit K or V cache whose rows read back as zeros."""
+    if group_size not in (32, 64, 128):
+        raise ValueError("group_size must be 32, 64 or 128")
+    head = (num_blocks, num_kv_heads, block_size)
+    return Q4Cache(torch.zeros(*head, 64, dtype=torch.uint8, device=device),
+                   torch.zeros(*head, 128 // group_size, 2, dtype=torch.bfloat16, device=device))
+
+
+def _need_current_device(*tensors):
+    """All tensors (None allowed) on the current device, where the library launches."""
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != current:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
+
+
+def _on(stream):
+    """Allocate for work on `stream` (None: the current one): memory that is freed
+    when a call returns is then reused in that stream's order only."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _q4(k_cache, v_cache):
+    """Checked (pointers, (num_blocks, block_size, H_kv, group_size)) of a 4-bit K and V cache."""
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(c, tuple) or len(c) != 2:
+            raise TypeError(f"{name} must be a Q4Cache or a (codes, params) pair")
+        _need(c[0], f"{name} codes", torch.uint8, 4)
+        _need(c[1], f"{name} params", torch.bfloat16, 5)
+    codes, params = k_cache
+    NB, H_kv, bs, row = codes.shape
+    groups = params.shape[3]
+    if row != 64 or groups not in (1, 2, 4) or params.shape != (NB, H_kv, bs, groups, 2) \
+            or v_cache[0].shape != codes.shape or v_cache[1].shape != params.shape:
+        raise ValueError("inconsistent shapes of a 4-bit cache")
+    _need_current_device(*k_cache, *v_cache)
+    return tuple(_ptr(t) for t in (*k_cache, *v_cache)), (NB, bs, H_kv, 128 // groups)
+
+
+def kv_store_q4(k, v, k_cache, v_cache, slot_mapping, stream=None):
+    """Quantise k, v [T, H_kv, 128] into the 4-bit caches at slot_mapping (-1: skip)."""
+    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
+    _need(k, "k", torch.bfloat16, 3)
+    _need(v, "v", torch.bfloat16, 3)
+    _need(slot_mapping, "slot_mapping", torch.int32, 1)
+    if k.shape != v.shape or k.shape[1:] != (H_kv, 128) or slot_mapping.shape[0] != k.shape[0]:
+        raise ValueError("inconsistent shapes")
+    _need_current_device(k, v, slot_mapping)
+    _check(lib().pkv_kv_store_q4(_ptr(k), _ptr(v), *ptrs, _ptr(slot_mapping), k.shape[0], H_kv, 128,
+                                 group, bs, NB, _stream(stream)), "pkv_kv_store_q4")
+
+
+def kv_load_q4(k_cache, v_cache, slots, k=None, v=None, stream=None):
+    """The rows at slots [T] as bf16 (k, v) [T, H_kv, 128]; zeros for slot -1."""
+    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
+    _need(slots, "slots", torch.int32, 1)
+    shape = (slots.shape[0], H_kv, 128)
+    with _on(stream):
+        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device) if v is None else v
+    _need(k, "k", torch.bfloat16, 3)
+    _need(v, "v", torch.bfloat16, 3)
+    if k.shape != shape or v.shape != shape:
+        raise ValueError("inconsistent shapes")
+    _need_current_device(slots, k, v)
+    _check(lib().pkv_kv_load_q4(*ptrs, _ptr(slots), _ptr(k), _ptr(v), shape[0], H_kv, 128, group, bs,
+                                NB, _stream(stream)), "pkv_kv_load_q4")
+    return k, v
+
+
+def q4_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context_len,
+                             with_scores=False) -> int:
+    """Workspace bytes of paged_decode_attn_q4 on the current device (0: invalid sizes)."""
+    return int(lib().pkv_decode_q4_workspace_size(num_seqs, num_q_heads, num_kv_heads, 128,
+                                                  max_context_len, 1 if with_scores else 0))
+
+
+def new_q4_decode_workspace(num_seqs, num_q_heads, num_kv_heads, max_context_len, with_scores=False,
+                            device="cuda"):
+    """A workspace of paged_decode_attn_q4 for these sizes on the current device."""
+    need = q4_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context_len, with_scores)
+    if need == 0:
+        raise PkvError(PKV_ERR_CUDA, "pkv_decode_q4_workspace_size")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _decode_inputs(q, block_tables, context_lens, max_context_len, out, lse, with_lse, key_scores):
+    """Checks shared by the decode calls below; returns (out, lse, score row stride)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    S, H_q, D = q.shape
+    if D != 128 or block_tables.shape[0] != S or context_lens.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, 3)
+    if lse is None and with_lse:
+        lse = torch.empty((S, H_q), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+    if out.shape != q.shape or (lse is not None and lse.shape != (S, H_q)):
+        raise ValueError("inconsistent shapes")
+    if key_scores is not None:
+        _need(key_scores, "key_scores", torch.float32, 2)
+        if key_scores.shape[0] != S or key_scores.shape[1] < max_context_len:
+            raise ValueError("key_scores must be [num_seqs, >= max_context_len]")
+    _need_current_device(q, block_tables, context_lens, out, lse, key_scores)
+    return out, lse, key_scores.shape[1] if key_scores is not None else 0
+
+
+def paged_decode_attn_q4(q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
+                         out=None, lse=None, workspace=None, stream=None, with_lse=True,
+                         sliding_window=0, key_scores=None):
+    """q=1 decode attention over a 4-bit cache. key_scores [S, >= max_context_len]
+    (fp32), if given, gains each key's attention weight, summed over the query
+    heads. Returns (out, lse)."""
+    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
+    with _on(stream):
+        out, lse, stride = _decode_inputs(q, block_tables, context_lens, int(max_context_len), out, lse,
+                                          with_lse, key_scores)
+        S, H_q, _ = q.shape
+        if workspace is None:
+            workspace = new_q4_decode_workspace(S, H_q, H_kv, int(max_context_len),
+                                                key_scores is not None, q.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    _need_current_device(workspace)
+    _check(lib().pkv_paged_decode_attn_q4(
+        _ptr(q), *ptrs, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
+        int(max_context_len), S, H_q, H_kv, 128, group, bs, NB, float(scale), int(sliding_window),
+        _ptr(out), _ptr(lse), _ptr(key_scores), stride, _ptr(workspace), workspace.numel(),
+        _stream(stream)), "pkv_paged_decode_attn_q4")
+    return out, lse
+
+
+def q4_prefill_workspace_size(num_seqs, total_k, max_seqlen_k, num_kv_heads) -> int:
+    """Workspace bytes of paged_prefill_attn_q4 (0: invalid sizes)."""
+    return int(lib().pkv_prefill_q4_workspace_size(num_seqs, total_k, max_seqlen_k, num_kv_heads, 128))
+
+
+def new_q4_prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads, device="cuda"):
+    """A workspace of paged_prefill_attn_q4 for these sizes."""
+    need = q4_prefill_workspace_size(num_seqs, total_k, max_seqlen_k, num_kv_heads)
+    if need == 0:
+        raise PkvError(PKV_ERR_INVALID_ARG, "pkv_prefill_q4_workspace_size")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def paged_prefill_attn_q4(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
+                          max_seqlen_q, max_seqlen_k, total_k, scale, out=None, lse=None,
+                          workspace=None, stream=None, with_lse=True, sliding_window=0):
+    """Varlen causal prefill over a 4-bit cache (arguments as paged_prefill_attn;
+    total_k: an upper bound of cu_seqlens_k[-1]). Returns (out, lse)."""
+    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
+    _need(q, "q", torch.bfloat16, 3)
+    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    T, H_q, D = q.shape
+    S = cu_seqlens_q.shape[0] - 1
+    if D != 128 or S < 0 or cu_seqlens_k.shape[0] != S + 1 or block_tables.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    with _on(stream):
+        out = torch.empty_like(q) if out is None else out
+        if lse is None and with_lse:
+            lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
+        if workspace is None and S > 0 and T > 0:
+            workspace = new_q4_prefill_workspace(S, int(total_k), int(max_seqlen_k), H_kv, q.device)
+    _need(out, "out", torch.bfloat16, 3)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, 2)
+    if out.shape != q.shape or (lse is not None and lse.shape != (T, H_q)):
+        raise ValueError("inconsistent shapes")
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, 1)
+    _need_current_device(q, cu_seqlens_q, cu_seqlens_k, block_tables, out, lse, workspace)
+    _check(lib().pkv_paged_prefill_attn_q4(
+        _ptr(q), *ptrs, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(block_tables),
+        block_tables.shape[1], S, T, int(total_k), int(max_seqlen_q), int(max_seqlen_k), H_q, H_kv,
+        128, group, bs, NB, float(scale), int(sliding_window), _ptr(out), _ptr(lse),
+        _ptr(workspace), workspace.numel() if workspace is not None else 0, _stream(stream)),
+        "pkv_paged_prefill_attn_q4")
     return out, lse
 
 

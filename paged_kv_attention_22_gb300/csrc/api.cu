@@ -120,15 +120,15 @@ pkv_status encode_rows_map(CUtensorMap *map, const void *base, int64_t rows, int
   return PKV_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using pkv::align_up;
+using pkv::aligned16;
+using pkv::kLog2e;
 
 std::atomic<int32_t> g_pdl{1};
 
 // Tuning overrides of the decode launch (0 = automatic / default).
 std::atomic<int32_t> g_decode_ctas{0};
 std::atomic<int32_t> g_decode_variant{0};
-
-constexpr float kLog2e = 1.4426950408889634f;
 
 // Sizes shared by the attention calls.
 pkv_status check_attention_shape(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -147,8 +147,6 @@ pkv_status check_attention_shape(int32_t num_q_heads, int32_t num_kv_heads, int3
   if (static_cast<int64_t>(max_blocks) * block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
 }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Decode workspace layout: per-CTA partial (max, sum) [2 grid, HG, G, 2], then
 // partial outputs [2 grid, HG, G, D].
@@ -353,9 +351,10 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
 
 namespace {
 
-// The device error words of the three kernel files on one device.
+// The device error words of the kernel files on one device.
+constexpr int kErrorWords = 5;
 struct ErrorWords {
-  uint32_t *w[3];
+  uint32_t *w[kErrorWords];
 };
 std::mutex g_words_mutex;
 ErrorWords g_words[kMaxDevices];
@@ -373,7 +372,9 @@ pkv_status error_words(ErrorWords *out) {
     ErrorWords w;
     if ((e = pkv::kv_store_error_word(&w.w[0])) != cudaSuccess ||
         (e = pkv::decode_error_word(&w.w[1])) != cudaSuccess ||
-        (e = pkv::prefill_error_word(&w.w[2])) != cudaSuccess)
+        (e = pkv::prefill_error_word(&w.w[2])) != cudaSuccess ||
+        (e = pkv::q4_cache_error_word(&w.w[3])) != cudaSuccess ||
+        (e = pkv::q4_decode_error_word(&w.w[4])) != cudaSuccess)
       return cuda_fail(e, "cudaGetSymbolAddress (device error words)");
     g_words[dev] = w;
     g_words_set[dev] = true;
@@ -393,18 +394,18 @@ cudaError_t launch_one_thread(void (*kernel)(KArgs...), void *stream, Args... ar
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-// One thread: *dst = the OR of the three words (dst may be a mapped host word).
+// One thread: *dst = the OR of the words (dst may be a mapped host word).
 __global__ void read_errors_kernel(ErrorWords w, uint32_t *dst) {
   uint32_t v = 0;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) v |= *reinterpret_cast<volatile uint32_t *>(w.w[i]);
+  for (int i = 0; i < kErrorWords; ++i) v |= *reinterpret_cast<volatile uint32_t *>(w.w[i]);
   *reinterpret_cast<volatile uint32_t *>(dst) = v;
 }
 
-// One thread: OR `bits` into each of the three words.
+// One thread: OR `bits` into each of the words.
 __global__ void raise_errors_kernel(ErrorWords w, uint32_t bits) {
 #pragma unroll
-  for (int i = 0; i < 3; ++i) atomicOr(w.w[i], bits);
+  for (int i = 0; i < kErrorWords; ++i) atomicOr(w.w[i], bits);
 }
 
 }  // namespace
@@ -566,6 +567,18 @@ pkv_status pkv_check_device_errors(void *stream, uint32_t *flags_out) {
     return cuda_fail(e, "decode error word");
   if ((e = pkv::take_prefill_errors(s, flags_out)) != cudaSuccess)
     return cuda_fail(e, "prefill error word");
+  // the words of the files without a taker of their own
+  ErrorWords w;
+  pkv_status st = error_words(&w);
+  if (st != PKV_OK) return st;
+  for (int i = 3; i < kErrorWords; ++i) {
+    uint32_t v = 0;
+    if ((e = cudaMemcpyAsync(&v, w.w[i], sizeof v, cudaMemcpyDeviceToHost, s)) != cudaSuccess ||
+        (e = cudaMemsetAsync(w.w[i], 0, sizeof v, s)) != cudaSuccess ||
+        (e = cudaStreamSynchronize(s)) != cudaSuccess)
+      return cuda_fail(e, "device error word");
+    *flags_out |= v;
+  }
   return PKV_OK;
 }
 

@@ -134,4 +134,60 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
 cudaError_t take_prefill_errors(cudaStream_t stream, uint32_t *flags);
 cudaError_t prefill_error_word(uint32_t **word);
 
+// ---------------------------------------------------------------- 4-bit cache
+struct Q4CacheArgs {
+  void *k_codes, *k_params, *v_codes, *v_params;
+  int32_t num_kv_heads, group_size, block_size;
+  int64_t num_blocks;
+};
+struct Q4RowsArgs {
+  Q4CacheArgs cache;
+  const void *k, *v;      // store: the rows
+  void *k_out, *v_out;    // load: where they go
+  const int32_t *slots;
+  int32_t num_tokens;
+};
+cudaError_t launch_q4_store(const Q4RowsArgs &a, cudaStream_t stream);
+cudaError_t launch_q4_load(const Q4RowsArgs &a, cudaStream_t stream);
+
+constexpr int32_t kQ4PrefillBlock = 128;  // rows of a workspace block: one K/V tile of the prefill kernel
+struct Q4GatherArgs {
+  Q4CacheArgs cache;
+  const int32_t *cu_seqlens_q, *cu_seqlens_k, *block_tables;
+  void *ws_k, *ws_v;
+  int32_t *ws_tables;
+  int32_t max_blocks, ws_max_blocks, num_seqs, max_seqlen_q, max_seqlen_k, total_k;
+  int32_t window, num_sms;
+};
+cudaError_t launch_q4_gather(const Q4GatherArgs &a, cudaStream_t stream);
+cudaError_t q4_cache_error_word(uint32_t **word);
+
+// How a decode call over the 4-bit cache cuts the keys of each (sequence, KV
+// head): n_splits CTAs of split_keys keys (a multiple of 16).
+struct Q4DecodePlan {
+  int32_t n_splits, split_keys;
+};
+struct Q4DecodeArgs {
+  Q4CacheArgs cache;
+  const void *q;
+  const int32_t *block_tables, *context_lens;
+  void *out;
+  float *lse;             // required when key_scores is given
+  float *ws_o, *ws_ml;    // split partials
+  float *logits;          // [S, H_q, logits_ld], with key_scores
+  float *key_scores;      // [S, score_stride] or null
+  int64_t logits_ld, score_stride;
+  int32_t max_blocks, max_context_len, num_seqs, num_q_heads;
+  int32_t window;
+  Q4DecodePlan plan;
+  float scale_log2;
+};
+cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream);
+cudaError_t q4_decode_error_word(uint32_t **word);
+
+// ---------------------------------------------------------------- shared by the C entries
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+constexpr float kLog2e = 1.4426950408889634f;
+
 }  // namespace pkv

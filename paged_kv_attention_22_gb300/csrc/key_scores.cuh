@@ -1,0 +1,51 @@
+// Accumulated attention weights: after a decode call has left its logits
+// z[s, h, p] (base 2, scaled) and lse[s, h] (natural log),
+//   key_scores[s, p] += sum_h 2^(z[s, h, p] - lse[s, h] log2 e)
+// for every key p that sequence s attended to. The sum runs over the heads in
+// order, so the result does not depend on the launch shape.
+#pragma once
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace pkv {
+
+constexpr int kScoreThreads = 256;  // one position each
+constexpr float kScoreLog2e = 1.4426950408889634f;
+
+struct KeyScoresParams {
+  const float *logits;      // [S, H_q, logits_ld]
+  const float *lse;         // [S, H_q]
+  float *key_scores;        // [S, score_stride]
+  const int32_t *context_lens;
+  int64_t logits_ld, score_stride;
+  int32_t max_context_len, num_q_heads, window;
+  int64_t ctx_cap;          // max_blocks * block_size
+};
+
+// Body of the per-file kernels; grid (position chunks, sequences).
+__device__ __forceinline__ void key_scores_body(const KeyScoresParams &p) {
+  const int s = blockIdx.y;
+  const int ctx = p.context_lens[s];
+  if (ctx <= 0 || ctx > p.max_context_len || ctx > p.ctx_cap) return;
+  const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
+  for (int pos = blockIdx.x * kScoreThreads + threadIdx.x; pos < ctx; pos += gridDim.x * kScoreThreads) {
+    if (pos < first) continue;
+    const float *z = p.logits + static_cast<int64_t>(s) * p.num_q_heads * p.logits_ld + pos;
+    const float *lse = p.lse + static_cast<int64_t>(s) * p.num_q_heads;
+    float w = 0.f;
+#pragma unroll 8
+    for (int h = 0; h < p.num_q_heads; ++h)
+      w += fast_exp2(fmaf(-kScoreLog2e, lse[h], z[h * p.logits_ld]));
+    float *dst = p.key_scores + s * p.score_stride + pos;
+    *dst += w;
+  }
+}
+
+// Position chunks of a launch for these sizes.
+inline unsigned key_scores_grid_x(int32_t max_context_len) {
+  const int64_t n = (static_cast<int64_t>(max_context_len) + kScoreThreads - 1) / kScoreThreads;
+  return static_cast<unsigned>(n < 4096 ? n : 4096);
+}
+
+}  // namespace pkv

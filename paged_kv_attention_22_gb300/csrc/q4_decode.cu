@@ -1,0 +1,487 @@
+// Paged decode attention over a cache held in 4 bits, one query token per
+// sequence.
+//
+// The keys of a (sequence, KV head) are cut into splits, one CTA each; the
+// CTA's four warps take the split's units of 16 keys in turn. A unit's codes
+// are 1 KiB of K and 1 KiB of V, contiguous in the cache, and its parameters
+// 64 to 256 bytes of each. Every warp streams its units through a ring of its
+// own with cp.async, so no warp waits for another before the end of the split.
+//
+// The products run on mma.sync m16n8k16 in bf16 with fp32 accumulators. A bf16
+// of the cache's definition is what the codes are widened to, so the logits
+// have exact products, as with a bf16 cache.
+//   S = Q K^T   A = the group's query heads (rows 0..7), B = 16 keys: two n8
+//               tiles. Lane (g, t) = (lane / 4, lane % 4) holds 32 dims of the
+//               keys of column g, 16 bytes of codes each.
+//   O^T += V^T P^T   A = V^T: 16 dims a tile, eight tiles, B = P^T, whose
+//               fragment is S's accumulator fragment packed to bf16: the
+//               probabilities never leave their registers. Lane (g, t) holds
+//               dims 16 g .. 16 g + 15 of four keys, 8 bytes of codes each.
+// Column n of tile j holds key 8 j + 4 (n & 1) + (n >> 1): lane t then needs V
+// rows t, 4 + t, 8 + t and 12 + t, so that four lanes of one load read
+// neighbouring rows (free of bank conflicts with the row swizzle below).
+//
+// P is rounded to bf16 and the output divided by the sum of the rounded
+// probabilities, the weights that the products used; the lse comes from the
+// fp32 sum.
+#include "internal.h"
+#include "key_scores.cuh"
+#include "q4.cuh"
+
+namespace pkv {
+
+static __device__ uint32_t g_q4_decode_errors;
+
+namespace {
+
+constexpr int kD = kQ4D;
+constexpr int kWarps = 4;
+constexpr int kUnit = 16;                    // keys a unit
+constexpr int kStages = 4;                   // units in flight a warp
+constexpr int kMaxG = 8;                     // query heads a KV head (columns of a P^T tile)
+constexpr int kUnitCodes = kUnit * kQ4RowBytes;  // 1 KiB of K or V codes
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kLazyMax = 8.0f;             // log2 units the running max may lag
+
+struct Q4DecodeParams {
+  const __nv_bfloat16 *q;
+  const uint8_t *k_codes, *v_codes, *k_params, *v_params;
+  const int32_t *block_tables, *context_lens;
+  __nv_bfloat16 *out;
+  float *lse;
+  float *ws_o;     // [S, H_kv, n_splits, G, 128] partial outputs
+  float4 *ws_ml;   // [S, H_kv, n_splits, G] (max, sum, sum of the rounded)
+  float *logits;   // [S, H_q, logits_ld] or null
+  int64_t logits_ld;
+  int32_t max_blocks, max_context_len, num_q_heads, num_kv_heads, block_size, num_blocks;
+  int32_t gqa, window, n_splits, split_keys;
+  float scale_log2;
+};
+
+template <int NG>  // parameter groups a row: 4, 2 or 1
+struct Q4DecodeSmem {
+  static constexpr int kParamBytes = kUnit * NG * 4;
+  static constexpr int kStageBytes = 2 * kUnitCodes + 2 * kParamBytes;
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kMergeBytes = kWarps * kMaxG * (kD + 4) * 4;  // O and (m, l, r) of each warp
+  static constexpr int kTotal = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
+  if constexpr (N == 16)
+    cp_async16(dst, src);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// d += a b, bf16 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The keys a sequence attends to: [first, ctx); its units start at the 16-key
+// boundary at or before first. ctx <= 0 marks an invalid length.
+struct KeyRange {
+  int ctx, first, unit0;
+};
+__device__ __forceinline__ KeyRange key_range(const Q4DecodeParams &p, int s) {
+  KeyRange r;
+  r.ctx = p.context_lens[s];
+  if (r.ctx > p.max_context_len || r.ctx > static_cast<int64_t>(p.max_blocks) * p.block_size) r.ctx = 0;
+  r.first = p.window > 0 && r.ctx > p.window ? r.ctx - p.window : 0;
+  r.unit0 = r.first / kUnit * kUnit;
+  return r;
+}
+
+template <int NG>
+__global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4DecodeParams p) {
+  using L = Q4DecodeSmem<NG>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  griddep_wait();  // inputs written by the previous kernel are visible from here on
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int split = blockIdx.x, head = blockIdx.y, s = blockIdx.z;
+  const int G = p.gqa;
+  const KeyRange range = key_range(p, s);
+  if (range.ctx <= 0) {
+    if (split == 0 && head == 0 && threadIdx.x == 0) atomicOr(&g_q4_decode_errors, kErrContext);
+    return;
+  }
+  const int64_t key_begin64 = range.unit0 + static_cast<int64_t>(split) * p.split_keys;
+  if (key_begin64 >= range.ctx) return;  // a split past this sequence's end
+  const int key_begin = static_cast<int>(key_begin64);
+  const int key_end = min(range.ctx - key_begin, p.split_keys) + key_begin;
+  const int n_units = (key_end - key_begin + kUnit - 1) / kUnit;
+  const int n_mine = n_units > warp ? (n_units - warp + kWarps - 1) / kWarps : 0;
+
+  // the query heads as A fragments: k-step 2w (2w + 1) pairs dims i and i + 4,
+  // i = 0, 1 (2, 3), of the lane's w-th code word
+  uint32_t qa[8][2];
+  {
+    const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + head * G + g;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * kD + 32 * t);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint4 x = g < G ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+      qa[2 * w][0] = q4_low_halves(x.x, x.z);
+      qa[2 * w][1] = q4_high_halves(x.x, x.z);
+      qa[2 * w + 1][0] = q4_low_halves(x.y, x.w);
+      qa[2 * w + 1][1] = q4_high_halves(x.y, x.w);
+    }
+  }
+
+  // rows / 16 of this warp's unit i in the codes array, 0xffffffff for an
+  // invalid table entry; a lane holds one unit of a batch of 32
+  const int32_t *table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks;
+  auto entry_of = [&](int i) -> uint32_t {
+    if (i >= n_mine) return 0;
+    const int key = key_begin + (warp + kWarps * i) * kUnit;
+    const int blk = table[key / p.block_size];
+    if (blk < 0 || blk >= p.num_blocks) {
+      atomicOr(&g_q4_decode_errors, kErrBlock);
+      return 0xffffffffu;
+    }
+    return static_cast<uint32_t>(
+        ((static_cast<int64_t>(blk) * p.num_kv_heads + head) * p.block_size + key % p.block_size) / kUnit);
+  };
+  uint32_t batch = entry_of(lane), next_batch = n_mine > 32 ? entry_of(32 + lane) : 0;
+  uint32_t used = batch;  // the batch of the unit being consumed
+
+  const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStageBytes;
+  const uint8_t *ring_ptr = smem + warp * kStages * L::kStageBytes;
+  const int kperm = 4 * (g & 1) + (g >> 1);             // key of column g in tile 0
+  const uint32_t v_swz = (lane & 3) ^ (((lane >> 3) & 1) << 1);  // chunk of the row this lane copies
+  auto issue = [&](int i) {
+    if (i < n_mine) {
+      if (i > 0 && (i & 31) == 0) {
+        batch = next_batch;
+        next_batch = entry_of(i + 32 + lane);
+      }
+      const uint32_t row16 = __shfl_sync(0xffffffffu, batch, i & 31);
+      if (row16 != 0xffffffffu) {
+        const uint32_t st = ring + (i % kStages) * L::kStageBytes;
+        const uint8_t *k = p.k_codes + static_cast<int64_t>(row16) * kUnitCodes;
+        const uint8_t *v = p.v_codes + static_cast<int64_t>(row16) * kUnitCodes;
+        // K: each lane copies the 16 bytes that it will read; V: rows in order,
+        // chunk c of row r at c ^ 2 ((r >> 1) & 1)
+        const int ko = kperm * kQ4RowBytes + t * 16;
+        cp_async16(st + lane * 16, k + ko);
+        cp_async16(st + 512 + lane * 16, k + 512 + ko);
+        const uint32_t vd = st + kUnitCodes + (lane >> 2) * kQ4RowBytes + v_swz * 16;
+        cp_async16(vd, v + lane * 16);
+        cp_async16(vd + 512, v + 512 + lane * 16);
+        // the parameter rows: lanes 0..15 K's, 16..31 V's
+        const uint8_t *pp = (lane < 16 ? p.k_params : p.v_params) +
+                            static_cast<int64_t>(row16) * L::kParamBytes + (lane & 15) * (4 * NG);
+        cp_async_small<4 * NG>(st + 2 * kUnitCodes + lane * (4 * NG), pp);
+      }
+    }
+    cp_async_commit();
+  };
+
+  float acc[8][4];  // O^T: dims 16 g + 2 m (and + 1), heads 2 t and 2 t + 1
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+  float mx = -INFINITY, lsum = 0.f, rsum = 0.f;  // of row (head) g, this lane's keys
+
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+#pragma unroll 1
+  for (int it = 0; it < n_mine; ++it) {
+    cp_async_wait<kStages - 2>();
+    __syncwarp();  // every lane's copies of this unit have landed, and the stage
+                   // that is filled next has been read by every lane
+    if (it > 0 && (it & 31) == 0) used = entry_of(it + lane);
+    const bool dead = __shfl_sync(0xffffffffu, used, it & 31) == 0xffffffffu;
+    issue(it + kStages - 1);
+    if (dead) continue;  // no such block: its keys are left out
+    const uint8_t *st = ring_ptr + (it % kStages) * L::kStageBytes;
+    const uint32_t *kp = reinterpret_cast<const uint32_t *>(st + 2 * kUnitCodes);
+    const uint32_t *vp = kp + kUnit * NG;
+
+    // ---- S = Q K^T
+    float sc[2][4] = {};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint4 kw = *reinterpret_cast<const uint4 *>(st + 512 * j + lane * 16);
+      const uint32_t pw = kp[(8 * j + kperm) * NG + t * NG / 4];
+      const uint32_t s2 = q4_dup_scale(pw), b2 = q4_dup_offset(pw);
+      const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t x[4];
+        q4_pairs(words[w], x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fma_bf16x2(x[i], s2, b2);
+        mma_16816(sc[j], qa[2 * w][0], 0u, qa[2 * w][1], 0u, x[0], x[1]);
+        mma_16816(sc[j], qa[2 * w + 1][0], 0u, qa[2 * w + 1][1], 0u, x[2], x[3]);
+      }
+    }
+
+    // ---- softmax: this lane's keys t, 4 + t, 8 + t, 12 + t of row g
+    const int key0 = key_begin + (warp + kWarps * it) * kUnit;
+    float z[4] = {sc[0][0] * p.scale_log2, sc[0][1] * p.scale_log2, sc[1][0] * p.scale_log2,
+                  sc[1][1] * p.scale_log2};
+    const bool partial = key0 < range.first || key0 + kUnit > key_end;
+    uint32_t pv[4];  // V parameters of those keys
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pv[i] = vp[(4 * i + t) * NG + g * NG / 8];
+    if (p.logits != nullptr && g < G) {  // rows hold whole units: masked keys are written too
+      float *dst = p.logits + (static_cast<int64_t>(s) * p.num_q_heads + head * G + g) * p.logits_ld + key0 + t;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[4 * i] = z[i];
+    }
+    if (partial) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = key0 + 4 * i + t;
+        if (key < range.first || key >= key_end) {
+          z[i] = -INFINITY;
+          pv[i] = 0u;  // the row reads as zeros, whatever its slot holds
+        }
+      }
+    }
+    const float zm = fmaxf(fmax3(z[0], z[1], z[2]), z[3]);
+    if (__any_sync(0xffffffffu, zm > mx + kLazyMax)) {  // always on a first unit
+      float m_new = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 1));
+      m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, 2));
+      m_new = fmaxf(m_new, mx);
+      const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(mx - m_new);
+      mx = m_new;
+      lsum *= alpha;
+      rsum *= alpha;
+      const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t);      // head 2 t
+      const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);  // head 2 t + 1
+#pragma unroll
+      for (int m = 0; m < 8; ++m) {
+        acc[m][0] *= a0;
+        acc[m][1] *= a1;
+        acc[m][2] *= a0;
+        acc[m][3] *= a1;
+      }
+    }
+    float pr[4];
+    const float m_ref = mx == -INFINITY ? 0.f : mx;  // logits of -inf alone have probability 0
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      pr[i] = fast_exp2(z[i] - m_ref);
+      lsum += pr[i];
+    }
+    const uint32_t b0 = pack_bf16x2(pr[0], pr[1]), b1 = pack_bf16x2(pr[2], pr[3]);
+    rsum += (bf16lo(b0) + bf16hi(b0)) + (bf16lo(b1) + bf16hi(b1));
+
+    // ---- O^T += V^T P^T
+    const uint32_t sa = q4_low_halves(pv[0], pv[1]), ba = q4_high_halves(pv[0], pv[1]);
+    const uint32_t sb = q4_low_halves(pv[2], pv[3]), bb = q4_high_halves(pv[2], pv[3]);
+    uint2 vw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 4 * i + t;
+      vw[i] = *reinterpret_cast<const uint2 *>(st + kUnitCodes + row * kQ4RowBytes +
+                                               (((g >> 1) ^ (((row >> 1) & 1) << 1)) * 16) + (g & 1) * 8);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // dims 16 g + 4 j .. + 3
+      const uint32_t w0 = (j & 2) ? vw[0].y : vw[0].x, w1 = (j & 2) ? vw[1].y : vw[1].x;
+      const uint32_t w2 = (j & 2) ? vw[2].y : vw[2].x, w3 = (j & 2) ? vw[3].y : vw[3].x;
+      uint32_t xa[4], xb[4];
+      q4_pairs((j & 1) ? q4_high_halves(w0, w1) : q4_low_halves(w0, w1), xa);
+      q4_pairs((j & 1) ? q4_high_halves(w2, w3) : q4_low_halves(w2, w3), xb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xa[i] = fma_bf16x2(xa[i], sa, ba);
+        xb[i] = fma_bf16x2(xb[i], sb, bb);
+      }
+      mma_16816(acc[2 * j], xa[0], xa[1], xb[0], xb[1], b0, b1);
+      mma_16816(acc[2 * j + 1], xa[2], xa[3], xb[2], xb[3], b0, b1);
+    }
+  }
+
+  // ---- join the four warps
+  lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+  lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+  rsum += __shfl_xor_sync(0xffffffffu, rsum, 1);
+  rsum += __shfl_xor_sync(0xffffffffu, rsum, 2);
+  cp_async_wait<0>();
+  __syncthreads();  // no warp still reads or fills its ring
+  float *so = reinterpret_cast<float *>(smem);                       // [warp][G][128]
+  float4 *sml = reinterpret_cast<float4 *>(so + kWarps * kMaxG * kD);  // [warp][G]
+#pragma unroll
+  for (int m = 0; m < 8; ++m)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      if (2 * t + c < G)
+        *reinterpret_cast<float2 *>(so + (warp * kMaxG + 2 * t + c) * kD + 16 * g + 2 * m) =
+            make_float2(acc[m][c], acc[m][2 + c]);
+  if (t == 0 && g < G) sml[warp * kMaxG + g] = make_float4(mx, lsum, rsum, 0.f);
+  __syncthreads();
+  const bool whole = range.unit0 + static_cast<int64_t>(p.split_keys) >= range.ctx;
+  const int d = threadIdx.x;
+  for (int h = 0; h < G; ++h) {
+    float4 ml[kWarps];
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      ml[w] = sml[w * kMaxG + h];
+      M = fmaxf(M, ml[w].x);
+    }
+    float o = 0.f, l = 0.f, r = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = ml[w].x == -INFINITY ? 0.f : fast_exp2(ml[w].x - M);
+      o = fmaf(so[(w * kMaxG + h) * kD + d], f, o);
+      l = fmaf(ml[w].y, f, l);
+      r = fmaf(ml[w].z, f, r);
+    }
+    const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + head * G + h;
+    if (whole) {
+      p.out[row * kD + d] = __float2bfloat16_rn(o / r);
+      if (d == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kLn2;
+    } else {
+      const int64_t piece = ((static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits + split) * G + h;
+      __stcg(p.ws_o + piece * kD + d, o);
+      if (d == 0) __stcg(p.ws_ml + piece, make_float4(M, l, r, 0.f));
+    }
+  }
+}
+
+// Join the splits of the (sequence, query head)s that have more than one. Four
+// groups of 128 threads, one thread a dim, take the splits in turn.
+constexpr int kMergeGroups = 4;
+
+__global__ void __launch_bounds__(kMergeGroups * kD) q4_merge_kernel(const Q4DecodeParams p) {
+  __shared__ float so[kMergeGroups][kD];
+  __shared__ float sl[kMergeGroups], sr[kMergeGroups];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int hq = blockIdx.x, s = blockIdx.y;
+  const KeyRange range = key_range(p, s);
+  const int n = range.ctx <= 0 ? 0 : (range.ctx - range.unit0 + p.split_keys - 1) / p.split_keys;
+  if (n <= 1) return;  // invalid, or written whole
+  const int G = p.gqa, head = hq / G, h = hq % G;
+  const int64_t piece0 = (static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits * G + h;
+  const int d = threadIdx.x % kD, grp = threadIdx.x / kD;
+  float M = -INFINITY;
+  for (int i = 0; i < n; ++i) M = fmaxf(M, p.ws_ml[piece0 + static_cast<int64_t>(i) * G].x);
+  float o = 0.f, l = 0.f, r = 0.f;
+#pragma unroll 4
+  for (int i = grp; i < n; i += kMergeGroups) {
+    const int64_t piece = piece0 + static_cast<int64_t>(i) * G;
+    const float4 ml = p.ws_ml[piece];
+    const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
+    o = fmaf(p.ws_o[piece * kD + d], f, o);
+    l = fmaf(ml.y, f, l);
+    r = fmaf(ml.z, f, r);
+  }
+  so[grp][d] = o;
+  if (d == 0) {
+    sl[grp] = l;
+    sr[grp] = r;
+  }
+  __syncthreads();
+  if (grp != 0) return;
+#pragma unroll
+  for (int i = 1; i < kMergeGroups; ++i) {
+    o += so[i][d];
+    l += sl[i];
+    r += sr[i];
+  }
+  const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + hq;
+  p.out[row * kD + d] = __float2bfloat16_rn(o / r);
+  if (d == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kLn2;
+}
+
+__global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScoresParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  key_scores_body(p);
+}
+
+template <int NG>
+cudaError_t launch_splits(const Q4DecodeParams &p, int32_t num_seqs, cudaStream_t stream) {
+  constexpr int kSmem = Q4DecodeSmem<NG>::kTotal;
+  cudaError_t e =
+      cudaFuncSetAttribute(q4_decode_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(q4_decode_kernel<NG>, dim3(p.n_splits, p.num_kv_heads, num_seqs), dim3(kWarps * 32),
+                    kSmem, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
+  Q4DecodeParams p;
+  p.q = static_cast<const __nv_bfloat16 *>(a.q);
+  p.k_codes = static_cast<const uint8_t *>(a.cache.k_codes);
+  p.v_codes = static_cast<const uint8_t *>(a.cache.v_codes);
+  p.k_params = static_cast<const uint8_t *>(a.cache.k_params);
+  p.v_params = static_cast<const uint8_t *>(a.cache.v_params);
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.out = static_cast<__nv_bfloat16 *>(a.out);
+  p.lse = a.lse;
+  p.ws_o = a.ws_o;
+  p.ws_ml = reinterpret_cast<float4 *>(a.ws_ml);
+  p.logits = a.key_scores != nullptr ? a.logits : nullptr;
+  p.logits_ld = a.logits_ld;
+  p.max_blocks = a.max_blocks;
+  p.max_context_len = a.max_context_len;
+  p.num_q_heads = a.num_q_heads;
+  p.num_kv_heads = a.cache.num_kv_heads;
+  p.block_size = a.cache.block_size;
+  p.num_blocks = static_cast<int32_t>(a.cache.num_blocks);
+  p.gqa = a.num_q_heads / a.cache.num_kv_heads;
+  p.window = a.window;
+  p.n_splits = a.plan.n_splits;
+  p.split_keys = a.plan.split_keys;
+  p.scale_log2 = a.scale_log2;
+  cudaError_t e;
+  switch (a.cache.group_size) {
+    case 32: e = launch_splits<4>(p, a.num_seqs, stream); break;
+    case 64: e = launch_splits<2>(p, a.num_seqs, stream); break;
+    case 128: e = launch_splits<1>(p, a.num_seqs, stream); break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e != cudaSuccess) return e;
+  if (p.n_splits > 1) {
+    e = launch_pdl(q4_merge_kernel, dim3(p.num_q_heads, a.num_seqs), dim3(kMergeGroups * kD), 0, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.key_scores == nullptr) return cudaSuccess;
+  KeyScoresParams k;
+  k.logits = a.logits;
+  k.lse = a.lse;
+  k.key_scores = a.key_scores;
+  k.context_lens = a.context_lens;
+  k.logits_ld = a.logits_ld;
+  k.score_stride = a.score_stride;
+  k.max_context_len = a.max_context_len;
+  k.num_q_heads = a.num_q_heads;
+  k.window = a.window;
+  k.ctx_cap = static_cast<int64_t>(a.max_blocks) * a.cache.block_size;
+  return launch_pdl(q4_scores_kernel, dim3(key_scores_grid_x(a.max_context_len), a.num_seqs),
+                    dim3(kScoreThreads), 0, stream, k);
+}
+
+cudaError_t q4_decode_error_word(uint32_t **word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void **>(word), g_q4_decode_errors);
+}
+
+}  // namespace pkv

@@ -1,0 +1,473 @@
+"""The 4-bit cache: quantising store, read-back, decode and prefill, against the
+plain 64-bit implementation in q4_plain.py; and the refusals of each call."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import paged_kv_attention_22_gb300 as pkv
+import q4_plain as Q
+from paged_kv_attention_22_gb300 import build as pkv_build
+
+SCALE = 1.0 / math.sqrt(128)
+
+
+@pytest.fixture(scope="module")
+def L():
+    pkv_build.build()
+    return pkv.lib()
+
+
+# ------------------------------------------------------------------ CPU: the plain form and refusals
+
+def test_plain_values_are_within_half_a_scale():
+    g = torch.Generator().manual_seed(1)
+    for group in (32, 64, 128):
+        x = (torch.randn(500, 128, generator=g) * torch.exp(3 * torch.randn(500, 1, generator=g))
+             + torch.randn(500, 1, generator=g)).to(torch.bfloat16)
+        codes, params = Q.quantise(x, group)
+        back = Q.values(codes, params)
+        s = params[..., 0].double().repeat_interleave(group, -1)
+        b = params[..., 1].double().repeat_interleave(group, -1)
+        # half a scale; the scale's rounding moves the top code by 15 U16 s, the
+        # offset's the whole grid by U16 |offset|, both only where codes clamp;
+        # the result is rounded once
+        tol = 0.5 * s + 15 * Q.U16 * s + Q.U16 * b.abs() + Q.U16 * back.abs()
+        assert bool(((back - x.double()).abs() <= tol * (1 + 1e-6)).all())
+
+
+FAKE = 0x10000
+
+
+def _store(L, **kw):
+    a = dict(k=FAKE, v=FAKE, kc=FAKE, kp=FAKE, vc=FAKE, vp=FAKE, sm=FAKE, T=4, H=8, D=128, gs=32, bs=16, NB=64)
+    a.update(kw)
+    return L.pkv_kv_store_q4(a["k"], a["v"], a["kc"], a["kp"], a["vc"], a["vp"], a["sm"], a["T"], a["H"], a["D"],
+                             a["gs"], a["bs"], a["NB"], None)
+
+
+def _load(L, **kw):
+    a = dict(k=FAKE, v=FAKE, kc=FAKE, kp=FAKE, vc=FAKE, vp=FAKE, sm=FAKE, T=4, H=8, D=128, gs=32, bs=16, NB=64)
+    a.update(kw)
+    return L.pkv_kv_load_q4(a["kc"], a["kp"], a["vc"], a["vp"], a["sm"], a["k"], a["v"], a["T"], a["H"], a["D"],
+                            a["gs"], a["bs"], a["NB"], None)
+
+
+@pytest.mark.parametrize("call", [_store, _load])
+def test_row_calls_refuse(L, call):
+    for null in ("k", "v", "kc", "kp", "vc", "vp", "sm"):
+        assert call(L, **{null: None}) == pkv.PKV_ERR_INVALID_ARG
+    for odd in ("k", "v", "kc", "kp", "vc", "vp"):
+        assert call(L, **{odd: FAKE + 8}) == pkv.PKV_ERR_INVALID_ARG
+    assert call(L, T=-1) == pkv.PKV_ERR_INVALID_ARG
+    assert call(L, NB=0) == pkv.PKV_ERR_INVALID_ARG
+    assert call(L, D=64) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(L, gs=16) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(L, NB=1 << 40) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(L, T=0, k=None, v=None, sm=None) == pkv.PKV_OK
+
+
+def _decode(L, **kw):
+    a = dict(q=FAKE, kc=FAKE, kp=FAKE, vc=FAKE, vp=FAKE, bt=FAKE, mb=4, cl=FAKE, mcl=64, S=2, Hq=16, Hkv=8, D=128,
+             gs=32, bs=16, NB=64, scale=0.088, win=0, out=FAKE, lse=None, ks=None, ld=0, ws=FAKE, wsb=1 << 30)
+    a.update(kw)
+    return L.pkv_paged_decode_attn_q4(a["q"], a["kc"], a["kp"], a["vc"], a["vp"], a["bt"], a["mb"], a["cl"], a["mcl"],
+                                      a["S"], a["Hq"], a["Hkv"], a["D"], a["gs"], a["bs"], a["NB"], a["scale"],
+                                      a["win"], a["out"], a["lse"], a["ks"], a["ld"], a["ws"], a["wsb"], None)
+
+
+def test_decode_refuses(L):
+    for null in ("q", "kc", "kp", "vc", "vp", "bt", "cl", "out"):
+        assert _decode(L, **{null: None}) == pkv.PKV_ERR_INVALID_ARG
+    for odd in ("q", "kc", "kp", "vc", "vp", "out", "ws"):
+        assert _decode(L, **{odd: FAKE + 8}) == pkv.PKV_ERR_INVALID_ARG
+    assert _decode(L, S=0) == pkv.PKV_ERR_INVALID_ARG
+    assert _decode(L, mcl=0) == pkv.PKV_ERR_INVALID_ARG
+    assert _decode(L, scale=float("inf")) == pkv.PKV_ERR_INVALID_ARG
+    assert _decode(L, win=-1) == pkv.PKV_ERR_INVALID_ARG
+    assert _decode(L, ks=FAKE, ld=63) == pkv.PKV_ERR_INVALID_ARG
+    assert _decode(L, ws=None) == pkv.PKV_ERR_WORKSPACE_TOO_SMALL
+    assert _decode(L, D=64) == pkv.PKV_ERR_UNSUPPORTED
+    assert _decode(L, gs=48) == pkv.PKV_ERR_UNSUPPORTED
+    assert _decode(L, bs=24) == pkv.PKV_ERR_UNSUPPORTED
+    assert _decode(L, Hq=24) == pkv.PKV_ERR_UNSUPPORTED      # 3 query heads a KV head
+    assert _decode(L, Hq=128) == pkv.PKV_ERR_UNSUPPORTED     # 16
+    assert _decode(L, Hq=12) == pkv.PKV_ERR_UNSUPPORTED
+    assert _decode(L, S=65536) == pkv.PKV_ERR_UNSUPPORTED
+    assert _decode(L, NB=1 << 40) == pkv.PKV_ERR_UNSUPPORTED
+    assert L.pkv_decode_q4_workspace_size(0, 16, 8, 128, 64, 0) == 0
+    assert L.pkv_decode_q4_workspace_size(2, 12, 8, 128, 64, 0) == 0
+    assert L.pkv_decode_q4_workspace_size(2, 16, 8, 64, 64, 0) == 0
+
+
+def test_prefill_refuses(L):
+    def call(**kw):
+        a = dict(q=FAKE, kc=FAKE, kp=FAKE, vc=FAKE, vp=FAKE, cq=FAKE, ck=FAKE, bt=FAKE, mb=4, S=2, T=100, TK=128,
+                 mq=64, mk=64, Hq=16, Hkv=8, D=128, gs=32, bs=16, NB=64, scale=0.088, win=0, out=FAKE, ws=FAKE,
+                 wsb=1 << 30)
+        a.update(kw)
+        return L.pkv_paged_prefill_attn_q4(a["q"], a["kc"], a["kp"], a["vc"], a["vp"], a["cq"], a["ck"], a["bt"],
+                                           a["mb"], a["S"], a["T"], a["TK"], a["mq"], a["mk"], a["Hq"], a["Hkv"],
+                                           a["D"], a["gs"], a["bs"], a["NB"], a["scale"], a["win"], a["out"], None,
+                                           a["ws"], a["wsb"], None)
+    for null in ("q", "kc", "kp", "vc", "vp", "cq", "ck", "bt", "out"):
+        assert call(**{null: None}) == pkv.PKV_ERR_INVALID_ARG
+    for odd in ("q", "kc", "kp", "vc", "vp", "out", "ws"):
+        assert call(**{odd: FAKE + 8}) == pkv.PKV_ERR_INVALID_ARG
+    assert call(mq=65) == pkv.PKV_ERR_INVALID_ARG
+    assert call(TK=-1) == pkv.PKV_ERR_INVALID_ARG
+    assert call(win=-1) == pkv.PKV_ERR_INVALID_ARG
+    assert call(Hq=64) == pkv.PKV_ERR_UNSUPPORTED            # 8 query heads a KV head
+    assert call(S=65536) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(TK=2 ** 31 - 1, S=65535) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(wsb=1 << 10) == pkv.PKV_ERR_WORKSPACE_TOO_SMALL
+    assert call(ws=None) == pkv.PKV_ERR_WORKSPACE_TOO_SMALL
+    assert call(T=0, q=None, out=None) == pkv.PKV_OK
+    assert call(S=0) == pkv.PKV_OK
+    assert L.pkv_prefill_q4_workspace_size(2, 128, 64, 8, 64) == 0
+    need = L.pkv_prefill_q4_workspace_size(2, 128, 64, 8, 128)
+    assert need >= 128 * 512 * 8
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="only meaningful without a GPU")
+def test_valid_calls_without_gpu_report_cuda_errors(L):
+    assert _decode(L) == pkv.PKV_ERR_CUDA
+    assert _store(L) == pkv.PKV_ERR_CUDA
+
+
+def test_binding_refuses_shapes_and_types():
+    k = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    sm = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        pkv.kv_store_q4(k, k, k, k, sm)                                  # not a pair
+    with pytest.raises(ValueError):
+        pkv.kv_store_q4(k, k, pkv.new_q4_cache(1, 16, 1, device="cpu"),  # CPU tensors
+                        pkv.new_q4_cache(1, 16, 1, device="cpu"), sm)
+    with pytest.raises(ValueError):
+        pkv.new_q4_cache(1, 16, 1, group_size=16, device="cpu")
+
+
+# ------------------------------------------------------------------ GPU: rows
+
+gpu = pytest.mark.gpu
+
+
+def _special_rows(heads):
+    """Rows where quantisation can go wrong."""
+    g = torch.Generator().manual_seed(9)
+    base = torch.randn(heads, 128, generator=g)
+    rows = [base, torch.zeros(heads, 128), -torch.zeros(heads, 128), torch.full((heads, 128), 3.25),
+            base * 1e-30, base * 2.0 ** -110, base * 1e30, base * 1e37, base + 1000.0,
+            torch.linspace(-7.5, 7.5, 128).expand(heads, 128),     # many exact halves of a scale of 1
+            torch.arange(128).float().expand(heads, 128) % 16 - 8,
+            torch.where(torch.arange(128) == 5, 100.0, 1e-3).expand(heads, 128)]
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        x = base.clone()
+        x[:, 70] = bad
+        rows.append(x)
+    x = base.clone()
+    x[:, 0], x[:, 1] = 3e38, -3e38
+    rows.append(x)
+    return torch.stack(rows).to(torch.bfloat16)
+
+
+def _as_bits(t):
+    return t.view(torch.uint8) if t.dtype == torch.uint8 else t.contiguous().view(torch.int16)
+
+
+@gpu
+@pytest.mark.parametrize("tokens,heads,block,group", [(1, 1, 16, 32), (16, 8, 16, 32), (333, 3, 48, 64), (1000, 8, 256, 128),
+                                                      (77, 1, 7, 32), (129, 2, 16, 128)])
+def test_store_and_load_are_exact(L, tokens, heads, block, group):
+    g = torch.Generator().manual_seed(tokens)
+    special = _special_rows(heads)
+    k = torch.randn(tokens, heads, 128, generator=g).to(torch.bfloat16)
+    k[:min(tokens, len(special))] = special[:tokens]
+    v = (torch.randn(tokens, heads, 128, generator=g) * 4 + 1).to(torch.bfloat16)
+    v[-min(tokens, len(special)):] = special[-tokens:]
+    blocks = -(-tokens // block) + 2
+    slots = torch.randperm(blocks * block, generator=g)[:tokens].to(torch.int32)
+    skipped = torch.arange(tokens) % 5 == 3
+    slots[skipped] = -1
+    caches, plain = [], []
+    for x in (k, v):
+        codes = torch.full((blocks, heads, block, 64), 0xA5, dtype=torch.uint8)
+        params = torch.full((blocks, heads, block, 128 // group, 2), 7.0, dtype=torch.bfloat16)
+        caches.append(pkv.Q4Cache(codes.cuda(), params.cuda()))
+        c, p = Q.quantise(x, group)
+        for t in range(tokens):
+            if slots[t] >= 0:
+                b, o = divmod(int(slots[t]), block)
+                codes[b, :, o], params[b, :, o] = c[t], p[t]
+        plain.append((codes, params))
+    pkv.kv_store_q4(k.cuda(), v.cuda(), *caches, slots.cuda())
+    back = pkv.kv_load_q4(*caches, slots.cuda())
+    assert pkv.check_device_errors() == 0
+    for cache, (codes, params), x, got in zip(caches, plain, (k, v), back):
+        assert torch.equal(cache.codes.cpu(), codes)
+        nan = torch.isnan(params.float())
+        assert torch.equal(torch.isnan(cache.params.cpu().float()), nan)
+        assert torch.equal(_as_bits(cache.params.cpu())[~nan], _as_bits(params)[~nan])
+        want = Q.values(*Q.quantise(x, group))
+        want[skipped] = 0.0
+        assert torch.equal(got.cpu().double().nan_to_num(nan=123.0), want.nan_to_num(nan=123.0))
+
+
+@gpu
+def test_row_calls_report_bad_slots_and_touch_nothing_else(L):
+    heads, block = 2, 16
+    kc, vc = pkv.new_q4_cache(4, block, heads), pkv.new_q4_cache(4, block, heads)
+    k = torch.randn(4, heads, 128).to(torch.bfloat16).cuda()
+    slots = torch.tensor([64, 5, -2, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    pkv.kv_store_q4(k, k, kc, vc, slots)
+    assert pkv.check_device_errors() == pkv.DEVERR_SLOT
+    assert int((kc.codes != 0).any(-1).sum()) == heads      # slot 5 alone
+    back, _ = pkv.kv_load_q4(kc, vc, slots)
+    assert pkv.check_device_errors() == pkv.DEVERR_SLOT
+    assert bool((back[[0, 2, 3]] == 0).all()) and bool((back[1] != 0).any())
+    # the same slot any number of times; no tokens at all
+    many, _ = pkv.kv_load_q4(kc, vc, torch.full((37,), 5, dtype=torch.int32, device="cuda"))
+    assert torch.equal(many, back[1:2].expand(37, -1, -1))
+    none, _ = pkv.kv_load_q4(kc, vc, slots[:0])
+    assert none.shape == (0, heads, 128) and pkv.check_device_errors() == 0
+
+
+# ------------------------------------------------------------------ GPU: decode
+
+def _decode_plain(c, q, gqa, window, scale=SCALE):
+    out, lse = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape[:2], dtype=torch.float64)
+    tol_o, tol_l = torch.zeros_like(out), torch.zeros_like(lse)
+    weights = torch.zeros(len(c.lens), max(c.lens), dtype=torch.float64)
+    tol_w = torch.zeros_like(weights)
+    for s, n in enumerate(c.lens):
+        first = max(0, n - window) if window else 0
+        for h in range(c.heads):
+            k, v = c.logical(c.k, s, n, h), c.logical(c.v, s, n, h)
+            rows = slice(h * gqa, (h + 1) * gqa)
+            o, l, w, wv, qk = Q.attend(q[s, rows].double(), k, v, scale, [first] * gqa, [n - 1] * gqa)
+            out[s, rows], lse[s, rows] = o, l
+            tol_o[s, rows] = Q.out_tolerance(o, wv)
+            tol_l[s, rows] = Q.lse_tolerance(l, qk, n / 4)
+            weights[s, :n] += w.sum(0)
+            # a weight is exp(z - lse): both are off by at most the lse's tolerance
+            tol_w[s, :n] += (w * 2 * tol_l[s, rows, None]).sum(0) + 2.0 ** -20 * w.sum(0)
+    return out, lse, tol_o, tol_l, weights, tol_w
+
+
+DECODE = [  # lens, heads, gqa, block, group, window
+    ([1], 1, 1, 16, 32, 0),
+    ([17, 64, 100, 128], 8, 2, 16, 32, 0),
+    ([1, 2, 15, 16, 17, 31, 33, 255], 2, 4, 48, 64, 0),
+    ([640] * 3, 8, 2, 256, 32, 0),
+    ([700, 3, 129, 1024], 4, 8, 64, 128, 0),
+    ([5000], 1, 2, 256, 32, 0),
+    ([2500, 1, 4097], 2, 1, 32, 64, 0),
+    ([9000, 40], 1, 4, 128, 128, 0),
+    ([17, 64, 100, 128], 3, 2, 16, 32, 1),
+    ([300, 5, 1000, 641], 2, 4, 64, 64, 100),
+    ([3000, 10], 2, 2, 16, 128, 1025),
+    ([500, 64], 1, 8, 32, 32, 4096),
+]
+
+
+@gpu
+@pytest.mark.parametrize("lens,heads,gqa,block,group,window", DECODE)
+@pytest.mark.parametrize("scored", [False, True])
+def test_decode(L, lens, heads, gqa, block, group, window, scored):
+    c = Q.Cache(sum(lens) + group, lens, heads, block, group, outliers=0.05)
+    g = torch.Generator().manual_seed(len(lens))
+    q = torch.randn(len(lens), heads * gqa, 128, generator=g).to(torch.bfloat16)
+    out, lse, tol_o, tol_l, weights, tol_w = _decode_plain(c, q, gqa, window)
+    kc, vc, bt = c.cuda()
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    scores = None
+    if scored:
+        scores = torch.full((len(lens), max(lens) + 5), 0.5, device="cuda")
+    o, l = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt, cl, max(lens), SCALE, sliding_window=window, key_scores=scores)
+    assert pkv.check_device_errors() == 0
+    assert bool(((o.cpu().double() - out).abs() <= tol_o).all()), float(((o.cpu().double() - out).abs() / tol_o).max())
+    assert bool(((l.cpu().double() - lse).abs() <= tol_l).all()), float(((l.cpu().double() - lse).abs() / tol_l).max())
+    if scored:
+        got = scores.cpu().double()
+        assert bool((got[:, max(lens):] == 0.5).all())
+        # untouched entries keep their bits; 0.5 + w rounds once
+        untouched = weights == 0
+        got = got[:, :max(lens)]
+        for s, n in enumerate(lens):
+            first = max(0, n - window) if window else 0
+            assert bool((got[s, n:] == 0.5).all()) and bool((got[s, :first] == 0.5).all())
+        tol = tol_w + Q.U32 * (0.5 + weights) + 1e-30
+        assert bool(((got - 0.5 - weights).abs() <= tol).all()), float(((got - 0.5 - weights).abs() / tol).max())
+        assert bool((got[untouched] == 0.5).all())
+
+
+@gpu
+def test_decode_skips_invalid_rows_and_reports_them(L):
+    lens = [40, 40, 40, 40]
+    c = Q.Cache(5, lens, 2, 16, 32)
+    q = torch.randn(4, 4, 128).to(torch.bfloat16)
+    out, _, tol_o, _, _, _ = _decode_plain(c, q, 2, 0)
+    kc, vc, bt = c.cuda()
+    o = torch.full_like(q, 9.0).cuda()
+    lse = torch.full((4, 4), 9.0, device="cuda")
+    cl = torch.tensor([40, 0, 41, 40], dtype=torch.int32, device="cuda")
+    scores = torch.zeros(4, 40, device="cuda")
+    pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt, cl, 40, SCALE, out=o, lse=lse, key_scores=scores)
+    assert pkv.check_device_errors() == pkv.DEVERR_CONTEXT
+    assert bool((o[1:3] == 9.0).all()) and bool((lse[1:3] == 9.0).all()) and bool((scores[1:3] == 0).all())
+    ok = [0, 3]
+    assert bool(((o[ok].cpu().double() - out[ok]).abs() <= tol_o[ok]).all())
+    # a bad table entry raises its bit and disturbs no other row
+    for bad in (-1, c.num_blocks, 2 ** 31 - 1):
+        bt2 = bt.clone()
+        bt2[1, 1] = bad
+        o, _ = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt2, torch.full_like(cl, 40), 40, SCALE)
+        assert pkv.check_device_errors() == pkv.DEVERR_BLOCK
+        ok = [0, 2, 3]
+        assert bool(((o[ok].cpu().double() - out[ok]).abs() <= tol_o[ok]).all())
+
+
+@gpu
+def test_decode_nan_group_reaches_its_sequence_only(L):
+    c = Q.Cache(6, [33, 33], 1, 16, 32)
+    b, o = int(c.tables[0, 1]), 4
+    c.v[1][b, 0, o, 2] = float("nan")           # dims 64..95 of one V row of sequence 0
+    kc, vc, bt = c.cuda()
+    q = torch.randn(2, 2, 128).to(torch.bfloat16).cuda()
+    out, lse = pkv.paged_decode_attn_q4(q, kc, vc, bt, torch.tensor([33, 33], dtype=torch.int32, device="cuda"), 33, SCALE)
+    assert pkv.check_device_errors() == 0
+    assert bool(torch.isnan(out[0, :, 64:96]).all()) and bool(torch.isfinite(out[0, :, :64]).all())
+    assert bool(torch.isfinite(out[1]).all()) and bool(torch.isfinite(lse).all())
+
+
+@gpu
+def test_decode_workspace_serves_smaller_calls_and_refuses_larger(L):
+    c = Q.Cache(7, [2000, 700, 30], 2, 32, 64)
+    kc, vc, bt = c.cuda()
+    q = torch.randn(3, 4, 128).to(torch.bfloat16)
+    out, _, tol_o, _, _, _ = _decode_plain(c, q, 2, 0)
+    ws = pkv.new_q4_decode_workspace(3, 4, 2, 2000, with_scores=True)
+    for rows in ([0, 1, 2], [1, 2], [2], [0]):
+        n = [c.lens[r] for r in rows]
+        o, _ = pkv.paged_decode_attn_q4(q[rows].cuda(), kc, vc, bt[rows], torch.tensor(n, dtype=torch.int32, device="cuda"),
+                                        max(n), SCALE, workspace=ws)
+        assert bool(((o.cpu().double() - out[rows]).abs() <= tol_o[rows]).all())
+    small = torch.empty(1024, dtype=torch.uint8, device="cuda")
+    with pytest.raises(pkv.PkvError):
+        pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt, torch.tensor(c.lens, dtype=torch.int32, device="cuda"), 2000, SCALE,
+                                 workspace=small)
+    assert pkv.check_device_errors() == 0
+
+
+@gpu
+def test_decode_in_a_graph_on_another_stream(L):
+    """Captured on a side stream and replayed: the same bits as the eager call,
+    with a context bound far above the lengths."""
+    c = Q.Cache(8, [300, 1, 77], 4, 16, 32)
+    kc, vc, bt = c.cuda()
+    q = torch.randn(3, 8, 128).to(torch.bfloat16).cuda()
+    cl = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    wide = torch.full((3, 1024), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.shape[1]] = bt
+    eager, lse = pkv.paged_decode_attn_q4(q, kc, vc, wide, cl, 16384, SCALE)
+    stream = torch.cuda.Stream()
+    ws = pkv.new_q4_decode_workspace(3, 8, 4, 16384, with_scores=True)
+    o, l = torch.zeros_like(eager), torch.zeros_like(lse)
+    scores = torch.zeros(3, 16384, device="cuda")
+    stream.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        pkv.paged_decode_attn_q4(q, kc, vc, wide, cl, 16384, SCALE, out=o, lse=l, workspace=ws, key_scores=scores)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, eager) and torch.equal(l, lse)
+    once = torch.zeros_like(scores)
+    pkv.paged_decode_attn_q4(q, kc, vc, wide, cl, 16384, SCALE, key_scores=once, stream=None)
+    assert torch.equal(scores, once + once)
+    assert pkv.check_device_errors() == 0
+
+
+# ------------------------------------------------------------------ GPU: prefill
+
+PREFILL = [  # q lens, k lens, heads, gqa, block, group, window
+    ([9, 33, 64, 64], [9, 33, 64, 64], 8, 2, 16, 32, 0),
+    ([1], [1], 1, 1, 16, 128, 0),
+    ([1, 0, 5], [300, 17, 5], 2, 4, 48, 64, 0),
+    ([200, 37, 300], [330, 37, 429], 2, 2, 64, 32, 0),
+    ([130, 1], [513, 2], 1, 4, 256, 128, 0),
+    ([200, 37, 300], [330, 37, 700], 2, 2, 16, 64, 100),
+    ([1, 3], [600, 129], 1, 2, 32, 32, 1),
+]
+
+
+def _prefill_plain(c, q, q_lens, gqa, window):
+    out, lse = torch.zeros(q.shape, dtype=torch.float64), torch.zeros(q.shape[:2], dtype=torch.float64)
+    tol_o, tol_l = torch.zeros_like(out), torch.zeros_like(lse)
+    at = 0
+    for s, (n, m) in enumerate(zip(c.lens, q_lens)):
+        last = torch.arange(n - m, n)
+        first = (last - window + 1).clamp(min=0) if window else torch.zeros_like(last)
+        for h in range(c.heads * gqa):
+            if m == 0:
+                continue
+            k, v = c.logical(c.k, s, n, h // gqa), c.logical(c.v, s, n, h // gqa)
+            o, l, _, wv, qk = Q.attend(q[at:at + m, h].double(), k, v, SCALE, first, last)
+            out[at:at + m, h], lse[at:at + m, h] = o, l
+            tol_o[at:at + m, h], tol_l[at:at + m, h] = Q.out_tolerance(o, wv), Q.lse_tolerance(l, qk, n)
+        at += m
+    return out, lse, tol_o, tol_l
+
+
+def _cu(lens):
+    return torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32).cuda()
+
+
+@gpu
+@pytest.mark.parametrize("q_lens,k_lens,heads,gqa,block,group,window", PREFILL)
+def test_prefill(L, q_lens, k_lens, heads, gqa, block, group, window):
+    c = Q.Cache(sum(k_lens), k_lens, heads, block, group)
+    g = torch.Generator().manual_seed(len(k_lens))
+    q = torch.randn(sum(q_lens), heads * gqa, 128, generator=g).to(torch.bfloat16)
+    out, lse, tol_o, tol_l = _prefill_plain(c, q, q_lens, gqa, window)
+    kc, vc, bt = c.cuda()
+    if window:  # an engine may drop the blocks that lie wholly before every window
+        for s, (n, m) in enumerate(zip(k_lens, q_lens)):
+            bt[s, :max(0, n - m - window + 1) // block] = -1
+    # a workspace of NaN: nothing may be read there that the call did not write
+    ws = pkv.new_q4_prefill_workspace(len(k_lens), sum(k_lens) + 3, max(k_lens), heads)
+    ws.fill_(0xFF)
+    o, l = pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu(q_lens), _cu(k_lens), bt, max(q_lens), max(k_lens),
+                                     sum(k_lens) + 3, SCALE, sliding_window=window, workspace=ws)
+    assert pkv.check_device_errors() == 0
+    assert bool(((o.cpu().double() - out).abs() <= tol_o).all()), float(((o.cpu().double() - out).abs() / tol_o).max())
+    assert bool(((l.cpu().double() - lse).abs() <= tol_l).all()), float(((l.cpu().double() - lse).abs() / tol_l).max())
+
+
+@gpu
+def test_prefill_refuses_a_segment_past_total_k_alone(L):
+    q_lens = k_lens = [20, 30]
+    c = Q.Cache(11, k_lens, 2, 16, 32)
+    q = torch.randn(50, 4, 128).to(torch.bfloat16)
+    out, _, tol_o, _ = _prefill_plain(c, q, q_lens, 2, 0)
+    kc, vc, bt = c.cuda()
+    o, _ = pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu(q_lens), _cu(k_lens), bt, 30, 30, 49, SCALE)
+    assert pkv.check_device_errors() & pkv.DEVERR_SEQLENS
+    assert bool(((o[:20].cpu().double() - out[:20]).abs() <= tol_o[:20]).all())
+
+
+@gpu
+def test_prefill_equals_the_bf16_call_on_the_same_values(L):
+    """The values are bf16 by definition: widening the cache by hand and calling
+    the bf16 prefill gives the same bits."""
+    q_lens, k_lens = [100, 260], [400, 260]
+    c = Q.Cache(12, k_lens, 4, 128, 32)
+    q = torch.randn(360, 8, 128).to(torch.bfloat16).cuda()
+    kc, vc, bt = c.cuda()
+    o, l = pkv.paged_prefill_attn_q4(q, kc, vc, _cu(q_lens), _cu(k_lens), bt, 260, 400, 660, SCALE)
+    slots = torch.arange(c.num_blocks * 128, dtype=torch.int32, device="cuda")
+    k16, v16 = (x.view(c.num_blocks, 128, 4, 128) for x in pkv.kv_load_q4(kc, vc, slots))
+    o16, l16 = pkv.paged_prefill_attn(q, k16, v16, _cu(q_lens), _cu(k_lens), bt, 260, 400, SCALE)
+    assert pkv.check_device_errors() == 0
+    assert torch.equal(o, o16) and torch.equal(l, l16)
