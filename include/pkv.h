@@ -418,6 +418,105 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
                                      void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Eviction by accumulated attention weight
+ * ----------------------------------------
+ * A sequence whose cache has grown past a budget keeps its most recent tokens
+ * and, of the older ones, those that have received most attention: decode calls
+ * accumulate each key's weight (pkv_paged_decode_attn_scores, or key_scores of
+ * pkv_paged_decode_attn_q4), pkv_evict_select chooses the positions, and
+ * pkv_evict_compact moves their rows together in order. Afterwards the sequence
+ * has new_lens[s] keys, at positions 0 .. new_lens[s] - 1 of the destination
+ * table (keys carry their rotary position in their values).
+ */
+
+/*
+ * pkv_paged_decode_attn that also accumulates the attention weights:
+ *   key_scores[s * score_stride + p] += sum over query heads h of exp(z_hp - lse[s, h])
+ * for every key p that sequence s attended to; other entries keep their values.
+ * The heads are summed in order: the same inputs give the same bits.
+ *   key_scores   device float32 [num_seqs, score_stride], not NULL; the caller
+ *                sets a sequence's row to zero when it admits the sequence
+ *   score_stride >= max_context_len
+ *   workspace    device, >= pkv_decode_scores_workspace_size(...) bytes: the
+ *                decode workspace and the call's logits (4 bytes per key and
+ *                query head). Conditions as for the decode workspace, but its
+ *                size follows num_seqs and max_context_len.
+ * After a timeout (see above) nothing is added.
+ */
+size_t pkv_decode_scores_workspace_size(int32_t num_seqs, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t head_dim,
+                                        int32_t max_context_len);
+pkv_status pkv_paged_decode_attn_scores(const void *q, const void *k_cache, const void *v_cache,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *context_lens, int32_t max_context_len,
+                                        int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                        float scale, int32_t sliding_window, void *out, float *lse,
+                                        float *key_scores, int64_t score_stride, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * The positions that stay: of a sequence with ctx = context_lens[s] keys, all if
+ * ctx <= budget; else the last `recent` and, of the others, the budget - recent
+ * with the highest scores (equal scores: the lowest positions; a NaN counts as
+ * lower than any number).
+ *   key_scores   device float32 [num_seqs, score_stride], score_stride >= max_context_len
+ *   context_lens device int32 [num_seqs], each in [0, max_context_len]
+ *   budget       >= 1;  recent in [0, budget]
+ *   keep         device int32 [num_seqs, budget]: the kept positions in
+ *                ascending order, then -1
+ *   new_lens     device int32 [num_seqs]: min(ctx, budget)
+ * A sequence whose length is invalid raises PKV_DEVERR_CONTEXT and its rows of
+ * keep and new_lens are not written.
+ */
+pkv_status pkv_evict_select(const float *key_scores, int64_t score_stride,
+                            const int32_t *context_lens, int32_t max_context_len, int32_t num_seqs,
+                            int32_t budget, int32_t recent, int32_t *keep, int32_t *new_lens,
+                            void *stream);
+
+/*
+ * Move the kept rows together: for i < new_lens[s], the K and V rows at position
+ * i of dst_tables[s] become those at position keep[s][i] of src_tables[s], in
+ * every head. keep must be strictly ascending, as pkv_evict_select writes it.
+ *   src_tables  device int32 [num_seqs, src_max_blocks]
+ *   dst_tables  device int32 [num_seqs, dst_max_blocks]. Each entry used is
+ *               either the source's entry at the same index, if no other
+ *               sequence of the call reads that block (compaction in place), or
+ *               a block that no source table of the call names. Equal tables
+ *               compact every sequence in place; sequences that share blocks
+ *               with others need fresh ones (pkv_bm_evict_sequence makes such
+ *               rows). Nothing else is written.
+ *   key_scores  device float32 [num_seqs, score_stride], or NULL (both):
+ *   dst_key_scores  dst_key_scores[s * dst_score_stride + i] =
+ *               key_scores[s * score_stride + keep[s][i]], and the entries from
+ *               new_lens[s] to dst_score_stride - 1 become 0, so that tokens
+ *               appended next start from zero. May be the same array (then with
+ *               the same stride), or must not overlap.
+ * A new_lens[s] outside [0, budget], past dst_tables or past dst_score_stride
+ * raises PKV_DEVERR_CONTEXT and nothing of that sequence moves; a position
+ * outside a table raises PKV_DEVERR_CONTEXT and an invalid table entry
+ * PKV_DEVERR_BLOCK, and that row does not move. num_seqs is at most 65535;
+ * head_dim 128; block_size any positive number.
+ */
+pkv_status pkv_evict_compact(void *k_cache, void *v_cache, const int32_t *src_tables,
+                             int32_t src_max_blocks, const int32_t *dst_tables,
+                             int32_t dst_max_blocks, const int32_t *keep, int32_t budget,
+                             const int32_t *new_lens, int32_t num_seqs, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                             const float *key_scores, int64_t score_stride, float *dst_key_scores,
+                             int64_t dst_score_stride, void *stream);
+
+/* The same for a 4-bit cache: codes and parameters move, bit for bit. */
+pkv_status pkv_evict_compact_q4(void *k_codes, void *k_params, void *v_codes, void *v_params,
+                                const int32_t *src_tables, int32_t src_max_blocks,
+                                const int32_t *dst_tables, int32_t dst_max_blocks,
+                                const int32_t *keep, int32_t budget, const int32_t *new_lens,
+                                int32_t num_seqs, int32_t num_kv_heads, int32_t head_dim,
+                                int32_t group_size, int32_t block_size, int64_t num_blocks,
+                                const float *key_scores, int64_t score_stride,
+                                float *dst_key_scores, int64_t dst_score_stride, void *stream);
+
+/*
  * Synchronise `stream`, then return in *flags_out the OR of the device error
  * words of every kernel of this library on the current device, and clear
  * them. It blocks the host; it is also the only way to clear the words, and

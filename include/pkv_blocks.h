@@ -73,6 +73,21 @@ pkv_status pkv_bm_add_sequence(pkv_block_manager *bm, int64_t seq_id, const int3
  * sequence's last block is full. The new token is at position num_tokens - 1. */
 pkv_status pkv_bm_append_token(pkv_block_manager *bm, int64_t seq_id, int32_t token_id);
 
+/* Eviction (pkv_evict_select, pkv_evict_compact): seq_id keeps num_kept (1 ..
+ * its token count) of its tokens. Its table becomes the destination of the
+ * compaction: the first ceil(num_kept / block_size) blocks, each the block it
+ * was unless another sequence shares it, in which case a fresh one takes its
+ * place; the others are released. Read the old row (pkv_bm_block_table) before
+ * this call and the new row after it, and enqueue the compaction between them
+ * on the stream of the cache's other calls before anything is stored into
+ * blocks handed out later: a released block still holds rows to be moved.
+ * From here on the sequence has num_kept tokens; its rows are no longer those of
+ * a prompt, so that none of its blocks is findable any more, those it fills
+ * later included (released ones keep their content and stay findable).
+ * PKV_ERR_OUT_OF_BLOCKS if fewer blocks are free than shared ones are to be
+ * replaced. */
+pkv_status pkv_bm_evict_sequence(pkv_block_manager *bm, int64_t seq_id, int32_t num_kept);
+
 /* Release seq_id: each of its blocks loses one reference; blocks left with
  * none go to the back of the free list. */
 pkv_status pkv_bm_free_sequence(pkv_block_manager *bm, int64_t seq_id);

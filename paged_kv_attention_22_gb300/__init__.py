@@ -107,6 +107,18 @@ def lib():
                                                        i32, i32, i32, i32, i64, f32, i32, P, P, P,
                                                        sz, P]
     L.pkv_paged_prefill_attn_q4.restype = ctypes.c_int
+    L.pkv_decode_scores_workspace_size.argtypes = [i32] * 5
+    L.pkv_decode_scores_workspace_size.restype = sz
+    L.pkv_paged_decode_attn_scores.argtypes = [P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32,
+                                               i64, f32, i32, P, P, P, i64, P, sz, P]
+    L.pkv_paged_decode_attn_scores.restype = ctypes.c_int
+    L.pkv_evict_select.argtypes = [P, i64, P, i32, i32, i32, i32, P, P, P]
+    L.pkv_evict_select.restype = ctypes.c_int
+    rows = [P, i32, P, i32, P, i32, P, i32]  # source and destination tables, keep, new_lens, num_seqs
+    L.pkv_evict_compact.argtypes = [P, P] + rows + [i32, i32, i32, i64, P, i64, P, i64, P]
+    L.pkv_evict_compact.restype = ctypes.c_int
+    L.pkv_evict_compact_q4.argtypes = q4 + rows + [i32, i32, i32, i32, i64, P, i64, P, i64, P]
+    L.pkv_evict_compact_q4.restype = ctypes.c_int
     L.pkv_check_device_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     L.pkv_check_device_errors.restype = ctypes.c_int
     L.pkv_read_device_errors_async.argtypes = [P, P]
@@ -126,6 +138,8 @@ def lib():
     L.pkv_bm_add_sequence.restype = ctypes.c_int
     L.pkv_bm_append_token.argtypes = [P, i64, i32]
     L.pkv_bm_append_token.restype = ctypes.c_int
+    L.pkv_bm_evict_sequence.argtypes = [P, i64, i32]
+    L.pkv_bm_evict_sequence.restype = ctypes.c_int
     L.pkv_bm_free_sequence.argtypes = [P, i64]
     L.pkv_bm_free_sequence.restype = ctypes.c_int
     L.pkv_bm_num_tokens.argtypes = [P, i64, pi32]
@@ -543,6 +557,120 @@ def paged_prefill_attn_q4(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block
     return out, lse
 
 
+def decode_scores_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context_len) -> int:
+    """Workspace bytes of paged_decode_attn_scores on the current device (0: invalid sizes)."""
+    return int(lib().pkv_decode_scores_workspace_size(num_seqs, num_q_heads, num_kv_heads, 128,
+                                                      max_context_len))
+
+
+def new_decode_scores_workspace(num_seqs, num_q_heads, num_kv_heads, max_context_len,
+                                device="cuda"):
+    """A workspace of paged_decode_attn_scores for these sizes on the current device."""
+    need = decode_scores_workspace_size(num_seqs, num_q_heads, num_kv_heads, max_context_len)
+    if need == 0:
+        raise PkvError(PKV_ERR_CUDA, "pkv_decode_scores_workspace_size")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def paged_decode_attn_scores(q, k_cache, v_cache, block_tables, context_lens, max_context_len,
+                             scale, key_scores, out=None, lse=None, workspace=None, stream=None,
+                             with_lse=True, sliding_window=0):
+    """paged_decode_attn that also adds each key's attention weight, summed over
+    the query heads, to key_scores [S, >= max_context_len] (fp32). Returns (out, lse)."""
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(key_scores, "key_scores", torch.float32, 2)
+    NB, bs, H_kv, D = k_cache.shape
+    if v_cache.shape != k_cache.shape or D != 128:
+        raise ValueError("inconsistent shapes")
+    with _on(stream):
+        out, lse, stride = _decode_inputs(q, block_tables, context_lens, int(max_context_len), out, lse,
+                                          with_lse, key_scores)
+        S, H_q, _ = q.shape
+        if workspace is None:
+            workspace = new_decode_scores_workspace(S, H_q, H_kv, int(max_context_len), q.device)
+    _need(workspace, "workspace", torch.uint8, 1)
+    _need_current_device(k_cache, v_cache, workspace)
+    _check(lib().pkv_paged_decode_attn_scores(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
+        _ptr(context_lens), int(max_context_len), S, H_q, H_kv, 128, bs, NB, float(scale),
+        int(sliding_window), _ptr(out), _ptr(lse), _ptr(key_scores), stride, _ptr(workspace),
+        workspace.numel(), _stream(stream)), "pkv_paged_decode_attn_scores")
+    return out, lse
+
+
+def evict_select(key_scores, context_lens, budget, recent, keep=None, new_lens=None, stream=None):
+    """Positions that stay: the last `recent` and the highest-scoring others, budget
+    in all, ascending. Returns (keep int32 [S, budget], -1 padded, new_lens int32 [S])."""
+    _need(key_scores, "key_scores", torch.float32, 2)
+    _need(context_lens, "context_lens", torch.int32, 1)
+    S, width = key_scores.shape
+    budget, recent = int(budget), int(recent)
+    if context_lens.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    with _on(stream):
+        if keep is None:
+            keep = torch.empty((S, max(budget, 0)), dtype=torch.int32, device=key_scores.device)
+        if new_lens is None:
+            new_lens = torch.empty(S, dtype=torch.int32, device=key_scores.device)
+    _need(keep, "keep", torch.int32, 2)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    if keep.shape != (S, budget) or new_lens.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    _need_current_device(key_scores, context_lens, keep, new_lens)
+    _check(lib().pkv_evict_select(_ptr(key_scores), width, _ptr(context_lens), width, S, budget,
+                                  recent, _ptr(keep), _ptr(new_lens), _stream(stream)),
+           "pkv_evict_select")
+    return keep, new_lens
+
+
+def _compact_args(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores):
+    """Checked arguments shared by the two compactions: (tables .. num_seqs, scores)."""
+    _need(src_tables, "src_tables", torch.int32, 2)
+    _need(dst_tables, "dst_tables", torch.int32, 2)
+    _need(keep, "keep", torch.int32, 2)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    S = src_tables.shape[0]
+    if dst_tables.shape[0] != S or keep.shape[0] != S or new_lens.shape[0] != S:
+        raise ValueError("inconsistent shapes")
+    strides = [0, 0]
+    for i, (t, name) in enumerate(((key_scores, "key_scores"), (dst_key_scores, "dst_key_scores"))):
+        if t is not None:
+            _need(t, name, torch.float32, 2)
+            if t.shape[0] != S:
+                raise ValueError("inconsistent shapes")
+            strides[i] = t.shape[1]
+    _need_current_device(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores)
+    return ((_ptr(src_tables), src_tables.shape[1], _ptr(dst_tables), dst_tables.shape[1], _ptr(keep),
+             keep.shape[1], _ptr(new_lens), S),
+            (_ptr(key_scores), strides[0], _ptr(dst_key_scores), strides[1]))
+
+
+def evict_compact(k_cache, v_cache, src_tables, dst_tables, keep, new_lens, key_scores=None,
+                  dst_key_scores=None, stream=None):
+    """Move each sequence's kept rows (evict_select) to positions 0 .. new_lens - 1 of
+    dst_tables; equal tables compact in place. The scores move along, with zeros
+    behind them (pass the same tensor twice for in place)."""
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    NB, bs, H_kv, D = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("inconsistent shapes")
+    _need_current_device(k_cache, v_cache)
+    rows, scores = _compact_args(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores)
+    _check(lib().pkv_evict_compact(_ptr(k_cache), _ptr(v_cache), *rows, H_kv, D, bs, NB, *scores,
+                                   _stream(stream)), "pkv_evict_compact")
+
+
+def evict_compact_q4(k_cache, v_cache, src_tables, dst_tables, keep, new_lens, key_scores=None,
+                     dst_key_scores=None, stream=None):
+    """evict_compact for a 4-bit cache."""
+    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
+    rows, scores = _compact_args(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores)
+    _check(lib().pkv_evict_compact_q4(*ptrs, *rows, H_kv, 128, group, bs, NB, *scores,
+                                      _stream(stream)), "pkv_evict_compact_q4")
+
+
 def check_device_errors(stream=None) -> int:
     """Synchronise, then return and clear the OR of the kernels' device error words."""
     flags = ctypes.c_uint32(0)
@@ -610,6 +738,11 @@ class BlockManager:
     def append_token(self, seq_id: int, token_id: int) -> None:
         _check(self._L.pkv_bm_append_token(self._h, int(seq_id), int(token_id)),
                "pkv_bm_append_token")
+
+    def evict_sequence(self, seq_id: int, num_kept: int) -> None:
+        """Keep num_kept tokens; block_table() is then the compaction's destination."""
+        _check(self._L.pkv_bm_evict_sequence(self._h, int(seq_id), int(num_kept)),
+               "pkv_bm_evict_sequence")
 
     def free_sequence(self, seq_id: int) -> None:
         _check(self._L.pkv_bm_free_sequence(self._h, int(seq_id)), "pkv_bm_free_sequence")

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libpkv.so")
 SOURCES = ["kv_store.cu", "decode.cu", "prefill.cu", "api.cu", "decode_noalloc.cu",
-           "q4_cache.cu", "q4_decode.cu", "api_q4.cu", "block_manager.cpp"]
+           "q4_cache.cu", "q4_decode.cu", "api_q4.cu", "evict.cu", "api_evict.cu",
+           "block_manager.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]

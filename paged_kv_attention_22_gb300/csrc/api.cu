@@ -253,8 +253,26 @@ void pkv_decode_set_config(int32_t ctas, int32_t variant) {
 
 namespace {
 
-// Shared by the plain and the fused-store decode entry points; k_new == nullptr
-// for the plain one.
+// The decode workspace followed by what accumulated weights need: the lse (for
+// callers that do not want it) and the logits.
+struct DecodeScoresWorkspace {
+  size_t lse, logits, total;
+  int64_t logits_ld;
+};
+
+DecodeScoresWorkspace decode_scores_layout(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                           size_t decode_bytes) {
+  DecodeScoresWorkspace w;
+  const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
+  w.logits_ld = static_cast<int64_t>(align_up(static_cast<size_t>(max_context_len), pkv::kDecodeChunk));
+  w.lse = align_up(decode_bytes, 256);
+  w.logits = w.lse + align_up(rows * sizeof(float), 256);
+  w.total = w.logits + rows * static_cast<size_t>(w.logits_ld) * sizeof(float);
+  return w;
+}
+
+// Shared by the decode entry points; k_new == nullptr without the fused store,
+// key_scores == nullptr without accumulated weights.
 pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *slot_mapping,
                          const void *q, const void *k_cache, const void *v_cache,
                          const int32_t *block_tables, int32_t max_blocks_per_seq,
@@ -262,7 +280,8 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
                          int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                          int32_t block_size, int64_t num_blocks, float scale,
                          int32_t sliding_window, void *out, float *lse, void *workspace,
-                         size_t workspace_bytes, uint32_t flags, void *stream) {
+                         size_t workspace_bytes, uint32_t flags, float *key_scores,
+                         int64_t score_stride, void *stream) {
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_tables == nullptr ||
       context_lens == nullptr || out == nullptr)
     return PKV_ERR_INVALID_ARG;
@@ -281,9 +300,20 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
   if ((st = current_sm_count(&sms)) != PKV_OK) return st;
   DecodeWorkspace w;
   decode_workspace_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, sms, &w);
-  if (workspace_bytes < w.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  const DecodeScoresWorkspace sw =
+      decode_scores_layout(num_seqs, num_q_heads, max_context_len, w.total);
+  if (workspace_bytes < (key_scores != nullptr ? sw.total : w.total))
+    return PKV_ERR_WORKSPACE_TOO_SMALL;
 
   pkv::DecodeArgs a;
+  a.key_scores = key_scores;
+  a.score_stride = score_stride;
+  a.logits = nullptr;
+  a.logits_ld = sw.logits_ld;
+  if (key_scores != nullptr) {
+    a.logits = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + sw.logits);
+    if (lse == nullptr) lse = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + sw.lse);
+  }
   a.k_new = k_new;
   a.v_new = v_new;
   a.k_cache_w = const_cast<void *>(k_cache);
@@ -352,7 +382,7 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
 namespace {
 
 // The device error words of the kernel files on one device.
-constexpr int kErrorWords = 5;
+constexpr int kErrorWords = 6;
 struct ErrorWords {
   uint32_t *w[kErrorWords];
 };
@@ -374,7 +404,8 @@ pkv_status error_words(ErrorWords *out) {
         (e = pkv::decode_error_word(&w.w[1])) != cudaSuccess ||
         (e = pkv::prefill_error_word(&w.w[2])) != cudaSuccess ||
         (e = pkv::q4_cache_error_word(&w.w[3])) != cudaSuccess ||
-        (e = pkv::q4_decode_error_word(&w.w[4])) != cudaSuccess)
+        (e = pkv::q4_decode_error_word(&w.w[4])) != cudaSuccess ||
+        (e = pkv::evict_error_word(&w.w[5])) != cudaSuccess)
       return cuda_fail(e, "cudaGetSymbolAddress (device error words)");
     g_words[dev] = w;
     g_words_set[dev] = true;
@@ -422,7 +453,30 @@ pkv_status pkv_paged_decode_attn(const void *q, const void *k_cache, const void 
   return decode_common(nullptr, nullptr, nullptr, q, k_cache, v_cache, block_tables,
                        max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads,
                        num_kv_heads, head_dim, block_size, num_blocks, scale, sliding_window,
-                       out, lse, workspace, workspace_bytes, 0u, stream);
+                       out, lse, workspace, workspace_bytes, 0u, nullptr, 0, stream);
+}
+
+size_t pkv_decode_scores_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t max_context_len) {
+  const size_t decode =
+      pkv_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);
+  if (decode == 0 || max_context_len <= 0) return 0;
+  return decode_scores_layout(num_seqs, num_q_heads, max_context_len, decode).total;
+}
+
+pkv_status pkv_paged_decode_attn_scores(const void *q, const void *k_cache, const void *v_cache,
+                                        const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t *context_lens, int32_t max_context_len,
+                                        int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                        float scale, int32_t sliding_window, void *out, float *lse,
+                                        float *key_scores, int64_t score_stride, void *workspace,
+                                        size_t workspace_bytes, void *stream) {
+  if (key_scores == nullptr || score_stride < max_context_len) return PKV_ERR_INVALID_ARG;
+  return decode_common(nullptr, nullptr, nullptr, q, k_cache, v_cache, block_tables,
+                       max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads,
+                       num_kv_heads, head_dim, block_size, num_blocks, scale, sliding_window,
+                       out, lse, workspace, workspace_bytes, 0u, key_scores, score_stride, stream);
 }
 
 pkv_status pkv_paged_decode_attn_store(const void *k_new, const void *v_new,
@@ -440,7 +494,7 @@ pkv_status pkv_paged_decode_attn_store(const void *k_new, const void *v_new,
   return decode_common(k_new, v_new, slot_mapping, q, k_cache, v_cache, block_tables,
                        max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads,
                        num_kv_heads, head_dim, block_size, num_blocks, scale, sliding_window,
-                       out, lse, workspace, workspace_bytes, flags, stream);
+                       out, lse, workspace, workspace_bytes, flags, nullptr, 0, stream);
 }
 
 size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t max_seqlen_q) {

@@ -43,6 +43,7 @@ struct Sequence {
   std::vector<int32_t> blocks;
   std::vector<int32_t> tokens;
   std::vector<uint64_t> chain;  // chain hash of each full block
+  bool evicted = false;         // its rows are no longer those of its tokens: never findable
 };
 
 }  // namespace
@@ -78,14 +79,18 @@ struct pkv_block_manager {
   int32_t take_fresh() {
     const int32_t b = free_head;
     unlink_free(b);
-    Block &x = blocks[b];
-    if (x.findable) {
-      auto it = by_hash.find(x.hash);
-      if (it != by_hash.end() && it->second == b) by_hash.erase(it);
-      x.findable = false;
-    }
-    x.ref = 1;
+    unpublish(b);
+    blocks[b].ref = 1;
     return b;
+  }
+
+  // Block b no longer holds the tokens it was findable under.
+  void unpublish(int32_t b) {
+    Block &x = blocks[b];
+    if (!x.findable) return;
+    auto it = by_hash.find(x.hash);
+    if (it != by_hash.end() && it->second == b) by_hash.erase(it);
+    x.findable = false;
   }
 
   // The findable block holding these tokens after `parent`, or -1.
@@ -220,7 +225,7 @@ pkv_status pkv_bm_append_token(pkv_block_manager *bm, int64_t seq_id, int32_t to
   }
   if (n % bs == 0) seq.blocks.push_back(bm->take_fresh());
   seq.tokens.push_back(token_id);
-  if ((n + 1) % bs == 0) {  // the last block is now full
+  if ((n + 1) % bs == 0 && !seq.evicted) {  // the last block is now full
     const int32_t i = n / bs;
     const uint64_t parent = i > 0 ? seq.chain[i - 1] : 0;
     const int32_t *tok = seq.tokens.data() + static_cast<size_t>(i) * bs;
@@ -228,6 +233,37 @@ pkv_status pkv_bm_append_token(pkv_block_manager *bm, int64_t seq_id, int32_t to
     bm->publish(seq.blocks[i], h, parent, tok);
     seq.chain.push_back(h);
   }
+  return PKV_OK;
+}
+
+pkv_status pkv_bm_evict_sequence(pkv_block_manager *bm, int64_t seq_id, int32_t num_kept) {
+  if (bm == nullptr) return PKV_ERR_INVALID_ARG;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end()) return PKV_ERR_INVALID_ARG;
+  Sequence &seq = it->second;
+  if (num_kept <= 0 || num_kept > static_cast<int32_t>(seq.tokens.size())) return PKV_ERR_INVALID_ARG;
+  const size_t n = (static_cast<size_t>(num_kept) + bm->block_size - 1) / bm->block_size;
+  int32_t fresh = 0;
+  for (size_t i = 0; i < n; ++i)
+    if (bm->blocks[seq.blocks[i]].ref > 1) ++fresh;
+  if (fresh > bm->num_free) return PKV_ERR_OUT_OF_BLOCKS;
+  for (size_t i = 0; i < n; ++i) {
+    const int32_t b = seq.blocks[i];
+    if (bm->blocks[b].ref > 1) {  // others still read it: this sequence's rows move to a fresh one
+      --bm->blocks[b].ref;
+      seq.blocks[i] = bm->take_fresh();
+    } else {
+      bm->unpublish(b);
+    }
+  }
+  for (size_t k = seq.blocks.size(); k-- > n;) {
+    const int32_t b = seq.blocks[k];
+    if (--bm->blocks[b].ref == 0) bm->push_free(b);
+  }
+  seq.blocks.resize(n);
+  seq.tokens.resize(num_kept);
+  seq.chain.clear();
+  seq.evicted = true;
   return PKV_OK;
 }
 

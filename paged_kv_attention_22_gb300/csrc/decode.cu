@@ -35,9 +35,15 @@
 //   token's rows from the inputs over the staged cache row, so the result is
 //   exactly that of storing first and attending after.
 //
+//   Accumulated weights. With kLogits each consumer warp also leaves its units'
+//   logits in the workspace (4 bytes per key and query head, beside 512 bytes
+//   of K and V per key and KV head), and a kernel behind the merge turns them
+//   into weights: K is not read a second time.
+//
 // The 2-wide GQA group makes the logits and P.V skinny matrix-vector products,
 // so the kernel is bound by HBM bandwidth, not by any tensor-core contraction.
 #include "internal.h"
+#include "key_scores.cuh"
 #include "ptx.cuh"
 
 namespace pkv {
@@ -81,6 +87,8 @@ struct DecodeParams {
   int32_t window;    // sliding window (keys per query, its own included), 0: none
   int32_t stable_inputs;  // caches, tables and lengths may be read before the wait
   float scale_log2;
+  float *logits;          // kLogits: [S, H_q, logits_ld]
+  int64_t logits_ld;
 };
 
 // With a sliding window the query of a sequence with ctx keys (at position
@@ -166,7 +174,7 @@ __device__ __forceinline__ void butterfly_half(float (&x)[N], bool upper, int la
   }
 }
 
-template <int G, int kMaxHG, int NS>
+template <int G, int kMaxHG, int NS, bool kLogits>
 __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
     decode_kernel(const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map,
@@ -502,6 +510,10 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
       butterfly_half<2>(q2, (sub & 2) != 0, 2);
       const float full = q2[0] + __shfl_xor_sync(0xffffffffu, q2[0], 1);
       sc[h] = (my_key < nvalid && my_key >= nskip) ? full : -INFINITY;
+      if constexpr (kLogits) {  // rows hold whole units: masked keys are written too
+        const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + (cur.hg * HG + g) * G + h;
+        if (counts) p.logits[row * p.logits_ld + key0 + my_key] = full;
+      }
     }
 
     // ---- online softmax over the unit (base 2), with a lazy maximum: the
@@ -816,14 +828,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
   }
 }
 
-template <int G, int HGM, int NS>
+// One position a thread; after a timeout the logits are stale: nothing is added.
+__global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(const KeyScoresParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if (*reinterpret_cast<volatile uint32_t *>(&g_decode_errors) & kErrTimeout) return;
+  key_scores_body(p);
+}
+
+template <int G, int HGM, int NS, bool kLogits = false>
 cudaError_t launch_variant(const DecodeArgs &a, const CUtensorMap &k_map,
                            const CUtensorMap &v_map, const CUtensorMap &q_map,
                            const CUtensorMap &kn_map, const CUtensorMap &vn_map,
                            const DecodeParams &p, cudaStream_t stream) {
   using L = DecodeSmem<G, HGM, NS>;
   static_assert(L::total(kDecodeMaxSeqs) <= 227 * 1024, "decode shared memory");
-  auto kern = decode_kernel<G, HGM, NS>;
+  auto kern = decode_kernel<G, HGM, NS, kLogits>;
   const int smem = L::total(a.num_seqs);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -843,6 +863,12 @@ cudaError_t launch_group(const DecodeArgs &a, const CUtensorMap &k_map, const CU
                          const CUtensorMap &vn_map, const DecodeParams &p, cudaStream_t stream) {
   // three stages when they fit in shared memory, else two
   constexpr int kDefaultStages = DecodeSmem<G, 8, 3>::total(kDecodeMaxSeqs) <= 227 * 1024 ? 3 : 2;
+  if (a.logits != nullptr) {
+    if (a.variant == 2)
+      return launch_variant<G, 4, 2, true>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
+    return launch_variant<G, 8, kDefaultStages, true>(a, k_map, v_map, q_map, kn_map, vn_map, p,
+                                                      stream);
+  }
   switch (a.variant) {
     case 1: return launch_variant<G, 8, 2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
     case 2: return launch_variant<G, 4, 2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
@@ -883,12 +909,29 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map,
   p.window = a.window;
   p.stable_inputs = a.stable_inputs ? 1 : 0;
   p.scale_log2 = a.scale_log2;
+  p.logits = a.logits;
+  p.logits_ld = a.logits_ld;
+  cudaError_t e;
   switch (a.num_q_heads / a.num_kv_heads) {
-    case 1: return launch_group<1>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
-    case 2: return launch_group<2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
-    case 4: return launch_group<4>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
+    case 1: e = launch_group<1>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream); break;
+    case 2: e = launch_group<2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream); break;
+    case 4: e = launch_group<4>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream); break;
     default: return cudaErrorInvalidValue;
   }
+  if (e != cudaSuccess || a.key_scores == nullptr) return e;
+  KeyScoresParams k;
+  k.logits = a.logits;
+  k.lse = a.lse;
+  k.key_scores = a.key_scores;
+  k.context_lens = a.context_lens;
+  k.logits_ld = a.logits_ld;
+  k.score_stride = a.score_stride;
+  k.max_context_len = a.max_context_len;
+  k.num_q_heads = a.num_q_heads;
+  k.window = a.window;
+  k.ctx_cap = static_cast<int64_t>(a.max_blocks) * a.block_size;
+  return launch_pdl(decode_scores_kernel, dim3(key_scores_grid_x(a.max_context_len), a.num_seqs),
+                    dim3(kScoreThreads), 0, stream, k);
 }
 
 cudaError_t decode_error_word(uint32_t **word) {

@@ -93,6 +93,9 @@ struct DecodeArgs {
   int32_t variant;          // launch shape (see kDecodeNumVariants)
   int32_t window;           // sliding window in keys (0: none)
   bool stable_inputs;       // caches, tables and lengths may be read before the wait
+  float *logits;            // [S, H_q, logits_ld] (base 2, scaled) for key_scores, or null
+  float *key_scores;        // [S, score_stride] or null; then lse is not null
+  int64_t logits_ld, score_stride;
   float scale_log2;         // scale * log2(e)
 };
 cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map,
@@ -184,6 +187,35 @@ struct Q4DecodeArgs {
 };
 cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream);
 cudaError_t q4_decode_error_word(uint32_t **word);
+
+// ---------------------------------------------------------------- eviction
+struct EvictSelectArgs {
+  const float *key_scores;
+  int64_t score_stride;
+  const int32_t *context_lens;
+  int32_t *keep, *new_lens;
+  int32_t max_context_len, num_seqs, budget, recent;
+};
+cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t stream);
+
+// An array of cache rows: [num_blocks, planes, block_size] rows of row_bytes.
+struct RowArray {
+  void *base;
+  int32_t planes, row_bytes;
+};
+constexpr int kMaxRowArrays = 4;
+constexpr int kSliceBytes = 64;  // bytes of a row that one CTA of the compaction moves, at most
+struct EvictCompactArgs {
+  RowArray arrays[kMaxRowArrays];
+  int32_t num_arrays;
+  const int32_t *src_tables, *dst_tables, *keep, *new_lens;
+  const float *key_scores;
+  float *dst_key_scores;
+  int64_t score_stride, dst_score_stride;
+  int32_t src_max_blocks, dst_max_blocks, budget, num_seqs, block_size, num_blocks;
+};
+cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream);
+cudaError_t evict_error_word(uint32_t **word);
 
 // ---------------------------------------------------------------- shared by the C entries
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -1,0 +1,421 @@
+"""Eviction by accumulated attention weight: decode that accumulates the weights
+(bf16 cache), selection, compaction and the block manager's part, against plain
+implementations; and the whole chain as an engine runs it."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_attention_22_gb300 as pkv
+import q4_plain as Q
+from paged_kv_attention_22_gb300 import build as pkv_build
+
+SCALE = 1.0 / math.sqrt(128)
+gpu = pytest.mark.gpu
+FAKE = 0x10000
+
+
+@pytest.fixture(scope="module")
+def L():
+    pkv_build.build()
+    return pkv.lib()
+
+
+def select_plain(scores, lens, budget, recent):
+    """Kept positions of every sequence, as lists."""
+    kept = []
+    for row, n in zip(scores.tolist(), lens):
+        r = min(recent, n)
+        want = min(n, budget) - r
+        # NaN behind every number
+        rank = sorted(range(n - r), key=lambda p: (row[p] != row[p], -row[p] if row[p] == row[p] else 0.0, p))
+        kept.append(sorted(rank[:want]) + list(range(n - r, n)))
+    return kept
+
+
+# ------------------------------------------------------------------ CPU
+
+def test_select_refuses(L):
+    def call(ks=FAKE, ld=64, cl=FAKE, mcl=64, S=2, B=16, R=4, keep=FAKE, nl=FAKE):
+        return L.pkv_evict_select(ks, ld, cl, mcl, S, B, R, keep, nl, None)
+    for null in ("ks", "cl", "keep", "nl"):
+        assert call(**{null: None}) == pkv.PKV_ERR_INVALID_ARG
+    for bad in (dict(S=-1), dict(B=0), dict(R=-1), dict(R=17), dict(mcl=0), dict(ld=63)):
+        assert call(**bad) == pkv.PKV_ERR_INVALID_ARG
+    assert call(S=0) == pkv.PKV_OK
+
+
+def test_compact_refuses(L):
+    def call(k=FAKE, v=FAKE, src=FAKE, sb=4, dst=FAKE, db=4, keep=FAKE, B=16, nl=FAKE, S=2, H=8, D=128, bs=16, NB=64,
+             ks=None, ld=0, dks=None, dld=0):
+        return L.pkv_evict_compact(k, v, src, sb, dst, db, keep, B, nl, S, H, D, bs, NB, ks, ld, dks, dld, None)
+    for null in ("k", "v", "src", "dst", "keep", "nl"):
+        assert call(**{null: None}) == pkv.PKV_ERR_INVALID_ARG
+    for bad in (dict(k=FAKE + 8), dict(S=-1), dict(B=0), dict(sb=0), dict(db=0), dict(H=0), dict(bs=0), dict(NB=0),
+                dict(ks=FAKE, ld=64), dict(dks=FAKE, dld=64), dict(ks=FAKE, ld=0, dks=FAKE, dld=64),
+                dict(ks=FAKE, ld=64, dks=FAKE, dld=32)):
+        assert call(**bad) == pkv.PKV_ERR_INVALID_ARG
+    assert call(D=64) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(S=65536) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(NB=1 << 40) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(S=0) == pkv.PKV_OK
+
+    def q4(gs=32, kc=FAKE, S=2):
+        return L.pkv_evict_compact_q4(kc, FAKE, FAKE, FAKE, FAKE, 4, FAKE, 4, FAKE, 16, FAKE, S, 8, 128, gs, 16, 64,
+                                      None, 0, None, 0, None)
+    assert q4(gs=16) == pkv.PKV_ERR_UNSUPPORTED
+    assert q4(kc=None) == pkv.PKV_ERR_INVALID_ARG
+    assert q4(S=0) == pkv.PKV_OK
+
+
+def test_scored_decode_refuses(L):
+    def call(**kw):
+        a = dict(q=FAKE, kc=FAKE, bt=FAKE, cl=FAKE, out=FAKE, ks=FAKE, ld=64, ws=FAKE, wsb=1 << 30, Hq=16)
+        a.update(kw)
+        return L.pkv_paged_decode_attn_scores(a["q"], a["kc"], a["kc"], a["bt"], 4, a["cl"], 64, 2, a["Hq"], 8, 128, 16, 64,
+                                              0.088, 0, a["out"], None, a["ks"], a["ld"], a["ws"], a["wsb"], None)
+    for null in ("q", "kc", "bt", "cl", "out", "ks"):
+        assert call(**{null: None}) == pkv.PKV_ERR_INVALID_ARG
+    assert call(ld=63) == pkv.PKV_ERR_INVALID_ARG
+    assert call(Hq=64) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(ws=None) == pkv.PKV_ERR_WORKSPACE_TOO_SMALL
+    assert L.pkv_decode_scores_workspace_size(0, 16, 8, 128, 64) == 0
+    assert L.pkv_decode_scores_workspace_size(2, 16, 8, 128, 0) == 0
+
+
+def test_manager_eviction_keeps_private_blocks_and_replaces_shared_ones(L):
+    rng = np.random.default_rng(1)
+    bm = pkv.BlockManager(20, 8)
+    base = rng.integers(0, 50000, 40).astype(np.int32)      # 5 blocks
+    bm.add_sequence(0, base)
+    other = np.concatenate([base[:16], rng.integers(0, 50000, 20).astype(np.int32)])
+    assert bm.add_sequence(1, other) == 16                  # 5 blocks, 2 of them shared
+    src = bm.block_table(1)
+    free = bm.num_free_blocks
+    bm.evict_sequence(1, 19)                                # 3 blocks stay
+    dst = bm.block_table(1)
+    assert len(dst) == 3 and bm.num_tokens(1) == 19
+    assert dst[2] == src[2]                                 # its own block
+    assert not set(dst[:2]) & set(src) and not set(dst[:2]) & set(bm.block_table(0))
+    assert [bm.ref_count(b) for b in src] == [1, 1, 1, 0, 0]
+    assert bm.num_free_blocks == free                       # two taken, two released
+    # sequence 0 is as it was, and still findable; the evicted rows are not
+    assert bm.add_sequence(2, base) == 32
+    assert bm.add_sequence(3, other) == 16
+    # tokens appended to the evicted sequence fill blocks that nobody finds
+    for t in range(21):
+        bm.append_token(1, t)
+    assert bm.num_tokens(1) == 40 and len(bm.block_table(1)) == 5
+    assert np.array_equal(bm.slots(1, 0, 40), np.repeat(bm.block_table(1), 8) * 8 + np.tile(np.arange(8), 5))
+    for s in range(4):
+        bm.free_sequence(s)
+    assert bm.num_free_blocks == 20
+
+
+def test_manager_eviction_refuses(L):
+    bm = pkv.BlockManager(4, 4)
+    tok = np.arange(12, dtype=np.int32)
+    bm.add_sequence(0, tok)
+    bm.add_sequence(1, np.concatenate([tok[:8], [99]]).astype(np.int32))    # shares 2, takes the last free one
+    assert bm.num_free_blocks == 0
+    with pytest.raises(pkv.PkvError) as e:
+        bm.evict_sequence(0, 5)
+    assert e.value.status == pkv.PKV_ERR_OUT_OF_BLOCKS
+    for seq, kept in ((7, 1), (0, 0), (0, 13)):
+        with pytest.raises(pkv.PkvError) as e:
+            bm.evict_sequence(seq, kept)
+        assert e.value.status == pkv.PKV_ERR_INVALID_ARG
+    assert bm.num_tokens(0) == 12 and len(bm.block_table(0)) == 3 and bm.ref_count(bm.block_table(0)[0]) == 2
+
+
+# ------------------------------------------------------------------ GPU: selection
+
+def _scores(kind, S, width, seed):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.rand(S, width, generator=g) ** 4
+    if kind == "ties":
+        x = (x * 3).round()
+    elif kind == "equal":
+        x = torch.full_like(x, 0.25)
+    elif kind == "signed":
+        x = (x - 0.2) * torch.tensor([1e-40, 1.0, 1e38])[torch.randint(0, 3, x.shape, generator=g)]
+        x[x.abs() < 1e-42] = -0.0
+    elif kind == "special":
+        pick = torch.randint(0, 8, x.shape, generator=g)
+        for i, v in enumerate((float("nan"), float("inf"), -float("inf"), 0.0, -0.0)):
+            x[pick == i] = v
+    return x
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "signed", "special"])
+@pytest.mark.parametrize("lens,budget,recent", [
+    ([1, 0, 5, 40], 16, 4), ([40, 41, 39, 1000], 40, 40), ([33, 64, 65], 32, 0), ([1, 2, 3], 1, 1), ([7, 100], 1, 0),
+    ([1023, 1024, 1025, 4097], 1000, 17), ([20000, 5], 4096, 100), ([2049], 2048, 2047)])
+def test_select(L, kind, lens, budget, recent):
+    S, width = len(lens), max(lens) + 3
+    x = _scores(kind, S, width, sum(lens))
+    keep, new = pkv.evict_select(x.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), budget, recent)
+    assert pkv.check_device_errors() == 0
+    for s, want in enumerate(select_plain(x, lens, budget, recent)):
+        assert int(new[s]) == len(want) == min(lens[s], budget)
+        assert keep[s].tolist() == want + [-1] * (budget - len(want))
+
+
+@gpu
+def test_select_reports_invalid_lengths(L):
+    x = torch.rand(4, 10, device="cuda")
+    keep = torch.full((4, 3), 77, dtype=torch.int32, device="cuda")
+    new = torch.full((4,), 77, dtype=torch.int32, device="cuda")
+    pkv.evict_select(x, torch.tensor([10, -1, 11, 2], dtype=torch.int32, device="cuda"), 3, 1, keep=keep, new_lens=new)
+    assert pkv.check_device_errors() == pkv.DEVERR_CONTEXT
+    assert new.tolist() == [3, 77, 77, 2] and bool((keep[1:3] == 77).all()) and keep[3].tolist() == [0, 1, -1]
+
+
+# ------------------------------------------------------------------ GPU: compaction
+
+def _fresh_tables(lens, block, first):
+    width = max(1, -(-max(lens) // block))
+    t = torch.full((len(lens), width), -1, dtype=torch.int32)
+    for s, n in enumerate(lens):
+        for j in range(-(-n // block)):
+            t[s, j], first = first, first + 1
+    return t
+
+
+def _compact_plain(arrays, src, dst, kept, block, planes_first):
+    """Moved copies of the arrays [NB, block, ...] or, planes_first, [NB, planes, block, ...]."""
+    moved = [a.clone() for a in arrays]
+    for s, rows in enumerate(kept):
+        for i, p in enumerate(rows):
+            a, b = int(src[s, p // block]), int(dst[s, i // block])
+            for old, new in zip(arrays, moved):
+                if planes_first:
+                    new[b, :, i % block] = old[a, :, p % block]
+                else:
+                    new[b, i % block] = old[a, p % block]
+    return moved
+
+
+COMPACT = [  # lens, budget, recent, heads, block
+    ([40, 17, 100, 3], 16, 4, 2, 16),
+    ([5, 1], 1, 1, 1, 16),
+    ([1000, 700], 333, 50, 3, 7),
+    ([2600], 2500, 100, 1, 256),
+    ([300] * 3, 299, 0, 8, 64),
+]
+
+
+@gpu
+@pytest.mark.parametrize("lens,budget,recent,heads,block", COMPACT)
+@pytest.mark.parametrize("group", [0, 32, 64, 128])
+@pytest.mark.parametrize("in_place", [True, False])
+def test_compact(L, lens, budget, recent, heads, block, group, in_place):
+    g = torch.Generator().manual_seed(sum(lens))
+    kept_lens = [min(n, budget) for n in lens]
+    used = sum(-(-n // block) for n in lens)
+    NB = used + sum(-(-n // block) for n in kept_lens) + 1
+    order = torch.randperm(NB, generator=g).to(torch.int32)
+    src = _fresh_tables(lens, block, 0)
+    dst = src if in_place else _fresh_tables(kept_lens, block, used)
+    src, dst = (torch.where(t >= 0, order[t.clamp(min=0).long()], t) for t in (src, dst))
+    if group == 0:
+        arrays = [torch.randint(-2 ** 15, 2 ** 15, (NB, block, heads, 128), generator=g, dtype=torch.int32).to(torch.int16)
+                  for _ in range(2)]
+    else:
+        arrays = [torch.randint(0, 256, (NB, heads, block, n), generator=g, dtype=torch.int32).to(torch.uint8)
+                  for n in (64, 64, 512 // group, 512 // group)]
+    scores = torch.rand(len(lens), max(lens) + 2, generator=g)
+    kept = select_plain(scores, lens, budget, recent)
+    want = _compact_plain(arrays, src, dst, kept, block, group > 0)
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    sc = scores.cuda()
+    keep, new = pkv.evict_select(sc, cl, budget, recent)
+    new_scores = sc if in_place else torch.full((len(lens), budget + 9), 5.0, device="cuda")
+    dev = [a.cuda() for a in arrays]
+    rest = (src.cuda(), dst.cuda(), keep, new)
+    if group == 0:
+        pkv.evict_compact(*(a.view(torch.bfloat16) for a in dev), *rest, key_scores=sc, dst_key_scores=new_scores)
+    else:
+        params = [a.view(torch.bfloat16).view(NB, heads, block, 128 // group, 2) for a in dev[2:]]
+        pkv.evict_compact_q4((dev[0], params[0]), (dev[1], params[1]), *rest, key_scores=sc, dst_key_scores=new_scores)
+    assert pkv.check_device_errors() == 0
+    for got, w in zip(dev, want):
+        assert torch.equal(got.cpu(), w)
+    for s, rows in enumerate(kept):
+        assert torch.equal(new_scores[s, :len(rows)].cpu(), scores[s][rows])
+        assert bool((new_scores[s, len(rows):] == 0).all())
+
+
+@gpu
+def test_compact_reports_bad_values_and_moves_the_rest(L):
+    NB, block, heads = 8, 16, 1
+    g = torch.Generator().manual_seed(3)
+    k = torch.randint(-2 ** 15, 2 ** 15, (NB, block, heads, 128), generator=g, dtype=torch.int32).to(torch.int16)
+    tables = torch.tensor([[0, 1], [2, 3], [4, 5], [6, NB]], dtype=torch.int32)
+    keep = torch.tensor([[3, 20], [1, 32], [2, 5], [1, 17]], dtype=torch.int32)
+    new = torch.tensor([2, 2, 3, 2], dtype=torch.int32)          # sequence 2: past the budget
+    kc, vc = k.view(torch.bfloat16).cuda(), k.view(torch.bfloat16).cuda()
+    pkv.evict_compact(kc, vc, tables.cuda(), tables.cuda(), keep.cuda(), new.cuda())
+    assert pkv.check_device_errors() == pkv.DEVERR_CONTEXT | pkv.DEVERR_BLOCK
+    want = k.clone()
+    want[0, 0], want[0, 1] = k[0, 3], k[1, 4]
+    want[2, 0] = k[2, 1]
+    want[6, 0] = k[6, 1]
+    assert torch.equal(kc.view(torch.int16).cpu(), want) and torch.equal(vc.view(torch.int16).cpu(), want)
+
+
+# ------------------------------------------------------------------ GPU: accumulated weights over a bf16 cache
+
+def _bf16_case(seed, lens, heads, block):
+    """A bf16 cache whose unused rows hold NaN: (k, v, tables, k rows, v rows) with rows [P, H, 128] per sequence."""
+    g = torch.Generator().manual_seed(seed)
+    tables = _fresh_tables(lens, block, 0)
+    NB = int(tables.max()) + 2
+    order = torch.randperm(NB, generator=g).to(torch.int32)
+    tables = torch.where(tables >= 0, order[tables.clamp(min=0).long()], tables)
+    caches, rows = [], []
+    for _ in range(2):
+        c = torch.full((NB, block, heads, 128), float("nan"), dtype=torch.bfloat16)
+        mine = []
+        for s, n in enumerate(lens):
+            x = torch.randn(n, heads, 128, generator=g).to(torch.bfloat16)
+            p = torch.arange(n)
+            c[tables[s].long()[p // block], p % block] = x
+            mine.append(x)
+        caches.append(c)
+        rows.append(mine)
+    return caches[0], caches[1], tables, rows[0], rows[1]
+
+
+@gpu
+@pytest.mark.parametrize("lens,heads,gqa,block,window", [
+    ([1], 1, 1, 16, 0), ([17, 64, 100, 128], 8, 2, 16, 0), ([640] * 3, 8, 2, 256, 0), ([5, 900, 33], 2, 4, 48, 0),
+    ([4000], 4, 2, 64, 0), ([300, 7, 1000], 8, 1, 32, 100), ([2000, 3], 2, 2, 16, 1)])
+def test_scored_decode(L, lens, heads, gqa, block, window):
+    pkv.decode_set_config(0, 0)
+    k, v, tables, kr, vr = _bf16_case(sum(lens), lens, heads, block)
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(len(lens), heads * gqa, 128, generator=g).to(torch.bfloat16)
+    width = max(lens) + 4
+    scores = torch.full((len(lens), width), 0.25, device="cuda")
+    args = (q.cuda(), k.cuda(), v.cuda(), tables.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), max(lens), SCALE)
+    o, l = pkv.paged_decode_attn_scores(*args, scores, sliding_window=window)
+    o0, l0 = pkv.paged_decode_attn(*args, sliding_window=window)
+    pkv.paged_decode_attn_scores(*args, scores, sliding_window=window, with_lse=False)
+    assert pkv.check_device_errors() == 0
+    assert torch.equal(o, o0) and torch.equal(l, l0)        # the attention itself is the plain call's
+    got = scores.cpu().double()
+    for s, n in enumerate(lens):
+        first = max(0, n - window) if window else 0
+        want, tol = torch.zeros(n, dtype=torch.float64), torch.zeros(n, dtype=torch.float64)
+        for h in range(heads * gqa):
+            ks = kr[s][:, h // gqa].double()
+            _, lse, w, _, qk = Q.attend(q[s, h:h + 1].double(), ks, vr[s][:, h // gqa].double(), SCALE, [first], [n - 1])
+            want += w[0]
+            # exp(z - lse): both within the lse's tolerance
+            tol += w[0] * 2 * Q.lse_tolerance(lse, qk, n) + 2.0 ** -20 * w[0]
+        # two calls add the weight twice; each addition rounds once
+        err = (got[s, :n] - 0.25 - 2 * want).abs()
+        assert bool((err <= 2 * tol + 2 * Q.U32 * (0.25 + 2 * want)).all()), float(err.max())
+        assert bool((got[s, n:] == 0.25).all()) and bool((got[s, :first] == 0.25).all())
+
+
+@gpu
+def test_scored_decode_adds_nothing_after_a_timeout(L):
+    k, v, tables, _, _ = _bf16_case(1, [50, 20], 2, 16)
+    args = (torch.randn(2, 4, 128).to(torch.bfloat16).cuda(), k.cuda(), v.cuda(), tables.cuda(),
+            torch.tensor([50, 20], dtype=torch.int32, device="cuda"), 50, SCALE)
+    scores = torch.zeros(2, 50, device="cuda")
+    pkv.raise_device_errors(pkv.DEVERR_TIMEOUT)
+    pkv.paged_decode_attn_scores(*args, scores)
+    assert pkv.check_device_errors() == pkv.DEVERR_TIMEOUT
+    assert bool((scores == 0).all())
+    pkv.paged_decode_attn_scores(*args, scores)
+    assert pkv.check_device_errors() == 0
+    assert bool((scores[0] > 0).all())
+
+
+# ------------------------------------------------------------------ GPU: the chain
+
+@gpu
+@pytest.mark.parametrize("q4", [False, True])
+def test_engine_steps_with_eviction(L, q4):
+    """Two sequences that share a prefix, driven by the block manager: prefill,
+    decode steps that accumulate weights, eviction of the longer one into fresh and
+    own blocks, and decode on. The attention after it equals plain attention over
+    exactly the kept rows, and the other sequence sees nothing of it."""
+    heads, gqa, block, group, budget, recent = 2, 2, 16, 32, 50, 12
+    g = torch.Generator().manual_seed(8)
+    bm = pkv.BlockManager(40, block)
+    prompts = [np.arange(100, dtype=np.int32), np.concatenate([np.arange(48), 900 + np.arange(30)]).astype(np.int32)]
+    if q4:
+        kc, vc = (pkv.new_q4_cache(40, block, heads, group) for _ in range(2))
+    else:
+        kc, vc = (torch.full((40, block, heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    rows = [[], []]                      # each sequence's (k, v) rows in logical order, as the cache holds them
+
+    def kept_value(x):
+        return Q.values(*Q.quantise(x, group)) if q4 else x.double()
+
+    def store(k, v, slots):
+        put = pkv.kv_store_q4 if q4 else pkv.kv_store
+        put(k.cuda(), v.cuda(), kc, vc, torch.from_numpy(slots).cuda())
+
+    shared = torch.randn(2, 48, heads, 128, generator=g).to(torch.bfloat16)
+    for s, prompt in enumerate(prompts):
+        cached = bm.add_sequence(s, prompt)
+        assert cached == (0, 48)[s]
+        n = len(prompt) - (48 if s else 0)
+        new = torch.randn(2, n, heads, 128, generator=g).to(torch.bfloat16)
+        if s == 0:
+            new[:, :48] = shared
+            rows[s] = [new[0], new[1]]
+        else:
+            rows[s] = [torch.cat([shared[i], new[i]]) for i in range(2)]
+        store(new[0], new[1], bm.slots(s, cached, n))
+
+    def decode(scores):
+        for s in range(2):
+            bm.append_token(s, 7)
+            x = torch.randn(2, 1, heads, 128, generator=g).to(torch.bfloat16)
+            rows[s] = [torch.cat([rows[s][i], x[i]]) for i in range(2)]
+            store(x[0], x[1], bm.slots(s, bm.num_tokens(s) - 1, 1))
+        lens = [bm.num_tokens(s) for s in range(2)]
+        tables = torch.from_numpy(bm.block_tables([0, 1], 8)).cuda()
+        q = torch.randn(2, heads * gqa, 128, generator=g).to(torch.bfloat16)
+        cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        if q4:
+            o, _ = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, tables, cl, 128, SCALE, key_scores=scores)
+        else:
+            o, _ = pkv.paged_decode_attn_scores(q.cuda(), kc, vc, tables, cl, 128, SCALE, scores)
+        for s in range(2):
+            assert lens[s] == rows[s][0].shape[0]
+            for h in range(heads * gqa):
+                k, v = (kept_value(rows[s][i][:, h // gqa]) for i in range(2))
+                want, _, _, wv, _ = Q.attend(q[s, h:h + 1].double(), k, v, SCALE, [0], [lens[s] - 1])
+                err = (o[s, h].cpu().double() - want[0]).abs()
+                assert bool((err <= Q.out_tolerance(want[0], wv[0])).all()), (s, h, float(err.max()))
+        return lens
+
+    scores = torch.zeros(2, 128, device="cuda")
+    for _ in range(3):
+        lens = decode(scores)
+    # evict sequence 0, in a call of its own
+    src = torch.from_numpy(bm.block_table(0, 8)[None]).cuda()
+    row = scores[:1].clone()
+    before = row.cpu()
+    keep, new = pkv.evict_select(row, torch.tensor(lens[:1], dtype=torch.int32, device="cuda"), budget, recent)
+    bm.evict_sequence(0, budget)
+    dst = torch.from_numpy(bm.block_table(0, 8)[None]).cuda()
+    assert bool((dst[0, :3] != src[0, :3]).all()) and int(dst[0, 3]) == int(src[0, 3])
+    (pkv.evict_compact_q4 if q4 else pkv.evict_compact)(kc, vc, src, dst, keep, new, key_scores=row, dst_key_scores=row)
+    scores[0] = row[0]
+    assert new.tolist() == [budget]
+    kept = keep[0].long().cpu()
+    assert kept.tolist() == select_plain(before, lens[:1], budget, recent)[0]
+    rows[0] = [x[kept] for x in rows[0]]
+    for _ in range(20):                 # past the end of a block
+        decode(scores)
+    assert pkv.check_device_errors() == 0

@@ -1,6 +1,5 @@
 """The 4-bit cache: quantising store, read-back, decode and prefill, against the
 plain 64-bit implementation in q4_plain.py; and the refusals of each call."""
-import ctypes
 import math
 
 import pytest
