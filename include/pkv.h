@@ -328,7 +328,7 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
  * Quantise the new tokens' K/V rows into their slots: pkv_kv_store for a 4-bit
  * cache, with the same slot_mapping semantics and errors (-1 skips the token;
  * another value outside the pool is skipped and raises PKV_DEVERR_SLOT; two
- * tokens with the same slot race).
+ * tokens with the same slot race). num_tokens * num_kv_heads must be below 2^31.
  *   k, v  device bf16 [num_tokens, num_kv_heads, 128]
  */
 pkv_status pkv_kv_store_q4(const void *k, const void *v, void *k_codes, void *k_params,

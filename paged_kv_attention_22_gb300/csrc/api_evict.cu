@@ -27,7 +27,7 @@ pkv_status compact(pkv::EvictCompactArgs &a, const int32_t *src_tables, int32_t 
   // one score array under two row strides would be overwritten while it is read
   if (key_scores != nullptr && key_scores == dst_key_scores && score_stride != dst_score_stride)
     return PKV_ERR_INVALID_ARG;
-  if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || budget > (1 << 29)) return PKV_ERR_UNSUPPORTED;
   if (num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   int sms = 0;
@@ -47,6 +47,7 @@ pkv_status compact(pkv::EvictCompactArgs &a, const int32_t *src_tables, int32_t 
   a.num_seqs = num_seqs;
   a.block_size = block_size;
   a.num_blocks = static_cast<int32_t>(num_blocks);
+  a.num_sms = sms;
   cudaError_t e = pkv::launch_evict_compact(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "evict_compact launch");
   return PKV_OK;

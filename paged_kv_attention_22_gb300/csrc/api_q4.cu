@@ -127,6 +127,7 @@ pkv_status pkv_kv_store_q4(const void *k, const void *v, void *k_codes, void *k_
   if (num_tokens < 0 || !aligned16(k) || !aligned16(v)) return PKV_ERR_INVALID_ARG;
   if (num_tokens == 0) return PKV_OK;
   if (k == nullptr || v == nullptr || slot_mapping == nullptr) return PKV_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_tokens) * num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   a.k = k;
   a.v = v;
   a.slots = slot_mapping;
@@ -147,6 +148,7 @@ pkv_status pkv_kv_load_q4(const void *k_codes, const void *k_params, const void 
   if (num_tokens < 0 || !aligned16(k) || !aligned16(v)) return PKV_ERR_INVALID_ARG;
   if (num_tokens == 0) return PKV_OK;
   if (k == nullptr || v == nullptr || slots == nullptr) return PKV_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(num_tokens) * num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   a.k_out = k;
   a.v_out = v;
   a.slots = slots;
@@ -247,7 +249,9 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
   if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
   if (!aligned16(q) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
   const PrefillWorkspace w = prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads);
+  // workspace rows are 32-bit TMA coordinates; units of 16 keys x heads are counted in 31 bits
   if (w.num_blocks * pkv::kQ4PrefillBlock > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(max_seqlen_k) / 16 + 1) * num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (workspace == nullptr || workspace_bytes < w.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
   int sms = 0;

@@ -3,17 +3,21 @@
 // (evict_compact).
 //
 // Selection. One CTA a sequence finds the want-th largest score with a radix
-// select over the scores' order-preserving 32-bit keys, eight bits a pass, then
-// writes the kept positions in ascending order: each warp owns a contiguous
-// range of positions, counts the keys above and at the threshold, and after one
-// scan over the warps writes its own with ballots. Equal scores are taken from
-// the lowest position on.
+// select over the scores' order-preserving 32-bit keys, eight bits a pass (the
+// keys stay in shared memory while they fit), until the bin that holds it is
+// taken whole. It then writes the kept positions in ascending order: each warp
+// owns a contiguous range of positions, counts the keys above and at the
+// threshold, and after one scan over the warps writes its own with ballots. Equal
+// scores are taken from the lowest position on.
 //
-// Compaction. Row i of the destination is row keep[i] >= i of the source, so
-// that in place nothing is overwritten before it has been read when the rows go
-// in order: a CTA owns a slice (up to 64 bytes) of every row of one sequence
-// and moves its rows in chunks, loading a whole chunk before it stores any of
-// it. Slices are independent, which is what spreads one sequence over the SMs.
+// Compaction, bound by HBM bandwidth: every kept row is read and written once.
+// Row i of the destination is row keep[i] >= i of the source. A sequence whose
+// destination blocks are all fresh has no hazard: warps move whole rows, in any
+// order. With a block in both tables (in place), nothing is overwritten before
+// it has been read as long as the rows go in order: a CTA then owns a slice (up
+// to kSliceBytes) of every row and moves its rows in chunks, loading a whole
+// chunk before it stores any of it; slices are independent. Which of the two
+// holds is found on the device, from the tables.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -28,7 +32,8 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 256;
-constexpr int kHistCopies = 8;  // histograms a warp group of four shares, against contention
+constexpr int kHistCopies = 8;  // histograms, each shared by four warps, against contention
+constexpr size_t kSelMaxKeyBytes = 200 * 1024;  // beside the histograms
 
 struct SelectParams {
   const float *key_scores;
@@ -45,9 +50,12 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// kCached: the competing positions' keys fit in dynamic shared memory.
+template <bool kCached>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
+  extern __shared__ uint32_t s_keys[];
   __shared__ uint32_t hist[kHistCopies][kBins];
-  __shared__ uint32_t s_prefix, s_want;
+  __shared__ uint32_t s_prefix, s_left, s_whole;
   __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
   griddep_wait();  // inputs written by the previous kernel are visible from here on
   griddep_launch_dependents();
@@ -70,6 +78,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     return;
   }
   if (want == 0) return;
+  auto key_of = [&](int i) { return kCached ? s_keys[i] : score_key(score[i]); };
 
   // ---- the want-th largest key, most significant digit first
   uint32_t prefix = 0, left = want;  // keys above the prefix are in; left more come from below it
@@ -78,9 +87,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     for (int i = tid; i < kHistCopies * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
     __syncthreads();
     uint32_t *h = hist[warp % kHistCopies];
-    for (int i = tid; i < old; i += kSelThreads) {
-      const uint32_t k = score_key(score[i]);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&h[(k >> shift) & 255u], 1u);
+    if (shift == 24) {
+#pragma unroll 4
+      for (int i = tid; i < old; i += kSelThreads) {
+        const uint32_t k = score_key(score[i]);
+        if (kCached) s_keys[i] = k;
+        atomicAdd(&h[k >> 24], 1u);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = tid; i < old; i += kSelThreads) {
+        const uint32_t k = key_of(i);
+        if ((k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&h[(k >> shift) & 255u], 1u);
+      }
     }
     __syncthreads();
     if (warp == 0) {
@@ -89,6 +108,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         n[j] = 0;
+#pragma unroll
         for (int c = 0; c < kHistCopies; ++c) n[j] += hist[c][255 - 8 * lane - j];
         sum += n[j];
       }
@@ -103,14 +123,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
       for (int j = 0; j < 8; ++j) {
         if (above < left && left <= above + n[j]) {
           s_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - j) << shift);
-          s_want = left - above;
+          s_left = left - above;
+          s_whole = left == above + n[j];
         }
         above += n[j];
       }
     }
     __syncthreads();
     prefix = s_prefix;
-    left = s_want;
+    left = s_left;
+    if (s_whole) {
+      // every key with this prefix stays: those above prefix - 1 (the prefix is
+      // not 0, or all positions would stay, with want < old)
+      prefix -= 1;
+      left = 0;
+      break;
+    }
   }
 
   // ---- kept positions in order: keys above the threshold, and the first
@@ -118,8 +146,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
   const int per_warp = ((old + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
   const int begin = min(old, warp * per_warp), end = min(old, begin + per_warp);
   int gt = 0, eq = 0;
+#pragma unroll 4
   for (int i = begin + lane; i - lane < end; i += 32) {
-    const uint32_t k = i < end ? score_key(score[i]) : 0u;
+    const uint32_t k = i < end ? key_of(i) : 0u;
     gt += __popc(__ballot_sync(0xffffffffu, i < end && k > prefix));
     eq += __popc(__ballot_sync(0xffffffffu, i < end && k == prefix));
   }
@@ -128,19 +157,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     s_eq[warp] = eq;
   }
   __syncthreads();
-  int gt0 = 0, eq0 = 0;  // in the warps before
-  for (int w = 0; w < warp; ++w) {
-    gt0 += s_gt[w];
-    eq0 += s_eq[w];
-  }
+  // in the warps before this one
+  int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+  int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
   const uint32_t below = (1u << lane) - 1u;
+  const int quota = static_cast<int>(left);
+#pragma unroll 2
   for (int i = begin + lane; i - lane < end; i += 32) {
-    const uint32_t k = i < end ? score_key(score[i]) : 0u;
+    const uint32_t k = i < end ? key_of(i) : 0u;
     const uint32_t bg = __ballot_sync(0xffffffffu, i < end && k > prefix);
     const uint32_t be = __ballot_sync(0xffffffffu, i < end && k == prefix);
     const int my_gt = gt0 + __popc(bg & below), my_eq = eq0 + __popc(be & below);
-    const bool in = ((bg >> lane) & 1u) || (((be >> lane) & 1u) && my_eq < static_cast<int>(left));
-    if (in) keep[my_gt + min(my_eq, static_cast<int>(left))] = i;
+    const bool in = ((bg >> lane) & 1u) || (((be >> lane) & 1u) && my_eq < quota);
+    if (in) keep[my_gt + min(my_eq, quota)] = i;
     gt0 += __popc(bg);
     eq0 += __popc(be);
   }
@@ -149,7 +178,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 // ---------------------------------------------------------------- compaction
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;       // rows a thread has in flight
+constexpr int kMoveUnroll = 8;       // pieces a thread has in flight
+constexpr int kRowsPerWarp = 4;      // rows a warp moves together, without hazards
 
 struct CompactParams {
   RowArray arrays[kMaxRowArrays];
@@ -158,7 +188,8 @@ struct CompactParams {
   const float *key_scores;           // [S, score_stride] or null
   float *dst_key_scores;             // [S, dst_score_stride]
   int64_t score_stride, dst_score_stride;
-  int32_t src_max_blocks, dst_max_blocks, budget, block_size, num_blocks;
+  int32_t src_max_blocks, dst_max_blocks, budget, num_blocks;
+  FastDiv block;
 };
 
 template <int N> struct Piece;
@@ -166,12 +197,11 @@ template <> struct Piece<16> { using T = uint4; };
 template <> struct Piece<8> { using T = uint2; };
 template <> struct Piece<4> { using T = uint32_t; };
 
-// Byte offset of position pos's row of one plane, or -1 (with its bit raised)
-// for a position or block that does not exist.
-__device__ __forceinline__ int64_t row_offset(const CompactParams &p, const int32_t *table, int max_blocks,
-                                              const RowArray &a, int plane, int pos) {
-  const int j = pos / p.block_size;
-  if (pos < 0 || j >= max_blocks) {
+// Slot of position pos in a table, or -1 (with its bit raised) for a position or
+// block that does not exist.
+__device__ __forceinline__ int64_t slot_of(const CompactParams &p, const int32_t *table, int max_blocks, int pos) {
+  const int j = pos < 0 ? max_blocks : static_cast<int>(fast_quotient(pos, p.block));
+  if (j >= max_blocks) {
     atomicOr(&g_evict_errors, kErrContext);
     return -1;
   }
@@ -180,7 +210,15 @@ __device__ __forceinline__ int64_t row_offset(const CompactParams &p, const int3
     atomicOr(&g_evict_errors, kErrBlock);
     return -1;
   }
-  return ((static_cast<int64_t>(blk) * a.planes + plane) * p.block_size + (pos - j * p.block_size)) * a.row_bytes;
+  return static_cast<int64_t>(blk) * p.block.d + (pos - j * static_cast<int>(p.block.d));
+}
+
+// Byte offset of a slot's row of one plane.
+__device__ __forceinline__ int64_t row_offset(const CompactParams &p, const RowArray &a, int plane, int64_t slot) {
+  if (a.planes == 1) return slot * a.row_bytes;
+  const uint32_t blk = fast_quotient(static_cast<uint32_t>(slot), p.block);
+  return ((static_cast<int64_t>(blk) * a.planes + plane) * p.block.d + (slot - static_cast<int64_t>(blk) * p.block.d)) *
+         a.row_bytes;
 }
 
 // Move `bytes` bytes at `at` of every kept row of one plane, N bytes a thread.
@@ -202,16 +240,48 @@ __device__ void move_slice(const CompactParams &p, const RowArray &a, int plane,
       const int i = i0 + u * rows + r;
       to[u] = -1;
       if (r < rows && i < n) {
-        const int64_t from = row_offset(p, src, p.src_max_blocks, a, plane, keep[i]);
-        to[u] = row_offset(p, dst, p.dst_max_blocks, a, plane, i);
-        if (from < 0 || from == to[u]) to[u] = -1;
-        if (to[u] >= 0) x[u] = *reinterpret_cast<const T *>(base + from + c);
+        const int64_t from = slot_of(p, src, p.src_max_blocks, keep[i]);
+        const int64_t into = slot_of(p, dst, p.dst_max_blocks, i);
+        if (from >= 0 && into >= 0 && from != into) {
+          to[u] = row_offset(p, a, plane, into);
+          x[u] = *reinterpret_cast<const T *>(base + row_offset(p, a, plane, from) + c);
+        }
       }
     }
     __syncthreads();  // the whole chunk is loaded: its places may be overwritten
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u)
       if (to[u] >= 0) *reinterpret_cast<T *>(base + to[u] + c) = x[u];
+  }
+}
+
+// The pieces of N bytes of kRowsPerWarp rows of one array: lane by lane, all
+// planes of a row together. from / to hold the rows' slots (-1: not moved).
+template <int N>
+__device__ __forceinline__ void move_rows(const CompactParams &p, const RowArray &a, const int64_t (&from)[kRowsPerWarp],
+                                          const int64_t (&to)[kRowsPerWarp], int lane) {
+  using T = typename Piece<N>::T;
+  const int per_plane = a.row_bytes / N, pieces = a.planes * per_plane;
+  uint8_t *base = static_cast<uint8_t *>(a.base);
+  for (int i0 = lane; i0 < pieces; i0 += 64) {
+    T x[2][kRowsPerWarp];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int i = i0 + 32 * v;
+      const int plane = a.planes == 1 ? 0 : i / per_plane, c = (i - plane * per_plane) * N;
+#pragma unroll
+      for (int u = 0; u < kRowsPerWarp; ++u)
+        if (i < pieces && to[u] >= 0)
+          x[v][u] = __ldcs(reinterpret_cast<const T *>(base + row_offset(p, a, plane, from[u]) + c));
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int i = i0 + 32 * v;
+      const int plane = a.planes == 1 ? 0 : i / per_plane, c = (i - plane * per_plane) * N;
+#pragma unroll
+      for (int u = 0; u < kRowsPerWarp; ++u)
+        if (i < pieces && to[u] >= 0) *reinterpret_cast<T *>(base + row_offset(p, a, plane, to[u]) + c) = x[v][u];
+    }
   }
 }
 
@@ -239,32 +309,70 @@ __device__ void move_scores(const CompactParams &p, int s, int n) {
   for (int64_t i = n + static_cast<int64_t>(threadIdx.x); i < p.dst_score_stride; i += kMoveThreads) dst[i] = 0.f;
 }
 
-// Grid (slices of all arrays, then one for the scores; sequences).
+// Grid (CTAs a sequence, the last one for the scores if there are any; sequences).
 __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int s = blockIdx.y;
   const int n = p.new_lens[s];
-  if (n < 0 || n > p.budget || n > static_cast<int64_t>(p.dst_max_blocks) * p.block_size ||
+  if (n < 0 || n > p.budget || n > static_cast<int64_t>(p.dst_max_blocks) * p.block.d ||
       (p.key_scores != nullptr && n > p.dst_score_stride)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_evict_errors, kErrContext);
     return;
   }
-  int slice = blockIdx.x;
+  const int movers = static_cast<int>(gridDim.x) - (p.key_scores != nullptr ? 1 : 0);
+  if (static_cast<int>(blockIdx.x) >= movers) {
+    move_scores(p, s, n);
+    return;
+  }
+  const int32_t *src = p.src_tables + static_cast<int64_t>(s) * p.src_max_blocks;
+  const int32_t *dst = p.dst_tables + static_cast<int64_t>(s) * p.dst_max_blocks;
+  bool in_place = false;
+  const int shared_blocks = min(p.src_max_blocks, static_cast<int>((n + p.block.d - 1) / p.block.d));
+  for (int j = threadIdx.x; j < shared_blocks; j += kMoveThreads) in_place |= src[j] == dst[j];
+  if (!__syncthreads_or(in_place)) {
+    const int32_t *keep = p.keep + static_cast<int64_t>(s) * p.budget;
+    const int lane = threadIdx.x & 31;
+    // an item is kRowsPerWarp rows of one array
+    const int items = (n + kRowsPerWarp - 1) / kRowsPerWarp * p.num_arrays;
+    for (int item = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); item < items;
+         item += movers * (kMoveThreads / 32)) {
+      const int quad = item / p.num_arrays, i0 = quad * kRowsPerWarp;
+      // lane u < kRowsPerWarp looks up row u
+      int64_t f = -1, t = -1;
+      if (lane < kRowsPerWarp && i0 + lane < n) {
+        f = slot_of(p, src, p.src_max_blocks, keep[i0 + lane]);
+        t = slot_of(p, dst, p.dst_max_blocks, i0 + lane);
+        if (f < 0) t = -1;
+      }
+      int64_t from[kRowsPerWarp], to[kRowsPerWarp];
+#pragma unroll
+      for (int u = 0; u < kRowsPerWarp; ++u) {
+        from[u] = __shfl_sync(0xffffffffu, f, u);
+        to[u] = __shfl_sync(0xffffffffu, t, u);
+      }
+      const RowArray &a = p.arrays[item - quad * p.num_arrays];
+      if (a.row_bytes % 16 == 0) move_rows<16>(p, a, from, to, lane);
+      else if (a.row_bytes % 8 == 0) move_rows<8>(p, a, from, to, lane);
+      else move_rows<4>(p, a, from, to, lane);
+    }
+    return;
+  }
+  // in place: slices of all arrays in turn
+  int first = blockIdx.x;
 #pragma unroll 1
   for (int k = 0; k < p.num_arrays; ++k) {
     const RowArray &a = p.arrays[k];
-    const int per_plane = a.row_bytes > kSliceBytes ? a.row_bytes / kSliceBytes : 1;
-    if (slice < a.planes * per_plane) {
-      const int bytes = a.row_bytes / per_plane, plane = slice / per_plane, at = slice % per_plane * bytes;
+    const int per_plane = a.row_bytes > kSliceBytes ? a.row_bytes / kSliceBytes : 1, slices = a.planes * per_plane;
+    const int bytes = a.row_bytes / per_plane;
+    for (; first < slices; first += movers) {
+      const int plane = first / per_plane, at = (first - plane * per_plane) * bytes;
       if (bytes % 16 == 0) move_slice<16>(p, a, plane, at, bytes, s, n);
       else if (bytes % 8 == 0) move_slice<8>(p, a, plane, at, bytes, s, n);
       else move_slice<4>(p, a, plane, at, bytes, s, n);
-      return;
     }
-    slice -= a.planes * per_plane;
+    first -= slices;
   }
-  move_scores(p, s, n);
 }
 
 }  // namespace
@@ -279,12 +387,19 @@ cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t stream) {
   p.max_context_len = a.max_context_len;
   p.budget = a.budget;
   p.recent = a.recent;
-  return launch_pdl(evict_select_kernel, dim3(a.num_seqs), dim3(kSelThreads), 0, stream, p);
+  // the largest number of competing positions whose keys a CTA can hold
+  const size_t smem = static_cast<size_t>(a.max_context_len) * sizeof(uint32_t);
+  if (smem > kSelMaxKeyBytes)
+    return launch_pdl(evict_select_kernel<false>, dim3(a.num_seqs), dim3(kSelThreads), 0, stream, p);
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSelMaxKeyBytes));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(evict_select_kernel<true>, dim3(a.num_seqs), dim3(kSelThreads), smem, stream, p);
 }
 
 cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream) {
   CompactParams p;
-  int64_t slices = a.key_scores != nullptr ? 1 : 0;
+  int64_t slices = 0;
   p.num_arrays = a.num_arrays;
   for (int k = 0; k < a.num_arrays; ++k) {
     p.arrays[k] = a.arrays[k];
@@ -302,10 +417,17 @@ cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream)
   p.src_max_blocks = a.src_max_blocks;
   p.dst_max_blocks = a.dst_max_blocks;
   p.budget = a.budget;
-  p.block_size = a.block_size;
   p.num_blocks = a.num_blocks;
-  return launch_pdl(evict_compact_kernel, dim3(static_cast<unsigned>(slices), a.num_seqs), dim3(kMoveThreads), 0,
-                    stream, p);
+  p.block = fast_div(a.block_size);
+  // CTAs a sequence: no more than its slices (in place) or its rows call for,
+  // and some 8 an SM in all, so that many sequences do not queue idle CTAs
+  const int64_t items = (static_cast<int64_t>(a.budget) + kRowsPerWarp - 1) / kRowsPerWarp * a.num_arrays;
+  const int64_t rows = (items + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
+  int64_t movers = slices > rows ? slices : rows;
+  const int64_t cap = (8 * static_cast<int64_t>(a.num_sms) + a.num_seqs - 1) / a.num_seqs;
+  if (movers > cap) movers = cap;
+  return launch_pdl(evict_compact_kernel, dim3(static_cast<unsigned>(movers + (a.key_scores != nullptr ? 1 : 0)), a.num_seqs),
+                    dim3(kMoveThreads), 0, stream, p);
 }
 
 cudaError_t evict_error_word(uint32_t **word) {

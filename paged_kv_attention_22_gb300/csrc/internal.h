@@ -137,6 +137,25 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
 cudaError_t take_prefill_errors(cudaStream_t stream, uint32_t *flags);
 cudaError_t prefill_error_word(uint32_t **word);
 
+// Division of a non-negative n < 2^31 by a fixed d >= 1 as a multiply and a
+// shift: with l = ceil(log2 d) and mul = ceil(2^(31 + l) / d), n * mul / 2^(31 + l)
+// exceeds n / d by less than n 2^l / (2^(31 + l) d) < 1 / d, so its floor is the
+// quotient's.
+struct FastDiv {
+  uint32_t mul, shift, d;
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t{1} << l) < d) ++l;
+  const uint64_t mul = ((uint64_t{1} << (31 + l)) + d - 1) / d;  // < 2^32, since d > 2^(l - 1)
+  return {static_cast<uint32_t>(mul), 31 + l, d};
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ uint32_t fast_quotient(uint32_t n, const FastDiv &f) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(n) * f.mul) >> f.shift);
+}
+#endif
+
 // ---------------------------------------------------------------- 4-bit cache
 struct Q4CacheArgs {
   void *k_codes, *k_params, *v_codes, *v_params;
@@ -212,7 +231,7 @@ struct EvictCompactArgs {
   const float *key_scores;
   float *dst_key_scores;
   int64_t score_stride, dst_score_stride;
-  int32_t src_max_blocks, dst_max_blocks, budget, num_seqs, block_size, num_blocks;
+  int32_t src_max_blocks, dst_max_blocks, budget, num_seqs, block_size, num_blocks, num_sms;
 };
 cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream);
 cudaError_t evict_error_word(uint32_t **word);

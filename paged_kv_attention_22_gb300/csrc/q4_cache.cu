@@ -5,8 +5,11 @@
 //
 // Half a warp handles one row of 128 values: eight values a lane, so that a
 // lane's codes are one 32-bit word; lanes 0-15 take a (token, head)'s K row and
-// lanes 16-31 its V row. Each warp has kRowsInFlight such pairs' loads in
-// flight.
+// lanes 16-31 its V row. A warp has several such pairs' loads in flight.
+//
+// All three are copies with some arithmetic: HBM bandwidth bounds them, once the
+// arithmetic is short enough (the store spends about six packed operations on
+// two values) and indices are found without 64-bit divisions.
 #include "internal.h"
 #include "q4.cuh"
 
@@ -17,38 +20,52 @@ static __device__ uint32_t g_q4_cache_errors;
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRowsInFlight = 4;
+constexpr int kStoreRows = 4;  // (token, head) pairs whose loads a warp has in flight
+constexpr int kLoadRows = 8;
+
+// The smaller of each half; a NaN in either operand wins.
+__device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// (smallest, -largest) of the eight values of x, as a bf16 pair.
+__device__ __forceinline__ uint32_t extremes(const uint4 x) {
+  constexpr uint32_t kSigns = 0x80008000u;
+  const uint32_t lo = min_nan_bf16x2(min_nan_bf16x2(x.x, x.y), min_nan_bf16x2(x.z, x.w));
+  const uint32_t hi = min_nan_bf16x2(min_nan_bf16x2(x.x ^ kSigns, x.y ^ kSigns),
+                                     min_nan_bf16x2(x.z ^ kSigns, x.w ^ kSigns));
+  return min_nan_bf16x2(q4_low_halves(lo, hi), q4_high_halves(lo, hi));
+}
 
 // (scale, offset) of a group with these extremes, as a params word:
 //   scale  = bf16(fp32(hi - lo) * fp32(1/15)), 0 if that product is below 2^-100
 //   offset = bf16(lo - 16 scale), the value of a code -16
 // A group whose spread or offset is not finite (a NaN or an infinity among its
 // values, or too wide a range) gets scale 0 and offset NaN.
-__device__ __forceinline__ uint32_t group_params(float lo, float hi, bool nan) {
+__device__ __forceinline__ uint32_t group_params(float lo, float hi) {
   const float range = hi - lo;
   float s = range * (1.0f / 15.0f);
   if (s < 0x1p-100f) s = 0.f;
   s = __bfloat162float(__float2bfloat16_rn(s));
   const float b = __bfloat162float(__float2bfloat16_rn(__fsub_rn(lo + 0.f, __fmul_rn(16.f, s))));
-  if (nan || !(fabsf(range) <= 3.4e38f) || !(fabsf(b) <= 3.4e38f)) return 0x7FC00000u;
+  if (!(fabsf(range) <= 3.4e38f) || !(fabsf(b) <= 3.4e38f)) return 0x7FC00000u;
   return pack_bf16x2(s, b);
 }
 
-// Codes of the eight values of x (four words of two bf16): with t = fp32(x - b),
-// n = clamp(floor(t / s + 1/2) - 16, 0, 15). The quotient is only estimated
-// (t * (1/s), rounded to the nearest integer c); the two comparisons with the
-// thresholds (c - 1/2) s and (c + 1/2) s, which are exact in fp32 (s has 8
-// bits, c at most 6), settle it.
-__device__ __forceinline__ uint32_t codes_of(const uint4 x, uint32_t pw) {
-  const float s = bf16lo(pw), b = bf16hi(pw);
-  if (s == 0.f) return 0u;
+// Codes of eight values, n = clamp(floor(t / s + 1/2) - 16, 0, 15) with
+// t = fp32(x - b), one value at a time. The quotient is only estimated and
+// rounded to the nearest integer c; the two comparisons with the thresholds
+// (c - 1/2) s and (c + 1/2) s, which are exact in fp32 (s has 8 bits, c at most
+// 12 here), settle it.
+__device__ __noinline__ uint32_t codes_one_by_one(const uint4 x, float s, float b) {
   const float r = 1.f / s, h = 0.5f * s;
   const uint32_t wx[4] = {x.x, x.y, x.z, x.w};
   uint32_t codes = 0;
-#pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float t = ((i & 1) ? bf16hi(wx[i >> 1]) : bf16lo(wx[i >> 1])) - b;
-    float c = rintf(t * r);
+    float c = rintf(fminf(fmaxf(t * r, 0.f), 100.f));
     const float at = c * s;
     if (t >= at + h) c += 1.f;
     else if (t < at - h) c -= 1.f;
@@ -58,22 +75,48 @@ __device__ __forceinline__ uint32_t codes_of(const uint4 x, uint32_t pw) {
   return codes;
 }
 
+// The same, two values at a time. y = t r' + M, with r' a little above 1 / s
+// and M = 2^23 + 2^22 - 16, rounds the quotient to an integer c in its low
+// mantissa bits, which then hold the code. r' exceeds the reciprocal by 2^-19,
+// more than the estimate's own error, so that a half (common: the inputs have 8
+// bits) rounds up and a quotient at most 2^-14 below one may do so wrongly: the
+// remainder t - c s, exact in fp32, is then below -s / 2 and the code one less.
+// Only groups whose offset's rounding pushes an extreme past the code range
+// need clamping; they take the other way.
+__device__ __forceinline__ uint32_t codes_of(const uint4 x, uint32_t pw, float lo, float hi) {
+  constexpr float kM = 12582896.f;
+  const float s = bf16lo(pw), b = bf16hi(pw);
+  if (s == 0.f) return 0u;
+  const float r = __fdividef(1.f + 0x1p-19f, s), nh = -0.5f * s;
+  if (lo - b < 15.75f * s || hi - b > 31.25f * s) return codes_one_by_one(x, s, b);
+  const uint64_t nb2 = f32x2(-b, -b), r2 = f32x2(r, r), m2 = f32x2(kM, kM), s2 = f32x2(s, s);
+  const uint64_t one2 = f32x2(1.f, 1.f), neg2 = f32x2(-1.f, -1.f);
+  const uint32_t wx[4] = {x.x, x.y, x.z, x.w};
+  uint32_t byte[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t t = fma2(f32x2(bf16lo(wx[i]), bf16hi(wx[i])), one2, nb2);
+    const uint64_t y = fma2(t, r2, m2);
+    const uint64_t rest = fma2(fma2(y, neg2, m2), s2, t);  // t - c s
+    uint32_t n0 = static_cast<uint32_t>(y), n1 = static_cast<uint32_t>(y >> 32);
+    if (f32x2_lo(rest) < nh) n0 -= 1;
+    if (f32x2_hi(rest) < nh) n1 -= 1;
+    byte[i] = n1 * 16 + n0;  // its low byte
+  }
+  return __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
+}
+
 struct Q4RowsParams {
-  const uint4 *k, *v;           // store: rows [T, H_kv, 128] bf16
-  uint4 *k_out, *v_out;         // load: the same, written
+  const uint4 *k, *v;             // store: rows [T, H_kv, 128] bf16
+  uint4 *k_out, *v_out;           // load: the same, written
   uint32_t *k_codes, *v_codes;    // eight codes a word
   uint32_t *k_params, *v_params;  // (scale, offset) words
   const int32_t *slots;
-  int32_t num_kv_heads, block_size, groups;
-  int64_t num_rows;             // T * H_kv
+  FastDiv heads, block;
+  int32_t groups_log2;            // log2 of the groups a row
+  uint32_t num_rows;              // T * H_kv
   int64_t num_slots;
 };
-
-// Row index of a slot's row of head h in the codes and params arrays.
-__device__ __forceinline__ int64_t q4_row(int64_t slot, int h, int num_kv_heads, int block_size) {
-  const int64_t blk = slot / block_size;
-  return (blk * num_kv_heads + h) * block_size + (slot - blk * block_size);
-}
 
 __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   uint4 r;
@@ -83,115 +126,108 @@ __device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
   return r;
 }
 
-// The slot of row i (a (token, head) pair), or -1 for none; an invalid one
-// raises its bit and counts as none.
-__device__ __forceinline__ int64_t slot_of_row(const Q4RowsParams &p, int64_t i, int lane) {
+// Where (token, head) pair i lives: its row in the codes and params arrays, or
+// -1 for none; an invalid slot raises its bit and counts as none.
+__device__ __forceinline__ int64_t cache_row(const Q4RowsParams &p, uint32_t i, int lane) {
   if (i >= p.num_rows) return -1;
-  const int64_t slot = p.slots[i / p.num_kv_heads];
-  if (slot < -1 || slot >= p.num_slots) {
-    if (lane == 0) atomicOr(&g_q4_cache_errors, kErrSlot);
+  const uint32_t token = fast_quotient(i, p.heads), head = i - token * p.heads.d;
+  const int32_t slot = p.slots[token];
+  if (slot < 0 || slot >= p.num_slots) {
+    if (slot != -1 && lane == 0) atomicOr(&g_q4_cache_errors, kErrSlot);
     return -1;
   }
-  return slot;
+  const uint32_t blk = fast_quotient(slot, p.block), off = slot - blk * p.block.d;
+  return (static_cast<int64_t>(blk) * p.heads.d + head) * p.block.d + off;
 }
 
 __global__ void __launch_bounds__(kWarps * 32) q4_store_kernel(const Q4RowsParams p) {
   griddep_wait();  // inputs written by the previous kernel are visible from here on
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, kv = lane >> 4, l = lane & 15;
-  const int64_t first =
-      (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRowsInFlight;
-  int64_t slot[kRowsInFlight];
-  uint4 x[kRowsInFlight];
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const bool is_v = lane >= 16;
+  const uint32_t first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kStoreRows;
+  const uint4 *in = is_v ? p.v : p.k;
+  int64_t row[kStoreRows];
+  uint4 x[kStoreRows];
 #pragma unroll
-  for (int u = 0; u < kRowsInFlight; ++u) {
-    slot[u] = slot_of_row(p, first + u, lane);
-    if (slot[u] >= 0) x[u] = ld_stream((kv ? p.v : p.k) + (first + u) * 16 + l);
-  }
-  const int per_group = 16 / p.groups;  // lanes sharing a group
+  for (int u = 0; u < kStoreRows; ++u)
+    if (first + u < p.num_rows) x[u] = ld_stream(in + static_cast<int64_t>(first + u) * 16 + l);
 #pragma unroll
-  for (int u = 0; u < kRowsInFlight; ++u) {
-    if (slot[u] < 0) continue;  // uniform over the warp
-    const uint32_t wx[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-    float lo = bf16lo(wx[0]), hi = lo;
-    bool nan = false;
+  for (int u = 0; u < kStoreRows; ++u) row[u] = cache_row(p, first + u, lane);
+  uint32_t *codes = is_v ? p.v_codes : p.k_codes, *params = is_v ? p.v_params : p.k_params;
+  const int lanes_log2 = 4 - p.groups_log2;  // lanes sharing a group
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float f = (i & 1) ? bf16hi(wx[i >> 1]) : bf16lo(wx[i >> 1]);
-      lo = fminf(lo, f);
-      hi = fmaxf(hi, f);
-      nan |= f != f;
-    }
-    for (int off = 1; off < per_group; off <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
-      nan |= __shfl_xor_sync(0xffffffffu, static_cast<int>(nan), off) != 0;
-    }
-    const uint32_t pw = group_params(lo, hi, nan);
-    const int64_t row = q4_row(slot[u], static_cast<int>((first + u) % p.num_kv_heads),
-                               p.num_kv_heads, p.block_size);
-    (kv ? p.v_codes : p.k_codes)[row * 16 + l] = codes_of(x[u], pw);
-    if (l % per_group == 0) (kv ? p.v_params : p.k_params)[row * p.groups + l / per_group] = pw;
+  for (int u = 0; u < kStoreRows; ++u) {
+    if (row[u] < 0) continue;  // uniform over the warp
+    uint32_t e = extremes(x[u]);
+    e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 1));
+    e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 2));
+    if (lanes_log2 >= 3) e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 4));
+    if (lanes_log2 >= 4) e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 8));
+    const float lo = bf16lo(e), hi = -bf16hi(e);
+    const uint32_t pw = group_params(lo, hi);
+    codes[row[u] * 16 + l] = codes_of(x[u], pw, lo, hi);
+    if ((l & ((1 << lanes_log2) - 1)) == 0) params[(row[u] << p.groups_log2) + (l >> lanes_log2)] = pw;
   }
 }
 
 __global__ void __launch_bounds__(kWarps * 32) q4_load_kernel(const Q4RowsParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, kv = lane >> 4, l = lane & 15;
-  const int64_t first =
-      (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRowsInFlight;
-  const int per_group = 16 / p.groups;
-  uint32_t w[kRowsInFlight], pw[kRowsInFlight];
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const bool is_v = lane >= 16;
+  const uint32_t first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kLoadRows;
+  const uint32_t *codes = is_v ? p.v_codes : p.k_codes, *params = is_v ? p.v_params : p.k_params;
+  const int lanes_log2 = 4 - p.groups_log2;
+  uint32_t w[kLoadRows], pw[kLoadRows];
 #pragma unroll
-  for (int u = 0; u < kRowsInFlight; ++u) {
-    const int64_t slot = slot_of_row(p, first + u, lane);
+  for (int u = 0; u < kLoadRows; ++u) {
+    const int64_t row = cache_row(p, first + u, lane);
     w[u] = pw[u] = 0;  // no slot: zeros
-    if (slot >= 0) {
-      const int64_t row = q4_row(slot, static_cast<int>((first + u) % p.num_kv_heads),
-                                 p.num_kv_heads, p.block_size);
-      w[u] = (kv ? p.v_codes : p.k_codes)[row * 16 + l];
-      pw[u] = (kv ? p.v_params : p.k_params)[row * p.groups + l / per_group];
+    if (row >= 0) {
+      w[u] = codes[row * 16 + l];
+      pw[u] = params[(row << p.groups_log2) + (l >> lanes_log2)];
     }
   }
+  uint4 *out = is_v ? p.v_out : p.k_out;
 #pragma unroll
-  for (int u = 0; u < kRowsInFlight; ++u)
-    if (first + u < p.num_rows) (kv ? p.v_out : p.k_out)[(first + u) * 16 + l] = q4_widen(w[u], pw[u]);
+  for (int u = 0; u < kLoadRows; ++u)
+    if (first + u < p.num_rows) out[static_cast<int64_t>(first + u) * 16 + l] = q4_widen(w[u], pw[u]);
 }
 
 // Widen the keys of a prefill batch into bf16 blocks of kQ4PrefillBlock rows in
 // the workspace, whose block tables it writes. Sequence s starts at workspace
 // block ceil(cu_k[s] / block) + s, which leaves every sequence its
-// ceil(Lk / block) blocks. Grid: (row chunks, sequences); a warp widens the
-// kRowsInFlight (position, head) pairs that follow each other.
+// ceil(Lk / block) blocks. Grid: (chunks, sequences); a warp takes 16 keys of one
+// head, which lie in one cache block: one table entry, 1 KiB of K and of V codes.
 struct Q4GatherParams {
   const int32_t *cu_q, *cu_k, *block_tables;
   const uint32_t *k_codes, *v_codes, *k_params, *v_params;
   uint4 *k_out, *v_out;         // workspace K and V [blocks, kQ4PrefillBlock, H_kv, 128]
   int32_t *ws_tables;           // [S, ws_max_blocks]
-  int32_t max_blocks, ws_max_blocks, num_seqs, max_seqlen_q, max_seqlen_k, total_k;
-  int32_t num_kv_heads, block_size, groups, num_blocks, window;
+  FastDiv heads, block;
+  int32_t max_blocks, ws_max_blocks, max_seqlen_q, max_seqlen_k, total_k;
+  int32_t groups_log2, num_blocks, window;
 };
+constexpr int kGatherKeys = 16;
 
 __global__ void __launch_bounds__(kWarps * 32) q4_gather_kernel(const Q4GatherParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int s = blockIdx.y;
   const int k_begin = p.cu_k[s], k_end = p.cu_k[s + 1];
-  const int Lk = k_end - k_begin, Lq = p.cu_q[s + 1] - p.cu_q[s];
-  // segments the prefill kernel refuses are not widened (it raises the bit):
-  // here they also must not pass the workspace's end
-  if (Lk <= 0 || Lq <= 0 || Lq > Lk || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k || k_begin < 0 ||
-      k_end > p.total_k || static_cast<int64_t>(Lk) > static_cast<int64_t>(p.max_blocks) * p.block_size) {
-    // empty or refused: no workspace block for it. A segment that only passes
-    // total_k is refused here, since the prefill kernel does not know it.
-    if (k_end > p.total_k && Lq > 0 && blockIdx.x == 0 && threadIdx.x == 0)
-      atomicOr(&g_q4_cache_errors, kErrSeqlens);
-    for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < p.ws_max_blocks; j += gridDim.x * blockDim.x)
-      p.ws_tables[static_cast<int64_t>(s) * p.ws_max_blocks + j] = -1;
-    return;
-  }
-  const int ws_block0 = (k_begin + kQ4PrefillBlock - 1) / kQ4PrefillBlock + s;
+  const int q_begin = p.cu_q[s], q_end = p.cu_q[s + 1];
+  const int64_t Lk64 = static_cast<int64_t>(k_end) - k_begin, Lq64 = static_cast<int64_t>(q_end) - q_begin;
+  // segments that the prefill kernel refuses (it raises the bit) are not
+  // widened; one that only passes total_k is refused here, since that kernel does
+  // not know it
+  const bool ok = Lk64 > 0 && Lq64 > 0 && Lq64 <= Lk64 && Lq64 <= p.max_seqlen_q && Lk64 <= p.max_seqlen_k &&
+                  k_begin >= 0 && k_end <= p.total_k &&
+                  Lk64 <= static_cast<int64_t>(p.max_blocks) * p.block.d;
+  const int Lk = ok ? static_cast<int>(Lk64) : 0, Lq = ok ? static_cast<int>(Lq64) : 0;
+  if (k_end > p.total_k && Lq64 > 0 && blockIdx.x == 0 && threadIdx.x == 0)
+    atomicOr(&g_q4_cache_errors, kErrSeqlens);
+  const int ws_block0 = ok ? (k_begin + kQ4PrefillBlock - 1) / kQ4PrefillBlock + s : 0;
   for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < p.ws_max_blocks; j += gridDim.x * blockDim.x)
     p.ws_tables[static_cast<int64_t>(s) * p.ws_max_blocks + j] =
         j < (Lk + kQ4PrefillBlock - 1) / kQ4PrefillBlock ? ws_block0 + j : -1;
@@ -199,34 +235,50 @@ __global__ void __launch_bounds__(kWarps * 32) q4_gather_kernel(const Q4GatherPa
   // workspace block) are still multiplied, by zeros: they must hold numbers
   const int first_seen = p.window > 0 ? max(0, Lk - Lq - p.window + 1) : 0;
   const int first_key = first_seen / kQ4PrefillBlock * kQ4PrefillBlock;
-  const int lane = threadIdx.x & 31, kv = lane >> 4, l = lane & 15;
-  const int per_group = 16 / p.groups;
-  const int64_t H = p.num_kv_heads, n_rows = (Lk - first_key) * H;
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const bool is_v = lane >= 16;
+  const uint32_t *codes = is_v ? p.v_codes : p.k_codes, *params = is_v ? p.v_params : p.k_params;
+  uint4 *out = is_v ? p.v_out : p.k_out;
+  const int lanes_log2 = 4 - p.groups_log2;
+  const int64_t H = p.heads.d;
+  // units of 16 keys, the heads of one key range after each other: what the
+  // warps write together is contiguous
+  const int64_t n_units = (static_cast<int64_t>(Lk - first_key) + kGatherKeys - 1) / kGatherKeys * H;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t i0 = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * kRowsInFlight;
-       i0 < n_rows; i0 += n_warps * kRowsInFlight) {
-    uint32_t w[kRowsInFlight], pw[kRowsInFlight];
+  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); unit < n_units;
+       unit += n_warps) {
+    const uint32_t chunk = fast_quotient(static_cast<uint32_t>(unit), p.heads);
+    const uint32_t head = static_cast<uint32_t>(unit) - chunk * p.heads.d;
+    const int pos0 = first_key + static_cast<int>(chunk) * kGatherKeys;
+    const int n = min(kGatherKeys, Lk - pos0);
+    const uint32_t j = fast_quotient(pos0, p.block);
+    const int blk = p.block_tables[static_cast<int64_t>(s) * p.max_blocks + j];
+    const bool there = blk >= 0 && blk < p.num_blocks;
+    if (!there && lane == 0 && pos0 + n > first_seen) atomicOr(&g_q4_cache_errors, kErrBlock);
+    const int64_t row0 = there ? (blk * H + head) * p.block.d + (pos0 - j * p.block.d) : 0;
+    uint4 *dst = out + ((static_cast<int64_t>(ws_block0) * kQ4PrefillBlock + pos0) * H + head) * 16 + l;
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
-      w[u] = pw[u] = 0;
-      const int64_t i = i0 + u;
-      if (i >= n_rows) continue;
-      const int pos = first_key + static_cast<int>(i / H);
-      const int blk = p.block_tables[static_cast<int64_t>(s) * p.max_blocks + pos / p.block_size];
-      if (blk < 0 || blk >= p.num_blocks) {
-        if (lane == 0 && pos >= first_seen) atomicOr(&g_q4_cache_errors, kErrBlock);
-        continue;  // zeros
+    for (int half = 0; half < 2; ++half) {
+      uint32_t w[kGatherKeys / 2], pw[kGatherKeys / 2];
+#pragma unroll
+      for (int u = 0; u < kGatherKeys / 2; ++u) {
+        const int i = half * (kGatherKeys / 2) + u;
+        w[u] = pw[u] = 0;  // no such block: zeros
+        if (there && i < n) {
+          w[u] = codes[(row0 + i) * 16 + l];
+          pw[u] = params[((row0 + i) << p.groups_log2) + (l >> lanes_log2)];
+        }
       }
-      const int64_t row = (blk * H + i % H) * p.block_size + pos % p.block_size;
-      w[u] = (kv ? p.v_codes : p.k_codes)[row * 16 + l];
-      pw[u] = (kv ? p.v_params : p.k_params)[row * p.groups + l / per_group];
-    }
-    const int64_t out0 = (static_cast<int64_t>(ws_block0) * kQ4PrefillBlock + first_key) * H + i0;
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u)
-      if (i0 + u < n_rows) (kv ? p.v_out : p.k_out)[(out0 + u) * 16 + l] = q4_widen(w[u], pw[u]);
+      for (int u = 0; u < kGatherKeys / 2; ++u) {
+        const int i = half * (kGatherKeys / 2) + u;
+        if (i < n) dst[i * H * 16] = q4_widen(w[u], pw[u]);
+      }
+    }
   }
 }
+
+int32_t groups_log2(int32_t group_size) { return group_size == 32 ? 2 : group_size == 64 ? 1 : 0; }
 
 Q4RowsParams rows_params(const Q4RowsArgs &a) {
   Q4RowsParams p;
@@ -239,31 +291,29 @@ Q4RowsParams rows_params(const Q4RowsArgs &a) {
   p.k_params = static_cast<uint32_t *>(a.cache.k_params);
   p.v_params = static_cast<uint32_t *>(a.cache.v_params);
   p.slots = a.slots;
-  p.num_kv_heads = a.cache.num_kv_heads;
-  p.block_size = a.cache.block_size;
-  p.groups = kQ4D / a.cache.group_size;
-  p.num_rows = static_cast<int64_t>(a.num_tokens) * a.cache.num_kv_heads;
+  p.heads = fast_div(a.cache.num_kv_heads);
+  p.block = fast_div(a.cache.block_size);
+  p.groups_log2 = groups_log2(a.cache.group_size);
+  p.num_rows = static_cast<uint32_t>(a.num_tokens) * static_cast<uint32_t>(a.cache.num_kv_heads);
   p.num_slots = a.cache.num_blocks * a.cache.block_size;
   return p;
 }
 
-cudaError_t launch_rows(void (*kernel)(Q4RowsParams), const Q4RowsArgs &a, cudaStream_t stream) {
+// The caller has checked that num_tokens * num_kv_heads is below 2^31.
+cudaError_t launch_rows(void (*kernel)(Q4RowsParams), int rows, const Q4RowsArgs &a, cudaStream_t stream) {
   const Q4RowsParams p = rows_params(a);
-  const int64_t per_cta = kWarps * kRowsInFlight;
-  const int64_t grid = (p.num_rows + per_cta - 1) / per_cta;
-  if (grid == 0) return cudaSuccess;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kWarps * 32), 0, stream, p);
+  const uint32_t per_cta = kWarps * rows;
+  return launch_pdl(kernel, dim3((p.num_rows + per_cta - 1) / per_cta), dim3(kWarps * 32), 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_q4_store(const Q4RowsArgs &a, cudaStream_t stream) {
-  return launch_rows(q4_store_kernel, a, stream);
+  return launch_rows(q4_store_kernel, kStoreRows, a, stream);
 }
 
 cudaError_t launch_q4_load(const Q4RowsArgs &a, cudaStream_t stream) {
-  return launch_rows(q4_load_kernel, a, stream);
+  return launch_rows(q4_load_kernel, kLoadRows, a, stream);
 }
 
 cudaError_t launch_q4_gather(const Q4GatherArgs &a, cudaStream_t stream) {
@@ -280,18 +330,17 @@ cudaError_t launch_q4_gather(const Q4GatherArgs &a, cudaStream_t stream) {
   p.ws_tables = a.ws_tables;
   p.max_blocks = a.max_blocks;
   p.ws_max_blocks = a.ws_max_blocks;
-  p.num_seqs = a.num_seqs;
   p.max_seqlen_q = a.max_seqlen_q;
   p.max_seqlen_k = a.max_seqlen_k;
   p.total_k = a.total_k;
-  p.num_kv_heads = a.cache.num_kv_heads;
-  p.block_size = a.cache.block_size;
-  p.groups = kQ4D / a.cache.group_size;
+  p.heads = fast_div(a.cache.num_kv_heads);
+  p.block = fast_div(a.cache.block_size);
+  p.groups_log2 = groups_log2(a.cache.group_size);
   p.num_blocks = static_cast<int32_t>(a.cache.num_blocks);
   p.window = a.window;
-  // enough CTAs a sequence for its longest possible key range, a few rounds each
-  const int64_t per_cta = kWarps * kRowsInFlight;
-  int64_t gx = (static_cast<int64_t>(a.max_seqlen_k) * a.cache.num_kv_heads + per_cta - 1) / per_cta;
+  // CTAs a sequence for its longest possible key range, at most some 16 an SM in all
+  const int64_t units = (static_cast<int64_t>(a.max_seqlen_k) + kGatherKeys - 1) / kGatherKeys * a.cache.num_kv_heads;
+  int64_t gx = (units + kWarps - 1) / kWarps;
   const int64_t cap = (16 * static_cast<int64_t>(a.num_sms) + a.num_seqs - 1) / a.num_seqs;
   if (gx > cap) gx = cap;
   return launch_pdl(q4_gather_kernel, dim3(static_cast<unsigned>(gx), a.num_seqs), dim3(kWarps * 32),

@@ -2,28 +2,31 @@
 // sequence.
 //
 // The keys of a (sequence, KV head) are cut into splits, one CTA each; the
-// CTA's four warps take the split's units of 16 keys in turn. A unit's codes
-// are 1 KiB of K and 1 KiB of V, contiguous in the cache, and its parameters
-// 64 to 256 bytes of each. Every warp streams its units through a ring of its
-// own with cp.async, so no warp waits for another before the end of the split.
+// CTA's four warps take the split's steps of 32 keys (two units of 16) in turn. A
+// unit's codes are 1 KiB of K and 1 KiB of V, contiguous in the cache, and its
+// parameters 64 to 256 bytes of each. Every warp streams its steps through a
+// ring of its own with cp.async, so no warp waits for another before the end of
+// the split.
 //
 // The products run on mma.sync m16n8k16 in bf16 with fp32 accumulators. A bf16
 // of the cache's definition is what the codes are widened to, so the logits
-// have exact products, as with a bf16 cache.
-//   S = Q K^T   A = the group's query heads (rows 0..7), B = 16 keys: two n8
-//               tiles. Lane (g, t) = (lane / 4, lane % 4) holds 32 dims of the
-//               keys of column g, 16 bytes of codes each.
-//   O^T += V^T P^T   A = V^T: 16 dims a tile, eight tiles, B = P^T, whose
-//               fragment is S's accumulator fragment packed to bf16: the
-//               probabilities never leave their registers. Lane (g, t) holds
-//               dims 16 g .. 16 g + 15 of four keys, 8 bytes of codes each.
-// Column n of tile j holds key 8 j + 4 (n & 1) + (n >> 1): lane t then needs V
-// rows t, 4 + t, 8 + t and 12 + t, so that four lanes of one load read
+// have exact products, as with a bf16 cache. With (g, t) = (lane / 4, lane % 4):
+//   S^T = K Q^T      A = a unit's 16 keys, B = up to 8 query heads. A lane holds
+//                    32 dims of two keys, 16 bytes of codes each.
+//   O^T += V^T P^T   A = 16 dims a tile, eight tiles, B = P^T: S^T's accumulator
+//                    fragment packed to bf16 and transposed in place (one
+//                    movmatrix for 8 keys). A lane holds dims 16 g .. 16 g + 15
+//                    of four keys, 8 bytes of codes each.
+// Row r (and r + 8) of S^T is key 4 (r & 1) + (r >> 1) (and + 8): lane t then
+// needs V rows t, 4 + t, 8 + t and 12 + t, so that four lanes of one load read
 // neighbouring rows (free of bank conflicts with the row swizzle below).
 //
 // P is rounded to bf16 and the output divided by the sum of the rounded
 // probabilities, the weights that the products used; the lse comes from the
 // fp32 sum.
+//
+// Widening the codes is what the kernel spends its issue slots on: three
+// instructions for two values, 400 of the some 600 that a step takes.
 #include "internal.h"
 #include "key_scores.cuh"
 #include "q4.cuh"
@@ -37,7 +40,8 @@ namespace {
 constexpr int kD = kQ4D;
 constexpr int kWarps = 4;
 constexpr int kUnit = 16;                    // keys a unit
-constexpr int kStages = 4;                   // units in flight a warp
+constexpr int kStep = 2 * kUnit;             // keys a step
+constexpr int kStages = 2;                   // steps in a warp's ring
 constexpr int kMaxG = 8;                     // query heads a KV head (columns of a P^T tile)
 constexpr int kUnitCodes = kUnit * kQ4RowBytes;  // 1 KiB of K or V codes
 constexpr float kLn2 = 0.693147180559945309f;
@@ -53,7 +57,8 @@ struct Q4DecodeParams {
   float4 *ws_ml;   // [S, H_kv, n_splits, G] (max, sum, sum of the rounded)
   float *logits;   // [S, H_q, logits_ld] or null
   int64_t logits_ld;
-  int32_t max_blocks, max_context_len, num_q_heads, num_kv_heads, block_size, num_blocks;
+  FastDiv block;
+  int32_t max_blocks, max_context_len, num_q_heads, num_kv_heads, num_blocks;
   int32_t gqa, window, n_splits, split_keys;
   float scale_log2;
 };
@@ -61,7 +66,8 @@ struct Q4DecodeParams {
 template <int NG>  // parameter groups a row: 4, 2 or 1
 struct Q4DecodeSmem {
   static constexpr int kParamBytes = kUnit * NG * 4;
-  static constexpr int kStageBytes = 2 * kUnitCodes + 2 * kParamBytes;
+  static constexpr int kUnitBytes = 2 * kUnitCodes + 2 * kParamBytes;  // K, V codes, K, V parameters
+  static constexpr int kStageBytes = 2 * kUnitBytes;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kMergeBytes = kWarps * kMaxG * (kD + 4) * 4;  // O and (m, l, r) of each warp
   static constexpr int kTotal = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
@@ -92,6 +98,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Transpose of an 8 x 8 matrix of 16-bit values held by the warp, row g in the
+// lanes 4 g .. 4 g + 3, two columns each.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
 // The keys a sequence attends to: [first, ctx); its units start at the 16-key
 // boundary at or before first. ctx <= 0 marks an invalid length.
 struct KeyRange {
@@ -100,7 +114,7 @@ struct KeyRange {
 __device__ __forceinline__ KeyRange key_range(const Q4DecodeParams &p, int s) {
   KeyRange r;
   r.ctx = p.context_lens[s];
-  if (r.ctx > p.max_context_len || r.ctx > static_cast<int64_t>(p.max_blocks) * p.block_size) r.ctx = 0;
+  if (r.ctx > p.max_context_len || r.ctx > static_cast<int64_t>(p.max_blocks) * p.block.d) r.ctx = 0;
   r.first = p.window > 0 && r.ctx > p.window ? r.ctx - p.window : 0;
   r.unit0 = r.first / kUnit * kUnit;
   return r;
@@ -126,68 +140,77 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
   const int key_begin = static_cast<int>(key_begin64);
   const int key_end = min(range.ctx - key_begin, p.split_keys) + key_begin;
   const int n_units = (key_end - key_begin + kUnit - 1) / kUnit;
-  const int n_mine = n_units > warp ? (n_units - warp + kWarps - 1) / kWarps : 0;
+  const int n_steps = (n_units + 1) / 2;
+  const int n_mine = n_steps > warp ? (n_steps - warp + kWarps - 1) / kWarps : 0;
 
-  // the query heads as A fragments: k-step 2w (2w + 1) pairs dims i and i + 4,
+  // the query heads as B fragments: k-step 2w (2w + 1) pairs dims i and i + 4,
   // i = 0, 1 (2, 3), of the lane's w-th code word
-  uint32_t qa[8][2];
+  uint32_t qb[8][2];
   {
     const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + head * G + g;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * kD + 32 * t);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       const uint4 x = g < G ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-      qa[2 * w][0] = q4_low_halves(x.x, x.z);
-      qa[2 * w][1] = q4_high_halves(x.x, x.z);
-      qa[2 * w + 1][0] = q4_low_halves(x.y, x.w);
-      qa[2 * w + 1][1] = q4_high_halves(x.y, x.w);
+      qb[2 * w][0] = q4_low_halves(x.x, x.z);
+      qb[2 * w][1] = q4_high_halves(x.x, x.z);
+      qb[2 * w + 1][0] = q4_low_halves(x.y, x.w);
+      qb[2 * w + 1][1] = q4_high_halves(x.y, x.w);
     }
   }
 
-  // rows / 16 of this warp's unit i in the codes array, 0xffffffff for an
-  // invalid table entry; a lane holds one unit of a batch of 32
+  // rows / 16 of this warp's unit i (two units a step) in the codes array, or
+  // kNoUnit past the split's end and for an invalid table entry; a lane holds one
+  // unit of a batch of 32
+  constexpr uint32_t kNoUnit = 0xffffffffu;
   const int32_t *table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks;
-  auto entry_of = [&](int i) -> uint32_t {
-    if (i >= n_mine) return 0;
-    const int key = key_begin + (warp + kWarps * i) * kUnit;
-    const int blk = table[key / p.block_size];
+  auto unit_row = [&](int i) -> uint32_t {
+    const int u = (warp + kWarps * (i >> 1)) * 2 + (i & 1);  // the split's unit
+    if (u >= n_units) return kNoUnit;
+    const int key = key_begin + u * kUnit;
+    const uint32_t j = fast_quotient(key, p.block);
+    const int blk = table[j];
     if (blk < 0 || blk >= p.num_blocks) {
       atomicOr(&g_q4_decode_errors, kErrBlock);
-      return 0xffffffffu;
+      return kNoUnit;
     }
     return static_cast<uint32_t>(
-        ((static_cast<int64_t>(blk) * p.num_kv_heads + head) * p.block_size + key % p.block_size) / kUnit);
+        ((static_cast<int64_t>(blk) * p.num_kv_heads + head) * p.block.d + (key - j * p.block.d)) / kUnit);
   };
-  uint32_t batch = entry_of(lane), next_batch = n_mine > 32 ? entry_of(32 + lane) : 0;
-  uint32_t used = batch;  // the batch of the unit being consumed
+  uint32_t batch = unit_row(lane), next_batch = n_mine > 16 ? unit_row(32 + lane) : kNoUnit;
+  // one bit a unit that is there, of the batch being consumed and of the next
+  uint32_t there = __ballot_sync(0xffffffffu, batch != kNoUnit);
+  uint32_t there_next = __ballot_sync(0xffffffffu, next_batch != kNoUnit);
 
+  const int kperm = 4 * (g & 1) + (g >> 1);  // key of row g
   const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStageBytes;
   const uint8_t *ring_ptr = smem + warp * kStages * L::kStageBytes;
-  const int kperm = 4 * (g & 1) + (g >> 1);             // key of column g in tile 0
-  const uint32_t v_swz = (lane & 3) ^ (((lane >> 3) & 1) << 1);  // chunk of the row this lane copies
-  auto issue = [&](int i) {
+  // what this lane copies of a unit. K: the 16 bytes that it will read; V: rows
+  // in order, chunk c of row r at c ^ 2 ((r >> 1) & 1); the parameter rows: lanes
+  // 0..15 K's, 16..31 V's
+  const uint8_t *k_src = p.k_codes + kperm * kQ4RowBytes + t * 16;
+  const uint8_t *v_src = p.v_codes + lane * 16;
+  const uint8_t *p_src = (lane < 16 ? p.k_params : p.v_params) + (lane & 15) * (4 * NG);
+  const uint32_t v_dst = kUnitCodes + (lane >> 2) * kQ4RowBytes + ((lane & 3) ^ (((lane >> 3) & 1) << 1)) * 16;
+  auto issue = [&](int i) {  // step i
     if (i < n_mine) {
-      if (i > 0 && (i & 31) == 0) {
+      if (i > 0 && (i & 15) == 0) {
         batch = next_batch;
-        next_batch = entry_of(i + 32 + lane);
+        next_batch = i + 16 < n_mine ? unit_row(2 * i + 32 + lane) : kNoUnit;
       }
-      const uint32_t row16 = __shfl_sync(0xffffffffu, batch, i & 31);
-      if (row16 != 0xffffffffu) {
-        const uint32_t st = ring + (i % kStages) * L::kStageBytes;
-        const uint8_t *k = p.k_codes + static_cast<int64_t>(row16) * kUnitCodes;
-        const uint8_t *v = p.v_codes + static_cast<int64_t>(row16) * kUnitCodes;
-        // K: each lane copies the 16 bytes that it will read; V: rows in order,
-        // chunk c of row r at c ^ 2 ((r >> 1) & 1)
-        const int ko = kperm * kQ4RowBytes + t * 16;
-        cp_async16(st + lane * 16, k + ko);
-        cp_async16(st + 512 + lane * 16, k + 512 + ko);
-        const uint32_t vd = st + kUnitCodes + (lane >> 2) * kQ4RowBytes + v_swz * 16;
-        cp_async16(vd, v + lane * 16);
-        cp_async16(vd + 512, v + 512 + lane * 16);
-        // the parameter rows: lanes 0..15 K's, 16..31 V's
-        const uint8_t *pp = (lane < 16 ? p.k_params : p.v_params) +
-                            static_cast<int64_t>(row16) * L::kParamBytes + (lane & 15) * (4 * NG);
-        cp_async_small<4 * NG>(st + 2 * kUnitCodes + lane * (4 * NG), pp);
+      uint32_t st = ring + (i % kStages) * L::kStageBytes;
+#pragma unroll
+      for (int u = 0; u < 2; ++u, st += L::kUnitBytes) {
+        const uint32_t row16 = __shfl_sync(0xffffffffu, batch, (2 * i + u) & 31);
+        if (row16 == kNoUnit) continue;
+        const uint8_t *k = k_src + static_cast<int64_t>(row16) * kUnitCodes;
+        const uint8_t *v = v_src + static_cast<int64_t>(row16) * kUnitCodes;
+        cp_async16(st + lane * 16, k);
+        cp_async16(st + 512 + lane * 16, k + 512);
+        cp_async16(st + v_dst, v);
+        cp_async16(st + v_dst + 512, v + 512);
+        cp_async_small<4 * NG>(st + 2 * kUnitCodes + lane * (4 * NG),
+                               p_src + static_cast<int64_t>(row16) * L::kParamBytes);
       }
     }
     cp_async_commit();
@@ -198,127 +221,171 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
   for (int m = 0; m < 8; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-  float mx = -INFINITY, lsum = 0.f, rsum = 0.f;  // of row (head) g, this lane's keys
+  // of heads 2 t and 2 t + 1; the sums are over this lane's keys
+  float mx[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f}, rsum[2] = {0.f, 0.f};
 
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kStages; ++i) issue(i);
 
 #pragma unroll 1
   for (int it = 0; it < n_mine; ++it) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();  // every lane's copies of this unit have landed, and the stage
-                   // that is filled next has been read by every lane
-    if (it > 0 && (it & 31) == 0) used = entry_of(it + lane);
-    const bool dead = __shfl_sync(0xffffffffu, used, it & 31) == 0xffffffffu;
-    issue(it + kStages - 1);
-    if (dead) continue;  // no such block: its keys are left out
+    cp_async_wait<kStages - 1>();
+    __syncwarp();  // every lane's copies of this step have landed
+    if (it > 0 && (it & 15) == 0) {
+      there = there_next;
+      there_next = __ballot_sync(0xffffffffu, next_batch != kNoUnit);
+    }
     const uint8_t *st = ring_ptr + (it % kStages) * L::kStageBytes;
-    const uint32_t *kp = reinterpret_cast<const uint32_t *>(st + 2 * kUnitCodes);
-    const uint32_t *vp = kp + kUnit * NG;
+    const int key0 = key_begin + (warp + kWarps * it) * kStep;
 
-    // ---- S = Q K^T
-    float sc[2][4] = {};
+    // ---- S^T = K Q^T
+    float z[2][4];  // keys kperm, 8 + kperm of each unit, heads 2 t, 2 t + 1: [u][2 * key + head]
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 kw = *reinterpret_cast<const uint4 *>(st + 512 * j + lane * 16);
-      const uint32_t pw = kp[(8 * j + kperm) * NG + t * NG / 4];
-      const uint32_t s2 = q4_dup_scale(pw), b2 = q4_dup_offset(pw);
-      const uint32_t words[4] = {kw.x, kw.y, kw.z, kw.w};
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t *su = st + u * L::kUnitBytes;
+      const uint32_t *kp = reinterpret_cast<const uint32_t *>(su + 2 * kUnitCodes) + kperm * NG + t * NG / 4;
+      uint32_t words[2][4], s2[2], b2[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint4 kw = *reinterpret_cast<const uint4 *>(su + 512 * j + lane * 16);
+        words[j][0] = kw.x;
+        words[j][1] = kw.y;
+        words[j][2] = kw.z;
+        words[j][3] = kw.w;
+        const uint32_t pw = kp[8 * j * NG];
+        s2[j] = q4_dup_scale(pw);
+        b2[j] = q4_dup_offset(pw);
+      }
+      float sc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        uint32_t x[4];
-        q4_pairs(words[w], x);
+        uint32_t x[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fma_bf16x2(x[i], s2, b2);
-        mma_16816(sc[j], qa[2 * w][0], 0u, qa[2 * w][1], 0u, x[0], x[1]);
-        mma_16816(sc[j], qa[2 * w + 1][0], 0u, qa[2 * w + 1][1], 0u, x[2], x[3]);
+        for (int j = 0; j < 2; ++j) {
+          q4_pairs(words[j][w], x[j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[j][i] = fma_bf16x2(x[j][i], s2[j], b2[j]);
+        }
+        mma_16816(sc, x[0][0], x[1][0], x[0][1], x[1][1], qb[2 * w][0], qb[2 * w][1]);
+        mma_16816(sc, x[0][2], x[1][2], x[0][3], x[1][3], qb[2 * w + 1][0], qb[2 * w + 1][1]);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) z[u][i] = sc[i] * p.scale_log2;
     }
 
-    // ---- softmax: this lane's keys t, 4 + t, 8 + t, 12 + t of row g
-    const int key0 = key_begin + (warp + kWarps * it) * kUnit;
-    float z[4] = {sc[0][0] * p.scale_log2, sc[0][1] * p.scale_log2, sc[1][0] * p.scale_log2,
-                  sc[1][1] * p.scale_log2};
-    const bool partial = key0 < range.first || key0 + kUnit > key_end;
-    uint32_t pv[4];  // V parameters of those keys
+    // ---- masks, softmax
+    uint32_t pv[2][4];  // V parameters of this lane's V rows
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pv[i] = vp[(4 * i + t) * NG + g * NG / 8];
-    if (p.logits != nullptr && g < G) {  // rows hold whole units: masked keys are written too
-      float *dst = p.logits + (static_cast<int64_t>(s) * p.num_q_heads + head * G + g) * p.logits_ld + key0 + t;
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dst[4 * i] = z[i];
-    }
-    if (partial) {
+      for (int i = 0; i < 4; ++i)
+        pv[u][i] = reinterpret_cast<const uint32_t *>(st + u * L::kUnitBytes + 2 * kUnitCodes +
+                                                      L::kParamBytes)[(4 * i + t) * NG + g * NG / 8];
+    const uint32_t units = (there >> (2 * it & 31)) & 3u;
+    if (p.logits != nullptr && 2 * t < G) {  // rows hold whole units: masked keys are written too
+      float *dst = p.logits + (static_cast<int64_t>(s) * p.num_q_heads + head * G + 2 * t) * p.logits_ld + key0 + kperm;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = key0 + 4 * i + t;
-        if (key < range.first || key >= key_end) {
-          z[i] = -INFINITY;
-          pv[i] = 0u;  // the row reads as zeros, whatever its slot holds
+      for (int u = 0; u < 2; ++u) {
+        if (!((units >> u) & 1u)) continue;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (2 * t + c >= G) continue;
+          dst[c * p.logits_ld + u * kUnit] = z[u][c];
+          dst[c * p.logits_ld + u * kUnit + 8] = z[u][2 + c];
         }
       }
     }
-    const float zm = fmaxf(fmax3(z[0], z[1], z[2]), z[3]);
-    if (__any_sync(0xffffffffu, zm > mx + kLazyMax)) {  // always on a first unit
-      float m_new = fmaxf(zm, __shfl_xor_sync(0xffffffffu, zm, 1));
-      m_new = fmaxf(m_new, __shfl_xor_sync(0xffffffffu, m_new, 2));
-      m_new = fmaxf(m_new, mx);
-      const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(mx - m_new);
-      mx = m_new;
-      lsum *= alpha;
-      rsum *= alpha;
-      const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * t);      // head 2 t
-      const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * t + 4);  // head 2 t + 1
+    if (key0 < range.first || key0 + kStep > key_end || units != 3u) {
 #pragma unroll
-      for (int m = 0; m < 8; ++m) {
-        acc[m][0] *= a0;
-        acc[m][1] *= a1;
-        acc[m][2] *= a0;
-        acc[m][3] *= a1;
+      for (int u = 0; u < 2; ++u) {
+        const int lo = range.first - (key0 + u * kUnit);
+        const int hi = ((units >> u) & 1u) ? key_end - (key0 + u * kUnit) : 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (8 * j + kperm < lo || 8 * j + kperm >= hi) z[u][2 * j] = z[u][2 * j + 1] = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // the row reads as zeros, whatever its slot holds
+          if (4 * i + t < lo || 4 * i + t >= hi) pv[u][i] = 0u;
       }
     }
-    float pr[4];
-    const float m_ref = mx == -INFINITY ? 0.f : mx;  // logits of -inf alone have probability 0
+    const float zm0 = fmaxf(fmax3(z[0][0], z[0][2], z[1][0]), z[1][2]);
+    const float zm1 = fmaxf(fmax3(z[0][1], z[0][3], z[1][1]), z[1][3]);
+    if (__any_sync(0xffffffffu, zm0 > mx[0] + kLazyMax || zm1 > mx[1] + kLazyMax)) {  // always on a first step
+      float m_new[2] = {fmaxf(zm0, mx[0]), fmaxf(zm1, mx[1])}, alpha[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      pr[i] = fast_exp2(z[i] - m_ref);
-      lsum += pr[i];
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) m_new[c] = fmaxf(m_new[c], __shfl_xor_sync(0xffffffffu, m_new[c], off));
+        alpha[c] = m_new[c] == -INFINITY ? 1.f : fast_exp2(mx[c] - m_new[c]);
+        mx[c] = m_new[c];
+        lsum[c] *= alpha[c];
+        rsum[c] *= alpha[c];
+      }
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] *= alpha[i & 1];
     }
-    const uint32_t b0 = pack_bf16x2(pr[0], pr[1]), b1 = pack_bf16x2(pr[2], pr[3]);
-    rsum += (bf16lo(b0) + bf16hi(b0)) + (bf16lo(b1) + bf16hi(b1));
-
-    // ---- O^T += V^T P^T
-    const uint32_t sa = q4_low_halves(pv[0], pv[1]), ba = q4_high_halves(pv[0], pv[1]);
-    const uint32_t sb = q4_low_halves(pv[2], pv[3]), bb = q4_high_halves(pv[2], pv[3]);
-    uint2 vw[4];
+    // logits of -inf alone have probability 0
+    const float ref[2] = {mx[0] == -INFINITY ? 0.f : mx[0], mx[1] == -INFINITY ? 0.f : mx[1]};
+    uint32_t pb[2][2];  // P^T fragments of each unit
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 4 * i + t;
-      vw[i] = *reinterpret_cast<const uint2 *>(st + kUnitCodes + row * kQ4RowBytes +
-                                               (((g >> 1) ^ (((row >> 1) & 1) << 1)) * 16) + (g & 1) * 8);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {  // dims 16 g + 4 j .. + 3
-      const uint32_t w0 = (j & 2) ? vw[0].y : vw[0].x, w1 = (j & 2) ? vw[1].y : vw[1].x;
-      const uint32_t w2 = (j & 2) ? vw[2].y : vw[2].x, w3 = (j & 2) ? vw[3].y : vw[3].x;
-      uint32_t xa[4], xb[4];
-      q4_pairs((j & 1) ? q4_high_halves(w0, w1) : q4_low_halves(w0, w1), xa);
-      q4_pairs((j & 1) ? q4_high_halves(w2, w3) : q4_low_halves(w2, w3), xb);
+    for (int u = 0; u < 2; ++u) {
+      float pr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        xa[i] = fma_bf16x2(xa[i], sa, ba);
-        xb[i] = fma_bf16x2(xb[i], sb, bb);
+        pr[i] = fast_exp2(z[u][i] - ref[i & 1]);
+        lsum[i & 1] += pr[i];
       }
-      mma_16816(acc[2 * j], xa[0], xa[1], xb[0], xb[1], b0, b1);
-      mma_16816(acc[2 * j + 1], xa[2], xa[3], xb[2], xb[3], b0, b1);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t x = pack_bf16x2(pr[2 * j], pr[2 * j + 1]);
+        rsum[0] += bf16lo(x);
+        rsum[1] += bf16hi(x);
+        pb[u][j] = transpose_8x8(x);
+      }
     }
+
+    // ---- O^T += V^T P^T
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t sa = q4_low_halves(pv[u][0], pv[u][1]), ba = q4_high_halves(pv[u][0], pv[u][1]);
+      const uint32_t sb = q4_low_halves(pv[u][2], pv[u][3]), bb = q4_high_halves(pv[u][2], pv[u][3]);
+      uint2 vw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 4 * i + t;
+        vw[i] = *reinterpret_cast<const uint2 *>(st + u * L::kUnitBytes + kUnitCodes + row * kQ4RowBytes +
+                                                 (((g >> 1) ^ (((row >> 1) & 1) << 1)) * 16) + (g & 1) * 8);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // dims 16 g + 4 j .. + 3
+        const uint32_t w0 = (j & 2) ? vw[0].y : vw[0].x, w1 = (j & 2) ? vw[1].y : vw[1].x;
+        const uint32_t w2 = (j & 2) ? vw[2].y : vw[2].x, w3 = (j & 2) ? vw[3].y : vw[3].x;
+        uint32_t xa[4], xb[4];
+        q4_pairs((j & 1) ? q4_high_halves(w0, w1) : q4_low_halves(w0, w1), xa);
+        q4_pairs((j & 1) ? q4_high_halves(w2, w3) : q4_low_halves(w2, w3), xb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          xa[i] = fma_bf16x2(xa[i], sa, ba);
+          xb[i] = fma_bf16x2(xb[i], sb, bb);
+        }
+        mma_16816(acc[2 * j], xa[0], xa[1], xb[0], xb[1], pb[u][0], pb[u][1]);
+        mma_16816(acc[2 * j + 1], xa[2], xa[3], xb[2], xb[3], pb[u][0], pb[u][1]);
+      }
+    }
+    __syncwarp();  // every lane has read the stage: it may be filled again
+    issue(it + kStages);
   }
 
   // ---- join the four warps
-  lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-  lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
-  rsum += __shfl_xor_sync(0xffffffffu, rsum, 1);
-  rsum += __shfl_xor_sync(0xffffffffu, rsum, 2);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      lsum[c] += __shfl_xor_sync(0xffffffffu, lsum[c], off);
+      rsum[c] += __shfl_xor_sync(0xffffffffu, rsum[c], off);
+    }
   cp_async_wait<0>();
   __syncthreads();  // no warp still reads or fills its ring
   float *so = reinterpret_cast<float *>(smem);                       // [warp][G][128]
@@ -330,7 +397,9 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
       if (2 * t + c < G)
         *reinterpret_cast<float2 *>(so + (warp * kMaxG + 2 * t + c) * kD + 16 * g + 2 * m) =
             make_float2(acc[m][c], acc[m][2 + c]);
-  if (t == 0 && g < G) sml[warp * kMaxG + g] = make_float4(mx, lsum, rsum, 0.f);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    if (g == 0 && 2 * t + c < G) sml[warp * kMaxG + 2 * t + c] = make_float4(mx[c], lsum[c], rsum[c], 0.f);
   __syncthreads();
   const bool whole = range.unit0 + static_cast<int64_t>(p.split_keys) >= range.ctx;
   const int d = threadIdx.x;
@@ -445,7 +514,7 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
   p.max_context_len = a.max_context_len;
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.cache.num_kv_heads;
-  p.block_size = a.cache.block_size;
+  p.block = fast_div(a.cache.block_size);
   p.num_blocks = static_cast<int32_t>(a.cache.num_blocks);
   p.gqa = a.num_q_heads / a.cache.num_kv_heads;
   p.window = a.window;
