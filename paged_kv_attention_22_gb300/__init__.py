@@ -3,7 +3,9 @@
 The functions here have the names of the C entry points in ``include/pkv.h``
 and do argument marshalling only: they check dtypes and shapes of torch
 tensors, pass their device pointers and the current CUDA stream to the C ABI,
-and allocate outputs the caller did not supply. Every step of the computation
+and allocate outputs the caller did not supply. (For 4-bit caches and eviction
+the checks are compiled, in the module ``_marshal`` beside the library; those
+calls also want every tensor on the current device.) Every step of the computation
 runs in the library's CUDA kernels. There is no fallback: if libpkv.so has not
 been built, or a call fails, an exception is raised.
 
@@ -25,6 +27,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(_HERE, "libpkv.so")
+MARSHAL_PATH = os.path.join(_HERE, "_marshal.so")
 
 PKV_OK = 0
 PKV_ERR_INVALID_ARG = 1
@@ -42,6 +45,7 @@ DEVERR_SEQLENS = 0x8
 DEVERR_TIMEOUT = 0x10
 
 _lib = None
+_m = None  # the _marshal module: argument marshalling of the calls below lib()
 
 
 class PkvError(RuntimeError):
@@ -54,14 +58,17 @@ class PkvError(RuntimeError):
 
 def lib():
     """The loaded libpkv.so (ctypes), with argument types declared."""
-    global _lib
+    global _lib, _m
     if _lib is not None:
         return _lib
-    if not os.path.exists(LIBRARY_PATH):
-        raise ImportError(
-            f"{LIBRARY_PATH} is missing: build it with "
-            "`python -m paged_kv_attention_22_gb300.build` (nvcc, sm_103a)")
+    for path in (LIBRARY_PATH, MARSHAL_PATH):
+        if not os.path.exists(path):
+            raise ImportError(
+                f"{path} is missing: build it with "
+                "`python -m paged_kv_attention_22_gb300.build` (nvcc, sm_103a)")
     L = ctypes.CDLL(LIBRARY_PATH)
+    from . import _marshal
+    _m = _marshal
     P, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                             ctypes.c_size_t)
     L.pkv_status_string.argtypes = [ctypes.c_int]
@@ -380,65 +387,35 @@ def new_q4_cache(num_blocks, block_size, num_kv_heads, group_size=32, device="cu
                    torch.zeros(*head, 128 // group_size, 2, dtype=torch.bfloat16, device=device))
 
 
-def _need_current_device(*tensors):
-    """All tensors (None allowed) on the current device, where the library launches."""
-    current = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != current:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
+def _calls():
+    """The _marshal module, which checks arguments and calls the C entries."""
+    if _m is None:
+        lib()
+    return _m
+
+
+_CURRENT = contextlib.nullcontext()
 
 
 def _on(stream):
     """Allocate for work on `stream` (None: the current one): memory that is freed
     when a call returns is then reused in that stream's order only."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
-
-
-def _q4(k_cache, v_cache):
-    """Checked (pointers, (num_blocks, block_size, H_kv, group_size)) of a 4-bit K and V cache."""
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(c, tuple) or len(c) != 2:
-            raise TypeError(f"{name} must be a Q4Cache or a (codes, params) pair")
-        _need(c[0], f"{name} codes", torch.uint8, 4)
-        _need(c[1], f"{name} params", torch.bfloat16, 5)
-    codes, params = k_cache
-    NB, H_kv, bs, row = codes.shape
-    groups = params.shape[3]
-    if row != 64 or groups not in (1, 2, 4) or params.shape != (NB, H_kv, bs, groups, 2) \
-            or v_cache[0].shape != codes.shape or v_cache[1].shape != params.shape:
-        raise ValueError("inconsistent shapes of a 4-bit cache")
-    _need_current_device(*k_cache, *v_cache)
-    return tuple(_ptr(t) for t in (*k_cache, *v_cache)), (NB, bs, H_kv, 128 // groups)
+    return torch.cuda.stream(stream) if stream is not None else _CURRENT
 
 
 def kv_store_q4(k, v, k_cache, v_cache, slot_mapping, stream=None):
     """Quantise k, v [T, H_kv, 128] into the 4-bit caches at slot_mapping (-1: skip)."""
-    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
-    _need(k, "k", torch.bfloat16, 3)
-    _need(v, "v", torch.bfloat16, 3)
-    _need(slot_mapping, "slot_mapping", torch.int32, 1)
-    if k.shape != v.shape or k.shape[1:] != (H_kv, 128) or slot_mapping.shape[0] != k.shape[0]:
-        raise ValueError("inconsistent shapes")
-    _need_current_device(k, v, slot_mapping)
-    _check(lib().pkv_kv_store_q4(_ptr(k), _ptr(v), *ptrs, _ptr(slot_mapping), k.shape[0], H_kv, 128,
-                                 group, bs, NB, _stream(stream)), "pkv_kv_store_q4")
+    st = _calls().kv_store_q4(k, v, k_cache, v_cache, slot_mapping, stream)
+    if st:
+        raise PkvError(st, "pkv_kv_store_q4")
 
 
 def kv_load_q4(k_cache, v_cache, slots, k=None, v=None, stream=None):
     """The rows at slots [T] as bf16 (k, v) [T, H_kv, 128]; zeros for slot -1."""
-    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
-    _need(slots, "slots", torch.int32, 1)
-    shape = (slots.shape[0], H_kv, 128)
     with _on(stream):
-        k = torch.empty(shape, dtype=torch.bfloat16, device=slots.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=slots.device) if v is None else v
-    _need(k, "k", torch.bfloat16, 3)
-    _need(v, "v", torch.bfloat16, 3)
-    if k.shape != shape or v.shape != shape:
-        raise ValueError("inconsistent shapes")
-    _need_current_device(slots, k, v)
-    _check(lib().pkv_kv_load_q4(*ptrs, _ptr(slots), _ptr(k), _ptr(v), shape[0], H_kv, 128, group, bs,
-                                NB, _stream(stream)), "pkv_kv_load_q4")
+        st, k, v = _calls().kv_load_q4(k_cache, v_cache, slots, k, v, stream)
+    if st:
+        raise PkvError(st, "pkv_kv_load_q4")
     return k, v
 
 
@@ -458,29 +435,13 @@ def new_q4_decode_workspace(num_seqs, num_q_heads, num_kv_heads, max_context_len
     return torch.empty(need, dtype=torch.uint8, device=device)
 
 
-def _decode_inputs(q, block_tables, context_lens, max_context_len, out, lse, with_lse, key_scores):
-    """Checks shared by the decode calls below; returns (out, lse, score row stride)."""
-    _need(q, "q", torch.bfloat16, 3)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
-    S, H_q, D = q.shape
-    if D != 128 or block_tables.shape[0] != S or context_lens.shape[0] != S:
-        raise ValueError("inconsistent shapes")
+def _decode_outputs(q, out, lse, with_lse):
+    """Allocate the outputs of a decode call that the caller did not supply."""
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "out", torch.bfloat16, 3)
     if lse is None and with_lse:
-        lse = torch.empty((S, H_q), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, 2)
-    if out.shape != q.shape or (lse is not None and lse.shape != (S, H_q)):
-        raise ValueError("inconsistent shapes")
-    if key_scores is not None:
-        _need(key_scores, "key_scores", torch.float32, 2)
-        if key_scores.shape[0] != S or key_scores.shape[1] < max_context_len:
-            raise ValueError("key_scores must be [num_seqs, >= max_context_len]")
-    _need_current_device(q, block_tables, context_lens, out, lse, key_scores)
-    return out, lse, key_scores.shape[1] if key_scores is not None else 0
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    return out, lse
 
 
 def paged_decode_attn_q4(q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
@@ -489,21 +450,18 @@ def paged_decode_attn_q4(q, k_cache, v_cache, block_tables, context_lens, max_co
     """q=1 decode attention over a 4-bit cache. key_scores [S, >= max_context_len]
     (fp32), if given, gains each key's attention weight, summed over the query
     heads. Returns (out, lse)."""
-    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
-    with _on(stream):
-        out, lse, stride = _decode_inputs(q, block_tables, context_lens, int(max_context_len), out, lse,
-                                          with_lse, key_scores)
-        S, H_q, _ = q.shape
-        if workspace is None:
-            workspace = new_q4_decode_workspace(S, H_q, H_kv, int(max_context_len),
-                                                key_scores is not None, q.device)
-    _need(workspace, "workspace", torch.uint8, 1)
-    _need_current_device(workspace)
-    _check(lib().pkv_paged_decode_attn_q4(
-        _ptr(q), *ptrs, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-        int(max_context_len), S, H_q, H_kv, 128, group, bs, NB, float(scale), int(sliding_window),
-        _ptr(out), _ptr(lse), _ptr(key_scores), stride, _ptr(workspace), workspace.numel(),
-        _stream(stream)), "pkv_paged_decode_attn_q4")
+    if out is None or workspace is None or (lse is None and with_lse):
+        with _on(stream):
+            out, lse = _decode_outputs(q, out, lse, with_lse)
+            if workspace is None:
+                workspace = new_q4_decode_workspace(q.shape[0], q.shape[1], k_cache[0].shape[1],
+                                                    int(max_context_len), key_scores is not None,
+                                                    q.device)
+    st = _calls().paged_decode_attn_q4(k_cache, v_cache, q, block_tables, context_lens,
+                                         max_context_len, scale, out, lse, key_scores, workspace,
+                                         sliding_window, stream)
+    if st:
+        raise PkvError(st, "pkv_paged_decode_attn_q4")
     return out, lse
 
 
@@ -525,35 +483,18 @@ def paged_prefill_attn_q4(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block
                           workspace=None, stream=None, with_lse=True, sliding_window=0):
     """Varlen causal prefill over a 4-bit cache (arguments as paged_prefill_attn;
     total_k: an upper bound of cu_seqlens_k[-1]). Returns (out, lse)."""
-    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
-    _need(q, "q", torch.bfloat16, 3)
-    _need(cu_seqlens_q, "cu_seqlens_q", torch.int32, 1)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    T, H_q, D = q.shape
-    S = cu_seqlens_q.shape[0] - 1
-    if D != 128 or S < 0 or cu_seqlens_k.shape[0] != S + 1 or block_tables.shape[0] != S:
-        raise ValueError("inconsistent shapes")
-    with _on(stream):
-        out = torch.empty_like(q) if out is None else out
-        if lse is None and with_lse:
-            lse = torch.empty((T, H_q), dtype=torch.float32, device=q.device)
-        if workspace is None and S > 0 and T > 0:
-            workspace = new_q4_prefill_workspace(S, int(total_k), int(max_seqlen_k), H_kv, q.device)
-    _need(out, "out", torch.bfloat16, 3)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, 2)
-    if out.shape != q.shape or (lse is not None and lse.shape != (T, H_q)):
-        raise ValueError("inconsistent shapes")
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, 1)
-    _need_current_device(q, cu_seqlens_q, cu_seqlens_k, block_tables, out, lse, workspace)
-    _check(lib().pkv_paged_prefill_attn_q4(
-        _ptr(q), *ptrs, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), _ptr(block_tables),
-        block_tables.shape[1], S, T, int(total_k), int(max_seqlen_q), int(max_seqlen_k), H_q, H_kv,
-        128, group, bs, NB, float(scale), int(sliding_window), _ptr(out), _ptr(lse),
-        _ptr(workspace), workspace.numel() if workspace is not None else 0, _stream(stream)),
-        "pkv_paged_prefill_attn_q4")
+    if out is None or workspace is None or (lse is None and with_lse):
+        with _on(stream):
+            out, lse = _decode_outputs(q, out, lse, with_lse)
+            S = cu_seqlens_q.shape[0] - 1
+            if workspace is None and S > 0 and q.shape[0] > 0:
+                workspace = new_q4_prefill_workspace(S, int(total_k), int(max_seqlen_k),
+                                                     k_cache[0].shape[1], q.device)
+    st = _calls().paged_prefill_attn_q4(k_cache, v_cache, q, cu_seqlens_q, cu_seqlens_k,
+                                          block_tables, max_seqlen_q, max_seqlen_k, total_k, scale,
+                                          out, lse, workspace, sliding_window, stream)
+    if st:
+        raise PkvError(st, "pkv_paged_prefill_attn_q4")
     return out, lse
 
 
@@ -577,73 +518,29 @@ def paged_decode_attn_scores(q, k_cache, v_cache, block_tables, context_lens, ma
                              with_lse=True, sliding_window=0):
     """paged_decode_attn that also adds each key's attention weight, summed over
     the query heads, to key_scores [S, >= max_context_len] (fp32). Returns (out, lse)."""
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    _need(key_scores, "key_scores", torch.float32, 2)
-    NB, bs, H_kv, D = k_cache.shape
-    if v_cache.shape != k_cache.shape or D != 128:
-        raise ValueError("inconsistent shapes")
-    with _on(stream):
-        out, lse, stride = _decode_inputs(q, block_tables, context_lens, int(max_context_len), out, lse,
-                                          with_lse, key_scores)
-        S, H_q, _ = q.shape
-        if workspace is None:
-            workspace = new_decode_scores_workspace(S, H_q, H_kv, int(max_context_len), q.device)
-    _need(workspace, "workspace", torch.uint8, 1)
-    _need_current_device(k_cache, v_cache, workspace)
-    _check(lib().pkv_paged_decode_attn_scores(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
-        _ptr(context_lens), int(max_context_len), S, H_q, H_kv, 128, bs, NB, float(scale),
-        int(sliding_window), _ptr(out), _ptr(lse), _ptr(key_scores), stride, _ptr(workspace),
-        workspace.numel(), _stream(stream)), "pkv_paged_decode_attn_scores")
+    if out is None or workspace is None or (lse is None and with_lse):
+        with _on(stream):
+            out, lse = _decode_outputs(q, out, lse, with_lse)
+            if workspace is None:
+                workspace = new_decode_scores_workspace(q.shape[0], q.shape[1], k_cache.shape[2],
+                                                        int(max_context_len), q.device)
+    st = _calls().paged_decode_attn_scores(k_cache, v_cache, q, block_tables, context_lens,
+                                             max_context_len, scale, out, lse, key_scores,
+                                             workspace, sliding_window, stream)
+    if st:
+        raise PkvError(st, "pkv_paged_decode_attn_scores")
     return out, lse
 
 
 def evict_select(key_scores, context_lens, budget, recent, keep=None, new_lens=None, stream=None):
     """Positions that stay: the last `recent` and the highest-scoring others, budget
     in all, ascending. Returns (keep int32 [S, budget], -1 padded, new_lens int32 [S])."""
-    _need(key_scores, "key_scores", torch.float32, 2)
-    _need(context_lens, "context_lens", torch.int32, 1)
-    S, width = key_scores.shape
-    budget, recent = int(budget), int(recent)
-    if context_lens.shape[0] != S:
-        raise ValueError("inconsistent shapes")
     with _on(stream):
-        if keep is None:
-            keep = torch.empty((S, max(budget, 0)), dtype=torch.int32, device=key_scores.device)
-        if new_lens is None:
-            new_lens = torch.empty(S, dtype=torch.int32, device=key_scores.device)
-    _need(keep, "keep", torch.int32, 2)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    if keep.shape != (S, budget) or new_lens.shape[0] != S:
-        raise ValueError("inconsistent shapes")
-    _need_current_device(key_scores, context_lens, keep, new_lens)
-    _check(lib().pkv_evict_select(_ptr(key_scores), width, _ptr(context_lens), width, S, budget,
-                                  recent, _ptr(keep), _ptr(new_lens), _stream(stream)),
-           "pkv_evict_select")
+        st, keep, new_lens = _calls().evict_select(key_scores, context_lens, budget, recent, keep,
+                                                     new_lens, stream)
+    if st:
+        raise PkvError(st, "pkv_evict_select")
     return keep, new_lens
-
-
-def _compact_args(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores):
-    """Checked arguments shared by the two compactions: (tables .. num_seqs, scores)."""
-    _need(src_tables, "src_tables", torch.int32, 2)
-    _need(dst_tables, "dst_tables", torch.int32, 2)
-    _need(keep, "keep", torch.int32, 2)
-    _need(new_lens, "new_lens", torch.int32, 1)
-    S = src_tables.shape[0]
-    if dst_tables.shape[0] != S or keep.shape[0] != S or new_lens.shape[0] != S:
-        raise ValueError("inconsistent shapes")
-    strides = [0, 0]
-    for i, (t, name) in enumerate(((key_scores, "key_scores"), (dst_key_scores, "dst_key_scores"))):
-        if t is not None:
-            _need(t, name, torch.float32, 2)
-            if t.shape[0] != S:
-                raise ValueError("inconsistent shapes")
-            strides[i] = t.shape[1]
-    _need_current_device(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores)
-    return ((_ptr(src_tables), src_tables.shape[1], _ptr(dst_tables), dst_tables.shape[1], _ptr(keep),
-             keep.shape[1], _ptr(new_lens), S),
-            (_ptr(key_scores), strides[0], _ptr(dst_key_scores), strides[1]))
 
 
 def evict_compact(k_cache, v_cache, src_tables, dst_tables, keep, new_lens, key_scores=None,
@@ -651,24 +548,19 @@ def evict_compact(k_cache, v_cache, src_tables, dst_tables, keep, new_lens, key_
     """Move each sequence's kept rows (evict_select) to positions 0 .. new_lens - 1 of
     dst_tables; equal tables compact in place. The scores move along, with zeros
     behind them (pass the same tensor twice for in place)."""
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    NB, bs, H_kv, D = k_cache.shape
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("inconsistent shapes")
-    _need_current_device(k_cache, v_cache)
-    rows, scores = _compact_args(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores)
-    _check(lib().pkv_evict_compact(_ptr(k_cache), _ptr(v_cache), *rows, H_kv, D, bs, NB, *scores,
-                                   _stream(stream)), "pkv_evict_compact")
+    st = _calls().evict_compact(k_cache, v_cache, src_tables, dst_tables, keep, new_lens,
+                                  key_scores, dst_key_scores, stream)
+    if st:
+        raise PkvError(st, "pkv_evict_compact")
 
 
 def evict_compact_q4(k_cache, v_cache, src_tables, dst_tables, keep, new_lens, key_scores=None,
                      dst_key_scores=None, stream=None):
     """evict_compact for a 4-bit cache."""
-    ptrs, (NB, bs, H_kv, group) = _q4(k_cache, v_cache)
-    rows, scores = _compact_args(src_tables, dst_tables, keep, new_lens, key_scores, dst_key_scores)
-    _check(lib().pkv_evict_compact_q4(*ptrs, *rows, H_kv, 128, group, bs, NB, *scores,
-                                      _stream(stream)), "pkv_evict_compact_q4")
+    st = _calls().evict_compact_q4(k_cache, v_cache, src_tables, dst_tables, keep, new_lens,
+                                     key_scores, dst_key_scores, stream)
+    if st:
+        raise PkvError(st, "pkv_evict_compact_q4")
 
 
 def check_device_errors(stream=None) -> int:

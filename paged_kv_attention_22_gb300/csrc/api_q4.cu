@@ -46,26 +46,62 @@ pkv_status check_attention(const pkv::Q4CacheArgs &c, int32_t num_q_heads, int32
   return PKV_OK;
 }
 
-// Splits: enough CTAs to fill the SMs (four CTAs an SM) when there are few
-// (sequence, KV head) pairs, splits no shorter than kSplitMin keys, and none
-// longer than kSplitMax, so that one long sequence in a batch of short ones is
-// not left to a single CTA.
-constexpr int32_t kSplitMin = 128, kSplitMax = 4096;
-constexpr int32_t kCtasPerSm = 4;
+// The plan of a decode call: warps a CTA (4, 8 or 16) and splits of the keys of
+// each (sequence, KV head) pair, by the least estimated time. With a step of 32
+// keys as the unit, an SM with 4, 8, 12 or 16 resident warps gets through 4.7,
+// 6.4, 7.4 or 8 steps a microsecond (measured with 16 x 8 pairs of 16,384 keys;
+// 16 warps are the most its registers hold); a CTA costs some 2 us to start and
+// finish, which its neighbours on the SM cover in part, and splits cost the 3 us
+// of the merge kernel. Measured against it, in us: 512 pairs of 640 keys 15.9
+// with 4 warps and one split, 18.6 with 8 warps, 20.9 with two splits; 128 pairs
+// of 16,384 keys 108 with 4 warps and one split, 69 with 16 warps, 70 with 4
+// warps and seven splits.
+// No CTA gets more than kWarpKeys keys a warp, so that one long sequence in a
+// batch of short ones is not left to a single CTA.
+constexpr int32_t kStepKeys = 32, kWarpKeys = 1024, kMaxSplits = 64, kCtasPerSm = 16;
 
+pkv::Q4DecodePlan search_plan(int64_t pairs, int64_t keys, int sms) {
+  const int64_t steps = (keys + kStepKeys - 1) / kStepKeys;
+  pkv::Q4DecodePlan best = {};
+  double best_us = 0;
+  for (int warps = 4; warps <= 16; warps *= 2) {
+    const int64_t least = (keys + kWarpKeys * warps - 1) / (kWarpKeys * warps);
+    const int64_t most = std::max(least, std::min<int64_t>(kMaxSplits, sms * kCtasPerSm / pairs));
+    for (int64_t n = least; n <= most; ++n) {
+      const int64_t split = (steps + n - 1) / n;           // steps a CTA
+      const int64_t used = (steps + split - 1) / split;    // splits that get any
+      if (used > least && split < warps) break;            // warps without work
+      const int64_t per_sm = (pairs * used + sms - 1) / sms, per_warp = (split + warps - 1) / warps;
+      const int64_t resident = std::min<int64_t>(16, per_sm * warps);
+      const double rate = resident <= 4 ? 4.7 : resident <= 8 ? 6.4 : resident <= 12 ? 7.4 : 8.0;
+      const double rounds = std::max(1.0, static_cast<double>(per_sm * warps) / 16);
+      const double us = per_sm * per_warp * warps / rate + 2 * rounds + (used > 1 ? 3.0 : 0.0) + (warps == 16 ? 0.8 : 0.0);
+      if (best.warps == 0 || us < best_us) {
+        best = {static_cast<int32_t>(used), static_cast<int32_t>(split * kStepKeys), warps};
+        best_us = us;
+      }
+    }
+  }
+  return best;
+}
+
+// The search takes a few microseconds: this thread's last plan is kept.
 pkv::Q4DecodePlan decode_plan(int64_t pairs, int64_t keys, int sms) {
-  const int64_t fill = std::max<int64_t>(1, static_cast<int64_t>(sms) * kCtasPerSm / pairs);
-  int64_t n = std::min<int64_t>(fill, (keys + kSplitMin - 1) / kSplitMin);
-  n = std::max<int64_t>(n, (keys + kSplitMax - 1) / kSplitMax);
-  pkv::Q4DecodePlan p;
-  p.split_keys = static_cast<int32_t>(align_up(static_cast<size_t>((keys + n - 1) / n), 16));
-  p.n_splits = static_cast<int32_t>((keys + p.split_keys - 1) / p.split_keys);
-  return p;
+  thread_local int64_t of[3] = {0, 0, 0};
+  thread_local pkv::Q4DecodePlan plan = {};
+  if (of[0] != pairs || of[1] != keys || of[2] != sms) {
+    plan = search_plan(pairs, keys, sms);
+    of[0] = pairs;
+    of[1] = keys;
+    of[2] = sms;
+  }
+  return plan;
 }
 
 // No plan for these sizes or smaller ones has more pieces.
 int64_t max_pieces(int64_t pairs, int64_t keys, int sms) {
-  return std::max(pairs, static_cast<int64_t>(sms) * kCtasPerSm) + pairs * ((keys + kSplitMax - 1) / kSplitMax);
+  return std::max<int64_t>(pairs, static_cast<int64_t>(sms) * kCtasPerSm) +
+         pairs * ((keys + 4 * kWarpKeys - 1) / (4 * kWarpKeys));
 }
 
 struct DecodeWorkspace {

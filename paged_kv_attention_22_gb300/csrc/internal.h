@@ -185,9 +185,10 @@ cudaError_t launch_q4_gather(const Q4GatherArgs &a, cudaStream_t stream);
 cudaError_t q4_cache_error_word(uint32_t **word);
 
 // How a decode call over the 4-bit cache cuts the keys of each (sequence, KV
-// head): n_splits CTAs of split_keys keys (a multiple of 16).
+// head): n_splits CTAs of `warps` (4, 8 or 16) warps and split_keys keys (a
+// multiple of 32).
 struct Q4DecodePlan {
-  int32_t n_splits, split_keys;
+  int32_t n_splits, split_keys, warps;
 };
 struct Q4DecodeArgs {
   Q4CacheArgs cache;

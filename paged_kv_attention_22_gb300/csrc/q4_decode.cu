@@ -2,7 +2,7 @@
 // sequence.
 //
 // The keys of a (sequence, KV head) are cut into splits, one CTA each; the
-// CTA's four warps take the split's steps of 32 keys (two units of 16) in turn. A
+// CTA's warps take the split's steps of 32 keys (two units of 16) in turn. A
 // unit's codes are 1 KiB of K and 1 KiB of V, contiguous in the cache, and its
 // parameters 64 to 256 bytes of each. Every warp streams its steps through a
 // ring of its own with cp.async, so no warp waits for another before the end of
@@ -38,13 +38,13 @@ static __device__ uint32_t g_q4_decode_errors;
 namespace {
 
 constexpr int kD = kQ4D;
-constexpr int kWarps = 4;
 constexpr int kUnit = 16;                    // keys a unit
 constexpr int kStep = 2 * kUnit;             // keys a step
 constexpr int kStages = 2;                   // steps in a warp's ring
 constexpr int kMaxG = 8;                     // query heads a KV head (columns of a P^T tile)
 constexpr int kUnitCodes = kUnit * kQ4RowBytes;  // 1 KiB of K or V codes
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kFloor = -1.7e38f;           // below every logit; differences stay finite
 constexpr float kLazyMax = 8.0f;             // log2 units the running max may lag
 
 struct Q4DecodeParams {
@@ -60,10 +60,11 @@ struct Q4DecodeParams {
   FastDiv block;
   int32_t max_blocks, max_context_len, num_q_heads, num_kv_heads, num_blocks;
   int32_t gqa, window, n_splits, split_keys;
-  float scale_log2;
+  float scale_log2;  // > 0: the sign of the scale is in q_signs, which flips q's
+  uint32_t q_signs;
 };
 
-template <int NG>  // parameter groups a row: 4, 2 or 1
+template <int NG, int kWarps>  // parameter groups a row: 4, 2 or 1; warps a CTA: 4, 8 or 16
 struct Q4DecodeSmem {
   static constexpr int kParamBytes = kUnit * NG * 4;
   static constexpr int kUnitBytes = 2 * kUnitCodes + 2 * kParamBytes;  // K, V codes, K, V parameters
@@ -120,9 +121,9 @@ __device__ __forceinline__ KeyRange key_range(const Q4DecodeParams &p, int s) {
   return r;
 }
 
-template <int NG>
-__global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4DecodeParams p) {
-  using L = Q4DecodeSmem<NG>;
+template <int NG, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(const Q4DecodeParams p) {
+  using L = Q4DecodeSmem<NG, kWarps>;
   extern __shared__ __align__(128) uint8_t smem[];
   griddep_wait();  // inputs written by the previous kernel are visible from here on
   griddep_launch_dependents();
@@ -151,7 +152,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
     const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * kD + 32 * t);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const uint4 x = g < G ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+      uint4 x = g < G ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+      x.x ^= p.q_signs;
+      x.y ^= p.q_signs;
+      x.z ^= p.q_signs;
+      x.w ^= p.q_signs;
       qb[2 * w][0] = q4_low_halves(x.x, x.z);
       qb[2 * w][1] = q4_high_halves(x.x, x.z);
       qb[2 * w + 1][0] = q4_low_halves(x.y, x.w);
@@ -221,8 +226,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
   for (int m = 0; m < 8; ++m)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-  // of heads 2 t and 2 t + 1; the sums are over this lane's keys
-  float mx[2] = {-INFINITY, -INFINITY}, lsum[2] = {0.f, 0.f}, rsum[2] = {0.f, 0.f};
+  // of heads 2 t and 2 t + 1; lsum is over this lane's keys, rsum (a product's
+  // fragment, its rows all alike) over the warp's. The maximum starts at a finite
+  // floor, so that masked logits (-inf) have probability 0 even before the first
+  // real one.
+  float mx[2] = {kFloor, kFloor}, lsum[2] = {0.f, 0.f}, rsum[4] = {0.f, 0.f, 0.f, 0.f};
 
 #pragma unroll
   for (int i = 0; i < kStages; ++i) issue(i);
@@ -239,7 +247,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
     const int key0 = key_begin + (warp + kWarps * it) * kStep;
 
     // ---- S^T = K Q^T
-    float z[2][4];  // keys kperm, 8 + kperm of each unit, heads 2 t, 2 t + 1: [u][2 * key + head]
+    float z[2][4];  // unscaled; keys kperm, 8 + kperm of each unit, heads 2 t, 2 t + 1: [u][2 * key + head]
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const uint8_t *su = st + u * L::kUnitBytes;
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
         s2[j] = q4_dup_scale(pw);
         b2[j] = q4_dup_offset(pw);
       }
-      float sc[4] = {0.f, 0.f, 0.f, 0.f};
+      float sc[2][4] = {};  // two chains of products
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t x[2][4];
@@ -266,11 +274,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[j][i] = fma_bf16x2(x[j][i], s2[j], b2[j]);
         }
-        mma_16816(sc, x[0][0], x[1][0], x[0][1], x[1][1], qb[2 * w][0], qb[2 * w][1]);
-        mma_16816(sc, x[0][2], x[1][2], x[0][3], x[1][3], qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        mma_16816(sc[0], x[0][0], x[1][0], x[0][1], x[1][1], qb[2 * w][0], qb[2 * w][1]);
+        mma_16816(sc[1], x[0][2], x[1][2], x[0][3], x[1][3], qb[2 * w + 1][0], qb[2 * w + 1][1]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[u][i] = sc[i] * p.scale_log2;
+      for (int i = 0; i < 4; ++i) z[u][i] = sc[0][i] + sc[1][i];
     }
 
     // ---- masks, softmax
@@ -290,8 +298,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (2 * t + c >= G) continue;
-          dst[c * p.logits_ld + u * kUnit] = z[u][c];
-          dst[c * p.logits_ld + u * kUnit + 8] = z[u][2 + c];
+          dst[c * p.logits_ld + u * kUnit] = z[u][c] * p.scale_log2;
+          dst[c * p.logits_ld + u * kUnit + 8] = z[u][2 + c] * p.scale_log2;
         }
       }
     }
@@ -308,42 +316,39 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
           if (4 * i + t < lo || 4 * i + t >= hi) pv[u][i] = 0u;
       }
     }
-    const float zm0 = fmaxf(fmax3(z[0][0], z[0][2], z[1][0]), z[1][2]);
-    const float zm1 = fmaxf(fmax3(z[0][1], z[0][3], z[1][1]), z[1][3]);
+    const float zm0 = fmaxf(fmax3(z[0][0], z[0][2], z[1][0]), z[1][2]) * p.scale_log2;
+    const float zm1 = fmaxf(fmax3(z[0][1], z[0][3], z[1][1]), z[1][3]) * p.scale_log2;
     if (__any_sync(0xffffffffu, zm0 > mx[0] + kLazyMax || zm1 > mx[1] + kLazyMax)) {  // always on a first step
       float m_new[2] = {fmaxf(zm0, mx[0]), fmaxf(zm1, mx[1])}, alpha[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) m_new[c] = fmaxf(m_new[c], __shfl_xor_sync(0xffffffffu, m_new[c], off));
-        alpha[c] = m_new[c] == -INFINITY ? 1.f : fast_exp2(mx[c] - m_new[c]);
+        alpha[c] = fast_exp2(mx[c] - m_new[c]);
         mx[c] = m_new[c];
         lsum[c] *= alpha[c];
-        rsum[c] *= alpha[c];
       }
 #pragma unroll
       for (int m = 0; m < 8; ++m)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][i] *= alpha[i & 1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rsum[i] *= alpha[i & 1];
     }
-    // logits of -inf alone have probability 0
-    const float ref[2] = {mx[0] == -INFINITY ? 0.f : mx[0], mx[1] == -INFINITY ? 0.f : mx[1]};
     uint32_t pb[2][2];  // P^T fragments of each unit
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float pr[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        pr[i] = fast_exp2(z[u][i] - ref[i & 1]);
+        pr[i] = fast_exp2(fmaf(z[u][i], p.scale_log2, -mx[i & 1]));
         lsum[i & 1] += pr[i];
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t x = pack_bf16x2(pr[2 * j], pr[2 * j + 1]);
-        rsum[0] += bf16lo(x);
-        rsum[1] += bf16hi(x);
-        pb[u][j] = transpose_8x8(x);
-      }
+      for (int j = 0; j < 2; ++j) pb[u][j] = transpose_8x8(pack_bf16x2(pr[2 * j], pr[2 * j + 1]));
+      // the sums of the rounded probabilities are one more product, with ones
+      constexpr uint32_t kOnes = 0x3F803F80u;
+      mma_16816(rsum, kOnes, kOnes, kOnes, kOnes, pb[u][0], pb[u][1]);
     }
 
     // ---- O^T += V^T P^T
@@ -378,14 +383,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
     issue(it + kStages);
   }
 
-  // ---- join the four warps
+  // ---- join the warps
 #pragma unroll
   for (int c = 0; c < 2; ++c)
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      lsum[c] += __shfl_xor_sync(0xffffffffu, lsum[c], off);
-      rsum[c] += __shfl_xor_sync(0xffffffffu, rsum[c], off);
-    }
+    for (int off = 4; off < 32; off <<= 1) lsum[c] += __shfl_xor_sync(0xffffffffu, lsum[c], off);
   cp_async_wait<0>();
   __syncthreads();  // no warp still reads or fills its ring
   float *so = reinterpret_cast<float *>(smem);                       // [warp][G][128]
@@ -402,79 +404,84 @@ __global__ void __launch_bounds__(kWarps * 32, 4) q4_decode_kernel(const Q4Decod
     if (g == 0 && 2 * t + c < G) sml[warp * kMaxG + 2 * t + c] = make_float4(mx[c], lsum[c], rsum[c], 0.f);
   __syncthreads();
   const bool whole = range.unit0 + static_cast<int64_t>(p.split_keys) >= range.ctx;
-  const int d = threadIdx.x;
-  for (int h = 0; h < G; ++h) {
-    float4 ml[kWarps];
+  const int d = threadIdx.x % kD;
+  for (int h = threadIdx.x / kD; h < G; h += kWarps * 32 / kD) {
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      ml[w] = sml[w * kMaxG + h];
-      M = fmaxf(M, ml[w].x);
-    }
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w * kMaxG + h].x);
     float o = 0.f, l = 0.f, r = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = ml[w].x == -INFINITY ? 0.f : fast_exp2(ml[w].x - M);
+      const float4 ml = sml[w * kMaxG + h];
+      const float f = fast_exp2(ml.x - M);
       o = fmaf(so[(w * kMaxG + h) * kD + d], f, o);
-      l = fmaf(ml[w].y, f, l);
-      r = fmaf(ml[w].z, f, r);
+      l = fmaf(ml.y, f, l);
+      r = fmaf(ml.z, f, r);
     }
     const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + head * G + h;
     if (whole) {
       p.out[row * kD + d] = __float2bfloat16_rn(o / r);
       if (d == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kLn2;
     } else {
-      const int64_t piece = ((static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits + split) * G + h;
-      __stcg(p.ws_o + piece * kD + d, o);
-      if (d == 0) __stcg(p.ws_ml + piece, make_float4(M, l, r, 0.f));
+      const int64_t at = ((static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits + split) * G + h;
+      __stcg(p.ws_o + at * kD + d, o);
+      if (d == 0) __stcg(p.ws_ml + at, make_float4(M, l, r, 0.f));
     }
   }
 }
 
-// Join the splits of the (sequence, query head)s that have more than one. Four
-// groups of 128 threads, one thread a dim, take the splits in turn.
-constexpr int kMergeGroups = 4;
+// Join the splits of the (sequence, query head)s that have more than one: a
+// warp each, four dims a lane.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeBatch = 8;  // splits whose loads are in flight
 
-__global__ void __launch_bounds__(kMergeGroups * kD) q4_merge_kernel(const Q4DecodeParams p) {
-  __shared__ float so[kMergeGroups][kD];
-  __shared__ float sl[kMergeGroups], sr[kMergeGroups];
+__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4DecodeParams p, int32_t num_seqs) {
   griddep_wait();
   griddep_launch_dependents();
-  const int hq = blockIdx.x, s = blockIdx.y;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(num_seqs) * p.num_q_heads) return;
+  const int s = static_cast<int>(row / p.num_q_heads), hq = static_cast<int>(row - static_cast<int64_t>(s) * p.num_q_heads);
   const KeyRange range = key_range(p, s);
-  const int n = range.ctx <= 0 ? 0 : (range.ctx - range.unit0 + p.split_keys - 1) / p.split_keys;
-  if (n <= 1) return;  // invalid, or written whole
+  if (range.ctx <= 0) return;
+  const int n = (range.ctx - range.unit0 + p.split_keys - 1) / p.split_keys;
+  if (n <= 1) return;  // written whole
   const int G = p.gqa, head = hq / G, h = hq % G;
-  const int64_t piece0 = (static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits * G + h;
-  const int d = threadIdx.x % kD, grp = threadIdx.x / kD;
+  const int64_t split0 = (static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits * G + h;
   float M = -INFINITY;
-  for (int i = 0; i < n; ++i) M = fmaxf(M, p.ws_ml[piece0 + static_cast<int64_t>(i) * G].x);
-  float o = 0.f, l = 0.f, r = 0.f;
-#pragma unroll 4
-  for (int i = grp; i < n; i += kMergeGroups) {
-    const int64_t piece = piece0 + static_cast<int64_t>(i) * G;
-    const float4 ml = p.ws_ml[piece];
-    const float f = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
-    o = fmaf(p.ws_o[piece * kD + d], f, o);
-    l = fmaf(ml.y, f, l);
-    r = fmaf(ml.z, f, r);
-  }
-  so[grp][d] = o;
-  if (d == 0) {
-    sl[grp] = l;
-    sr[grp] = r;
-  }
-  __syncthreads();
-  if (grp != 0) return;
+  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ws_ml[split0 + static_cast<int64_t>(i) * G].x);
 #pragma unroll
-  for (int i = 1; i < kMergeGroups; ++i) {
-    o += so[i][d];
-    l += sl[i];
-    r += sr[i];
+  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, r = 0.f;
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
+    float4 ml[kMergeBatch], ov[kMergeBatch];
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      ml[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      ov[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i0 + u < n) {
+        const int64_t at = split0 + static_cast<int64_t>(i0 + u) * G;
+        ml[u] = p.ws_ml[at];
+        ov[u] = reinterpret_cast<const float4 *>(p.ws_o + at * kD)[lane];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const float f = fast_exp2(ml[u].x - M);
+      o[0] = fmaf(ov[u].x, f, o[0]);
+      o[1] = fmaf(ov[u].y, f, o[1]);
+      o[2] = fmaf(ov[u].z, f, o[2]);
+      o[3] = fmaf(ov[u].w, f, o[3]);
+      l = fmaf(ml[u].y, f, l);
+      r = fmaf(ml[u].z, f, r);
+    }
   }
-  const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + hq;
-  p.out[row * kD + d] = __float2bfloat16_rn(o / r);
-  if (d == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kLn2;
+  uint2 v;
+  v.x = pack_bf16x2(o[0] / r, o[1] / r);
+  v.y = pack_bf16x2(o[2] / r, o[3] / r);
+  reinterpret_cast<uint2 *>(p.out + row * kD)[lane] = v;
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kLn2;
 }
 
 __global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScoresParams p) {
@@ -483,14 +490,26 @@ __global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScore
   key_scores_body(p);
 }
 
-template <int NG>
+template <int NG, int kWarps>
 cudaError_t launch_splits(const Q4DecodeParams &p, int32_t num_seqs, cudaStream_t stream) {
-  constexpr int kSmem = Q4DecodeSmem<NG>::kTotal;
-  cudaError_t e =
-      cudaFuncSetAttribute(q4_decode_kernel<NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(q4_decode_kernel<NG>, dim3(p.n_splits, p.num_kv_heads, num_seqs), dim3(kWarps * 32),
+  constexpr int kSmem = Q4DecodeSmem<NG, kWarps>::kTotal;
+  if (kSmem > 48 * 1024) {
+    cudaError_t e =
+        cudaFuncSetAttribute(q4_decode_kernel<NG, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(q4_decode_kernel<NG, kWarps>, dim3(p.n_splits, p.num_kv_heads, num_seqs), dim3(kWarps * 32),
                     kSmem, stream, p);
+}
+
+template <int NG>
+cudaError_t launch_warps(const Q4DecodeParams &p, int32_t warps, int32_t num_seqs, cudaStream_t stream) {
+  switch (warps) {
+    case 4: return launch_splits<NG, 4>(p, num_seqs, stream);
+    case 8: return launch_splits<NG, 8>(p, num_seqs, stream);
+    case 16: return launch_splits<NG, 16>(p, num_seqs, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace
@@ -520,17 +539,22 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
   p.window = a.window;
   p.n_splits = a.plan.n_splits;
   p.split_keys = a.plan.split_keys;
-  p.scale_log2 = a.scale_log2;
+  // a scale of 0 becomes the smallest positive one: its logits stay below 2^-100
+  // unless a product passes 2^26, and masked logits stay -inf
+  p.scale_log2 = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
+  p.q_signs = a.scale_log2 < 0.f ? 0x80008000u : 0u;
   cudaError_t e;
   switch (a.cache.group_size) {
-    case 32: e = launch_splits<4>(p, a.num_seqs, stream); break;
-    case 64: e = launch_splits<2>(p, a.num_seqs, stream); break;
-    case 128: e = launch_splits<1>(p, a.num_seqs, stream); break;
+    case 32: e = launch_warps<4>(p, a.plan.warps, a.num_seqs, stream); break;
+    case 64: e = launch_warps<2>(p, a.plan.warps, a.num_seqs, stream); break;
+    case 128: e = launch_warps<1>(p, a.plan.warps, a.num_seqs, stream); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
   if (p.n_splits > 1) {
-    e = launch_pdl(q4_merge_kernel, dim3(p.num_q_heads, a.num_seqs), dim3(kMergeGroups * kD), 0, stream, p);
+    const int64_t rows = static_cast<int64_t>(a.num_seqs) * p.num_q_heads;
+    e = launch_pdl(q4_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps)),
+                   dim3(kMergeWarps * 32), 0, stream, p, a.num_seqs);
     if (e != cudaSuccess) return e;
   }
   if (a.key_scores == nullptr) return cudaSuccess;

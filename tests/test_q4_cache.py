@@ -139,7 +139,11 @@ def test_binding_refuses_shapes_and_types():
     k = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
     sm = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(TypeError):
-        pkv.kv_store_q4(k, k, k, k, sm)                                  # not a pair
+        pkv.kv_store_q4(k.tolist(), k, k, k, sm)                         # not a tensor
+    with pytest.raises(TypeError):
+        pkv.kv_store_q4(k.float(), k, k, k, sm)                          # not bf16
+    with pytest.raises(TypeError):
+        pkv.paged_decode_attn_q4(k, k, k, sm, sm, 1, 1.0, k, sm, sm)     # caches that are not pairs
     with pytest.raises(ValueError):
         pkv.kv_store_q4(k, k, pkv.new_q4_cache(1, 16, 1, device="cpu"),  # CPU tensors
                         pkv.new_q4_cache(1, 16, 1, device="cpu"), sm)
