@@ -31,6 +31,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelLoads = 16;
 constexpr int kBins = 256;
 constexpr int kHistCopies = 8;  // histograms, each shared by four warps, against contention
 constexpr size_t kSelMaxKeyBytes = 200 * 1024;  // beside the histograms
@@ -88,14 +89,22 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     __syncthreads();
     uint32_t *h = hist[warp % kHistCopies];
     if (shift == 24) {
-#pragma unroll 4
-      for (int i = tid; i < old; i += kSelThreads) {
-        const uint32_t k = score_key(score[i]);
-        if (kCached) s_keys[i] = k;
-        atomicAdd(&h[k >> 24], 1u);
+      // the one pass over global memory: kSelLoads loads a thread in flight
+      for (int i0 = tid; i0 < old; i0 += kSelThreads * kSelLoads) {
+        float f[kSelLoads];
+#pragma unroll
+        for (int u = 0; u < kSelLoads; ++u) f[u] = i0 + u * kSelThreads < old ? score[i0 + u * kSelThreads] : 0.f;
+#pragma unroll
+        for (int u = 0; u < kSelLoads; ++u) {
+          const int i = i0 + u * kSelThreads;
+          if (i >= old) break;
+          const uint32_t k = score_key(f[u]);
+          if (kCached) s_keys[i] = k;
+          atomicAdd(&h[k >> 24], 1u);
+        }
       }
     } else {
-#pragma unroll 4
+#pragma unroll 8
       for (int i = tid; i < old; i += kSelThreads) {
         const uint32_t k = key_of(i);
         if ((k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&h[(k >> shift) & 255u], 1u);
@@ -310,7 +319,7 @@ __device__ void move_scores(const CompactParams &p, int s, int n) {
 }
 
 // Grid (CTAs a sequence, the last one for the scores if there are any; sequences).
-__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_compact_kernel(const CompactParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int s = blockIdx.y;

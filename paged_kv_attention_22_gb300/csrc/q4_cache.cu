@@ -3,9 +3,9 @@
 // keys of a prefill batch into a bf16 workspace (first half of
 // pkv_paged_prefill_attn_q4).
 //
-// Half a warp handles one row of 128 values: eight values a lane, so that a
-// lane's codes are one 32-bit word; lanes 0-15 take a (token, head)'s K row and
-// lanes 16-31 its V row. A warp has several such pairs' loads in flight.
+// A (token, head)'s K row and V row are handled together, by 8 lanes each in the
+// store (16 values a lane) and by 16 in the others (8 values a lane, one 32-bit
+// word of codes). A warp has several such pairs' loads in flight.
 //
 // All three are copies with some arithmetic: HBM bandwidth bounds them, once the
 // arithmetic is short enough (the store spends about six packed operations on
@@ -20,7 +20,7 @@ static __device__ uint32_t g_q4_cache_errors;
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kStoreRows = 4;  // (token, head) pairs whose loads a warp has in flight
+constexpr int kStoreRows = 4;  // (token, head) pairs whose loads a warp has in flight, two at a time
 constexpr int kLoadRows = 8;
 
 // The smaller of each half; a NaN in either operand wins.
@@ -30,12 +30,15 @@ __device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// (smallest, -largest) of the eight values of x, as a bf16 pair.
-__device__ __forceinline__ uint32_t extremes(const uint4 x) {
+// (smallest, -largest) of the sixteen values of x, as a bf16 pair.
+__device__ __forceinline__ uint32_t extremes(const uint32_t (&x)[8]) {
   constexpr uint32_t kSigns = 0x80008000u;
-  const uint32_t lo = min_nan_bf16x2(min_nan_bf16x2(x.x, x.y), min_nan_bf16x2(x.z, x.w));
-  const uint32_t hi = min_nan_bf16x2(min_nan_bf16x2(x.x ^ kSigns, x.y ^ kSigns),
-                                     min_nan_bf16x2(x.z ^ kSigns, x.w ^ kSigns));
+  uint32_t lo = x[0], hi = x[0] ^ kSigns;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) {
+    lo = min_nan_bf16x2(lo, x[i]);
+    hi = min_nan_bf16x2(hi, x[i] ^ kSigns);
+  }
   return min_nan_bf16x2(q4_low_halves(lo, hi), q4_high_halves(lo, hi));
 }
 
@@ -54,12 +57,12 @@ __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
   return pack_bf16x2(s, b);
 }
 
-// Codes of eight values, n = clamp(floor(t / s + 1/2) - 16, 0, 15) with
-// t = fp32(x - b), one value at a time. The quotient is only estimated and
+// Codes of the eight values in four words, n = clamp(floor(t / s + 1/2) - 16, 0, 15)
+// with t = fp32(x - b), one value at a time. The quotient is only estimated and
 // rounded to the nearest integer c; the two comparisons with the thresholds
 // (c - 1/2) s and (c + 1/2) s, which are exact in fp32 (s has 8 bits, c at most
 // 12 here), settle it.
-__device__ __noinline__ uint32_t codes_one_by_one(const uint4 x, float s, float b) {
+__device__ __noinline__ uint32_t codes_one_by_one(uint4 x, float s, float b) {
   const float r = 1.f / s, h = 0.5f * s;
   const uint32_t wx[4] = {x.x, x.y, x.z, x.w};
   uint32_t codes = 0;
@@ -75,27 +78,28 @@ __device__ __noinline__ uint32_t codes_one_by_one(const uint4 x, float s, float 
   return codes;
 }
 
-// The same, two values at a time. y = t r' + M, with r' a little above 1 / s
-// and M = 2^23 + 2^22 - 16, rounds the quotient to an integer c in its low
-// mantissa bits, which then hold the code. r' exceeds the reciprocal by 2^-19,
+// The same for sixteen values, two at a time. y = t r' + M, with r' a little
+// above 1 / s and M = 2^23 + 2^22 - 16, rounds the quotient to an integer c in its
+// low mantissa bits, which then hold the code. r' exceeds the reciprocal by 2^-19,
 // more than the estimate's own error, so that a half (common: the inputs have 8
 // bits) rounds up and a quotient at most 2^-14 below one may do so wrongly: the
 // remainder t - c s, exact in fp32, is then below -s / 2 and the code one less.
 // Only groups whose offset's rounding pushes an extreme past the code range
 // need clamping; they take the other way.
-__device__ __forceinline__ uint32_t codes_of(const uint4 x, uint32_t pw, float lo, float hi) {
+__device__ __forceinline__ uint2 codes_of(const uint32_t (&x)[8], uint32_t pw, float lo, float hi) {
   constexpr float kM = 12582896.f;
   const float s = bf16lo(pw), b = bf16hi(pw);
-  if (s == 0.f) return 0u;
+  if (s == 0.f) return make_uint2(0u, 0u);
+  if (lo - b < 15.75f * s || hi - b > 31.25f * s)
+    return make_uint2(codes_one_by_one(make_uint4(x[0], x[1], x[2], x[3]), s, b),
+                      codes_one_by_one(make_uint4(x[4], x[5], x[6], x[7]), s, b));
   const float r = __fdividef(1.f + 0x1p-19f, s), nh = -0.5f * s;
-  if (lo - b < 15.75f * s || hi - b > 31.25f * s) return codes_one_by_one(x, s, b);
   const uint64_t nb2 = f32x2(-b, -b), r2 = f32x2(r, r), m2 = f32x2(kM, kM), s2 = f32x2(s, s);
   const uint64_t one2 = f32x2(1.f, 1.f), neg2 = f32x2(-1.f, -1.f);
-  const uint32_t wx[4] = {x.x, x.y, x.z, x.w};
-  uint32_t byte[4];
+  uint32_t byte[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint64_t t = fma2(f32x2(bf16lo(wx[i]), bf16hi(wx[i])), one2, nb2);
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t t = fma2(f32x2(bf16lo(x[i]), bf16hi(x[i])), one2, nb2);
     const uint64_t y = fma2(t, r2, m2);
     const uint64_t rest = fma2(fma2(y, neg2, m2), s2, t);  // t - c s
     uint32_t n0 = static_cast<uint32_t>(y), n1 = static_cast<uint32_t>(y >> 32);
@@ -103,7 +107,12 @@ __device__ __forceinline__ uint32_t codes_of(const uint4 x, uint32_t pw, float l
     if (f32x2_hi(rest) < nh) n1 -= 1;
     byte[i] = n1 * 16 + n0;  // its low byte
   }
-  return __byte_perm(__byte_perm(byte[0], byte[1], 0x0040), __byte_perm(byte[2], byte[3], 0x0040), 0x5410);
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = __byte_perm(__byte_perm(byte[4 * i], byte[4 * i + 1], 0x0040),
+                       __byte_perm(byte[4 * i + 2], byte[4 * i + 3], 0x0040), 0x5410);
+  return make_uint2(w[0], w[1]);
 }
 
 struct Q4RowsParams {
@@ -118,12 +127,11 @@ struct Q4RowsParams {
   int64_t num_slots;
 };
 
-__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
+// 32 bytes, 32-byte aligned or (two loads) 16-byte aligned.
+__device__ __forceinline__ void ld_stream(const uint4 *p, uint32_t (&r)[8]) {
+  const uint4 a = __ldcs(p), b = __ldcs(p + 1);
+  r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w;
+  r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
 }
 
 // Where (token, head) pair i lives: its row in the codes and params arrays, or
@@ -143,30 +151,34 @@ __device__ __forceinline__ int64_t cache_row(const Q4RowsParams &p, uint32_t i, 
 __global__ void __launch_bounds__(kWarps * 32) q4_store_kernel(const Q4RowsParams p) {
   griddep_wait();  // inputs written by the previous kernel are visible from here on
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, l = lane & 15;
-  const bool is_v = lane >= 16;
-  const uint32_t first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kStoreRows;
+  const int lane = threadIdx.x & 31, l = lane & 7;
+  const bool is_v = (lane & 8) != 0;
+  const uint32_t first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kStoreRows + (lane >> 4);
   const uint4 *in = is_v ? p.v : p.k;
-  int64_t row[kStoreRows];
-  uint4 x[kStoreRows];
+  uint32_t x[kStoreRows / 2][8];
+  int64_t row[kStoreRows / 2];
 #pragma unroll
-  for (int u = 0; u < kStoreRows; ++u)
-    if (first + u < p.num_rows) x[u] = ld_stream(in + static_cast<int64_t>(first + u) * 16 + l);
+  for (int u = 0; u < kStoreRows / 2; ++u) {
+    const uint32_t i = first + 2 * u;
 #pragma unroll
-  for (int u = 0; u < kStoreRows; ++u) row[u] = cache_row(p, first + u, lane);
+    for (int j = 0; j < 8; ++j) x[u][j] = 0;
+    if (i < p.num_rows) ld_stream(in + static_cast<int64_t>(i) * 16 + 2 * l, x[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kStoreRows / 2; ++u) row[u] = cache_row(p, first + 2 * u, lane & 15);
   uint32_t *codes = is_v ? p.v_codes : p.k_codes, *params = is_v ? p.v_params : p.k_params;
-  const int lanes_log2 = 4 - p.groups_log2;  // lanes sharing a group
+  const int lanes_log2 = 3 - p.groups_log2;  // lanes sharing a group
 #pragma unroll
-  for (int u = 0; u < kStoreRows; ++u) {
-    if (row[u] < 0) continue;  // uniform over the warp
+  for (int u = 0; u < kStoreRows / 2; ++u) {
+    if (first - (lane >> 4) + 2 * u >= p.num_rows) break;  // uniform over the warp
     uint32_t e = extremes(x[u]);
     e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 1));
-    e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 2));
+    if (lanes_log2 >= 2) e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 2));
     if (lanes_log2 >= 3) e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 4));
-    if (lanes_log2 >= 4) e = min_nan_bf16x2(e, __shfl_xor_sync(0xffffffffu, e, 8));
     const float lo = bf16lo(e), hi = -bf16hi(e);
     const uint32_t pw = group_params(lo, hi);
-    codes[row[u] * 16 + l] = codes_of(x[u], pw, lo, hi);
+    if (row[u] < 0) continue;
+    reinterpret_cast<uint2 *>(codes)[row[u] * 8 + l] = codes_of(x[u], pw, lo, hi);
     if ((l & ((1 << lanes_log2) - 1)) == 0) params[(row[u] << p.groups_log2) + (l >> lanes_log2)] = pw;
   }
 }
