@@ -46,62 +46,38 @@ pkv_status check_attention(const pkv::Q4CacheArgs &c, int32_t num_q_heads, int32
   return PKV_OK;
 }
 
-// The plan of a decode call: warps a CTA (4, 8 or 16) and splits of the keys of
-// each (sequence, KV head) pair, by the least estimated time. With a step of 32
-// keys as the unit, an SM with 4, 8, 12 or 16 resident warps gets through 4.7,
-// 6.4, 7.4 or 8 steps a microsecond (measured with 16 x 8 pairs of 16,384 keys;
-// 16 warps are the most its registers hold); a CTA costs some 2 us to start and
-// finish, which its neighbours on the SM cover in part, and splits cost the 3 us
-// of the merge kernel. Measured against it, in us: 512 pairs of 640 keys 15.9
-// with 4 warps and one split, 18.6 with 8 warps, 20.9 with two splits; 128 pairs
-// of 16,384 keys 108 with 4 warps and one split, 69 with 16 warps, 70 with 4
-// warps and seven splits.
-// No CTA gets more than kWarpKeys keys a warp, so that one long sequence in a
-// batch of short ones is not left to a single CTA.
-constexpr int32_t kStepKeys = 32, kWarpKeys = 1024, kMaxSplits = 64, kCtasPerSm = 16;
+// The plan of a decode call, by the least estimated time. With a step of 32 keys
+// as the unit, an SM with 4, 8, 12 or 16 resident warps gets through 4.7, 6.4, 7.4
+// or 8 steps a microsecond (measured with 16 x 8 pairs of 16,384 keys; 16 warps
+// are the most its registers hold). A CTA for each pair costs some 2 us to start
+// and finish, which its neighbours on the SM cover in part; ranges cost the scan
+// of the lengths and the merge kernel.
+// The estimate takes every sequence at the longest. Where they are not, ranges
+// stay even, and one CTA a pair may be left with most of the work: pairs of more
+// than kWarpKeys keys a warp always go by ranges.
+constexpr int32_t kStepKeys = 32, kWarpKeys = 1024;
 
-pkv::Q4DecodePlan search_plan(int64_t pairs, int64_t keys, int sms) {
-  const int64_t steps = (keys + kStepKeys - 1) / kStepKeys;
-  pkv::Q4DecodePlan best = {};
+pkv::Q4DecodePlan decode_plan(int64_t num_seqs, int64_t heads, int64_t keys, int sms) {
+  const int64_t steps = (keys + kStepKeys - 1) / kStepKeys, pairs = num_seqs * heads;
+  pkv::Q4DecodePlan best = {16, 0};
   double best_us = 0;
   for (int warps = 4; warps <= 16; warps *= 2) {
-    const int64_t least = (keys + kWarpKeys * warps - 1) / (kWarpKeys * warps);
-    const int64_t most = std::max(least, std::min<int64_t>(kMaxSplits, sms * kCtasPerSm / pairs));
-    for (int64_t n = least; n <= most; ++n) {
-      const int64_t split = (steps + n - 1) / n;           // steps a CTA
-      const int64_t used = (steps + split - 1) / split;    // splits that get any
-      if (used > least && split < warps) break;            // warps without work
-      const int64_t per_sm = (pairs * used + sms - 1) / sms, per_warp = (split + warps - 1) / warps;
-      const int64_t resident = std::min<int64_t>(16, per_sm * warps);
-      const double rate = resident <= 4 ? 4.7 : resident <= 8 ? 6.4 : resident <= 12 ? 7.4 : 8.0;
-      const double rounds = std::max(1.0, static_cast<double>(per_sm * warps) / 16);
-      const double us = per_sm * per_warp * warps / rate + 2 * rounds + (used > 1 ? 3.0 : 0.0) + (warps == 16 ? 0.8 : 0.0);
-      if (best.warps == 0 || us < best_us) {
-        best = {static_cast<int32_t>(used), static_cast<int32_t>(split * kStepKeys), warps};
-        best_us = us;
-      }
+    const int64_t per_sm = (pairs + sms - 1) / sms, per_warp = (steps + warps - 1) / warps;
+    const int64_t resident = std::min<int64_t>(16, per_sm * warps);
+    const double rate = resident <= 4 ? 4.7 : resident <= 8 ? 6.4 : resident <= 12 ? 7.4 : 8.0;
+    const double rounds = std::max(1.0, static_cast<double>(per_sm * warps) / 16);
+    const double us = per_sm * per_warp * warps / rate + 2 * rounds + (warps == 16 ? 0.8 : 0.0);
+    if (warps == 4 || us < best_us) {
+      best.warps = warps;
+      best_us = us;
     }
   }
-  return best;
-}
-
-// The search takes a few microseconds: this thread's last plan is kept.
-pkv::Q4DecodePlan decode_plan(int64_t pairs, int64_t keys, int sms) {
-  thread_local int64_t of[3] = {0, 0, 0};
-  thread_local pkv::Q4DecodePlan plan = {};
-  if (of[0] != pairs || of[1] != keys || of[2] != sms) {
-    plan = search_plan(pairs, keys, sms);
-    of[0] = pairs;
-    of[1] = keys;
-    of[2] = sms;
+  if (num_seqs <= pkv::kQ4MaxRangeSeqs) {
+    const double per_warp = static_cast<double>(pairs * steps) / (16 * sms);
+    const double us = std::max(1.0, per_warp) * 2.0 + 7;
+    if (us < best_us || keys > kWarpKeys * best.warps) best.range_ctas = sms;
   }
-  return plan;
-}
-
-// No plan for these sizes or smaller ones has more pieces.
-int64_t max_pieces(int64_t pairs, int64_t keys, int sms) {
-  return std::max<int64_t>(pairs, static_cast<int64_t>(sms) * kCtasPerSm) +
-         pairs * ((keys + 4 * kWarpKeys - 1) / (4 * kWarpKeys));
+  return best;
 }
 
 struct DecodeWorkspace {
@@ -112,8 +88,8 @@ struct DecodeWorkspace {
 DecodeWorkspace decode_workspace(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t max_context_len,
                                  bool with_scores, int sms) {
   DecodeWorkspace w;
-  const int64_t pieces = max_pieces(static_cast<int64_t>(num_seqs) * num_kv_heads, max_context_len, sms) *
-                         (num_q_heads / num_kv_heads);
+  // two pieces of a range a warp, 16 warps an SM, whatever the sequences
+  const int64_t pieces = static_cast<int64_t>(sms) * 16 * 2 * (num_q_heads / num_kv_heads);
   const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads;
   w.logits_ld = static_cast<int64_t>(align_up(static_cast<size_t>(max_context_len), 16));
   w.o = 0;
@@ -251,7 +227,7 @@ pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const vo
   a.num_seqs = num_seqs;
   a.num_q_heads = num_q_heads;
   a.window = sliding_window;
-  a.plan = decode_plan(static_cast<int64_t>(num_seqs) * num_kv_heads, keys, sms);
+  a.plan = decode_plan(num_seqs, num_kv_heads, keys, sms);
   a.scale_log2 = scale * pkv::kLog2e;
   cudaError_t e = pkv::launch_q4_decode(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "decode_q4 launch");

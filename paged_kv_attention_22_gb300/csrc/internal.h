@@ -184,11 +184,12 @@ struct Q4GatherArgs {
 cudaError_t launch_q4_gather(const Q4GatherArgs &a, cudaStream_t stream);
 cudaError_t q4_cache_error_word(uint32_t **word);
 
-// How a decode call over the 4-bit cache cuts the keys of each (sequence, KV
-// head): n_splits CTAs of `warps` (4, 8 or 16) warps and split_keys keys (a
-// multiple of 32).
+// How a decode call over the 4-bit cache shares its work out: a CTA of `warps`
+// (4, 8 or 16) warps for each (sequence, KV head), or, with range_ctas > 0, equal
+// ranges for the 16 warps of each of that many CTAs.
+constexpr int kQ4MaxRangeSeqs = 1024;  // sequences whose lengths fit beside the rings
 struct Q4DecodePlan {
-  int32_t n_splits, split_keys, warps;
+  int32_t warps, range_ctas;
 };
 struct Q4DecodeArgs {
   Q4CacheArgs cache;

@@ -1,12 +1,18 @@
 // Paged decode attention over a cache held in 4 bits, one query token per
 // sequence.
 //
-// The keys of a (sequence, KV head) are cut into splits, one CTA each; the
-// CTA's warps take the split's steps of 32 keys (two units of 16) in turn. A
+// The work is (sequence, KV head) pairs of steps of 32 keys (two units of 16). A
 // unit's codes are 1 KiB of K and 1 KiB of V, contiguous in the cache, and its
-// parameters 64 to 256 bytes of each. Every warp streams its steps through a
-// ring of its own with cp.async, so no warp waits for another before the end of
-// the split.
+// parameters 64 to 256 bytes of each. Every warp streams its steps through a ring
+// of its own with cp.async, so no warp waits for another within its work. Two
+// ways of sharing the steps out (decode_plan in api_q4.cu chooses):
+//   pairs    one CTA of 4, 8 or 16 warps a pair, which take its steps in turn
+//            and join through shared memory. One kernel: the way for many pairs.
+//   ranges   16 warps an SM; the steps of all pairs, listed in order, are cut into
+//            equal ranges, one a warp, whatever the lengths. A pair cut between
+//            warps leaves one partial result each in the workspace (a warp's
+//            first piece in slot 2w, its last in slot 2w + 1), joined by a
+//            second kernel: the way for few or unequal pairs.
 //
 // The products run on mma.sync m16n8k16 in bf16 with fp32 accumulators. A bf16
 // of the cache's definition is what the codes are widened to, so the logits
@@ -53,13 +59,13 @@ struct Q4DecodeParams {
   const int32_t *block_tables, *context_lens;
   __nv_bfloat16 *out;
   float *lse;
-  float *ws_o;     // [S, H_kv, n_splits, G, 128] partial outputs
-  float4 *ws_ml;   // [S, H_kv, n_splits, G] (max, sum, sum of the rounded)
+  float *ws_o;     // ranges: [2 warps, G, 128] partial outputs
+  float4 *ws_ml;   // ranges: [2 warps, G] (max, sum, sum of the rounded)
   float *logits;   // [S, H_q, logits_ld] or null
   int64_t logits_ld;
   FastDiv block;
   int32_t max_blocks, max_context_len, num_q_heads, num_kv_heads, num_blocks;
-  int32_t gqa, window, n_splits, split_keys;
+  int32_t num_seqs, gqa, window;
   float scale_log2;  // > 0: the sign of the scale is in q_signs, which flips q's
   uint32_t q_signs;
 };
@@ -108,20 +114,68 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 }
 
 // The keys a sequence attends to: [first, ctx); its units start at the 16-key
-// boundary at or before first. ctx <= 0 marks an invalid length.
+// boundary at or before first. ctx == 0 marks an invalid length.
 struct KeyRange {
   int ctx, first, unit0;
 };
-__device__ __forceinline__ KeyRange key_range(const Q4DecodeParams &p, int s) {
+__device__ __forceinline__ KeyRange key_range(const Q4DecodeParams &p, int ctx) {
   KeyRange r;
-  r.ctx = p.context_lens[s];
-  if (r.ctx > p.max_context_len || r.ctx > static_cast<int64_t>(p.max_blocks) * p.block.d) r.ctx = 0;
+  r.ctx = ctx;
+  if (ctx <= 0 || ctx > p.max_context_len || ctx > static_cast<int64_t>(p.max_blocks) * p.block.d) r.ctx = 0;
   r.first = p.window > 0 && r.ctx > p.window ? r.ctx - p.window : 0;
   r.unit0 = r.first / kUnit * kUnit;
   return r;
 }
+__device__ __forceinline__ int steps_of(const KeyRange &r) { return (r.ctx - r.unit0 + kStep - 1) / kStep; }
 
-template <int NG, int kWarps>
+// ---- ranges: the list of steps, in (sequence, KV head, step) order
+
+// prefix[s] = steps of one head of the sequences before s, for all s <= num_seqs,
+// and the lengths (0: invalid); one warp.
+__device__ __forceinline__ void build_prefix(const Q4DecodeParams &p, int64_t *prefix, int *ctx_of, bool raise,
+                                             int lane) {
+  int64_t carry = 0;
+  for (int base = 0; base < p.num_seqs; base += 32) {
+    const int s = base + lane;
+    int64_t n = 0;
+    if (s < p.num_seqs) {
+      const KeyRange r = key_range(p, p.context_lens[s]);
+      if (r.ctx == 0 && raise) atomicOr(&g_q4_decode_errors, kErrContext);
+      n = r.ctx > 0 ? steps_of(r) : 0;
+      if (ctx_of != nullptr) ctx_of[s] = r.ctx;
+    }
+    int64_t incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (s < p.num_seqs) prefix[s] = carry + incl - n;
+    carry += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) prefix[p.num_seqs] = carry;
+}
+
+struct Step {
+  int s, head, k;
+};
+// Step u of the list (u below its length).
+__device__ __forceinline__ Step locate(const int64_t *prefix, int num_seqs, int heads, int64_t u) {
+  int lo = 0, hi = num_seqs - 1;  // the last s with heads * prefix[s] <= u: it has steps
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (heads * prefix[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  const int64_t n = prefix[lo + 1] - prefix[lo], r = u - heads * prefix[lo];
+  const int head = static_cast<int>(r / n);
+  return {lo, head, static_cast<int>(r - head * n)};
+}
+// First step of warp w's range of U steps among W <= U warps, and the warp whose
+// range holds step u.
+__device__ __forceinline__ int64_t range_start(int64_t w, int64_t W, int64_t U) { return w * U / W; }
+__device__ __forceinline__ int64_t owner_of(int64_t u, int64_t W, int64_t U) { return ((u + 1) * W + U - 1) / U - 1; }
+
+template <int NG, int kWarps, bool kRanges>
 __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(const Q4DecodeParams p) {
   using L = Q4DecodeSmem<NG, kWarps>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -129,26 +183,40 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, head = blockIdx.y, s = blockIdx.z;
   const int G = p.gqa;
-  const KeyRange range = key_range(p, s);
-  if (range.ctx <= 0) {
-    if (split == 0 && head == 0 && threadIdx.x == 0) atomicOr(&g_q4_decode_errors, kErrContext);
-    return;
+  // ranges: the list of steps, behind the rings
+  [[maybe_unused]] int64_t *prefix = reinterpret_cast<int64_t *>(smem + L::kTotal);
+  [[maybe_unused]] int *ctx_of = reinterpret_cast<int *>(prefix + p.num_seqs + 1);
+  [[maybe_unused]] int64_t first_step = 0;  // this warp's range starts there
+  Step cur = {static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x), 0};
+  KeyRange range;
+  int n_mine;  // this warp's steps
+  if constexpr (kRanges) {
+    if (warp == 0) build_prefix(p, prefix, ctx_of, blockIdx.x == 0, lane);
+    __syncthreads();
+    const int64_t U = p.num_kv_heads * prefix[p.num_seqs];
+    const int64_t W = min(static_cast<int64_t>(gridDim.x) * kWarps, U);
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    if (w >= W) return;
+    first_step = range_start(w, W, U);
+    n_mine = static_cast<int>(range_start(w + 1, W, U) - first_step);
+    cur = locate(prefix, p.num_seqs, p.num_kv_heads, first_step);
+    range = key_range(p, ctx_of[cur.s]);
+  } else {
+    range = key_range(p, p.context_lens[cur.s]);
+    if (range.ctx == 0) {
+      if (cur.head == 0 && threadIdx.x == 0) atomicOr(&g_q4_decode_errors, kErrContext);
+      return;
+    }
+    const int n_steps = steps_of(range);
+    n_mine = n_steps > warp ? (n_steps - warp + kWarps - 1) / kWarps : 0;
   }
-  const int64_t key_begin64 = range.unit0 + static_cast<int64_t>(split) * p.split_keys;
-  if (key_begin64 >= range.ctx) return;  // a split past this sequence's end
-  const int key_begin = static_cast<int>(key_begin64);
-  const int key_end = min(range.ctx - key_begin, p.split_keys) + key_begin;
-  const int n_units = (key_end - key_begin + kUnit - 1) / kUnit;
-  const int n_steps = (n_units + 1) / 2;
-  const int n_mine = n_steps > warp ? (n_steps - warp + kWarps - 1) / kWarps : 0;
 
-  // the query heads as B fragments: k-step 2w (2w + 1) pairs dims i and i + 4,
-  // i = 0, 1 (2, 3), of the lane's w-th code word
+  // the pair's query heads as B fragments: k-step 2w (2w + 1) pairs dims i and
+  // i + 4, i = 0, 1 (2, 3), of the lane's w-th code word
   uint32_t qb[8][2];
-  {
-    const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + head * G + g;
+  auto load_q = [&]() {
+    const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + cur.head * G + g;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * kD + 32 * t);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -162,19 +230,30 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
       qb[2 * w + 1][0] = q4_low_halves(x.y, x.w);
       qb[2 * w + 1][1] = q4_high_halves(x.y, x.w);
     }
-  }
+  };
+  load_q();
 
   // rows / 16 of this warp's unit i (two units a step) in the codes array, or
-  // kNoUnit past the split's end and for an invalid table entry; a lane holds one
+  // kNoUnit past the last key and for an invalid table entry; a lane holds one
   // unit of a batch of 32
   constexpr uint32_t kNoUnit = 0xffffffffu;
-  const int32_t *table = p.block_tables + static_cast<int64_t>(s) * p.max_blocks;
   auto unit_row = [&](int i) -> uint32_t {
-    const int u = (warp + kWarps * (i >> 1)) * 2 + (i & 1);  // the split's unit
-    if (u >= n_units) return kNoUnit;
-    const int key = key_begin + u * kUnit;
+    int s, head, key, ctx;
+    if constexpr (kRanges) {
+      if ((i >> 1) >= n_mine) return kNoUnit;
+      const Step at = locate(prefix, p.num_seqs, p.num_kv_heads, first_step + (i >> 1));
+      const KeyRange r = key_range(p, ctx_of[at.s]);
+      s = at.s, head = at.head, ctx = r.ctx;
+      key = r.unit0 + at.k * kStep + (i & 1) * kUnit;
+    } else {
+      const int64_t k = range.unit0 + static_cast<int64_t>(warp + kWarps * (i >> 1)) * kStep + (i & 1) * kUnit;
+      if (k >= range.ctx) return kNoUnit;
+      s = cur.s, head = cur.head, ctx = range.ctx;
+      key = static_cast<int>(k);
+    }
+    if (key >= ctx) return kNoUnit;
     const uint32_t j = fast_quotient(key, p.block);
-    const int blk = table[j];
+    const int blk = p.block_tables[static_cast<int64_t>(s) * p.max_blocks + j];
     if (blk < 0 || blk >= p.num_blocks) {
       atomicOr(&g_q4_decode_errors, kErrBlock);
       return kNoUnit;
@@ -222,15 +301,32 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   };
 
   float acc[8][4];  // O^T: dims 16 g + 2 m (and + 1), heads 2 t and 2 t + 1
-#pragma unroll
-  for (int m = 0; m < 8; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
   // of heads 2 t and 2 t + 1; lsum is over this lane's keys, rsum (a product's
   // fragment, its rows all alike) over the warp's. The maximum starts at a finite
   // floor, so that masked logits (-inf) have probability 0 even before the first
   // real one.
-  float mx[2] = {kFloor, kFloor}, lsum[2] = {0.f, 0.f}, rsum[4] = {0.f, 0.f, 0.f, 0.f};
+  float mx[2], lsum[2], rsum[4];
+  auto reset = [&]() {
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+    mx[0] = mx[1] = kFloor;
+    lsum[0] = lsum[1] = 0.f;
+    rsum[0] = rsum[1] = rsum[2] = rsum[3] = 0.f;
+  };
+  reset();
+  // lsum over the warp's keys
+  auto join_lanes = [&]() {
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) lsum[c] += __shfl_xor_sync(0xffffffffu, lsum[c], off);
+  };
+  int key0 = range.unit0 + (kRanges ? cur.k : warp) * kStep;  // first key of the step
+  // ranges: whether the pair's first step is this warp's, and its slot
+  [[maybe_unused]] bool opened = cur.k == 0;
+  [[maybe_unused]] int64_t slot = 2 * (static_cast<int64_t>(blockIdx.x) * kWarps + warp);
 
 #pragma unroll
   for (int i = 0; i < kStages; ++i) issue(i);
@@ -244,8 +340,6 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
       there_next = __ballot_sync(0xffffffffu, next_batch != kNoUnit);
     }
     const uint8_t *st = ring_ptr + (it % kStages) * L::kStageBytes;
-    const int key0 = key_begin + (warp + kWarps * it) * kStep;
-
     // ---- S^T = K Q^T
     float z[2][4];  // unscaled; keys kperm, 8 + kperm of each unit, heads 2 t, 2 t + 1: [u][2 * key + head]
 #pragma unroll
@@ -291,7 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
                                                       L::kParamBytes)[(4 * i + t) * NG + g * NG / 8];
     const uint32_t units = (there >> (2 * it & 31)) & 3u;
     if (p.logits != nullptr && 2 * t < G) {  // rows hold whole units: masked keys are written too
-      float *dst = p.logits + (static_cast<int64_t>(s) * p.num_q_heads + head * G + 2 * t) * p.logits_ld + key0 + kperm;
+      float *dst = p.logits + (static_cast<int64_t>(cur.s) * p.num_q_heads + cur.head * G + 2 * t) * p.logits_ld + key0 + kperm;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (!((units >> u) & 1u)) continue;
@@ -303,11 +397,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
         }
       }
     }
-    if (key0 < range.first || key0 + kStep > key_end || units != 3u) {
+    if (key0 < range.first || key0 + kStep > range.ctx || units != 3u) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int lo = range.first - (key0 + u * kUnit);
-        const int hi = ((units >> u) & 1u) ? key_end - (key0 + u * kUnit) : 0;
+        const int hi = ((units >> u) & 1u) ? range.ctx - (key0 + u * kUnit) : 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
           if (8 * j + kperm < lo || 8 * j + kperm >= hi) z[u][2 * j] = z[u][2 * j + 1] = -INFINITY;
@@ -381,13 +475,58 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
     }
     __syncwarp();  // every lane has read the stage: it may be filled again
     issue(it + kStages);
+    if constexpr (!kRanges) {
+      key0 += kWarps * kStep;
+    } else {
+      key0 += kStep;
+      const bool closes = key0 >= range.ctx;
+      if (closes || it == n_mine - 1) {
+        join_lanes();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (2 * t + c >= G) continue;
+          if (opened && closes) {  // the whole pair
+            const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + cur.head * G + 2 * t + c;
+            const float inv = 1.f / rsum[c];
+            uint32_t o[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) o[m] = pack_bf16x2(acc[m][c] * inv, acc[m][2 + c] * inv);
+            uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD + 16 * g);
+            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            if (g == 0 && p.lse != nullptr) p.lse[row] = (mx[c] + log2f(lsum[c])) * kLn2;
+          } else {
+            const int64_t at = slot * G + 2 * t + c;
+            float4 *dst = reinterpret_cast<float4 *>(p.ws_o + at * kD + 16 * g);
+#pragma unroll
+            for (int m = 0; m < 8; m += 2)
+              __stcg(dst + m / 2, make_float4(acc[m][c], acc[m][2 + c], acc[m + 1][c], acc[m + 1][2 + c]));
+            if (g == 0) __stcg(p.ws_ml + at, make_float4(mx[c], lsum[c], rsum[c], 0.f));
+          }
+        }
+        if (it + 1 < n_mine) {  // the next pair, past sequences without steps
+          if (++cur.head == p.num_kv_heads) {
+            cur.head = 0;
+            do ++cur.s;
+            while (prefix[cur.s + 1] == prefix[cur.s]);
+            range = key_range(p, ctx_of[cur.s]);
+          }
+          key0 = range.unit0;
+          opened = true;
+          slot |= 1;
+          load_q();
+          reset();
+        }
+      }
+    }
+  }
+  if constexpr (kRanges) {
+    cp_async_wait<0>();
+    return;
   }
 
-  // ---- join the warps
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) lsum[c] += __shfl_xor_sync(0xffffffffu, lsum[c], off);
+  // ---- pairs: join the warps
+  join_lanes();
   cp_async_wait<0>();
   __syncthreads();  // no warp still reads or fills its ring
   float *so = reinterpret_cast<float *>(smem);                       // [warp][G][128]
@@ -403,7 +542,6 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   for (int c = 0; c < 2; ++c)
     if (g == 0 && 2 * t + c < G) sml[warp * kMaxG + 2 * t + c] = make_float4(mx[c], lsum[c], rsum[c], 0.f);
   __syncthreads();
-  const bool whole = range.unit0 + static_cast<int64_t>(p.split_keys) >= range.ctx;
   const int d = threadIdx.x % kD;
   for (int h = threadIdx.x / kD; h < G; h += kWarps * 32 / kD) {
     float M = -INFINITY;
@@ -418,54 +556,69 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
       l = fmaf(ml.y, f, l);
       r = fmaf(ml.z, f, r);
     }
-    const int64_t row = static_cast<int64_t>(s) * p.num_q_heads + head * G + h;
-    if (whole) {
-      p.out[row * kD + d] = __float2bfloat16_rn(o / r);
-      if (d == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kLn2;
-    } else {
-      const int64_t at = ((static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits + split) * G + h;
-      __stcg(p.ws_o + at * kD + d, o);
-      if (d == 0) __stcg(p.ws_ml + at, make_float4(M, l, r, 0.f));
-    }
+    const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + cur.head * G + h;
+    p.out[row * kD + d] = __float2bfloat16_rn(o / r);
+    if (d == 0 && p.lse != nullptr) p.lse[row] = (M + log2f(l)) * kLn2;
   }
 }
 
-// Join the splits of the (sequence, query head)s that have more than one: a
-// warp each, four dims a lane.
-constexpr int kMergeWarps = 4;
-constexpr int kMergeBatch = 8;  // splits whose loads are in flight
+// Ranges: join the pieces of the (sequence, query head)s whose pairs were cut,
+// kPerRow warps each (8 for pairs cut into many pieces), four dims a lane.
+constexpr int kMergeWarps = 8;
+constexpr int kMergeBatch = 8;  // pieces whose loads a warp has in flight
 
-__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4DecodeParams p, int32_t num_seqs) {
+template <int kPerRow>
+__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4DecodeParams p, int32_t decode_warps) {
+  extern __shared__ int64_t merge_prefix[];
+  __shared__ float4 s_o[kMergeWarps][32];
+  __shared__ float s_ml[kMergeWarps][3];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(num_seqs) * p.num_q_heads) return;
-  const int s = static_cast<int>(row / p.num_q_heads), hq = static_cast<int>(row - static_cast<int64_t>(s) * p.num_q_heads);
-  const KeyRange range = key_range(p, s);
-  if (range.ctx <= 0) return;
-  const int n = (range.ctx - range.unit0 + p.split_keys - 1) / p.split_keys;
-  if (n <= 1) return;  // written whole
-  const int G = p.gqa, head = hq / G, h = hq % G;
-  const int64_t split0 = (static_cast<int64_t>(s) * p.num_kv_heads + head) * p.n_splits * G + h;
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ws_ml[split0 + static_cast<int64_t>(i) * G].x);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, r = 0.f;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kPerRow;
+  if (warp == 0) build_prefix(p, merge_prefix, nullptr, false, lane);
+  __syncthreads();
+  const int64_t U = p.num_kv_heads * merge_prefix[p.num_seqs];
+  const int64_t W = min(static_cast<int64_t>(decode_warps), U);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeWarps / kPerRow) + warp / kPerRow;
+  int64_t wa = 0, n = 0, slot_a = 0;  // first warp, pieces, the first one's slot
+  int h = 0;
+  if (row < static_cast<int64_t>(p.num_seqs) * p.num_q_heads) {
+    const int s = static_cast<int>(row / p.num_q_heads), hq = static_cast<int>(row % p.num_q_heads);
+    const int head = hq / p.gqa;
+    h = hq - head * p.gqa;
+    const int64_t steps = merge_prefix[s + 1] - merge_prefix[s];
+    const int64_t P0 = p.num_kv_heads * merge_prefix[s] + head * steps;
+    if (steps > 0) {
+      wa = owner_of(P0, W, U);
+      n = owner_of(P0 + steps - 1, W, U) - wa + 1;
+      slot_a = 2 * wa + (range_start(wa, W, U) < P0 ? 1 : 0);
+    }
+  }
+  if (n == 1) n = 0;  // written whole
+  float M = kFloor, o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, r = 0.f;
 #pragma unroll 1
-  for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
+  for (int64_t i0 = sub; i0 < n; i0 += kMergeBatch * kPerRow) {
     float4 ml[kMergeBatch], ov[kMergeBatch];
+    float m_new = M;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
-      ml[u] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      const int64_t i = i0 + u * kPerRow;
+      ml[u] = make_float4(kFloor, 0.f, 0.f, 0.f);
       ov[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i0 + u < n) {
-        const int64_t at = split0 + static_cast<int64_t>(i0 + u) * G;
+      if (i < n) {
+        const int64_t at = (i == 0 ? slot_a : 2 * (wa + i)) * p.gqa + h;
         ml[u] = p.ws_ml[at];
         ov[u] = reinterpret_cast<const float4 *>(p.ws_o + at * kD)[lane];
       }
     }
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) m_new = fmaxf(m_new, ml[u].x);
+    const float alpha = fast_exp2(M - m_new);
+    M = m_new;
+    l *= alpha;
+    r *= alpha;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] *= alpha;
 #pragma unroll
     for (int u = 0; u < kMergeBatch; ++u) {
       const float f = fast_exp2(ml[u].x - M);
@@ -477,6 +630,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4Deco
       r = fmaf(ml[u].z, f, r);
     }
   }
+  if constexpr (kPerRow > 1) {
+    s_o[warp][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    if (lane == 0) s_ml[warp][0] = M, s_ml[warp][1] = l, s_ml[warp][2] = r;
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int w = 1; w < kPerRow; ++w) M = fmaxf(M, s_ml[warp + w][0]);
+    o[0] = o[1] = o[2] = o[3] = l = r = 0.f;
+#pragma unroll
+    for (int w = 0; w < kPerRow; ++w) {
+      const float f = fast_exp2(s_ml[warp + w][0] - M);
+      const float4 v = s_o[warp + w][lane];
+      o[0] = fmaf(v.x, f, o[0]);
+      o[1] = fmaf(v.y, f, o[1]);
+      o[2] = fmaf(v.z, f, o[2]);
+      o[3] = fmaf(v.w, f, o[3]);
+      l = fmaf(s_ml[warp + w][1], f, l);
+      r = fmaf(s_ml[warp + w][2], f, r);
+    }
+  }
+  if (n == 0) return;
   uint2 v;
   v.x = pack_bf16x2(o[0] / r, o[1] / r);
   v.y = pack_bf16x2(o[2] / r, o[3] / r);
@@ -490,24 +664,38 @@ __global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScore
   key_scores_body(p);
 }
 
-template <int NG, int kWarps>
-cudaError_t launch_splits(const Q4DecodeParams &p, int32_t num_seqs, cudaStream_t stream) {
-  constexpr int kSmem = Q4DecodeSmem<NG, kWarps>::kTotal;
-  if (kSmem > 48 * 1024) {
-    cudaError_t e =
-        cudaFuncSetAttribute(q4_decode_kernel<NG, kWarps>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <int NG, int kWarps, bool kRanges>
+cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream) {
+  auto kernel = q4_decode_kernel<NG, kWarps, kRanges>;
+  int smem = Q4DecodeSmem<NG, kWarps>::kTotal;
+  if (kRanges) smem += static_cast<int>(sizeof(int64_t)) * (p.num_seqs + 1) + static_cast<int>(sizeof(int)) * p.num_seqs;
+  if (smem > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(q4_decode_kernel<NG, kWarps>, dim3(p.n_splits, p.num_kv_heads, num_seqs), dim3(kWarps * 32),
-                    kSmem, stream, p);
+  return launch_pdl(kernel, grid, dim3(kWarps * 32), smem, stream, p);
 }
 
 template <int NG>
-cudaError_t launch_warps(const Q4DecodeParams &p, int32_t warps, int32_t num_seqs, cudaStream_t stream) {
-  switch (warps) {
-    case 4: return launch_splits<NG, 4>(p, num_seqs, stream);
-    case 8: return launch_splits<NG, 8>(p, num_seqs, stream);
-    case 16: return launch_splits<NG, 16>(p, num_seqs, stream);
+cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, cudaStream_t stream) {
+  static_assert(Q4DecodeSmem<NG, 16>::kTotal + 12 * kQ4MaxRangeSeqs + 8 <= 227 * 1024, "shared memory of the ranges");
+  const dim3 pairs(p.num_kv_heads, p.num_seqs);
+  if (plan.range_ctas > 0) {
+    cudaError_t e = launch_shape<NG, 16, true>(p, dim3(plan.range_ctas), stream);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
+    const int warps = plan.range_ctas * 16;
+    const size_t smem = sizeof(int64_t) * (p.num_seqs + 1);
+    // many pieces a pair: as many warps a row as a CTA has
+    const bool many = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * 16 < warps;
+    const int64_t ctas = many ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
+    return launch_pdl(many ? q4_merge_kernel<kMergeWarps> : q4_merge_kernel<1>, dim3(static_cast<unsigned>(ctas)),
+                      dim3(kMergeWarps * 32), smem, stream, p, warps);
+  }
+  switch (plan.warps) {
+    case 4: return launch_shape<NG, 4, false>(p, pairs, stream);
+    case 8: return launch_shape<NG, 8, false>(p, pairs, stream);
+    case 16: return launch_shape<NG, 16, false>(p, pairs, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -537,26 +725,19 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
   p.num_blocks = static_cast<int32_t>(a.cache.num_blocks);
   p.gqa = a.num_q_heads / a.cache.num_kv_heads;
   p.window = a.window;
-  p.n_splits = a.plan.n_splits;
-  p.split_keys = a.plan.split_keys;
+  p.num_seqs = a.num_seqs;
   // a scale of 0 becomes the smallest positive one: its logits stay below 2^-100
   // unless a product passes 2^26, and masked logits stay -inf
   p.scale_log2 = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
   p.q_signs = a.scale_log2 < 0.f ? 0x80008000u : 0u;
   cudaError_t e;
   switch (a.cache.group_size) {
-    case 32: e = launch_warps<4>(p, a.plan.warps, a.num_seqs, stream); break;
-    case 64: e = launch_warps<2>(p, a.plan.warps, a.num_seqs, stream); break;
-    case 128: e = launch_warps<1>(p, a.plan.warps, a.num_seqs, stream); break;
+    case 32: e = launch_plan<4>(p, a.plan, stream); break;
+    case 64: e = launch_plan<2>(p, a.plan, stream); break;
+    case 128: e = launch_plan<1>(p, a.plan, stream); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  if (p.n_splits > 1) {
-    const int64_t rows = static_cast<int64_t>(a.num_seqs) * p.num_q_heads;
-    e = launch_pdl(q4_merge_kernel, dim3(static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps)),
-                   dim3(kMergeWarps * 32), 0, stream, p, a.num_seqs);
-    if (e != cudaSuccess) return e;
-  }
   if (a.key_scores == nullptr) return cudaSuccess;
   KeyScoresParams k;
   k.logits = a.logits;

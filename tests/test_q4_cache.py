@@ -306,6 +306,78 @@ def test_decode(L, lens, heads, gqa, block, group, window, scored):
 
 
 @gpu
+def test_decode_long_and_short_sequences_of_many_pairs(L):
+    """Many (sequence, KV head) pairs: one CTA each, the long one's warps with more
+    than one batch of table entries."""
+    lens = [4000] + [30] * 94
+    c = Q.Cache(21, lens, 8, 256, 32)
+    q = torch.randn(95, 16, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    out, lse, tol_o, tol_l, _, _ = _decode_plain(c, q, 2, 0)
+    kc, vc, bt = c.cuda()
+    o, l = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt, torch.tensor(lens, dtype=torch.int32, device="cuda"), 4000, SCALE)
+    assert pkv.check_device_errors() == 0
+    assert bool(((o.cpu().double() - out).abs() <= tol_o).all()) and bool(((l.cpu().double() - lse).abs() <= tol_l).all())
+
+
+def _random_cache(seqs, blocks_per_seq, heads, block, group):
+    """A large random cache made on the GPU, tables of seqs sequences in shuffled blocks."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = seqs * blocks_per_seq
+    caches = []
+    for _ in range(2):
+        codes = torch.randint(0, 256, (n, heads, block, 64), generator=g, device="cuda", dtype=torch.uint8)
+        params = torch.rand(n, heads, block, 128 // group, 2, generator=g, device="cuda") * 0.2 + 0.1
+        params[..., 1] = -23.5 * params[..., 0]
+        caches.append((codes, params.to(torch.bfloat16)))
+    return caches[0], caches[1], torch.randperm(n, generator=g, device="cuda").to(torch.int32).view(seqs, blocks_per_seq)
+
+
+@gpu
+@pytest.mark.parametrize("window", [0, 20000])
+def test_decode_long_ranges(L, window):
+    """Enough keys that every warp's range takes several batches of table entries;
+    unequal lengths, one of them invalid; a few pairs compared."""
+    seqs, heads, block = 12, 8, 256
+    kc, vc, bt = _random_cache(seqs, 160, heads, block, 32)
+    lens = [40960, 40959, 33000, 40960, 17, 0, 40960, 40000, 40960, 1, 40960, 40960]
+    q = torch.randn(seqs, 16, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    o = torch.full_like(q, 9.0)
+    o, l = pkv.paged_decode_attn_q4(q, kc, vc, bt, torch.tensor(lens, dtype=torch.int32, device="cuda"), 40960, SCALE, out=o,
+                                    sliding_window=window)
+    assert pkv.check_device_errors() == pkv.DEVERR_CONTEXT
+    assert bool((o[5] == 9.0).all())
+    for s, h in ((0, 0), (1, 3), (2, 7), (4, 5), (6, 2), (7, 7), (9, 0), (11, 7)):
+        n = lens[s]
+        first = max(0, n - window) if window else 0
+        p = torch.arange(n, device="cuda")
+        rows = (bt[s].long()[p // block], h, p % block)
+        k, v = (Q.values(*(x[rows].cpu() for x in c)) for c in (kc, vc))
+        want, lse, _, wv, qk = Q.attend(q[s, 2 * h:2 * h + 2].cpu().double(), k, v, SCALE, [first] * 2, [n - 1] * 2)
+        err, tol = (o[s, 2 * h:2 * h + 2].cpu().double() - want).abs(), Q.out_tolerance(want, wv)
+        assert bool((err <= tol).all()), (s, h, float((err / tol).max()))
+        err, tol = (l[s, 2 * h:2 * h + 2].cpu().double() - lse).abs(), Q.lse_tolerance(lse, qk, n / 4)
+        assert bool((err <= tol).all()), (s, h, float((err / tol).max()))
+
+
+@gpu
+def test_decode_scale_of_any_sign(L):
+    lens = [100, 7]
+    c = Q.Cache(31, lens, 2, 16, 32)
+    q = torch.randn(2, 4, 128, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    kc, vc, bt = c.cuda()
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for scale in (-0.3, 0.0, 2.5):
+        for s, n in enumerate(lens):
+            o, l = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt, cl, 100, scale)
+            for h in range(4):
+                k, v = c.logical(c.k, s, n, h // 2), c.logical(c.v, s, n, h // 2)
+                want, lse, _, wv, qk = Q.attend(q[s, h:h + 1].double(), k, v, scale, [0], [n - 1])
+                assert bool(((o[s, h].cpu().double() - want[0]).abs() <= Q.out_tolerance(want[0], wv[0])).all())
+                assert abs(float(l[s, h]) - float(lse)) <= float(Q.lse_tolerance(lse, qk, n / 4))
+    assert pkv.check_device_errors() == 0
+
+
+@gpu
 def test_decode_skips_invalid_rows_and_reports_them(L):
     lens = [40, 40, 40, 40]
     c = Q.Cache(5, lens, 2, 16, 32)
