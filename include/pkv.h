@@ -364,7 +364,8 @@ size_t pkv_decode_q4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32
 /*
  * pkv_paged_decode_attn over a 4-bit cache. Arguments, result, sliding window
  * and device errors are that call's, except:
- *   - H_q / H_kv may be 1, 2, 4 or 8, and num_seqs at most 65535;
+ *   - H_q / H_kv may be 1, 2, 4 or 8, num_seqs is at most 65535 and
+ *     max_context_len at most 2^30 (PKV_ERR_UNSUPPORTED);
  *   - an invalid table entry raises PKV_DEVERR_BLOCK and its keys are left out;
  *   - no wait inside the kernels can run out, so the call takes no notice of
  *     PKV_DEVERR_TIMEOUT (like pkv_kv_store);
@@ -436,7 +437,7 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
  * The heads are summed in order: the same inputs give the same bits.
  *   key_scores   device float32 [num_seqs, score_stride], not NULL; the caller
  *                sets a sequence's row to zero when it admits the sequence
- *   score_stride >= max_context_len
+ *   score_stride >= max_context_len, which is at most 2^30 (PKV_ERR_UNSUPPORTED)
  *   workspace    device, >= pkv_decode_scores_workspace_size(...) bytes: the
  *                decode workspace and the call's logits (4 bytes per key and
  *                query head). Conditions as for the decode workspace, but its
@@ -462,7 +463,7 @@ pkv_status pkv_paged_decode_attn_scores(const void *q, const void *k_cache, cons
  * lower than any number).
  *   key_scores   device float32 [num_seqs, score_stride], score_stride >= max_context_len
  *   context_lens device int32 [num_seqs], each in [0, max_context_len]
- *   budget       >= 1;  recent in [0, budget]
+ *   budget       in [1, 2^29] here and below;  recent in [0, budget]
  *   keep         device int32 [num_seqs, budget]: the kept positions in
  *                ascending order, then -1
  *   new_lens     device int32 [num_seqs]: min(ctx, budget)

@@ -460,7 +460,9 @@ size_t pkv_decode_scores_workspace_size(int32_t num_seqs, int32_t num_q_heads, i
                                         int32_t head_dim, int32_t max_context_len) {
   const size_t decode =
       pkv_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);
-  if (decode == 0 || max_context_len <= 0) return 0;
+  if (decode == 0 || max_context_len <= 0 || max_context_len > pkv::kMaxContext ||
+      !pkv::logits_fit(num_seqs, num_q_heads, max_context_len))
+    return 0;
   return decode_scores_layout(num_seqs, num_q_heads, max_context_len, decode).total;
 }
 
@@ -473,6 +475,10 @@ pkv_status pkv_paged_decode_attn_scores(const void *q, const void *k_cache, cons
                                         float *key_scores, int64_t score_stride, void *workspace,
                                         size_t workspace_bytes, void *stream) {
   if (key_scores == nullptr || score_stride < max_context_len) return PKV_ERR_INVALID_ARG;
+  if (num_seqs > 0 && num_q_heads > 0 && max_context_len > 0 &&
+      (max_context_len > pkv::kMaxContext ||
+       !pkv::logits_fit(num_seqs, num_q_heads, max_context_len)))
+    return PKV_ERR_UNSUPPORTED;
   return decode_common(nullptr, nullptr, nullptr, q, k_cache, v_cache, block_tables,
                        max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads,
                        num_kv_heads, head_dim, block_size, num_blocks, scale, sliding_window,

@@ -9,6 +9,8 @@ using pkv::aligned16;
 using pkv::cuda_fail;
 using pkv::current_sm_count;
 
+constexpr int32_t kMaxBudget = 1 << 29;  // the kernels count kept positions, four arrays of them, in 32 bits
+
 // Checks shared by the two compactions; the arrays are already in `a`.
 pkv_status compact(pkv::EvictCompactArgs &a, const int32_t *src_tables, int32_t src_max_blocks,
                    const int32_t *dst_tables, int32_t dst_max_blocks, const int32_t *keep, int32_t budget,
@@ -27,7 +29,7 @@ pkv_status compact(pkv::EvictCompactArgs &a, const int32_t *src_tables, int32_t 
   // one score array under two row strides would be overwritten while it is read
   if (key_scores != nullptr && key_scores == dst_key_scores && score_stride != dst_score_stride)
     return PKV_ERR_INVALID_ARG;
-  if (num_seqs > 65535 || budget > (1 << 29)) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || budget > kMaxBudget) return PKV_ERR_UNSUPPORTED;
   if (num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   int sms = 0;
@@ -65,6 +67,7 @@ pkv_status pkv_evict_select(const float *key_scores, int64_t score_stride, const
     return PKV_ERR_INVALID_ARG;
   if (key_scores == nullptr || context_lens == nullptr || keep == nullptr || new_lens == nullptr)
     return PKV_ERR_INVALID_ARG;
+  if (max_context_len > pkv::kMaxContext || budget > kMaxBudget) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   int sms = 0;
   pkv_status st = current_sm_count(&sms);

@@ -173,7 +173,8 @@ pkv_status pkv_kv_load_q4(const void *k_codes, const void *k_params, const void 
 size_t pkv_decode_q4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                     int32_t max_context_len, int32_t with_scores) {
   if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim != kD || max_context_len <= 0 ||
-      num_q_heads % num_kv_heads != 0)
+      num_q_heads % num_kv_heads != 0 || max_context_len > pkv::kMaxContext ||
+      (with_scores != 0 && !pkv::logits_fit(num_seqs, num_q_heads, max_context_len)))
     return 0;
   int sms = 0;
   if (current_sm_count(&sms) != PKV_OK) return 0;
@@ -197,7 +198,8 @@ pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const vo
   pkv_status st = check_cache(a.cache, head_dim);
   if (st != PKV_OK) return st;
   if ((st = check_attention(a.cache, num_q_heads, max_blocks_per_seq, 8)) != PKV_OK) return st;
-  if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || max_context_len > pkv::kMaxContext) return PKV_ERR_UNSUPPORTED;
+  if (key_scores != nullptr && !pkv::logits_fit(num_seqs, num_q_heads, max_context_len)) return PKV_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
   if (workspace == nullptr) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;

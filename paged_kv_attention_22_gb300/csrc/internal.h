@@ -242,5 +242,13 @@ cudaError_t evict_error_word(uint32_t **word);
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 constexpr float kLog2e = 1.4426950408889634f;
+// Longest context of the calls on 4-bit caches and of eviction: their kernels
+// step through positions in 32 bits.
+constexpr int32_t kMaxContext = 1 << 30;
+// Whether the logits of a call with accumulated weights have a size that a
+// workspace can have at all (2^40 values), before sizes are multiplied out.
+inline bool logits_fit(int64_t num_seqs, int64_t num_q_heads, int64_t max_context_len) {
+  return num_seqs * num_q_heads <= (int64_t{1} << 40) / (max_context_len + 15);
+}
 
 }  // namespace pkv

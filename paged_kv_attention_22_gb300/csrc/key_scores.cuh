@@ -29,7 +29,7 @@ __device__ __forceinline__ void key_scores_body(const KeyScoresParams &p) {
   const int ctx = p.context_lens[s];
   if (ctx <= 0 || ctx > p.max_context_len || ctx > p.ctx_cap) return;
   const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
-  for (int pos = blockIdx.x * kScoreThreads + threadIdx.x; pos < ctx; pos += gridDim.x * kScoreThreads) {
+  for (int64_t pos = blockIdx.x * kScoreThreads + threadIdx.x; pos < ctx; pos += gridDim.x * kScoreThreads) {
     if (pos < first) continue;
     const float *z = p.logits + static_cast<int64_t>(s) * p.num_q_heads * p.logits_ld + pos;
     const float *lse = p.lse + static_cast<int64_t>(s) * p.num_q_heads;

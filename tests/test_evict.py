@@ -43,6 +43,8 @@ def test_select_refuses(L):
         assert call(**{null: None}) == pkv.PKV_ERR_INVALID_ARG
     for bad in (dict(S=-1), dict(B=0), dict(R=-1), dict(R=17), dict(mcl=0), dict(ld=63)):
         assert call(**bad) == pkv.PKV_ERR_INVALID_ARG
+    assert call(B=(1 << 29) + 1) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(mcl=(1 << 30) + 1, ld=1 << 31) == pkv.PKV_ERR_UNSUPPORTED
     assert call(S=0) == pkv.PKV_OK
 
 
@@ -58,6 +60,7 @@ def test_compact_refuses(L):
         assert call(**bad) == pkv.PKV_ERR_INVALID_ARG
     assert call(D=64) == pkv.PKV_ERR_UNSUPPORTED
     assert call(S=65536) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(B=(1 << 29) + 1) == pkv.PKV_ERR_UNSUPPORTED
     assert call(NB=1 << 40) == pkv.PKV_ERR_UNSUPPORTED
     assert call(S=0) == pkv.PKV_OK
 
@@ -82,6 +85,7 @@ def test_scored_decode_refuses(L):
     assert call(ws=None) == pkv.PKV_ERR_WORKSPACE_TOO_SMALL
     assert L.pkv_decode_scores_workspace_size(0, 16, 8, 128, 64) == 0
     assert L.pkv_decode_scores_workspace_size(2, 16, 8, 128, 0) == 0
+    assert L.pkv_decode_scores_workspace_size(1 << 30, 1 << 14, 1, 128, 1 << 30) == 0
 
 
 def test_manager_eviction_keeps_private_blocks_and_replaces_shared_ones(L):
@@ -152,7 +156,7 @@ def _scores(kind, S, width, seed):
 @pytest.mark.parametrize("kind", ["plain", "ties", "equal", "signed", "special"])
 @pytest.mark.parametrize("lens,budget,recent", [
     ([1, 0, 5, 40], 16, 4), ([40, 41, 39, 1000], 40, 40), ([33, 64, 65], 32, 0), ([1, 2, 3], 1, 1), ([7, 100], 1, 0),
-    ([1023, 1024, 1025, 4097], 1000, 17), ([20000, 5], 4096, 100), ([2049], 2048, 2047)])
+    ([1023, 1024, 1025, 4097], 1000, 17), ([20000, 5], 4096, 100), ([2049], 2048, 2047), ([60000, 51201, 100], 30000, 64)])
 def test_select(L, kind, lens, budget, recent):
     S, width = len(lens), max(lens) + 3
     x = _scores(kind, S, width, sum(lens))
@@ -246,6 +250,26 @@ def test_compact(L, lens, budget, recent, heads, block, group, in_place):
     for s, rows in enumerate(kept):
         assert torch.equal(new_scores[s, :len(rows)].cpu(), scores[s][rows])
         assert bool((new_scores[s, len(rows):] == 0).all())
+
+
+@gpu
+def test_compact_into_fresh_blocks_reports_bad_values(L):
+    NB, block, heads = 8, 16, 2
+    g = torch.Generator().manual_seed(4)
+    codes = torch.randint(0, 256, (NB, heads, block, 64), generator=g, dtype=torch.int32).to(torch.uint8)
+    params = torch.randn(NB, heads, block, 1, 2, generator=g).to(torch.bfloat16)
+    src = torch.tensor([[0, 1], [2, -1], [3, 3]], dtype=torch.int32)
+    dst = torch.tensor([[4], [5], [NB]], dtype=torch.int32)
+    keep = torch.tensor([[3, 20, 31], [1, 17, 40], [0, 1, 2]], dtype=torch.int32)
+    new = torch.tensor([3, 3, 1], dtype=torch.int32)
+    kc, vc = [(codes.cuda(), params.cuda()) for _ in range(2)]
+    pkv.evict_compact_q4(kc, vc, src.cuda(), dst.cuda(), keep.cuda(), new.cuda())
+    assert pkv.check_device_errors() == pkv.DEVERR_CONTEXT | pkv.DEVERR_BLOCK
+    for old, got in ((codes, kc[0]), (codes, vc[0]), (params, kc[1]), (params, vc[1])):
+        want = old.clone()
+        want[4, :, 0], want[4, :, 1], want[4, :, 2] = old[0, :, 3], old[1, :, 4], old[1, :, 15]
+        want[5, :, 0] = old[2, :, 1]
+        assert torch.equal(got.cpu().view(torch.uint8), want.view(torch.uint8))
 
 
 @gpu

@@ -95,6 +95,9 @@ def test_decode_refuses(L):
     assert _decode(L, Hq=12) == pkv.PKV_ERR_UNSUPPORTED
     assert _decode(L, S=65536) == pkv.PKV_ERR_UNSUPPORTED
     assert _decode(L, NB=1 << 40) == pkv.PKV_ERR_UNSUPPORTED
+    assert _decode(L, mcl=(1 << 30) + 1) == pkv.PKV_ERR_UNSUPPORTED
+    assert _decode(L, S=65535, mcl=1 << 30, ks=FAKE, ld=1 << 30) == pkv.PKV_ERR_UNSUPPORTED
+    assert L.pkv_decode_q4_workspace_size(65535, 16, 8, 128, 1 << 30, 1) == 0
     assert L.pkv_decode_q4_workspace_size(0, 16, 8, 128, 64, 0) == 0
     assert L.pkv_decode_q4_workspace_size(2, 12, 8, 128, 64, 0) == 0
     assert L.pkv_decode_q4_workspace_size(2, 16, 8, 64, 64, 0) == 0
@@ -271,6 +274,8 @@ DECODE = [  # lens, heads, gqa, block, group, window
     ([300, 5, 1000, 641], 2, 4, 64, 64, 100),
     ([3000, 10], 2, 2, 16, 128, 1025),
     ([500, 64], 1, 8, 32, 32, 4096),
+    ([6000, 7, 300], 2, 8, 16, 64, 0),
+    ([3300, 65], 3, 1, 32, 32, 0),
 ]
 
 
@@ -461,6 +466,62 @@ def test_decode_in_a_graph_on_another_stream(L):
     once = torch.zeros_like(scores)
     pkv.paged_decode_attn_q4(q, kc, vc, wide, cl, 16384, SCALE, key_scores=once, stream=None)
     assert torch.equal(scores, once + once)
+    assert pkv.check_device_errors() == 0
+
+
+@gpu
+def test_rows_past_32_bit_offsets(L):
+    """A pool whose arrays pass 4 GiB: rows in its last blocks."""
+    heads, block, group = 8, 256, 128
+    NB = (1 << 32) // (heads * block * 64) + 40
+    kc, vc = [(torch.empty(NB, heads, block, 64, dtype=torch.uint8, device="cuda"),
+               torch.empty(NB, heads, block, 1, 2, dtype=torch.bfloat16, device="cuda")) for _ in range(2)]
+    assert kc[0].numel() > 1 << 32
+    n = 300
+    tables = torch.tensor([[NB - 1, NB - 3]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(12)
+    k, v = (torch.randn(n, heads, 128, generator=g).to(torch.bfloat16) for _ in range(2))
+    p = torch.arange(n)
+    slots = (tables[0].long()[p // block] * block + p % block).to(torch.int32).cuda()
+    pkv.kv_store_q4(k.cuda(), v.cuda(), kc, vc, slots)
+    kk, vv = (Q.values(*Q.quantise(x, group)) for x in (k, v))
+    bk, bv = pkv.kv_load_q4(kc, vc, slots)
+    assert torch.equal(bk.cpu().double(), kk) and torch.equal(bv.cpu().double(), vv)
+    q = torch.randn(1, 8, 128, generator=g).to(torch.bfloat16)
+    o, _ = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, tables.cuda(), torch.tensor([n], dtype=torch.int32, device="cuda"), n, SCALE)
+    po, _ = pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu([1]), _cu([n]), tables.cuda(), 1, n, n, SCALE)
+    for h in range(8):
+        want, _, _, wv, _ = Q.attend(q[0, h:h + 1].double(), kk[:, h], vv[:, h], SCALE, [0], [n - 1])
+        for got in (o, po):
+            assert bool(((got[0, h].cpu().double() - want[0]).abs() <= Q.out_tolerance(want[0], wv[0])).all())
+    # compaction between far blocks
+    keep = torch.arange(0, 300, 3, dtype=torch.int32, device="cuda")[None]
+    dst = torch.tensor([[NB - 5]], dtype=torch.int32, device="cuda")
+    pkv.evict_compact_q4(kc, vc, tables.cuda(), dst, keep, torch.tensor([100], dtype=torch.int32, device="cuda"))
+    got, _ = pkv.kv_load_q4(kc, vc, (torch.arange(100) + (NB - 5) * block).to(torch.int32).cuda())
+    assert torch.equal(got.cpu().double(), kk[::3])
+    assert pkv.check_device_errors() == 0
+
+
+@gpu
+def test_two_streams_with_workspaces_of_their_own(L):
+    """Calls that overlap on two streams: each gets the bits of the call alone."""
+    c = Q.Cache(41, [3000, 50], 2, 16, 32)
+    kc, vc, bt = c.cuda()
+    cl = torch.tensor([3000, 50], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(6)
+    qs = [torch.randn(2, 4, 128, generator=g).to(torch.bfloat16).cuda() for _ in range(2)]
+    alone = [pkv.paged_decode_attn_q4(q, kc, vc, bt, cl, 3000, SCALE) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, st in enumerate(streams):
+            got[i].append(pkv.paged_decode_attn_q4(qs[i], kc, vc, bt, cl, 3000, SCALE, stream=st))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, l in got[i]:
+            assert torch.equal(o, alone[i][0]) and torch.equal(l, alone[i][1])
     assert pkv.check_device_errors() == 0
 
 
