@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   Step cur = {static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x), 0};
   KeyRange range;
   int n_mine;  // this warp's steps
+  [[maybe_unused]] int first_entry = 0;
   if constexpr (kRanges) {
     if (warp == 0) build_prefix(p, prefix, ctx_of, blockIdx.x == 0, lane);
     __syncthreads();
@@ -203,6 +204,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
     cur = locate(prefix, p.num_seqs, p.num_kv_heads, first_step);
     range = key_range(p, ctx_of[cur.s]);
   } else {
+    // the table entry of the lane's first unit is loaded beside the length,
+    // before the length says whether the unit exists (without a window the first
+    // unit is at position 0)
+    const uint32_t j = fast_quotient((warp + kWarps * (lane >> 1)) * kStep + (lane & 1) * kUnit, p.block);
+    first_entry = p.block_tables[static_cast<int64_t>(cur.s) * p.max_blocks + min(j, static_cast<uint32_t>(p.max_blocks) - 1)];
     range = key_range(p, p.context_lens[cur.s]);
     if (range.ctx == 0) {
       if (cur.head == 0 && threadIdx.x == 0) atomicOr(&g_q4_decode_errors, kErrContext);
@@ -237,7 +243,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   // kNoUnit past the last key and for an invalid table entry; a lane holds one
   // unit of a batch of 32
   constexpr uint32_t kNoUnit = 0xffffffffu;
-  auto unit_row = [&](int i) -> uint32_t {
+  auto unit_row = [&](int i, bool loaded = false) -> uint32_t {
     int s, head, key, ctx;
     if constexpr (kRanges) {
       if ((i >> 1) >= n_mine) return kNoUnit;
@@ -253,7 +259,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
     }
     if (key >= ctx) return kNoUnit;
     const uint32_t j = fast_quotient(key, p.block);
-    const int blk = p.block_tables[static_cast<int64_t>(s) * p.max_blocks + j];
+    const int blk = loaded ? first_entry : p.block_tables[static_cast<int64_t>(s) * p.max_blocks + j];
     if (blk < 0 || blk >= p.num_blocks) {
       atomicOr(&g_q4_decode_errors, kErrBlock);
       return kNoUnit;
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
     return static_cast<uint32_t>(
         ((static_cast<int64_t>(blk) * p.num_kv_heads + head) * p.block.d + (key - j * p.block.d)) / kUnit);
   };
-  uint32_t batch = unit_row(lane), next_batch = n_mine > 16 ? unit_row(32 + lane) : kNoUnit;
+  uint32_t batch = unit_row(lane, !kRanges && range.unit0 == 0), next_batch = n_mine > 16 ? unit_row(32 + lane) : kNoUnit;
   // one bit a unit that is there, of the batch being consumed and of the next
   uint32_t there = __ballot_sync(0xffffffffu, batch != kNoUnit);
   uint32_t there_next = __ballot_sync(0xffffffffu, next_batch != kNoUnit);
