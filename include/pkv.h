@@ -485,8 +485,8 @@ pkv_status pkv_evict_select(const float *key_scores, int64_t score_stride,
  *               sequence of the call reads that block (compaction in place), or
  *               a block that no source table of the call names. Equal tables
  *               compact every sequence in place; sequences that share blocks
- *               with others need fresh ones (pkv_bm_evict_sequence makes such
- *               rows). Nothing else is written.
+ *               with others need fresh ones (pkv_bm_evict_sequences makes
+ *               such rows). Nothing else is written.
  *   key_scores  device float32 [num_seqs, score_stride], or NULL (both):
  *   dst_key_scores  dst_key_scores[s * dst_score_stride + i] =
  *               key_scores[s * score_stride + keep[s][i]], and the entries from

@@ -73,20 +73,24 @@ pkv_status pkv_bm_add_sequence(pkv_block_manager *bm, int64_t seq_id, const int3
  * sequence's last block is full. The new token is at position num_tokens - 1. */
 pkv_status pkv_bm_append_token(pkv_block_manager *bm, int64_t seq_id, int32_t token_id);
 
-/* Eviction (pkv_evict_select, pkv_evict_compact): seq_id keeps num_kept (1 ..
- * its token count) of its tokens. Its table becomes the destination of the
- * compaction: the first ceil(num_kept / block_size) blocks, each the block it
- * was unless another sequence shares it, in which case a fresh one takes its
- * place; the others are released. Read the old row (pkv_bm_block_table) before
- * this call and the new row after it, and enqueue the compaction between them
- * on the stream of the cache's other calls before anything is stored into
- * blocks handed out later: a released block still holds rows to be moved.
- * From here on the sequence has num_kept tokens; its rows are no longer those of
- * a prompt, so that none of its blocks is findable any more, those it fills
+/* Eviction (pkv_evict_select, pkv_evict_compact) of num_seqs different
+ * sequences: seq_ids[k] keeps num_kept[k] (1 .. its token count) of its tokens.
+ * Its table becomes the destination of the compaction, of
+ * ceil(num_kept / block_size) blocks: fresh ones for all the sequences if there
+ * are enough (the compaction is then a parallel copy), else each the block it was
+ * (compacted in place), but a fresh one where another sequence shares it. The
+ * other blocks are released; none of them is handed out by this call.
+ * Read the old rows (pkv_bm_block_table) before this call and the new rows after
+ * it, and enqueue ONE compaction of these sequences from the old to the new
+ * rows, on the stream of the cache's other calls, before the next call that hands
+ * out blocks is acted upon: a released block still holds rows to be moved.
+ * From here on the sequences have num_kept tokens; their rows are no longer those
+ * of a prompt, so that none of their blocks is findable any more, those they fill
  * later included (released ones keep their content and stay findable).
  * PKV_ERR_OUT_OF_BLOCKS if fewer blocks are free than shared ones are to be
  * replaced. */
-pkv_status pkv_bm_evict_sequence(pkv_block_manager *bm, int64_t seq_id, int32_t num_kept);
+pkv_status pkv_bm_evict_sequences(pkv_block_manager *bm, const int64_t *seq_ids,
+                                  const int32_t *num_kept, int32_t num_seqs);
 
 /* Release seq_id: each of its blocks loses one reference; blocks left with
  * none go to the back of the free list. */

@@ -145,8 +145,8 @@ def lib():
     L.pkv_bm_add_sequence.restype = ctypes.c_int
     L.pkv_bm_append_token.argtypes = [P, i64, i32]
     L.pkv_bm_append_token.restype = ctypes.c_int
-    L.pkv_bm_evict_sequence.argtypes = [P, i64, i32]
-    L.pkv_bm_evict_sequence.restype = ctypes.c_int
+    L.pkv_bm_evict_sequences.argtypes = [P, P, P, i32]
+    L.pkv_bm_evict_sequences.restype = ctypes.c_int
     L.pkv_bm_free_sequence.argtypes = [P, i64]
     L.pkv_bm_free_sequence.restype = ctypes.c_int
     L.pkv_bm_num_tokens.argtypes = [P, i64, pi32]
@@ -631,10 +631,16 @@ class BlockManager:
         _check(self._L.pkv_bm_append_token(self._h, int(seq_id), int(token_id)),
                "pkv_bm_append_token")
 
-    def evict_sequence(self, seq_id: int, num_kept: int) -> None:
-        """Keep num_kept tokens; block_table() is then the compaction's destination."""
-        _check(self._L.pkv_bm_evict_sequence(self._h, int(seq_id), int(num_kept)),
-               "pkv_bm_evict_sequence")
+    def evict_sequences(self, seq_ids, num_kept) -> None:
+        """Keep num_kept[k] tokens of seq_ids[k]; block_table() then gives the
+        destination rows of one compaction of these sequences."""
+        import numpy as np
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        kept = np.ascontiguousarray(num_kept, dtype=np.int32)
+        if ids.ndim != 1 or ids.shape != kept.shape:
+            raise ValueError("seq_ids and num_kept must be lists of the same length")
+        _check(self._L.pkv_bm_evict_sequences(self._h, ids.ctypes.data, kept.ctypes.data,
+                                              ids.shape[0]), "pkv_bm_evict_sequences")
 
     def free_sequence(self, seq_id: int) -> None:
         _check(self._L.pkv_bm_free_sequence(self._h, int(seq_id)), "pkv_bm_free_sequence")

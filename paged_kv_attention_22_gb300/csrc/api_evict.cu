@@ -11,6 +11,8 @@ using pkv::current_sm_count;
 
 constexpr int32_t kMaxBudget = 1 << 29;  // the kernels count kept positions, four arrays of them, in 32 bits
 
+constexpr int32_t kMaxSeqs = 1 << 27;    // of a selection: eight CTAs each
+
 // Checks shared by the two compactions; the arrays are already in `a`.
 pkv_status compact(pkv::EvictCompactArgs &a, const int32_t *src_tables, int32_t src_max_blocks,
                    const int32_t *dst_tables, int32_t dst_max_blocks, const int32_t *keep, int32_t budget,
@@ -67,7 +69,7 @@ pkv_status pkv_evict_select(const float *key_scores, int64_t score_stride, const
     return PKV_ERR_INVALID_ARG;
   if (key_scores == nullptr || context_lens == nullptr || keep == nullptr || new_lens == nullptr)
     return PKV_ERR_INVALID_ARG;
-  if (max_context_len > pkv::kMaxContext || budget > kMaxBudget) return PKV_ERR_UNSUPPORTED;
+  if (max_context_len > pkv::kMaxContext || budget > kMaxBudget || num_seqs > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
   int sms = 0;
   pkv_status st = current_sm_count(&sms);

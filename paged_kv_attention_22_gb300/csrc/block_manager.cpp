@@ -236,34 +236,55 @@ pkv_status pkv_bm_append_token(pkv_block_manager *bm, int64_t seq_id, int32_t to
   return PKV_OK;
 }
 
-pkv_status pkv_bm_evict_sequence(pkv_block_manager *bm, int64_t seq_id, int32_t num_kept) {
-  if (bm == nullptr) return PKV_ERR_INVALID_ARG;
-  auto it = bm->seqs.find(seq_id);
-  if (it == bm->seqs.end()) return PKV_ERR_INVALID_ARG;
-  Sequence &seq = it->second;
-  if (num_kept <= 0 || num_kept > static_cast<int32_t>(seq.tokens.size())) return PKV_ERR_INVALID_ARG;
-  const size_t n = (static_cast<size_t>(num_kept) + bm->block_size - 1) / bm->block_size;
-  int32_t fresh = 0;
-  for (size_t i = 0; i < n; ++i)
-    if (bm->blocks[seq.blocks[i]].ref > 1) ++fresh;
-  if (fresh > bm->num_free) return PKV_ERR_OUT_OF_BLOCKS;
-  for (size_t i = 0; i < n; ++i) {
-    const int32_t b = seq.blocks[i];
-    if (bm->blocks[b].ref > 1) {  // others still read it: this sequence's rows move to a fresh one
-      --bm->blocks[b].ref;
-      seq.blocks[i] = bm->take_fresh();
-    } else {
-      bm->unpublish(b);
+pkv_status pkv_bm_evict_sequences(pkv_block_manager *bm, const int64_t *seq_ids, const int32_t *num_kept,
+                                  int32_t num_seqs) {
+  if (bm == nullptr || num_seqs < 0 || (num_seqs > 0 && (seq_ids == nullptr || num_kept == nullptr)))
+    return PKV_ERR_INVALID_ARG;
+  const int32_t bs = bm->block_size;
+  // checks, and how many blocks the kept tokens take, before any change
+  int64_t all = 0, shared = 0;
+  for (int32_t k = 0; k < num_seqs; ++k) {
+    for (int32_t j = 0; j < k; ++j)
+      if (seq_ids[j] == seq_ids[k]) return PKV_ERR_INVALID_ARG;
+    auto it = bm->seqs.find(seq_ids[k]);
+    if (it == bm->seqs.end()) return PKV_ERR_INVALID_ARG;
+    const Sequence &seq = it->second;
+    if (num_kept[k] <= 0 || num_kept[k] > static_cast<int32_t>(seq.tokens.size())) return PKV_ERR_INVALID_ARG;
+    const size_t n = (static_cast<size_t>(num_kept[k]) + bs - 1) / bs;
+    all += static_cast<int64_t>(n);
+    for (size_t i = 0; i < n; ++i)
+      if (bm->blocks[seq.blocks[i]].ref > 1) ++shared;
+  }
+  if (shared > bm->num_free) return PKV_ERR_OUT_OF_BLOCKS;
+  const bool fresh = all <= bm->num_free;
+  std::vector<int32_t> released;
+  try {
+    size_t most = 0;
+    for (int32_t k = 0; k < num_seqs; ++k) most += bm->seqs.find(seq_ids[k])->second.blocks.size();
+    released.reserve(most);
+  } catch (const std::bad_alloc &) {
+    return PKV_ERR_INVALID_ARG;
+  }
+  for (int32_t k = 0; k < num_seqs; ++k) {
+    Sequence &seq = bm->seqs.find(seq_ids[k])->second;
+    const size_t n = (static_cast<size_t>(num_kept[k]) + bs - 1) / bs;
+    for (size_t i = 0; i < seq.blocks.size(); ++i) {
+      const int32_t b = seq.blocks[i];
+      if (i < n && !fresh && bm->blocks[b].ref == 1) {
+        bm->unpublish(b);  // compacted in place
+      } else {
+        released.push_back(b);
+        if (i < n) seq.blocks[i] = bm->take_fresh();
+      }
     }
+    seq.blocks.resize(n);
+    seq.tokens.resize(num_kept[k]);
+    seq.chain.clear();
+    seq.evicted = true;
   }
-  for (size_t k = seq.blocks.size(); k-- > n;) {
-    const int32_t b = seq.blocks[k];
+  // only now: no block that is still to be read was handed out above
+  for (const int32_t b : released)
     if (--bm->blocks[b].ref == 0) bm->push_free(b);
-  }
-  seq.blocks.resize(n);
-  seq.tokens.resize(num_kept);
-  seq.chain.clear();
-  seq.evicted = true;
   return PKV_OK;
 }
 

@@ -2,10 +2,10 @@
 // of each sequence stay (evict_select) and moving their rows together
 // (evict_compact).
 //
-// Selection. One CTA a sequence finds the want-th largest score with a radix
-// select over the scores' order-preserving 32-bit keys, eight bits a pass (the
-// keys stay in shared memory while they fit), until the bin that holds it is
-// taken whole. It then writes the kept positions in ascending order: each warp
+// Selection. One CTA, or a cluster of eight for long sequences, finds the
+// want-th largest score with a radix select over the scores' order-preserving
+// 32-bit keys, eight bits a pass (the keys stay in shared memory while they fit),
+// until the bin that holds it is taken whole. It then writes the kept positions in ascending order: each warp
 // owns a contiguous range of positions, counts the keys above and at the
 // threshold, and after one scan over the warps writes its own with ballots. Equal
 // scores are taken from the lowest position on.
@@ -35,6 +35,8 @@ constexpr int kSelLoads = 16;
 constexpr int kBins = 256;
 constexpr int kHistCopies = 8;  // histograms, each shared by four warps, against contention
 constexpr size_t kSelMaxKeyBytes = 200 * 1024;  // beside the histograms
+constexpr unsigned kSelCluster = 8;             // CTAs a long sequence
+constexpr int32_t kSelAlone = 4096;             // longest sequences that one CTA takes
 
 struct SelectParams {
   const float *key_scores;
@@ -51,19 +53,26 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// kCached: the competing positions' keys fit in dynamic shared memory.
+// One cluster of CTAs a sequence (grid: sequences x cluster), each with a part of
+// the competing positions: their histograms are summed through distributed
+// shared memory, and every CTA finds the threshold for itself. kCached: the
+// part's keys fit in dynamic shared memory.
 template <bool kCached>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
   extern __shared__ uint32_t s_keys[];
   __shared__ uint32_t hist[kHistCopies][kBins];
-  __shared__ uint32_t s_prefix, s_left, s_whole;
+  __shared__ uint32_t part[2][kBins];   // this CTA's histogram, of odd and even passes
+  __shared__ uint32_t total[kBins];     // the cluster's
+  __shared__ uint32_t s_prefix, s_left, s_whole, s_counts[2];
   __shared__ int s_gt[kSelWarps], s_eq[kSelWarps];
   griddep_wait();  // inputs written by the previous kernel are visible from here on
   griddep_launch_dependents();
-  const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int C = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int s = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // the CTAs of a cluster leave before its first barrier together, or not at all
   const int ctx = p.context_lens[s];
   if (ctx < 0 || ctx > p.max_context_len) {
-    if (tid == 0) atomicOr(&g_evict_errors, kErrContext);
+    if (tid == 0 && rank == 0) atomicOr(&g_evict_errors, kErrContext);
     return;
   }
   const float *score = p.key_scores + s * p.score_stride;
@@ -71,14 +80,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
   const int new_len = min(ctx, p.budget), recent = min(ctx, p.recent);
   const int old = ctx - recent;         // positions that compete
   const int want = new_len - recent;    // how many of them stay
-  if (tid == 0) p.new_lens[s] = new_len;
-  for (int i = new_len + tid; i < p.budget; i += kSelThreads) keep[i] = -1;
-  for (int i = tid; i < recent; i += kSelThreads) keep[want + i] = old + i;
+  const int me = rank * kSelThreads + tid, all = C * kSelThreads;
+  if (me == 0) p.new_lens[s] = new_len;
+  for (int i = new_len + me; i < p.budget; i += all) keep[i] = -1;
+  for (int i = me; i < recent; i += all) keep[want + i] = old + i;
   if (want == old) {  // nothing to evict
-    for (int i = tid; i < old; i += kSelThreads) keep[i] = i;
+    for (int i = me; i < old; i += all) keep[i] = i;
     return;
   }
   if (want == 0) return;
+  // this CTA's positions
+  const int per_cta = ((old + C - 1) / C + 31) / 32 * 32;
+  const int cta0 = min(old, rank * per_cta), mine = min(old, cta0 + per_cta) - cta0;
+  score += cta0;
   auto key_of = [&](int i) { return kCached ? s_keys[i] : score_key(score[i]); };
 
   // ---- the want-th largest key, most significant digit first
@@ -90,14 +104,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     uint32_t *h = hist[warp % kHistCopies];
     if (shift == 24) {
       // the one pass over global memory: kSelLoads loads a thread in flight
-      for (int i0 = tid; i0 < old; i0 += kSelThreads * kSelLoads) {
+      for (int i0 = tid; i0 < mine; i0 += kSelThreads * kSelLoads) {
         float f[kSelLoads];
 #pragma unroll
-        for (int u = 0; u < kSelLoads; ++u) f[u] = i0 + u * kSelThreads < old ? score[i0 + u * kSelThreads] : 0.f;
+        for (int u = 0; u < kSelLoads; ++u) f[u] = i0 + u * kSelThreads < mine ? score[i0 + u * kSelThreads] : 0.f;
 #pragma unroll
         for (int u = 0; u < kSelLoads; ++u) {
           const int i = i0 + u * kSelThreads;
-          if (i >= old) break;
+          if (i >= mine) break;
           const uint32_t k = score_key(f[u]);
           if (kCached) s_keys[i] = k;
           atomicAdd(&h[k >> 24], 1u);
@@ -105,9 +119,28 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
       }
     } else {
 #pragma unroll 8
-      for (int i = tid; i < old; i += kSelThreads) {
+      for (int i = tid; i < mine; i += kSelThreads) {
         const uint32_t k = key_of(i);
         if ((k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&h[(k >> shift) & 255u], 1u);
+      }
+    }
+    __syncthreads();
+    if (tid < kBins) {
+      uint32_t n = 0;
+#pragma unroll
+      for (int c = 0; c < kHistCopies; ++c) n += hist[c][tid];
+      if (C == 1) total[tid] = n;
+      else part[(shift >> 3) & 1][tid] = n;
+    }
+    if (C > 1) {
+      // a part is read until its CTA's next barrier but one writes it again
+      cluster_sync();
+      if (tid < kBins) {
+        const uint32_t at = smem_u32(&part[(shift >> 3) & 1][tid]);
+        uint32_t n = 0;
+#pragma unroll 8
+        for (int c = 0; c < C; ++c) n += ld_cluster_u32(at, c);
+        total[tid] = n;
       }
     }
     __syncthreads();
@@ -116,9 +149,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
       uint32_t n[8], sum = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        n[j] = 0;
-#pragma unroll
-        for (int c = 0; c < kHistCopies; ++c) n[j] += hist[c][255 - 8 * lane - j];
+        n[j] = total[255 - 8 * lane - j];
         sum += n[j];
       }
       uint32_t above = sum;
@@ -152,8 +183,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 
   // ---- kept positions in order: keys above the threshold, and the first
   // `left` of those equal to it
-  const int per_warp = ((old + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
-  const int begin = min(old, warp * per_warp), end = min(old, begin + per_warp);
+  const int per_warp = ((mine + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int begin = min(mine, warp * per_warp), end = min(mine, begin + per_warp);
   int gt = 0, eq = 0;
 #pragma unroll 4
   for (int i = begin + lane; i - lane < end; i += 32) {
@@ -166,9 +197,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     s_eq[warp] = eq;
   }
   __syncthreads();
-  // in the warps before this one
+  // in the warps before this one, and in the CTAs before this one
   int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
   int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? s_eq[lane] : 0);
+  if (C > 1) {
+    if (warp == 0) {
+      const int a = __reduce_add_sync(0xffffffffu, s_gt[lane]), b = __reduce_add_sync(0xffffffffu, s_eq[lane]);
+      if (lane == 0) {
+        s_counts[0] = a;
+        s_counts[1] = b;
+      }
+    }
+    cluster_sync();
+    gt0 += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster_u32(smem_u32(&s_counts[0]), lane) : 0u);
+    eq0 += __reduce_add_sync(0xffffffffu, lane < rank ? ld_cluster_u32(smem_u32(&s_counts[1]), lane) : 0u);
+  }
   const uint32_t below = (1u << lane) - 1u;
   const int quota = static_cast<int>(left);
 #pragma unroll 2
@@ -178,10 +221,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     const uint32_t be = __ballot_sync(0xffffffffu, i < end && k == prefix);
     const int my_gt = gt0 + __popc(bg & below), my_eq = eq0 + __popc(be & below);
     const bool in = ((bg >> lane) & 1u) || (((be >> lane) & 1u) && my_eq < quota);
-    if (in) keep[my_gt + min(my_eq, quota)] = i;
+    if (in) keep[my_gt + min(my_eq, quota)] = cta0 + i;
     gt0 += __popc(bg);
     eq0 += __popc(be);
   }
+  if (C > 1) cluster_sync();  // no CTA leaves while another reads its counts
 }
 
 // ---------------------------------------------------------------- compaction
@@ -198,6 +242,7 @@ struct CompactParams {
   float *dst_key_scores;             // [S, dst_score_stride]
   int64_t score_stride, dst_score_stride;
   int32_t src_max_blocks, dst_max_blocks, budget, num_blocks;
+  int32_t slice_bytes;               // in place: bytes of a row a CTA moves at a time, at most
   FastDiv block;
 };
 
@@ -206,9 +251,11 @@ template <> struct Piece<16> { using T = uint4; };
 template <> struct Piece<8> { using T = uint2; };
 template <> struct Piece<4> { using T = uint32_t; };
 
-// Slot of position pos in a table, or -1 (with its bit raised) for a position or
-// block that does not exist.
-__device__ __forceinline__ int64_t slot_of(const CompactParams &p, const int32_t *table, int max_blocks, int pos) {
+// Byte offset of position pos's row of plane 0 in an array, or -1 (with its bit
+// raised) for a position or block that does not exist. Plane k's row lies k
+// times block_size * row_bytes further.
+__device__ __forceinline__ int64_t row_at(const CompactParams &p, const RowArray &a, const int32_t *table, int max_blocks,
+                                          int pos) {
   const int j = pos < 0 ? max_blocks : static_cast<int>(fast_quotient(pos, p.block));
   if (j >= max_blocks) {
     atomicOr(&g_evict_errors, kErrContext);
@@ -219,15 +266,7 @@ __device__ __forceinline__ int64_t slot_of(const CompactParams &p, const int32_t
     atomicOr(&g_evict_errors, kErrBlock);
     return -1;
   }
-  return static_cast<int64_t>(blk) * p.block.d + (pos - j * static_cast<int>(p.block.d));
-}
-
-// Byte offset of a slot's row of one plane.
-__device__ __forceinline__ int64_t row_offset(const CompactParams &p, const RowArray &a, int plane, int64_t slot) {
-  if (a.planes == 1) return slot * a.row_bytes;
-  const uint32_t blk = fast_quotient(static_cast<uint32_t>(slot), p.block);
-  return ((static_cast<int64_t>(blk) * a.planes + plane) * p.block.d + (slot - static_cast<int64_t>(blk) * p.block.d)) *
-         a.row_bytes;
+  return (static_cast<int64_t>(blk) * a.planes * p.block.d + (pos - j * static_cast<int>(p.block.d))) * a.row_bytes;
 }
 
 // Move `bytes` bytes at `at` of every kept row of one plane, N bytes a thread.
@@ -236,11 +275,12 @@ __device__ void move_slice(const CompactParams &p, const RowArray &a, int plane,
   using T = typename Piece<N>::T;
   const int per_row = bytes / N;
   const int rows = kMoveThreads / per_row;  // rows a step
-  const int r = threadIdx.x / per_row, c = at + threadIdx.x % per_row * N;
+  const int r = threadIdx.x / per_row;
   const int32_t *keep = p.keep + static_cast<int64_t>(s) * p.budget;
   const int32_t *src = p.src_tables + static_cast<int64_t>(s) * p.src_max_blocks;
   const int32_t *dst = p.dst_tables + static_cast<int64_t>(s) * p.dst_max_blocks;
-  uint8_t *base = static_cast<uint8_t *>(a.base);
+  uint8_t *base = static_cast<uint8_t *>(a.base) + static_cast<int64_t>(plane) * p.block.d * a.row_bytes + at +
+                  threadIdx.x % per_row * N;
   for (int i0 = 0; i0 < n; i0 += rows * kMoveUnroll) {
     T x[kMoveUnroll];
     int64_t to[kMoveUnroll];
@@ -249,48 +289,50 @@ __device__ void move_slice(const CompactParams &p, const RowArray &a, int plane,
       const int i = i0 + u * rows + r;
       to[u] = -1;
       if (r < rows && i < n) {
-        const int64_t from = slot_of(p, src, p.src_max_blocks, keep[i]);
-        const int64_t into = slot_of(p, dst, p.dst_max_blocks, i);
+        const int64_t from = row_at(p, a, src, p.src_max_blocks, keep[i]);
+        const int64_t into = row_at(p, a, dst, p.dst_max_blocks, i);
         if (from >= 0 && into >= 0 && from != into) {
-          to[u] = row_offset(p, a, plane, into);
-          x[u] = *reinterpret_cast<const T *>(base + row_offset(p, a, plane, from) + c);
+          to[u] = into;
+          x[u] = *reinterpret_cast<const T *>(base + from);
         }
       }
     }
     __syncthreads();  // the whole chunk is loaded: its places may be overwritten
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u)
-      if (to[u] >= 0) *reinterpret_cast<T *>(base + to[u] + c) = x[u];
+      if (to[u] >= 0) *reinterpret_cast<T *>(base + to[u]) = x[u];
   }
 }
 
-// The pieces of N bytes of kRowsPerWarp rows of one array: lane by lane, all
-// planes of a row together. from / to hold the rows' slots (-1: not moved).
+// The pieces of N bytes of kRowsPerWarp rows of one array, all planes of a row
+// together, kPieces a lane in flight. from / to hold the rows' offsets (to -1: not
+// moved).
+constexpr int kPieces = 2;
 template <int N>
 __device__ __forceinline__ void move_rows(const CompactParams &p, const RowArray &a, const int64_t (&from)[kRowsPerWarp],
                                           const int64_t (&to)[kRowsPerWarp], int lane) {
   using T = typename Piece<N>::T;
   const int per_plane = a.row_bytes / N, pieces = a.planes * per_plane;
+  const int64_t plane_bytes = static_cast<int64_t>(p.block.d) * a.row_bytes;
   uint8_t *base = static_cast<uint8_t *>(a.base);
-  for (int i0 = lane; i0 < pieces; i0 += 64) {
-    T x[2][kRowsPerWarp];
+#pragma unroll 1
+  for (int i0 = lane; i0 < pieces; i0 += 32 * kPieces) {
+    T x[kPieces][kRowsPerWarp];
+    int64_t at[kPieces];
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
+    for (int v = 0; v < kPieces; ++v) {
       const int i = i0 + 32 * v;
-      const int plane = a.planes == 1 ? 0 : i / per_plane, c = (i - plane * per_plane) * N;
+      const int plane = a.planes == 1 ? 0 : i / per_plane;
+      at[v] = plane * plane_bytes + (i - plane * per_plane) * N;
 #pragma unroll
       for (int u = 0; u < kRowsPerWarp; ++u)
-        if (i < pieces && to[u] >= 0)
-          x[v][u] = __ldcs(reinterpret_cast<const T *>(base + row_offset(p, a, plane, from[u]) + c));
+        if (i < pieces && to[u] >= 0) x[v][u] = __ldcs(reinterpret_cast<const T *>(base + from[u] + at[v]));
     }
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int i = i0 + 32 * v;
-      const int plane = a.planes == 1 ? 0 : i / per_plane, c = (i - plane * per_plane) * N;
+    for (int v = 0; v < kPieces; ++v)
 #pragma unroll
       for (int u = 0; u < kRowsPerWarp; ++u)
-        if (i < pieces && to[u] >= 0) *reinterpret_cast<T *>(base + row_offset(p, a, plane, to[u]) + c) = x[v][u];
-    }
+        if (i0 + 32 * v < pieces && to[u] >= 0) *reinterpret_cast<T *>(base + to[u] + at[v]) = x[v][u];
   }
 }
 
@@ -342,25 +384,33 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_compact_kernel(const Co
   if (!__syncthreads_or(in_place)) {
     const int32_t *keep = p.keep + static_cast<int64_t>(s) * p.budget;
     const int lane = threadIdx.x & 31;
-    // an item is kRowsPerWarp rows of one array
+    // an item is kRowsPerWarp rows of one array; the next item's slots (kept
+    // position, then table entry: two loads in a row) are looked up while this
+    // one's rows move
     const int items = (n + kRowsPerWarp - 1) / kRowsPerWarp * p.num_arrays;
-    for (int item = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); item < items;
-         item += movers * (kMoveThreads / 32)) {
-      const int quad = item / p.num_arrays, i0 = quad * kRowsPerWarp;
-      // lane u < kRowsPerWarp looks up row u
-      int64_t f = -1, t = -1;
-      if (lane < kRowsPerWarp && i0 + lane < n) {
-        f = slot_of(p, src, p.src_max_blocks, keep[i0 + lane]);
-        t = slot_of(p, dst, p.dst_max_blocks, i0 + lane);
+    const int step = movers * (kMoveThreads / 32);
+    int item = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
+    int64_t f, t;  // of row `lane` of the item, lane < kRowsPerWarp
+    auto look_up = [&](int it) {
+      f = t = -1;
+      const int quad = it / p.num_arrays, i = quad * kRowsPerWarp + lane;
+      if (it < items && lane < kRowsPerWarp && i < n) {
+        const RowArray &a = p.arrays[it - quad * p.num_arrays];
+        f = row_at(p, a, src, p.src_max_blocks, keep[i]);
+        t = row_at(p, a, dst, p.dst_max_blocks, i);
         if (f < 0) t = -1;
       }
+    };
+    look_up(item);
+    for (; item < items; item += step) {
       int64_t from[kRowsPerWarp], to[kRowsPerWarp];
 #pragma unroll
       for (int u = 0; u < kRowsPerWarp; ++u) {
         from[u] = __shfl_sync(0xffffffffu, f, u);
         to[u] = __shfl_sync(0xffffffffu, t, u);
       }
-      const RowArray &a = p.arrays[item - quad * p.num_arrays];
+      look_up(item + step);
+      const RowArray &a = p.arrays[item % p.num_arrays];
       if (a.row_bytes % 16 == 0) move_rows<16>(p, a, from, to, lane);
       else if (a.row_bytes % 8 == 0) move_rows<8>(p, a, from, to, lane);
       else move_rows<4>(p, a, from, to, lane);
@@ -372,7 +422,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_compact_kernel(const Co
 #pragma unroll 1
   for (int k = 0; k < p.num_arrays; ++k) {
     const RowArray &a = p.arrays[k];
-    const int per_plane = a.row_bytes > kSliceBytes ? a.row_bytes / kSliceBytes : 1, slices = a.planes * per_plane;
+    const int per_plane = a.row_bytes > p.slice_bytes ? a.row_bytes / p.slice_bytes : 1, slices = a.planes * per_plane;
     const int bytes = a.row_bytes / per_plane;
     for (; first < slices; first += movers) {
       const int plane = first / per_plane, at = (first - plane * per_plane) * bytes;
@@ -396,25 +446,53 @@ cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t stream) {
   p.max_context_len = a.max_context_len;
   p.budget = a.budget;
   p.recent = a.recent;
-  // the largest number of competing positions whose keys a CTA can hold
-  const size_t smem = static_cast<size_t>(a.max_context_len) * sizeof(uint32_t);
-  if (smem > kSelMaxKeyBytes)
-    return launch_pdl(evict_select_kernel<false>, dim3(a.num_seqs), dim3(kSelThreads), 0, stream, p);
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSelMaxKeyBytes));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(evict_select_kernel<true>, dim3(a.num_seqs), dim3(kSelThreads), smem, stream, p);
+  // one CTA for a short sequence (its passes take less than the cluster's
+  // barriers), a cluster for longer ones
+  const unsigned C = a.max_context_len <= kSelAlone ? 1 : kSelCluster;
+  const size_t per_cta = ((static_cast<size_t>(a.max_context_len) + C - 1) / C + 31) / 32 * 32;
+  const bool cached = per_cta * sizeof(uint32_t) <= kSelMaxKeyBytes;
+  const auto kernel = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
+  const size_t smem = cached ? per_cta * sizeof(uint32_t) : 0;
+  if (smem > 32 * 1024) {  // beside the static arrays
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(kSelMaxKeyBytes));
+    if (e != cudaSuccess) return e;
+  }
+  if (C == 1) return launch_pdl(kernel, dim3(a.num_seqs), dim3(kSelThreads), smem, stream, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * C);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream) {
   CompactParams p;
-  int64_t slices = 0;
   p.num_arrays = a.num_arrays;
+  int64_t row_bytes = 0;
   for (int k = 0; k < a.num_arrays; ++k) {
     p.arrays[k] = a.arrays[k];
-    slices += static_cast<int64_t>(a.arrays[k].planes) *
-              (a.arrays[k].row_bytes > kSliceBytes ? a.arrays[k].row_bytes / kSliceBytes : 1);
+    row_bytes += static_cast<int64_t>(a.arrays[k].planes) * a.arrays[k].row_bytes;
   }
+  // in place the slices of a sequence are all that spreads it over the SMs: half
+  // as wide where there are too few for four CTAs an SM (in place, one sequence of
+  // 8,192 kept rows of 4 KiB takes 48 us with 32 bytes and 83 with 64; 64 of 512
+  // rows 93 and 78)
+  p.slice_bytes = a.num_seqs * (row_bytes / kSliceBytes) < 4 * static_cast<int64_t>(a.num_sms) ? kSliceBytes / 2 : kSliceBytes;
+  int64_t slices = 0;
+  for (int k = 0; k < a.num_arrays; ++k)
+    slices += static_cast<int64_t>(a.arrays[k].planes) *
+              (a.arrays[k].row_bytes > p.slice_bytes ? a.arrays[k].row_bytes / p.slice_bytes : 1);
   p.src_tables = a.src_tables;
   p.dst_tables = a.dst_tables;
   p.keep = a.keep;

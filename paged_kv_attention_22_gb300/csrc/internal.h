@@ -225,7 +225,7 @@ struct RowArray {
   int32_t planes, row_bytes;
 };
 constexpr int kMaxRowArrays = 4;
-constexpr int kSliceBytes = 64;  // bytes of a row that one CTA of the compaction moves, at most
+constexpr int kSliceBytes = 64;  // bytes of a row that one CTA of an in-place compaction moves, at most
 struct EvictCompactArgs {
   RowArray arrays[kMaxRowArrays];
   int32_t num_arrays;

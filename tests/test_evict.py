@@ -88,49 +88,74 @@ def test_scored_decode_refuses(L):
     assert L.pkv_decode_scores_workspace_size(1 << 30, 1 << 14, 1, 128, 1 << 30) == 0
 
 
-def test_manager_eviction_keeps_private_blocks_and_replaces_shared_ones(L):
+def _manager(num_blocks):
+    """Two sequences of 5 blocks of 8 tokens that share the first 2."""
     rng = np.random.default_rng(1)
-    bm = pkv.BlockManager(20, 8)
-    base = rng.integers(0, 50000, 40).astype(np.int32)      # 5 blocks
-    bm.add_sequence(0, base)
+    bm = pkv.BlockManager(num_blocks, 8)
+    base = rng.integers(0, 50000, 40).astype(np.int32)
     other = np.concatenate([base[:16], rng.integers(0, 50000, 20).astype(np.int32)])
-    assert bm.add_sequence(1, other) == 16                  # 5 blocks, 2 of them shared
-    src = bm.block_table(1)
-    free = bm.num_free_blocks
-    bm.evict_sequence(1, 19)                                # 3 blocks stay
+    assert bm.add_sequence(0, base) == 0 and bm.add_sequence(1, other) == 16
+    return bm, base, other
+
+
+@pytest.mark.parametrize("spare", [2, 12])
+def test_manager_eviction(L, spare):
+    """With 3 fresh blocks at hand the kept rows go there; with 2, only the shared
+    blocks are replaced and the third is compacted in place."""
+    bm, base, other = _manager(8 + spare)
+    src, free = bm.block_table(1), bm.num_free_blocks
+    assert free == spare
+    bm.evict_sequences([1], [19])                           # 3 blocks stay
     dst = bm.block_table(1)
     assert len(dst) == 3 and bm.num_tokens(1) == 19
-    assert dst[2] == src[2]                                 # its own block
-    assert not set(dst[:2]) & set(src) and not set(dst[:2]) & set(bm.block_table(0))
-    assert [bm.ref_count(b) for b in src] == [1, 1, 1, 0, 0]
-    assert bm.num_free_blocks == free                       # two taken, two released
-    # sequence 0 is as it was, and still findable; the evicted rows are not
-    assert bm.add_sequence(2, base) == 32
-    assert bm.add_sequence(3, other) == 16
-    # tokens appended to the evicted sequence fill blocks that nobody finds
-    for t in range(21):
-        bm.append_token(1, t)
-    assert bm.num_tokens(1) == 40 and len(bm.block_table(1)) == 5
-    assert np.array_equal(bm.slots(1, 0, 40), np.repeat(bm.block_table(1), 8) * 8 + np.tile(np.arange(8), 5))
-    for s in range(4):
-        bm.free_sequence(s)
-    assert bm.num_free_blocks == 20
+    fresh = 3 if spare == 12 else 2
+    assert not set(dst[:fresh]) & set(src) and not set(dst[:fresh]) & set(bm.block_table(0))
+    assert fresh == 3 or dst[2] == src[2]
+    assert [bm.ref_count(b) for b in src] == [1, 1, 3 - fresh, 0, 0]
+    assert bm.num_free_blocks == spare + 3 - 3              # three released or replaced, three in use
+    if spare == 12:
+        # sequence 0 is as it was, and still findable; the evicted rows are not
+        assert bm.add_sequence(2, base) == 32
+        # tokens appended to the evicted sequence fill blocks that nobody finds
+        for t in range(21):
+            bm.append_token(1, t)
+        assert bm.num_tokens(1) == 40 and len(bm.block_table(1)) == 5
+        assert np.array_equal(bm.slots(1, 0, 40), np.repeat(bm.block_table(1), 8) * 8 + np.tile(np.arange(8), 5))
+        bm.free_sequence(2)
+    bm.free_sequence(0)
+    bm.free_sequence(1)
+    assert bm.num_free_blocks == 8 + spare
+
+
+def test_manager_eviction_of_several_hands_out_no_block_that_is_still_read(L):
+    bm, _, _ = _manager(14)                                 # 6 free: exactly the kept blocks
+    old = set(bm.block_table(0)) | set(bm.block_table(1))
+    bm.evict_sequences([1, 0], [24, 20])
+    new = list(bm.block_table(0)) + list(bm.block_table(1))
+    assert len(set(new)) == 6 and not set(new) & old
+    assert bm.num_free_blocks == 8 and all(bm.ref_count(b) == 0 for b in old)
+    bm, _, _ = _manager(13)                                 # 5 free: in place but the shared blocks
+    src = [bm.block_table(s) for s in range(2)]
+    bm.evict_sequences([0, 1], [40, 20])
+    assert all(b not in set(src[0]) | set(src[1]) for s in range(2) for b in bm.block_table(s)[:2])
+    assert list(bm.block_table(0)[2:]) == list(src[0][2:]) and bm.block_table(1)[2] == src[1][2]
+    assert bm.ref_count(src[0][0]) == 0                     # shared by nobody any more
 
 
 def test_manager_eviction_refuses(L):
-    bm = pkv.BlockManager(4, 4)
-    tok = np.arange(12, dtype=np.int32)
-    bm.add_sequence(0, tok)
-    bm.add_sequence(1, np.concatenate([tok[:8], [99]]).astype(np.int32))    # shares 2, takes the last free one
-    assert bm.num_free_blocks == 0
+    bm, _, _ = _manager(9)                                  # 1 free, 2 shared
+    state = [list(bm.block_table(s)) for s in range(2)]
     with pytest.raises(pkv.PkvError) as e:
-        bm.evict_sequence(0, 5)
+        bm.evict_sequences([0], [20])
     assert e.value.status == pkv.PKV_ERR_OUT_OF_BLOCKS
-    for seq, kept in ((7, 1), (0, 0), (0, 13)):
+    for seqs, kept in (([7], [1]), ([0], [0]), ([0], [41]), ([0, 0], [9, 9]), ([0, 7], [1, 1])):
         with pytest.raises(pkv.PkvError) as e:
-            bm.evict_sequence(seq, kept)
+            bm.evict_sequences(seqs, kept)
         assert e.value.status == pkv.PKV_ERR_INVALID_ARG
-    assert bm.num_tokens(0) == 12 and len(bm.block_table(0)) == 3 and bm.ref_count(bm.block_table(0)[0]) == 2
+    with pytest.raises(ValueError):
+        bm.evict_sequences([0, 1], [1])
+    bm.evict_sequences([], [])
+    assert state == [list(bm.block_table(s)) for s in range(2)] and bm.num_free_blocks == 1
 
 
 # ------------------------------------------------------------------ GPU: selection
@@ -365,19 +390,20 @@ def test_scored_decode_adds_nothing_after_a_timeout(L):
 
 @gpu
 @pytest.mark.parametrize("q4", [False, True])
-def test_engine_steps_with_eviction(L, q4):
+@pytest.mark.parametrize("pool", [13, 40])
+def test_engine_steps_with_eviction(L, q4, pool):
     """Two sequences that share a prefix, driven by the block manager: prefill,
-    decode steps that accumulate weights, eviction of the longer one into fresh and
-    own blocks, and decode on. The attention after it equals plain attention over
+    decode steps that accumulate weights, eviction of the longer one (into fresh
+    blocks, or with a small pool into fresh and own ones), and decode on. The attention after it equals plain attention over
     exactly the kept rows, and the other sequence sees nothing of it."""
     heads, gqa, block, group, budget, recent = 2, 2, 16, 32, 50, 12
     g = torch.Generator().manual_seed(8)
-    bm = pkv.BlockManager(40, block)
+    bm = pkv.BlockManager(pool, block)
     prompts = [np.arange(100, dtype=np.int32), np.concatenate([np.arange(48), 900 + np.arange(30)]).astype(np.int32)]
     if q4:
-        kc, vc = (pkv.new_q4_cache(40, block, heads, group) for _ in range(2))
+        kc, vc = (pkv.new_q4_cache(pool, block, heads, group) for _ in range(2))
     else:
-        kc, vc = (torch.full((40, block, heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        kc, vc = (torch.full((pool, block, heads, 128), float("nan"), dtype=torch.bfloat16, device="cuda") for _ in range(2))
     rows = [[], []]                      # each sequence's (k, v) rows in logical order, as the cache holds them
 
     def kept_value(x):
@@ -431,15 +457,15 @@ def test_engine_steps_with_eviction(L, q4):
     row = scores[:1].clone()
     before = row.cpu()
     keep, new = pkv.evict_select(row, torch.tensor(lens[:1], dtype=torch.int32, device="cuda"), budget, recent)
-    bm.evict_sequence(0, budget)
+    bm.evict_sequences([0], [budget])
     dst = torch.from_numpy(bm.block_table(0, 8)[None]).cuda()
-    assert bool((dst[0, :3] != src[0, :3]).all()) and int(dst[0, 3]) == int(src[0, 3])
+    assert bool((dst[0, :3] != src[0, :3]).all()) and (int(dst[0, 3]) == int(src[0, 3])) == (pool == 13)
     (pkv.evict_compact_q4 if q4 else pkv.evict_compact)(kc, vc, src, dst, keep, new, key_scores=row, dst_key_scores=row)
     scores[0] = row[0]
     assert new.tolist() == [budget]
     kept = keep[0].long().cpu()
     assert kept.tolist() == select_plain(before, lens[:1], budget, recent)[0]
     rows[0] = [x[kept] for x in rows[0]]
-    for _ in range(20):                 # past the end of a block
+    for _ in range(15):                 # past the end of a block
         decode(scores)
     assert pkv.check_device_errors() == 0
