@@ -35,6 +35,7 @@ constexpr int kSelLoads = 16;
 constexpr int kBins = 256;
 constexpr int kHistCopies = 8;  // histograms, each shared by four warps, against contention
 constexpr size_t kSelMaxKeyBytes = 200 * 1024;  // beside the histograms
+constexpr int kSelSmall = 256;                  // positions that are ranked by comparison instead
 constexpr unsigned kSelCluster = 8;             // CTAs a long sequence
 constexpr int32_t kSelAlone = 4096;             // longest sequences that one CTA takes
 
@@ -89,6 +90,27 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     return;
   }
   if (want == 0) return;
+  if (kCached && C == 1 && old <= kSelSmall) {
+    // a thread a position: its rank is the number of keys before its own (by key,
+    // then by position), found by comparing with all of them
+    if (tid < kSelSmall) s_keys[tid] = tid < old ? score_key(score[tid]) : 0u;
+    __syncthreads();
+    if (tid >= kSelSmall) return;
+    const uint32_t k = s_keys[tid];
+    int rank_of = 0;
+#pragma unroll 8
+    for (int i = 0; i < old; ++i) {
+      const uint32_t other = s_keys[i];
+      rank_of += other > k || (other == k && i < tid);
+    }
+    const bool in = tid < old && rank_of < want;
+    const uint32_t kept = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) s_gt[warp] = __popc(kept);
+    asm volatile("bar.sync 1, %0;" ::"n"(kSelSmall) : "memory");  // the threads still here
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? s_gt[lane] : 0);
+    if (in) keep[before + __popc(kept & ((1u << lane) - 1u))] = tid;
+    return;
+  }
   // this CTA's positions
   const int per_cta = ((old + C - 1) / C + 31) / 32 * 32;
   const int cta0 = min(old, rank * per_cta), mine = min(old, cta0 + per_cta) - cta0;
@@ -452,7 +474,7 @@ cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t stream) {
   const size_t per_cta = ((static_cast<size_t>(a.max_context_len) + C - 1) / C + 31) / 32 * 32;
   const bool cached = per_cta * sizeof(uint32_t) <= kSelMaxKeyBytes;
   const auto kernel = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
-  const size_t smem = cached ? per_cta * sizeof(uint32_t) : 0;
+  const size_t smem = cached ? (per_cta > kSelSmall ? per_cta : kSelSmall) * sizeof(uint32_t) : 0;
   if (smem > 32 * 1024) {  // beside the static arrays
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSelMaxKeyBytes));
