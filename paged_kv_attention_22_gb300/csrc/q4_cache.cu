@@ -9,7 +9,11 @@
 //
 // All three are copies with some arithmetic: HBM bandwidth bounds them, once the
 // arithmetic is short enough (the store spends about six packed operations on
-// two values) and indices are found without 64-bit divisions.
+// two values) and indices are found without 64-bit divisions. 32,768 tokens of 8
+// heads: store 41 us (176 MB, 4.3 TB/s; its issue slots are 73 % used, so it is
+// between the two bounds), load 30 us (176 MB, 5.9 TB/s), widening for prefill 28 us
+// (6.3 TB/s). With 8 values a lane the store took 51 us, its per-row work being
+// shared by half as many values.
 #include "internal.h"
 #include "q4.cuh"
 

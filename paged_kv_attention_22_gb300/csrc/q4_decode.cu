@@ -12,7 +12,9 @@
 //            equal ranges, one a warp, whatever the lengths. A pair cut between
 //            warps leaves one partial result each in the workspace (a warp's
 //            first piece in slot 2w, its last in slot 2w + 1), joined by a
-//            second kernel: the way for few or unequal pairs.
+//            second kernel: the way for few or unequal pairs. (Splits of fixed
+//            length in CTAs of their own took 68 us where ranges take 66.7;
+//            joined in clusters through distributed shared memory, 73.)
 //
 // The products run on mma.sync m16n8k16 in bf16 with fp32 accumulators. A bf16
 // of the cache's definition is what the codes are widened to, so the logits
@@ -31,8 +33,13 @@
 // probabilities, the weights that the products used; the lse comes from the
 // fp32 sum.
 //
-// Widening the codes is what the kernel spends its issue slots on: three
-// instructions for two values, 400 of the some 600 that a step takes.
+// What bounds it: widening the codes, a shift, a logic operation and a packed fma
+// for two values, some 420 of the 680 instructions of a step. Shifts and logic
+// share one half-rate pipe and packed fmas have another. 16 sequences of 16,384
+// keys, 8 KV heads, 2 query heads each: 65.6 us, 336 MB at 5.1 TB/s; issue slots
+// 62 % used, the shift and logic pipe 57 %. (Without the widening the same loop
+// streams at 6.3 TB/s; a step of 16 keys, or 20 or 24 warps an SM with fewer
+// registers, took 71 to 78 us.) 64 sequences of 640 keys: 15.7 us.
 #include "internal.h"
 #include "key_scores.cuh"
 #include "q4.cuh"

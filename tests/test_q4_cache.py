@@ -324,6 +324,44 @@ def test_decode_long_and_short_sequences_of_many_pairs(L):
     assert bool(((o.cpu().double() - out).abs() <= tol_o).all()) and bool(((l.cpu().double() - lse).abs() <= tol_l).all())
 
 
+@gpu
+def test_decode_more_sequences_than_ranges_take(L):
+    """Above 1,024 sequences every (sequence, KV head) has a CTA of its own."""
+    lens = [5, 40, 17] * 350 + [900]
+    c = Q.Cache(22, lens, 1, 16, 64)
+    q = torch.randn(len(lens), 1, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    kc, vc, bt = c.cuda()
+    scores = torch.zeros(len(lens), 900, device="cuda")
+    o, none = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt, torch.tensor(lens, dtype=torch.int32, device="cuda"), 900, SCALE,
+                                       with_lse=False, key_scores=scores)
+    assert none is None and pkv.check_device_errors() == 0
+    for s in (0, 1, 2, 500, 1049, 1050):
+        n = lens[s]
+        want, lse, w, wv, qk = Q.attend(q[s].double(), c.logical(c.k, s, n, 0), c.logical(c.v, s, n, 0), SCALE, [0], [n - 1])
+        assert bool(((o[s, 0].cpu().double() - want[0]).abs() <= Q.out_tolerance(want[0], wv[0])).all())
+        tol = w[0] * (2 * Q.lse_tolerance(lse, qk, n / 4) + 2.0 ** -20) + 1e-30
+        assert bool(((scores[s, :n].cpu().double() - w[0]).abs() <= tol).all()) and bool((scores[s, n:] == 0).all())
+
+
+@gpu
+def test_head_shards_of_a_4_bit_cache(L):
+    """A rank of a KV-head shard (heads are dimension 1 of a 4-bit cache) computes
+    its heads of the whole call."""
+    from paged_kv_attention_22_gb300.shard import head_shard, take_heads
+    lens = [700, 33, 64]
+    c = Q.Cache(23, lens, 4, 64, 32)
+    q = torch.randn(3, 8, 128, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    out, _, tol_o, _, _, _ = _decode_plain(c, q, 2, 0)
+    kc, vc, bt = c.cuda()
+    cl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for rank in range(2):
+        qs, ks = head_shard(rank, 2, 8, 4)
+        kr, vr = (tuple(take_heads(x, ks, 1) for x in cache) for cache in (kc, vc))
+        o, _ = pkv.paged_decode_attn_q4(take_heads(q, qs, 1).cuda(), kr, vr, bt, cl, 700, SCALE)
+        assert bool(((o.cpu().double() - out[:, qs]).abs() <= tol_o[:, qs]).all())
+    assert pkv.check_device_errors() == 0
+
+
 def _random_cache(seqs, blocks_per_seq, heads, block, group):
     """A large random cache made on the GPU, tables of seqs sequences in shuffled blocks."""
     g = torch.Generator(device="cuda").manual_seed(3)
