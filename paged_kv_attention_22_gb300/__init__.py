@@ -412,8 +412,11 @@ def kv_store_q4(k, v, k_cache, v_cache, slot_mapping, stream=None):
 
 def kv_load_q4(k_cache, v_cache, slots, k=None, v=None, stream=None):
     """The rows at slots [T] as bf16 (k, v) [T, H_kv, 128]; zeros for slot -1."""
-    with _on(stream):
-        st, k, v = _calls().kv_load_q4(k_cache, v_cache, slots, k, v, stream)
+    if stream is None:
+        st, k, v = _calls().kv_load_q4(k_cache, v_cache, slots, k, v, None)
+    else:  # what the call allocates belongs to its stream
+        with torch.cuda.stream(stream):
+            st, k, v = _calls().kv_load_q4(k_cache, v_cache, slots, k, v, stream)
     if st:
         raise PkvError(st, "pkv_kv_load_q4")
     return k, v
@@ -535,9 +538,13 @@ def paged_decode_attn_scores(q, k_cache, v_cache, block_tables, context_lens, ma
 def evict_select(key_scores, context_lens, budget, recent, keep=None, new_lens=None, stream=None):
     """Positions that stay: the last `recent` and the highest-scoring others, budget
     in all, ascending. Returns (keep int32 [S, budget], -1 padded, new_lens int32 [S])."""
-    with _on(stream):
+    if stream is None:
         st, keep, new_lens = _calls().evict_select(key_scores, context_lens, budget, recent, keep,
-                                                     new_lens, stream)
+                                                   new_lens, None)
+    else:  # what the call allocates belongs to its stream
+        with torch.cuda.stream(stream):
+            st, keep, new_lens = _calls().evict_select(key_scores, context_lens, budget, recent,
+                                                       keep, new_lens, stream)
     if st:
         raise PkvError(st, "pkv_evict_select")
     return keep, new_lens

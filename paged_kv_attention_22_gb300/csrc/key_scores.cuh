@@ -23,23 +23,27 @@ struct KeyScoresParams {
   int64_t ctx_cap;          // max_blocks * block_size
 };
 
-// Body of the per-file kernels; grid (position chunks, sequences).
-__device__ __forceinline__ void key_scores_body(const KeyScoresParams &p) {
-  const int s = blockIdx.y;
+// Chunk `chunk` of `chunks` of sequence s's positions, kScoreThreads at a time;
+// lse holds the sequence's [H_q] values.
+__device__ __forceinline__ void add_key_scores(const KeyScoresParams &p, int s, int chunk, int chunks, const float *lse) {
   const int ctx = p.context_lens[s];
   if (ctx <= 0 || ctx > p.max_context_len || ctx > p.ctx_cap) return;
   const int first = p.window > 0 && ctx > p.window ? ctx - p.window : 0;
-  for (int64_t pos = blockIdx.x * kScoreThreads + threadIdx.x; pos < ctx; pos += gridDim.x * kScoreThreads) {
+  for (int64_t pos = static_cast<int64_t>(chunk) * kScoreThreads + threadIdx.x; pos < ctx;
+       pos += static_cast<int64_t>(chunks) * kScoreThreads) {
     if (pos < first) continue;
     const float *z = p.logits + static_cast<int64_t>(s) * p.num_q_heads * p.logits_ld + pos;
-    const float *lse = p.lse + static_cast<int64_t>(s) * p.num_q_heads;
     float w = 0.f;
 #pragma unroll 8
     for (int h = 0; h < p.num_q_heads; ++h)
       w += fast_exp2(fmaf(-kScoreLog2e, lse[h], z[h * p.logits_ld]));
-    float *dst = p.key_scores + s * p.score_stride + pos;
-    *dst += w;
+    p.key_scores[s * p.score_stride + pos] += w;
   }
+}
+
+// Body of the per-file kernels; grid (position chunks, sequences).
+__device__ __forceinline__ void key_scores_body(const KeyScoresParams &p) {
+  add_key_scores(p, blockIdx.y, blockIdx.x, gridDim.x, p.lse + static_cast<int64_t>(blockIdx.y) * p.num_q_heads);
 }
 
 // Position chunks of a launch for these sizes.

@@ -579,10 +579,29 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
 // kPerRow warps each (8 for pairs cut into many pieces), four dims a lane.
 constexpr int kMergeWarps = 8;
 constexpr int kMergeBatch = 8;  // pieces whose loads a warp has in flight
+static_assert(kMergeWarps * 32 == kScoreThreads, "a CTA of the merge's launch may be one of the weights'");
 
+// The pieces of a (sequence, query head): the first one's warp, how many, and the
+// first one's slot (the others': twice their warp).
+struct Pieces {
+  int64_t first, n, slot;
+};
+__device__ __forceinline__ Pieces pieces_of(const Q4DecodeParams &p, const int64_t *prefix, int64_t W, int64_t U, int s,
+                                            int head) {
+  const int64_t steps = prefix[s + 1] - prefix[s], P0 = p.num_kv_heads * prefix[s] + head * steps;
+  if (steps == 0) return {0, 0, 0};
+  const int64_t wa = owner_of(P0, W, U);
+  return {wa, owner_of(P0 + steps - 1, W, U) - wa + 1, 2 * wa + (range_start(wa, W, U) < P0 ? 1 : 0)};
+}
+
+// With accumulated weights the launch's first `score_ctas` CTAs (chunks of each
+// sequence's positions) add them, beside the CTAs that merge: they take the
+// lse from the pieces themselves, a warp a head, and need not wait for the merge.
 template <int kPerRow>
-__global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4DecodeParams p, int32_t decode_warps) {
-  extern __shared__ int64_t merge_prefix[];
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    q4_merge_kernel(const Q4DecodeParams p, int32_t decode_warps, const KeyScoresParams k, int32_t score_ctas,
+                    int32_t score_chunks) {
+  extern __shared__ int64_t merge_prefix[];  // [S + 1], then the lse of a scoring CTA's sequence [H_q]
   __shared__ float4 s_o[kMergeWarps][32];
   __shared__ float s_ml[kMergeWarps][3];
   griddep_wait();
@@ -592,22 +611,44 @@ __global__ void __launch_bounds__(kMergeWarps * 32) q4_merge_kernel(const Q4Deco
   __syncthreads();
   const int64_t U = p.num_kv_heads * merge_prefix[p.num_seqs];
   const int64_t W = min(static_cast<int64_t>(decode_warps), U);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kMergeWarps / kPerRow) + warp / kPerRow;
-  int64_t wa = 0, n = 0, slot_a = 0;  // first warp, pieces, the first one's slot
+  if (static_cast<int>(blockIdx.x) < score_ctas) {
+    float *lse = reinterpret_cast<float *>(merge_prefix + p.num_seqs + 1);
+    const int s = blockIdx.x / score_chunks, chunk = blockIdx.x - s * score_chunks;
+    for (int hq = warp; hq < p.num_q_heads; hq += kMergeWarps) {
+      const Pieces c = pieces_of(p, merge_prefix, W, U, s, hq / p.gqa);
+      if (c.n <= 1) {  // written whole by the decode kernel (or an invalid length)
+        if (lane == 0 && c.n == 1) lse[hq] = p.lse[static_cast<int64_t>(s) * p.num_q_heads + hq];
+        continue;
+      }
+      float M = kFloor, l = 0.f;
+      for (int64_t i = lane; i < c.n; i += 32) {
+        const float4 ml = p.ws_ml[(i == 0 ? c.slot : 2 * (c.first + i)) * p.gqa + hq % p.gqa];
+        const float m_new = fmaxf(M, ml.x);
+        l = fmaf(l, fast_exp2(M - m_new), ml.y * fast_exp2(ml.x - m_new));
+        M = m_new;
+      }
+      float top = M;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      l *= fast_exp2(M - top);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+      if (lane == 0) lse[hq] = (top + log2f(l)) * kLn2;
+    }
+    __syncthreads();
+    add_key_scores(k, s, chunk, score_chunks, lse);
+    return;
+  }
+  const int64_t row = static_cast<int64_t>(blockIdx.x - score_ctas) * (kMergeWarps / kPerRow) + warp / kPerRow;
+  Pieces c = {0, 0, 0};
   int h = 0;
   if (row < static_cast<int64_t>(p.num_seqs) * p.num_q_heads) {
     const int s = static_cast<int>(row / p.num_q_heads), hq = static_cast<int>(row % p.num_q_heads);
-    const int head = hq / p.gqa;
-    h = hq - head * p.gqa;
-    const int64_t steps = merge_prefix[s + 1] - merge_prefix[s];
-    const int64_t P0 = p.num_kv_heads * merge_prefix[s] + head * steps;
-    if (steps > 0) {
-      wa = owner_of(P0, W, U);
-      n = owner_of(P0 + steps - 1, W, U) - wa + 1;
-      slot_a = 2 * wa + (range_start(wa, W, U) < P0 ? 1 : 0);
-    }
+    h = hq % p.gqa;
+    c = pieces_of(p, merge_prefix, W, U, s, hq / p.gqa);
   }
-  if (n == 1) n = 0;  // written whole
+  const int64_t wa = c.first, slot_a = c.slot;
+  const int64_t n = c.n == 1 ? 0 : c.n;  // one piece: written whole
   float M = kFloor, o[4] = {0.f, 0.f, 0.f, 0.f}, l = 0.f, r = 0.f;
 #pragma unroll 1
   for (int64_t i0 = sub; i0 < n; i0 += kMergeBatch * kPerRow) {
@@ -689,8 +730,10 @@ cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream
   return launch_pdl(kernel, grid, dim3(kWarps * 32), smem, stream, p);
 }
 
+// k: the accumulated weights, or null.
 template <int NG>
-cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, cudaStream_t stream) {
+cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, const KeyScoresParams *k,
+                        cudaStream_t stream) {
   static_assert(Q4DecodeSmem<NG, 16>::kTotal + 12 * kQ4MaxRangeSeqs + 8 <= 227 * 1024, "shared memory of the ranges");
   const dim3 pairs(p.num_kv_heads, p.num_seqs);
   if (plan.range_ctas > 0) {
@@ -698,12 +741,19 @@ cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, cudaS
     if (e != cudaSuccess) return e;
     const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
     const int warps = plan.range_ctas * 16;
-    const size_t smem = sizeof(int64_t) * (p.num_seqs + 1);
     // many pieces a pair: as many warps a row as a CTA has
     const bool many = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * 16 < warps;
     const int64_t ctas = many ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
-    return launch_pdl(many ? q4_merge_kernel<kMergeWarps> : q4_merge_kernel<1>, dim3(static_cast<unsigned>(ctas)),
-                      dim3(kMergeWarps * 32), smem, stream, p, warps);
+    const int64_t chunks = k != nullptr ? key_scores_grid_x(p.max_context_len) : 0;
+    const size_t smem = sizeof(int64_t) * (p.num_seqs + 1) + (k != nullptr ? sizeof(float) * p.num_q_heads : 0);
+    const auto kernel = many ? q4_merge_kernel<kMergeWarps> : q4_merge_kernel<1>;
+    if (smem > 40 * 1024) {  // beside the static arrays
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+      if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas + chunks * p.num_seqs)), dim3(kMergeWarps * 32), smem,
+                      stream, p, warps, k != nullptr ? *k : KeyScoresParams{},
+                      static_cast<int32_t>(chunks * p.num_seqs), static_cast<int32_t>(chunks));
   }
   switch (plan.warps) {
     case 4: return launch_shape<NG, 4, false>(p, pairs, stream);
@@ -743,16 +793,7 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
   // unless a product passes 2^26, and masked logits stay -inf
   p.scale_log2 = fmaxf(fabsf(a.scale_log2), 0x1p-126f);
   p.q_signs = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-  cudaError_t e;
-  switch (a.cache.group_size) {
-    case 32: e = launch_plan<4>(p, a.plan, stream); break;
-    case 64: e = launch_plan<2>(p, a.plan, stream); break;
-    case 128: e = launch_plan<1>(p, a.plan, stream); break;
-    default: return cudaErrorInvalidValue;
-  }
-  if (e != cudaSuccess) return e;
-  if (a.key_scores == nullptr) return cudaSuccess;
-  KeyScoresParams k;
+  KeyScoresParams k = {};
   k.logits = a.logits;
   k.lse = a.lse;
   k.key_scores = a.key_scores;
@@ -763,6 +804,15 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
   k.num_q_heads = a.num_q_heads;
   k.window = a.window;
   k.ctx_cap = static_cast<int64_t>(a.max_blocks) * a.cache.block_size;
+  const KeyScoresParams *scores = a.key_scores != nullptr ? &k : nullptr;
+  cudaError_t e;
+  switch (a.cache.group_size) {
+    case 32: e = launch_plan<4>(p, a.plan, scores, stream); break;
+    case 64: e = launch_plan<2>(p, a.plan, scores, stream); break;
+    case 128: e = launch_plan<1>(p, a.plan, scores, stream); break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e != cudaSuccess || scores == nullptr || a.plan.range_ctas > 0) return e;
   return launch_pdl(q4_scores_kernel, dim3(key_scores_grid_x(a.max_context_len), a.num_seqs),
                     dim3(kScoreThreads), 0, stream, k);
 }
