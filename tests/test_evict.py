@@ -469,3 +469,64 @@ def test_engine_steps_with_eviction(L, q4, pool):
     for _ in range(15):                 # past the end of a block
         decode(scores)
     assert pkv.check_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("pdl", [True, False])
+def test_captured_step_with_eviction(L, pdl):
+    """Store, decode with weights, selection, compaction into fresh blocks, decode over
+    the kept rows and prefill, captured in one graph and replayed on new inputs: the
+    bits of the eager calls; with programmatic launches and without."""
+    heads, gqa, block, S, ctx, budget = 4, 2, 32, 3, 500, 128
+    g = torch.Generator(device="cuda").manual_seed(17)
+    per, kept_blocks = 16, budget // block
+    NB = S * (per + kept_blocks)
+    ids = torch.randperm(NB, generator=g, device="cuda").to(torch.int32)
+    src, dst = ids[:S * per].view(S, per).contiguous(), ids[S * per:].view(S, kept_blocks).contiguous()
+    lens = torch.tensor([ctx, ctx - 77, 129], dtype=torch.int32, device="cuda")
+    p = torch.arange(ctx, device="cuda")
+    slots = (src.long()[:, p // block] * block + p % block).to(torch.int32).flatten()
+    slots[(p >= lens[:, None]).flatten()] = -1
+    cu = torch.tensor([0, 8, 16, 24], dtype=torch.int32, device="cuda")
+    cu_k = torch.tensor([0, budget, 2 * budget, 3 * budget], dtype=torch.int32, device="cuda")
+    cache = [pkv.new_q4_cache(NB, block, heads) for _ in range(2)]
+    k, v = (torch.zeros(S * ctx, heads, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(S, heads * gqa, 128, dtype=torch.bfloat16, device="cuda")
+    qp = torch.zeros(24, heads * gqa, 128, dtype=torch.bfloat16, device="cuda")
+    scores, new_scores = torch.zeros(S, ctx, device="cuda"), torch.zeros(S, budget, device="cuda")
+    ws = pkv.new_q4_decode_workspace(S, heads * gqa, heads, ctx, with_scores=True)
+
+    def step():
+        scores.zero_()
+        pkv.kv_store_q4(k, v, *cache, slots)
+        a = pkv.paged_decode_attn_q4(q, *cache, src, lens, ctx, SCALE, workspace=ws, key_scores=scores)
+        keep, new = pkv.evict_select(scores, lens, budget, 20)
+        pkv.evict_compact_q4(*cache, src, dst, keep, new, key_scores=scores, dst_key_scores=new_scores)
+        b = pkv.paged_decode_attn_q4(q, *cache, dst, new, budget, SCALE, workspace=ws)
+        c = pkv.paged_prefill_attn_q4(qp, *cache, cu, cu_k, dst, 8, budget, 3 * budget, SCALE)
+        return [*a, keep, new, new_scores, *b, *c, scores]
+
+    def fill(seed):
+        g.manual_seed(seed)
+        for x in (k, v, q, qp):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda").to(torch.bfloat16))
+
+    pkv.set_programmatic_launch(pdl)
+    try:
+        fill(1)
+        step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            captured = step()
+        for seed in (2, 3):
+            fill(seed)
+            want = [x.clone() for x in step()]
+            graph.replay()
+            torch.cuda.synchronize()
+            for i, (x, y) in enumerate(zip(captured, want)):
+                assert torch.equal(x, y), (seed, i)
+            assert want[3].tolist() == [budget, budget, budget] and bool(torch.isfinite(want[7].float()).all())
+        assert pkv.check_device_errors() == 0
+    finally:
+        pkv.set_programmatic_launch(True)
