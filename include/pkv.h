@@ -390,9 +390,10 @@ pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const vo
                                     size_t workspace_bytes, void *stream);
 
 /*
- * Bytes of device workspace of pkv_paged_prefill_attn_q4 (0 on invalid sizes):
- * the call widens the batch's keys to bf16 there, 512 * num_kv_heads bytes per
- * key, and up to 128 keys more per sequence. Conditions as above.
+ * Bytes of device workspace of pkv_paged_prefill_attn_q4 (0 on invalid sizes or
+ * without a device): the call may widen the batch's keys to bf16 there, 512 *
+ * num_kv_heads bytes per key and up to 128 keys more per sequence. Conditions as
+ * above.
  */
 size_t pkv_prefill_q4_workspace_size(int32_t num_seqs, int32_t total_k, int32_t max_seqlen_k,
                                      int32_t num_kv_heads, int32_t head_dim);
@@ -405,7 +406,9 @@ size_t pkv_prefill_q4_workspace_size(int32_t num_seqs, int32_t total_k, int32_t 
  *   total_k    host int: an upper bound of cu_seqlens_k[num_seqs]; a segment
  *              that ends past it raises PKV_DEVERR_SEQLENS and is not written
  *   workspace  device, >= pkv_prefill_q4_workspace_size(...) bytes
- * num_seqs is at most 65535.
+ * num_seqs is at most 65535. With few query tokens over many keys the call runs
+ * each row through the decode kernels instead of widening the keys (the same
+ * sums in another order); it then takes no notice of PKV_DEVERR_TIMEOUT.
  */
 pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const void *k_params,
                                      const void *v_codes, const void *v_params,

@@ -469,15 +469,15 @@ def paged_decode_attn_q4(q, k_cache, v_cache, block_tables, context_lens, max_co
 
 
 def q4_prefill_workspace_size(num_seqs, total_k, max_seqlen_k, num_kv_heads) -> int:
-    """Workspace bytes of paged_prefill_attn_q4 (0: invalid sizes)."""
+    """Workspace bytes of paged_prefill_attn_q4 on the current device (0: invalid sizes)."""
     return int(lib().pkv_prefill_q4_workspace_size(num_seqs, total_k, max_seqlen_k, num_kv_heads, 128))
 
 
 def new_q4_prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads, device="cuda"):
-    """A workspace of paged_prefill_attn_q4 for these sizes."""
+    """A workspace of paged_prefill_attn_q4 for these sizes on the current device."""
     need = q4_prefill_workspace_size(num_seqs, total_k, max_seqlen_k, num_kv_heads)
     if need == 0:
-        raise PkvError(PKV_ERR_INVALID_ARG, "pkv_prefill_q4_workspace_size")
+        raise PkvError(PKV_ERR_CUDA, "pkv_prefill_q4_workspace_size")
     return torch.empty(need, dtype=torch.uint8, device=device)
 
 

@@ -49,35 +49,56 @@ pkv_status check_attention(const pkv::Q4CacheArgs &c, int32_t num_q_heads, int32
 // The plan of a decode call, by the least estimated time. With a step of 32 keys
 // as the unit, an SM with 4, 8, 12 or 16 resident warps gets through 4.7, 6.4, 7.4
 // or 8 steps a microsecond (measured with 16 x 8 pairs of 16,384 keys; 16 warps
-// are the most its registers hold). A CTA for each pair costs some 2 us to start
-// and finish, which its neighbours on the SM cover in part; ranges cost the scan
-// of the lengths and the merge kernel.
+// are the most its registers hold). The first CTAs of an SM cost 5 us to start
+// and finish; later ones, which start while others run, 2.5 for each round. Ranges
+// take 2.1 us a step and warp, 9 for the scan of the lengths and the merge kernel,
+// and 11 for every pair that a warp finishes. Estimated and measured, in us, with 4
+// warps a pair, 8, 16 and by ranges:
+//     512 pairs of   640 keys   15/16    18/19    23/-     22/22
+//     128 pairs of 16,384       114/-    85/-     70/68    66/67
+//     184 pairs of 1,015        15/13    15/13    16/16    16/16
+//   4,096 pairs of   128        33/32    50/52    84/102   42/44
+//   2,400 pairs of 2,048       141/138  151/150  171/188  154/154
 // The estimate takes every sequence at the longest. Where they are not, ranges
 // stay even, and one CTA a pair may be left with most of the work: pairs of more
 // than kWarpKeys keys a warp always go by ranges.
 constexpr int32_t kStepKeys = 32, kWarpKeys = 1024;
 
-pkv::Q4DecodePlan decode_plan(int64_t num_seqs, int64_t heads, int64_t keys, int sms) {
+struct PlannedDecode {
+  pkv::Q4DecodePlan plan;
+  double us;
+};
+
+PlannedDecode decode_plan(int64_t num_seqs, int64_t heads, int64_t keys, int sms) {
   const int64_t steps = (keys + kStepKeys - 1) / kStepKeys, pairs = num_seqs * heads;
-  pkv::Q4DecodePlan best = {16, 0};
-  double best_us = 0;
+  PlannedDecode best = {{16, 0}, 0};
   for (int warps = 4; warps <= 16; warps *= 2) {
     const int64_t per_sm = (pairs + sms - 1) / sms, per_warp = (steps + warps - 1) / warps;
     const int64_t resident = std::min<int64_t>(16, per_sm * warps);
     const double rate = resident <= 4 ? 4.7 : resident <= 8 ? 6.4 : resident <= 12 ? 7.4 : 8.0;
     const double rounds = std::max(1.0, static_cast<double>(per_sm * warps) / 16);
-    const double us = per_sm * per_warp * warps / rate + 2 * rounds + (warps == 16 ? 0.8 : 0.0);
-    if (warps == 4 || us < best_us) {
-      best.warps = warps;
-      best_us = us;
+    const double work = static_cast<double>(std::max(per_warp * resident, per_sm * steps)) / rate;
+    const double us = work + 2.5 + 2.5 * rounds + (warps == 16 ? 0.8 : 0.0);
+    if (warps == 4 || us < best.us) {
+      best.plan.warps = warps;
+      best.us = us;
     }
   }
   if (num_seqs <= pkv::kQ4MaxRangeSeqs) {
-    const double per_warp = static_cast<double>(pairs * steps) / (16 * sms);
-    const double us = std::max(1.0, per_warp) * 2.0 + 7;
-    if (us < best_us || keys > kWarpKeys * best.warps) best.range_ctas = sms;
+    const int64_t warps = 16 * static_cast<int64_t>(sms), per_warp = (pairs * steps + warps - 1) / warps;
+    const double us = 2.1 * per_warp + 9 + 11.0 * pairs / warps;
+    if (us < best.us || keys > kWarpKeys * best.plan.warps) {
+      best.plan.range_ctas = sms;
+      best.us = us;
+    }
   }
   return best;
+}
+
+// Keys of the longest sequence that are read: with a window they start at the
+// 16-key boundary at or before its first one.
+int64_t window_keys(int64_t keys, int32_t window) {
+  return window > 0 ? std::min<int64_t>(keys, static_cast<int64_t>(window) + 15) : keys;
 }
 
 struct DecodeWorkspace {
@@ -100,13 +121,35 @@ DecodeWorkspace decode_workspace(int32_t num_seqs, int32_t num_q_heads, int32_t 
   return w;
 }
 
+// Prefill goes one of two ways. By rows, each query row is a decode of its own
+// over the codes: for few new tokens over many keys. Widened, the keys are made
+// bf16 once and the tensor-core prefill kernel reads them; there a (segment, two
+// query heads) is one CTA that passes all its keys, 128 in 1.4 us. Measured, in us,
+// by rows and widened: 8 segments of 8,192 keys with 1 query token each 28 and 150,
+// with 8 127 and 150, with 16 239 and 150; one of 32,768 keys with 16 tokens 124
+// and 390; 64 of 128 keys with 4 tokens 18 and 34.
+constexpr int32_t kRowsMaxQ = 64;   // query tokens a segment by rows, at most (a workspace bound)
+
+bool prefill_by_rows(int64_t num_seqs, int64_t total_q, int64_t max_q, int64_t total_k, int64_t keys, int64_t q_heads,
+                     int64_t kv_heads, int sms) {
+  if (max_q > kRowsMaxQ || total_q > std::min<int64_t>(65535, num_seqs * kRowsMaxQ)) return false;
+  const double rows_us = 2 + decode_plan(total_q, kv_heads, keys, sms).us;
+  const double widen_us = std::min<double>(total_k, static_cast<double>(num_seqs) * keys) * kv_heads * 672 / 6.2e6;
+  const int64_t ctas = num_seqs * (q_heads > kv_heads ? q_heads / 2 : q_heads);
+  const double attend_us = (ctas + sms - 1) / sms * (4 + keys / 128 * 1.4);
+  return rows_us < 4 + widen_us + attend_us;
+}
+
 struct PrefillWorkspace {
-  size_t tables, k, v, total;
+  size_t tables, k, v;               // widened
+  size_t lens, rows, o, ml;          // by rows
+  size_t total;
   int32_t max_blocks;
   int64_t num_blocks;
 };
 
-PrefillWorkspace prefill_workspace(int32_t num_seqs, int32_t total_k, int32_t max_seqlen_k, int32_t num_kv_heads) {
+PrefillWorkspace prefill_workspace(int32_t num_seqs, int32_t total_k, int32_t max_seqlen_k, int32_t num_kv_heads,
+                                   int sms) {
   constexpr int64_t B = pkv::kQ4PrefillBlock;
   PrefillWorkspace w;
   w.max_blocks = static_cast<int32_t>((static_cast<int64_t>(max_seqlen_k) + B - 1) / B);
@@ -115,7 +158,13 @@ PrefillWorkspace prefill_workspace(int32_t num_seqs, int32_t total_k, int32_t ma
   w.tables = 0;
   w.k = align_up(static_cast<size_t>(num_seqs) * w.max_blocks * sizeof(int32_t), 256);
   w.v = w.k + cache;
-  w.total = w.v + cache;
+  const size_t most_rows = align_up(static_cast<size_t>(num_seqs) * kRowsMaxQ * sizeof(int32_t), 256);
+  const size_t pieces = static_cast<size_t>(sms) * 16 * 2 * 4;  // of up to 4 query heads a KV head
+  w.lens = 0;
+  w.rows = most_rows;
+  w.o = 2 * most_rows;
+  w.ml = w.o + pieces * kD * sizeof(float);
+  w.total = std::max(w.v + cache, w.ml + pieces * 4 * sizeof(float));
   return w;
 }
 
@@ -209,10 +258,6 @@ pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const vo
       decode_workspace(num_seqs, num_q_heads, num_kv_heads, max_context_len, key_scores != nullptr, sms);
   if (workspace_bytes < w.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  // with a window, each sequence's keys start at the 16-key boundary at or
-  // before its first one
-  const int64_t keys = sliding_window > 0 ? std::min<int64_t>(max_context_len, static_cast<int64_t>(sliding_window) + 15)
-                                          : max_context_len;
   a.q = q;
   a.block_tables = block_tables;
   a.context_lens = context_lens;
@@ -229,7 +274,7 @@ pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const vo
   a.num_seqs = num_seqs;
   a.num_q_heads = num_q_heads;
   a.window = sliding_window;
-  a.plan = decode_plan(num_seqs, num_kv_heads, keys, sms);
+  a.plan = decode_plan(num_seqs, num_kv_heads, window_keys(max_context_len, sliding_window), sms).plan;
   a.scale_log2 = scale * pkv::kLog2e;
   cudaError_t e = pkv::launch_q4_decode(a, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "decode_q4 launch");
@@ -239,7 +284,9 @@ pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const vo
 size_t pkv_prefill_q4_workspace_size(int32_t num_seqs, int32_t total_k, int32_t max_seqlen_k, int32_t num_kv_heads,
                                      int32_t head_dim) {
   if (num_seqs <= 0 || total_k < 0 || max_seqlen_k < 0 || num_kv_heads <= 0 || head_dim != kD) return 0;
-  return prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads).total;
+  int sms = 0;
+  if (current_sm_count(&sms) != PKV_OK) return 0;
+  return prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads, sms).total;
 }
 
 pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const void *k_params, const void *v_codes,
@@ -262,15 +309,58 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
   if (total_q > 0 && (q == nullptr || out == nullptr)) return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
   if (!aligned16(q) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
-  const PrefillWorkspace w = prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads);
-  // workspace rows are 32-bit TMA coordinates; units of 16 keys x heads are counted in 31 bits
-  if (w.num_blocks * pkv::kQ4PrefillBlock > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-  if ((static_cast<int64_t>(max_seqlen_k) / 16 + 1) * num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-  if (workspace == nullptr || workspace_bytes < w.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace == nullptr) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+  // workspace rows are 32-bit TMA coordinates; units of 16 keys x heads are counted in 31 bits
+  if (((static_cast<int64_t>(total_k) + pkv::kQ4PrefillBlock - 1) / pkv::kQ4PrefillBlock + num_seqs) *
+          pkv::kQ4PrefillBlock > INT32_MAX)
+    return PKV_ERR_UNSUPPORTED;
+  if ((static_cast<int64_t>(max_seqlen_k) / 16 + 1) * num_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (workspace_bytes < prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads, 0).total)
+    return PKV_ERR_WORKSPACE_TOO_SMALL;  // for any device
   int sms = 0;
   if ((st = current_sm_count(&sms)) != PKV_OK) return st;
+  const PrefillWorkspace w = prefill_workspace(num_seqs, total_k, max_seqlen_k, num_kv_heads, sms);
+  if (workspace_bytes < w.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
+  if (max_seqlen_k <= pkv::kMaxContext &&
+      prefill_by_rows(num_seqs, total_q, max_seqlen_q, total_k, window_keys(max_seqlen_k, sliding_window), num_q_heads,
+                      num_kv_heads, sms)) {
+    pkv::Q4PrefillRowsArgs r = {};
+    r.cu_seqlens_q = cu_seqlens_q;
+    r.cu_seqlens_k = cu_seqlens_k;
+    r.context_lens = reinterpret_cast<int32_t *>(ws + w.lens);
+    r.table_rows = reinterpret_cast<int32_t *>(ws + w.rows);
+    r.num_seqs = num_seqs;
+    r.total_q = total_q;
+    r.total_k = total_k;
+    r.max_seqlen_q = max_seqlen_q;
+    r.max_seqlen_k = max_seqlen_k;
+    r.max_blocks = max_blocks_per_seq;
+    r.block_size = block_size;
+    cudaError_t e = pkv::launch_q4_prefill_rows(r, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prefill_q4 rows launch");
+    pkv::Q4DecodeArgs d = {};
+    d.cache = g.cache;
+    d.q = q;
+    d.block_tables = block_tables;
+    d.context_lens = r.context_lens;
+    d.table_rows = r.table_rows;
+    d.out = out;
+    d.lse = lse;
+    d.ws_o = reinterpret_cast<float *>(ws + w.o);
+    d.ws_ml = reinterpret_cast<float *>(ws + w.ml);
+    d.max_blocks = max_blocks_per_seq;
+    d.max_context_len = max_seqlen_k;
+    d.num_seqs = total_q;
+    d.num_q_heads = num_q_heads;
+    d.window = sliding_window;
+    d.plan = decode_plan(total_q, num_kv_heads, window_keys(max_seqlen_k, sliding_window), sms).plan;
+    d.scale_log2 = scale * pkv::kLog2e;
+    e = pkv::launch_q4_decode(d, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prefill_q4 rows launch");
+    return PKV_OK;
+  }
   g.cu_seqlens_q = cu_seqlens_q;
   g.cu_seqlens_k = cu_seqlens_k;
   g.block_tables = block_tables;

@@ -195,6 +195,7 @@ struct Q4DecodeArgs {
   Q4CacheArgs cache;
   const void *q;
   const int32_t *block_tables, *context_lens;
+  const int32_t *table_rows;  // table row of each sequence, or null; with it, length 0 raises nothing
   void *out;
   float *lse;             // required when key_scores is given
   float *ws_o, *ws_ml;    // split partials
@@ -206,6 +207,13 @@ struct Q4DecodeArgs {
   Q4DecodePlan plan;
   float scale_log2;
 };
+// Prefill by rows: fills context_lens and table_rows [total_q] for a decode launch.
+struct Q4PrefillRowsArgs {
+  const int32_t *cu_seqlens_q, *cu_seqlens_k;
+  int32_t *context_lens, *table_rows;
+  int32_t num_seqs, total_q, total_k, max_seqlen_q, max_seqlen_k, max_blocks, block_size;
+};
+cudaError_t launch_q4_prefill_rows(const Q4PrefillRowsArgs &a, cudaStream_t stream);
 cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream);
 cudaError_t q4_decode_error_word(uint32_t **word);
 

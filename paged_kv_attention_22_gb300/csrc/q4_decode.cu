@@ -64,6 +64,7 @@ struct Q4DecodeParams {
   const __nv_bfloat16 *q;
   const uint8_t *k_codes, *v_codes, *k_params, *v_params;
   const int32_t *block_tables, *context_lens;
+  const int32_t *table_rows;  // row of block_tables of each sequence, or null: its own index
   __nv_bfloat16 *out;
   float *lse;
   float *ws_o;     // ranges: [2 warps, G, 128] partial outputs
@@ -133,6 +134,9 @@ __device__ __forceinline__ KeyRange key_range(const Q4DecodeParams &p, int ctx) 
   r.unit0 = r.first / kUnit * kUnit;
   return r;
 }
+__device__ __forceinline__ const int32_t *table_of(const Q4DecodeParams &p, int s) {
+  return p.block_tables + static_cast<int64_t>(p.table_rows != nullptr ? p.table_rows[s] : s) * p.max_blocks;
+}
 __device__ __forceinline__ int steps_of(const KeyRange &r) { return (r.ctx - r.unit0 + kStep - 1) / kStep; }
 
 // ---- ranges: the list of steps, in (sequence, KV head, step) order
@@ -141,24 +145,35 @@ __device__ __forceinline__ int steps_of(const KeyRange &r) { return (r.ctx - r.u
 // and the lengths (0: invalid); one warp.
 __device__ __forceinline__ void build_prefix(const Q4DecodeParams &p, int64_t *prefix, int *ctx_of, bool raise,
                                              int lane) {
+  constexpr int kLoads = 8;  // lengths a lane has in flight
   int64_t carry = 0;
-  for (int base = 0; base < p.num_seqs; base += 32) {
-    const int s = base + lane;
-    int64_t n = 0;
-    if (s < p.num_seqs) {
-      const KeyRange r = key_range(p, p.context_lens[s]);
-      if (r.ctx == 0 && raise) atomicOr(&g_q4_decode_errors, kErrContext);
-      n = r.ctx > 0 ? steps_of(r) : 0;
-      if (ctx_of != nullptr) ctx_of[s] = r.ctx;
-    }
-    int64_t incl = n;
+  for (int base = 0; base < p.num_seqs; base += 32 * kLoads) {
+    int len[kLoads];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
+    for (int u = 0; u < kLoads; ++u) {
+      const int s = base + 32 * u + lane;
+      len[u] = s < p.num_seqs ? p.context_lens[s] : 0;
     }
-    if (s < p.num_seqs) prefix[s] = carry + incl - n;
-    carry += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int s = base + 32 * u + lane;
+      if (base + 32 * u >= p.num_seqs) break;
+      int64_t n = 0;
+      if (s < p.num_seqs) {
+        const KeyRange r = key_range(p, len[u]);
+        if (r.ctx == 0 && raise && p.table_rows == nullptr) atomicOr(&g_q4_decode_errors, kErrContext);
+        n = r.ctx > 0 ? steps_of(r) : 0;
+        if (ctx_of != nullptr) ctx_of[s] = r.ctx;
+      }
+      int64_t incl = n;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      if (s < p.num_seqs) prefix[s] = carry + incl - n;
+      carry += __shfl_sync(0xffffffffu, incl, 31);
+    }
   }
   if (lane == 0) prefix[p.num_seqs] = carry;
 }
@@ -215,10 +230,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
     // before the length says whether the unit exists (without a window the first
     // unit is at position 0)
     const uint32_t j = fast_quotient((warp + kWarps * (lane >> 1)) * kStep + (lane & 1) * kUnit, p.block);
-    first_entry = p.block_tables[static_cast<int64_t>(cur.s) * p.max_blocks + min(j, static_cast<uint32_t>(p.max_blocks) - 1)];
+    first_entry = table_of(p, cur.s)[min(j, static_cast<uint32_t>(p.max_blocks) - 1)];
     range = key_range(p, p.context_lens[cur.s]);
     if (range.ctx == 0) {
-      if (cur.head == 0 && threadIdx.x == 0) atomicOr(&g_q4_decode_errors, kErrContext);
+      if (cur.head == 0 && threadIdx.x == 0 && p.table_rows == nullptr) atomicOr(&g_q4_decode_errors, kErrContext);
       return;
     }
     const int n_steps = steps_of(range);
@@ -266,7 +281,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
     }
     if (key >= ctx) return kNoUnit;
     const uint32_t j = fast_quotient(key, p.block);
-    const int blk = loaded ? first_entry : p.block_tables[static_cast<int64_t>(s) * p.max_blocks + j];
+    const int blk = loaded ? first_entry : table_of(p, s)[j];
     if (blk < 0 || blk >= p.num_blocks) {
       atomicOr(&g_q4_decode_errors, kErrBlock);
       return kNoUnit;
@@ -718,6 +733,34 @@ __global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScore
   key_scores_body(p);
 }
 
+// Prefill by rows: every query row of a varlen batch becomes a sequence of its own
+// for the decode kernel, with the keys up to its position and its segment's
+// table. A row of a segment that the prefill call refuses (raising the bit), and
+// a row behind the last segment, gets length 0: it is left out.
+__global__ void __launch_bounds__(256) q4_rows_kernel(const Q4PrefillRowsArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int row = blockIdx.x * blockDim.x + threadIdx.x;
+  if (row >= a.total_q) return;
+  int lo = 0, hi = a.num_seqs - 1;  // the last segment that starts at or before the row
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.cu_seqlens_q[mid] <= row) lo = mid; else hi = mid - 1;
+  }
+  const int64_t q0 = a.cu_seqlens_q[lo], Lq = a.cu_seqlens_q[lo + 1] - q0;
+  const int64_t k0 = a.cu_seqlens_k[lo], k1 = a.cu_seqlens_k[lo + 1], Lk = k1 - k0;
+  int ctx = 0;
+  if (row >= q0 && row < q0 + Lq) {
+    if (Lq > Lk || Lq > a.max_seqlen_q || Lk > a.max_seqlen_k || k1 > a.total_k || k0 < 0 ||
+        Lk > static_cast<int64_t>(a.max_blocks) * a.block_size)
+      atomicOr(&g_q4_decode_errors, kErrSeqlens);
+    else
+      ctx = static_cast<int>(Lk - Lq + (row - q0) + 1);
+  }
+  a.context_lens[row] = ctx;
+  a.table_rows[row] = lo;
+}
+
 template <int NG, int kWarps, bool kRanges>
 cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream) {
   auto kernel = q4_decode_kernel<NG, kWarps, kRanges>;
@@ -774,6 +817,7 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
   p.v_params = static_cast<const uint8_t *>(a.cache.v_params);
   p.block_tables = a.block_tables;
   p.context_lens = a.context_lens;
+  p.table_rows = a.table_rows;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;
   p.ws_o = a.ws_o;
@@ -815,6 +859,10 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
   if (e != cudaSuccess || scores == nullptr || a.plan.range_ctas > 0) return e;
   return launch_pdl(q4_scores_kernel, dim3(key_scores_grid_x(a.max_context_len), a.num_seqs),
                     dim3(kScoreThreads), 0, stream, k);
+}
+
+cudaError_t launch_q4_prefill_rows(const Q4PrefillRowsArgs &a, cudaStream_t stream) {
+  return launch_pdl(q4_rows_kernel, dim3((a.total_q + 255) / 256), dim3(256), 0, stream, a);
 }
 
 cudaError_t q4_decode_error_word(uint32_t **word) {

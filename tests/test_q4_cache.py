@@ -128,8 +128,8 @@ def test_prefill_refuses(L):
     assert call(T=0, q=None, out=None) == pkv.PKV_OK
     assert call(S=0) == pkv.PKV_OK
     assert L.pkv_prefill_q4_workspace_size(2, 128, 64, 8, 64) == 0
-    need = L.pkv_prefill_q4_workspace_size(2, 128, 64, 8, 128)
-    assert need >= 128 * 512 * 8
+    need = L.pkv_prefill_q4_workspace_size(2, 128, 64, 8, 128)   # depends on the device's SM count
+    assert need >= 128 * 512 * 8 if torch.cuda.is_available() else need == 0
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="only meaningful without a GPU")
@@ -573,6 +573,12 @@ PREFILL = [  # q lens, k lens, heads, gqa, block, group, window
     ([130, 1], [513, 2], 1, 4, 256, 128, 0),
     ([200, 37, 300], [330, 37, 700], 2, 2, 16, 64, 100),
     ([1, 3], [600, 129], 1, 2, 32, 32, 1),
+    # few query tokens over many keys: by rows
+    ([4, 1, 0, 2], [3000, 17, 40, 1025], 2, 2, 16, 32, 0),
+    ([1], [9000], 1, 4, 64, 128, 0),
+    ([16], [5000], 2, 1, 256, 64, 0),
+    ([3, 8], [2500, 700], 2, 4, 32, 32, 300),
+    ([1] * 20, [40] * 20, 8, 2, 16, 64, 0),
 ]
 
 
@@ -629,6 +635,26 @@ def test_prefill_refuses_a_segment_past_total_k_alone(L):
     o, _ = pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu(q_lens), _cu(k_lens), bt, 30, 30, 49, SCALE)
     assert pkv.check_device_errors() & pkv.DEVERR_SEQLENS
     assert bool(((o[:20].cpu().double() - out[:20]).abs() <= tol_o[:20]).all())
+
+
+@gpu
+def test_prefill_by_rows_leaves_refused_segments_alone(L):
+    """Few tokens over many keys, one segment past total_k, one longer than the stated
+    maximum, and rows behind the last segment."""
+    q_lens, k_lens = [2, 1, 3], [2000, 1500, 1000]
+    c = Q.Cache(13, k_lens, 2, 16, 32)
+    q = torch.randn(8, 4, 128, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    out, lse, tol_o, tol_l = _prefill_plain(c, q, q_lens, 2, 0)
+    kc, vc, bt = c.cuda()
+    for total_k, max_k, good in ((4500, 2000, [0, 1, 2, 3, 4, 5]), (4499, 2000, [0, 1, 2]), (4500, 1999, [2, 3, 4, 5])):
+        o = torch.full_like(q, 9.0).cuda()
+        l = torch.full((8, 4), 9.0, device="cuda")
+        pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu(q_lens), _cu(k_lens), bt, 3, max_k, total_k, SCALE, out=o, lse=l)
+        assert pkv.check_device_errors() == (0 if len(good) == 6 else pkv.DEVERR_SEQLENS)
+        rest = [r for r in range(8) if r not in good]
+        assert bool((o[rest] == 9.0).all()) and bool((l[rest] == 9.0).all())
+        assert bool(((o[good].cpu().double() - out[good]).abs() <= tol_o[good]).all())
+        assert bool(((l[good].cpu().double() - lse[good]).abs() <= tol_l[good]).all())
 
 
 @gpu
