@@ -15,11 +15,12 @@
 // destination blocks are all fresh has no hazard: warps move whole rows, in any
 // order. With a block in both tables (in place), nothing is overwritten before
 // it has been read as long as the rows go in order: a CTA then owns a slice (up
-// to kSliceBytes) of every row and moves its rows in chunks, loading a whole
-// chunk before it stores any of it; slices are independent. Which of the two
+// to kSliceBytes) of every row and moves its rows in chunks, a whole chunk loaded
+// before any of it is stored, the next one on its way meanwhile; slices are independent. Which of the two
 // holds is found on the device, from the tables. 8 x 4,096 rows of 4 KiB: 49 us
 // fresh (268 MB, 5.5 TB/s; it waits for memory with 24 warps an SM, the lookup of
-// the next rows running ahead), 105 us in place (the chunks follow each other).
+// the next rows running ahead), 73 us in place (issue slots: every slice looks
+// all the rows up).
 // Selection: 12 us for 8 x 16,384 scores, mostly barriers between its passes.
 #include "internal.h"
 #include "ptx.cuh"
@@ -256,7 +257,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 // ---------------------------------------------------------------- compaction
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;       // pieces a thread has in flight
+constexpr int kMoveUnroll = 8;       // scores a thread has in flight
+constexpr int kRingStages = 2, kRingUnroll = 4;  // chunks in the ring; pieces of a chunk a thread
+constexpr size_t kRingBytes = static_cast<size_t>(kRingStages) * kRingUnroll * kMoveThreads * 16;
+static_assert(kRingStages * kRingUnroll <= 32, "bits of `moved`");
 constexpr int kRowsPerWarp = 4;      // rows a warp moves together, without hazards
 
 struct CompactParams {
@@ -291,41 +295,78 @@ __device__ __forceinline__ int64_t row_at(const CompactParams &p, const RowArray
     atomicOr(&g_evict_errors, kErrBlock);
     return -1;
   }
-  return (static_cast<int64_t>(blk) * a.planes * p.block.d + (pos - j * static_cast<int>(p.block.d))) * a.row_bytes;
+  return blk * a.block_bytes + static_cast<int64_t>(pos - j * static_cast<int>(p.block.d)) * a.row_bytes;
 }
 
-// Move `bytes` bytes at `at` of every kept row of one plane, N bytes a thread.
+// Move `bytes` bytes at `at` of every kept row of one plane, N bytes a piece. The
+// rows go in chunks through a ring in shared memory, kRingStages - 1 chunks ahead
+// of the stores; a piece is loaded and stored by the same thread. (Three or four
+// stages take as long as two.) A row of chunk c
+// comes from position keep[i] >= i, behind all that earlier chunks overwrite: its
+// load may run ahead of their stores. What chunk c overwrites was loaded by chunks
+// up to c, which the barrier makes sure of.
 template <int N>
-__device__ void move_slice(const CompactParams &p, const RowArray &a, int plane, int at, int bytes, int s, int n) {
+__device__ void move_slice(const CompactParams &p, const RowArray &a, int plane, int at, int bytes, int s, int n,
+                           uint4 *ring) {
   using T = typename Piece<N>::T;
   const int per_row = bytes / N;
   const int rows = kMoveThreads / per_row;  // rows a step
+  const int chunk = rows * kRingUnroll;
   const int r = threadIdx.x / per_row;
   const int32_t *keep = p.keep + static_cast<int64_t>(s) * p.budget;
   const int32_t *src = p.src_tables + static_cast<int64_t>(s) * p.src_max_blocks;
   const int32_t *dst = p.dst_tables + static_cast<int64_t>(s) * p.dst_max_blocks;
   uint8_t *base = static_cast<uint8_t *>(a.base) + static_cast<int64_t>(plane) * p.block.d * a.row_bytes + at +
                   threadIdx.x % per_row * N;
-  for (int i0 = 0; i0 < n; i0 += rows * kMoveUnroll) {
-    T x[kMoveUnroll];
-    int64_t to[kMoveUnroll];
+  const int end = r < rows ? n : 0;
+  uint32_t moved = 0;  // which pieces are on their way, kRingUnroll bits a chunk, the newest lowest
+  int next[kRingUnroll];
+  auto look_up = [&](int i0) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
+    for (int u = 0; u < kRingUnroll; ++u) {
       const int i = i0 + u * rows + r;
-      to[u] = -1;
-      if (r < rows && i < n) {
-        const int64_t from = row_at(p, a, src, p.src_max_blocks, keep[i]);
-        const int64_t into = row_at(p, a, dst, p.dst_max_blocks, i);
-        if (from >= 0 && into >= 0 && from != into) {
-          to[u] = into;
-          x[u] = *reinterpret_cast<const T *>(base + from);
+      next[u] = i < end ? keep[i] : 0;
+    }
+  };
+  auto load = [&](int i0, int stage) {
+#pragma unroll
+    for (int u = 0; u < kRingUnroll; ++u) {
+      const int i = i0 + u * rows + r;
+      moved <<= 1;
+      if (i < end) {
+        const int64_t from = row_at(p, a, src, p.src_max_blocks, next[u]);
+        bool stays = false;  // at its place already, in a block that others may share
+        if (next[u] == i) {
+          const uint32_t j = fast_quotient(i, p.block);
+          stays = from >= 0 && src[j] == dst[j];
+        }
+        if (from >= 0 && !stays) {
+          moved |= 1;
+          cp_async<N>(smem_u32(ring + (stage * kRingUnroll + u) * kMoveThreads + threadIdx.x), base + from);
         }
       }
     }
-    __syncthreads();  // the whole chunk is loaded: its places may be overwritten
+    cp_async_commit();
+    look_up(i0 + chunk);
+  };
+  look_up(0);
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (to[u] >= 0) *reinterpret_cast<T *>(base + to[u]) = x[u];
+  for (int c = 0; c < kRingStages - 1; ++c) load(c * chunk, c);
+  int stage = 0;
+  for (int i0 = 0; i0 < n; i0 += chunk) {
+    cp_async_wait<kRingStages - 2>();
+    __syncthreads();  // the whole chunk is loaded: its places may be overwritten
+    const uint32_t now = moved >> (kRingUnroll * (kRingStages - 2));
+    load(i0 + (kRingStages - 1) * chunk, stage == 0 ? kRingStages - 1 : stage - 1);
+#pragma unroll
+    for (int u = 0; u < kRingUnroll; ++u) {
+      if (now >> (kRingUnroll - 1 - u) & 1) {
+        const int64_t into = row_at(p, a, dst, p.dst_max_blocks, i0 + u * rows + r);
+        if (into >= 0) *reinterpret_cast<T *>(base + into) =
+            *reinterpret_cast<const T *>(ring + (stage * kRingUnroll + u) * kMoveThreads + threadIdx.x);
+      }
+    }
+    stage = stage == kRingStages - 1 ? 0 : stage + 1;
   }
 }
 
@@ -443,6 +484,7 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_compact_kernel(const Co
     return;
   }
   // in place: slices of all arrays in turn
+  extern __shared__ uint4 ring[];
   int first = blockIdx.x;
 #pragma unroll 1
   for (int k = 0; k < p.num_arrays; ++k) {
@@ -451,9 +493,9 @@ __global__ void __launch_bounds__(kMoveThreads, 3) evict_compact_kernel(const Co
     const int bytes = a.row_bytes / per_plane;
     for (; first < slices; first += movers) {
       const int plane = first / per_plane, at = (first - plane * per_plane) * bytes;
-      if (bytes % 16 == 0) move_slice<16>(p, a, plane, at, bytes, s, n);
-      else if (bytes % 8 == 0) move_slice<8>(p, a, plane, at, bytes, s, n);
-      else move_slice<4>(p, a, plane, at, bytes, s, n);
+      if (bytes % 16 == 0) move_slice<16>(p, a, plane, at, bytes, s, n, ring);
+      else if (bytes % 8 == 0) move_slice<8>(p, a, plane, at, bytes, s, n, ring);
+      else move_slice<4>(p, a, plane, at, bytes, s, n, ring);
     }
     first -= slices;
   }
@@ -507,12 +549,13 @@ cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream)
   int64_t row_bytes = 0;
   for (int k = 0; k < a.num_arrays; ++k) {
     p.arrays[k] = a.arrays[k];
+    p.arrays[k].block_bytes = static_cast<int64_t>(a.arrays[k].planes) * a.block_size * a.arrays[k].row_bytes;
     row_bytes += static_cast<int64_t>(a.arrays[k].planes) * a.arrays[k].row_bytes;
   }
   // in place the slices of a sequence are all that spreads it over the SMs: half
   // as wide where there are too few for four CTAs an SM (in place, one sequence of
-  // 8,192 kept rows of 4 KiB takes 48 us with 32 bytes and 83 with 64; 64 of 512
-  // rows 93 and 78)
+  // 8,192 kept rows of 4 KiB takes 37 us with 32 bytes and 52 with 64; 64 of 512
+  // rows 80 and 67)
   p.slice_bytes = a.num_seqs * (row_bytes / kSliceBytes) < 4 * static_cast<int64_t>(a.num_sms) ? kSliceBytes / 2 : kSliceBytes;
   int64_t slices = 0;
   for (int k = 0; k < a.num_arrays; ++k)
@@ -538,8 +581,11 @@ cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream)
   int64_t movers = slices > rows ? slices : rows;
   const int64_t cap = (8 * static_cast<int64_t>(a.num_sms) + a.num_seqs - 1) / a.num_seqs;
   if (movers > cap) movers = cap;
+  cudaError_t e = cudaFuncSetAttribute(evict_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kRingBytes));
+  if (e != cudaSuccess) return e;
   return launch_pdl(evict_compact_kernel, dim3(static_cast<unsigned>(movers + (a.key_scores != nullptr ? 1 : 0)), a.num_seqs),
-                    dim3(kMoveThreads), 0, stream, p);
+                    dim3(kMoveThreads), kRingBytes, stream, p);
 }
 
 cudaError_t evict_error_word(uint32_t **word) {

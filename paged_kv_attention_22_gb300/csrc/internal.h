@@ -231,6 +231,7 @@ cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t stream);
 struct RowArray {
   void *base;
   int32_t planes, row_bytes;
+  int64_t block_bytes;  // of all planes; set by the launch
 };
 constexpr int kMaxRowArrays = 4;
 constexpr int kSliceBytes = 64;  // bytes of a row that one CTA of an in-place compaction moves, at most

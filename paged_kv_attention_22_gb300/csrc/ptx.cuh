@@ -364,6 +364,23 @@ __device__ __forceinline__ void setmaxnreg_inc() {
 
 // ---------------------------------------------------------------- dependent launch
 
+// Asynchronous copies of a thread's own (16, 8 or 4 bytes, aligned to their size).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+  if constexpr (N == 16)
+    cp_async16(dst, src);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Programmatic dependent launch: a kernel launched with programmatic stream
 // serialization may start before the previous kernel on its stream ends.
 // griddep_wait blocks until that kernel has completed and its writes are

@@ -88,22 +88,6 @@ struct Q4DecodeSmem {
   static constexpr int kTotal = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
-  if constexpr (N == 16)
-    cp_async16(dst, src);
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // d += a b, bf16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -321,7 +305,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
         cp_async16(st + 512 + lane * 16, k + 512);
         cp_async16(st + v_dst, v);
         cp_async16(st + v_dst + 512, v + 512);
-        cp_async_small<4 * NG>(st + 2 * kUnitCodes + lane * (4 * NG),
+        cp_async<4 * NG>(st + 2 * kUnitCodes + lane * (4 * NG),
                                p_src + static_cast<int64_t>(row16) * L::kParamBytes);
       }
     }
