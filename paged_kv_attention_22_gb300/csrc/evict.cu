@@ -5,10 +5,10 @@
 // Selection. One CTA, or a cluster of eight for long sequences, finds the
 // want-th largest score with a radix select over the scores' order-preserving
 // 32-bit keys, eight bits a pass (the keys stay in shared memory while they fit),
-// until the bin that holds it is taken whole. It then writes the kept positions in ascending order: each warp
-// owns a contiguous range of positions, counts the keys above and at the
-// threshold, and after one scan over the warps writes its own with ballots. Equal
-// scores are taken from the lowest position on.
+// until the bin that holds it is taken whole. It then writes the kept positions
+// in ascending order: each warp owns a contiguous range of positions, counts the
+// keys above and at the threshold, and after one scan over the warps writes its
+// own with ballots. Equal scores are taken from the lowest position on.
 //
 // Compaction, bound by HBM bandwidth: every kept row is read and written once.
 // Row i of the destination is row keep[i] >= i of the source. A sequence whose
@@ -16,11 +16,11 @@
 // order. With a block in both tables (in place), nothing is overwritten before
 // it has been read as long as the rows go in order: a CTA then owns a slice (up
 // to kSliceBytes) of every row and moves its rows in chunks, a whole chunk loaded
-// before any of it is stored, the next one on its way meanwhile; slices are independent. Which of the two
-// holds is found on the device, from the tables. 8 x 4,096 rows of 4 KiB: 49 us
-// fresh (268 MB, 5.5 TB/s; it waits for memory with 24 warps an SM, the lookup of
-// the next rows running ahead), 73 us in place (issue slots: every slice looks
-// all the rows up).
+// before any of it is stored, the next one on its way meanwhile; slices are
+// independent. Which of the two holds is found on the device, from the tables.
+// 8 x 4,096 rows of 4 KiB: 49 us fresh (268 MB, 5.5 TB/s; it waits for memory with
+// 24 warps an SM, the lookup of the next rows running ahead), 73 us in place
+// (issue slots: every slice looks all the rows up).
 // Selection: 12 us for 8 x 16,384 scores, mostly barriers between its passes.
 #include "internal.h"
 #include "ptx.cuh"
@@ -261,6 +261,7 @@ constexpr int kMoveUnroll = 8;       // scores a thread has in flight
 constexpr int kRingStages = 2, kRingUnroll = 4;  // chunks in the ring; pieces of a chunk a thread
 constexpr size_t kRingBytes = static_cast<size_t>(kRingStages) * kRingUnroll * kMoveThreads * 16;
 static_assert(kRingStages * kRingUnroll <= 32, "bits of `moved`");
+static_assert(kRingBytes <= 48 * 1024, "no attribute needed");
 constexpr int kRowsPerWarp = 4;      // rows a warp moves together, without hazards
 
 struct CompactParams {
@@ -581,9 +582,6 @@ cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream)
   int64_t movers = slices > rows ? slices : rows;
   const int64_t cap = (8 * static_cast<int64_t>(a.num_sms) + a.num_seqs - 1) / a.num_seqs;
   if (movers > cap) movers = cap;
-  cudaError_t e = cudaFuncSetAttribute(evict_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kRingBytes));
-  if (e != cudaSuccess) return e;
   return launch_pdl(evict_compact_kernel, dim3(static_cast<unsigned>(movers + (a.key_scores != nullptr ? 1 : 0)), a.num_seqs),
                     dim3(kMoveThreads), kRingBytes, stream, p);
 }

@@ -1,7 +1,8 @@
 // Accumulated attention weights: after a decode call has left its logits
 // z[s, h, p] (base 2, scaled) and lse[s, h] (natural log),
 //   key_scores[s, p] += sum_h 2^(z[s, h, p] - lse[s, h] log2 e)
-// for every key p that sequence s attended to. The sum runs over the heads in
+// for every key p that sequence s attended to; a logit of -inf has weight 0, also
+// where the whole row is such (lse -inf). The sum runs over the heads in
 // order, so the result does not depend on the launch shape.
 #pragma once
 
@@ -35,8 +36,10 @@ __device__ __forceinline__ void add_key_scores(const KeyScoresParams &p, int s, 
     const float *z = p.logits + static_cast<int64_t>(s) * p.num_q_heads * p.logits_ld + pos;
     float w = 0.f;
 #pragma unroll 8
-    for (int h = 0; h < p.num_q_heads; ++h)
-      w += fast_exp2(fmaf(-kScoreLog2e, lse[h], z[h * p.logits_ld]));
+    for (int h = 0; h < p.num_q_heads; ++h) {
+      const float x = z[h * p.logits_ld];
+      w += x == -INFINITY ? 0.f : fast_exp2(fmaf(-kScoreLog2e, lse[h], x));
+    }
     p.key_scores[s * p.score_stride + pos] += w;
   }
 }

@@ -36,7 +36,7 @@
 // What bounds it: widening the codes, a shift, a logic operation and a packed fma
 // for two values, some 420 of the 680 instructions of a step. Shifts and logic
 // share one half-rate pipe and packed fmas have another. 16 sequences of 16,384
-// keys, 8 KV heads, 2 query heads each: 65.6 us, 336 MB at 5.1 TB/s; issue slots
+// keys, 8 KV heads, 2 query heads each: 67 us, 336 MB at 5.0 TB/s; issue slots
 // 62 % used, the shift and logic pipe 57 %. (Without the widening the same loop
 // streams at 6.3 TB/s; a step of 16 keys, or 20 or 24 warps an SM with fewer
 // registers, took 71 to 78 us.) 64 sequences of 640 keys: 15.7 us.
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
         cp_async16(st + v_dst, v);
         cp_async16(st + v_dst + 512, v + 512);
         cp_async<4 * NG>(st + 2 * kUnitCodes + lane * (4 * NG),
-                               p_src + static_cast<int64_t>(row16) * L::kParamBytes);
+                         p_src + static_cast<int64_t>(row16) * L::kParamBytes);
       }
     }
     cp_async_commit();
@@ -400,12 +400,13 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
       float *dst = p.logits + (static_cast<int64_t>(cur.s) * p.num_q_heads + cur.head * G + 2 * t) * p.logits_ld + key0 + kperm;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if (!((units >> u) & 1u)) continue;
+        if (key0 + u * kUnit >= range.ctx) continue;
+        const bool is = (units >> u) & 1u;  // no such block: left out
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (2 * t + c >= G) continue;
-          dst[c * p.logits_ld + u * kUnit] = z[u][c] * p.scale_log2;
-          dst[c * p.logits_ld + u * kUnit + 8] = z[u][2 + c] * p.scale_log2;
+          dst[c * p.logits_ld + u * kUnit] = is ? z[u][c] * p.scale_log2 : -INFINITY;
+          dst[c * p.logits_ld + u * kUnit + 8] = is ? z[u][2 + c] * p.scale_log2 : -INFINITY;
         }
       }
     }

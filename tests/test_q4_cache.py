@@ -447,6 +447,34 @@ def test_decode_skips_invalid_rows_and_reports_them(L):
 
 
 @gpu
+@pytest.mark.parametrize("ctx,block", [(40, 16), (20000, 64)])  # a CTA for each pair, ranges
+def test_decode_leaves_keys_of_bad_table_entries_out(L, ctx, block):
+    """Sequence 0 has one bad entry, sequence 1 nothing but bad ones, whatever an
+    earlier call left in the workspace."""
+    c = Q.Cache(11, [ctx, ctx], 1, block, 32)
+    q = torch.randn(2, 2, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    kc, vc, bt = c.cuda()
+    bt[0, 1] = c.num_blocks
+    bt[1] = -1
+    ws = pkv.new_q4_decode_workspace(2, 2, 1, ctx, True).fill_(255)    # NaNs
+    scores = torch.full((2, ctx), 0.5, device="cuda")
+    cl = torch.full((2,), ctx, dtype=torch.int32, device="cuda")
+    out, lse = pkv.paged_decode_attn_q4(q.cuda(), kc, vc, bt, cl, ctx, SCALE, workspace=ws, key_scores=scores)
+    assert pkv.check_device_errors() == pkv.DEVERR_BLOCK
+    rest = torch.cat([torch.arange(block), torch.arange(2 * block, ctx)])
+    ks, vs = c.logical(c.k, 0, ctx, 0)[rest], c.logical(c.v, 0, ctx, 0)[rest]
+    o, l, w, wv, qk = Q.attend(q[0].double(), ks, vs, SCALE, [0, 0], [len(rest) - 1] * 2)
+    assert bool(((out[0].cpu().double() - o).abs() <= Q.out_tolerance(o, wv)).all())
+    tol_l = Q.lse_tolerance(l, qk, ctx / 4)
+    assert bool(((lse[0].cpu().double() - l).abs() <= tol_l).all())
+    got = scores.cpu().double()
+    assert bool((got[0, block:2 * block] == 0.5).all()) and bool((got[1] == 0.5).all())
+    # exp(z - lse): both within the lse's tolerance; the additions round
+    tol = (w * (2 * tol_l[:, None] + 2.0 ** -20)).sum(0) + 2 * Q.U32 * (0.5 + w.sum(0))
+    assert bool(((got[0, rest] - 0.5 - w.sum(0)).abs() <= tol).all())
+
+
+@gpu
 def test_decode_nan_group_reaches_its_sequence_only(L):
     c = Q.Cache(6, [33, 33], 1, 16, 32)
     b, o = int(c.tables[0, 1]), 4
