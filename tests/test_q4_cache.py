@@ -686,6 +686,55 @@ def test_prefill_by_rows_leaves_refused_segments_alone(L):
 
 
 @gpu
+@pytest.mark.parametrize("total,bound", [(12, 3000), (600, 400)])  # by rows, widened
+def test_prefill_in_a_graph_replayed_for_other_segments(L, total, bound):
+    """Captured with bounds; replayed for batches cut up differently, with padding
+    rows and empty segments, on a stream of its own: the eager call's bits."""
+    batches = {12: [([4, 4, 4], [3000, 100, 700]), ([1, 0, 11], [1, 0, 2500]), ([0, 0, 5], [0, 9, 5])],
+               600: [([200, 200, 200], [400, 300, 200]), ([400, 0, 150], [400, 0, 151]), ([1, 2, 3], [400, 2, 400])]}[total]
+    heads, gqa, block = 2, 2, 32
+    c = Q.Cache(12, [bound] * 3, heads, block, 64)
+    kc, vc, bt = c.cuda()
+    q = torch.randn(total, heads * gqa, 128, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    cu_q, cu_k = _cu(batches[0][0]), _cu(batches[0][1])
+    total_k = 3 * bound
+    ws = pkv.new_q4_prefill_workspace(3, total_k, bound, heads)
+    out, lse = torch.zeros_like(q), torch.zeros(total, heads * gqa, device="cuda")
+
+    def call(stream=None, o=out, l=lse):
+        pkv.paged_prefill_attn_q4(q, kc, vc, cu_q, cu_k, bt, min(total, bound), bound, total_k, SCALE, out=o, lse=l, workspace=ws,
+                                  stream=stream)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        call(side)
+        with torch.cuda.graph(graph, stream=side):
+            call(side)
+    torch.cuda.synchronize()
+    for q_lens, k_lens in batches:
+        cu_q.copy_(_cu(q_lens))
+        cu_k.copy_(_cu(k_lens))
+        out.fill_(7)
+        lse.fill_(7)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        got, got_l, n = out.clone(), lse.clone(), sum(q_lens)
+        c.lens = k_lens
+        want, want_l, tol_o, tol_l = _prefill_plain(c, q.cpu()[:n], q_lens, gqa, 0)
+        assert bool(((got[:n].cpu().double() - want).abs() <= tol_o).all())
+        assert bool(((got_l[:n].cpu().double() - want_l).abs() <= tol_l).all())
+        assert bool((got[n:] == 7).all()) and bool((got_l[n:] == 7).all())     # rows behind the last segment
+        eager, eager_l = torch.full_like(out, 7), torch.full_like(lse, 7)
+        call(None, eager, eager_l)
+        assert torch.equal(eager, got) and torch.equal(eager_l, got_l)
+    assert pkv.check_device_errors() == 0
+
+
+@gpu
 def test_prefill_equals_the_bf16_call_on_the_same_values(L):
     """The values are bf16 by definition: widening the cache by hand and calling
     the bf16 prefill gives the same bits."""
