@@ -55,7 +55,7 @@ pkv_status check_attention(const pkv::Q4CacheArgs &c, int32_t num_q_heads, int32
 // and 11 for every pair that a warp finishes. Estimated and measured, in us, with 4
 // warps a pair, 8, 16 and by ranges:
 //     512 pairs of   640 keys   15/16    18/19    23/-     22/22
-//     128 pairs of 16,384       114/-    85/-     70/68    66/67
+//     128 pairs of 16,384       114/-    85/-     70/68    66/66
 //     184 pairs of 1,015        15/13    15/13    16/16    16/16
 //   4,096 pairs of   128        33/32    50/52    84/102   42/44
 //   2,400 pairs of 2,048       141/138  151/150  171/188  154/154

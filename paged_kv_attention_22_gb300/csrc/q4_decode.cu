@@ -13,7 +13,7 @@
 //            warps leaves one partial result each in the workspace (a warp's
 //            first piece in slot 2w, its last in slot 2w + 1), joined by a
 //            second kernel: the way for few or unequal pairs. (Splits of fixed
-//            length in CTAs of their own took 68 us where ranges take 66.7;
+//            length in CTAs of their own took 68 us where ranges take 65.9;
 //            joined in clusters through distributed shared memory, 73.)
 //
 // The products run on mma.sync m16n8k16 in bf16 with fp32 accumulators. A bf16
@@ -36,7 +36,7 @@
 // What bounds it: widening the codes, a shift, a logic operation and a packed fma
 // for two values, some 420 of the 680 instructions of a step. Shifts and logic
 // share one half-rate pipe and packed fmas have another. 16 sequences of 16,384
-// keys, 8 KV heads, 2 query heads each: 67 us, 336 MB at 5.0 TB/s; issue slots
+// keys, 8 KV heads, 2 query heads each: 65.9 us, 336 MB at 5.1 TB/s; issue slots
 // 62 % used, the shift and logic pipe 57 %. (Without the widening the same loop
 // streams at 6.3 TB/s; a step of 16 keys, or 20 or 24 warps an SM with fewer
 // registers, took 71 to 78 us.) 64 sequences of 640 keys: 15.7 us.
@@ -56,6 +56,7 @@ constexpr int kStep = 2 * kUnit;             // keys a step
 constexpr int kStages = 2;                   // steps in a warp's ring
 constexpr int kMaxG = 8;                     // query heads a KV head (columns of a P^T tile)
 constexpr int kUnitCodes = kUnit * kQ4RowBytes;  // 1 KiB of K or V codes
+constexpr int kQueryBytes = 32 * 64;         // a warp's query fragments, where they are in shared memory
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1.7e38f;           // below every logit; differences stay finite
 constexpr float kLazyMax = 8.0f;             // log2 units the running max may lag
@@ -190,8 +191,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.gqa;
-  // ranges: the list of steps, behind the rings
-  [[maybe_unused]] int64_t *prefix = reinterpret_cast<int64_t *>(smem + L::kTotal);
+  // ranges: the warps' queries and the list of steps, behind the rings
+  [[maybe_unused]] int64_t *prefix = reinterpret_cast<int64_t *>(smem + L::kTotal + kWarps * kQueryBytes);
   [[maybe_unused]] int *ctx_of = reinterpret_cast<int *>(prefix + p.num_seqs + 1);
   [[maybe_unused]] int64_t first_step = 0;  // this warp's range starts there
   Step cur = {static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x), 0};
@@ -225,8 +226,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   }
 
   // the pair's query heads as B fragments: k-step 2w (2w + 1) pairs dims i and
-  // i + 4, i = 0, 1 (2, 3), of the lane's w-th code word
-  uint32_t qb[8][2];
+  // i + 4, i = 0, 1 (2, 3), of the lane's w-th code word. Ranges keep them in shared
+  // memory (each lane its own, read back for every unit), where their 16 registers
+  // go to the cursor (16 x 16,384 keys 67.8 us in registers, 65.9 so)
+  [[maybe_unused]] uint32_t qb[8][2];
+  [[maybe_unused]] uint4 *sq = reinterpret_cast<uint4 *>(smem + L::kTotal) + warp * 4 * 32 + lane;
   auto load_q = [&]() {
     const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + cur.head * G + g;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * kD + 32 * t);
@@ -237,10 +241,16 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
       x.y ^= p.q_signs;
       x.z ^= p.q_signs;
       x.w ^= p.q_signs;
-      qb[2 * w][0] = q4_low_halves(x.x, x.z);
-      qb[2 * w][1] = q4_high_halves(x.x, x.z);
-      qb[2 * w + 1][0] = q4_low_halves(x.y, x.w);
-      qb[2 * w + 1][1] = q4_high_halves(x.y, x.w);
+      const uint4 y = make_uint4(q4_low_halves(x.x, x.z), q4_high_halves(x.x, x.z), q4_low_halves(x.y, x.w),
+                                 q4_high_halves(x.y, x.w));
+      if constexpr (kRanges) {
+        sq[w * 32] = y;
+      } else {
+        qb[2 * w][0] = y.x;
+        qb[2 * w][1] = y.y;
+        qb[2 * w + 1][0] = y.z;
+        qb[2 * w + 1][1] = y.w;
+      }
     }
   };
   load_q();
@@ -380,8 +390,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[j][i] = fma_bf16x2(x[j][i], s2[j], b2[j]);
         }
-        mma_16816(sc[0], x[0][0], x[1][0], x[0][1], x[1][1], qb[2 * w][0], qb[2 * w][1]);
-        mma_16816(sc[1], x[0][2], x[1][2], x[0][3], x[1][3], qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        uint4 y;
+        if constexpr (kRanges) y = sq[w * 32];
+        else y = make_uint4(qb[2 * w][0], qb[2 * w][1], qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        mma_16816(sc[0], x[0][0], x[1][0], x[0][1], x[1][1], y.x, y.y);
+        mma_16816(sc[1], x[0][2], x[1][2], x[0][3], x[1][3], y.z, y.w);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) z[u][i] = sc[0][i] + sc[1][i];
@@ -750,7 +763,7 @@ template <int NG, int kWarps, bool kRanges>
 cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream) {
   auto kernel = q4_decode_kernel<NG, kWarps, kRanges>;
   int smem = Q4DecodeSmem<NG, kWarps>::kTotal;
-  if (kRanges) smem += static_cast<int>(sizeof(int64_t)) * (p.num_seqs + 1) + static_cast<int>(sizeof(int)) * p.num_seqs;
+  if (kRanges) smem += kWarps * kQueryBytes + static_cast<int>(sizeof(int64_t)) * (p.num_seqs + 1) + static_cast<int>(sizeof(int)) * p.num_seqs;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -762,7 +775,7 @@ cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream
 template <int NG>
 cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, const KeyScoresParams *k,
                         cudaStream_t stream) {
-  static_assert(Q4DecodeSmem<NG, 16>::kTotal + 12 * kQ4MaxRangeSeqs + 8 <= 227 * 1024, "shared memory of the ranges");
+  static_assert(Q4DecodeSmem<NG, 16>::kTotal + 16 * kQueryBytes + 12 * kQ4MaxRangeSeqs + 8 <= 227 * 1024, "shared memory of the ranges");
   const dim3 pairs(p.num_kv_heads, p.num_seqs);
   if (plan.range_ctas > 0) {
     cudaError_t e = launch_shape<NG, 16, true>(p, dim3(plan.range_ctas), stream);
