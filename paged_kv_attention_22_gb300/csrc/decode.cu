@@ -828,12 +828,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
   }
 }
 
-// One position a thread; after a timeout the logits are stale: nothing is added.
+constexpr int kScoreVec = 4;  // positions a thread (two take as long, within 1 %)
+
+// After a timeout the logits are stale: nothing is added.
 __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(const KeyScoresParams p) {
   griddep_wait();
   griddep_launch_dependents();
   if (*reinterpret_cast<volatile uint32_t *>(&g_decode_errors) & kErrTimeout) return;
-  key_scores_body(p);
+  key_scores_body<kScoreVec>(p);
 }
 
 template <int G, int HGM, int NS, bool kLogits = false>
@@ -930,7 +932,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map,
   k.num_q_heads = a.num_q_heads;
   k.window = a.window;
   k.ctx_cap = static_cast<int64_t>(a.max_blocks) * a.block_size;
-  return launch_pdl(decode_scores_kernel, dim3(key_scores_grid_x(a.max_context_len), a.num_seqs),
+  return launch_pdl(decode_scores_kernel, dim3(key_scores_grid_x(a.max_context_len, kScoreVec), a.num_seqs),
                     dim3(kScoreThreads), 0, stream, k);
 }
 

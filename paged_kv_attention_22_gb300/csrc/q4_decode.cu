@@ -609,8 +609,8 @@ __device__ __forceinline__ Pieces pieces_of(const Q4DecodeParams &p, const int64
 
 // With accumulated weights the launch's first `score_ctas` CTAs (chunks of each
 // sequence's positions) add them, beside the CTAs that merge: they take the
-// lse from the pieces themselves, a warp a head, and need not wait for the merge.
-template <int kPerRow>
+// lse from the pieces themselves, half a warp a head, and need not wait for the merge.
+template <int kPerRow, int kVec>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     q4_merge_kernel(const Q4DecodeParams p, int32_t decode_warps, const KeyScoresParams k, int32_t score_ctas,
                     int32_t score_chunks) {
@@ -627,29 +627,31 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (static_cast<int>(blockIdx.x) < score_ctas) {
     float *lse = reinterpret_cast<float *>(merge_prefix + p.num_seqs + 1);
     const int s = blockIdx.x / score_chunks, chunk = blockIdx.x - s * score_chunks;
-    for (int hq = warp; hq < p.num_q_heads; hq += kMergeWarps) {
-      const Pieces c = pieces_of(p, merge_prefix, W, U, s, hq / p.gqa);
-      if (c.n <= 1) {  // written whole by the decode kernel (or an invalid length)
-        if (lane == 0 && c.n == 1) lse[hq] = p.lse[static_cast<int64_t>(s) * p.num_q_heads + hq];
-        continue;
-      }
-      float M = kFloor, l = 0.f;
-      for (int64_t i = lane; i < c.n; i += 32) {
-        const float4 ml = p.ws_ml[(i == 0 ? c.slot : 2 * (c.first + i)) * p.gqa + hq % p.gqa];
-        const float m_new = fmaxf(M, ml.x);
-        l = fmaf(l, fast_exp2(M - m_new), ml.y * fast_exp2(ml.x - m_new));
-        M = m_new;
-      }
-      float top = M;
+    add_key_scores<kVec>(k, s, chunk, score_chunks, [&]() -> const float * {
+      const int half = lane & 15;
+      for (int h0 = 2 * warp; h0 < p.num_q_heads; h0 += 2 * kMergeWarps) {
+        const int hq = h0 + (lane >> 4);
+        const Pieces c = hq < p.num_q_heads ? pieces_of(p, merge_prefix, W, U, s, hq / p.gqa) : Pieces{0, 0, 0};
+        float M = kFloor, l = 0.f;
+        for (int64_t i = half; i < (c.n > 1 ? c.n : 0); i += 16) {
+          const float4 ml = p.ws_ml[(i == 0 ? c.slot : 2 * (c.first + i)) * p.gqa + hq % p.gqa];
+          const float m_new = fmaxf(M, ml.x);
+          l = fmaf(l, fast_exp2(M - m_new), ml.y * fast_exp2(ml.x - m_new));
+          M = m_new;
+        }
+        float top = M;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      l *= fast_exp2(M - top);
+        for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        l *= fast_exp2(M - top);
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-      if (lane == 0) lse[hq] = (top + log2f(l)) * kLn2;
-    }
-    __syncthreads();
-    add_key_scores(k, s, chunk, score_chunks, lse);
+        for (int off = 8; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        // one piece: written whole by the decode kernel (none: an invalid length)
+        if (half == 0 && c.n > 0)
+          lse[hq] = c.n == 1 ? p.lse[static_cast<int64_t>(s) * p.num_q_heads + hq] : (top + log2f(l)) * kLn2;
+      }
+      __syncthreads();
+      return lse;
+    });
     return;
   }
   const int64_t row = static_cast<int64_t>(blockIdx.x - score_ctas) * (kMergeWarps / kPerRow) + warp / kPerRow;
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 __global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScoresParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  key_scores_body(p);
+  key_scores_body<2>(p);
 }
 
 // Prefill by rows: every query row of a varlen batch becomes a sequence of its own
@@ -785,9 +787,19 @@ cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, const
     // many pieces a pair: as many warps a row as a CTA has
     const bool many = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * 16 < warps;
     const int64_t ctas = many ? rows : (rows + kMergeWarps - 1) / kMergeWarps;
-    const int64_t chunks = k != nullptr ? key_scores_grid_x(p.max_context_len) : 0;
+    // scoring CTAs: two positions a thread if all the CTAs then run at once (two an
+    // SM), else four. With 16 heads: 8 sequences of 8,193 keys 28.1 and 28.8 us, 16 of
+    // them 46.0 and 44.1
+    int64_t chunks = 0;
+    bool pairs_of = true;
+    if (k != nullptr) {
+      chunks = key_scores_grid_x(p.max_context_len, 2);
+      pairs_of = ctas + chunks * p.num_seqs <= 2 * plan.range_ctas;
+      if (!pairs_of) chunks = key_scores_grid_x(p.max_context_len, 4);
+    }
     const size_t smem = sizeof(int64_t) * (p.num_seqs + 1) + (k != nullptr ? sizeof(float) * p.num_q_heads : 0);
-    const auto kernel = many ? q4_merge_kernel<kMergeWarps> : q4_merge_kernel<1>;
+    const auto kernel = many ? (pairs_of ? q4_merge_kernel<kMergeWarps, 2> : q4_merge_kernel<kMergeWarps, 4>)
+                             : (pairs_of ? q4_merge_kernel<1, 2> : q4_merge_kernel<1, 4>);
     if (smem > 40 * 1024) {  // beside the static arrays
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
       if (e != cudaSuccess) return e;
@@ -855,7 +867,7 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || scores == nullptr || a.plan.range_ctas > 0) return e;
-  return launch_pdl(q4_scores_kernel, dim3(key_scores_grid_x(a.max_context_len), a.num_seqs),
+  return launch_pdl(q4_scores_kernel, dim3(key_scores_grid_x(a.max_context_len, 2), a.num_seqs),
                     dim3(kScoreThreads), 0, stream, k);
 }
 
