@@ -37,8 +37,8 @@
 //
 //   Accumulated weights. With kLogits each consumer warp also leaves its units'
 //   logits in the workspace (4 bytes per key and query head, beside 512 bytes
-//   of K and V per key and KV head), and a kernel behind the merge turns them
-//   into weights: K is not read a second time.
+//   of K and V per key and KV head), and CTAs beside the merge turn them into
+//   weights: K is not read a second time.
 //
 // The 2-wide GQA group makes the logits and P.V skinny matrix-vector products,
 // so the kernel is bound by HBM bandwidth, not by any tensor-core contraction.
@@ -677,9 +677,24 @@ __device__ __forceinline__ void build_prefix(const DecodeParams &p, int *prefix,
 // CTA c of the decode kernel stored its first piece in slot 2c, its last in
 // slot 2c+1; the pair's first CTA holds its piece in its last slot unless its
 // range starts at the pair's first unit.
-template <int G>
-__global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const DecodeParams p, int32_t decode_grid) {
-  extern __shared__ int merge_prefix[];
+//
+// With accumulated weights (kScored; kMergeWarps warps) the launch's first CTAs,
+// score_chunks for each sequence, add them beside the CTAs that merge: they take the
+// lse of pairs that were cut from the pieces themselves, half a warp a head. (In a
+// kernel of their own behind the merge: 64 x 640 keys 35.7 us, 33.9 so.) After a timeout
+// the logits are stale, and nothing is added.
+struct ScoredMerge {
+  KeyScoresParams k;
+  int32_t score_ctas, score_chunks;
+  int32_t merge_warps;  // of a CTA that merges; the others leave
+};
+constexpr int kScoreVec = 4;  // positions a thread (two take as long, within 1 %)
+static_assert(kMergeWarps * 32 == kScoreThreads, "a CTA of the merge's launch may be a scoring one");
+
+template <int G, bool kScored>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    decode_merge_kernel(const DecodeParams p, int32_t decode_grid, const ScoredMerge scored) {
+  extern __shared__ int merge_prefix[];  // [S + 1], then the lse of a scoring CTA's sequence [H_q]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // The partition depends on context lengths only, which the decode kernel
   // before this one does not write, and every kernel before that one has
@@ -697,10 +712,48 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
   // earlier launch, which made that kernel skip its work) the partials are
   // stale: write nothing, as the decode kernel did not
   if (*reinterpret_cast<volatile uint32_t *>(&g_decode_errors) & kErrTimeout) return;
+  int cta = static_cast<int>(blockIdx.x), n_ctas = static_cast<int>(gridDim.x);
+  if constexpr (kScored) {
+    if (cta < scored.score_ctas) {
+      float *lse = reinterpret_cast<float *>(merge_prefix + p.num_seqs + 1);
+      const int s = cta / scored.score_chunks, chunk = cta - s * scored.score_chunks;
+      add_key_scores<kScoreVec>(scored.k, s, chunk, scored.score_chunks, [&]() -> const float * {
+        const int nch = chunks_of(merge_prefix, s), half = lane & 15;
+        for (int h0 = 2 * warp; nch > 0 && h0 < p.num_q_heads; h0 += 2 * kMergeWarps) {
+          const int hq = h0 + (lane >> 4), kvh = hq / G, h = hq % G;
+          const int64_t P0 = static_cast<int64_t>(n_groups) * merge_prefix[s] + static_cast<int64_t>(kvh / HG) * nch;
+          const int64_t wa = owner_of(P0, W, U);
+          const int64_t n = hq < p.num_q_heads ? owner_of(P0 + nch - 1, W, U) - wa + 1 : 0;
+          const int64_t wa_slot = 2 * wa + (range_start(wa, W, U) < P0 ? 1 : 0);
+          float M = -1.7e38f, l = 0.f;  // finite, below every logit
+          for (int64_t x = half; x < (n > 1 ? n : 0); x += 16) {
+            const int64_t i = ((x == 0 ? wa_slot : 2 * (wa + x)) * HG + kvh % HG) * G + h;
+            const float m = p.ws_ml[i * 2], m_new = fmaxf(M, m);
+            l = fmaf(l, fast_exp2(M - m_new), p.ws_ml[i * 2 + 1] * fast_exp2(m - m_new));
+            M = m_new;
+          }
+          float top = M;
+#pragma unroll
+          for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+          l *= fast_exp2(M - top);
+#pragma unroll
+          for (int off = 8; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+          if (half == 0 && n > 0)
+            lse[hq] = n == 1 ? p.lse[static_cast<int64_t>(s) * p.num_q_heads + hq] : (top + log2f(l)) * kLn2;
+        }
+        __syncthreads();
+        return lse;
+      });
+      return;
+    }
+    cta -= scored.score_ctas;
+    n_ctas -= scored.score_ctas;
+    if (warp >= scored.merge_warps) return;
+  }
   const int64_t n_pairs = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
-  const int n_warps = static_cast<int>(blockDim.x >> 5);
-  for (int64_t pi = static_cast<int64_t>(blockIdx.x) * n_warps + warp; pi < n_pairs;
-       pi += static_cast<int64_t>(gridDim.x) * n_warps) {
+  const int n_warps = kScored ? scored.merge_warps : static_cast<int>(blockDim.x >> 5);
+  for (int64_t pi = static_cast<int64_t>(cta) * n_warps + warp; pi < n_pairs;
+       pi += static_cast<int64_t>(n_ctas) * n_warps) {
     const int s = static_cast<int>(pi / p.num_kv_heads), kvh = static_cast<int>(pi % p.num_kv_heads);
     const int hg = kvh / HG, g = kvh % HG;
     const int nch = chunks_of(merge_prefix, s);
@@ -828,14 +881,27 @@ __global__ void __launch_bounds__(kMergeWarps * 32) decode_merge_kernel(const De
   }
 }
 
-constexpr int kScoreVec = 4;  // positions a thread (two take as long, within 1 %)
-
-// After a timeout the logits are stale: nothing is added.
+// The weights behind the merge, where the heads' lse would not fit beside it.
 __global__ void __launch_bounds__(kScoreThreads) decode_scores_kernel(const KeyScoresParams p) {
   griddep_wait();
   griddep_launch_dependents();
   if (*reinterpret_cast<volatile uint32_t *>(&g_decode_errors) & kErrTimeout) return;
   key_scores_body<kScoreVec>(p);
+}
+
+KeyScoresParams scores_params(const DecodeArgs &a) {
+  KeyScoresParams k;
+  k.logits = a.logits;
+  k.lse = a.lse;
+  k.key_scores = a.key_scores;
+  k.context_lens = a.context_lens;
+  k.logits_ld = a.logits_ld;
+  k.score_stride = a.score_stride;
+  k.max_context_len = a.max_context_len;
+  k.num_q_heads = a.num_q_heads;
+  k.window = a.window;
+  k.ctx_cap = static_cast<int64_t>(a.max_blocks) * a.block_size;
+  return k;
 }
 
 template <int G, int HGM, int NS, bool kLogits = false>
@@ -855,8 +921,24 @@ cudaError_t launch_variant(const DecodeArgs &a, const CUtensorMap &k_map,
   const int64_t n_pairs = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   const int merge_warps = n_pairs >= kMergeWideMin ? kMergeWarps : kMergeWarpsFew;
   const int merge_grid = static_cast<int>((n_pairs + merge_warps - 1) / merge_warps);
-  return launch_pdl(decode_merge_kernel<G>, dim3(merge_grid), dim3(merge_warps * 32),
-                    sizeof(int) * static_cast<size_t>(a.num_seqs + 1), stream, p, a.grid);
+  const size_t prefix_bytes = sizeof(int) * static_cast<size_t>(a.num_seqs + 1);
+  if constexpr (kLogits) {
+    ScoredMerge scored = {};
+    scored.k = scores_params(a);
+    const int64_t chunks = key_scores_grid_x(a.max_context_len, kScoreVec);
+    scored.score_chunks = static_cast<int32_t>(chunks);
+    const bool beside = a.num_q_heads <= kMaxScoredHeads;
+    scored.score_ctas = beside ? static_cast<int32_t>(chunks * a.num_seqs) : 0;
+    scored.merge_warps = merge_warps;
+    e = launch_pdl(decode_merge_kernel<G, true>, dim3(static_cast<unsigned>(merge_grid + scored.score_ctas)),
+                   dim3(kMergeWarps * 32), prefix_bytes + (beside ? sizeof(float) * a.num_q_heads : 0), stream, p,
+                   a.grid, scored);
+    if (e != cudaSuccess || beside) return e;
+    return launch_pdl(decode_scores_kernel, dim3(static_cast<unsigned>(chunks), a.num_seqs), dim3(kScoreThreads), 0,
+                      stream, scored.k);
+  }
+  return launch_pdl(decode_merge_kernel<G, false>, dim3(merge_grid), dim3(merge_warps * 32), prefix_bytes, stream, p,
+                    a.grid, ScoredMerge{});
 }
 
 template <int G>
@@ -913,27 +995,12 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map,
   p.scale_log2 = a.scale_log2;
   p.logits = a.logits;
   p.logits_ld = a.logits_ld;
-  cudaError_t e;
   switch (a.num_q_heads / a.num_kv_heads) {
-    case 1: e = launch_group<1>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream); break;
-    case 2: e = launch_group<2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream); break;
-    case 4: e = launch_group<4>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream); break;
+    case 1: return launch_group<1>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
+    case 2: return launch_group<2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
+    case 4: return launch_group<4>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
     default: return cudaErrorInvalidValue;
   }
-  if (e != cudaSuccess || a.key_scores == nullptr) return e;
-  KeyScoresParams k;
-  k.logits = a.logits;
-  k.lse = a.lse;
-  k.key_scores = a.key_scores;
-  k.context_lens = a.context_lens;
-  k.logits_ld = a.logits_ld;
-  k.score_stride = a.score_stride;
-  k.max_context_len = a.max_context_len;
-  k.num_q_heads = a.num_q_heads;
-  k.window = a.window;
-  k.ctx_cap = static_cast<int64_t>(a.max_blocks) * a.block_size;
-  return launch_pdl(decode_scores_kernel, dim3(key_scores_grid_x(a.max_context_len, kScoreVec), a.num_seqs),
-                    dim3(kScoreThreads), 0, stream, k);
 }
 
 cudaError_t decode_error_word(uint32_t **word) {

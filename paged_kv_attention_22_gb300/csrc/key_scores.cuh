@@ -15,6 +15,7 @@ constexpr int kScoreThreads = 256;
 template <int N> struct ScoreVecOf;    // N neighbouring positions a thread
 template <> struct ScoreVecOf<2> { using T = float2; };
 template <> struct ScoreVecOf<4> { using T = float4; };
+constexpr int kMaxScoredHeads = 4096;  // query heads whose lse a scoring CTA holds in shared memory
 constexpr float kScoreLog2e = 1.4426950408889634f;
 
 struct KeyScoresParams {

@@ -773,7 +773,8 @@ cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream
   return launch_pdl(kernel, grid, dim3(kWarps * 32), smem, stream, p);
 }
 
-// k: the accumulated weights, or null.
+// k: the accumulated weights, or null; added here by ranges with at most
+// kMaxScoredHeads query heads.
 template <int NG>
 cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, const KeyScoresParams *k,
                         cudaStream_t stream) {
@@ -792,6 +793,7 @@ cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, const
     // them 46.0 and 44.1
     int64_t chunks = 0;
     bool pairs_of = true;
+    if (k != nullptr && p.num_q_heads > kMaxScoredHeads) k = nullptr;  // behind the merge
     if (k != nullptr) {
       chunks = key_scores_grid_x(p.max_context_len, 2);
       pairs_of = ctas + chunks * p.num_seqs <= 2 * plan.range_ctas;
@@ -866,7 +868,7 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
     case 128: e = launch_plan<1>(p, a.plan, scores, stream); break;
     default: return cudaErrorInvalidValue;
   }
-  if (e != cudaSuccess || scores == nullptr || a.plan.range_ctas > 0) return e;
+  if (e != cudaSuccess || scores == nullptr || (a.plan.range_ctas > 0 && a.num_q_heads <= kMaxScoredHeads)) return e;
   return launch_pdl(q4_scores_kernel, dim3(key_scores_grid_x(a.max_context_len, 2), a.num_seqs),
                     dim3(kScoreThreads), 0, stream, k);
 }

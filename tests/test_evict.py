@@ -386,6 +386,39 @@ def test_scored_decode_adds_nothing_after_a_timeout(L):
     assert bool((scores[0] > 0).all())
 
 
+@gpu
+@pytest.mark.parametrize("q4", [False, True])
+def test_scored_decode_of_very_many_heads(L, q4):
+    """More query heads than a scoring CTA holds: the same as two calls of half the
+    heads. The sums run over the heads in order, in fp32: n terms are off by at most
+    n U32 of their sum, the logits and the lse are the same numbers in both."""
+    heads, block, ctx = 8192, 16, 4200 if q4 else 100
+    g = torch.Generator().manual_seed(4)
+    bt = (torch.arange(-(-ctx // block)) % 2).to(torch.int32)[None].cuda()   # two blocks, again and again
+    q = torch.randn(1, heads, 128, generator=g).to(torch.bfloat16).cuda()
+    cl = torch.tensor([ctx], dtype=torch.int32, device="cuda")
+    if q4:
+        rows = torch.randn(2, 2, heads, block, 128, generator=g).to(torch.bfloat16)
+        caches = [tuple(x.cuda() for x in Q.quantise(rows[i], 32)) for i in range(2)]
+        call, cut = pkv.paged_decode_attn_q4, lambda c, a, b: tuple(x[:, a:b].contiguous() for x in c)
+    else:
+        caches = list(torch.randn(2, 2, block, heads, 128, generator=g).to(torch.bfloat16).cuda())
+        call, cut = pkv.paged_decode_attn_scores, lambda c, a, b: c[:, :, a:b].contiguous()
+    whole, halves = (torch.zeros(1, ctx, device="cuda") for _ in range(2))
+    out, lse = call(q, *caches, bt, cl, ctx, SCALE, key_scores=whole)
+    for a in (0, heads // 2):
+        b = a + heads // 2
+        o, l = call(q[:, a:b].contiguous(), *(cut(c, a, b) for c in caches), bt, cl, ctx, SCALE, key_scores=halves)
+        # another plan may cut the keys elsewhere. out, below 4: 3 U16 of it, twice. lse:
+        # its tolerance with sums |q k| scale below 16, twice: 2^-11
+        assert bool(((o - out[:, a:b]).abs() <= 6 * Q.U16 * 4).all()) and bool(((l - lse[:, a:b]).abs() <= 2.0 ** -11).all())
+    assert pkv.check_device_errors() == 0
+    tol = (2 * heads * Q.U32 + 2.0 ** -10) * halves.double()                 # the lse's difference, too
+    assert bool(((whole.double() - halves.double()).abs() <= tol).all())
+    total = float(whole.double().sum())
+    assert abs(total - heads) <= (heads * Q.U32 + 2.0 ** -11) * heads
+
+
 # ------------------------------------------------------------------ GPU: the chain
 
 @gpu
