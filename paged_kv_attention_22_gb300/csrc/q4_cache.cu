@@ -8,12 +8,12 @@
 // word of codes). A warp has several such pairs' loads in flight.
 //
 // All three are copies with some arithmetic: HBM bandwidth bounds them, once the
-// arithmetic is short enough (the store spends about six packed operations on
+// arithmetic is short enough (the store spends some five packed operations on
 // two values) and indices are found without 64-bit divisions. 32,768 tokens of 8
-// heads: store 41 us (176 MB, 4.3 TB/s; its issue slots are 73 % used, so it is
-// between the two bounds), load 30 us (176 MB, 5.9 TB/s), widening for prefill 28 us
-// (6.3 TB/s). With 8 values a lane the store took 51 us, its per-row work being
-// shared by half as many values.
+// heads: store 37 us (176 MB, 4.8 TB/s; its issue slots are 74 % used, so it is between
+// the two bounds), load 30 us (176 MB, 5.9 TB/s), widening for prefill 28 us
+// (6.3 TB/s). With 8 values a lane the store took 10 us more, its per-row work
+// being shared by half as many values.
 #include "internal.h"
 #include "q4.cuh"
 
@@ -24,8 +24,12 @@ static __device__ uint32_t g_q4_cache_errors;
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kStoreRows = 4;  // (token, head) pairs whose loads a warp has in flight, two at a time
-constexpr int kLoadRows = 8;
+// (token, head) pairs whose loads a warp has in flight (the store's two at a time).
+// More leave large calls as they are and lengthen small ones: 64 tokens of 8 heads
+// stored and read back 3.6 us in a graph, 5.0 with 4 and 8; 32,768 tokens 63.9 and
+// 63.5 (with 2 and 2: 68.7).
+constexpr int kStoreRows = 2;
+constexpr int kLoadRows = 4;
 
 // The smaller of each half; a NaN in either operand wins.
 __device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
@@ -34,15 +38,21 @@ __device__ __forceinline__ uint32_t min_nan_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // (smallest, -largest) of the sixteen values of x, as a bf16 pair.
 __device__ __forceinline__ uint32_t extremes(const uint32_t (&x)[8]) {
-  constexpr uint32_t kSigns = 0x80008000u;
-  uint32_t lo = x[0], hi = x[0] ^ kSigns;
+  uint32_t lo = x[0], hi = x[0];
 #pragma unroll
   for (int i = 1; i < 8; ++i) {
     lo = min_nan_bf16x2(lo, x[i]);
-    hi = min_nan_bf16x2(hi, x[i] ^ kSigns);
+    hi = max_nan_bf16x2(hi, x[i]);
   }
+  hi ^= 0x80008000u;
   return min_nan_bf16x2(q4_low_halves(lo, hi), q4_high_halves(lo, hi));
 }
 
@@ -87,7 +97,8 @@ __device__ __noinline__ uint32_t codes_one_by_one(uint4 x, float s, float b) {
 // low mantissa bits, which then hold the code. r' exceeds the reciprocal by 2^-19,
 // more than the estimate's own error, so that a half (common: the inputs have 8
 // bits) rounds up and a quotient at most 2^-14 below one may do so wrongly: the
-// remainder t - c s, exact in fp32, is then below -s / 2 and the code one less.
+// remainder t - c s, exact in fp32, is then below -s / 2 and the code one less (the
+// sign of remainder + s / 2, as an integer, is added).
 // Only groups whose offset's rounding pushes an extreme past the code range
 // need clamping; they take the other way.
 __device__ __forceinline__ uint2 codes_of(const uint32_t (&x)[8], uint32_t pw, float lo, float hi) {
@@ -97,18 +108,18 @@ __device__ __forceinline__ uint2 codes_of(const uint32_t (&x)[8], uint32_t pw, f
   if (lo - b < 15.75f * s || hi - b > 31.25f * s)
     return make_uint2(codes_one_by_one(make_uint4(x[0], x[1], x[2], x[3]), s, b),
                       codes_one_by_one(make_uint4(x[4], x[5], x[6], x[7]), s, b));
-  const float r = __fdividef(1.f + 0x1p-19f, s), nh = -0.5f * s;
+  const float r = __fdividef(1.f + 0x1p-19f, s), h = 0.5f * s;
   const uint64_t nb2 = f32x2(-b, -b), r2 = f32x2(r, r), m2 = f32x2(kM, kM), s2 = f32x2(s, s);
-  const uint64_t one2 = f32x2(1.f, 1.f), neg2 = f32x2(-1.f, -1.f);
+  const uint64_t one2 = f32x2(1.f, 1.f), neg2 = f32x2(-1.f, -1.f), h2 = f32x2(h, h);
   uint32_t byte[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint64_t t = fma2(f32x2(bf16lo(x[i]), bf16hi(x[i])), one2, nb2);
     const uint64_t y = fma2(t, r2, m2);
     const uint64_t rest = fma2(fma2(y, neg2, m2), s2, t);  // t - c s
-    uint32_t n0 = static_cast<uint32_t>(y), n1 = static_cast<uint32_t>(y >> 32);
-    if (f32x2_lo(rest) < nh) n0 -= 1;
-    if (f32x2_hi(rest) < nh) n1 -= 1;
+    const uint64_t over = fma2(rest, one2, h2);            // its sign is exact
+    const int n0 = static_cast<int>(y) + (static_cast<int>(over) >> 31);
+    const int n1 = static_cast<int>(y >> 32) + (static_cast<int>(over >> 32) >> 31);
     byte[i] = n1 * 16 + n0;  // its low byte
   }
   uint32_t w[2];
