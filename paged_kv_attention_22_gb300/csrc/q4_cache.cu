@@ -73,9 +73,9 @@ __device__ __forceinline__ uint32_t group_params(float lo, float hi) {
 
 // Codes of the eight values in four words, n = clamp(floor(t / s + 1/2) - 16, 0, 15)
 // with t = fp32(x - b), one value at a time. The quotient is only estimated and
-// rounded to the nearest integer c; the two comparisons with the thresholds
-// (c - 1/2) s and (c + 1/2) s, which are exact in fp32 (s has 8 bits, c at most
-// 12 here), settle it.
+// rounded to the nearest integer c; the remainder t - c s, where it is near the
+// thresholds -s / 2 and s / 2 exact in fp32 (s has 8 bits, c at most 7), settles it.
+// t may be infinite: its code is the last one.
 __device__ __noinline__ uint32_t codes_one_by_one(uint4 x, float s, float b) {
   const float r = 1.f / s, h = 0.5f * s;
   const uint32_t wx[4] = {x.x, x.y, x.z, x.w};
@@ -83,9 +83,9 @@ __device__ __noinline__ uint32_t codes_one_by_one(uint4 x, float s, float b) {
   for (int i = 0; i < 8; ++i) {
     const float t = ((i & 1) ? bf16hi(wx[i >> 1]) : bf16lo(wx[i >> 1])) - b;
     float c = rintf(fminf(fmaxf(t * r, 0.f), 100.f));
-    const float at = c * s;
-    if (t >= at + h) c += 1.f;
-    else if (t < at - h) c -= 1.f;
+    const float rest = fmaf(-c, s, t);
+    if (rest >= h) c += 1.f;
+    else if (rest < -h) c -= 1.f;
     const int n = min(max(static_cast<int>(c) - 16, 0), 15);
     codes |= static_cast<uint32_t>(n) << (4 * i);
   }
@@ -99,13 +99,13 @@ __device__ __noinline__ uint32_t codes_one_by_one(uint4 x, float s, float b) {
 // bits) rounds up and a quotient at most 2^-14 below one may do so wrongly: the
 // remainder t - c s, exact in fp32, is then below -s / 2 and the code one less (the
 // sign of remainder + s / 2, as an integer, is added).
-// Only groups whose offset's rounding pushes an extreme past the code range
-// need clamping; they take the other way.
+// Only groups whose offset's rounding pushes an extreme past the code range, or
+// whose differences overflow, need clamping; they take the other way.
 __device__ __forceinline__ uint2 codes_of(const uint32_t (&x)[8], uint32_t pw, float lo, float hi) {
   constexpr float kM = 12582896.f;
   const float s = bf16lo(pw), b = bf16hi(pw);
   if (s == 0.f) return make_uint2(0u, 0u);
-  if (lo - b < 15.75f * s || hi - b > 31.25f * s)
+  if (lo - b < 15.75f * s || hi - b > fminf(31.25f * s, 3.4e38f))  // an infinite difference, too
     return make_uint2(codes_one_by_one(make_uint4(x[0], x[1], x[2], x[3]), s, b),
                       codes_one_by_one(make_uint4(x[4], x[5], x[6], x[7]), s, b));
   const float r = __fdividef(1.f + 0x1p-19f, s), h = 0.5f * s;

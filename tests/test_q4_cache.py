@@ -221,6 +221,31 @@ def test_store_and_load_are_exact(L, tokens, heads, block, group):
 
 
 @gpu
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_store_is_exact_to_the_ends_of_the_range(L, group):
+    """Groups whose differences overflow fp32, and rows of any bits at all."""
+    g = torch.Generator().manual_seed(group)
+    x = torch.randint(-2 ** 15, 2 ** 15, (512, 2, 128), generator=g, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    big = 3.3e38 * torch.rand(256, 2, 128, generator=g)          # from -x/8 to 7x/8 and the other way round
+    x[:256] = torch.where(torch.rand(256, 2, 128, generator=g) < 0.3, -big / 8, big * 0.875).to(torch.bfloat16)
+    x[128:256] = -x[128:256]
+    y = x.flip(0).contiguous()
+    kc, vc = (pkv.new_q4_cache(32, 16, 2, group) for _ in range(2))
+    slots = torch.arange(512, dtype=torch.int32, device="cuda")
+    pkv.kv_store_q4(x.cuda(), y.cuda(), kc, vc, slots)
+    rk, rv = pkv.kv_load_q4(kc, vc, slots)
+    assert pkv.check_device_errors() == 0
+    for c, rows, back in ((kc, x, rk), (vc, y, rv)):
+        codes, params = Q.quantise(rows, group)
+        assert torch.equal(c.codes.permute(0, 2, 1, 3).reshape(512, 2, 64).cpu(), codes)
+        got, nan = c.params.permute(0, 2, 1, 3, 4).reshape(params.shape).cpu(), torch.isnan(params.float())
+        assert torch.equal(torch.isnan(got.float()), nan) and torch.equal(_as_bits(got)[~nan], _as_bits(params)[~nan])
+        want = Q.values(codes, params)
+        assert torch.equal(back.cpu().double().nan_to_num(nan=123.0, posinf=4e38, neginf=-4e38),
+                           want.nan_to_num(nan=123.0, posinf=4e38, neginf=-4e38))
+
+
+@gpu
 def test_row_calls_report_bad_slots_and_touch_nothing_else(L):
     heads, block = 2, 16
     kc, vc = pkv.new_q4_cache(4, block, heads), pkv.new_q4_cache(4, block, heads)
