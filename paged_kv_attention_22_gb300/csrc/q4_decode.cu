@@ -13,7 +13,7 @@
 //            warps leaves one partial result each in the workspace (a warp's
 //            first piece in slot 2w, its last in slot 2w + 1), joined by a
 //            second kernel: the way for few or unequal pairs. (Splits of fixed
-//            length in CTAs of their own took 68 us where ranges take 65.9;
+//            length in CTAs of their own took 68 us where ranges take 65.7;
 //            joined in clusters through distributed shared memory, 73.)
 //
 // The products run on mma.sync m16n8k16 in bf16 with fp32 accumulators. A bf16
@@ -36,7 +36,7 @@
 // What bounds it: widening the codes, a shift, a logic operation and a packed fma
 // for two values, some 420 of the 680 instructions of a step. Shifts and logic
 // share one half-rate pipe and packed fmas have another. 16 sequences of 16,384
-// keys, 8 KV heads, 2 query heads each: 65.9 us, 336 MB at 5.1 TB/s; issue slots
+// keys, 8 KV heads, 2 query heads each: 65.7 us, 336 MB at 5.1 TB/s; issue slots
 // 62 % used, the shift and logic pipe 57 %. (Without the widening the same loop
 // streams at 6.3 TB/s; a step of 16 keys, or 20 or 24 warps an SM with fewer
 // registers, took 71 to 78 us.) 64 sequences of 640 keys: 15.7 us.
@@ -56,7 +56,7 @@ constexpr int kStep = 2 * kUnit;             // keys a step
 constexpr int kStages = 2;                   // steps in a warp's ring
 constexpr int kMaxG = 8;                     // query heads a KV head (columns of a P^T tile)
 constexpr int kUnitCodes = kUnit * kQ4RowBytes;  // 1 KiB of K or V codes
-constexpr int kQueryBytes = 32 * 64;         // a warp's query fragments, where they are in shared memory
+constexpr int kQueryBytes = 32 * 64;         // a warp's query fragments
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kFloor = -1.7e38f;           // below every logit; differences stay finite
 constexpr float kLazyMax = 8.0f;             // log2 units the running max may lag
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.gqa;
-  // ranges: the warps' queries and the list of steps, behind the rings
+  // ranges: the list of steps, behind the rings and the warps' queries
   [[maybe_unused]] int64_t *prefix = reinterpret_cast<int64_t *>(smem + L::kTotal + kWarps * kQueryBytes);
   [[maybe_unused]] int *ctx_of = reinterpret_cast<int *>(prefix + p.num_seqs + 1);
   [[maybe_unused]] int64_t first_step = 0;  // this warp's range starts there
@@ -226,11 +226,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
   }
 
   // the pair's query heads as B fragments: k-step 2w (2w + 1) pairs dims i and
-  // i + 4, i = 0, 1 (2, 3), of the lane's w-th code word. Ranges keep them in shared
-  // memory (each lane its own, read back for every unit), where their 16 registers
-  // go to the cursor (16 x 16,384 keys 67.8 us in registers, 65.9 so)
-  [[maybe_unused]] uint32_t qb[8][2];
-  [[maybe_unused]] uint4 *sq = reinterpret_cast<uint4 *>(smem + L::kTotal) + warp * 4 * 32 + lane;
+  // i + 4, i = 0, 1 (2, 3), of the lane's w-th code word. They are kept in shared
+  // memory (each lane its own, read back for every unit), not in 16 registers (16 x
+  // 16,384 keys 67.8 us in registers, 65.7 so; 300 x 2,048 136.0 and 134.2)
+  uint4 *sq = reinterpret_cast<uint4 *>(smem + L::kTotal) + warp * 4 * 32 + lane;
   auto load_q = [&]() {
     const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + cur.head * G + g;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.q + row * kD + 32 * t);
@@ -241,16 +240,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
       x.y ^= p.q_signs;
       x.z ^= p.q_signs;
       x.w ^= p.q_signs;
-      const uint4 y = make_uint4(q4_low_halves(x.x, x.z), q4_high_halves(x.x, x.z), q4_low_halves(x.y, x.w),
-                                 q4_high_halves(x.y, x.w));
-      if constexpr (kRanges) {
-        sq[w * 32] = y;
-      } else {
-        qb[2 * w][0] = y.x;
-        qb[2 * w][1] = y.y;
-        qb[2 * w + 1][0] = y.z;
-        qb[2 * w + 1][1] = y.w;
-      }
+      sq[w * 32] = make_uint4(q4_low_halves(x.x, x.z), q4_high_halves(x.x, x.z), q4_low_halves(x.y, x.w),
+                              q4_high_halves(x.y, x.w));
     }
   };
   load_q();
@@ -390,9 +381,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[j][i] = fma_bf16x2(x[j][i], s2[j], b2[j]);
         }
-        uint4 y;
-        if constexpr (kRanges) y = sq[w * 32];
-        else y = make_uint4(qb[2 * w][0], qb[2 * w][1], qb[2 * w + 1][0], qb[2 * w + 1][1]);
+        const uint4 y = sq[w * 32];
         mma_16816(sc[0], x[0][0], x[1][0], x[0][1], x[1][1], y.x, y.y);
         mma_16816(sc[1], x[0][2], x[1][2], x[0][3], x[1][3], y.z, y.w);
       }
@@ -764,8 +753,8 @@ __global__ void __launch_bounds__(256) q4_rows_kernel(const Q4PrefillRowsArgs a)
 template <int NG, int kWarps, bool kRanges>
 cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream) {
   auto kernel = q4_decode_kernel<NG, kWarps, kRanges>;
-  int smem = Q4DecodeSmem<NG, kWarps>::kTotal;
-  if (kRanges) smem += kWarps * kQueryBytes + static_cast<int>(sizeof(int64_t)) * (p.num_seqs + 1) + static_cast<int>(sizeof(int)) * p.num_seqs;
+  int smem = Q4DecodeSmem<NG, kWarps>::kTotal + kWarps * kQueryBytes;
+  if (kRanges) smem += static_cast<int>(sizeof(int64_t)) * (p.num_seqs + 1) + static_cast<int>(sizeof(int)) * p.num_seqs;
   if (smem > 48 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
