@@ -39,7 +39,7 @@
 // keys, 8 KV heads, 2 query heads each: 65.7 us, 336 MB at 5.1 TB/s; issue slots
 // 62 % used, the shift and logic pipe 57 %. (Without the widening the same loop
 // streams at 6.3 TB/s; a step of 16 keys, or 20 or 24 warps an SM with fewer
-// registers, took 71 to 78 us.) 64 sequences of 640 keys: 15.7 us.
+// registers, took 71 to 78 us.) 64 sequences of 640 keys: 15.4 us.
 #include "internal.h"
 #include "key_scores.cuh"
 #include "q4.cuh"
@@ -371,7 +371,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
         s2[j] = q4_dup_scale(pw);
         b2[j] = q4_dup_offset(pw);
       }
-      float sc[2][4] = {};  // two chains of products
+      // chains of products: one for pairs (64 x 640 keys 15.4 us, 15.6 with two), two
+      // for ranges (16 x 16,384 keys 65.5 us, 66.8 with one)
+      constexpr int kChains = kRanges ? 2 : 1;
+      float sc[kChains][4] = {};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         uint32_t x[2][4];
@@ -383,10 +386,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) q4_decode_kernel(con
         }
         const uint4 y = sq[w * 32];
         mma_16816(sc[0], x[0][0], x[1][0], x[0][1], x[1][1], y.x, y.y);
-        mma_16816(sc[1], x[0][2], x[1][2], x[0][3], x[1][3], y.z, y.w);
+        mma_16816(sc[kChains - 1], x[0][2], x[1][2], x[0][3], x[1][3], y.z, y.w);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) z[u][i] = sc[0][i] + sc[1][i];
+      for (int i = 0; i < 4; ++i) z[u][i] = kChains == 2 ? sc[0][i] + sc[kChains - 1][i] : sc[0][i];
     }
 
     // ---- masks, softmax
