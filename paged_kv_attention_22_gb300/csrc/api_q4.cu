@@ -127,7 +127,8 @@ DecodeWorkspace decode_workspace(int32_t num_seqs, int32_t num_q_heads, int32_t 
 // query heads) is one CTA that passes all its keys, 128 in 1.4 us. Measured, in us,
 // by rows and widened: 8 segments of 8,192 keys with 1 query token each 28 and 150,
 // with 8 127 and 150, with 16 239 and 150; one of 32,768 keys with 16 tokens 124
-// and 390; 64 of 128 keys with 4 tokens 18 and 34.
+// and 390; 64 of 128 keys with 4 tokens 18 and 34, with 8 30 and 34; prompts alone, 4
+// of 9 tokens 6.3 and 10.8, of 32 8.7 and 10.6, of 64 14.5 and 10.8.
 constexpr int32_t kRowsMaxQ = 64;   // query tokens a segment by rows, at most (a workspace bound)
 
 bool prefill_by_rows(int64_t num_seqs, int64_t total_q, int64_t max_q, int64_t total_k, int64_t keys, int64_t q_heads,
@@ -137,7 +138,7 @@ bool prefill_by_rows(int64_t num_seqs, int64_t total_q, int64_t max_q, int64_t t
   const double widen_us = std::min<double>(total_k, static_cast<double>(num_seqs) * keys) * kv_heads * 672 / 6.2e6;
   const int64_t ctas = num_seqs * (q_heads > kv_heads ? q_heads / 2 : q_heads);
   const double attend_us = (ctas + sms - 1) / sms * (4 + keys / 128 * 1.4);
-  return rows_us < 4 + widen_us + attend_us;
+  return rows_us < 6.5 + widen_us + attend_us;
 }
 
 struct PrefillWorkspace {
