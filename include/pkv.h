@@ -437,7 +437,9 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
  * pkv_paged_decode_attn that also accumulates the attention weights:
  *   key_scores[s * score_stride + p] += sum over query heads h of exp(z_hp - lse[s, h])
  * for every key p that sequence s attended to; other entries keep their values.
- * The heads are summed in order: the same inputs give the same bits.
+ * The heads are summed in order: the same inputs give the same bits. An invalid
+ * table entry raises PKV_DEVERR_BLOCK and its keys are left out, of the attention
+ * and of the weights.
  *   key_scores   device float32 [num_seqs, score_stride], not NULL; the caller
  *                sets a sequence's row to zero when it admits the sequence
  *   score_stride >= max_context_len, which is at most 2^30 (PKV_ERR_UNSUPPORTED)

@@ -57,6 +57,7 @@ constexpr int kChunk = kDecodeChunk;    // 16 keys per unit
 constexpr int kRowBytes = kD * 2;       // 256 bytes of one head's K (or V) row
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kLazyMax = 8.0f;         // log2 units the running max may lag
+constexpr float kFloor = -1.7e38f;       // finite, below every logit
 constexpr int kMergeFast = 8;            // pieces merged with all loads issued at once
 // Warps per merge CTA (one pair each). With many pairs, eight: the merge of a
 // call then occupies fewer SMs, which the next call's decode CTAs find free
@@ -112,7 +113,8 @@ struct DecodeSmem {
   static constexpr int kProbOffset = NS * kStageBytes;            // float [HG][G][16]
   static constexpr int kProbBytes = kMaxHG * G * kChunk * 4;
   static constexpr int kBarOffset = kProbOffset + kProbBytes;     // u64 full[NS], empty[NS]
-  static constexpr int kPrefixOffset = kBarOffset + 2 * NS * 8;   // int [S + 1] chunk prefix,
+  static constexpr int kThereOffset = kBarOffset + 2 * NS * 8;    // int [NS]: the stage's K and V were copied (kLogits)
+  static constexpr int kPrefixOffset = kThereOffset + (NS * 4 + 7) / 8 * 8;  // int [S + 1] chunk prefix,
                                                                   // then int [S] context lengths
   static constexpr int total(int num_seqs) { return kPrefixOffset + 4 * (2 * num_seqs + 1) + 128; }
 };
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
 
   int *prefix = reinterpret_cast<int *>(smem + L::kPrefixOffset);
   int *ctx_of = prefix + p.num_seqs + 1;
+  [[maybe_unused]] int *there_of = reinterpret_cast<int *>(smem + L::kThereOffset);
   const uint32_t full0 = smem_u32(smem + L::kBarOffset);
   const uint32_t empty0 = full0 + NS * 8;
   const bool fused = p.k_new != nullptr;
@@ -316,6 +319,7 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
       const bool ok = blk >= 0 && blk < p.num_blocks;
       if (arm) {
         if (!ok) atomicOr(&g_decode_errors, kErrBlock);
+        if constexpr (kLogits) there_of[st] = ok;  // the arrival publishes it
         mbar_arrive_expect_tx(bar, (ok ? 2 * box : 0) + (with_q ? qbox : 0) +
                                        (with_new ? 2 * nbox : 0));
       }
@@ -462,7 +466,19 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
       }
     }
     const int key0 = (chunk0 + cur.k) * kChunk;   // the unit's first key
-    const int nvalid = min(kChunk, ctx - key0);   // keys >= nvalid are past the context
+    // A unit without a block: the stage holds whatever was there before. The outputs
+    // of a bad entry are undefined, but weights are added to what the caller keeps:
+    // with kLogits such keys are left out (logit -inf), and the maximum of a segment
+    // that begins with them is finite, so that no difference of infinities arises.
+    bool there = true;
+    if constexpr (kLogits) {
+      there = there_of[st] != 0;
+      if (!there) {
+#pragma unroll
+        for (int h = 0; h < G; ++h) m[h] = fmaxf(m[h], kFloor);
+      }
+    }
+    const int nvalid = there ? min(kChunk, ctx - key0) : 0;  // keys >= nvalid are past the context
     const int nskip = key_lo - key0;              // keys < nskip are before the window
     const bool with_new = fused && cur.k == chunks_of(prefix, cur.s) - 1;
     if (with_new) {
@@ -512,7 +528,7 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
       sc[h] = (my_key < nvalid && my_key >= nskip) ? full : -INFINITY;
       if constexpr (kLogits) {  // rows hold whole units: masked keys are written too
         const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + (cur.hg * HG + g) * G + h;
-        if (counts) p.logits[row * p.logits_ld + key0 + my_key] = full;
+        if (counts) p.logits[row * p.logits_ld + key0 + my_key] = there ? full : -INFINITY;
       }
     }
 
@@ -725,7 +741,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
           const int64_t wa = owner_of(P0, W, U);
           const int64_t n = hq < p.num_q_heads ? owner_of(P0 + nch - 1, W, U) - wa + 1 : 0;
           const int64_t wa_slot = 2 * wa + (range_start(wa, W, U) < P0 ? 1 : 0);
-          float M = -1.7e38f, l = 0.f;  // finite, below every logit
+          float M = kFloor, l = 0.f;
           for (int64_t x = half; x < (n > 1 ? n : 0); x += 16) {
             const int64_t i = ((x == 0 ? wa_slot : 2 * (wa + x)) * HG + kvh % HG) * G + h;
             const float m = p.ws_ml[i * 2], m_new = fmaxf(M, m);

@@ -372,6 +372,51 @@ def test_scored_decode(L, lens, heads, gqa, block, window):
 
 
 @gpu
+@pytest.mark.parametrize("ctx,block,heads,gqa,window,variant", [
+    (40, 16, 1, 2, 0, 0), (20000, 64, 2, 1, 0, 0), (3000, 32, 8, 2, 0, 2), (1000, 16, 4, 4, 0, 0), (700, 16, 8, 2, 300, 0)])
+def test_scored_decode_leaves_keys_of_bad_table_entries_out(L, ctx, block, heads, gqa, window, variant):
+    """Sequence 0 has one bad entry, sequence 1 nothing but bad ones, sequence 2 none:
+    the weights of sequence 0 are those over its other keys, sequence 1's stay, and
+    sequence 2 has the plain call's bits, whatever the workspace held."""
+    k, v, tables, kr, vr = _bf16_case(ctx, [ctx] * 3, heads, block)
+    q = torch.randn(3, heads * gqa, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    first = max(0, ctx - window) if window else 0
+    bad = first // block + 1
+    tables[0, bad] = int(tables.max()) + 9
+    tables[1] = -1
+    args = (q.cuda(), k.cuda(), v.cuda(), tables.cuda(), torch.full((3,), ctx, dtype=torch.int32, device="cuda"), ctx, SCALE)
+    scores = torch.full((3, ctx), 0.5, device="cuda")
+    pkv.decode_set_config(0, variant)
+    try:
+        ws = pkv.new_decode_scores_workspace(3, heads * gqa, heads, ctx).fill_(255)      # NaNs
+        out, lse = pkv.paged_decode_attn_scores(*args, scores, workspace=ws, sliding_window=window)
+        assert pkv.check_device_errors() == pkv.DEVERR_BLOCK
+        o0, l0 = pkv.paged_decode_attn(*args, sliding_window=window)
+        assert pkv.check_device_errors() == pkv.DEVERR_BLOCK
+    finally:
+        pkv.decode_set_config(0, 0)
+    assert torch.equal(out[2], o0[2]) and torch.equal(lse[2], l0[2])
+    got = scores.cpu().double()
+    rest = torch.cat([torch.arange(first, bad * block), torch.arange((bad + 1) * block, ctx)])
+    want, tol = torch.zeros(len(rest), dtype=torch.float64), torch.zeros(len(rest), dtype=torch.float64)
+    for h in range(heads * gqa):
+        ks, vs = kr[0][rest, h // gqa].double(), vr[0][rest, h // gqa].double()
+        o, l, w, wv, qk = Q.attend(q[0, h:h + 1].double(), ks, vs, SCALE, [0], [len(rest) - 1])
+        assert bool(((out[0, h].cpu().double() - o[0]).abs() <= Q.out_tolerance(o[0], wv[0])).all())
+        tol_l = Q.lse_tolerance(l, qk, ctx)
+        assert abs(float(lse[0, h]) - float(l)) <= float(tol_l)
+        want += w[0]
+        tol += w[0] * (2 * tol_l + 2.0 ** -20)          # exp(z - lse): both within the lse's tolerance
+    # the heads' additions and the last one round
+    tol += (heads * gqa + 2) * Q.U32 * (0.5 + want)
+    assert bool(((got[0, rest] - 0.5 - want).abs() <= tol).all())
+    others = torch.ones(ctx, dtype=torch.bool)
+    others[rest] = False
+    assert bool((got[0, others] == 0.5).all()) and bool((got[1] == 0.5).all())
+    assert bool(torch.isfinite(got[2]).all())
+
+
+@gpu
 def test_scored_decode_adds_nothing_after_a_timeout(L):
     k, v, tables, _, _ = _bf16_case(1, [50, 20], 2, 16)
     args = (torch.randn(2, 4, 128).to(torch.bfloat16).cuda(), k.cuda(), v.cuda(), tables.cuda(),
