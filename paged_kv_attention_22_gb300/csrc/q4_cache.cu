@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32) q4_load_kernel(const Q4RowsParams
 }
 
 // Widen the keys of a prefill batch into bf16 blocks of kQ4PrefillBlock rows in
-// the workspace, whose block tables it writes. Sequence s starts at workspace
+// the workspace, whose block tables and segment lengths it writes. Sequence s starts at workspace
 // block ceil(cu_k[s] / block) + s, which leaves every sequence its
 // ceil(Lk / block) blocks. Grid: (chunks, sequences); a warp takes 16 keys of one
 // head, which lie in one cache block: one table entry, 1 KiB of K and of V codes.
@@ -232,6 +232,7 @@ struct Q4GatherParams {
   const uint32_t *k_codes, *v_codes, *k_params, *v_params;
   uint4 *k_out, *v_out;         // workspace K and V [blocks, kQ4PrefillBlock, H_kv, 128]
   int32_t *ws_tables;           // [S, ws_max_blocks]
+  int32_t *ws_k_end, *ws_k_begin;  // [S], for the prefill kernel: the segment's keys, and 0
   FastDiv heads, block;
   int32_t max_blocks, ws_max_blocks, max_seqlen_q, max_seqlen_k, total_k;
   int32_t groups_log2, num_blocks, window;
@@ -245,15 +246,17 @@ __global__ void __launch_bounds__(kWarps * 32) q4_gather_kernel(const Q4GatherPa
   const int k_begin = p.cu_k[s], k_end = p.cu_k[s + 1];
   const int q_begin = p.cu_q[s], q_end = p.cu_q[s + 1];
   const int64_t Lk64 = static_cast<int64_t>(k_end) - k_begin, Lq64 = static_cast<int64_t>(q_end) - q_begin;
-  // segments that the prefill kernel refuses (it raises the bit) are not
-  // widened; one that only passes total_k is refused here, since that kernel does
-  // not know it
-  const bool ok = Lk64 > 0 && Lq64 > 0 && Lq64 <= Lk64 && Lq64 <= p.max_seqlen_q && Lk64 <= p.max_seqlen_k &&
-                  k_begin >= 0 && k_end <= p.total_k &&
-                  Lk64 <= static_cast<int64_t>(p.max_blocks) * p.block.d;
+  // The prefill kernel refuses a segment (raising the bit) by its lengths; it knows
+  // neither total_k nor the cache's tables, so that a segment beyond those gets the
+  // length -1, which it refuses. Only what it takes is widened.
+  const bool beyond = Lk64 < 0 || Lk64 > INT32_MAX || Lk64 > static_cast<int64_t>(p.max_blocks) * p.block.d ||
+                      (Lq64 > 0 && (k_begin < 0 || k_end > p.total_k));
+  const bool ok = !beyond && Lk64 > 0 && Lq64 > 0 && Lq64 <= Lk64 && Lq64 <= p.max_seqlen_q && Lk64 <= p.max_seqlen_k;
   const int Lk = ok ? static_cast<int>(Lk64) : 0, Lq = ok ? static_cast<int>(Lq64) : 0;
-  if (k_end > p.total_k && Lq64 > 0 && blockIdx.x == 0 && threadIdx.x == 0)
-    atomicOr(&g_q4_cache_errors, kErrSeqlens);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.ws_k_end[s] = beyond ? -1 : static_cast<int>(Lk64);
+    p.ws_k_begin[s] = 0;
+  }
   const int ws_block0 = ok ? (k_begin + kQ4PrefillBlock - 1) / kQ4PrefillBlock + s : 0;
   for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < p.ws_max_blocks; j += gridDim.x * blockDim.x)
     p.ws_tables[static_cast<int64_t>(s) * p.ws_max_blocks + j] =
@@ -355,6 +358,8 @@ cudaError_t launch_q4_gather(const Q4GatherArgs &a, cudaStream_t stream) {
   p.k_out = static_cast<uint4 *>(a.ws_k);
   p.v_out = static_cast<uint4 *>(a.ws_v);
   p.ws_tables = a.ws_tables;
+  p.ws_k_end = a.ws_k_end;
+  p.ws_k_begin = a.ws_k_begin;
   p.max_blocks = a.max_blocks;
   p.ws_max_blocks = a.ws_max_blocks;
   p.max_seqlen_q = a.max_seqlen_q;

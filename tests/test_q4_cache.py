@@ -710,6 +710,58 @@ def test_prefill_by_rows_leaves_refused_segments_alone(L):
         assert bool(((l[good].cpu().double() - lse[good]).abs() <= tol_l[good]).all())
 
 
+REFUSED = {  # what is wrong: the segments that are left alone (None: not looked at)
+    "total_k": [2], "max_k": [0], "max_q": [0], "table": [0], "total_q": [2], "cu_k": [0], "decreasing": None, "empty": []}
+
+
+@gpu
+@pytest.mark.parametrize("what", list(REFUSED))
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("q_lens,k_lens", [([100, 80, 90], [300, 200, 150])])  # widened
+def test_prefill_leaves_refused_segments_alone(L, q_lens, k_lens, window, what):
+    """A segment that the call refuses raises the bit and keeps its rows; the others
+    are attended. Sequence 0 is the longest in queries and in keys."""
+    alone, heads, gqa, block = REFUSED[what], 2, 2, 16
+    if what == "empty":                         # nothing to write, but keys past the maximum
+        q_lens = [0] + q_lens[1:]
+    c = Q.Cache(15, k_lens, heads, block, 32)
+    rows = sum(q_lens) + (-1 if what == "total_q" else 3)
+    q = torch.randn(rows + 1, heads * gqa, 128, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16)
+    out, lse, tol_o, tol_l = _prefill_plain(c, q, q_lens, gqa, window)
+    q = q[:rows]
+    kc, vc, bt = c.cuda()
+    cu_q, cu_k = _cu(q_lens), _cu(k_lens)
+    max_q, max_k, total_k = max(q_lens), max(k_lens), sum(k_lens)
+    if what == "total_k":
+        total_k -= 1
+    elif what in ("max_k", "empty"):
+        max_k -= 1
+    elif what == "max_q":
+        max_q -= 1
+    elif what == "table":
+        bt = bt[:, :-1].contiguous()            # sequence 0 alone needs the last column
+    elif what == "cu_k":
+        cu_k[0], max_k = -8, max_k + 8
+    elif what == "decreasing":
+        cu_q[1], max_q = cu_q[2] + 1, 64 if max_q < 64 else max_k
+    o = torch.full_like(q, 9.0).cuda()
+    l = torch.full((rows, heads * gqa), 9.0, device="cuda")
+    pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, cu_q, cu_k, bt, max_q, max_k, total_k, SCALE, out=o, lse=l,
+                              sliding_window=window)
+    assert pkv.check_device_errors() == pkv.DEVERR_SEQLENS
+    if alone is None:
+        return
+    at = [0, q_lens[0], q_lens[0] + q_lens[1], sum(q_lens)]
+    written = torch.zeros(rows, dtype=torch.bool)
+    for s in range(3):
+        if s not in alone:
+            written[at[s]:at[s + 1]] = True
+    o, l = o.cpu(), l.cpu()
+    assert bool((o[~written] == 9.0).all()) and bool((l[~written] == 9.0).all())
+    out, lse, tol_o, tol_l = (x[:rows][written] for x in (out, lse, tol_o, tol_l))
+    assert bool(((o[written].double() - out).abs() <= tol_o).all()) and bool(((l[written].double() - lse).abs() <= tol_l).all())
+
+
 @gpu
 @pytest.mark.parametrize("total,bound", [(12, 3000), (600, 400)])  # by rows, widened
 def test_prefill_in_a_graph_replayed_for_other_segments(L, total, bound):
