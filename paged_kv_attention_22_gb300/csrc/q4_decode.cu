@@ -727,28 +727,29 @@ __global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScore
 
 // Prefill by rows: every query row of a varlen batch becomes a sequence of its own
 // for the decode kernel, with the keys up to its position and its segment's
-// table. A row of a segment that the prefill call refuses (raising the bit), and
-// a row behind the last segment, gets length 0: it is left out.
+// table. A row of a segment that the call refuses, and a row behind the last
+// segment, gets length 0: it is left out. The bit is raised by a thread a segment,
+// also for one without rows, as the widened way's prefill kernel does.
+__device__ __forceinline__ bool segment_refused(const Q4PrefillRowsArgs &a, int s) {
+  const int64_t q0 = a.cu_seqlens_q[s], q1 = a.cu_seqlens_q[s + 1], k0 = a.cu_seqlens_k[s], k1 = a.cu_seqlens_k[s + 1];
+  const int64_t Lq = q1 - q0, Lk = k1 - k0;
+  return q0 < 0 || Lq < 0 || Lk < Lq || Lq > a.max_seqlen_q || Lk > a.max_seqlen_k || q1 > a.total_q ||
+         Lk > static_cast<int64_t>(a.max_blocks) * a.block_size || (Lq > 0 && (k0 < 0 || k1 > a.total_k));
+}
 __global__ void __launch_bounds__(256) q4_rows_kernel(const Q4PrefillRowsArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int row = blockIdx.x * blockDim.x + threadIdx.x;
+  if (row < a.num_seqs && segment_refused(a, row)) atomicOr(&g_q4_decode_errors, kErrSeqlens);
   if (row >= a.total_q) return;
   int lo = 0, hi = a.num_seqs - 1;  // the last segment that starts at or before the row
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (a.cu_seqlens_q[mid] <= row) lo = mid; else hi = mid - 1;
   }
-  const int64_t q0 = a.cu_seqlens_q[lo], Lq = a.cu_seqlens_q[lo + 1] - q0;
-  const int64_t k0 = a.cu_seqlens_k[lo], k1 = a.cu_seqlens_k[lo + 1], Lk = k1 - k0;
   int ctx = 0;
-  if (row >= q0 && row < q0 + Lq) {
-    if (Lq > Lk || Lq > a.max_seqlen_q || Lk > a.max_seqlen_k || k1 > a.total_k || k0 < 0 ||
-        Lk > static_cast<int64_t>(a.max_blocks) * a.block_size)
-      atomicOr(&g_q4_decode_errors, kErrSeqlens);
-    else
-      ctx = static_cast<int>(Lk - Lq + (row - q0) + 1);
-  }
+  if (a.cu_seqlens_q[lo] <= row && row < a.cu_seqlens_q[lo + 1] && !segment_refused(a, lo))
+    ctx = a.cu_seqlens_k[lo + 1] - a.cu_seqlens_k[lo] - (a.cu_seqlens_q[lo + 1] - row) + 1;
   a.context_lens[row] = ctx;
   a.table_rows[row] = lo;
 }
@@ -866,7 +867,8 @@ cudaError_t launch_q4_decode(const Q4DecodeArgs &a, cudaStream_t stream) {
 }
 
 cudaError_t launch_q4_prefill_rows(const Q4PrefillRowsArgs &a, cudaStream_t stream) {
-  return launch_pdl(q4_rows_kernel, dim3((a.total_q + 255) / 256), dim3(256), 0, stream, a);
+  const int threads = a.total_q > a.num_seqs ? a.total_q : a.num_seqs;
+  return launch_pdl(q4_rows_kernel, dim3((threads + 255) / 256), dim3(256), 0, stream, a);
 }
 
 cudaError_t q4_decode_error_word(uint32_t **word) {

@@ -717,8 +717,8 @@ REFUSED = {  # what is wrong: the segments that are left alone (None: not looked
 @gpu
 @pytest.mark.parametrize("what", list(REFUSED))
 @pytest.mark.parametrize("window", [0, 60])
-@pytest.mark.parametrize("q_lens,k_lens", [([100, 80, 90], [300, 200, 150])])  # widened
-def test_prefill_leaves_refused_segments_alone(L, q_lens, k_lens, window, what):
+@pytest.mark.parametrize("q_lens,k_lens", [([3, 2, 1], [2000, 1500, 1000]), ([100, 80, 90], [300, 200, 150])])  # by rows, widened
+def test_prefill_refuses_segments_alike_on_both_ways(L, q_lens, k_lens, window, what):
     """A segment that the call refuses raises the bit and keeps its rows; the others
     are attended. Sequence 0 is the longest in queries and in keys."""
     alone, heads, gqa, block = REFUSED[what], 2, 2, 16
