@@ -473,12 +473,23 @@ pkv_status pkv_paged_decode_attn_scores(const void *q, const void *k_cache, cons
  *                ascending order, then -1
  *   new_lens     device int32 [num_seqs]: min(ctx, budget)
  * A sequence whose length is invalid raises PKV_DEVERR_CONTEXT and its rows of
- * keep and new_lens are not written.
+ * keep and new_lens are not written: a compaction enqueued behind the call acts on
+ * what they held. Set them to -1 beforehand, or use pkv_evict_select_new.
  */
 pkv_status pkv_evict_select(const float *key_scores, int64_t score_stride,
                             const int32_t *context_lens, int32_t max_context_len, int32_t num_seqs,
                             int32_t budget, int32_t recent, int32_t *keep, int32_t *new_lens,
                             void *stream);
+
+/*
+ * The same into arrays that hold nothing yet: a sequence whose length is invalid
+ * raises PKV_DEVERR_CONTEXT and gets -1 in new_lens and in its whole row of keep, a
+ * length that pkv_evict_compact refuses.
+ */
+pkv_status pkv_evict_select_new(const float *key_scores, int64_t score_stride,
+                                const int32_t *context_lens, int32_t max_context_len,
+                                int32_t num_seqs, int32_t budget, int32_t recent, int32_t *keep,
+                                int32_t *new_lens, void *stream);
 
 /*
  * Move the kept rows together: for i < new_lens[s], the K and V rows at position

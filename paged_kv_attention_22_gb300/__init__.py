@@ -121,6 +121,8 @@ def lib():
     L.pkv_paged_decode_attn_scores.restype = ctypes.c_int
     L.pkv_evict_select.argtypes = [P, i64, P, i32, i32, i32, i32, P, P, P]
     L.pkv_evict_select.restype = ctypes.c_int
+    L.pkv_evict_select_new.argtypes = L.pkv_evict_select.argtypes
+    L.pkv_evict_select_new.restype = ctypes.c_int
     rows = [P, i32, P, i32, P, i32, P, i32]  # source and destination tables, keep, new_lens, num_seqs
     L.pkv_evict_compact.argtypes = [P, P] + rows + [i32, i32, i32, i64, P, i64, P, i64, P]
     L.pkv_evict_compact.restype = ctypes.c_int
@@ -537,7 +539,9 @@ def paged_decode_attn_scores(q, k_cache, v_cache, block_tables, context_lens, ma
 
 def evict_select(key_scores, context_lens, budget, recent, keep=None, new_lens=None, stream=None):
     """Positions that stay: the last `recent` and the highest-scoring others, budget
-    in all, ascending. Returns (keep int32 [S, budget], -1 padded, new_lens int32 [S])."""
+    in all, ascending. Returns (keep int32 [S, budget], -1 padded, new_lens int32 [S]).
+    A sequence of invalid length gets -1 in both, which a compaction refuses, unless
+    keep and new_lens are both given: its rows are then left as they were."""
     if stream is None:
         st, keep, new_lens = _calls().evict_select(key_scores, context_lens, budget, recent, keep,
                                                    new_lens, None)

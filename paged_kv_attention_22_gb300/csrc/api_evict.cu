@@ -13,6 +13,36 @@ constexpr int32_t kMaxBudget = 1 << 29;  // the kernels count kept positions, fo
 
 constexpr int32_t kMaxSeqs = 1 << 27;    // of a selection: eight CTAs each
 
+// The two selections; mark_invalid: the second's -1 for sequences of invalid length.
+pkv_status select(const float *key_scores, int64_t score_stride, const int32_t *context_lens, int32_t max_context_len,
+                  int32_t num_seqs, int32_t budget, int32_t recent, int32_t *keep, int32_t *new_lens, bool mark_invalid,
+                  void *stream) {
+  if (num_seqs < 0 || budget <= 0 || recent < 0 || recent > budget || max_context_len <= 0 ||
+      score_stride < max_context_len)
+    return PKV_ERR_INVALID_ARG;
+  if (key_scores == nullptr || context_lens == nullptr || keep == nullptr || new_lens == nullptr)
+    return PKV_ERR_INVALID_ARG;
+  if (max_context_len > pkv::kMaxContext || budget > kMaxBudget || num_seqs > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs == 0) return PKV_OK;
+  int sms = 0;
+  pkv_status st = current_sm_count(&sms);
+  if (st != PKV_OK) return st;
+  pkv::EvictSelectArgs a;
+  a.key_scores = key_scores;
+  a.score_stride = score_stride;
+  a.context_lens = context_lens;
+  a.keep = keep;
+  a.new_lens = new_lens;
+  a.max_context_len = max_context_len;
+  a.num_seqs = num_seqs;
+  a.budget = budget;
+  a.recent = recent;
+  a.mark_invalid = mark_invalid;
+  cudaError_t e = pkv::launch_evict_select(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "evict_select launch");
+  return PKV_OK;
+}
+
 // Checks shared by the two compactions; the arrays are already in `a`.
 pkv_status compact(pkv::EvictCompactArgs &a, const int32_t *src_tables, int32_t src_max_blocks,
                    const int32_t *dst_tables, int32_t dst_max_blocks, const int32_t *keep, int32_t budget,
@@ -64,29 +94,15 @@ extern "C" {
 pkv_status pkv_evict_select(const float *key_scores, int64_t score_stride, const int32_t *context_lens,
                             int32_t max_context_len, int32_t num_seqs, int32_t budget, int32_t recent, int32_t *keep,
                             int32_t *new_lens, void *stream) {
-  if (num_seqs < 0 || budget <= 0 || recent < 0 || recent > budget || max_context_len <= 0 ||
-      score_stride < max_context_len)
-    return PKV_ERR_INVALID_ARG;
-  if (key_scores == nullptr || context_lens == nullptr || keep == nullptr || new_lens == nullptr)
-    return PKV_ERR_INVALID_ARG;
-  if (max_context_len > pkv::kMaxContext || budget > kMaxBudget || num_seqs > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
-  if (num_seqs == 0) return PKV_OK;
-  int sms = 0;
-  pkv_status st = current_sm_count(&sms);
-  if (st != PKV_OK) return st;
-  pkv::EvictSelectArgs a;
-  a.key_scores = key_scores;
-  a.score_stride = score_stride;
-  a.context_lens = context_lens;
-  a.keep = keep;
-  a.new_lens = new_lens;
-  a.max_context_len = max_context_len;
-  a.num_seqs = num_seqs;
-  a.budget = budget;
-  a.recent = recent;
-  cudaError_t e = pkv::launch_evict_select(a, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "evict_select launch");
-  return PKV_OK;
+  return select(key_scores, score_stride, context_lens, max_context_len, num_seqs, budget, recent, keep, new_lens, false,
+                stream);
+}
+
+pkv_status pkv_evict_select_new(const float *key_scores, int64_t score_stride, const int32_t *context_lens,
+                                int32_t max_context_len, int32_t num_seqs, int32_t budget, int32_t recent, int32_t *keep,
+                                int32_t *new_lens, void *stream) {
+  return select(key_scores, score_stride, context_lens, max_context_len, num_seqs, budget, recent, keep, new_lens, true,
+                stream);
 }
 
 pkv_status pkv_evict_compact(void *k_cache, void *v_cache, const int32_t *src_tables, int32_t src_max_blocks,

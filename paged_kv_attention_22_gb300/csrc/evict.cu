@@ -49,6 +49,7 @@ struct SelectParams {
   const int32_t *context_lens;
   int32_t *keep, *new_lens;
   int32_t max_context_len, budget, recent;
+  bool mark_invalid;
 };
 
 // Larger scores have larger keys; NaN sorts below every number; -0 equals 0.
@@ -76,16 +77,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
   const int s = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the CTAs of a cluster leave before its first barrier together, or not at all
   const int ctx = p.context_lens[s];
+  const int me = rank * kSelThreads + tid, all = C * kSelThreads;
+  int32_t *keep = p.keep + static_cast<int64_t>(s) * p.budget;
   if (ctx < 0 || ctx > p.max_context_len) {
-    if (tid == 0 && rank == 0) atomicOr(&g_evict_errors, kErrContext);
+    if (me == 0) atomicOr(&g_evict_errors, kErrContext);
+    if (p.mark_invalid) {
+      if (me == 0) p.new_lens[s] = -1;
+      for (int i = me; i < p.budget; i += all) keep[i] = -1;
+    }
     return;
   }
   const float *score = p.key_scores + s * p.score_stride;
-  int32_t *keep = p.keep + static_cast<int64_t>(s) * p.budget;
   const int new_len = min(ctx, p.budget), recent = min(ctx, p.recent);
   const int old = ctx - recent;         // positions that compete
   const int want = new_len - recent;    // how many of them stay
-  const int me = rank * kSelThreads + tid, all = C * kSelThreads;
   if (me == 0) p.new_lens[s] = new_len;
   for (int i = new_len + me; i < p.budget; i += all) keep[i] = -1;
   for (int i = me; i < recent; i += all) keep[want + i] = old + i;
@@ -514,6 +519,7 @@ cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t stream) {
   p.max_context_len = a.max_context_len;
   p.budget = a.budget;
   p.recent = a.recent;
+  p.mark_invalid = a.mark_invalid;
   // one CTA for a short sequence (its passes take less than the cluster's
   // barriers), a cluster for longer ones
   const unsigned C = a.max_context_len <= kSelAlone ? 1 : kSelCluster;

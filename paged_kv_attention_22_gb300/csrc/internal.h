@@ -234,6 +234,7 @@ struct EvictSelectArgs {
   const int32_t *context_lens;
   int32_t *keep, *new_lens;
   int32_t max_context_len, num_seqs, budget, recent;
+  bool mark_invalid;  // a sequence of invalid length gets -1 everywhere
 };
 cudaError_t launch_evict_select(const EvictSelectArgs &a, cudaStream_t stream);
 

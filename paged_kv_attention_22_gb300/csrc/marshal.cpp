@@ -247,9 +247,11 @@ PyObject *evict_select(Args &a) {
   at::Tensor keep = given[0] != nullptr ? *given[0] : at::empty({S, budget > 0 ? budget : 0}, lens.options());
   at::Tensor new_lens = given[1] != nullptr ? *given[1] : at::empty({S}, lens.options());
   require(keep.size(0) == S && keep.size(1) == (budget > 0 ? budget : 0) && new_lens.size(0) == S);
-  const pkv_status st =
-      pkv_evict_select(ptr<float>(scores), scores.size(1), ptr<int32_t>(lens), size32(scores, 1), size32(scores, 0),
-                       budget, recent, ptr<int32_t>(keep), ptr<int32_t>(new_lens), a.stream());
+  // memory allocated here may hold an earlier step's selection
+  const auto select = given[0] != nullptr && given[1] != nullptr ? pkv_evict_select : pkv_evict_select_new;
+  const pkv_status st = select(ptr<float>(scores), scores.size(1), ptr<int32_t>(lens), size32(scores, 1),
+                               size32(scores, 0), budget, recent, ptr<int32_t>(keep), ptr<int32_t>(new_lens),
+                               a.stream());
   return Py_BuildValue("(iNN)", static_cast<int>(st), THPVariable_Wrap(keep), THPVariable_Wrap(new_lens));
 }
 

@@ -48,6 +48,15 @@ def test_select_refuses(L):
     assert call(S=0) == pkv.PKV_OK
 
 
+def test_select_into_new_arrays_refuses(L):
+    def call(ks=FAKE, ld=64, S=2, B=16, R=4, keep=FAKE, nl=FAKE):
+        return L.pkv_evict_select_new(ks, ld, FAKE, 64, S, B, R, keep, nl, None)
+    for bad in (dict(ks=None), dict(keep=None), dict(nl=None), dict(S=-1), dict(B=0), dict(R=17), dict(ld=63)):
+        assert call(**bad) == pkv.PKV_ERR_INVALID_ARG
+    assert call(B=(1 << 29) + 1) == pkv.PKV_ERR_UNSUPPORTED
+    assert call(S=0) == pkv.PKV_OK
+
+
 def test_compact_refuses(L):
     def call(k=FAKE, v=FAKE, src=FAKE, sb=4, dst=FAKE, db=4, keep=FAKE, B=16, nl=FAKE, S=2, H=8, D=128, bs=16, NB=64,
              ks=None, ld=0, dks=None, dld=0):
@@ -200,6 +209,32 @@ def test_select_reports_invalid_lengths(L):
     pkv.evict_select(x, torch.tensor([10, -1, 11, 2], dtype=torch.int32, device="cuda"), 3, 1, keep=keep, new_lens=new)
     assert pkv.check_device_errors() == pkv.DEVERR_CONTEXT
     assert new.tolist() == [3, 77, 77, 2] and bool((keep[1:3] == 77).all()) and keep[3].tolist() == [0, 1, -1]
+
+
+@gpu
+def test_invalid_length_moves_nothing_where_the_call_makes_the_arrays(L):
+    """The arrays that a call without keep and new_lens makes may be memory of an
+    earlier step's: a sequence of invalid length has no row of it in them, and the
+    compaction behind the call refuses it."""
+    S, block, heads, budget = 3, 16, 1, 20
+    bf = torch.randn(2, S * 3, block, heads, 128, generator=torch.Generator().manual_seed(9)).to(torch.bfloat16)
+    k, v = bf.cuda()
+    bt = torch.arange(S * 3, dtype=torch.int32, device="cuda").view(S, 3)
+    scores = torch.rand(S, 48, device="cuda")
+    for lens in ([48, 48, 48], [48, 49, -1]):
+        before = [x.clone() for x in (k, v, scores)]
+        keep, new = pkv.evict_select(scores, torch.tensor(lens, dtype=torch.int32, device="cuda"), budget, 4)
+        pkv.evict_compact(k, v, bt, bt, keep, new, scores, scores)
+        flags = pkv.check_device_errors()
+        bad = [s for s in range(S) if not 0 <= lens[s] <= 48]
+        assert flags == (pkv.DEVERR_CONTEXT if bad else 0)
+        assert new.tolist() == [-1 if s in bad else budget for s in range(S)]
+        for s in bad:
+            assert bool((keep[s] == -1).all())
+            for x, y in zip(before[:2], (k, v)):
+                assert torch.equal(x[bt[s].long()], y[bt[s].long()])
+            assert torch.equal(before[2][s], scores[s])
+        del keep, new               # the next call's arrays are these again
 
 
 # ------------------------------------------------------------------ GPU: compaction
