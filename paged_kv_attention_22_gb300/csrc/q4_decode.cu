@@ -757,13 +757,18 @@ __global__ void __launch_bounds__(256) q4_rows_kernel(const Q4PrefillRowsArgs a)
 template <int NG, int kWarps, bool kRanges>
 cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream) {
   auto kernel = q4_decode_kernel<NG, kWarps, kRanges>;
-  int smem = Q4DecodeSmem<NG, kWarps>::kTotal + kWarps * kQueryBytes;
-  if (kRanges) smem += static_cast<int>(sizeof(int64_t)) * (p.num_seqs + 1) + static_cast<int>(sizeof(int)) * p.num_seqs;
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // beside the rings and queries, by ranges, what grows with the sequences. The limit
+  // is the kernel's, not the call's: another host thread may be between its own two
+  // lines here, so it is always set to the most that any call wants.
+  constexpr int kFixed = Q4DecodeSmem<NG, kWarps>::kTotal + kWarps * kQueryBytes;
+  constexpr auto of_seqs = [](int n) { return kRanges ? 8 * (n + 1) + 4 * n : 0; };
+  constexpr int kMost = kFixed + of_seqs(kQ4MaxRangeSeqs);
+  static_assert(kMost <= 227 * 1024, "shared memory");
+  if (kMost > 48 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kernel, grid, dim3(kWarps * 32), smem, stream, p);
+  return launch_pdl(kernel, grid, dim3(kWarps * 32), kFixed + of_seqs(p.num_seqs), stream, p);
 }
 
 // k: the accumulated weights, or null; added here by ranges with at most
@@ -771,7 +776,6 @@ cudaError_t launch_shape(const Q4DecodeParams &p, dim3 grid, cudaStream_t stream
 template <int NG>
 cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, const KeyScoresParams *k,
                         cudaStream_t stream) {
-  static_assert(Q4DecodeSmem<NG, 16>::kTotal + 16 * kQueryBytes + 12 * kQ4MaxRangeSeqs + 8 <= 227 * 1024, "shared memory of the ranges");
   const dim3 pairs(p.num_kv_heads, p.num_seqs);
   if (plan.range_ctas > 0) {
     cudaError_t e = launch_shape<NG, 16, true>(p, dim3(plan.range_ctas), stream);
@@ -795,10 +799,7 @@ cudaError_t launch_plan(const Q4DecodeParams &p, const Q4DecodePlan &plan, const
     const size_t smem = sizeof(int64_t) * (p.num_seqs + 1) + (k != nullptr ? sizeof(float) * p.num_q_heads : 0);
     const auto kernel = many ? (pairs_of ? q4_merge_kernel<kMergeWarps, 2> : q4_merge_kernel<kMergeWarps, 4>)
                              : (pairs_of ? q4_merge_kernel<1, 2> : q4_merge_kernel<1, 4>);
-    if (smem > 40 * 1024) {  // beside the static arrays
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-      if (e != cudaSuccess) return e;
-    }
+    static_assert(8 * (kQ4MaxRangeSeqs + 1) + 4 * kMaxScoredHeads <= 40 * 1024, "no attribute needed, beside the static arrays");
     return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas + chunks * p.num_seqs)), dim3(kMergeWarps * 32), smem,
                       stream, p, warps, k != nullptr ? *k : KeyScoresParams{},
                       static_cast<int32_t>(chunks * p.num_seqs), static_cast<int32_t>(chunks));

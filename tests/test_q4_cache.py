@@ -1,6 +1,9 @@
 """The 4-bit cache: quantising store, read-back, decode and prefill, against the
 plain 64-bit implementation in q4_plain.py; and the refusals of each call."""
+import ctypes
 import math
+import os
+import subprocess
 
 import pytest
 import torch
@@ -760,6 +763,79 @@ def test_prefill_refuses_segments_alike_on_both_ways(L, q_lens, k_lens, window, 
     assert bool((o[~written] == 9.0).all()) and bool((l[~written] == 9.0).all())
     out, lse, tol_o, tol_l = (x[:rows][written] for x in (out, lse, tol_o, tol_l))
     assert bool(((o[written].double() - out).abs() <= tol_o).all()) and bool(((l[written].double() - lse).abs() <= tol_l).all())
+
+
+THREADS = r"""
+#include <thread>
+#include "pkv.h"
+struct Call {
+  const void *q, *kc, *kp, *vc, *vp;
+  const int32_t *bt, *lens;
+  int32_t max_blocks, bound, seqs, block;
+  int64_t num_blocks;
+  void *out, *ws;
+  size_t ws_bytes;
+  void *stream;
+};
+static pkv_status one(const Call &c) {
+  if (c.kp != nullptr)
+    return pkv_paged_decode_attn_q4(c.q, c.kc, c.kp, c.vc, c.vp, c.bt, c.max_blocks, c.lens, c.bound, c.seqs, 2, 1, 128, 32,
+                                    c.block, c.num_blocks, 0.088f, 0, c.out, nullptr, nullptr, 0, c.ws, c.ws_bytes, c.stream);
+  return pkv_paged_decode_attn(c.q, c.kc, c.vc, c.bt, c.max_blocks, c.lens, c.bound, c.seqs, 2, 1, 128, c.block, c.num_blocks,
+                               0.088f, 0, c.out, nullptr, c.ws, c.ws_bytes, c.stream);
+}
+// n calls of each of two threads; how many failed
+extern "C" void two_threads(const Call *calls, int n, int *failed) {
+  auto run = [&](int i) {
+    for (int k = 0; k < n; ++k) failed[i] += one(calls[i]) != PKV_OK;
+  };
+  std::thread other(run, 1);
+  run(0);
+  other.join();
+}
+"""
+
+
+@gpu
+@pytest.mark.parametrize("q4", [True])
+def test_host_threads_with_calls_of_their_own_sizes(L, q4, tmp_path):
+    """Two host threads, each with its stream, buffers and number of sequences: every
+    call is launched."""
+    (tmp_path / "threads.cpp").write_text(THREADS)
+    here = os.path.dirname(pkv.LIBRARY_PATH)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-pthread", str(tmp_path / "threads.cpp"), "-I",
+                    os.path.join(os.path.dirname(here), "include"), "-L", here, "-Wl,-rpath," + here, "-l:libpkv.so", "-o",
+                    str(tmp_path / "threads.so")], check=True)
+    block, ctx, bound = 16, 16, 20000
+    P, i32 = ctypes.c_void_p, ctypes.c_int32
+
+    class Call(ctypes.Structure):
+        _fields_ = ([(n, P) for n in ("q", "kc", "kp", "vc", "vp", "bt", "lens")] +
+                    [(n, i32) for n in ("max_blocks", "bound", "seqs", "block")] +
+                    [("num_blocks", ctypes.c_int64), ("out", P), ("ws", P), ("ws_bytes", ctypes.c_size_t), ("stream", P)])
+
+    c = Q.Cache(18, [ctx], 1, block, 32)
+    kc, vc, _ = c.cuda()
+    k16 = torch.randn(c.num_blocks, block, 1, 128).to(torch.bfloat16).cuda()
+    caches = [x.data_ptr() for x in (*kc, *vc)] if q4 else [k16.data_ptr(), None, k16.data_ptr(), None]
+    calls, keep = (Call * 2)(), []
+    for i, S in enumerate((1, 1000)):
+        q = torch.randn(S, 2, 128).to(torch.bfloat16).cuda()
+        bt = torch.full((S, bound // block), -1, dtype=torch.int32, device="cuda")
+        bt[:, 0] = int(c.tables[0, 0])
+        lens = torch.full((S,), ctx, dtype=torch.int32, device="cuda")
+        out, stream = torch.full_like(q, float("nan")), torch.cuda.Stream()
+        ws = pkv.new_q4_decode_workspace(S, 2, 1, bound) if q4 else pkv.new_decode_workspace(S, 2, 1, 128, bound)
+        calls[i] = Call(q.data_ptr(), *caches, bt.data_ptr(), lens.data_ptr(), bt.shape[1], bound, S, block, c.num_blocks,
+                        out.data_ptr(), ws.data_ptr(), ws.numel(), stream.cuda_stream)
+        keep.append((q, bt, lens, out, stream, ws))
+    torch.cuda.synchronize()
+    failed = (ctypes.c_int * 2)()
+    ctypes.CDLL(str(tmp_path / "threads.so")).two_threads(calls, 20000, failed)
+    torch.cuda.synchronize()
+    assert list(failed) == [0, 0]
+    assert all(bool(torch.isfinite(k[3]).all()) for k in keep)
+    assert pkv.check_device_errors() == 0
 
 
 @gpu
