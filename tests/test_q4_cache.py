@@ -4,6 +4,7 @@ import ctypes
 import math
 import os
 import subprocess
+import threading
 
 import pytest
 import torch
@@ -616,6 +617,63 @@ def test_two_streams_with_workspaces_of_their_own(L):
     for i in range(2):
         for o, l in got[i]:
             assert torch.equal(o, alone[i][0]) and torch.equal(l, alone[i][1])
+    assert pkv.check_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("call", ["decode_q4", "prefill_q4", "store_q4", "decode", "scores", "prefill", "select"])
+def test_first_call_of_a_host_thread(L, call):
+    """A thread that has made no CUDA call yet: the same bits as from the main one."""
+    c = Q.Cache(19, [40], 2, 16, 32)
+    kc, vc, bt = c.cuda()
+    g = torch.Generator().manual_seed(3)
+    k16 = torch.randn(c.num_blocks, 16, 2, 128, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(1, 4, 128, generator=g).to(torch.bfloat16).cuda()
+    out, lse, scores = torch.zeros_like(q), torch.zeros(1, 4, device="cuda"), torch.zeros(1, 40, device="cuda")
+    cl, cu_q, cu_k = torch.tensor([40], dtype=torch.int32, device="cuda"), _cu([1]), _cu([40])
+    keep, new = torch.zeros(1, 9, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    w4, wp = pkv.new_q4_decode_workspace(1, 4, 2, 40), pkv.new_q4_prefill_workspace(1, 40, 40, 2)
+    w16, ws = pkv.new_decode_workspace(1, 4, 2, 128, 40), pkv.new_decode_scores_workspace(1, 4, 2, 40)
+    stream = torch.cuda.current_stream()
+
+    def run():
+        if call == "decode_q4":
+            pkv.paged_decode_attn_q4(q, kc, vc, bt, cl, 40, SCALE, out=out, lse=lse, workspace=w4, stream=stream)
+        elif call == "prefill_q4":
+            pkv.paged_prefill_attn_q4(q, kc, vc, cu_q, cu_k, bt, 1, 40, 40, SCALE, out=out, lse=lse, workspace=wp, stream=stream)
+        elif call == "store_q4":
+            pkv.kv_store_q4(k16[0, :1], k16[1, :1], kc, vc, cl * 0, stream=stream)
+        elif call == "decode":
+            pkv.paged_decode_attn(q, k16, k16, bt, cl, 40, SCALE, out=out, lse=lse, workspace=w16, stream=stream)
+        elif call == "scores":
+            pkv.paged_decode_attn_scores(q, k16, k16, bt, cl, 40, SCALE, scores, out=out, lse=lse, workspace=ws, stream=stream)
+        elif call == "prefill":
+            pkv.paged_prefill_attn(q, k16, k16, cu_q, cu_k, bt, 1, 40, SCALE, out=out, lse=lse, stream=stream)
+        else:
+            pkv.evict_select(scores, cl, 9, 2, keep=keep, new_lens=new, stream=stream)
+
+    results = []
+    for first in (False, True):
+        for x in (out, lse, scores, keep, new):
+            x.zero_()
+        torch.cuda.synchronize()
+        raised = []
+
+        def body():
+            try:
+                run()
+            except Exception as e:      # reported below: an exception would end in the thread
+                raised.append(e)
+        if first:
+            t = threading.Thread(target=body)
+            t.start()
+            t.join()
+        else:
+            body()
+        assert not raised, raised
+        torch.cuda.synchronize()
+        results.append([x.clone() for x in (out, lse, scores, keep, new, kc[0], vc[0])])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
     assert pkv.check_device_errors() == 0
 
 
