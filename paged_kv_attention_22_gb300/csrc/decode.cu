@@ -929,7 +929,10 @@ cudaError_t launch_variant(const DecodeArgs &a, const CUtensorMap &k_map,
   static_assert(L::total(kDecodeMaxSeqs) <= 227 * 1024, "decode shared memory");
   auto kern = decode_kernel<G, HGM, NS, kLogits>;
   const int smem = L::total(a.num_seqs);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the limit is the kernel's, not the call's: another host thread may be between its
+  // own two calls here, so it is always set to the most that any call wants
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       L::total(kDecodeMaxSeqs));
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3(a.grid), dim3((p.hg + 2) * 32), smem, stream, k_map, v_map, q_map,
                  kn_map, vn_map, p);

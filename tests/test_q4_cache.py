@@ -855,7 +855,7 @@ extern "C" void two_threads(const Call *calls, int n, int *failed) {
 
 
 @gpu
-@pytest.mark.parametrize("q4", [True])
+@pytest.mark.parametrize("q4", [False, True])
 def test_host_threads_with_calls_of_their_own_sizes(L, q4, tmp_path):
     """Two host threads, each with its stream, buffers and number of sequences: every
     call is launched."""
