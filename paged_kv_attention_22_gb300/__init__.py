@@ -4,8 +4,8 @@ The functions here have the names of the C entry points in ``include/pkv.h``
 and do argument marshalling only: they check dtypes and shapes of torch
 tensors, pass their device pointers and the current CUDA stream to the C ABI,
 and allocate outputs the caller did not supply. (For 4-bit caches and eviction
-the checks are compiled, in the module ``_marshal`` beside the library; those
-calls also want every tensor on the current device.) Every step of the computation
+the checks are compiled, in the module ``_marshal`` beside the library, which
+only those calls load; they also want every tensor on the current device.) Every step of the computation
 runs in the library's CUDA kernels. There is no fallback: if libpkv.so has not
 been built, or a call fails, an exception is raised.
 
@@ -45,7 +45,7 @@ DEVERR_SEQLENS = 0x8
 DEVERR_TIMEOUT = 0x10
 
 _lib = None
-_m = None  # the _marshal module: argument marshalling of the calls below lib()
+_m = None  # the _marshal module (see _calls)
 
 
 class PkvError(RuntimeError):
@@ -56,19 +56,20 @@ class PkvError(RuntimeError):
         super().__init__(f"{what}: {name}" + (f" ({detail})" if detail else ""))
 
 
+def _require(path):
+    if not os.path.exists(path):
+        raise ImportError(
+            f"{path} is missing: build it with "
+            "`python -m paged_kv_attention_22_gb300.build` (nvcc, sm_103a)")
+
+
 def lib():
     """The loaded libpkv.so (ctypes), with argument types declared."""
-    global _lib, _m
+    global _lib
     if _lib is not None:
         return _lib
-    for path in (LIBRARY_PATH, MARSHAL_PATH):
-        if not os.path.exists(path):
-            raise ImportError(
-                f"{path} is missing: build it with "
-                "`python -m paged_kv_attention_22_gb300.build` (nvcc, sm_103a)")
+    _require(LIBRARY_PATH)
     L = ctypes.CDLL(LIBRARY_PATH)
-    from . import _marshal
-    _m = _marshal
     P, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                             ctypes.c_size_t)
     L.pkv_status_string.argtypes = [ctypes.c_int]
@@ -391,8 +392,12 @@ def new_q4_cache(num_blocks, block_size, num_kv_heads, group_size=32, device="cu
 
 def _calls():
     """The _marshal module, which checks arguments and calls the C entries."""
+    global _m
     if _m is None:
         lib()
+        _require(MARSHAL_PATH)
+        from . import _marshal
+        _m = _marshal
     return _m
 
 

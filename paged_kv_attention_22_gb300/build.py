@@ -6,7 +6,9 @@ library needs only the driver at run time; it builds the same way on x86_64
 and aarch64 hosts.
 
 Beside it goes _marshal.so, the compiled part of the Python binding, built by
-g++ against the installed torch (and rebuilt when torch changes).
+g++ against the installed torch (and rebuilt when torch changes). The library
+needs neither torch nor Python's headers: build_library() makes it alone, and
+build() has it in place before anything that concerns _marshal.so can fail.
 """
 import os
 import subprocess
@@ -20,6 +22,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libpkv.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_SOURCE = "marshal.cpp"
 MARSHAL_TORCH = os.path.join(BUILD_DIR, "marshal_torch_version")  # what MARSHAL was built against
 SOURCES = ["kv_store.cu", "decode.cu", "prefill.cu", "api.cu", "decode_noalloc.cu",
            "q4_cache.cu", "q4_decode.cu", "api_q4.cu", "evict.cu", "api_evict.cu",
@@ -44,7 +47,7 @@ def _marshal_command(torch_dir: str):
                os.path.join(torch_dir, "include"),
                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                os.path.join(_cuda_home(), "include")]
-    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "marshal.cpp")]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, MARSHAL_SOURCE)]
             + ["-I" + d for d in include] + ["-L" + lib, "-L" + HERE, "-Wl,-rpath,$ORIGIN"]
             + ["-l:libpkv.so", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
 
@@ -54,23 +57,37 @@ def _torch():
     return os.path.dirname(torch.__file__), torch.__version__
 
 
-def _needs_rebuild() -> bool:
-    if not os.path.exists(LIBRARY) or not os.path.exists(MARSHAL) \
-            or not os.path.exists(MARSHAL_TORCH):
+def _older(target: str, deps) -> bool:
+    if not os.path.exists(target):
+        return True
+    made = os.path.getmtime(target)
+    include = os.path.join(ROOT, "include")
+    deps = [os.path.join(CSRC, f) for f in deps] + [os.path.join(include, f) for f in os.listdir(include)]
+    return any(os.path.getmtime(d) > made for d in deps + [os.path.abspath(__file__)])
+
+
+def _library_stale() -> bool:
+    return _older(LIBRARY, [f for f in os.listdir(CSRC) if f != MARSHAL_SOURCE])
+
+
+def _marshal_stale() -> bool:
+    if _older(MARSHAL, [MARSHAL_SOURCE]) or not os.path.exists(MARSHAL_TORCH):
         return True
     with open(MARSHAL_TORCH) as f:
-        if f.read() != _torch()[1]:
-            return True
-    lib_time = min(os.path.getmtime(LIBRARY), os.path.getmtime(MARSHAL))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    include = os.path.join(ROOT, "include")
-    deps += [os.path.join(include, f) for f in os.listdir(include)]
-    deps.append(os.path.abspath(__file__))
-    return any(os.path.getmtime(d) > lib_time for d in deps)
+        return f.read() != _torch()[1]
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and not _needs_rebuild():
+def _link(cmd, target: str) -> None:
+    tmp = target + ".tmp"
+    proc = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError("link failed:\n" + proc.stdout + proc.stderr)
+    os.replace(tmp, target)
+
+
+def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """libpkv.so, if it is missing or older than its sources."""
+    if not force and not _library_stale():
         return LIBRARY
     os.makedirs(BUILD_DIR, exist_ok=True)
     nvcc = _nvcc()
@@ -81,15 +98,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         proc = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, cmd, proc
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
-        # the object first: linking it needs the library
-        marshal_obj = os.path.join(BUILD_DIR, "marshal.o")
-        torch_dir, torch_version = _torch()
-        cmd = [a for a in _marshal_command(torch_dir) if not a.startswith(("-l", "-L", "-Wl", "-shared"))]
-        marshal = pool.submit(subprocess.run, cmd + ["-c", "-o", marshal_obj], capture_output=True,
-                              text=True)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
         results = list(pool.map(compile_one, SOURCES))
-        marshal = marshal.result()
     errors = []
     for src, obj, cmd, proc in results:
         if verbose or proc.returncode != 0:
@@ -98,22 +108,34 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             errors.append(src)
     if errors:
         raise RuntimeError("nvcc failed for " + ", ".join(errors))
-    tmp = LIBRARY + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp] + [r[1] for r in results]
-    proc = subprocess.run(cmd, capture_output=True, text=True)
+    _link([nvcc, *ARCH, "-shared"] + [r[1] for r in results], LIBRARY)
+    return LIBRARY
+
+
+def _compile_marshal(force: bool):
+    """marshal.o and the command that links it (which needs the library), or None."""
+    if not force and not _marshal_stale():
+        return None
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    torch_dir, torch_version = _torch()
+    obj = os.path.join(BUILD_DIR, "marshal.o")
+    cmd = [a for a in _marshal_command(torch_dir) if not a.startswith(("-l", "-L", "-Wl", "-shared"))]
+    proc = subprocess.run(cmd + ["-c", "-o", obj], capture_output=True, text=True)
     if proc.returncode != 0:
-        raise RuntimeError("link failed:\n" + proc.stdout + proc.stderr)
-    os.replace(tmp, LIBRARY)
-    if marshal.returncode != 0:
-        raise RuntimeError("g++ failed for marshal.cpp:\n" + marshal.stdout + marshal.stderr)
-    tmp = MARSHAL + ".tmp"
-    cmd = [marshal_obj if a.endswith("marshal.cpp") else a for a in _marshal_command(torch_dir)]
-    proc = subprocess.run(cmd + ["-o", tmp], capture_output=True, text=True)
-    if proc.returncode != 0:
-        raise RuntimeError("link failed:\n" + proc.stdout + proc.stderr)
-    os.replace(tmp, MARSHAL)
-    with open(MARSHAL_TORCH, "w") as f:
-        f.write(torch_version)
+        raise RuntimeError("g++ failed for marshal.cpp:\n" + proc.stdout + proc.stderr)
+    return [obj if a.endswith(MARSHAL_SOURCE) else a for a in _marshal_command(torch_dir)], torch_version
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Both, the two compilations side by side."""
+    with ThreadPoolExecutor(max_workers=1) as pool:
+        marshal = pool.submit(_compile_marshal, force)
+        build_library(force, verbose, extra_flags)
+    made = marshal.result()
+    if made is not None:
+        _link(made[0], MARSHAL)
+        with open(MARSHAL_TORCH, "w") as f:
+            f.write(made[1])
     return LIBRARY
 
 
