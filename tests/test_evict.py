@@ -237,6 +237,37 @@ def test_invalid_length_moves_nothing_where_the_call_makes_the_arrays(L):
         del keep, new               # the next call's arrays are these again
 
 
+def _select_sorted(row, n, budget, recent):
+    """select_plain of one long sequence: a stable sort, NaN behind every number."""
+    r = min(recent, n)
+    order = torch.sort(-row[:n - r].double(), stable=True).indices
+    return torch.cat([order[:min(n, budget) - r].sort().values, torch.arange(n - r, n)])
+
+
+def test_sorted_selection_is_the_plain_one():
+    for kind in ("plain", "ties", "equal", "signed", "special"):
+        x = _scores(kind, 1, 700, 3)
+        for n, budget, recent in ((700, 300, 20), (699, 1, 0), (700, 699, 5), (3, 9, 1)):
+            assert _select_sorted(x[0], n, budget, recent).tolist() == select_plain(x, [n], budget, recent)[0]
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "signed", "special"])
+@pytest.mark.parametrize("lens,budget,recent", [
+    ([65537, 65536, 70000, 1], 30000, 64), ([131073], 131072, 0), ([409600, 409599], 200000, 1000),   # keys in shared memory
+    ([409601, 5, 300000], 1000, 100), ([450000], 449999, 64)])                                         # read again each pass
+def test_select_of_very_long_sequences(L, kind, lens, budget, recent):
+    S, width = len(lens), max(lens)
+    x = _scores(kind, S, width, sum(lens))
+    keep, new = pkv.evict_select(x.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), budget, recent)
+    assert pkv.check_device_errors() == 0
+    for s, n in enumerate(lens):
+        want = _select_sorted(x[s], n, budget, recent)
+        assert int(new[s]) == len(want) == min(n, budget)
+        got = keep[s].cpu()
+        assert torch.equal(got[:len(want)].long(), want) and bool((got[len(want):] == -1).all())
+
+
 # ------------------------------------------------------------------ GPU: compaction
 
 def _fresh_tables(lens, block, first):
