@@ -406,6 +406,10 @@ size_t pkv_prefill_q4_workspace_size(int32_t num_seqs, int32_t total_k, int32_t 
  *   total_k    host int: an upper bound of cu_seqlens_k[num_seqs]; a segment
  *              that ends past it raises PKV_DEVERR_SEQLENS and is not written
  *   workspace  device, >= pkv_prefill_q4_workspace_size(...) bytes
+ * An invalid table entry that a segment's queries see raises PKV_DEVERR_BLOCK; that
+ * segment's rows are then undefined (which of the two ways below the call takes
+ * decides what stands for the missing keys), the other segments' are not touched
+ * by it.
  * num_seqs is at most 65535. With few query tokens over many keys the call runs
  * each row through the decode kernels instead of widening the keys (the same
  * sums in another order); it then takes no notice of PKV_DEVERR_TIMEOUT.

@@ -823,6 +823,23 @@ def test_prefill_refuses_segments_alike_on_both_ways(L, q_lens, k_lens, window, 
     assert bool(((o[written].double() - out).abs() <= tol_o).all()) and bool(((l[written].double() - lse).abs() <= tol_l).all())
 
 
+@gpu
+@pytest.mark.parametrize("q_lens,k_lens", [([3, 2, 1], [2000, 1500, 1000]), ([100, 80, 90], [300, 200, 150])])  # by rows, widened
+def test_prefill_reports_bad_table_entries_and_attends_the_other_segments(L, q_lens, k_lens):
+    c = Q.Cache(16, k_lens, 2, 16, 32)
+    q = torch.randn(sum(q_lens), 4, 128, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    out, lse, tol_o, tol_l = _prefill_plain(c, q, q_lens, 2, 0)
+    kc, vc, bt = c.cuda()
+    for bad in (-1, -7, c.num_blocks, 2 ** 31 - 1):
+        bt[1, 1] = bad
+        o, l = pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu(q_lens), _cu(k_lens), bt, max(q_lens), max(k_lens), sum(k_lens),
+                                         SCALE)
+        assert pkv.check_device_errors() == pkv.DEVERR_BLOCK
+        good = list(range(q_lens[0])) + list(range(q_lens[0] + q_lens[1], sum(q_lens)))
+        assert bool(((o[good].cpu().double() - out[good]).abs() <= tol_o[good]).all())
+        assert bool(((l[good].cpu().double() - lse[good]).abs() <= tol_l[good]).all())
+
+
 THREADS = r"""
 #include <thread>
 #include "pkv.h"
