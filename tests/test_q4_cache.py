@@ -840,6 +840,24 @@ def test_prefill_reports_bad_table_entries_and_attends_the_other_segments(L, q_l
         assert bool(((l[good].cpu().double() - lse[good]).abs() <= tol_l[good]).all())
 
 
+@gpu
+@pytest.mark.parametrize("window", [0, 50])
+def test_prefill_by_rows_of_more_rows_than_ranges_take(L, window):
+    """1,280 query rows in 256 short segments: more sequences than a decode by ranges
+    takes, fewer microseconds than widening."""
+    g = torch.Generator().manual_seed(6)
+    q_lens = [8, 0, 5, 4, 1, 16, 2, 4] * 32
+    k_lens = [n + int(torch.randint(1, 200, (), generator=g)) for n in q_lens]
+    c = Q.Cache(17, k_lens, 1, 16, 64)
+    q = torch.randn(sum(q_lens), 2, 128, generator=g).to(torch.bfloat16)
+    out, lse, tol_o, tol_l = _prefill_plain(c, q, q_lens, 2, window)
+    kc, vc, bt = c.cuda()
+    o, l = pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu(q_lens), _cu(k_lens), bt, max(q_lens), max(k_lens), sum(k_lens), SCALE,
+                                     sliding_window=window)
+    assert pkv.check_device_errors() == 0
+    assert bool(((o.cpu().double() - out).abs() <= tol_o).all()) and bool(((l.cpu().double() - lse).abs() <= tol_l).all())
+
+
 THREADS = r"""
 #include <thread>
 #include "pkv.h"
