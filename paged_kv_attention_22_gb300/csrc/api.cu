@@ -521,18 +521,19 @@ size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t max_seqlen_q) {
   return 0;
 }
 
-}  // extern "C"
-
-pkv_status pkv::prefill_segments(const void *q, const void *k_cache, const void *v_cache,
-                                 const int32_t *cu_seqlens_q, const int32_t *k_end,
-                                 const int32_t *k_begin, const int32_t *block_tables,
-                                 int32_t max_blocks_per_seq, int32_t num_seqs, int32_t total_q,
-                                 int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_q_heads,
-                                 int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-                                 int64_t num_blocks, float scale, int32_t sliding_window, void *out,
-                                 float *lse, void *stream) {
+pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                  int32_t max_seqlen_k, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                  int64_t num_blocks, float scale, int32_t sliding_window,
+                                  void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+  (void)workspace;
+  (void)workspace_bytes;
   if (k_cache == nullptr || v_cache == nullptr || cu_seqlens_q == nullptr ||
-      k_end == nullptr || k_begin == nullptr || block_tables == nullptr)
+      cu_seqlens_k == nullptr || block_tables == nullptr)
     return PKV_ERR_INVALID_ARG;
   if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
       !std::isfinite(scale) || sliding_window < 0)
@@ -550,8 +551,7 @@ pkv_status pkv::prefill_segments(const void *q, const void *k_cache, const void 
 
   pkv::PrefillArgs a;
   a.cu_seqlens_q = cu_seqlens_q;
-  a.k_end = k_end;
-  a.k_begin = k_begin;
+  a.cu_seqlens_k = cu_seqlens_k;
   a.block_tables = block_tables;
   a.out = out;
   a.lse = lse;
@@ -590,26 +590,6 @@ pkv_status pkv::prefill_segments(const void *q, const void *k_cache, const void 
   cudaError_t e = pkv::launch_prefill(a, qmap, kmap, vmap, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
   return PKV_OK;
-}
-
-extern "C" {
-
-pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void *v_cache,
-                                  const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
-                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
-                                  int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
-                                  int32_t max_seqlen_k, int32_t num_q_heads,
-                                  int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-                                  int64_t num_blocks, float scale, int32_t sliding_window,
-                                  void *out, float *lse, void *workspace, size_t workspace_bytes,
-                                  void *stream) {
-  (void)workspace;
-  (void)workspace_bytes;
-  if (cu_seqlens_k == nullptr) return PKV_ERR_INVALID_ARG;
-  return pkv::prefill_segments(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k + 1, cu_seqlens_k,
-                               block_tables, max_blocks_per_seq, num_seqs, total_q, max_seqlen_q,
-                               max_seqlen_k, num_q_heads, num_kv_heads, head_dim, block_size,
-                               num_blocks, scale, sliding_window, out, lse, stream);
 }
 
 pkv_status pkv_read_device_errors_async(uint32_t *host_flags, void *stream) {

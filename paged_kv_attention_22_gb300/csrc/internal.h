@@ -107,8 +107,7 @@ cudaError_t decode_error_word(uint32_t **word);
 
 // ---------------------------------------------------------------- prefill
 struct PrefillArgs {
-  const int32_t *cu_seqlens_q;
-  const int32_t *k_end, *k_begin;  // [S]: segment s has k_end[s] - k_begin[s] keys
+  const int32_t *cu_seqlens_q, *cu_seqlens_k;
   const int32_t *block_tables;
   void *out;
   float *lse;
@@ -135,15 +134,6 @@ inline int32_t prefill_box_rows(int32_t block_size) {
 cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
                            const CUtensorMap &k_map, const CUtensorMap &v_map,
                            cudaStream_t stream);
-// pkv_paged_prefill_attn, its segments' keys given as two arrays (see PrefillArgs): a
-// segment with fewer keys than queries, -1 for one, is refused.
-pkv_status prefill_segments(const void *q, const void *k_cache, const void *v_cache,
-                            const int32_t *cu_seqlens_q, const int32_t *k_end, const int32_t *k_begin,
-                            const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t num_seqs,
-                            int32_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
-                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
-                            int32_t block_size, int64_t num_blocks, float scale,
-                            int32_t sliding_window, void *out, float *lse, void *stream);
 cudaError_t take_prefill_errors(cudaStream_t stream, uint32_t *flags);
 cudaError_t prefill_error_word(uint32_t **word);
 
@@ -187,7 +177,7 @@ struct Q4GatherArgs {
   Q4CacheArgs cache;
   const int32_t *cu_seqlens_q, *cu_seqlens_k, *block_tables;
   void *ws_k, *ws_v;
-  int32_t *ws_tables, *ws_k_end, *ws_k_begin;
+  int32_t *ws_tables, *ws_cu_k;
   int32_t max_blocks, ws_max_blocks, num_seqs, max_seqlen_q, max_seqlen_k, total_k;
   int32_t window, num_sms;
 };

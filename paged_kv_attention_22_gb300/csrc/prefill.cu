@@ -113,7 +113,7 @@ constexpr float kLazyBound = 256.0f;  // 2^kLazyMax: the largest tile sum taken 
 static_assert(kLazyBound == 256.0f && kLazyMax == 8.0f, "kLazyBound is 2^kLazyMax");
 
 struct PrefillParams {
-  const int32_t *cu_q, *k_end, *k_begin, *block_tables;  // segment s has k_end[s] - k_begin[s] keys
+  const int32_t *cu_q, *cu_k, *block_tables;
   __nv_bfloat16 *out;
   float *lse;
   int32_t max_blocks, num_seqs, total_q, max_seqlen_q, max_seqlen_k;
@@ -209,7 +209,7 @@ __device__ __forceinline__ bool make_item(const PrefillParams &p, int lin, bool 
   it.q0 = p.cu_q[it.s];
   const int q1 = p.cu_q[it.s + 1];
   it.Lq = q1 - it.q0;
-  it.Lk = p.k_end[it.s] - p.k_begin[it.s];
+  it.Lk = p.cu_k[it.s + 1] - p.cu_k[it.s];
   if (it.q0 < 0 || it.Lq < 0 || it.Lk < it.Lq || it.Lq > p.max_seqlen_q ||
       it.Lk > p.max_seqlen_k || q1 > p.total_q ||
       static_cast<int64_t>(it.Lk) > static_cast<int64_t>(p.max_blocks) * p.block_size) {
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
 
   const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1];
-  const int Lq = q1 - q0, Lk = p.k_end[s] - p.k_begin[s];
+  const int Lq = q1 - q0, Lk = p.cu_k[s + 1] - p.cu_k[s];
   if (q0 < 0 || Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k ||
       q1 > p.total_q ||
       static_cast<int64_t>(Lk) > static_cast<int64_t>(p.max_blocks) * p.block_size) {
@@ -1348,8 +1348,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
   const int G = a.num_q_heads / a.num_kv_heads;
   PrefillParams p;
   p.cu_q = a.cu_seqlens_q;
-  p.k_end = a.k_end;
-  p.k_begin = a.k_begin;
+  p.cu_k = a.cu_seqlens_k;
   p.block_tables = a.block_tables;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;

@@ -824,6 +824,32 @@ def test_prefill_refuses_segments_alike_on_both_ways(L, q_lens, k_lens, window, 
 
 
 @gpu
+@pytest.mark.parametrize("segments", [32, 33, 129, 300])
+def test_widened_prefill_of_many_segments(L, segments):
+    """Lengths from 1 on, empty segments among them, and every 17th longer than the
+    tables: those are left alone, the others attended."""
+    g = torch.Generator().manual_seed(segments)
+    q_lens = torch.randint(0, 12, (segments,), generator=g).tolist()
+    q_lens[5] = 70                                      # more than the way by rows takes
+    k_lens = [max(1, n + int(torch.randint(0, 40, (), generator=g))) for n in q_lens]
+    for s in range(16, segments, 17):
+        q_lens[s], k_lens[s] = 3, 113 + s % 8
+    c = Q.Cache(20, k_lens, 1, 16, 32)
+    rows = sum(q_lens)
+    q = torch.randn(rows, 2, 128, generator=g).to(torch.bfloat16)
+    out, lse, tol_o, tol_l = _prefill_plain(c, q, q_lens, 2, 0)
+    kc, vc, bt = c.cuda()
+    bt = bt[:, :7].contiguous()                         # 112 keys
+    o, l = torch.full_like(q, 9.0).cuda(), torch.full((rows, 2), 9.0, device="cuda")
+    pkv.paged_prefill_attn_q4(q.cuda(), kc, vc, _cu(q_lens), _cu(k_lens), bt, 70, 128, sum(k_lens), SCALE, out=o, lse=l)
+    alone = torch.cat([torch.full((n,), s % 17 == 16) for s, n in enumerate(q_lens)])
+    assert pkv.check_device_errors() == (pkv.DEVERR_SEQLENS if bool(alone.any()) else 0)
+    o, l, ok = o.cpu(), l.cpu(), ~alone
+    assert bool((o[alone] == 9.0).all()) and bool((l[alone] == 9.0).all())
+    assert bool(((o[ok].double() - out[ok]).abs() <= tol_o[ok]).all()) and bool(((l[ok].double() - lse[ok]).abs() <= tol_l[ok]).all())
+
+
+@gpu
 @pytest.mark.parametrize("q_lens,k_lens", [([3, 2, 1], [2000, 1500, 1000]), ([100, 80, 90], [300, 200, 150])])  # by rows, widened
 def test_prefill_reports_bad_table_entries_and_attends_the_other_segments(L, q_lens, k_lens):
     c = Q.Cache(16, k_lens, 2, 16, 32)
