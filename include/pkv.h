@@ -517,7 +517,8 @@ pkv_status pkv_evict_select_new(const float *key_scores, int64_t score_stride,
  * raises PKV_DEVERR_CONTEXT and nothing of that sequence moves; a position
  * outside a table raises PKV_DEVERR_CONTEXT and an invalid table entry
  * PKV_DEVERR_BLOCK, and that row does not move. num_seqs is at most 65535;
- * head_dim 128; block_size any positive number.
+ * head_dim 128; block_size any positive number. Here and in the selections
+ * num_seqs == 0 is a no-op.
  */
 pkv_status pkv_evict_compact(void *k_cache, void *v_cache, const int32_t *src_tables,
                              int32_t src_max_blocks, const int32_t *dst_tables,

@@ -20,7 +20,7 @@ pkv_status select(const float *key_scores, int64_t score_stride, const int32_t *
   if (num_seqs < 0 || budget <= 0 || recent < 0 || recent > budget || max_context_len <= 0 ||
       score_stride < max_context_len)
     return PKV_ERR_INVALID_ARG;
-  if (key_scores == nullptr || context_lens == nullptr || keep == nullptr || new_lens == nullptr)
+  if (num_seqs > 0 && (key_scores == nullptr || context_lens == nullptr || keep == nullptr || new_lens == nullptr))
     return PKV_ERR_INVALID_ARG;
   if (max_context_len > pkv::kMaxContext || budget > kMaxBudget || num_seqs > kMaxSeqs) return PKV_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PKV_OK;
@@ -54,7 +54,7 @@ pkv_status compact(pkv::EvictCompactArgs &a, const int32_t *src_tables, int32_t 
   }
   if (num_seqs < 0 || budget <= 0 || src_max_blocks <= 0 || dst_max_blocks <= 0 || block_size <= 0 || num_blocks <= 0)
     return PKV_ERR_INVALID_ARG;
-  if (src_tables == nullptr || dst_tables == nullptr || keep == nullptr || new_lens == nullptr)
+  if (num_seqs > 0 && (src_tables == nullptr || dst_tables == nullptr || keep == nullptr || new_lens == nullptr))
     return PKV_ERR_INVALID_ARG;
   if ((key_scores == nullptr) != (dst_key_scores == nullptr)) return PKV_ERR_INVALID_ARG;
   if (key_scores != nullptr && (score_stride <= 0 || dst_score_stride <= 0)) return PKV_ERR_INVALID_ARG;

@@ -57,6 +57,17 @@ def test_select_into_new_arrays_refuses(L):
     assert call(S=0) == pkv.PKV_OK
 
 
+def test_no_sequences(L):
+    """An empty tensor has no address."""
+    for call in (L.pkv_evict_select, L.pkv_evict_select_new):
+        assert call(None, 64, None, 64, 0, 16, 4, None, None, None) == pkv.PKV_OK
+        assert call(None, 64, None, 64, 0, 16, 17, None, None, None) == pkv.PKV_ERR_INVALID_ARG
+    assert L.pkv_evict_compact(FAKE, FAKE, None, 4, None, 4, None, 16, None, 0, 8, 128, 16, 64, None, 0, None, 0,
+                               None) == pkv.PKV_OK
+    assert L.pkv_evict_compact(None, FAKE, None, 4, None, 4, None, 16, None, 0, 8, 128, 16, 64, None, 0, None, 0,
+                               None) == pkv.PKV_ERR_INVALID_ARG
+
+
 def test_compact_refuses(L):
     def call(k=FAKE, v=FAKE, src=FAKE, sb=4, dst=FAKE, db=4, keep=FAKE, B=16, nl=FAKE, S=2, H=8, D=128, bs=16, NB=64,
              ks=None, ld=0, dks=None, dld=0):
@@ -341,6 +352,19 @@ def test_compact(L, lens, budget, recent, heads, block, group, in_place):
     for s, rows in enumerate(kept):
         assert torch.equal(new_scores[s, :len(rows)].cpu(), scores[s][rows])
         assert bool((new_scores[s, len(rows):] == 0).all())
+
+
+@gpu
+def test_calls_of_no_sequences(L):
+    kc, vc = (pkv.new_q4_cache(4, 16, 2) for _ in range(2))
+    empty = torch.empty(0, 3, dtype=torch.int32, device="cuda")
+    scores = torch.empty(0, 48, device="cuda")
+    keep, new = pkv.evict_select(scores, torch.empty(0, dtype=torch.int32, device="cuda"), 9, 2)
+    assert keep.shape == (0, 9) and new.shape == (0,)
+    pkv.evict_compact_q4(kc, vc, empty, empty, keep, new, scores, scores)
+    k16 = torch.zeros(4, 16, 2, 128, dtype=torch.bfloat16, device="cuda")
+    pkv.evict_compact(k16, k16.clone(), empty, empty, keep, new)
+    assert pkv.check_device_errors() == 0
 
 
 @gpu
