@@ -521,17 +521,16 @@ size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t max_seqlen_q) {
   return 0;
 }
 
-pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void *v_cache,
-                                  const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
-                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
-                                  int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
-                                  int32_t max_seqlen_k, int32_t num_q_heads,
-                                  int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
-                                  int64_t num_blocks, float scale, int32_t sliding_window,
-                                  void *out, float *lse, void *workspace, size_t workspace_bytes,
-                                  void *stream) {
-  (void)workspace;
-  (void)workspace_bytes;
+}  // extern "C"
+
+pkv_status pkv::prefill_bounded(const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                int32_t max_seqlen_k, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                float scale, int32_t sliding_window, void *out, float *lse,
+                                int32_t max_keys, int32_t total_k, void *stream) {
   if (k_cache == nullptr || v_cache == nullptr || cu_seqlens_q == nullptr ||
       cu_seqlens_k == nullptr || block_tables == nullptr)
     return PKV_ERR_INVALID_ARG;
@@ -559,7 +558,8 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
   a.num_seqs = num_seqs;
   a.total_q = total_q;
   a.max_seqlen_q = max_seqlen_q;
-  a.max_seqlen_k = max_seqlen_k;
+  a.max_seqlen_k = max_seqlen_k < max_keys ? max_seqlen_k : max_keys;
+  a.total_k = total_k;
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
   a.head_dim = head_dim;
@@ -590,6 +590,25 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
   cudaError_t e = pkv::launch_prefill(a, qmap, kmap, vmap, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
   return PKV_OK;
+}
+
+extern "C" {
+
+pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                  const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                  int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                  int32_t max_seqlen_k, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                  int64_t num_blocks, float scale, int32_t sliding_window,
+                                  void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  return pkv::prefill_bounded(q, k_cache, v_cache, cu_seqlens_q, cu_seqlens_k, block_tables,
+                              max_blocks_per_seq, num_seqs, total_q, max_seqlen_q, max_seqlen_k,
+                              num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                              sliding_window, out, lse, INT32_MAX, -1, stream);
 }
 
 pkv_status pkv_read_device_errors_async(uint32_t *host_flags, void *stream) {

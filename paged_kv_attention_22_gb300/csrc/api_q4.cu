@@ -142,7 +142,7 @@ bool prefill_by_rows(int64_t num_seqs, int64_t total_q, int64_t max_q, int64_t t
 }
 
 struct PrefillWorkspace {
-  size_t tables, cu_k, k, v;         // widened
+  size_t tables, k, v;               // widened
   size_t lens, rows, o, ml;          // by rows
   size_t total;
   int32_t max_blocks;
@@ -157,8 +157,7 @@ PrefillWorkspace prefill_workspace(int32_t num_seqs, int32_t total_k, int32_t ma
   w.num_blocks = (static_cast<int64_t>(total_k) + B - 1) / B + num_seqs;
   const size_t cache = static_cast<size_t>(w.num_blocks) * B * num_kv_heads * kD * 2;
   w.tables = 0;
-  w.cu_k = align_up(static_cast<size_t>(num_seqs) * w.max_blocks * sizeof(int32_t), 256);
-  w.k = align_up(w.cu_k + (static_cast<size_t>(num_seqs) + 1) * sizeof(int32_t), 256);
+  w.k = align_up(static_cast<size_t>(num_seqs) * w.max_blocks * sizeof(int32_t), 256);
   w.v = w.k + cache;
   const size_t most_rows = align_up(static_cast<size_t>(num_seqs) * kRowsMaxQ * sizeof(int32_t), 256);
   const size_t pieces = static_cast<size_t>(sms) * 16 * 2 * 4;  // of up to 4 query heads a KV head
@@ -369,7 +368,6 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
   g.ws_k = ws + w.k;
   g.ws_v = ws + w.v;
   g.ws_tables = reinterpret_cast<int32_t *>(ws + w.tables);
-  g.ws_cu_k = reinterpret_cast<int32_t *>(ws + w.cu_k);
   g.max_blocks = max_blocks_per_seq;
   g.ws_max_blocks = w.max_blocks;
   g.num_seqs = num_seqs;
@@ -380,10 +378,10 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
   g.num_sms = sms;
   cudaError_t e = pkv::launch_q4_gather(g, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "prefill_q4 widening launch");
-  return pkv_paged_prefill_attn(q, g.ws_k, g.ws_v, cu_seqlens_q, g.ws_cu_k, g.ws_tables, w.max_blocks, num_seqs,
-                                total_q, max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads, head_dim,
-                                pkv::kQ4PrefillBlock, w.num_blocks, scale, sliding_window, out, lse, nullptr, 0,
-                                stream);
+  return pkv::prefill_bounded(q, g.ws_k, g.ws_v, cu_seqlens_q, cu_seqlens_k, g.ws_tables, w.max_blocks, num_seqs, total_q,
+                              max_seqlen_q, max_seqlen_k, num_q_heads, num_kv_heads, head_dim, pkv::kQ4PrefillBlock,
+                              w.num_blocks, scale, sliding_window, out, lse, max_blocks_per_seq * block_size, total_k,
+                              stream);
 }
 
 }  // extern "C"

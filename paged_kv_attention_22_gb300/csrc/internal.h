@@ -118,6 +118,7 @@ struct PrefillArgs {
   int32_t window;  // sliding window in keys (0: none)
   int32_t box_rows;  // rows per K/V TMA box: prefill_box_rows(block_size)
   int32_t num_sms;   // SMs of the device (persistent grid)
+  int32_t total_k;   // segments end there at the latest, or -1: no such bound
   float scale_log2;
 };
 // Work items of one prefill call (row tiles x head pairs x sequences) are
@@ -134,6 +135,16 @@ inline int32_t prefill_box_rows(int32_t block_size) {
 cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
                            const CUtensorMap &k_map, const CUtensorMap &v_map,
                            cudaStream_t stream);
+// pkv_paged_prefill_attn that also refuses segments of more than max_keys keys and, with
+// total_k >= 0, those that lie outside [0, total_k) (and have queries).
+pkv_status prefill_bounded(const void *q, const void *k_cache, const void *v_cache,
+                           const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                           const int32_t *block_tables, int32_t max_blocks_per_seq, int32_t num_seqs,
+                           int32_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                           int32_t block_size, int64_t num_blocks, float scale,
+                           int32_t sliding_window, void *out, float *lse, int32_t max_keys,
+                           int32_t total_k, void *stream);
 cudaError_t take_prefill_errors(cudaStream_t stream, uint32_t *flags);
 cudaError_t prefill_error_word(uint32_t **word);
 
@@ -177,7 +188,7 @@ struct Q4GatherArgs {
   Q4CacheArgs cache;
   const int32_t *cu_seqlens_q, *cu_seqlens_k, *block_tables;
   void *ws_k, *ws_v;
-  int32_t *ws_tables, *ws_cu_k;
+  int32_t *ws_tables;
   int32_t max_blocks, ws_max_blocks, num_seqs, max_seqlen_q, max_seqlen_k, total_k;
   int32_t window, num_sms;
 };

@@ -122,6 +122,7 @@ struct PrefillParams {
   int32_t window;    // sliding window in keys (0: none)
   int32_t box_rows;  // rows per K/V box: 16, 32, 64 or 128, dividing block_size
   float scale_log2;
+  int32_t total_k;   // kBounded: segments with queries lie in [0, total_k)
 };
 
 __device__ __forceinline__ bool wait_(uint32_t bar, uint32_t parity, const volatile int *abort) {
@@ -184,6 +185,12 @@ __device__ __forceinline__ void store_o_rows(uint32_t tO, float inv_l, uint32_t 
   }
 }
 
+// Whether segment s's keys lie outside [0, total_k): a cache over which total_k keys
+// were made has none there.
+__device__ __forceinline__ bool beyond(const PrefillParams &p, int s) {
+  return p.cu_k[s] < 0 || p.cu_k[s + 1] > p.total_k;
+}
+
 // One work item: two 128-row query tiles that share every K/V tile. With
 // grouped queries (H_q / H_kv >= 2) the two query heads of a head pair over
 // the same 128 rows; without grouping, two consecutive row tiles of one head.
@@ -199,7 +206,7 @@ struct Item {
 // the most keys) to the first, each over all head pairs and sequences. False
 // for an item without work (rows past the segment, or lengths that fail the
 // checks, which `raise` reports once per sequence).
-template <bool kWindowed>
+template <bool kWindowed, bool kBounded>
 __device__ __forceinline__ bool make_item(const PrefillParams &p, int lin, bool raise, Item &it) {
   const int per_rt = p.n_pairs * p.num_seqs;
   const int rt = p.n_rowtiles - 1 - lin / per_rt;
@@ -211,7 +218,7 @@ __device__ __forceinline__ bool make_item(const PrefillParams &p, int lin, bool 
   it.Lq = q1 - it.q0;
   it.Lk = p.cu_k[it.s + 1] - p.cu_k[it.s];
   if (it.q0 < 0 || it.Lq < 0 || it.Lk < it.Lq || it.Lq > p.max_seqlen_q ||
-      it.Lk > p.max_seqlen_k || q1 > p.total_q ||
+      it.Lk > p.max_seqlen_k || q1 > p.total_q || (kBounded && it.Lq > 0 && beyond(p, it.s)) ||
       static_cast<int64_t>(it.Lk) > static_cast<int64_t>(p.max_blocks) * p.block_size) {
     if (raise && rt == p.n_rowtiles - 1 && pair == 0) atomicOr(&g_prefill_errors, kErrSeqlens);
     return false;
@@ -255,7 +262,7 @@ __device__ __forceinline__ bool make_item(const PrefillParams &p, int lin, bool 
 // This CTA's items in order: CTA c of C takes items c, 2C - 1 - c, 2C + c, ...
 // of the heaviest-first list (rounds alternate direction, so that every CTA
 // gets a similar mix of heavy and light items).
-template <bool kWindowed>
+template <bool kWindowed, bool kBounded>
 struct ItemWalk {
   int k = 0;         // next round to look at
   int item_no = -1;  // index of the current item among this CTA's items with work
@@ -266,7 +273,7 @@ struct ItemWalk {
       const int lin = k * C + ((k & 1) ? C - 1 - c : c);
       ++k;
       if (lin >= p.n_items) return false;
-      if (make_item<kWindowed>(p, lin, raise, it)) {
+      if (make_item<kWindowed, kBounded>(p, lin, raise, it)) {
         ++item_no;
         return true;
       }
@@ -278,6 +285,7 @@ struct ItemWalk {
 // heaviest-first list (the hardware hands CTAs to SMs as they free up, which
 // balances these long items). Calls with a window run
 // prefill_persistent_kernel.
+template <bool kBounded>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap k_map,
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1];
   const int Lq = q1 - q0, Lk = p.cu_k[s + 1] - p.cu_k[s];
   if (q0 < 0 || Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k ||
-      q1 > p.total_q ||
+      q1 > p.total_q || (kBounded && Lq > 0 && beyond(p, s)) ||
       static_cast<int64_t>(Lk) > static_cast<int64_t>(p.max_blocks) * p.block_size) {
     if (rt == p.n_rowtiles - 1 && pair == 0 && tid == 0) atomicOr(&g_prefill_errors, kErrSeqlens);
     return;
@@ -756,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // completed (kBarQEmpty), its first S MMAs follow the current item's last
 // P.V in issue order, and its first P.V (which overwrites O) waits for the
 // softmax warps' P, which they write only after reading the current O.
-template <bool kWindowed>
+template <bool kWindowed, bool kBounded>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_persistent_kernel(const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap k_map,
@@ -826,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         prefetch_tensormap(&k_map);
         prefetch_tensormap(&v_map);
       }
-      ItemWalk<kWindowed> w;
+      ItemWalk<kWindowed, kBounded> w;
       int G0 = 0;  // KV steps of earlier items
       bool good = true;
       Item it;
@@ -1116,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // The walk to the next item (a few global loads and divisions) runs in
       // the middle of this one: after the tile's last P, while its last P.V
       // completes, instead of between the epilogue and the next item's start.
-      ItemWalk<kWindowed> w;
+      ItemWalk<kWindowed, kBounded> w;
       Item nxt;
       bool have_nxt = false;
       auto run_item = [&](const Item &it, int T0) -> bool {
@@ -1311,19 +1319,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 }  // namespace
 
 // The kernel to launch: prefill_persistent_kernel or prefill_kernel.
-template <bool kWindowed, bool kPersistent>
+template <bool kWindowed, bool kPersistent, bool kBounded>
 constexpr auto prefill_entry() {
   if constexpr (kPersistent)
-    return prefill_persistent_kernel<kWindowed>;
+    return prefill_persistent_kernel<kWindowed, kBounded>;
   else
-    return prefill_kernel;
+    return prefill_kernel<kBounded>;
 }
 
-template <bool kWindowed, bool kPersistent>
+template <bool kWindowed, bool kPersistent, bool kBounded>
 cudaError_t launch_instance(dim3 grid, const CUtensorMap &q_map, const CUtensorMap &k_map,
                             const CUtensorMap &v_map, const PrefillParams &p,
                             cudaStream_t stream) {
-  auto kern = prefill_entry<kWindowed, kPersistent>();
+  auto kern = prefill_entry<kWindowed, kPersistent, kBounded>();
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -1331,7 +1339,7 @@ cudaError_t launch_instance(dim3 grid, const CUtensorMap &q_map, const CUtensorM
   // free: launch only a build whose per-thread allocation covers the split
   static const int launch_regs = [] {
     cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, prefill_entry<kWindowed, kPersistent>()) == cudaSuccess
+    return cudaFuncGetAttributes(&fa, prefill_entry<kWindowed, kPersistent, kBounded>()) == cudaSuccess
                ? fa.numRegs
                : 0;
   }();
@@ -1370,15 +1378,18 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
   p.window = a.window;
   p.box_rows = a.box_rows;
   p.scale_log2 = a.scale_log2;
+  p.total_k = a.total_k;
   if (p.window > 0) {
     // persistent: one CTA per SM (the shared memory admits no second one)
     const dim3 grid(static_cast<unsigned>(n_items < a.num_sms ? n_items : a.num_sms));
-    return launch_instance<true, true>(grid, q_map, k_map, v_map, p, stream);
+    return a.total_k >= 0 ? launch_instance<true, true, true>(grid, q_map, k_map, v_map, p, stream)
+                          : launch_instance<true, true, false>(grid, q_map, k_map, v_map, p, stream);
   }
   const dim3 grid = p.n_pairs <= 65535 && p.num_seqs <= 65535
                        ? dim3(p.n_rowtiles, p.n_pairs, p.num_seqs)
                        : dim3(static_cast<unsigned>(n_items));
-  return launch_instance<false, false>(grid, q_map, k_map, v_map, p, stream);
+  return a.total_k >= 0 ? launch_instance<false, false, true>(grid, q_map, k_map, v_map, p, stream)
+                        : launch_instance<false, false, false>(grid, q_map, k_map, v_map, p, stream);
 }
 
 cudaError_t prefill_error_word(uint32_t **word) {

@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32) q4_load_kernel(const Q4RowsParams
 }
 
 // Widen the keys of a prefill batch into bf16 blocks of kQ4PrefillBlock rows in
-// the workspace, whose block tables and lengths it writes. Sequence s starts at workspace
+// the workspace, whose block tables it writes. Sequence s starts at workspace
 // block ceil(cu_k[s] / block) + s, which leaves every sequence its
 // ceil(Lk / block) blocks. Grid: (chunks, sequences); a warp takes 16 keys of one
 // head, which lie in one cache block: one table entry, 1 KiB of K and of V codes.
@@ -232,69 +232,24 @@ struct Q4GatherParams {
   const uint32_t *k_codes, *v_codes, *k_params, *v_params;
   uint4 *k_out, *v_out;         // workspace K and V [blocks, kQ4PrefillBlock, H_kv, 128]
   int32_t *ws_tables;           // [S, ws_max_blocks]
-  int32_t *ws_cu_k;             // [S + 1], for the prefill kernel (see write_cu_k)
   FastDiv heads, block;
   int32_t max_blocks, ws_max_blocks, max_seqlen_q, max_seqlen_k, total_k;
   int32_t groups_log2, num_blocks, window;
 };
 constexpr int kGatherKeys = 16;
 
-// The keys of a segment, or -1. The prefill kernel refuses a segment (raising the
-// bit) by its lengths, fewer keys than queries among them; it knows neither total_k
-// nor the cache's tables, so that a segment beyond those gets the length -1.
-__device__ __forceinline__ int segment_keys(const Q4GatherParams &p, int k_begin, int k_end, bool queries) {
-  const int64_t n = static_cast<int64_t>(k_end) - k_begin;
-  const bool beyond = n < 0 || n > static_cast<int64_t>(p.max_blocks) * p.block.d ||
-                      (queries && (k_begin < 0 || k_end > p.total_k));
-  return beyond ? -1 : static_cast<int>(n);  // max_blocks * block_size fits
-}
-
-// ws_cu_k: numbers whose differences are the segments' lengths (the prefill kernel
-// uses nothing else of them; they may wrap); one warp, beside the others' widening
-// (a CTA of its own took as long). Writing them and reading them back costs four
-// short prompts 0.2 of 9.9 us. Lengths of the prefill kernel's own, in a second array,
-// cost the bf16 prefill 1 %.
-__device__ __forceinline__ void write_cu_k(const Q4GatherParams &p, int num_seqs, int lane) {
-  constexpr int kLoads = 4;
-  uint32_t carry = 0;
-  if (lane == 0) p.ws_cu_k[0] = 0;
-  for (int base = 0; base < num_seqs; base += 32 * kLoads) {
-    uint32_t n[kLoads];
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int s = base + 32 * u + lane;
-      n[u] = 0;
-      if (s < num_seqs) {
-        const int k0 = p.cu_k[s], k1 = p.cu_k[s + 1], q0 = p.cu_q[s], q1 = p.cu_q[s + 1];  // loads in flight together
-        n[u] = segment_keys(p, k0, k1, q1 > q0);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int s = base + 32 * u + lane;
-      if (base + 32 * u >= num_seqs) break;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, n[u], off);
-        if (lane >= off) n[u] += v;
-      }
-      if (s < num_seqs) p.ws_cu_k[s + 1] = static_cast<int32_t>(carry + n[u]);
-      carry += __shfl_sync(0xffffffffu, n[u], 31);
-    }
-  }
-}
-
 __global__ void __launch_bounds__(kWarps * 32) q4_gather_kernel(const Q4GatherParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int s = blockIdx.y;
-  if (blockIdx.x == 0 && s == 0 && threadIdx.x >= (kWarps - 1) * 32) write_cu_k(p, gridDim.y, threadIdx.x & 31);
-  const int k_begin = p.cu_k[s], k_end = p.cu_k[s + 1], q_begin = p.cu_q[s], q_end = p.cu_q[s + 1];
-  const int keys = segment_keys(p, k_begin, k_end, q_end > q_begin);
-  const int64_t Lq64 = static_cast<int64_t>(q_end) - q_begin;
-  // only what the prefill kernel takes is widened
-  const bool ok = keys > 0 && Lq64 > 0 && Lq64 <= keys && Lq64 <= p.max_seqlen_q && keys <= p.max_seqlen_k;
-  const int Lk = ok ? keys : 0, Lq = ok ? static_cast<int>(Lq64) : 0;
+  const int k_begin = p.cu_k[s], k_end = p.cu_k[s + 1];
+  const int q_begin = p.cu_q[s], q_end = p.cu_q[s + 1];
+  const int64_t Lk64 = static_cast<int64_t>(k_end) - k_begin, Lq64 = static_cast<int64_t>(q_end) - q_begin;
+  // segments that the prefill kernel refuses (it raises the bit) are not widened
+  const bool ok = Lk64 > 0 && Lq64 > 0 && Lq64 <= Lk64 && Lq64 <= p.max_seqlen_q && Lk64 <= p.max_seqlen_k &&
+                  k_begin >= 0 && k_end <= p.total_k &&
+                  Lk64 <= static_cast<int64_t>(p.max_blocks) * p.block.d;
+  const int Lk = ok ? static_cast<int>(Lk64) : 0, Lq = ok ? static_cast<int>(Lq64) : 0;
   const int ws_block0 = ok ? (k_begin + kQ4PrefillBlock - 1) / kQ4PrefillBlock + s : 0;
   for (int j = blockIdx.x * blockDim.x + threadIdx.x; j < p.ws_max_blocks; j += gridDim.x * blockDim.x)
     p.ws_tables[static_cast<int64_t>(s) * p.ws_max_blocks + j] =
@@ -396,7 +351,6 @@ cudaError_t launch_q4_gather(const Q4GatherArgs &a, cudaStream_t stream) {
   p.k_out = static_cast<uint4 *>(a.ws_k);
   p.v_out = static_cast<uint4 *>(a.ws_v);
   p.ws_tables = a.ws_tables;
-  p.ws_cu_k = a.ws_cu_k;
   p.max_blocks = a.max_blocks;
   p.ws_max_blocks = a.ws_max_blocks;
   p.max_seqlen_q = a.max_seqlen_q;
