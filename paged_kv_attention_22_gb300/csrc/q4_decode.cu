@@ -730,27 +730,34 @@ __global__ void __launch_bounds__(kScoreThreads) q4_scores_kernel(const KeyScore
 // table. A row of a segment that the call refuses, and a row behind the last
 // segment, gets length 0: it is left out. The bit is raised by a thread a segment,
 // also for one without rows, as the widened way's prefill kernel does.
-__device__ __forceinline__ bool segment_refused(const Q4PrefillRowsArgs &a, int s) {
-  const int64_t q0 = a.cu_seqlens_q[s], q1 = a.cu_seqlens_q[s + 1], k0 = a.cu_seqlens_k[s], k1 = a.cu_seqlens_k[s + 1];
-  const int64_t Lq = q1 - q0, Lk = k1 - k0;
-  return q0 < 0 || Lq < 0 || Lk < Lq || Lq > a.max_seqlen_q || Lk > a.max_seqlen_k || q1 > a.total_q ||
-         Lk > static_cast<int64_t>(a.max_blocks) * a.block_size || (Lq > 0 && (k0 < 0 || k1 > a.total_k));
+struct Segment {
+  int64_t q0, q1, k0, k1;
+  bool refused;
+};
+__device__ __forceinline__ Segment load_segment(const Q4PrefillRowsArgs &a, int s) {
+  // four loads in flight together
+  Segment g = {a.cu_seqlens_q[s], a.cu_seqlens_q[s + 1], a.cu_seqlens_k[s], a.cu_seqlens_k[s + 1], false};
+  const int64_t Lq = g.q1 - g.q0, Lk = g.k1 - g.k0;
+  g.refused = g.q0 < 0 || Lq < 0 || Lk < Lq || Lq > a.max_seqlen_q || Lk > a.max_seqlen_k || g.q1 > a.total_q ||
+              Lk > static_cast<int64_t>(a.max_blocks) * a.block_size || (Lq > 0 && (g.k0 < 0 || g.k1 > a.total_k));
+  return g;
 }
 __global__ void __launch_bounds__(256) q4_rows_kernel(const Q4PrefillRowsArgs a) {
   griddep_wait();
   griddep_launch_dependents();
   const int row = blockIdx.x * blockDim.x + threadIdx.x;
-  if (row < a.num_seqs && segment_refused(a, row)) atomicOr(&g_q4_decode_errors, kErrSeqlens);
+  // segments from the last thread on: in a small batch, other warps than those with rows
+  const int s = static_cast<int>(gridDim.x * blockDim.x) - 1 - row;
+  if (s < a.num_seqs && load_segment(a, s).refused) atomicOr(&g_q4_decode_errors, kErrSeqlens);
   if (row >= a.total_q) return;
   int lo = 0, hi = a.num_seqs - 1;  // the last segment that starts at or before the row
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (a.cu_seqlens_q[mid] <= row) lo = mid; else hi = mid - 1;
   }
-  int ctx = 0;
-  if (a.cu_seqlens_q[lo] <= row && row < a.cu_seqlens_q[lo + 1] && !segment_refused(a, lo))
-    ctx = a.cu_seqlens_k[lo + 1] - a.cu_seqlens_k[lo] - (a.cu_seqlens_q[lo + 1] - row) + 1;
-  a.context_lens[row] = ctx;
+  const Segment g = load_segment(a, lo);
+  const bool in = g.q0 <= row && row < g.q1 && !g.refused;
+  a.context_lens[row] = in ? static_cast<int>(g.k1 - g.k0 - (g.q1 - row) + 1) : 0;
   a.table_rows[row] = lo;
 }
 
