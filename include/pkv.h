@@ -354,8 +354,9 @@ pkv_status pkv_kv_load_q4(const void *k_codes, const void *k_params, const void 
  * Bytes of device workspace of pkv_paged_decode_attn_q4 (0 on invalid sizes or
  * without a device). with_scores != 0: for calls with key_scores, which keep the
  * logits of the call there (4 bytes per key and query head). A workspace serves
- * every call with sizes no larger than these; it needs no initialisation; calls
- * that share one must be ordered (same stream, or graphs that never overlap).
+ * every call with these head counts whose num_seqs and max_context_len are no
+ * larger; it needs no initialisation; calls that share one must be ordered (same
+ * stream, or graphs that never overlap).
  */
 size_t pkv_decode_q4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                     int32_t head_dim, int32_t max_context_len,
@@ -375,8 +376,8 @@ size_t pkv_decode_q4_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32
  *     for every key p that sequence s attended to (those in its window, if
  *     any); other entries keep their values. float32, score_stride >=
  *     max_context_len. The caller sets a sequence's row to zero when it admits
- *     the sequence. The heads are summed in order: the same inputs give the
- *     same bits.
+ *     the sequence. The heads are summed in order: the same call (sizes and
+ *     inputs) on the same device gives the same bits.
  */
 pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const void *k_params,
                                     const void *v_codes, const void *v_params,
@@ -392,8 +393,8 @@ pkv_status pkv_paged_decode_attn_q4(const void *q, const void *k_codes, const vo
 /*
  * Bytes of device workspace of pkv_paged_prefill_attn_q4 (0 on invalid sizes or
  * without a device): the call may widen the batch's keys to bf16 there, 512 *
- * num_kv_heads bytes per key and up to 128 keys more per sequence. Conditions as
- * above.
+ * num_kv_heads bytes per key and up to 128 keys more per sequence. A workspace
+ * serves every call with sizes no larger than these; else conditions as above.
  */
 size_t pkv_prefill_q4_workspace_size(int32_t num_seqs, int32_t total_k, int32_t max_seqlen_k,
                                      int32_t num_kv_heads, int32_t head_dim);
@@ -441,9 +442,9 @@ pkv_status pkv_paged_prefill_attn_q4(const void *q, const void *k_codes, const v
  * pkv_paged_decode_attn that also accumulates the attention weights:
  *   key_scores[s * score_stride + p] += sum over query heads h of exp(z_hp - lse[s, h])
  * for every key p that sequence s attended to; other entries keep their values.
- * The heads are summed in order: the same inputs give the same bits. An invalid
- * table entry raises PKV_DEVERR_BLOCK and its keys are left out, of the attention
- * and of the weights.
+ * The heads are summed in order: the same call (sizes and inputs) on the same
+ * device gives the same bits. An invalid table entry raises PKV_DEVERR_BLOCK and its
+ * keys are left out, of the attention and of the weights.
  *   key_scores   device float32 [num_seqs, score_stride], not NULL; the caller
  *                sets a sequence's row to zero when it admits the sequence
  *   score_stride >= max_context_len, which is at most 2^30 (PKV_ERR_UNSUPPORTED)

@@ -61,7 +61,9 @@ pkv_status check_attention(const pkv::Q4CacheArgs &c, int32_t num_q_heads, int32
 //   2,400 pairs of 2,048       141/138  151/150  171/188  154/154
 // The estimate takes every sequence at the longest. Where they are not, ranges
 // stay even, and one CTA a pair may be left with most of the work: pairs of more
-// than kWarpKeys keys a warp always go by ranges.
+// than kWarpKeys keys a warp go by ranges, in calls of at most kQ4MaxRangeSeqs
+// sequences. Above that there is no list of steps to cut, and one long sequence among
+// short ones runs on one CTA a KV head to its end.
 constexpr int32_t kStepKeys = 32, kWarpKeys = 1024;
 
 struct PlannedDecode {

@@ -18,10 +18,15 @@
 // to kSliceBytes) of every row and moves its rows in chunks, a whole chunk loaded
 // before any of it is stored, the next one on its way meanwhile; slices are
 // independent. Which of the two holds is found on the device, from the tables.
-// 8 x 4,096 rows of 4 KiB: 49 us fresh (268 MB, 5.5 TB/s; it waits for memory with
+// 8 x 4,096 rows of 4 KiB: 48 us fresh (268 MB, 5.6 TB/s; it waits for memory with
 // 24 warps an SM, the lookup of the next rows running ahead), 73 us in place
-// (issue slots: every slice looks all the rows up).
-// Selection: 12 us for 8 x 16,384 scores, mostly barriers between its passes.
+// (issue slots: every slice looks all the rows up). The same rows of a 4-bit cache (8
+// heads, groups of 32: 84 MB, 12 us at the memory's rate): 33 us fresh (its lanes take
+// the pieces of one array's row, 8 of 32 of them those of its parameters), 29 in place.
+// One kernel for both ways at three CTAs an SM: 80 registers, 112 bytes of stack, 228
+// bytes of spill stores and 212 of loads.
+// Selection: 10.3 us for 8 x 16,384 scores (back to back in a graph; 12.8 as a single
+// cold launch), mostly barriers between its passes.
 #include "internal.h"
 #include "ptx.cuh"
 

@@ -2,8 +2,10 @@
 // z[s, h, p] (base 2, scaled) and lse[s, h] (natural log),
 //   key_scores[s, p] += sum_h 2^(z[s, h, p] - lse[s, h] log2 e)
 // for every key p that sequence s attended to; a logit of -inf has weight 0, also
-// where the whole row is such (lse -inf). The sum runs over the heads in
-// order, so the result does not depend on the launch shape.
+// where the whole row is such (lse -inf). The sum runs over the heads in order,
+// without atomics: the same call on the same device gives the same bits. Another
+// launch shape (other sizes, bounds or SM count) may not: the logits' products and
+// the pieces that the lse comes from are then summed in another order.
 #pragma once
 
 #include "internal.h"
