@@ -248,6 +248,18 @@ def test_invalid_length_moves_nothing_where_the_call_makes_the_arrays(L):
         del keep, new               # the next call's arrays are these again
 
 
+@gpu
+@pytest.mark.parametrize("given", ["keep", "new_lens"])
+def test_invalid_length_where_one_array_is_given(L, given):
+    """The call makes the other one: the sequence gets -1 in both."""
+    lens = torch.tensor([10, -1, 11, 2], dtype=torch.int32, device="cuda")
+    keep = torch.full((4, 3), 7, dtype=torch.int32, device="cuda") if given == "keep" else None
+    new = torch.full((4,), 7, dtype=torch.int32, device="cuda") if given == "new_lens" else None
+    keep, new = pkv.evict_select(torch.rand(4, 10, device="cuda"), lens, 3, 1, keep=keep, new_lens=new)
+    assert pkv.check_device_errors() == pkv.DEVERR_CONTEXT
+    assert new.tolist() == [3, -1, -1, 2] and bool((keep[1:3] == -1).all()) and keep[3].tolist() == [0, 1, -1]
+
+
 def _select_sorted(row, n, budget, recent):
     """select_plain of one long sequence: a stable sort, NaN behind every number."""
     r = min(recent, n)
