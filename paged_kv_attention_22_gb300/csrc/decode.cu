@@ -697,8 +697,8 @@ __device__ __forceinline__ void build_prefix(const DecodeParams &p, int *prefix,
 // With accumulated weights (kScored; kMergeWarps warps) the launch's first CTAs,
 // score_chunks for each sequence, add them beside the CTAs that merge: they take the
 // lse of pairs that were cut from the pieces themselves, half a warp a head. (In a
-// kernel of their own behind the merge, one box: 64 x 640 keys 35.7 us in a graph and
-// 37.4 through the calls, 33.8 and 35.4 so; other boxes take up to 35.3 in a graph.)
+// kernel of their own behind the merge, in turn on one GPU: 64 x 640 keys 35.7 us in a
+// graph and 37.4 through the calls, 33.8 and 35.4 so; others took up to 35.3 in a graph.)
 // After a timeout the logits are stale, and nothing is added.
 struct ScoredMerge {
   KeyScoresParams k;
