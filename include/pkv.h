@@ -540,6 +540,102 @@ pkv_status pkv_evict_compact_q4(void *k_codes, void *k_params, void *v_codes, vo
                                 float *dst_key_scores, int64_t dst_score_stride, void *stream);
 
 /*
+ * Queries and keys on their way to attention
+ * ------------------------------------------
+ * The step of a layer between its projections and its attention: each head's
+ * row x of 128 values is normed and rotated by its token's position,
+ *   y = w x / sqrt(mean(x^2) + eps),
+ *   (y_a, y_b) -> magnitude (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
+ * for the pairs (a, b) of the first rotary_dim dims and the angle t = position
+ * * frequency of the pair; the other dims stay y. Computed in fp32, with the
+ * angle exact to 2^-32 of a turn at any position, and rounded once, to bf16.
+ */
+
+/*
+ * A rotation, in host memory: filled by one of the two calls below, then passed
+ * to any number of calls, which copy it. rotary_dim is 0 (none) to 128, a
+ * multiple of 8. The pairs are (i, i + rotary_dim / 2), or with interleaved != 0
+ * (2 i, 2 i + 1).
+ */
+typedef struct {
+  int32_t rotary_dim, interleaved;
+  float magnitude;
+  int32_t reserved;
+  uint64_t turns[64]; /* of each pair: frequency / (2 pi), times 2^64, modulo 2^64 */
+} pkv_rope;
+
+/*
+ * frequency_i = base^(-2 i / rotary_dim), base > 1, for i < rotary_dim / 2, then
+ *   PKV_ROPE_PLAIN   as it is
+ *   PKV_ROPE_LINEAR  divided by factor
+ *   PKV_ROPE_NTK     with base * factor^(rotary_dim / (rotary_dim - 2)) for base
+ *   PKV_ROPE_YARN    f (1 - r) + r f / factor with the ramp r = clamp((i - lo) /
+ *                    max(hi - lo, 0.001), 0, 1), lo = max(floor(d(beta_fast)), 0),
+ *                    hi = min(ceil(d(beta_slow)), rotary_dim - 1), d(b) = rotary_dim
+ *                    ln(original_positions / (2 pi b)) / (2 ln base); and magnitude
+ *                    0.1 ln(factor) + 1 (otherwise 1; factor >= 1 here)
+ * factor > 0 (not read by PKV_ROPE_PLAIN); original_positions > 0 and beta_fast >=
+ * beta_slow > 0 are read by PKV_ROPE_YARN only. Frequencies that no 64-bit number
+ * holds, and other values outside these ranges, are PKV_ERR_INVALID_ARG; a rotary_dim
+ * outside them is PKV_ERR_UNSUPPORTED. Nothing is written then.
+ */
+#define PKV_ROPE_PLAIN 0
+#define PKV_ROPE_LINEAR 1
+#define PKV_ROPE_NTK 2
+#define PKV_ROPE_YARN 3
+pkv_status pkv_rope_init(pkv_rope *rope, int32_t rotary_dim, int32_t interleaved, double base,
+                         int32_t scaling, double factor, int32_t original_positions,
+                         double beta_fast, double beta_slow);
+
+/* The same from the frequencies themselves (radians a position, host [rotary_dim / 2]). */
+pkv_status pkv_rope_init_frequencies(pkv_rope *rope, int32_t rotary_dim, int32_t interleaved,
+                                     const double *frequencies, float magnitude);
+
+/*
+ * Norm and rotate the rows of q and k, in one pass over them.
+ *   q, k       device bf16: head h of token t is the 128 values at element
+ *              t * stride + h * 128, so that both may be parts of one packed
+ *              projection [num_tokens, (H_q + 2 H_kv) * 128]. Strides count elements
+ *              and are multiples of 8; 0 heads: NULL, and nothing is done for it
+ *   q_weight, k_weight  device bf16 [128], or NULL: that tensor is not normed
+ *   eps        finite, >= 0
+ *   rope       host, or NULL: no rotation
+ *   positions  device int32 [num_tokens], any values; may be NULL without a rotation
+ *   q_out, k_out  device bf16, written; strides as above, with rows that do not
+ *              overlap (stride >= heads * 128). May be q and k themselves with
+ *              their strides (in place); otherwise must not overlap an input.
+ * num_tokens == 0 is a no-op; num_tokens * (H_q + H_kv) must be below 2^31.
+ */
+pkv_status pkv_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                            const void *q_weight, const void *k_weight, float eps,
+                            const pkv_rope *rope, const int32_t *positions, int32_t num_tokens,
+                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                            void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride,
+                            void *stream);
+
+/*
+ * The same on the way into the paged cache: q's rows go to q_out, k's, normed and
+ * rotated, to their slots in k_cache, and v's, as they are, to theirs in v_cache.
+ * Equivalent to pkv_qk_norm_rope, then pkv_kv_store of its keys and v; one pass.
+ * A token whose slot is -1 is left out of the caches, not of q_out; another slot
+ * outside the pool also raises PKV_DEVERR_SLOT. Two tokens with the same slot race.
+ *   v          device bf16, as k
+ *   slot_mapping  device int32 [num_tokens]
+ *   k_cache, v_cache  device bf16 [num_blocks, block_size, H_kv, 128]; must not
+ *              overlap the inputs or q_out
+ * num_q_heads may be 0 (q and q_out are then not read); num_kv_heads may not. For a
+ * 4-bit cache use pkv_qk_norm_rope, then pkv_kv_store_q4.
+ * num_tokens * (H_q + 2 H_kv) must be below 2^31.
+ */
+pkv_status pkv_kv_append(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const void *q_weight,
+                         const void *k_weight, float eps, const pkv_rope *rope,
+                         const int32_t *positions, const int32_t *slot_mapping,
+                         int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                         int32_t head_dim, int32_t block_size, int64_t num_blocks, void *q_out,
+                         int64_t q_out_stride, void *k_cache, void *v_cache, void *stream);
+
+/*
  * Synchronise `stream`, then return in *flags_out the OR of the device error
  * words of every kernel of this library on the current device, and clear
  * them. It blocks the host; it is also the only way to clear the words, and

@@ -3,9 +3,10 @@
 The functions here have the names of the C entry points in ``include/pkv.h``
 and do argument marshalling only: they check dtypes and shapes of torch
 tensors, pass their device pointers and the current CUDA stream to the C ABI,
-and allocate outputs the caller did not supply. (For 4-bit caches and eviction
-the checks are compiled, in the module ``_marshal`` beside the library, which
-only those calls load; they also want every tensor on the current device.) Every step of the computation
+and allocate outputs the caller did not supply. (For 4-bit caches, eviction and
+the calls on queries and keys before attention the checks are compiled, in the module
+``_marshal`` beside the library, which only those calls load; they also want every
+tensor on the current device.) Every step of the computation
 runs in the library's CUDA kernels. There is no fallback: if libpkv.so has not
 been built, or a call fails, an exception is raised.
 
@@ -129,6 +130,16 @@ def lib():
     L.pkv_evict_compact.restype = ctypes.c_int
     L.pkv_evict_compact_q4.argtypes = q4 + rows + [i32, i32, i32, i32, i64, P, i64, P, i64, P]
     L.pkv_evict_compact_q4.restype = ctypes.c_int
+    L.pkv_rope_init.argtypes = [P, i32, i32, ctypes.c_double, i32, ctypes.c_double, i32, ctypes.c_double,
+                                ctypes.c_double]
+    L.pkv_rope_init.restype = ctypes.c_int
+    L.pkv_rope_init_frequencies.argtypes = [P, i32, i32, P, f32]
+    L.pkv_rope_init_frequencies.restype = ctypes.c_int
+    L.pkv_qk_norm_rope.argtypes = [P, i64, P, i64, P, P, f32, P, P, i32, i32, i32, i32, P, i64, P, i64, P]
+    L.pkv_qk_norm_rope.restype = ctypes.c_int
+    L.pkv_kv_append.argtypes = [P, i64, P, i64, P, i64, P, P, f32, P, P, P, i32, i32, i32, i32, i32, i64,
+                                P, i64, P, P, P]
+    L.pkv_kv_append.restype = ctypes.c_int
     L.pkv_check_device_errors.argtypes = [P, ctypes.POINTER(ctypes.c_uint32)]
     L.pkv_check_device_errors.restype = ctypes.c_int
     L.pkv_read_device_errors_async.argtypes = [P, P]
@@ -577,6 +588,82 @@ def evict_compact_q4(k_cache, v_cache, src_tables, dst_tables, keep, new_lens, k
                                      key_scores, dst_key_scores, stream)
     if st:
         raise PkvError(st, "pkv_evict_compact_q4")
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
+class Rope(NamedTuple):
+    """A rotation by position (pkv_rope), made by rope() once for a model."""
+    data: bytes        # the C structure
+    rotary_dim: int
+    interleaved: bool
+    magnitude: float
+
+
+_ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}
+
+
+def rope(rotary_dim=128, base=10000.0, interleaved=False, scaling=None, factor=1.0,
+         original_positions=0, beta_fast=32.0, beta_slow=1.0, frequencies=None, magnitude=1.0) -> Rope:
+    """The rotation of the first rotary_dim dims of a head, in pairs (i, i + rotary_dim / 2) or,
+    interleaved, (2 i, 2 i + 1). scaling: None, "linear", "ntk" or "yarn" (pkv.h has the formulas).
+    frequencies: radians a position of each pair, in place of base and scaling, with a magnitude."""
+    made = _RopeStruct()
+    if frequencies is not None:
+        values = [float(f) for f in frequencies]
+        if len(values) * 2 != rotary_dim:
+            raise ValueError("frequencies must have rotary_dim / 2 values")
+        if scaling is not None:
+            raise ValueError("frequencies take no scaling")
+        _check(lib().pkv_rope_init_frequencies(ctypes.byref(made), int(rotary_dim), int(bool(interleaved)),
+                                               (ctypes.c_double * max(1, len(values)))(*values),
+                                               float(magnitude)), "pkv_rope_init_frequencies")
+    else:
+        if scaling not in _ROPE_SCALINGS:
+            raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+        if magnitude != 1.0:
+            raise ValueError("a magnitude goes with frequencies")
+        _check(lib().pkv_rope_init(ctypes.byref(made), int(rotary_dim), int(bool(interleaved)), float(base),
+                                   _ROPE_SCALINGS[scaling], float(factor), int(original_positions),
+                                   float(beta_fast), float(beta_slow)), "pkv_rope_init")
+    return Rope(bytes(made), made.rotary_dim, bool(made.interleaved), made.magnitude)
+
+
+def qk_norm_rope(q, k, rope, positions, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None,
+                 stream=None):
+    """Norm each head's row of q [T, H_q, 128] and k [T, H_kv, 128] (with weights [128]; None: not
+    normed) and rotate it by its token's position. q and k may be parts of a packed projection
+    (heads contiguous, any distance between tokens), q_out and k_out the same tensors. Either of q
+    and k may be None; rope None: no rotation. Returns (q_out, k_out)."""
+    if (q_out is None and q is not None) or (k_out is None and k is not None):
+        with _on(stream):
+            if q_out is None and q is not None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if k_out is None and k is not None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    st = _calls().qk_norm_rope(q, k, q_weight, k_weight, positions, eps, rope.data if rope is not None else None,
+                               q_out, k_out, stream)
+    if st:
+        raise PkvError(st, "pkv_qk_norm_rope")
+    return q_out, k_out
+
+
+def kv_append(q, k, v, rope, positions, k_cache, v_cache, slot_mapping, q_weight=None, k_weight=None, eps=1e-6,
+              q_out=None, stream=None):
+    """qk_norm_rope on the way into the paged cache: k's rows, normed and rotated, and v's, as they
+    are, go to slot_mapping (-1: skip), q's to q_out. q may be None. Returns q_out."""
+    if q_out is None and q is not None:
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    st = _calls().kv_append(q, k, v, q_weight, k_weight, positions, eps, rope.data if rope is not None else None,
+                            k_cache, v_cache, slot_mapping, q_out, stream)
+    if st:
+        raise PkvError(st, "pkv_kv_append")
+    return q_out
 
 
 def check_device_errors(stream=None) -> int:

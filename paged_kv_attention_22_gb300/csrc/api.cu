@@ -394,7 +394,7 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
 namespace {
 
 // The device error words of the kernel files on one device.
-constexpr int kErrorWords = 6;
+constexpr int kErrorWords = 7;
 struct ErrorWords {
   uint32_t *w[kErrorWords];
 };
@@ -417,7 +417,8 @@ pkv_status error_words(ErrorWords *out) {
         (e = pkv::prefill_error_word(&w.w[2])) != cudaSuccess ||
         (e = pkv::q4_cache_error_word(&w.w[3])) != cudaSuccess ||
         (e = pkv::q4_decode_error_word(&w.w[4])) != cudaSuccess ||
-        (e = pkv::evict_error_word(&w.w[5])) != cudaSuccess)
+        (e = pkv::evict_error_word(&w.w[5])) != cudaSuccess ||
+        (e = pkv::heads_error_word(&w.w[6])) != cudaSuccess)
       return cuda_fail(e, "cudaGetSymbolAddress (device error words)");
     g_words[dev] = w;
     g_words_set[dev] = true;

@@ -259,6 +259,21 @@ struct EvictCompactArgs {
 cudaError_t launch_evict_compact(const EvictCompactArgs &a, cudaStream_t stream);
 cudaError_t evict_error_word(uint32_t **word);
 
+// ---------------------------------------------------------------- queries and keys
+struct HeadsArgs {
+  const void *q, *k, *v, *q_weight, *k_weight;
+  void *q_out, *k_out, *v_out;   // with slots: q's rows and the two caches
+  const int32_t *positions, *slots;
+  const pkv_rope *rope;          // host, or null
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+  int64_t num_slots;
+  int32_t num_tokens, num_q_heads, num_kv_heads;
+  int num_sms;
+  float eps;
+};
+cudaError_t launch_heads(const HeadsArgs &a, cudaStream_t stream);
+cudaError_t heads_error_word(uint32_t **word);
+
 // ---------------------------------------------------------------- shared by the C entries
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

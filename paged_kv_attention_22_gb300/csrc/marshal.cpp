@@ -1,5 +1,5 @@
-// Argument marshalling of the Python binding for the calls on 4-bit caches and
-// of eviction: checks torch tensors (type, dtype, shape, device, layout), takes
+// Argument marshalling of the Python binding for the calls on 4-bit caches, of
+// eviction and on queries and keys before attention: checks torch tensors (type, dtype, shape, device, layout), takes
 // their pointers and the current CUDA stream, and calls the C entries of
 // include/pkv.h. It computes nothing; a call costs about a microsecond here
 // where checks in Python cost ten to twenty, several times the launch itself.
@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
+#include <cstring>
 #include <exception>
 
 #include "pkv.h"
@@ -55,6 +56,24 @@ class Args {
     *codes = &check(PyTuple_GET_ITEM(o, 0), name, at::kByte, 4);
     *params = &check(PyTuple_GET_ITEM(o, 1), name, at::kBFloat16, 5);
   }
+  // Rows [T, heads, 128] bf16 on the current device whose heads lie side by side, at any
+  // distance between tokens (a part of a packed projection), or nullptr for None.
+  const at::Tensor *rows(const char *name) {
+    PyObject *o = next();
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = check(o, name, at::kBFloat16, 3, false);
+    if (t.size(2) != 128 || t.stride(2) != 1 || (t.size(1) > 1 && t.stride(1) != 128))
+      fail(PyExc_ValueError, "%s must be [tokens, heads, 128] with contiguous heads", name);
+    return &t;
+  }
+  // A rotation's bytes, or nullptr for None.
+  const pkv_rope *rope() {
+    PyObject *o = next();
+    if (o == Py_None) return nullptr;
+    if (!PyBytes_Check(o) || PyBytes_GET_SIZE(o) != sizeof(pkv_rope)) fail(PyExc_TypeError, "rope must be a Rope");
+    std::memcpy(&rope_, PyBytes_AS_STRING(o), sizeof rope_);
+    return &rope_;
+  }
   int32_t i32(const char *name) {
     const long long v = PyLong_AsLongLong(next());
     if (v == -1 && PyErr_Occurred()) throw PythonError{};
@@ -81,13 +100,13 @@ class Args {
  private:
   PyObject *next() { return args_[at_++]; }
 
-  const at::Tensor &check(PyObject *o, const char *name, at::ScalarType dtype, int64_t ndim) {
+  const at::Tensor &check(PyObject *o, const char *name, at::ScalarType dtype, int64_t ndim, bool contiguous = true) {
     if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a torch.Tensor", name);
     const at::Tensor &t = THPVariable_Unpack(o);
     if (t.scalar_type() != dtype) fail(PyExc_TypeError, "%s must be %s", name, c10::toString(dtype));
     if (t.dim() != ndim) fail(PyExc_ValueError, "%s has the wrong number of dims", name);
     if (!t.is_cuda()) fail(PyExc_ValueError, "%s must be a CUDA tensor", name);
-    if (!t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", name);
+    if (contiguous && !t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", name);
     if (device_ < 0) device_ = c10::cuda::current_device();
     if (t.get_device() != device_) fail(PyExc_ValueError, "%s is not on the current device", name);
     return t;
@@ -96,6 +115,7 @@ class Args {
   PyObject *const *args_;
   Py_ssize_t at_ = 0;
   int device_ = -1;
+  pkv_rope rope_;
 };
 
 void require(bool ok) {
@@ -294,6 +314,58 @@ pkv_status evict_compact_q4(Args &a) {
                               c.stride(c.dst_scores), a.stream());
 }
 
+// Elements between the tokens of rows(); those of one token have no distance.
+int64_t stride(const at::Tensor *t) {
+  return t == nullptr ? 0 : t->size(0) > 1 ? t->stride(0) : t->size(1) * 128;
+}
+int32_t heads_of(const at::Tensor *t) { return t == nullptr ? 0 : size32(*t, 1); }
+
+// Queries, keys and how they are normed and rotated.
+struct Heads {
+  const at::Tensor *q, *k, *v, *q_weight, *k_weight, *positions;
+  float eps;
+  const pkv_rope *rope;
+  Heads(Args &a, bool with_v)
+      : q(a.rows("q")),
+        k(a.rows("k")),
+        v(with_v ? a.rows("v") : nullptr),
+        q_weight(a.maybe("q_weight", kBf16, 1)),
+        k_weight(a.maybe("k_weight", kBf16, 1)),
+        positions(a.maybe("positions", kI32, 1)),
+        eps(a.f32()),
+        rope(a.rope()) {
+    require((q == nullptr || k == nullptr || q->size(0) == k->size(0)) &&
+            (q_weight == nullptr || q_weight->size(0) == 128) && (k_weight == nullptr || k_weight->size(0) == 128) &&
+            (positions == nullptr || positions->size(0) == tokens()));
+  }
+  int64_t tokens() const { return q != nullptr ? q->size(0) : k != nullptr ? k->size(0) : 0; }
+};
+
+pkv_status qk_norm_rope(Args &a) {
+  const Heads h(a, false);
+  const at::Tensor *q_out = a.rows("q_out"), *k_out = a.rows("k_out");
+  require((h.q == nullptr || (q_out != nullptr && q_out->sizes() == h.q->sizes())) &&
+          (h.k == nullptr || (k_out != nullptr && k_out->sizes() == h.k->sizes())));
+  const at::Tensor *any = h.q != nullptr ? h.q : h.k;
+  return pkv_qk_norm_rope(ptr(h.q), stride(h.q), ptr(h.k), stride(h.k), ptr(h.q_weight), ptr(h.k_weight), h.eps, h.rope,
+                          ptr<int32_t>(h.positions), any != nullptr ? size32(*any, 0) : 0, heads_of(h.q), heads_of(h.k),
+                          128, ptr(q_out), stride(q_out), ptr(k_out), stride(k_out), a.stream());
+}
+
+pkv_status kv_append(Args &a) {
+  const Heads h(a, true);
+  const at::Tensor &kc = a.tensor("k_cache", kBf16, 4), &vc = a.tensor("v_cache", kBf16, 4);
+  const at::Tensor &slots = a.tensor("slot_mapping", kI32, 1);
+  const at::Tensor *q_out = a.rows("q_out");
+  require(h.k != nullptr && h.v != nullptr && h.v->sizes() == h.k->sizes() && vc.sizes() == kc.sizes() &&
+          kc.size(3) == 128 && kc.size(2) == h.k->size(1) && slots.size(0) == h.tokens() &&
+          (h.q == nullptr || (q_out != nullptr && q_out->sizes() == h.q->sizes())));
+  return pkv_kv_append(ptr(h.q), stride(h.q), ptr(h.k), stride(h.k), ptr(h.v), stride(h.v), ptr(h.q_weight),
+                       ptr(h.k_weight), h.eps, h.rope, ptr<int32_t>(h.positions), ptr<int32_t>(slots), size32(*h.k, 0),
+                       heads_of(h.q), heads_of(h.k), 128, size32(kc, 1), kc.size(0), ptr(q_out), stride(q_out), ptr(kc),
+                       ptr(vc), a.stream());
+}
+
 PyObject *result(pkv_status st) { return PyLong_FromLong(static_cast<long>(st)); }
 PyObject *result(PyObject *o) { return o; }
 
@@ -316,7 +388,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n) {
 PyMethodDef kMethods[] = {
     PKV_ENTRY(kv_store_q4, 6),           PKV_ENTRY(kv_load_q4, 6),         PKV_ENTRY(paged_decode_attn_q4, 13),
     PKV_ENTRY(paged_decode_attn_scores, 13), PKV_ENTRY(paged_prefill_attn_q4, 15), PKV_ENTRY(evict_select, 7),
-    PKV_ENTRY(evict_compact, 9),         PKV_ENTRY(evict_compact_q4, 9),   {nullptr, nullptr, 0, nullptr}};
+    PKV_ENTRY(evict_compact, 9),         PKV_ENTRY(evict_compact_q4, 9),   PKV_ENTRY(qk_norm_rope, 10),
+    PKV_ENTRY(kv_append, 13),            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
