@@ -257,6 +257,32 @@ pkv_status pkv_paged_decode_attn_noalloc(const void *q, const void *k_cache, con
                                          void *stream);
 
 /*
+ * Decode attention under a sliding window with first tokens that stay visible
+ * ("sinks"): pkv_paged_decode_attn, or with new rows pkv_paged_decode_attn_store,
+ * where sequence s attends to the keys
+ *   p < num_sinks  or  p >= context_lens[s] - sliding_window.
+ * Streams longer than their window keep the statistics of their softmax this way.
+ * Blocks that hold neither kind of key are not read: their table entries may be
+ * -1, their memory another sequence's. Keys that are not attended to may hold
+ * anything, NaN and infinities included.
+ *   k_new, v_new, slot_mapping  as in pkv_paged_decode_attn_store, or all NULL: no store
+ *   num_sinks  >= 0 (negative: PKV_ERR_INVALID_ARG); without a window every key is
+ *              attended to, as in the two calls above
+ *   flags      0, or with new rows PKV_DECODE_STABLE_INPUTS
+ * Other arguments, the workspace and the errors are theirs.
+ */
+pkv_status pkv_paged_decode_attn_sinks(const void *k_new, const void *v_new,
+                                       const int32_t *slot_mapping, const void *q, void *k_cache,
+                                       void *v_cache, const int32_t *block_tables,
+                                       int32_t max_blocks_per_seq, const int32_t *context_lens,
+                                       int32_t max_context_len, int32_t num_seqs,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, int64_t num_blocks, float scale,
+                                       int32_t sliding_window, int32_t num_sinks, void *out,
+                                       float *lse, void *workspace, size_t workspace_bytes,
+                                       uint32_t flags, void *stream);
+
+/*
  * Bytes of device workspace that pkv_paged_prefill_attn needs (currently 0 for
  * every size: the prefill kernel keeps all its state on chip).
  */

@@ -130,6 +130,9 @@ def lib():
     L.pkv_evict_compact.restype = ctypes.c_int
     L.pkv_evict_compact_q4.argtypes = q4 + rows + [i32, i32, i32, i32, i64, P, i64, P, i64, P]
     L.pkv_evict_compact_q4.restype = ctypes.c_int
+    L.pkv_paged_decode_attn_sinks.argtypes = [P, P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i64,
+                                              f32, i32, i32, P, P, P, sz, ctypes.c_uint32, P]
+    L.pkv_paged_decode_attn_sinks.restype = ctypes.c_int
     L.pkv_rope_init.argtypes = [P, i32, i32, ctypes.c_double, i32, ctypes.c_double, i32, ctypes.c_double,
                                 ctypes.c_double]
     L.pkv_rope_init.restype = ctypes.c_int
@@ -588,6 +591,28 @@ def evict_compact_q4(k_cache, v_cache, src_tables, dst_tables, keep, new_lens, k
                                      key_scores, dst_key_scores, stream)
     if st:
         raise PkvError(st, "pkv_evict_compact_q4")
+
+
+def paged_decode_attn_sinks(q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
+                            sliding_window, num_sinks, out=None, lse=None, workspace=None, stream=None,
+                            with_lse=True, k_new=None, v_new=None, slot_mapping=None, stable_inputs=False):
+    """q=1 decode attention where each sequence sees its first num_sinks keys and its last
+    sliding_window ones. With k_new, v_new [S, H_kv, 128] and slot_mapping the new token's rows are
+    stored by the call, as in paged_decode_attn_store. The workspace is new_decode_workspace's.
+    Returns (out, lse)."""
+    if out is None or workspace is None or (lse is None and with_lse):
+        with _on(stream):
+            out, lse = _decode_outputs(q, out, lse, with_lse)
+            if workspace is None:
+                workspace = new_decode_workspace(q.shape[0], q.shape[1], k_cache.shape[2], 128,
+                                                 int(max_context_len), q.device)
+    st = _calls().paged_decode_attn_sinks(k_cache, v_cache, q, block_tables, context_lens, max_context_len,
+                                          scale, out, lse, None, workspace, sliding_window, num_sinks, k_new,
+                                          v_new, slot_mapping, DECODE_STABLE_INPUTS if stable_inputs else 0,
+                                          stream)
+    if st:
+        raise PkvError(st, "pkv_paged_decode_attn_sinks")
+    return out, lse
 
 
 class _RopeStruct(ctypes.Structure):

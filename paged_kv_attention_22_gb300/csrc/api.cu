@@ -3,6 +3,7 @@
 // Allocates nothing; every call only enqueues work on the caller's stream.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -293,7 +294,7 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
                          int32_t block_size, int64_t num_blocks, float scale,
                          int32_t sliding_window, void *out, float *lse, void *workspace,
                          size_t workspace_bytes, uint32_t flags, float *key_scores,
-                         int64_t score_stride, void *stream) {
+                         int64_t score_stride, void *stream, int32_t num_sinks = -1) {
   if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_tables == nullptr ||
       context_lens == nullptr || out == nullptr)
     return PKV_ERR_INVALID_ARG;
@@ -353,6 +354,9 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
   if (a.variant == 0 && pkv::decode_group_heads(num_kv_heads, 8) < 8) a.variant = 2;
   a.grid = decode_grid_ctas(sms, a.variant);
   a.window = sliding_window;
+  // without a window every key is seen; no sequence has more than max_context_len (and
+  // the kernel rounds up to whole units)
+  a.sinks = sliding_window > 0 ? std::min(num_sinks, std::min(max_context_len, pkv::kMaxContext)) : -1;
   a.stable_inputs = (flags & PKV_DECODE_STABLE_INPUTS) != 0 && pkv::pdl_enabled();
   a.scale_log2 = scale * kLog2e;
 
@@ -514,6 +518,25 @@ pkv_status pkv_paged_decode_attn_store(const void *k_new, const void *v_new,
                        max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads,
                        num_kv_heads, head_dim, block_size, num_blocks, scale, sliding_window,
                        out, lse, workspace, workspace_bytes, flags, nullptr, 0, stream);
+}
+
+pkv_status pkv_paged_decode_attn_sinks(const void *k_new, const void *v_new, const int32_t *slot_mapping,
+                                       const void *q, void *k_cache, void *v_cache,
+                                       const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t *context_lens, int32_t max_context_len,
+                                       int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                                       float scale, int32_t sliding_window, int32_t num_sinks,
+                                       void *out, float *lse, void *workspace,
+                                       size_t workspace_bytes, uint32_t flags, void *stream) {
+  if (num_sinks < 0) return PKV_ERR_INVALID_ARG;
+  const bool store = k_new != nullptr;
+  if ((v_new != nullptr) != store || (slot_mapping != nullptr) != store) return PKV_ERR_INVALID_ARG;
+  if ((flags & ~(store ? PKV_DECODE_STABLE_INPUTS : 0u)) != 0) return PKV_ERR_INVALID_ARG;
+  return decode_common(k_new, v_new, slot_mapping, q, k_cache, v_cache, block_tables,
+                       max_blocks_per_seq, context_lens, max_context_len, num_seqs, num_q_heads,
+                       num_kv_heads, head_dim, block_size, num_blocks, scale, sliding_window, out,
+                       lse, workspace, workspace_bytes, flags, nullptr, 0, stream, num_sinks);
 }
 
 size_t pkv_prefill_workspace_size(int32_t num_seqs, int32_t max_seqlen_q) {

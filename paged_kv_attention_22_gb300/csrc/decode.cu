@@ -86,6 +86,7 @@ struct DecodeParams {
   int32_t hg;        // KV heads per group (= consumer warps)
   int32_t n_groups;  // num_kv_heads / hg
   int32_t window;    // sliding window (keys per query, its own included), 0: none
+  int32_t sinks;     // first keys that stay visible under a window (kSinks; else 0)
   int32_t stable_inputs;  // caches, tables and lengths may be read before the wait
   float scale_log2;
   float *logits;          // kLogits: [S, H_q, logits_ld]
@@ -100,6 +101,11 @@ __device__ __forceinline__ int first_chunk(int ctx, int window) {
 }
 __device__ __forceinline__ int first_key(int ctx, int window) {
   return (window > 0 && ctx > window) ? ctx - window : 0;
+}
+// Sinks, keys that stay visible before the window, put the chunks that hold them in
+// front of that list, as far as the window's own do not.
+__device__ __forceinline__ int sink_chunks(int first, int sinks) {
+  return min((sinks + kChunk - 1) / kChunk, first);
 }
 
 // Shared memory layout for G query heads per KV head, head groups of up to
@@ -176,7 +182,7 @@ __device__ __forceinline__ void butterfly_half(float (&x)[N], bool upper, int la
   }
 }
 
-template <int G, int kMaxHG, int NS, bool kLogits>
+template <int G, int kMaxHG, int NS, bool kLogits, bool kSinks>
 __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
     decode_kernel(const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map,
@@ -259,7 +265,9 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
         if (ctx <= 0 || ctx > p.max_context_len || ctx > ctx_cap) {
           if (blockIdx.x == 0) atomicOr(&g_decode_errors, kErrContext);
         } else {
-          n = (ctx + kChunk - 1) / kChunk - first_chunk(ctx, p.window);
+          const int skipped = first_chunk(ctx, p.window);
+          n = (ctx + kChunk - 1) / kChunk - skipped;
+          if constexpr (kSinks) n += sink_chunks(skipped, p.sinks);
         }
       }
       int incl = n;  // inclusive warp scan
@@ -295,7 +303,12 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
     const uint64_t policy = l2_policy_evict_first();
     // first key of the unit at `c` (the window, if any, starts its list)
     auto unit_key = [&](const Cursor &c) {
-      return (first_chunk(ctx_of[c.s], p.window) + c.k) * kChunk;
+      const int first = first_chunk(ctx_of[c.s], p.window);
+      if constexpr (kSinks) {
+        const int lead = sink_chunks(first, p.sinks);
+        return (c.k < lead ? c.k : c.k - lead + first) * kChunk;
+      }
+      return (first + c.k) * kChunk;
     };
     auto entry_of = [&](int i) -> int32_t {  // table entry of this CTA's unit i, 0 past the end
       if (i >= n_mine) return 0;
@@ -427,6 +440,7 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
   int seg_first_k = 0;
   bool seg_is_first = true;
   int ctx = 0, chunk0 = 0, key_lo = 0;  // the segment's length, first chunk and first key
+  [[maybe_unused]] int lead = 0;        // kSinks: its units before the window's
 
 #pragma unroll 1
   for (int it = 0; it < n_mine; ++it) {
@@ -442,6 +456,7 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
       ctx = ctx_of[cur.s];
       chunk0 = first_chunk(ctx, p.window);
       key_lo = first_key(ctx, p.window);
+      if constexpr (kSinks) lead = sink_chunks(chunk0, p.sinks);
       seg_first_k = cur.k;
       seg_is_first = (it == 0);
       const uint8_t *qs = kst + 2 * L::kKBytes + g * G * kRowBytes;
@@ -465,7 +480,8 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
         for (int i = 0; i < 4; ++i) o[h][i] = 0ull;
       }
     }
-    const int key0 = (chunk0 + cur.k) * kChunk;   // the unit's first key
+    int key0 = (chunk0 + cur.k) * kChunk;         // the unit's first key
+    if constexpr (kSinks) key0 = (cur.k < lead ? cur.k : cur.k - lead + chunk0) * kChunk;
     // A unit without a block: the stage holds whatever was there before. The outputs
     // of a bad entry are undefined, but weights are added to what the caller keeps:
     // with kLogits such keys are left out (logit -inf), and the maximum of a segment
@@ -480,6 +496,7 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
     }
     const int nvalid = there ? min(kChunk, ctx - key0) : 0;  // keys >= nvalid are past the context
     const int nskip = key_lo - key0;              // keys < nskip are before the window
+    [[maybe_unused]] const int nsink = p.sinks - key0;  // kSinks: keys < nsink are seen all the same
     const bool with_new = fused && cur.k == chunks_of(prefix, cur.s) - 1;
     if (with_new) {
       // the unit holds the sequence's new token (key ctx-1): take its K and V
@@ -525,7 +542,9 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
       float q2[2] = {part[h][0], part[h][1]};
       butterfly_half<2>(q2, (sub & 2) != 0, 2);
       const float full = q2[0] + __shfl_xor_sync(0xffffffffu, q2[0], 1);
-      sc[h] = (my_key < nvalid && my_key >= nskip) ? full : -INFINITY;
+      bool seen = my_key < nvalid && my_key >= nskip;
+      if constexpr (kSinks) seen = my_key < nvalid && (my_key >= nskip || my_key < nsink);
+      sc[h] = seen ? full : -INFINITY;
       if constexpr (kLogits) {  // rows hold whole units: masked keys are written too
         const int64_t row = static_cast<int64_t>(cur.s) * p.num_q_heads + (cur.hg * HG + g) * G + h;
         if (counts) p.logits[row * p.logits_ld + key0 + my_key] = there ? full : -INFINITY;
@@ -579,7 +598,10 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
         for (int h = 0; h < G; ++h) ffma2(o[h][i], pr2[h], v0, v1);
       }
     };
-    if (nvalid == kChunk) {
+    // kSinks: units of which the query does not see every key are told apart, and what
+    // lies between the sinks and the window is not multiplied, even by zeros
+    const bool whole = nvalid == kChunk && (!kSinks || nskip <= max(nsink, 0) || nsink >= kChunk);
+    if (whole) {
       // a full unit (almost every one): fully unrolled, so that all its loads
       // can be issued ahead of the arithmetic
 #pragma unroll
@@ -589,7 +611,7 @@ __global__ void __launch_bounds__((kMaxHG + 2) * 32, 8 / kMaxHG)
       for (int pp = 0; pp < kChunk / 2; ++pp) {
         const int key = 2 * pp + half;
         if (2 * pp >= nvalid) break;
-        if (key < nvalid) pv_key(key);
+        if (key < nvalid && (!kSinks || key >= nskip || key < nsink)) pv_key(key);
       }
     }
     // this warp is done with the stage (and with prob): release it (after its
@@ -673,8 +695,10 @@ __device__ __forceinline__ void build_prefix(const DecodeParams &p, int *prefix,
     int n = 0;
     if (s < p.num_seqs) {
       const int ctx = p.context_lens[s];
-      if (ctx > 0 && ctx <= p.max_context_len && ctx <= ctx_cap)
-        n = (ctx + kChunk - 1) / kChunk - first_chunk(ctx, p.window);
+      if (ctx > 0 && ctx <= p.max_context_len && ctx <= ctx_cap) {
+        const int skipped = first_chunk(ctx, p.window);
+        n = (ctx + kChunk - 1) / kChunk - skipped + sink_chunks(skipped, p.sinks);
+      }
     }
     int incl = n;
 #pragma unroll
@@ -921,14 +945,14 @@ KeyScoresParams scores_params(const DecodeArgs &a) {
   return k;
 }
 
-template <int G, int HGM, int NS, bool kLogits = false>
+template <int G, int HGM, int NS, bool kLogits = false, bool kSinks = false>
 cudaError_t launch_variant(const DecodeArgs &a, const CUtensorMap &k_map,
                            const CUtensorMap &v_map, const CUtensorMap &q_map,
                            const CUtensorMap &kn_map, const CUtensorMap &vn_map,
                            const DecodeParams &p, cudaStream_t stream) {
   using L = DecodeSmem<G, HGM, NS>;
   static_assert(L::total(kDecodeMaxSeqs) <= 227 * 1024, "decode shared memory");
-  auto kern = decode_kernel<G, HGM, NS, kLogits>;
+  auto kern = decode_kernel<G, HGM, NS, kLogits, kSinks>;
   const int smem = L::total(a.num_seqs);
   // the limit is the kernel's, not the call's: another host thread may be between its
   // own two calls here, so it is always set to the most that any call wants
@@ -973,6 +997,12 @@ cudaError_t launch_group(const DecodeArgs &a, const CUtensorMap &k_map, const CU
     return launch_variant<G, 8, kDefaultStages, true>(a, k_map, v_map, q_map, kn_map, vn_map, p,
                                                       stream);
   }
+  if (a.sinks >= 0) {
+    if (a.variant == 2)
+      return launch_variant<G, 4, 2, false, true>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
+    return launch_variant<G, 8, kDefaultStages, false, true>(a, k_map, v_map, q_map, kn_map, vn_map, p,
+                                                             stream);
+  }
   switch (a.variant) {
     case 1: return launch_variant<G, 8, 2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
     case 2: return launch_variant<G, 4, 2>(a, k_map, v_map, q_map, kn_map, vn_map, p, stream);
@@ -1011,6 +1041,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map,
   p.hg = decode_group_heads(a.num_kv_heads, decode_variant_group_max(a.variant));
   p.n_groups = a.num_kv_heads / p.hg;
   p.window = a.window;
+  p.sinks = a.sinks > 0 ? a.sinks : 0;
   p.stable_inputs = a.stable_inputs ? 1 : 0;
   p.scale_log2 = a.scale_log2;
   p.logits = a.logits;

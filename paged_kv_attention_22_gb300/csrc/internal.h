@@ -92,6 +92,7 @@ struct DecodeArgs {
   int32_t grid;             // CTAs (persistent; one per SM by default)
   int32_t variant;          // launch shape (see kDecodeNumVariants)
   int32_t window;           // sliding window in keys (0: none)
+  int32_t sinks;            // first keys that stay visible under a window, or -1: a call without sinks
   bool stable_inputs;       // caches, tables and lengths may be read before the wait
   float *logits;            // [S, H_q, logits_ld] (base 2, scaled) for key_scores, or null
   float *key_scores;        // [S, score_stride] or null; then lse is not null

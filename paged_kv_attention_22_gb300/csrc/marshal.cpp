@@ -1,5 +1,5 @@
 // Argument marshalling of the Python binding for the calls on 4-bit caches, of
-// eviction and on queries and keys before attention: checks torch tensors (type, dtype, shape, device, layout), takes
+// eviction, on queries and keys before attention and with sinks: checks torch tensors (type, dtype, shape, device, layout), takes
 // their pointers and the current CUDA stream, and calls the C entries of
 // include/pkv.h. It computes nothing; a call costs about a microsecond here
 // where checks in Python cost ten to twenty, several times the launch itself.
@@ -314,6 +314,24 @@ pkv_status evict_compact_q4(Args &a) {
                               c.stride(c.dst_scores), a.stream());
 }
 
+pkv_status paged_decode_attn_sinks(Args &a) {
+  const at::Tensor &k = a.tensor("k_cache", kBf16, 4), &v = a.tensor("v_cache", kBf16, 4);
+  require(v.sizes() == k.sizes() && k.size(3) == 128);
+  const Decode d(a);
+  const int32_t sinks = a.i32("num_sinks");
+  const at::Tensor *kn = a.maybe("k_new", kBf16, 3), *vn = a.maybe("v_new", kBf16, 3);
+  const at::Tensor *slots = a.maybe("slot_mapping", kI32, 1);
+  const int32_t flags = a.i32("flags");
+  require((kn == nullptr) == (vn == nullptr) && (kn == nullptr) == (slots == nullptr) &&
+          (kn == nullptr || (kn->size(0) == d.q.size(0) && kn->size(1) == k.size(2) && kn->size(2) == 128 &&
+                             vn->sizes() == kn->sizes() && slots->size(0) == d.q.size(0))));
+  return pkv_paged_decode_attn_sinks(ptr(kn), ptr(vn), ptr<int32_t>(slots), ptr(d.q), ptr(k), ptr(v),
+                                     ptr<int32_t>(d.tables), size32(d.tables, 1), ptr<int32_t>(d.lens), d.max_len,
+                                     size32(d.q, 0), size32(d.q, 1), size32(k, 2), 128, size32(k, 1), k.size(0),
+                                     d.scale, d.window, sinks, ptr(d.out), ptr<float>(d.lse), ptr(d.workspace),
+                                     d.workspace.nbytes(), static_cast<uint32_t>(flags), a.stream());
+}
+
 // Elements between the tokens of rows(); those of one token have no distance.
 int64_t stride(const at::Tensor *t) {
   return t == nullptr ? 0 : t->size(0) > 1 ? t->stride(0) : t->size(1) * 128;
@@ -389,7 +407,7 @@ PyMethodDef kMethods[] = {
     PKV_ENTRY(kv_store_q4, 6),           PKV_ENTRY(kv_load_q4, 6),         PKV_ENTRY(paged_decode_attn_q4, 13),
     PKV_ENTRY(paged_decode_attn_scores, 13), PKV_ENTRY(paged_prefill_attn_q4, 15), PKV_ENTRY(evict_select, 7),
     PKV_ENTRY(evict_compact, 9),         PKV_ENTRY(evict_compact_q4, 9),   PKV_ENTRY(qk_norm_rope, 10),
-    PKV_ENTRY(kv_append, 13),            {nullptr, nullptr, 0, nullptr}};
+    PKV_ENTRY(kv_append, 13),            PKV_ENTRY(paged_decode_attn_sinks, 18), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
