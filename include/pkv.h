@@ -325,6 +325,45 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
                                   void *stream);
 
 /*
+ * Attention of a chunk of new tokens of each sequence over the paged cache: the
+ * next tokens of a prompt that is taken in pieces, drafted tokens to be checked, the
+ * single tokens of sequences that decode beside them, in one call. Segment s has Lq =
+ * cu_seqlens_q[s+1] - cu_seqlens_q[s] query tokens, the last Lq of the sequence's
+ * context_lens[s] positions, whose rows are in the cache (store them first). Query i,
+ * at position p_i = context_lens[s] - Lq + i, sees the keys
+ *   p <= p_i,  and with a window  p > p_i - sliding_window  or  p < num_sinks.
+ * Output and lse as in decode, for every query row. A pkv_paged_prefill_attn with
+ * context lengths in place of cu_seqlens_k, whose keys are shared out over all SMs
+ * whatever the lengths, and joined by a second kernel.
+ *   q, out       device bf16 [total_q, num_q_heads, head_dim]
+ *   lse          device float32 [total_q, num_q_heads], or NULL
+ *   cu_seqlens_q device int32 [num_seqs + 1], non-decreasing, from 0; rows of q and
+ *                out past its last value are not touched
+ *   context_lens device int32 [num_seqs]; not looked at where Lq == 0
+ *   max_seqlen_q, max_context_len  host ints: upper bounds, the latter at most 2^30
+ *   workspace    device, >= pkv_chunk_workspace_size(...) bytes, 16-byte aligned
+ * num_seqs is at most 1024. Blocks with no key that a query of the segment sees are not
+ * read (their entries may be -1), and keys that none sees may hold anything; keys that
+ * some query of a segment sees must be finite, or that segment's rows may all be
+ * NaN. Segments with Lq < 0, Lq > max_seqlen_q, Lq > context_lens[s], rows past
+ * total_q, or context_lens[s] above max_context_len or past the table raise
+ * PKV_DEVERR_SEQLENS and are not written; an invalid table entry raises
+ * PKV_DEVERR_BLOCK and makes its segment's rows undefined. After a PKV_DEVERR_TIMEOUT
+ * the call does nothing, as the decode and prefill calls.
+ */
+size_t pkv_chunk_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim);
+pkv_status pkv_paged_chunk_attn(const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *cu_seqlens_q, const int32_t *context_lens,
+                                const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q,
+                                int32_t max_context_len, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int64_t num_blocks, float scale, int32_t sliding_window,
+                                int32_t num_sinks, void *out, float *lse, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
  * A cache held in 4 bits
  * ----------------------
  * The same paged cache with each K and V row quantised: codes of 4 bits and a

@@ -133,6 +133,11 @@ def lib():
     L.pkv_paged_decode_attn_sinks.argtypes = [P, P, P, P, P, P, P, i32, P, i32, i32, i32, i32, i32, i32, i64,
                                               f32, i32, i32, P, P, P, sz, ctypes.c_uint32, P]
     L.pkv_paged_decode_attn_sinks.restype = ctypes.c_int
+    L.pkv_chunk_workspace_size.argtypes = [i32] * 4
+    L.pkv_chunk_workspace_size.restype = sz
+    L.pkv_paged_chunk_attn.argtypes = [P, P, P, P, P, P, i32, i32, i32, i32, i32, i32, i32, i32, i32, i64, f32,
+                                       i32, i32, P, P, P, sz, P]
+    L.pkv_paged_chunk_attn.restype = ctypes.c_int
     L.pkv_rope_init.argtypes = [P, i32, i32, ctypes.c_double, i32, ctypes.c_double, i32, ctypes.c_double,
                                 ctypes.c_double]
     L.pkv_rope_init.restype = ctypes.c_int
@@ -612,6 +617,38 @@ def paged_decode_attn_sinks(q, k_cache, v_cache, block_tables, context_lens, max
                                           stream)
     if st:
         raise PkvError(st, "pkv_paged_decode_attn_sinks")
+    return out, lse
+
+
+def chunk_workspace_size(num_seqs, num_q_heads, num_kv_heads) -> int:
+    """Workspace bytes of paged_chunk_attn on the current device (0: invalid sizes)."""
+    return int(lib().pkv_chunk_workspace_size(num_seqs, num_q_heads, num_kv_heads, 128))
+
+
+def new_chunk_workspace(num_seqs, num_q_heads, num_kv_heads, device="cuda"):
+    """A workspace of paged_chunk_attn for these sizes on the current device."""
+    need = chunk_workspace_size(num_seqs, num_q_heads, num_kv_heads)
+    if need == 0:
+        raise PkvError(PKV_ERR_CUDA, "pkv_chunk_workspace_size")
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def paged_chunk_attn(q, k_cache, v_cache, cu_seqlens_q, context_lens, block_tables, max_seqlen_q,
+                     max_context_len, scale, sliding_window=0, num_sinks=0, out=None, lse=None, workspace=None,
+                     stream=None, with_lse=True):
+    """Attention of each sequence's last cu_seqlens_q[s + 1] - cu_seqlens_q[s] positions (their rows
+    stored before) over its context_lens[s] keys in the paged cache, causal; with a window each query sees
+    the last sliding_window keys up to its own and the first num_sinks. Returns (out, lse)."""
+    if out is None or workspace is None or (lse is None and with_lse):
+        with _on(stream):
+            out, lse = _decode_outputs(q, out, lse, with_lse)
+            S = cu_seqlens_q.shape[0] - 1
+            if workspace is None and S > 0 and q.shape[0] > 0:
+                workspace = new_chunk_workspace(S, q.shape[1], k_cache.shape[2], q.device)
+    st = _calls().paged_chunk_attn(k_cache, v_cache, q, cu_seqlens_q, context_lens, block_tables, max_seqlen_q,
+                                   max_context_len, scale, out, lse, workspace, sliding_window, num_sinks, stream)
+    if st:
+        raise PkvError(st, "pkv_paged_chunk_attn")
     return out, lse
 
 

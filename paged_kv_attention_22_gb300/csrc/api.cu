@@ -397,8 +397,22 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
 
 namespace {
 
+// Chunk workspace: the tiles that CTAs' ranges cut, then their pieces, two a CTA.
+struct ChunkWorkspace {
+  size_t cuts, ml, o, total;
+};
+ChunkWorkspace chunk_workspace(int sms) {
+  ChunkWorkspace w;
+  const size_t rows = 2 * static_cast<size_t>(sms) * 128;
+  w.cuts = 0;
+  w.ml = align_up(static_cast<size_t>(sms) * sizeof(pkv::ChunkCut), 256);
+  w.o = w.ml + rows * 4 * sizeof(float);
+  w.total = w.o + rows * 128 * sizeof(float);
+  return w;
+}
+
 // The device error words of the kernel files on one device.
-constexpr int kErrorWords = 7;
+constexpr int kErrorWords = 8;
 struct ErrorWords {
   uint32_t *w[kErrorWords];
 };
@@ -422,7 +436,8 @@ pkv_status error_words(ErrorWords *out) {
         (e = pkv::q4_cache_error_word(&w.w[3])) != cudaSuccess ||
         (e = pkv::q4_decode_error_word(&w.w[4])) != cudaSuccess ||
         (e = pkv::evict_error_word(&w.w[5])) != cudaSuccess ||
-        (e = pkv::heads_error_word(&w.w[6])) != cudaSuccess)
+        (e = pkv::heads_error_word(&w.w[6])) != cudaSuccess ||
+        (e = pkv::chunk_error_word(&w.w[7])) != cudaSuccess)
       return cuda_fail(e, "cudaGetSymbolAddress (device error words)");
     g_words[dev] = w;
     g_words_set[dev] = true;
@@ -633,6 +648,75 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
                               max_blocks_per_seq, num_seqs, total_q, max_seqlen_q, max_seqlen_k,
                               num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                               sliding_window, out, lse, INT32_MAX, -1, stream);
+}
+
+size_t pkv_chunk_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0 || head_dim != 128)
+    return 0;
+  int sms = 0;
+  if (current_sm_count(&sms) != PKV_OK) return 0;
+  return chunk_workspace(sms).total;
+}
+
+pkv_status pkv_paged_chunk_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *cu_seqlens_q,
+                                const int32_t *context_lens, const int32_t *block_tables, int32_t max_blocks_per_seq,
+                                int32_t num_seqs, int32_t total_q, int32_t max_seqlen_q, int32_t max_context_len,
+                                int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                                int64_t num_blocks, float scale, int32_t sliding_window, int32_t num_sinks, void *out,
+                                float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+  if (k_cache == nullptr || v_cache == nullptr || cu_seqlens_q == nullptr || context_lens == nullptr ||
+      block_tables == nullptr)
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs < 0 || total_q < 0 || max_seqlen_q < 0 || max_context_len < 0 || !std::isfinite(scale) ||
+      sliding_window < 0 || num_sinks < 0 || max_seqlen_q > max_context_len)
+    return PKV_ERR_INVALID_ARG;
+  pkv_status st = check_attention_shape(num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                                        max_blocks_per_seq);
+  if (st != PKV_OK) return st;
+  if (num_seqs > pkv::kChunkMaxSeqs || max_context_len > pkv::kMaxContext) return PKV_ERR_UNSUPPORTED;
+  if (total_q > 0 && (q == nullptr || out == nullptr)) return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return PKV_OK;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PKV_ERR_INVALID_ARG;
+  if (workspace == nullptr) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
+  pkv::ChunkArgs a;
+  if ((st = current_sm_count(&a.num_sms)) != PKV_OK) return st;
+  const ChunkWorkspace w = chunk_workspace(a.num_sms);
+  if (workspace_bytes < w.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a.cu_seqlens_q = cu_seqlens_q;
+  a.context_lens = context_lens;
+  a.block_tables = block_tables;
+  a.out = out;
+  a.lse = lse;
+  a.cuts = reinterpret_cast<pkv::ChunkCut *>(ws + w.cuts);
+  a.ws_ml = reinterpret_cast<float *>(ws + w.ml);
+  a.ws_o = reinterpret_cast<float *>(ws + w.o);
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.max_seqlen_q = max_seqlen_q;
+  a.max_context_len = max_context_len;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.block_size = block_size;
+  a.num_blocks = static_cast<int32_t>(num_blocks);
+  a.window = sliding_window;
+  a.sinks = sliding_window > 0 ? std::min(num_sinks, max_context_len) : 0;
+  a.scale_log2 = scale * kLog2e;
+
+  // Q: a KV head's G query heads of 128 / G tokens a box; K and V as in prefill
+  CUtensorMap qmap, kmap, vmap;
+  const int64_t rows = num_blocks * block_size;
+  const uint32_t G = static_cast<uint32_t>(num_q_heads / num_kv_heads);
+  const uint32_t box = static_cast<uint32_t>(pkv::prefill_box_rows(block_size));
+  if ((st = encode_rows_map(&qmap, q, total_q, num_q_heads, head_dim, 64, G, 128 / G, true)) != PKV_OK ||
+      (st = encode_rows_map(&kmap, k_cache, rows, num_kv_heads, head_dim, 64, 1, box, true)) != PKV_OK ||
+      (st = encode_rows_map(&vmap, v_cache, rows, num_kv_heads, head_dim, 64, 1, box, true)) != PKV_OK)
+    return st;
+  const cudaError_t e = pkv::launch_chunk(a, qmap, kmap, vmap, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk launch");
+  return PKV_OK;
 }
 
 pkv_status pkv_read_device_errors_async(uint32_t *host_flags, void *stream) {

@@ -275,6 +275,30 @@ struct HeadsArgs {
 cudaError_t launch_heads(const HeadsArgs &a, cudaStream_t stream);
 cudaError_t heads_error_word(uint32_t **word);
 
+// ---------------------------------------------------------------- chunks
+constexpr int kChunkMaxSeqs = 1024;  // sequences per call (their prefix lives in shared memory)
+// A tile of 128 query rows whose keys are cut between CTAs, as the joining kernel reads it.
+struct ChunkCut {
+  int32_t pieces;  // 0: none
+  int32_t slot0;   // of the first piece; piece x is in slot 2 (slot0 / 2 + x)
+  int32_t head, row, n_tok;
+};
+struct ChunkArgs {
+  const int32_t *cu_seqlens_q, *context_lens, *block_tables;
+  void *out;
+  float *lse;
+  float *ws_o, *ws_ml;  // [2 num_sms, 128, 128], [2 num_sms, 128, 4]
+  ChunkCut *cuts;       // [num_sms]
+  int32_t max_blocks, num_seqs, total_q, max_seqlen_q, max_context_len;
+  int32_t num_q_heads, num_kv_heads, block_size, num_blocks;
+  int32_t window, sinks;  // sinks: 0 without a window
+  int32_t num_sms;
+  float scale_log2;
+};
+cudaError_t launch_chunk(const ChunkArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
+                         const CUtensorMap &v_map, cudaStream_t stream);
+cudaError_t chunk_error_word(uint32_t **word);
+
 // ---------------------------------------------------------------- shared by the C entries
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

@@ -1,5 +1,5 @@
 // Argument marshalling of the Python binding for the calls on 4-bit caches, of
-// eviction, on queries and keys before attention and with sinks: checks torch tensors (type, dtype, shape, device, layout), takes
+// eviction, on queries and keys before attention, with sinks and on chunks: checks torch tensors (type, dtype, shape, device, layout), takes
 // their pointers and the current CUDA stream, and calls the C entries of
 // include/pkv.h. It computes nothing; a call costs about a microsecond here
 // where checks in Python cost ten to twenty, several times the launch itself.
@@ -332,6 +332,26 @@ pkv_status paged_decode_attn_sinks(Args &a) {
                                      d.workspace.nbytes(), static_cast<uint32_t>(flags), a.stream());
 }
 
+pkv_status paged_chunk_attn(Args &a) {
+  const at::Tensor &k = a.tensor("k_cache", kBf16, 4), &v = a.tensor("v_cache", kBf16, 4);
+  const at::Tensor &q = a.tensor("q", kBf16, 3), &cu_q = a.tensor("cu_seqlens_q", kI32, 1);
+  const at::Tensor &lens = a.tensor("context_lens", kI32, 1), &tables = a.tensor("block_tables", kI32, 2);
+  const int32_t max_q = a.i32("max_seqlen_q"), max_len = a.i32("max_context_len");
+  const float scale = a.f32();
+  const at::Tensor &out = a.tensor("out", kBf16, 3);
+  const at::Tensor *lse = a.maybe("lse", kF32, 2), *workspace = a.maybe("workspace", at::kByte, 1);
+  const int32_t window = a.i32("sliding_window"), sinks = a.i32("num_sinks");
+  const int64_t S = cu_q.size(0) - 1;
+  require(v.sizes() == k.sizes() && k.size(3) == 128 && q.size(2) == 128 && S >= 0 && lens.size(0) == S &&
+          tables.size(0) == S && out.sizes() == q.sizes() &&
+          (lse == nullptr || (lse->size(0) == q.size(0) && lse->size(1) == q.size(1))));
+  return pkv_paged_chunk_attn(ptr(q), ptr(k), ptr(v), ptr<int32_t>(cu_q), ptr<int32_t>(lens), ptr<int32_t>(tables),
+                              size32(tables, 1), static_cast<int32_t>(S), size32(q, 0), max_q, max_len, size32(q, 1),
+                              size32(k, 2), 128, size32(k, 1), k.size(0), scale, window, sinks, ptr(out),
+                              ptr<float>(lse), ptr(workspace), workspace != nullptr ? workspace->nbytes() : 0,
+                              a.stream());
+}
+
 // Elements between the tokens of rows(); those of one token have no distance.
 int64_t stride(const at::Tensor *t) {
   return t == nullptr ? 0 : t->size(0) > 1 ? t->stride(0) : t->size(1) * 128;
@@ -407,7 +427,8 @@ PyMethodDef kMethods[] = {
     PKV_ENTRY(kv_store_q4, 6),           PKV_ENTRY(kv_load_q4, 6),         PKV_ENTRY(paged_decode_attn_q4, 13),
     PKV_ENTRY(paged_decode_attn_scores, 13), PKV_ENTRY(paged_prefill_attn_q4, 15), PKV_ENTRY(evict_select, 7),
     PKV_ENTRY(evict_compact, 9),         PKV_ENTRY(evict_compact_q4, 9),   PKV_ENTRY(qk_norm_rope, 10),
-    PKV_ENTRY(kv_append, 13),            PKV_ENTRY(paged_decode_attn_sinks, 18), {nullptr, nullptr, 0, nullptr}};
+    PKV_ENTRY(kv_append, 13),            PKV_ENTRY(paged_decode_attn_sinks, 18), PKV_ENTRY(paged_chunk_attn, 15),
+    {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
