@@ -397,15 +397,17 @@ pkv_status decode_common(const void *k_new, const void *v_new, const int32_t *sl
 
 namespace {
 
-// Chunk workspace: the tiles that CTAs' ranges cut, then their pieces, two a CTA.
+// CTAs of a chunk call, one per SM, and its workspace: the tiles that their ranges cut,
+// then the pieces, two a CTA.
+int chunk_ctas(int sms) { return std::min(sms, pkv::kChunkMaxCtas); }
 struct ChunkWorkspace {
   size_t cuts, ml, o, total;
 };
-ChunkWorkspace chunk_workspace(int sms) {
+ChunkWorkspace chunk_workspace(int ctas) {
   ChunkWorkspace w;
-  const size_t rows = 2 * static_cast<size_t>(sms) * 128;
+  const size_t rows = 2 * static_cast<size_t>(ctas) * 128;
   w.cuts = 0;
-  w.ml = align_up(static_cast<size_t>(sms) * sizeof(pkv::ChunkCut), 256);
+  w.ml = align_up(static_cast<size_t>(ctas) * sizeof(pkv::ChunkCut), 256);
   w.o = w.ml + rows * 4 * sizeof(float);
   w.total = w.o + rows * 128 * sizeof(float);
   return w;
@@ -655,7 +657,7 @@ size_t pkv_chunk_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t n
     return 0;
   int sms = 0;
   if (current_sm_count(&sms) != PKV_OK) return 0;
-  return chunk_workspace(sms).total;
+  return chunk_workspace(chunk_ctas(sms)).total;
 }
 
 pkv_status pkv_paged_chunk_attn(const void *q, const void *k_cache, const void *v_cache, const int32_t *cu_seqlens_q,
@@ -680,8 +682,10 @@ pkv_status pkv_paged_chunk_attn(const void *q, const void *k_cache, const void *
   if (workspace == nullptr) return PKV_ERR_WORKSPACE_TOO_SMALL;
   if (!aligned16(workspace)) return PKV_ERR_INVALID_ARG;
   pkv::ChunkArgs a;
-  if ((st = current_sm_count(&a.num_sms)) != PKV_OK) return st;
-  const ChunkWorkspace w = chunk_workspace(a.num_sms);
+  int sms = 0;
+  if ((st = current_sm_count(&sms)) != PKV_OK) return st;
+  a.num_ctas = chunk_ctas(sms);
+  const ChunkWorkspace w = chunk_workspace(a.num_ctas);
   if (workspace_bytes < w.total) return PKV_ERR_WORKSPACE_TOO_SMALL;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   a.cu_seqlens_q = cu_seqlens_q;
@@ -701,7 +705,8 @@ pkv_status pkv_paged_chunk_attn(const void *q, const void *k_cache, const void *
   a.num_kv_heads = num_kv_heads;
   a.block_size = block_size;
   a.num_blocks = static_cast<int32_t>(num_blocks);
-  a.window = sliding_window;
+  // no sequence has more keys than max_context_len
+  a.window = std::min(sliding_window, max_context_len);
   a.sinks = sliding_window > 0 ? std::min(num_sinks, max_context_len) : 0;
   a.scale_log2 = scale * kLog2e;
 

@@ -5,29 +5,36 @@
 //
 // Work list. A tile is 128 query rows of one KV head: 128 / G tokens times the head's
 // G query heads, which are neighbours in the row of a token, so that one TMA box
-// loads them in the order (token, head). A tile's steps are the 128-key tiles that
-// its rows see: those that hold sinks, then those from its window's start to its
-// last token's position. The steps of all tiles, listed in (sequence, KV head, tile,
-// step) order, are cut into equal contiguous ranges, one per CTA (one CTA per SM),
-// whatever the lengths: a few tokens over long contexts use every SM, and long
-// chunks, many tiles a CTA, have no tail. A tile cut by a range boundary leaves its
-// pieces (maximum, sums, unnormalised output) in the workspace, a CTA's first in slot
-// 2c, its last in slot 2c + 1; a second kernel, launched right behind, joins them.
+// loads them in the order (token, head). Its steps are the 128-key tiles that its rows
+// see: those that hold sinks, then those from its window's start to its last token's
+// position. Tiles are listed in (sequence, KV head, tile) order.
 //
-// 8 warps:
-//   warp 0     TMA producer: Q tiles (two buffers), K and V tiles (two each).
-//   warp 1     MMAs. S(j + 1) = Q K(j + 1)^T goes out before O += P(j) V(j), into
-//              the other of two S buffers in TMEM, so that the tensor pipe computes the
-//              next logits while the softmax warps work on these. MMAs complete in
-//              order: S(j) complete means that P.V of step j - 2 is. While it
-//              waits for P(j) it zeroes the V rows that no row of the segment sees (past
-//              the last key; between the sinks and the window), which may be absent or
-//              hold anything: a probability of zero must not meet a NaN. Their
-//              logits are masked by selection.
-//   warp 2     walks the range and publishes its pieces to the other warps.
-//   warps 4-7  softmax, one row per thread (TMEM lane = row): read S, mask, online
-//              softmax in base 2 with a lazy maximum, P as bf16 over S's columns; at
-//              the end of a piece the output.
+// Shares, one CTA per SM. Where several tiles have the same keys and there are tiles
+// enough, CTA c takes whole tiles c, c + W, ... of the list's front: CTAs that run side
+// by side then pass the same keys at the same time, which reach the SMs through L2 once
+// from memory. The steps of the tiles behind, or of all, are cut into one contiguous
+// range a CTA, of the length that evens out the CTAs' totals: a few tokens over long
+// contexts use every SM, and no CTA is left with the last tile. A tile cut between
+// ranges leaves its pieces (maximum, sums, unnormalised output) in the workspace, a
+// range's first in slot 2k, its last in slot 2k + 1; a second kernel, launched right
+// behind, joins them.
+//
+// 12 warps:
+//   warp 0      TMA producer: walks the CTA's share, publishes its pieces to the other
+//               warps, and copies Q (two buffers), K and V (two stages each).
+//   warp 1      MMAs. S(j + 1) = Q K^T goes out before O += P(j) V(j), into the other of
+//               two S buffers in TMEM, so that the tensor pipe computes the next logits
+//               while the softmax warps work on these. MMAs complete in order: S(j)
+//               complete means that P.V of step j - 2 is. V rows that no row of the tile
+//               sees (past the last key; between the sinks and the window) may be absent
+//               or hold anything; the warp zeroes them before P.V, for a probability of
+//               zero must not meet a NaN. Their logits are masked by selection.
+//   warps 4-11  softmax, one row and half of the columns per thread (TMEM lane = row;
+//               warps 4-7 the lower half, 8-11 the upper): read S, mask, online softmax in
+//               base 2 with a lazy maximum, for which the two threads of a row swap their
+//               halves' maxima through shared memory, P as bf16 over S's columns; at the
+//               end of a piece half of the output's columns each. (With whole rows to a
+//               thread a step is bound by the time that one thread takes for it.)
 //
 // P is rounded to bf16 and the output divided by the sum of the rounded
 // probabilities, the weights that the products used; the lse comes from the fp32 sum.
@@ -48,60 +55,82 @@ constexpr int kRows = 128;                  // query rows a tile
 constexpr int kKeys = 128;                  // keys a step
 constexpr int kHalfBytes = 128 * 128;       // 128 rows x 64 bf16 (one swizzle column group)
 constexpr int kTileBytes = 2 * kHalfBytes;  // 128 rows x 128 bf16
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 1, kSoftmaxWarp0 = 4;
 constexpr int kDescs = 4;                   // pieces published ahead
 constexpr int kDescInts = 16;
+constexpr int kMaxWaves = 128;              // whole items a CTA, at most
+
+// barriers (8 bytes each): K and V landed, S complete (which frees its K), P written, P.V
+// complete (which frees its V), by the parity of the step; Q landed and free, by that of the
+// piece; descriptors full and free; of each TMEM quadrant the exchange between its two
+// softmax warps; the end
+constexpr int kBarK = 0, kBarV = 2, kBarS = 4, kBarP = 6, kBarO = 8, kBarQ = 10, kBarQFree = 12, kBarDesc = 14,
+              kBarDescFree = kBarDesc + kDescs, kBarX = kBarDescFree + kDescs, kBarDone = kBarX + 4,
+              kNumBars = kBarDone + 1;
+constexpr int kDescReaders = 1 + 8;  // the MMA warp, the softmax warps
+
+// A sequence's segment; Lq = 0: nothing to do.
+struct Seq {
+  int q0, Lq, ctx;
+};
+// A whole tile of a CTA's share.
+struct Wave {
+  Seq q;
+  int s, head, tile;
+};
 
 // shared memory
-constexpr int kQOff = 0;                            // two Q tiles
-constexpr int kKOff = kQOff + 2 * kTileBytes;       // two K tiles
-constexpr int kVOff = kKOff + 2 * kTileBytes;       // two V tiles
-constexpr int kEpiWarpBytes = 32 * 128;
-constexpr int kEpiOff = kVOff + 2 * kTileBytes;     // staging areas of the four softmax warps
-constexpr int kBarOff = kEpiOff + 4 * kEpiWarpBytes;
-// barriers (8 bytes each), those of steps and Q buffers in pairs by parity: K and V
-// landed, S complete (which frees its K), P written, P.V complete (which frees its V),
-// Q landed, Q free; descriptors full and empty; the end
-constexpr int kBarK = 0, kBarV = 2, kBarS = 4, kBarP = 6, kBarO = 8, kBarQ = 10, kBarQFree = 12, kBarDesc = 14, kBarDescFree = kBarDesc + kDescs, kBarDone = kBarDescFree + kDescs, kNumBars = kBarDone + 1;
+constexpr int kQOff = 0;                       // two Q tiles
+constexpr int kKOff = kQOff + 2 * kTileBytes;  // two K tiles
+constexpr int kVOff = kKOff + 2 * kTileBytes;  // two V tiles
+constexpr int kEpiWarpBytes = 32 * 64;
+constexpr int kEpiOff = kVOff + 2 * kTileBytes;  // staging areas of the softmax warps
+constexpr int kBarOff = kEpiOff + 8 * kEpiWarpBytes;
 constexpr int kDescOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
-constexpr int kMiscOff = kDescOff + kDescs * kDescInts * 4;  // TMEM address, abort flag
-constexpr int kPrefixOff = kMiscOff + 16;                    // int64 [S + 1]
-constexpr int smem_bytes(int num_seqs) { return kPrefixOff + 8 * (num_seqs + 1) + 1024; }  // + slack for alignment
-static_assert(smem_bytes(kChunkMaxSeqs) <= 227 * 1024, "shared memory per CTA");
+constexpr int kMiscOff = kDescOff + kDescs * kDescInts * 4;  // TMEM address, abort flag, unseen rows of the V tiles
+constexpr int kSwapOff = kMiscOff + 16;                      // float [4][2][128]: maxima of two steps, two sums, by half
+constexpr int kWaveOff = kSwapOff + 4 * 2 * kRows * 4;       // Wave [kMaxWaves]
+constexpr int kSmemBytes = kWaveOff + kMaxWaves * static_cast<int>(sizeof(Wave)) + 1024;  // + slack for alignment
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+// until the first copies, in the place of the V tiles: the list of sequences
+constexpr int kStepsOff = kVOff;                                          // int64 [S + 1]: steps before
+constexpr int kTilesOff = kStepsOff + 8 * (kChunkMaxSeqs + 2);            // int64 [S + 1]: tiles before
+constexpr int kSeqOff = kTilesOff + 8 * (kChunkMaxSeqs + 2);              // Seq [S]
+constexpr int kShareOff = kSeqOff + static_cast<int>(sizeof(Seq)) * kChunkMaxSeqs;  // int64 [W + 1]: ranges' starts
+constexpr int kRankOff = kShareOff + 8 * (kChunkMaxCtas + 2);             // int [W + 1]: ranges before
+static_assert(kRankOff + 4 * (kChunkMaxCtas + 2) <= kEpiOff, "the list fits the V tiles");
+static_assert(kChunkMaxCtas <= kThreads, "a thread for each CTA's share");
 
 constexpr uint32_t kTmemCols = 512;  // S (two), O: 128 columns each; a power of two
 constexpr int kTmemO = 256;
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kRows, kKeys, 0, 0);  // A = Q K-major, B = K K-major
 constexpr uint32_t kIdescPV = idesc_bf16_f32(kRows, kD, 0, 1);     // A = P (TMEM), B = V MN-major
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr float kLazyBound = 256.0f;  // the largest sum of a row's step taken with an old maximum
+constexpr float kLazyMax = 8.0f;      // log2 units that the running maximum may lag
 constexpr float kFloor = -1e30f;      // finite, below every logit: a row that has seen no key yet
 
 struct ChunkParams {
   const int32_t *cu_q, *lens, *block_tables;
   __nv_bfloat16 *out;
   float *lse;
-  float *ws_o;         // [2 grid, 128, 128]
-  float4 *ws_ml;       // [2 grid, 128]: maximum, sum, sum of the rounded
-  ChunkCut *cuts;      // [grid]: the tile that boundary c is the first to cut
+  float *ws_o;         // [2 ranges, 128, 128]
+  float4 *ws_ml;       // [2 ranges, 128]: maximum, sum, sum of the rounded
+  ChunkCut *cuts;      // [ranges]: the tile that the start of range k is the first to cut
   FastDiv block;
   int32_t max_blocks, num_seqs, total_q, max_seqlen_q, max_context_len;
   int32_t num_q_heads, num_kv_heads, num_blocks;
   int32_t gqa_log2;    // log2 of the query heads of a KV head
   int32_t lanes_log2;  // lanes that add up one sequence's steps
+  int32_t shared_keys; // some segment has several tiles over the same keys
   int32_t window, sinks, box_rows;
-  float scale_log2;    // > 0; the sign is in flip
-  uint32_t flip;       // sign bit of the logits' factor
+  float scale_log2;
 };
 
 __device__ __forceinline__ bool wait_(uint32_t bar, uint32_t parity, const volatile int *abort) {
   return mbar_wait(bar, parity, &g_chunk_errors, abort);
 }
 
-// A sequence's segment; Lq = 0: nothing to do.
-struct Seq {
-  int q0, Lq, ctx;
-};
 __device__ __forceinline__ Seq load_seq(const ChunkParams &p, int s, bool raise) {
   const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1], ctx = p.lens[s];
   Seq r = {q0, q1 - q0, ctx};
@@ -114,133 +143,219 @@ __device__ __forceinline__ Seq load_seq(const ChunkParams &p, int s, bool raise)
   return r;
 }
 
-// The key tiles of row tile rt: lead of them from the first key, then j_start ..
-// n_end - 1; lo is the first key of its window.
+__device__ __forceinline__ int tile_tokens(const ChunkParams &p) { return kRows >> p.gqa_log2; }
+
+// The key tiles of row tile i: `lead` of them from the first key, then j_start .. n_end - 1;
+// lo is the first key of its window.
 struct Tile {
+  int t0, n_tok;  // its first token within the segment, and its tokens
   int lead, j_start, n_end, lo;
   __device__ __forceinline__ int steps() const { return lead + n_end - j_start; }
 };
-__device__ __forceinline__ int tile_tokens(const ChunkParams &p) { return kRows >> p.gqa_log2; }
-__device__ __forceinline__ Tile tile_of(const ChunkParams &p, int Lq, int ctx, int rt) {
-  const int diag = ctx - Lq, t0 = rt * tile_tokens(p);
+template <bool kWindowed>
+__device__ __forceinline__ Tile tile_of(const ChunkParams &p, const Seq &q, int i) {
+  const int diag = q.ctx - q.Lq;
   Tile t;
-  t.n_end = (diag + min(Lq, t0 + tile_tokens(p)) + kKeys - 1) / kKeys;
-  t.lo = p.window > 0 ? max(0, diag + t0 + 1 - p.window) : 0;
-  t.j_start = t.lo / kKeys;
-  t.lead = min((p.sinks + kKeys - 1) / kKeys, t.j_start);
+  t.t0 = i * tile_tokens(p);
+  t.n_tok = min(q.Lq - t.t0, tile_tokens(p));
+  t.n_end = (diag + t.t0 + t.n_tok + kKeys - 1) / kKeys;
+  t.lo = t.j_start = t.lead = 0;
+  if constexpr (kWindowed) {
+    t.lo = max(0, diag + t.t0 + 1 - p.window);
+    t.j_start = t.lo / kKeys;
+    t.lead = min((p.sinks + kKeys - 1) / kKeys, t.j_start);
+  }
   return t;
 }
-__device__ __forceinline__ int row_tiles(const ChunkParams &p, int Lq) {
-  return (Lq + tile_tokens(p) - 1) / tile_tokens(p);
+__device__ __forceinline__ int tiles_of(const ChunkParams &p, const Seq &q) {
+  return (q.Lq + tile_tokens(p) - 1) / tile_tokens(p);
 }
 
-// First step of CTA c's range among W CTAs over U steps (W <= U), and the CTA
-// whose range holds step u.
-__device__ __forceinline__ int64_t range_start(int64_t c, int64_t W, int64_t U) { return c * U / W; }
-__device__ __forceinline__ int64_t owner_of(int64_t u, int64_t W, int64_t U) { return ((u + 1) * W + U - 1) / U - 1; }
+// a / b for 0 <= a, 0 < b, with 32-bit division where it does.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (a | b) >> 32 == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
 
-// prefix[s] = steps of the sequences before s, for all s <= num_seqs; the whole CTA.
-__device__ __forceinline__ void build_prefix(const ChunkParams &p, int64_t *prefix, bool raise) {
-  const int tid = threadIdx.x, lanes = 1 << p.lanes_log2, sub = tid & (lanes - 1);
+// The last s in [0, n) with before[s] <= x.
+__device__ __forceinline__ int find(const int64_t *before, int n, int64_t x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (before[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Inclusive prefix sums of a[1 .. n] in place, a[0] = 0; one warp.
+__device__ __forceinline__ void scan(int64_t *a, int n, int lane) {
+  int64_t carry = 0;
+  for (int base = 0; base < n; base += 32) {
+    const int i = base + lane;
+    int64_t x = i < n ? a[i + 1] : 0;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    if (i < n) a[i + 1] = carry + x;
+    carry += __shfl_sync(0xffffffffu, x, 31);
+  }
+  if (lane == 0) a[0] = 0;
+}
+
+// What the whole call comes to, as every thread knows it. Without whole tiles (front == 0)
+// range c starts at step c * even; else the starts and ranks are in shared memory.
+struct Shares {
+  int64_t U, even;  // steps in all, and the even share of a CTA
+  int W;            // CTAs with work
+  int waves;        // whole tiles of each
+  int front;
+};
+
+// Builds the list and the shares; the whole CTA. Afterwards this CTA's whole tiles are in
+// shared memory.
+template <bool kWindowed>
+__device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
+  int64_t *steps = reinterpret_cast<int64_t *>(smem + kStepsOff);
+  int64_t *tiles = reinterpret_cast<int64_t *>(smem + kTilesOff);
+  Seq *seqs = reinterpret_cast<Seq *>(smem + kSeqOff);
+  int64_t *starts = reinterpret_cast<int64_t *>(smem + kShareOff);
+  int *ranks = reinterpret_cast<int *>(smem + kRankOff);
+  Wave *list = reinterpret_cast<Wave *>(smem + kWaveOff);
+  const int lanes = 1 << p.lanes_log2, sub = tid & (lanes - 1);
   for (int base = 0; base < p.num_seqs; base += kThreads >> p.lanes_log2) {
     const int s = base + (tid >> p.lanes_log2);
     int64_t n = 0;
     if (s < p.num_seqs) {
-      const Seq q = load_seq(p, s, raise && sub == 0);
-      const int n_rt = row_tiles(p, q.Lq);
-      for (int rt = sub; rt < n_rt; rt += lanes) n += tile_of(p, q.Lq, q.ctx, rt).steps();
+      const Seq q = load_seq(p, s, cta == 0 && sub == 0);
+      const int n_tiles = tiles_of(p, q);
+      for (int i = sub; i < n_tiles; i += lanes) n += tile_of<kWindowed>(p, q, i).steps();
+      if (sub == 0) {
+        seqs[s] = q;
+        tiles[s + 1] = static_cast<int64_t>(n_tiles) * p.num_kv_heads;
+      }
     }
     for (int off = lanes >> 1; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-    if (s < p.num_seqs && sub == 0) prefix[s + 1] = n * p.num_kv_heads;
+    if (s < p.num_seqs && sub == 0) steps[s + 1] = n * p.num_kv_heads;
   }
   __syncthreads();
-  if (tid < 32) {
-    int64_t carry = 0;
-    for (int base = 0; base < p.num_seqs; base += 32) {
-      const int s = base + tid;
-      int64_t n = s < p.num_seqs ? prefix[s + 1] : 0;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, n, off);
-        if (tid >= off) n += v;
+  if (warp == 0) scan(steps, p.num_seqs, lane);
+  if (warp == 1 && p.shared_keys) scan(tiles, p.num_seqs, lane);
+  __syncthreads();
+  const int64_t U = steps[p.num_seqs];
+  Shares r;
+  r.U = U;
+  r.W = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));
+  r.waves = r.front = 0;
+  r.even = r.W == 0 ? 0 : quotient(U + r.W - 1, r.W);
+  if (r.W == 0 || !p.shared_keys) return r;
+  // tile i of the list
+  auto locate = [&](int64_t i) {
+    Wave w;
+    w.s = find(tiles, p.num_seqs, i);  // it has tiles
+    w.q = seqs[w.s];
+    const int64_t at = i - tiles[w.s];
+    const int n = tiles_of(p, w.q);
+    w.head = static_cast<int>(quotient(at, n));
+    w.tile = static_cast<int>(at - static_cast<int64_t>(w.head) * n);
+    return w;
+  };
+  // Whole tiles as far as no CTA gets more than its even share, and one more each is left
+  // to even out with.
+  int64_t mine = 0;  // thread c: steps of CTA c's whole tiles
+  for (r.waves = static_cast<int>(min(quotient(tiles[p.num_seqs], r.W) - 1, static_cast<int64_t>(kMaxWaves)));
+       r.waves > 0; r.waves >>= 1) {
+    mine = 0;
+    if (tid < r.W)
+      for (int w = 0; w < r.waves; ++w) {
+        const Wave x = locate(tid + static_cast<int64_t>(w) * r.W);
+        mine += tile_of<kWindowed>(p, x.q, x.tile).steps();
       }
-      if (s < p.num_seqs) prefix[s + 1] = carry + n;
-      carry += __shfl_sync(0xffffffffu, n, 31);
+    if (!__syncthreads_or(mine > r.even)) break;
+  }
+  if (r.waves <= 0) {
+    r.waves = 0;
+    return r;
+  }
+  if (tid < r.waves) list[tid] = locate(cta + static_cast<int64_t>(tid) * r.W);
+  if (tid < r.W) starts[tid + 1] = r.even - mine;  // what CTA c may still take
+  __syncthreads();
+  if (warp == 0) {
+    // the whole tiles, all in front of the ranges, are `front` steps
+    scan(starts, r.W, lane);
+    const int64_t front = r.even * r.W - starts[r.W];
+    int before = 0;
+    for (int base = 0; base <= r.W; base += 32) {
+      const int c = base + lane;
+      const int64_t at = c <= r.W ? min(front + starts[c], U) : U;
+      const int64_t next = c < r.W ? min(front + starts[c + 1], U) : U;
+      const uint32_t some = __ballot_sync(0xffffffffu, next > at);
+      if (c <= r.W) ranks[c] = before + __popc(some & ((1u << lane) - 1));
+      before += __popc(some);
+      __syncwarp();
+      if (c <= r.W) starts[c] = at;
+      __syncwarp();
     }
-    if (tid == 0) prefix[0] = 0;
   }
   __syncthreads();
+  r.front = 1;
+  return r;
 }
 
-// A piece as the walker publishes it: steps first .. first + steps - 1 of a tile.
+// A piece as the producer publishes it: `steps` steps from `first` of a tile's.
 struct Piece {
   int steps;       // 0: no more pieces
-  int first;
-  int s, head;     // table row, KV head
-  int row, n_tok;  // the tile's first token among all, and its tokens
-  int pos;         // position of its first token
-  int ctx, lead, j_start, lo;
+  int first, lead, j_start;
+  int pos;         // position of the tile's first token
+  int row, n_tok;  // its first token among all, and its tokens
+  int head;        // KV head
   int slot;        // where its partial result goes, or -1: it is the whole tile
   __device__ __forceinline__ int key_tile(int j) const {  // of the piece's step j
     const int k = first + j;
     return k < lead ? k : k - lead + j_start;
   }
 };
-// The rows of a key tile that no row of the segment sees: from .. to - 1 (between sinks and
-// window) and end .. (past the last key).
-struct Unseen {
-  int from, to, end;
-  __device__ __forceinline__ Unseen(const Piece &d, int j, int sinks) {
-    const int k0 = d.key_tile(j) * kKeys;
-    from = max(sinks - k0, 0);
-    to = min(d.lo - k0, kKeys);
-    end = min(d.ctx - k0, kKeys);
-  }
-};
-static_assert(sizeof(Piece) <= kDescInts * 4, "a piece fits its slot");
+constexpr int kPieceInts = sizeof(Piece) / 4;
+static_assert(kPieceInts <= kDescInts, "a piece fits its slot");
 
-// The pieces of one CTA as a role reads them.
-struct PieceReader {
-  int n = 0;  // pieces read
-  __device__ __forceinline__ bool next(uint8_t *smem, uint32_t bars, const volatile int *abort, int lane, Piece &d) {
-    const int i = n % kDescs;
-    if (!__all_sync(0xffffffffu, wait_(bars + 8 * (kBarDesc + i), (n / kDescs) & 1, abort))) return false;
-    const volatile int *src = reinterpret_cast<const volatile int *>(smem + kDescOff) + i * kDescInts;
-    int *dst = reinterpret_cast<int *>(&d);
+// Descriptor n, the first kInts ints of it, once its barrier's phase is complete.
+template <int kInts>
+__device__ __forceinline__ void read_piece(int n, const uint8_t *smem, uint32_t bars, int lane, Piece &d) {
+  const int i = n % kDescs;
+  const volatile int *src = reinterpret_cast<const volatile int *>(smem + kDescOff) + i * kDescInts;
+  int *dst = reinterpret_cast<int *>(&d);
 #pragma unroll
-    for (int k = 0; k < static_cast<int>(sizeof(Piece) / 4); ++k) dst[k] = src[k];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars + 8 * (kBarDescFree + i));
-    ++n;
-    return true;
-  }
-};
-constexpr int kDescReaders = 2 + 4;  // producer, MMA and softmax warps
+  for (int k = 0; k < kInts; ++k) dst[k] = src[k];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bars + 8 * (kBarDescFree + i));
+}
 
-// 32 columns a lane through the warp's staging area to rows of 128 bytes each:
-// words w[8 k .. 8 k + 3] and so on in 16-byte chunks, chunk c of row i at c ^ (i & 7),
-// which keeps both sides free of bank conflicts; `to` gives a row's address.
+// 16 words a lane through the warp's staging area to rows of 64 bytes each, 16-byte
+// chunk c of row i at c ^ ((i >> 1) & 3), which keeps both sides free of bank
+// conflicts; `to` gives a row's address.
 template <typename To>
-__device__ __forceinline__ void store_rows(const uint32_t (&w)[32], uint32_t scr, int n_valid, int lane, To to) {
+__device__ __forceinline__ void store_rows(const uint32_t *w, uint32_t scr, int n_valid, int lane, To to) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(scr + lane * 128 + ((k ^ (lane & 7)) * 16)),
+  for (int k = 0; k < 4; ++k)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(scr + lane * 64 + ((k ^ ((lane >> 1) & 3)) * 16)),
                  "r"(w[4 * k]), "r"(w[4 * k + 1]), "r"(w[4 * k + 2]), "r"(w[4 * k + 3])
                  : "memory");
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3), c = lane & 7;
+  for (int i = 0; i < 4; ++i) {
+    const int row = 8 * i + (lane >> 2), c = lane & 3;
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(scr + row * 128 + ((c ^ (row & 7)) * 16))
+                 : "r"(scr + row * 64 + ((c ^ ((row >> 1) & 3)) * 16))
                  : "memory");
     if (row < n_valid) *reinterpret_cast<uint4 *>(to(row) + c * 16) = v;
   }
   __syncwarp();
 }
 
+template <bool kWindowed>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map, const ChunkParams p) {
@@ -248,21 +363,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t sbase = smem_u32(smem);
-  const uint32_t bars = sbase + kBarOff;
+  const uint32_t sbase = smem_u32(smem), bars = sbase + kBarOff;
   auto bar = [&](int i) { return bars + 8u * i; };
   volatile int *abort = reinterpret_cast<volatile int *>(smem + kMiscOff + 4);
-  int64_t *prefix = reinterpret_cast<int64_t *>(smem + kPrefixOff);
+  volatile uint32_t *unseen = reinterpret_cast<volatile uint32_t *>(smem + kMiscOff + 8);  // [2]
   auto fail = [&]() {
     *abort = 1;
     atomicOr(&g_chunk_errors, kErrTimeout);
   };
-
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const bool softmax = i >= kBarP && i < kBarP + 2;
-      const bool readers = i >= kBarDescFree && i < kBarDescFree + kDescs;
-      mbar_init(bar(i), softmax ? 4 : readers ? kDescReaders : 1);
+      int count = 1;
+      if (i >= kBarP && i < kBarP + 2) count = 8;
+      if (i >= kBarDescFree && i < kBarDescFree + kDescs) count = kDescReaders;
+      if (i >= kBarX && i < kBarX + 4) count = 2;
+      mbar_init(bar(i), count);
     }
     *abort = 0;
     fence_barrier_init();
@@ -270,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&k_map);
     prefetch_tensormap(&v_map);
   }
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc(sbase + kMiscOff, kTmemCols);
     tmem_relinquish();
   }
@@ -282,456 +397,512 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncthreads_or(tid == 0 && (*reinterpret_cast<volatile uint32_t *>(&g_chunk_errors) & kErrTimeout));
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kMiscOff);
+  const int cta = blockIdx.x;
+  Shares shares = {};
+  if (!skipped) shares = build<kWindowed>(p, smem);
+  const bool works = cta < shares.W;
+  const int *ranks = reinterpret_cast<const int *>(smem + kRankOff);
+  // ranges that no CTA has cut nothing
+  if (tid == 0 && cta >= (shares.front ? ranks[shares.W]
+                                       : shares.W == 0 ? 0 : static_cast<int>(quotient(shares.U + shares.even - 1, shares.even))))
+    p.cuts[cta].pieces = 0;
 
-  const int64_t cta = blockIdx.x;
-  if (!skipped) build_prefix(p, prefix, cta == 0);
-  const int64_t U = skipped ? 0 : prefix[p.num_seqs];
-  const int64_t W = min(static_cast<int64_t>(gridDim.x), U);
-  if (cta >= W && tid == 0) p.cuts[cta].pieces = 0;
-
-  if (cta < W) {
-    if (warp == 2) {
-      // ------------------------------------------------------------ walker
-      const int64_t u_lo = range_start(cta, W, U);
-      int64_t left = range_start(cta + 1, W, U) - u_lo;
-      int lo = 0, hi = p.num_seqs - 1;  // the last s with prefix[s] <= u_lo: it has steps
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= u_lo) lo = mid; else hi = mid - 1;
-      }
-      int s = lo;
-      Seq q = load_seq(p, s, false);
-      int n_rt = row_tiles(p, q.Lq);
-      const int64_t per_head = (prefix[s + 1] - prefix[s]) / p.num_kv_heads;
-      const int64_t in_seq = u_lo - prefix[s];
-      int head = static_cast<int>(in_seq / per_head);
-      int64_t skip = in_seq - head * per_head;
-      int rt = 0;
-      for (;; rt += 32) {  // the row tile that holds step `skip` of the head: 32 at a time
-        const int n = rt + lane < n_rt ? tile_of(p, q.Lq, q.ctx, rt + lane).steps() : 0;
-        int64_t incl = n;
+  if (warp == 0 && works) {
+    // -------------------------------------------------------------- TMA producer
+    auto wait_all = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait_(bar(i), parity, abort)); };
+    const Wave *waves = reinterpret_cast<const Wave *>(smem + kWaveOff);
+    volatile int *descs = reinterpret_cast<volatile int *>(smem + kDescOff);
+    // the range: where it starts (s, head, i, first) and its length
+    int s = 0, head = 0, i = 0, n_tiles = 0, first = 0, rank, left;
+    Seq q = {0, 0, 0};
+    {
+      const int64_t *starts = reinterpret_cast<const int64_t *>(smem + kShareOff);
+      auto start = [&](int c) { return shares.front ? starts[c] : min(c * shares.even, shares.U); };
+      auto owner = [&](int64_t u) {
+        return shares.front ? find(starts, shares.W, u) : static_cast<int>(quotient(u, shares.even));
+      };
+      auto rank_of = [&](int c) { return shares.front ? ranks[c] : c; };
+      const int64_t u_lo = start(cta);
+      rank = rank_of(cta);
+      left = static_cast<int>(start(cta + 1) - u_lo);  // steps that no piece has yet
+      if (left > 0) {
+        const int64_t *steps = reinterpret_cast<const int64_t *>(smem + kStepsOff);
+        s = find(steps, p.num_seqs, u_lo);  // it has steps
+        q = reinterpret_cast<const Seq *>(smem + kSeqOff)[s];
+        n_tiles = tiles_of(p, q);
+        int64_t skip = u_lo - steps[s];
+        const int64_t per_head = quotient(steps[s + 1] - steps[s], p.num_kv_heads);
+        head = static_cast<int>(quotient(skip, per_head));
+        skip -= head * per_head;
+        for (i = 0;; i += 32) {  // the tile that holds step `skip` of the head: 32 at a time
+          const int n = i + lane < n_tiles ? tile_of<kWindowed>(p, q, i + lane).steps() : 0;
+          int64_t incl = n;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += v;
-        }
-        const uint32_t beyond = __ballot_sync(0xffffffffu, incl > skip);
-        if (beyond != 0) {
-          const int at = __ffs(beyond) - 1;
-          skip -= __shfl_sync(0xffffffffu, incl - n, at);
-          rt += at;
-          break;
-        }
-        skip -= __shfl_sync(0xffffffffu, incl, 31);
-        if (rt + 32 >= n_rt) break;  // not reached: the step lies within the head
-      }
-      int first = static_cast<int>(skip);
-      for (int n = 0;; ++n) {
-        Piece d;
-        d.steps = 0;
-        if (left > 0) {
-          const Tile t = tile_of(p, q.Lq, q.ctx, rt);
-          const int all = t.steps();
-          d.steps = static_cast<int>(min(static_cast<int64_t>(all - first), left));
-          d.first = first;
-          d.s = s;
-          d.head = head;
-          d.row = q.q0 + rt * tile_tokens(p);
-          d.n_tok = min(tile_tokens(p), q.Lq - rt * tile_tokens(p));
-          d.pos = q.ctx - q.Lq + rt * tile_tokens(p);
-          d.ctx = q.ctx;
-          d.lead = t.lead;
-          d.j_start = t.j_start;
-          d.lo = t.lo;
-          d.slot = d.steps == all ? -1 : static_cast<int>(2 * cta) + (n == 0 ? 0 : 1);
-          if (n == 0 && lane == 0) {
-            // the tile that this CTA's boundary cuts, if no boundary before does
-            ChunkCut cut = {};
-            const int64_t P0 = u_lo - first;
-            if (first > 0 && range_start(cta - 1, W, U) <= P0) {
-              cut.pieces = static_cast<int32_t>(owner_of(P0 + all - 1, W, U) - (cta - 1) + 1);
-              cut.slot0 = static_cast<int32_t>(2 * (cta - 1) + (range_start(cta - 1, W, U) < P0 ? 1 : 0));
-              cut.head = head;
-              cut.row = d.row;
-              cut.n_tok = d.n_tok;
-            }
-            p.cuts[cta] = cut;
+          for (int off = 1; off < 32; off <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
           }
-        }
-        const int i = n % kDescs;
-        if (n >= kDescs &&
-            !__all_sync(0xffffffffu, wait_(bar(kBarDescFree + i), ((n / kDescs) - 1) & 1, abort))) {
-          if (lane == 0) fail();
-          break;
-        }
-        if (lane == 0) {
-          volatile int *dst = reinterpret_cast<volatile int *>(smem + kDescOff) + i * kDescInts;
-          const int *src = reinterpret_cast<const int *>(&d);
-#pragma unroll
-          for (int k = 0; k < static_cast<int>(sizeof(Piece) / 4); ++k) dst[k] = src[k];
-          mbar_arrive(bar(kBarDesc + i));  // publishes it
-        }
-        __syncwarp();
-        if (d.steps == 0) break;
-        left -= d.steps;
-        first = 0;
-        if (left > 0 && ++rt == n_rt) {
-          rt = 0;
-          if (++head == p.num_kv_heads) {
-            head = 0;
-            do {
-              ++s;
-            } while (prefix[s + 1] == prefix[s]);  // steps are left, so a sequence has them
-            q = load_seq(p, s, false);
-            n_rt = row_tiles(p, q.Lq);
-          }
-        }
-      }
-    } else if (warp == 0) {
-      // ------------------------------------------------------------ TMA producer
-      // Lane b < 128 / box_rows owns the b-th box of every key tile: it reads that
-      // box's table entry a step ahead and issues the box's copies; lane 0 arms the
-      // barriers. Boxes that no row of the segment sees are left out.
-      const int box_rows = p.box_rows, n_boxes = kKeys / box_rows;
-      PieceReader reader;
-      Piece d;
-      bool good = true;
-      int gk = 0;  // steps of this CTA so far
-      while (good && (good = reader.next(smem, bars, abort, lane, d)) && d.steps > 0) {
-        const int piece = reader.n - 1, qb = piece & 1;
-        const int32_t *table = p.block_tables + static_cast<int64_t>(d.s) * p.max_blocks;
-        auto key_of = [&](int j) { return d.key_tile(j) * kKeys + lane * box_rows; };
-        auto wanted = [&](int j) {
-          if (lane >= n_boxes || j >= d.steps) return false;
-          const int k = key_of(j);
-          return k < d.ctx && (k + box_rows > d.lo || k < p.sinks);
-        };
-        auto entry = [&](int j) { return wanted(j) ? __ldg(table + fast_quotient(key_of(j), p.block)) : -1; };
-        int32_t blk = entry(0);
-        if (piece >= 2 &&
-            !__all_sync(0xffffffffu, wait_(bar(kBarQFree + qb), ((piece >> 1) - 1) & 1, abort))) {
-          good = false;
-          break;
-        }
-        if (lane == 0) {
-          const uint32_t dst = sbase + kQOff + qb * kTileBytes;
-          mbar_arrive_expect_tx(bar(kBarQ + qb), kTileBytes);
-          tma_load_3d(dst, &q_map, bar(kBarQ + qb), 0, d.head << p.gqa_log2, d.row);
-          tma_load_3d(dst + kHalfBytes, &q_map, bar(kBarQ + qb), 64, d.head << p.gqa_log2, d.row);
-        }
-        for (int j = 0; j < d.steps; ++j, ++gk) {
-          const int32_t next = entry(j + 1);
-          int32_t row = -1;  // cache row of this lane's box
-          if (wanted(j)) {
-            if (blk >= 0 && blk < p.num_blocks) {
-              const uint32_t key = key_of(j);
-              row = blk * static_cast<int32_t>(p.block.d) + (key - fast_quotient(key, p.block) * p.block.d);
-            } else {
-              atomicOr(&g_chunk_errors, kErrBlock);
-            }
-          }
-          blk = next;
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * 2u * box_rows * 128u;
-          const int b = gk & 1;
-          const uint32_t at = b * kTileBytes + lane * box_rows * 128;
-          // S of step gk - 2 has been the last to read this K tile, P.V this V tile
-          if (gk >= 2 && !__all_sync(0xffffffffu, wait_(bar(kBarS + b), ((gk >> 1) - 1) & 1, abort))) {
-            good = false;
+          const uint32_t beyond = __ballot_sync(0xffffffffu, incl > skip);
+          if (beyond != 0 || i + 32 >= n_tiles) {  // the step lies within the head: some lane is beyond it
+            const int at = max(__ffs(beyond) - 1, 0);
+            skip -= __shfl_sync(0xffffffffu, incl - n, at);
+            i += at;
             break;
           }
-          if (lane == 0) mbar_arrive_expect_tx(bar(kBarK + b), bytes);
-          __syncwarp();
-          if (row >= 0) {
-            tma_load_3d(sbase + kKOff + at, &k_map, bar(kBarK + b), 0, d.head, row);
-            tma_load_3d(sbase + kKOff + at + kHalfBytes, &k_map, bar(kBarK + b), 64, d.head, row);
-          }
-          if (gk >= 2 && !__all_sync(0xffffffffu, wait_(bar(kBarO + b), ((gk >> 1) - 1) & 1, abort))) {
-            good = false;
-            break;
-          }
-          if (lane == 0) mbar_arrive_expect_tx(bar(kBarV + b), bytes);
-          __syncwarp();
-          if (row >= 0) {
-            tma_load_3d(sbase + kVOff + at, &v_map, bar(kBarV + b), 0, d.head, row);
-            tma_load_3d(sbase + kVOff + at + kHalfBytes, &v_map, bar(kBarV + b), 64, d.head, row);
+          skip -= __shfl_sync(0xffffffffu, incl, 31);
+        }
+        first = static_cast<int>(skip);
+        // the tile that the range's start cuts, if no range before does
+        ChunkCut cut = {};
+        const int64_t P0 = u_lo - first;
+        if (first > 0) {
+          const int before = owner(u_lo - 1);  // the range before
+          if (start(before) <= P0) {
+            const Tile t = tile_of<kWindowed>(p, q, i);
+            cut.pieces = rank_of(owner(P0 + t.steps() - 1)) - rank_of(before) + 1;
+            cut.slot0 = 2 * rank_of(before) + (start(before) < P0 ? 1 : 0);
+            cut.head = head;
+            cut.row = q.q0 + t.t0;
+            cut.n_tok = t.n_tok;
           }
         }
+        if (lane == 0) p.cuts[rank] = cut;
       }
-      // every copy of this CTA is issued: the next kernel may start launching
-      if (lane == 0) griddep_launch_dependents();
-      if (!good && lane == 0) fail();
-    } else if (warp == 1) {
-      // ------------------------------------------------------------ MMA issuer
-      // The whole warp runs the loop and its waits (warp-uniform control flow) and
-      // one elected lane, always the same, issues every MMA and commit. The operand
-      // descriptors are 32-bit low halves over one common high half.
-      auto wait_all = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait_(bar(i), parity, abort)); };
-      const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_sw128(sbase, 16, 1024) >> 32);
-      const uint32_t lo0 = static_cast<uint32_t>(smem_desc_sw128(sbase, 16, 1024));
-      constexpr uint32_t kVLbo = static_cast<uint32_t>((kHalfBytes - 16) >> 4) << 16;
-      auto desc = [&](int off) { return lo0 + static_cast<uint32_t>(off >> 4); };
-      auto issue_s = [&](int gk, int piece, bool opens, bool closes) -> bool {
-        const int b = gk & 1, qb = piece & 1;
-        if (opens && !wait_all(kBarQ + qb, (piece >> 1) & 1)) return false;
-        if (!wait_all(kBarK + b, (gk >> 1) & 1)) return false;
-        const uint32_t qd = desc(kQOff + qb * kTileBytes), kd = desc(kKOff + b * kTileBytes);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kD / 16; ++kk) {
-            const uint32_t off16 = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
-            mma_bf16_ss(tmem + b * kKeys, qd + off16, kd + off16, desc_hi, kIdescQK, kk > 0);
-          }
-          mma_commit(bar(kBarS + b));
-          if (closes) mma_commit(bar(kBarQFree + qb));
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_pv = [&](int gk, bool opens, const Unseen &u) -> bool {
-        const int b = gk & 1;
-        if (!wait_all(kBarV + b, (gk >> 1) & 1)) return false;
-        if (u.from < u.to || u.end < kKeys) {
-          auto zero = [&](int from, int to) {
-            const uint32_t base = sbase + kVOff + b * kTileBytes;
-            for (int i = from * 16 + lane; i < to * 16; i += 32) {
-              const uint32_t addr = base + ((i & 8) ? kHalfBytes : 0) + (i >> 4) * 128 + (i & 7) * 16;
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
-            }
-          };
-          zero(u.from, u.to);
-          zero(u.end, kKeys);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        if (!wait_all(kBarP + b, (gk >> 1) & 1)) return false;
-        tc_fence_after();
-        const uint32_t vd = desc(kVOff + b * kTileBytes) + kVLbo;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_bf16_ts(tmem + kTmemO, tmem + b * kKeys + kk * 8, vd + ((kk * 16 * 128) >> 4), desc_hi, kIdescPV,
-                        (!opens || kk > 0) ? 1u : 0u);
-          mma_commit(bar(kBarO + b));
-        }
-        __syncwarp();
-        return true;
-      };
-      PieceReader reader;
-      Piece d;
-      bool good = reader.next(smem, bars, abort, lane, d);
-      bool more = good && d.steps > 0;
-      int gk = 0, j = 0;
-      if (more) good = issue_s(0, 0, true, d.steps == 1);
-      while (good && more) {
-        const bool opens = j == 0;
-        const Unseen unseen(d, j, p.sinks);
-        if (++j == d.steps) {
-          good = reader.next(smem, bars, abort, lane, d);
-          more = good && d.steps > 0;
-          j = 0;
-        }
-        if (good && more) good = issue_s(gk + 1, reader.n - 1, j == 0, j == d.steps - 1);
-        if (good) good = issue_pv(gk, opens, unseen);
-        ++gk;
-      }
-      // every MMA issued here has completed, and its commits arrived, before the CTA ends
-      if (elect_one()) mma_commit(bar(kBarDone));
       __syncwarp();
-      if (!wait_all(kBarDone, 0)) good = false;
-      for (int g = max(gk - 2, 0); good && g < gk; ++g)
-        good = wait_all(kBarS + (g & 1), (g >> 1) & 1) && wait_all(kBarO + (g & 1), (g >> 1) & 1);
-      for (int n = max(reader.n - 3, 0); good && n < reader.n - 1; ++n)
-        good = wait_all(kBarQFree + (n & 1), (n >> 1) & 1);
-      if (!good && lane == 0) fail();
-    } else if (warp >= 4) {
-      // ------------------------------------------------------------ softmax
-      const int quad = warp & 3;       // TMEM lane quadrant this warp may access
-      const int r = quad * 32 + lane;  // row within the tile == TMEM lane
-      const int tok = r >> p.gqa_log2, h = r & ((1 << p.gqa_log2) - 1);
-      const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-      const uint32_t tO = tmem + kTmemO + lane_off;
-      const uint32_t scr = sbase + kEpiOff + quad * kEpiWarpBytes;
-      const uint64_t scl = f32x2(p.scale_log2, p.scale_log2);
-      PieceReader reader;
-      Piece d;
-      bool good = true;
-      int gk = 0;
-      while (good && (good = reader.next(smem, bars, abort, lane, d)) && d.steps > 0) {
-        const bool live = tok < d.n_tok;
-        const bool any = (quad * 32) >> p.gqa_log2 < d.n_tok;  // some row of the warp is
-        const int lim = d.pos + tok;                           // last key this row sees
-        const int first = p.window > 0 ? lim - p.window + 1 : 0;
-        // of the warp's rows: the smallest last key and the largest first one
-        const int lim_min = d.pos + ((quad * 32) >> p.gqa_log2);
-        const int first_max = p.window > 0 ? d.pos + ((quad * 32 + 31) >> p.gqa_log2) - p.window + 1 : 0;
-        float m = kFloor, l = 0.f, lr = 0.f;
-        for (int j = 0; j < d.steps; ++j, ++gk) {
-          const int b = gk & 1;
-          if (!__all_sync(0xffffffffu, wait_(bar(kBarS + b), (gk >> 1) & 1, abort))) {
-            good = false;
-            break;
+      fence_proxy_async_smem();  // the copies overwrite the list
+    }
+    // The next piece into d, published; false if a wait gave up.
+    int n_pieces = 0, lo = 0, ctx = 0;
+    bool in_range = false;  // a piece of the range has been published
+    const int32_t *table = nullptr;  // of d's sequence
+    Piece d;
+    auto next_piece = [&]() -> bool {
+      const int slot = n_pieces % kDescs;
+      d.steps = 0;
+      const bool wave = n_pieces < shares.waves;
+      if (wave || left > 0) {
+        Seq x;
+        int at, xs, from = 0;
+        if (wave) {
+          const Wave w = waves[n_pieces];
+          x = w.q, at = w.tile, xs = w.s, d.head = w.head;
+        } else {
+          if (in_range && ++i == n_tiles) {
+            i = 0;
+            if (++head == p.num_kv_heads) {
+              head = 0;
+              do q = load_seq(p, ++s, false);  // steps are left, so a sequence has them
+              while (q.Lq == 0);
+              n_tiles = tiles_of(p, q);
+            }
           }
-          if (any) {
-            tc_fence_after();
-            const uint32_t tS = tmem + b * kKeys + lane_off;
-            const int k0 = d.key_tile(j) * kKeys;
-            uint32_t x[kKeys];
-#pragma unroll
-            for (int c = 0; c < kKeys; c += 32) tmem_ld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
-            tmem_wait_ld();
-            if (p.flip != 0) {
-#pragma unroll
-              for (int c = 0; c < kKeys; ++c) x[c] ^= 0x80000000u;
-            }
-            // masked logits become -inf, their probabilities 0
-            if (k0 + kKeys - 1 > lim_min || (k0 < first_max && k0 + kKeys > p.sinks)) {
-              const int keep = lim - k0, skip = first - k0, sink = p.sinks - k0;
-#pragma unroll
-              for (int c = 0; c < kKeys; ++c)
-                if (c > keep || (c < skip && c >= sink)) x[c] = 0xFF800000u;
-            }
-            // P = 2^(x * scale - mm), packed two per column over the first 64 columns
-            // of S; ts and tr get the row's sums of the fp32 and of the rounded values
-            auto exps = [&](float mm, float &ts, float &tr) {
-              const uint64_t nm = f32x2(-mm, -mm);
-              uint64_t s0 = 0, s1 = 0;
-              float r0l = 0.f, r0h = 0.f, r1l = 0.f, r1h = 0.f;
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                uint32_t pk[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  const int k = hf * 64 + 2 * c;
-                  const uint64_t e = fma2(f32x2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), scl, nm);
-                  const float p0 = fast_exp2(f32x2_lo(e)), p1 = fast_exp2(f32x2_hi(e));
-                  pk[c] = pack_bf16x2(p0, p1);
-                  if (c & 1) {
-                    add2(s1, f32x2(p0, p1));
-                    add_bf16x2_to_f32(r1l, r1h, pk[c]);
-                  } else {
-                    add2(s0, f32x2(p0, p1));
-                    add_bf16x2_to_f32(r0l, r0h, pk[c]);
-                  }
-                }
-                tmem_st32(tS + hf * 32, pk);
-              }
-              add2(s0, s1);
-              ts = f32x2_lo(s0) + f32x2_hi(s0);
-              tr = (r0l + r1l) + (r0h + r1h);
-            };
-            // First with the row's current maximum; if some row's probabilities then sum
-            // to more than 2^8 (a logit well above m), the warp takes the exact maximum,
-            // rescales O and recomputes P over what it wrote. A piece's first step
-            // always takes the maximum.
-            float ts, tr;
-            bool exact = j == 0;
-#pragma unroll 1
-            for (;;) {
-              if (exact) {
-                float a[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] = __uint_as_float(x[i]);
-#pragma unroll
-                for (int c = 8; c < kKeys; c += 16)
-#pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    a[i] = fmax3(a[i], __uint_as_float(x[c + i]), __uint_as_float(x[c + 8 + i]));
-                const float mx = fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
-                const float m_new = fmaxf(m, mx * p.scale_log2);  // -inf stays -inf
-                if (j > 0) {
-                  // O holds every step up to j - 1 once that P.V is complete
-                  if (!__all_sync(0xffffffffu, wait_(bar(kBarO + (b ^ 1)), ((gk - 1) >> 1) & 1, abort))) {
-                    good = false;
-                    break;
-                  }
-                  tc_fence_after();
-                  const float alpha = fast_exp2(m - m_new);
-#pragma unroll 1
-                  for (int c = 0; c < kD; c += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + c, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                    tmem_st32(tO + c, o);
-                  }
-                  tmem_wait_st();
-                  l *= alpha;
-                  lr *= alpha;
-                }
-                m = m_new;
-              }
-              exps(m, ts, tr);
-              if (exact || !__any_sync(0xffffffffu, live && !(ts <= kLazyBound))) break;
-              exact = true;
-            }
-            if (!good) break;
-            l += ts;
-            lr += tr;
-            tmem_wait_st();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarP + b));
+          if (!in_range) from = first;
+          x = q, at = i, xs = s, d.head = head;
         }
+        const Tile t = tile_of<kWindowed>(p, x, at);
+        const int all = t.steps();
+        d.steps = wave ? all : min(all - from, left);
+        d.first = from;
+        d.lead = t.lead;
+        d.j_start = t.j_start;
+        d.pos = x.ctx - x.Lq + t.t0;
+        d.row = x.q0 + t.t0;
+        d.n_tok = t.n_tok;
+        d.slot = d.steps == all ? -1 : 2 * rank + (in_range ? 1 : 0);
+        table = p.block_tables + static_cast<int64_t>(xs) * p.max_blocks;
+        lo = t.lo;
+        ctx = x.ctx;
+        if (!wave) {
+          left -= d.steps;
+          in_range = true;
+        }
+      }
+      if (n_pieces >= kDescs && !wait_all(kBarDescFree + slot, ((n_pieces / kDescs) - 1) & 1)) return false;
+      if (lane == 0) {
+        const int *src = reinterpret_cast<const int *>(&d);
+#pragma unroll
+        for (int k = 0; k < kPieceInts; ++k) descs[slot * kDescInts + k] = src[k];
+        mbar_arrive(bar(kBarDesc + slot));  // publishes it
+      }
+      __syncwarp();
+      ++n_pieces;
+      return true;
+    };
+    // Lane b < 128 / box_rows owns the b-th box of every key tile: it reads that
+    // box's table entry a step ahead and issues the box's copies; lane 0 arms the
+    // barriers. Boxes that no row of the tile sees are left out.
+    const int box_rows = p.box_rows;
+    auto key_of = [&](int j) { return d.key_tile(j) * kKeys + lane * box_rows; };
+    auto wanted = [&](int j) {
+      const int k = key_of(j);
+      return lane * box_rows < kKeys && k < ctx && (!kWindowed || k + box_rows > lo || k < p.sinks);
+    };
+    auto entry = [&](int j) { return wanted(j) ? __ldg(table + fast_quotient(key_of(j), p.block)) : -1; };
+    bool good = next_piece();
+    int32_t blk = d.steps > 0 ? entry(0) : -1;
+    int g = 0;  // steps so far
+    // V goes out a step behind K: the next K is wanted first, and its stage is free first
+    int32_t v_row = -1;
+    uint32_t v_bytes = 0, v_unseen = 0;
+    int v_head = 0;
+    auto load_v = [&](int step) -> bool {
+      const int b = step & 1;
+      // P.V of step - 2 has been the last to read this V tile
+      if (step >= 2 && !wait_all(kBarO + b, ((step >> 1) - 1) & 1)) return false;
+      if (lane == 0) {
+        unseen[b] = v_unseen;
+        mbar_arrive_expect_tx(bar(kBarV + b), v_bytes);  // publishes `unseen` as well
+      }
+      __syncwarp();
+      if (v_row >= 0) {
+        const uint32_t at = sbase + kVOff + b * kTileBytes + lane * box_rows * 128;
+        tma_load_3d(at, &v_map, bar(kBarV + b), 0, v_head, v_row);
+        tma_load_3d(at + kHalfBytes, &v_map, bar(kBarV + b), 64, v_head, v_row);
+      }
+      return true;
+    };
+    while (good && d.steps > 0) {
+      const int steps = d.steps, kv_head = d.head, piece = n_pieces - 1, qb = piece & 1;
+      if (piece >= 2 && !(good = wait_all(kBarQFree + qb, ((piece >> 1) - 1) & 1))) break;
+      if (lane == 0) {
+        const uint32_t dst = sbase + kQOff + qb * kTileBytes;
+        mbar_arrive_expect_tx(bar(kBarQ + qb), kTileBytes);
+        tma_load_3d(dst, &q_map, bar(kBarQ + qb), 0, kv_head << p.gqa_log2, d.row);
+        tma_load_3d(dst + kHalfBytes, &q_map, bar(kBarQ + qb), 64, kv_head << p.gqa_log2, d.row);
+      }
+      __syncwarp();
+      for (int j = 0; good && j < steps; ++j, ++g) {
+        const int k0 = d.key_tile(j) * kKeys;
+        // V rows that no row of the tile sees: from .. to - 1 and end ..
+        const uint32_t from = static_cast<uint32_t>(min(max(p.sinks - k0, 0), kKeys));
+        const uint32_t to = static_cast<uint32_t>(min(max(lo - k0, 0), kKeys));
+        const uint32_t end = static_cast<uint32_t>(min(ctx - k0, kKeys));
+        int32_t row = -1;  // cache row of this lane's box
+        if (wanted(j)) {
+          if (blk >= 0 && blk < p.num_blocks) {
+            const uint32_t key = key_of(j);
+            row = blk * static_cast<int32_t>(p.block.d) + (key - fast_quotient(key, p.block) * p.block.d);
+          } else {
+            atomicOr(&g_chunk_errors, kErrBlock);
+          }
+        }
+        // the entry of the next step, which may be the next piece's first
+        if (j + 1 < steps) {
+          blk = entry(j + 1);
+        } else {
+          good = next_piece();
+          blk = d.steps > 0 ? entry(0) : -1;
+        }
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * 2u * box_rows * 128u;
+        const int b = g & 1;
+        // S of step g - 2 has been the last to read this K tile
+        if (g >= 2) good = good && wait_all(kBarS + b, ((g >> 1) - 1) & 1);
         if (!good) break;
-        const int last = gk - 1;
-        if (!any) continue;
-        if (!__all_sync(0xffffffffu, wait_(bar(kBarO + (last & 1)), (last >> 1) & 1, abort))) {
-          good = false;
-          break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(kBarK + b), bytes);
+        __syncwarp();
+        if (row >= 0) {
+          const uint32_t at = sbase + kKOff + b * kTileBytes + lane * box_rows * 128;
+          tma_load_3d(at, &k_map, bar(kBarK + b), 0, kv_head, row);
+          tma_load_3d(at + kHalfBytes, &k_map, bar(kBarK + b), 64, kv_head, row);
         }
-        tc_fence_after();
-        const int n_valid = min(32, (d.n_tok << p.gqa_log2) - quad * 32);
-        if (d.slot < 0) {
-          const float inv = 1.f / lr;
-          const int64_t head0 = static_cast<int64_t>(d.head) << p.gqa_log2;
-          auto to = [&](int i, int half) {
-            const int ri = quad * 32 + i;
-            const int64_t at = static_cast<int64_t>(d.row + (ri >> p.gqa_log2)) * p.num_q_heads + head0 +
-                               (ri & ((1 << p.gqa_log2) - 1));
-            return reinterpret_cast<uint8_t *>(p.out + at * kD + half * 64);
-          };
+        if (g >= 1 && !(good = load_v(g - 1))) break;
+        v_row = row;
+        v_bytes = bytes;
+        v_head = kv_head;
+        v_unseen = (from < to ? from | to << 8 : 0) | end << 16;
+      }
+    }
+    if (good && g >= 1) good = load_v(g - 1);
+    if (!good) {
+      if (lane == 0) fail();
+      // copies that nobody waits for any more land in this CTA's memory: outlast them
+      for (int k = 0; k < 200; ++k) __nanosleep(1000);
+    }
+  } else if (warp == kMmaWarp && works) {
+    // -------------------------------------------------------------- MMA issuer
+    // The whole warp runs the loop and its waits (warp-uniform control flow) and
+    // one elected lane, always the same, issues every MMA and commit. The operand
+    // descriptors are 32-bit low halves over one common high half.
+    const uint32_t desc_hi = static_cast<uint32_t>(smem_desc_sw128(sbase, 16, 1024) >> 32);
+    const uint32_t lo0 = static_cast<uint32_t>(smem_desc_sw128(sbase, 16, 1024));
+    constexpr uint32_t kVLbo = static_cast<uint32_t>((kHalfBytes - 16) >> 4) << 16;
+    bool good = true;
+    int n = 0;  // pieces read
+    // steps of the next piece, in a uniform register (0: none)
+    auto read = [&]() -> int {
+      const bool ok = wait_(bar(kBarDesc + n % kDescs), (n / kDescs) & 1, abort);
+      if (!(good = __all_sync(0xffffffffu, ok))) return 0;
+      const int steps = reinterpret_cast<const volatile int *>(smem + kDescOff)[n % kDescs * kDescInts];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarDescFree + n % kDescs));
+      ++n;
+      return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<uint32_t>(steps)));
+    };
+    // S of step g; opens, closes: the first, the last of piece `piece`
+    auto issue_s = [&](int g, int piece, bool opens, bool closes) {
+      const int b = g & 1, qb = piece & 1;
+      bool ok = !opens || wait_(bar(kBarQ + qb), (piece >> 1) & 1, abort);
+      ok = wait_(bar(kBarK + b), (g >> 1) & 1, abort) && ok;
+      if (!(good = __all_sync(0xffffffffu, ok && good))) return;
+      const uint32_t qd = lo0 + (kQOff >> 4) + qb * (kTileBytes >> 4), kd = lo0 + (kKOff >> 4) + b * (kTileBytes >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kD / 16; ++kk) {
+          const uint32_t off16 = ((kk >> 2) * kHalfBytes + (kk & 3) * 32) >> 4;
+          mma_bf16_ss(tmem + b * kKeys, qd + off16, kd + off16, desc_hi, kIdescQK, kk > 0);
+        }
+        mma_commit(bar(kBarS + b));
+        if (closes) mma_commit(bar(kBarQFree + qb));
+      }
+      __syncwarp();
+    };
+    auto issue_pv = [&](int g, bool opens) {
+      const int b = g & 1;
+      bool ok = wait_(bar(kBarV + b), (g >> 1) & 1, abort);
+      if (!(good = __all_sync(0xffffffffu, ok && good))) return;
+      const uint32_t u = unseen[b];
+      if (u != kKeys << 16) {
+        const uint32_t tile = sbase + kVOff + b * kTileBytes;
+        auto zero = [&](int from, int to) {
+          for (int i = from * 16 + lane; i < to * 16; i += 32) {
+            const uint32_t addr = tile + ((i & 8) ? kHalfBytes : 0) + (i >> 4) * 128 + (i & 7) * 16;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0u) : "memory");
+          }
+        };
+        __syncwarp();
+        zero(u & 255, (u >> 8) & 255);
+        zero(u >> 16, kKeys);
+        fence_proxy_async_smem();
+      }
+      ok = wait_(bar(kBarP + b), (g >> 1) & 1, abort);
+      if (!(good = __all_sync(0xffffffffu, ok && good))) return;
+      tc_fence_after();
+      const uint32_t vd = lo0 + (kVOff >> 4) + b * (kTileBytes >> 4) + kVLbo, old = opens ? 0u : 1u;
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_bf16_ts(tmem + kTmemO, tmem + b * kKeys + (kk >> 2) * 64 + (kk & 3) * 8, vd + ((kk * 16 * 128) >> 4), desc_hi, kIdescPV,
+                      kk > 0 ? 1u : old);
+        mma_commit(bar(kBarO + b));
+      }
+      __syncwarp();
+    };
+    int g = 0, j = 0, steps = read();
+    bool more = good && steps > 0;
+    if (more) issue_s(0, 0, true, steps == 1);
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[64], w[32];
-            tmem_ld32(tO + half * 64, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-            tmem_ld32(tO + half * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+    while (good && more) {
+      const bool opens = j == 0;
+      if (++j == steps) {
+        steps = read();
+        more = steps > 0;
+        j = 0;
+      }
+      if (good && more) issue_s(g + 1, n - 1, j == 0, j + 1 == steps);
+      if (good) issue_pv(g, opens);
+      ++g;
+    }
+    // every copy that this CTA needs has landed: the next kernel may start launching
+    if (lane == 0) griddep_launch_dependents();
+    // every MMA issued here has completed, and its commits arrived, before the CTA ends
+    if (elect_one()) mma_commit(bar(kBarDone));
+    __syncwarp();
+    auto wait_all = [&](int i, uint32_t parity) { return __all_sync(0xffffffffu, wait_(bar(i), parity, abort)); };
+    if (!wait_all(kBarDone, 0)) good = false;
+    for (int x = max(g - 2, 0); good && x < g; ++x)
+      good = wait_all(kBarS + (x & 1), (x >> 1) & 1) && wait_all(kBarO + (x & 1), (x >> 1) & 1);
+    for (int x = max(n - 3, 0); good && x < n - 1; ++x) good = wait_all(kBarQFree + (x & 1), (x >> 1) & 1);
+    if (!good && lane == 0) fail();
+  } else if (warp >= kSoftmaxWarp0 && works) {
+    // -------------------------------------------------------------- softmax
+    const int half = (warp - kSoftmaxWarp0) >> 2;  // of the columns
+    const int quad = warp & 3;                     // TMEM lane quadrant this warp may access
+    const int r = quad * 32 + lane;                // row within the tile == TMEM lane
+    const int tok0 = (quad * 32) >> p.gqa_log2, tok = r >> p.gqa_log2;  // the warp's first token, the row's
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t tO = tmem + kTmemO + half * 64 + lane_off;
+    const uint32_t scr = sbase + kEpiOff + (warp - kSoftmaxWarp0) * kEpiWarpBytes;
+    // [2 steps][2 halves][128]: maxima; then [2 sums][2 halves][128]
+    volatile float *swap = reinterpret_cast<volatile float *>(smem + kSwapOff);
+    const uint32_t masked = p.scale_log2 < 0.f ? 0x7F800000u : 0xFF800000u;  // times the scale: -inf
+    bool good = true;
+    int g = 0;
+    uint32_t x_par = 0;  // parity of the next exchange
+    // Both warps of the quadrant have come here, and see what the other wrote before.
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarX + quad));
+      const bool ok = __all_sync(0xffffffffu, wait_(bar(kBarX + quad), x_par, abort));
+      x_par ^= 1;
+      return ok;
+    };
+    for (int n = 0;; ++n) {
+      Piece d;
+      if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarDesc + n % kDescs), (n / kDescs) & 1, abort)))) break;
+      read_piece<kPieceInts>(n, smem, bars, lane, d);
+      if (d.steps == 0) break;
+      const bool live = tok < d.n_tok;
+      const bool any = tok0 < d.n_tok;  // some row of the warp is
+      const int lim = d.pos + tok;      // last key this row sees
+      float m = kFloor, l = 0.f, lr = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < d.steps; ++j, ++g) {
+        const int b = g & 1;
+        if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarS + b), (g >> 1) & 1, abort)))) break;
+        if (any) {
+          tc_fence_after();
+          const uint32_t tS = tmem + b * kKeys + lane_off;
+          const int k0 = d.key_tile(j) * kKeys;
+          // whether some key of the step is masked for some row of the warp
+          bool some = k0 + kKeys - 1 > d.pos + tok0;
+          if constexpr (kWindowed)  // the largest first key of the warp's rows
+            some = some || (k0 <= d.pos + tok0 + (31 >> p.gqa_log2) - p.window && k0 + kKeys > p.sinks);
+          const int keep = lim - k0;  // columns up to it are at or before the row's position
+          // 32 columns of S, masked logits as -inf once scaled. Columns that every row of the
+          // warp sees are left alone.
+          auto columns = [&](int c, uint32_t (&x)[32]) {
+            tmem_ld32(tS + c, x);
             tmem_wait_ld();
+            if (!some) return;
+            auto below = [](int i) { return i <= 0 ? 0u : i >= 32 ? 0xffffffffu : (1u << i) - 1; };
+            uint32_t seen = below(keep + 1 - c);  // as bits
+            if constexpr (kWindowed)              // but for those between the sinks and the window
+              seen &= ~below(keep - p.window + 1 - c) | below(p.sinks - k0 - c);
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) return;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-            store_rows(w, scr, n_valid, lane, [&](int i) { return to(i, half); });
-          }
-          if (live && p.lse != nullptr)
-            p.lse[static_cast<int64_t>(d.row + tok) * p.num_q_heads + head0 + h] = (m + log2f(l)) * kLn2;
-        } else {
-          float *dst = p.ws_o + (static_cast<int64_t>(d.slot) * kRows + quad * 32) * kD;
+              if (!(seen >> i & 1)) x[i] = masked;
+          };
+          // First pass: the maximum of the thread's columns, then of the row's. The running one
+          // moves only where it is exceeded by more than 2^8: the warps then rescale O. A
+          // piece's first step always does. Neither pass is unrolled over the columns: their
+          // code then stays in the instruction cache beside the MMA warp's (as one piece of
+          // code over 128 values in registers a step took 2,200 to 3,000 cycles).
+          float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < kD; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(tO + c, o);
-            tmem_wait_ld();
-            store_rows(o, scr, n_valid, lane, [&](int i) { return reinterpret_cast<uint8_t *>(dst + i * kD + c); });
+          for (int c = half * 64; c < half * 64 + 64; c += 32) {
+            uint32_t x[32];
+            columns(c, x);
+            if (p.scale_log2 < 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] ^= 0x80000000u;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              a[(i >> 1) & 3] = fmax3(a[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
           }
-          if (live) p.ws_ml[static_cast<int64_t>(d.slot) * kRows + r] = make_float4(m, l, lr, 0.f);
+          // (two steps' worth of places: a warp may be a step ahead of the other's reading)
+          float mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * fabsf(p.scale_log2);  // -inf stays -inf
+          swap[(b * 2 + half) * kRows + r] = mx;
+          if (!(good = meet())) break;
+          mx = fmaxf(mx, swap[(b * 2 + 1 - half) * kRows + r]);
+          if (__any_sync(0xffffffffu, live && !(mx <= m + kLazyMax))) {
+            const float m_new = fmaxf(m, mx);
+            if (j > 0) {
+              // O holds every step up to j - 1 once that P.V is complete
+              if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarO + (b ^ 1)), ((g - 1) >> 1) & 1, abort)))) break;
+              tc_fence_after();
+              const float alpha = fast_exp2(m - m_new);
+#pragma unroll 1
+              for (int c = 0; c < 64; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st32(tO + c, o);
+              }
+              l *= alpha;
+              lr *= alpha;
+            }
+            m = m_new;
+          }
+          // Second pass: P = 2^(x * scale - m), packed two per column over the first columns
+          // of the thread's own half, whose logits have been read, and the sums of the fp32
+          // and of the rounded values, over eight chains each.
+          float s8[8] = {}, r8[8] = {};
+#pragma unroll 1
+          for (int c = half * 64; c < half * 64 + 64; c += 32) {
+            uint32_t x[32], pk[16];
+            columns(c, x);
+            float e[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) e[i] = fast_exp2(fmaf(__uint_as_float(x[i]), p.scale_log2, -m));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
+            tmem_st16(tS + half * 32 + c / 2, pk);  // over columns of this half
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s8[i & 7] += e[i];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) add_bf16x2_to_f32(r8[2 * (i & 3)], r8[2 * (i & 3) + 1], pk[i]);
+          }
+          l += ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
+          lr += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + b));
+      }
+      if (!good) break;
+      if (!any) continue;
+      // The piece's last P.V; the next one's first, which overwrites O, waits for this
+      // warp's next P. The halves' sums are added up, then each warp has half of O's columns.
+      if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort)))) break;
+      tc_fence_after();
+      swap[(4 + half) * kRows + r] = l;
+      swap[(6 + half) * kRows + r] = lr;
+      if (!(good = meet())) break;
+      l += swap[(5 - half) * kRows + r];
+      lr += swap[(7 - half) * kRows + r];
+      const int n_valid = min(32, (d.n_tok - tok0) << p.gqa_log2);
+      const float inv = d.slot < 0 ? 1.f / lr : 1.f;
+      const int64_t row0 = static_cast<int64_t>(d.row + tok0) * p.num_q_heads + (static_cast<int64_t>(d.head) << p.gqa_log2);
+#pragma unroll 1
+      for (int c = 0; c < 64; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+        const int col = half * 64 + c;
+        if (d.slot < 0) {
+          uint32_t y[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            y[i] = pack_bf16x2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+          store_rows(y, scr, n_valid, lane, [&](int i) {
+            const int64_t at = row0 + static_cast<int64_t>(i >> p.gqa_log2) * p.num_q_heads + (i & ((1 << p.gqa_log2) - 1));
+            return reinterpret_cast<uint8_t *>(p.out + at * kD + col);
+          });
+        } else {
+          float *dst = p.ws_o + (static_cast<int64_t>(d.slot) * kRows + quad * 32) * kD + col;
+          store_rows(o, scr, n_valid, lane, [&](int i) { return reinterpret_cast<uint8_t *>(dst + i * kD); });
+          store_rows(o + 16, scr, n_valid, lane, [&](int i) { return reinterpret_cast<uint8_t *>(dst + i * kD + 16); });
         }
       }
-      if (!good && lane == 0) fail();
+      if (live && half == 0) {
+        if (d.slot >= 0)
+          p.ws_ml[static_cast<int64_t>(d.slot) * kRows + r] = make_float4(m, l, lr, 0.f);
+        else if (p.lse != nullptr)
+          p.lse[row0 + static_cast<int64_t>(lane >> p.gqa_log2) * p.num_q_heads + (lane & ((1 << p.gqa_log2) - 1))] =
+              (m + log2f(l)) * kLn2;
+      }
     }
+    if (!good && lane == 0) fail();
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
 }
 
-// Joins the pieces of the tiles that range boundaries cut: CTA (c, y) takes rows
-// kJoinRows y .. of the tile that boundary c + 1 is the first to cut, a warp a row,
-// four dims a lane. Piece x > 0 is in slot 2 (cta of piece 0 + x).
+// Joins the pieces of the tiles that ranges cut: CTA (k, y) takes rows kJoinRows y ..
+// of the tile that the start of range k + 1 is the first to cut, a warp a row, four dims
+// a lane. Piece x > 0 is in slot 2 (range of piece 0 + x).
 constexpr int kJoinWarps = 4;
 constexpr int kJoinRows = 8;
 constexpr int kJoinLoads = 8;  // pieces whose outputs are in flight
@@ -760,7 +931,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Chunk
       float f = 0.f;
       if (base + lane < cut.pieces) {
         const float4 ml = p.ws_ml[at(base + lane)];
-        // a piece that the row sees nothing of has a sum of 0 and an output of zeros
         f = fast_exp2(ml.x - M);
         l = fmaf(ml.y, f, l);
         lr = fmaf(ml.z, f, lr);
@@ -770,8 +940,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Chunk
         float4 o[kJoinLoads];
 #pragma unroll
         for (int x = 0; x < kJoinLoads; ++x)
-          o[x] = x0 + x < n ? reinterpret_cast<const float4 *>(p.ws_o + at(base + x0 + x) * kD)[lane]
-                            : make_float4(0.f, 0.f, 0.f, 0.f);
+          // of a piece without weight nothing is read: it may not have written its output
+          o[x] = __shfl_sync(0xffffffffu, f, (x0 + x) & 31) != 0.f && x0 + x < n
+                     ? reinterpret_cast<const float4 *>(p.ws_o + at(base + x0 + x) * kD)[lane]
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int x = 0; x < kJoinLoads; ++x) {
           const float fx = __shfl_sync(0xffffffffu, f, (x0 + x) & 31);
@@ -828,26 +1000,23 @@ cudaError_t launch_chunk(const ChunkArgs &a, const CUtensorMap &q_map, const CUt
   p.num_blocks = a.num_blocks;
   p.gqa_log2 = log2_of(a.num_q_heads / a.num_kv_heads);
   const int tokens = kRows >> p.gqa_log2;
-  const int tiles = (a.max_seqlen_q - 1) / tokens + 1;  // row tiles of the longest segment
+  const int tiles = (a.max_seqlen_q - 1) / tokens + 1;  // of the longest segment
   p.lanes_log2 = tiles >= 32 ? 5 : log2_of(tiles);
+  p.shared_keys = tiles > 1;
   p.window = a.window;
   p.sinks = a.sinks;
   p.box_rows = prefill_box_rows(a.block_size);
-  p.flip = a.scale_log2 < 0.f ? 1u : 0u;
   // a factor of zero would make NaN of masked logits: the smallest normal number
   // gives the same weights to any logits below 10^30
-  p.scale_log2 = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
-  // the limit is the kernel's, not the call's: another host thread may be between its
-  // own two calls here, so it is always set to the most that any call wants
-  cudaError_t e = cudaFuncSetAttribute(chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_bytes(kChunkMaxSeqs));
+  p.scale_log2 = a.scale_log2 == 0.f ? 1.17549435e-38f : a.scale_log2;
+  const auto kernel = a.window > 0 ? chunk_kernel<true> : chunk_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(chunk_kernel, dim3(a.num_sms), dim3(kThreads), smem_bytes(a.num_seqs), stream, q_map, k_map, v_map, p);
-  if (e != cudaSuccess || a.num_sms < 2) return e;
+  e = launch_pdl(kernel, dim3(a.num_ctas), dim3(kThreads), kSmemBytes, stream, q_map, k_map, v_map, p);
   // tiles of one step have no boundary inside
-  if (tiles == 1 && a.max_context_len <= kKeys) return cudaSuccess;
+  if (e != cudaSuccess || a.num_ctas < 2 || (tiles == 1 && a.max_context_len <= kKeys)) return e;
   const int rows = static_cast<int>(std::min<int64_t>(kRows, static_cast<int64_t>(a.max_seqlen_q) << p.gqa_log2));
-  return launch_pdl(chunk_join_kernel, dim3(a.num_sms - 1, (rows + kJoinRows - 1) / kJoinRows),
+  return launch_pdl(chunk_join_kernel, dim3(a.num_ctas - 1, (rows + kJoinRows - 1) / kJoinRows),
                     dim3(kJoinWarps * 32), 0, stream, p);
 }
 

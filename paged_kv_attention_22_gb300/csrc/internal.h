@@ -276,7 +276,8 @@ cudaError_t launch_heads(const HeadsArgs &a, cudaStream_t stream);
 cudaError_t heads_error_word(uint32_t **word);
 
 // ---------------------------------------------------------------- chunks
-constexpr int kChunkMaxSeqs = 1024;  // sequences per call (their prefix lives in shared memory)
+constexpr int kChunkMaxSeqs = 1024;  // sequences per call (their list fits in shared memory)
+constexpr int kChunkMaxCtas = 384;    // one per SM, as many as share out the work in one block's threads
 // A tile of 128 query rows whose keys are cut between CTAs, as the joining kernel reads it.
 struct ChunkCut {
   int32_t pieces;  // 0: none
@@ -287,12 +288,12 @@ struct ChunkArgs {
   const int32_t *cu_seqlens_q, *context_lens, *block_tables;
   void *out;
   float *lse;
-  float *ws_o, *ws_ml;  // [2 num_sms, 128, 128], [2 num_sms, 128, 4]
-  ChunkCut *cuts;       // [num_sms]
+  float *ws_o, *ws_ml;  // [2 num_ctas, 128, 128], [2 num_ctas, 128, 4]
+  ChunkCut *cuts;       // [num_ctas]
   int32_t max_blocks, num_seqs, total_q, max_seqlen_q, max_context_len;
   int32_t num_q_heads, num_kv_heads, block_size, num_blocks;
   int32_t window, sinks;  // sinks: 0 without a window
-  int32_t num_sms;
+  int32_t num_ctas;
   float scale_log2;
 };
 cudaError_t launch_chunk(const ChunkArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
