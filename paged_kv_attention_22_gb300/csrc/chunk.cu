@@ -89,8 +89,8 @@ constexpr int kEpiOff = kVOff + 2 * kTileBytes;  // staging areas of the softmax
 constexpr int kBarOff = kEpiOff + 8 * kEpiWarpBytes;
 constexpr int kDescOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
 constexpr int kMiscOff = kDescOff + kDescs * kDescInts * 4;  // TMEM address, abort flag, unseen rows of the V tiles
-constexpr int kSwapOff = kMiscOff + 16;                      // float [4][2][128]: maxima of two steps, two sums, by half
-constexpr int kWaveOff = kSwapOff + 4 * 2 * kRows * 4;       // Wave [kMaxWaves]
+constexpr int kSwapOff = kMiscOff + 16;                      // float [6][2][128] by half: maxima of two steps, two sums of two pieces
+constexpr int kWaveOff = kSwapOff + 6 * 2 * kRows * 4;       // Wave [kMaxWaves]
 constexpr int kSmemBytes = kWaveOff + kMaxWaves * static_cast<int>(sizeof(Wave)) + 1024;  // + slack for alignment
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 // until the first copies, in the place of the V tiles: the list of sequences
@@ -250,35 +250,39 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
   r.waves = r.front = 0;
   r.even = r.W == 0 ? 0 : quotient(U + r.W - 1, r.W);
   if (r.W == 0 || !p.shared_keys) return r;
-  // tile i of the list
-  auto locate = [&](int64_t i) {
+  // Tile i of the list (the rows of q are fewer than 2^31, so are the tiles), found from
+  // a sequence at or before it.
+  const int n_tiles = static_cast<int>(tiles[p.num_seqs]);
+  auto locate = [&](int i, int from) {
     Wave w;
-    w.s = find(tiles, p.num_seqs, i);  // it has tiles
+    w.s = from;
+    while (tiles[w.s + 1] <= i) ++w.s;  // the last has tiles[] = n_tiles
     w.q = seqs[w.s];
-    const int64_t at = i - tiles[w.s];
-    const int n = tiles_of(p, w.q);
-    w.head = static_cast<int>(quotient(at, n));
-    w.tile = static_cast<int>(at - static_cast<int64_t>(w.head) * n);
+    const uint32_t at = i - static_cast<int>(tiles[w.s]), n = tiles_of(p, w.q);
+    w.head = at / n;
+    w.tile = at - w.head * n;
     return w;
   };
   // Whole tiles as far as no CTA gets more than its even share, and one more each is left
   // to even out with.
   int64_t mine = 0;  // thread c: steps of CTA c's whole tiles
-  for (r.waves = static_cast<int>(min(quotient(tiles[p.num_seqs], r.W) - 1, static_cast<int64_t>(kMaxWaves)));
-       r.waves > 0; r.waves >>= 1) {
+  for (r.waves = min(n_tiles / r.W - 1, kMaxWaves); r.waves > 0; r.waves >>= 1) {
     mine = 0;
-    if (tid < r.W)
+    if (tid < r.W) {
+      int at = find(tiles, p.num_seqs, tid);
       for (int w = 0; w < r.waves; ++w) {
-        const Wave x = locate(tid + static_cast<int64_t>(w) * r.W);
+        const Wave x = locate(tid + w * r.W, at);
+        at = x.s;
         mine += tile_of<kWindowed>(p, x.q, x.tile).steps();
       }
+    }
     if (!__syncthreads_or(mine > r.even)) break;
   }
   if (r.waves <= 0) {
     r.waves = 0;
     return r;
   }
-  if (tid < r.waves) list[tid] = locate(cta + static_cast<int64_t>(tid) * r.W);
+  if (tid < r.waves) list[tid] = locate(cta + tid * r.W, find(tiles, p.num_seqs, cta + tid * r.W));
   if (tid < r.W) starts[tid + 1] = r.even - mine;  // what CTA c may still take
   __syncthreads();
   if (warp == 0) {
@@ -471,21 +475,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       fence_proxy_async_smem();  // the copies overwrite the list
     }
-    // The next piece into d, published; false if a wait gave up.
-    int n_pieces = 0, lo = 0, ctx = 0;
+    struct Work {  // a piece, as its copies need it
+      Piece d;
+      const int32_t *table;  // of its sequence
+      int lo, ctx;           // the first key of its window, the sequence's keys
+    };
+    int n_pieces = 0;
     bool in_range = false;  // a piece of the range has been published
-    const int32_t *table = nullptr;  // of d's sequence
-    Piece d;
-    auto next_piece = [&]() -> bool {
+    // The next piece into x, published; false if a wait gave up.
+    auto next_piece = [&](Work &x) -> bool {
       const int slot = n_pieces % kDescs;
+      Piece &d = x.d;
       d.steps = 0;
       const bool wave = n_pieces < shares.waves;
       if (wave || left > 0) {
-        Seq x;
+        Seq sq;
         int at, xs, from = 0;
         if (wave) {
           const Wave w = waves[n_pieces];
-          x = w.q, at = w.tile, xs = w.s, d.head = w.head;
+          sq = w.q, at = w.tile, xs = w.s, d.head = w.head;
         } else {
           if (in_range && ++i == n_tiles) {
             i = 0;
@@ -497,21 +505,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!in_range) from = first;
-          x = q, at = i, xs = s, d.head = head;
+          sq = q, at = i, xs = s, d.head = head;
         }
-        const Tile t = tile_of<kWindowed>(p, x, at);
+        const Tile t = tile_of<kWindowed>(p, sq, at);
         const int all = t.steps();
         d.steps = wave ? all : min(all - from, left);
         d.first = from;
         d.lead = t.lead;
         d.j_start = t.j_start;
-        d.pos = x.ctx - x.Lq + t.t0;
-        d.row = x.q0 + t.t0;
+        d.pos = sq.ctx - sq.Lq + t.t0;
+        d.row = sq.q0 + t.t0;
         d.n_tok = t.n_tok;
         d.slot = d.steps == all ? -1 : 2 * rank + (in_range ? 1 : 0);
-        table = p.block_tables + static_cast<int64_t>(xs) * p.max_blocks;
-        lo = t.lo;
-        ctx = x.ctx;
+        x.table = p.block_tables + static_cast<int64_t>(xs) * p.max_blocks;
+        x.lo = t.lo;
+        x.ctx = sq.ctx;
         if (!wave) {
           left -= d.steps;
           in_range = true;
@@ -532,14 +540,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // box's table entry a step ahead and issues the box's copies; lane 0 arms the
     // barriers. Boxes that no row of the tile sees are left out.
     const int box_rows = p.box_rows;
-    auto key_of = [&](int j) { return d.key_tile(j) * kKeys + lane * box_rows; };
-    auto wanted = [&](int j) {
-      const int k = key_of(j);
-      return lane * box_rows < kKeys && k < ctx && (!kWindowed || k + box_rows > lo || k < p.sinks);
+    auto key_of = [&](const Work &x, int j) { return x.d.key_tile(j) * kKeys + lane * box_rows; };
+    auto wanted = [&](const Work &x, int j) {
+      const int k = key_of(x, j);
+      return lane * box_rows < kKeys && k < x.ctx && (!kWindowed || k + box_rows > x.lo || k < p.sinks);
     };
-    auto entry = [&](int j) { return wanted(j) ? __ldg(table + fast_quotient(key_of(j), p.block)) : -1; };
-    bool good = next_piece();
-    int32_t blk = d.steps > 0 ? entry(0) : -1;
+    auto entry = [&](const Work &x, int j) {
+      return wanted(x, j) ? __ldg(x.table + fast_quotient(key_of(x, j), p.block)) : -1;
+    };
+    Work cur = {}, next = {};
+    bool good = next_piece(cur);
+    int32_t blk = cur.d.steps > 0 ? entry(cur, 0) : -1;
     int g = 0;  // steps so far
     // V goes out a step behind K: the next K is wanted first, and its stage is free first
     int32_t v_row = -1;
@@ -561,38 +572,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    while (good && d.steps > 0) {
-      const int steps = d.steps, kv_head = d.head, piece = n_pieces - 1, qb = piece & 1;
+    for (int piece = 0; good && cur.d.steps > 0; ++piece) {
+      const int steps = cur.d.steps, kv_head = cur.d.head, qb = piece & 1;
       if (piece >= 2 && !(good = wait_all(kBarQFree + qb, ((piece >> 1) - 1) & 1))) break;
       if (lane == 0) {
         const uint32_t dst = sbase + kQOff + qb * kTileBytes;
         mbar_arrive_expect_tx(bar(kBarQ + qb), kTileBytes);
-        tma_load_3d(dst, &q_map, bar(kBarQ + qb), 0, kv_head << p.gqa_log2, d.row);
-        tma_load_3d(dst + kHalfBytes, &q_map, bar(kBarQ + qb), 64, kv_head << p.gqa_log2, d.row);
+        tma_load_3d(dst, &q_map, bar(kBarQ + qb), 0, kv_head << p.gqa_log2, cur.d.row);
+        tma_load_3d(dst + kHalfBytes, &q_map, bar(kBarQ + qb), 64, kv_head << p.gqa_log2, cur.d.row);
       }
       __syncwarp();
       for (int j = 0; good && j < steps; ++j, ++g) {
-        const int k0 = d.key_tile(j) * kKeys;
+        const int k0 = cur.d.key_tile(j) * kKeys;
         // V rows that no row of the tile sees: from .. to - 1 and end ..
         const uint32_t from = static_cast<uint32_t>(min(max(p.sinks - k0, 0), kKeys));
-        const uint32_t to = static_cast<uint32_t>(min(max(lo - k0, 0), kKeys));
-        const uint32_t end = static_cast<uint32_t>(min(ctx - k0, kKeys));
+        const uint32_t to = static_cast<uint32_t>(min(max(cur.lo - k0, 0), kKeys));
+        const uint32_t end = static_cast<uint32_t>(min(cur.ctx - k0, kKeys));
         int32_t row = -1;  // cache row of this lane's box
-        if (wanted(j)) {
+        if (wanted(cur, j)) {
           if (blk >= 0 && blk < p.num_blocks) {
-            const uint32_t key = key_of(j);
+            const uint32_t key = key_of(cur, j);
             row = blk * static_cast<int32_t>(p.block.d) + (key - fast_quotient(key, p.block) * p.block.d);
           } else {
             atomicOr(&g_chunk_errors, kErrBlock);
           }
         }
         // the entry of the next step, which may be the next piece's first
-        if (j + 1 < steps) {
-          blk = entry(j + 1);
-        } else {
-          good = next_piece();
-          blk = d.steps > 0 ? entry(0) : -1;
-        }
+        if (j + 1 < steps)
+          blk = entry(cur, j + 1);
+        else if (j > 0)
+          blk = next.d.steps > 0 ? entry(next, 0) : -1;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, row >= 0)) * 2u * box_rows * 128u;
         const int b = g & 1;
         // S of step g - 2 has been the last to read this K tile
@@ -605,12 +614,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(at, &k_map, bar(kBarK + b), 0, kv_head, row);
           tma_load_3d(at + kHalfBytes, &k_map, bar(kBarK + b), 64, kv_head, row);
         }
+        if (j == 0) {  // the next piece is known before the other warps are done with this one
+          if (!(good = next_piece(next))) break;
+          if (steps == 1) blk = next.d.steps > 0 ? entry(next, 0) : -1;
+        }
         if (g >= 1 && !(good = load_v(g - 1))) break;
         v_row = row;
         v_bytes = bytes;
         v_head = kv_head;
         v_unseen = (from < to ? from | to << 8 : 0) | end << 16;
       }
+      cur = next;
     }
     if (good && g >= 1) good = load_v(g - 1);
     if (!good) {
@@ -722,142 +736,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t tO = tmem + kTmemO + half * 64 + lane_off;
     const uint32_t scr = sbase + kEpiOff + (warp - kSoftmaxWarp0) * kEpiWarpBytes;
-    // [2 steps][2 halves][128]: maxima; then [2 sums][2 halves][128]
-    volatile float *swap = reinterpret_cast<volatile float *>(smem + kSwapOff);
+    // by half: maxima of two steps, then two sums of two pieces
+    volatile float *swap = reinterpret_cast<volatile float *>(smem + kSwapOff) + r;
     const uint32_t masked = p.scale_log2 < 0.f ? 0x7F800000u : 0xFF800000u;  // times the scale: -inf
     bool good = true;
     int g = 0;
     uint32_t x_par = 0;  // parity of the next exchange
-    // Both warps of the quadrant have come here, and see what the other wrote before.
-    auto meet = [&]() -> bool {
+    // Both warps of the quadrant have come to offer(), and see what the other wrote before.
+    auto offer = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarX + quad));
+    };
+    auto meet = [&]() -> bool {
       const bool ok = __all_sync(0xffffffffu, wait_(bar(kBarX + quad), x_par, abort));
       x_par ^= 1;
       return ok;
     };
-    for (int n = 0;; ++n) {
-      Piece d;
-      if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarDesc + n % kDescs), (n / kDescs) & 1, abort)))) break;
-      read_piece<kPieceInts>(n, smem, bars, lane, d);
-      if (d.steps == 0) break;
-      const bool live = tok < d.n_tok;
-      const bool any = tok0 < d.n_tok;  // some row of the warp is
-      const int lim = d.pos + tok;      // last key this row sees
-      float m = kFloor, l = 0.f, lr = 0.f;
-#pragma unroll 1
-      for (int j = 0; j < d.steps; ++j, ++g) {
-        const int b = g & 1;
-        if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarS + b), (g >> 1) & 1, abort)))) break;
-        if (any) {
-          tc_fence_after();
-          const uint32_t tS = tmem + b * kKeys + lane_off;
-          const int k0 = d.key_tile(j) * kKeys;
-          // whether some key of the step is masked for some row of the warp
-          bool some = k0 + kKeys - 1 > d.pos + tok0;
-          if constexpr (kWindowed)  // the largest first key of the warp's rows
-            some = some || (k0 <= d.pos + tok0 + (31 >> p.gqa_log2) - p.window && k0 + kKeys > p.sinks);
-          const int keep = lim - k0;  // columns up to it are at or before the row's position
-          // 32 columns of S, masked logits as -inf once scaled. Columns that every row of the
-          // warp sees are left alone.
-          auto columns = [&](int c, uint32_t (&x)[32]) {
-            tmem_ld32(tS + c, x);
-            tmem_wait_ld();
-            if (!some) return;
-            auto below = [](int i) { return i <= 0 ? 0u : i >= 32 ? 0xffffffffu : (1u << i) - 1; };
-            uint32_t seen = below(keep + 1 - c);  // as bits
-            if constexpr (kWindowed)              // but for those between the sinks and the window
-              seen &= ~below(keep - p.window + 1 - c) | below(p.sinks - k0 - c);
-            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) return;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!(seen >> i & 1)) x[i] = masked;
-          };
-          // First pass: the maximum of the thread's columns, then of the row's. The running one
-          // moves only where it is exceeded by more than 2^8: the warps then rescale O. A
-          // piece's first step always does. Neither pass is unrolled over the columns: their
-          // code then stays in the instruction cache beside the MMA warp's (as one piece of
-          // code over 128 values in registers a step took 2,200 to 3,000 cycles).
-          float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c = half * 64; c < half * 64 + 64; c += 32) {
-            uint32_t x[32];
-            columns(c, x);
-            if (p.scale_log2 < 0.f) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] ^= 0x80000000u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              a[(i >> 1) & 3] = fmax3(a[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          }
-          // (two steps' worth of places: a warp may be a step ahead of the other's reading)
-          float mx = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * fabsf(p.scale_log2);  // -inf stays -inf
-          swap[(b * 2 + half) * kRows + r] = mx;
-          if (!(good = meet())) break;
-          mx = fmaxf(mx, swap[(b * 2 + 1 - half) * kRows + r]);
-          if (__any_sync(0xffffffffu, live && !(mx <= m + kLazyMax))) {
-            const float m_new = fmaxf(m, mx);
-            if (j > 0) {
-              // O holds every step up to j - 1 once that P.V is complete
-              if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarO + (b ^ 1)), ((g - 1) >> 1) & 1, abort)))) break;
-              tc_fence_after();
-              const float alpha = fast_exp2(m - m_new);
-#pragma unroll 1
-              for (int c = 0; c < 64; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(tO + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                tmem_st32(tO + c, o);
-              }
-              l *= alpha;
-              lr *= alpha;
-            }
-            m = m_new;
-          }
-          // Second pass: P = 2^(x * scale - m), packed two per column over the first columns
-          // of the thread's own half, whose logits have been read, and the sums of the fp32
-          // and of the rounded values, over eight chains each.
-          float s8[8] = {}, r8[8] = {};
-#pragma unroll 1
-          for (int c = half * 64; c < half * 64 + 64; c += 32) {
-            uint32_t x[32], pk[16];
-            columns(c, x);
-            float e[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) e[i] = fast_exp2(fmaf(__uint_as_float(x[i]), p.scale_log2, -m));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
-            tmem_st16(tS + half * 32 + c / 2, pk);  // over columns of this half
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s8[i & 7] += e[i];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) add_bf16x2_to_f32(r8[2 * (i & 3)], r8[2 * (i & 3) + 1], pk[i]);
-          }
-          l += ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
-          lr += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + b));
-      }
-      if (!good) break;
-      if (!any) continue;
-      // The piece's last P.V; the next one's first, which overwrites O, waits for this
-      // warp's next P. The halves' sums are added up, then each warp has half of O's columns.
-      if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarO + ((g - 1) & 1)), ((g - 1) >> 1) & 1, abort)))) break;
+    Piece d;
+    bool live = false;
+    int lim = 0;  // last key this row sees
+    uint32_t x[64];  // the thread's logits of the step
+    // Reads those of the piece's step j, step h of the CTA, masked as -inf once scaled, and
+    // offers their maximum to the other half's warp. Blocks of 32 columns that every row of
+    // the warp sees are left alone.
+    auto logits = [&](int j, int h) -> bool {
+      const int b = h & 1;
+      if (!__all_sync(0xffffffffu, wait_(bar(kBarS + b), (h >> 1) & 1, abort))) return false;
       tc_fence_after();
-      swap[(4 + half) * kRows + r] = l;
-      swap[(6 + half) * kRows + r] = lr;
-      if (!(good = meet())) break;
-      l += swap[(5 - half) * kRows + r];
-      lr += swap[(7 - half) * kRows + r];
-      const int n_valid = min(32, (d.n_tok - tok0) << p.gqa_log2);
-      const float inv = d.slot < 0 ? 1.f / lr : 1.f;
-      const int64_t row0 = static_cast<int64_t>(d.row + tok0) * p.num_q_heads + (static_cast<int64_t>(d.head) << p.gqa_log2);
+      const uint32_t tS = tmem + b * kKeys + half * 64 + lane_off;
+      tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(x[0]));
+      tmem_ld32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
+      const int k0 = d.key_tile(j) * kKeys + half * 64;  // the thread's first key
+      bool some = k0 + 63 > d.pos + tok0;
+      if constexpr (kWindowed)  // the largest first key of the warp's rows
+        some = some || (k0 <= d.pos + tok0 + (31 >> p.gqa_log2) - p.window && k0 + 64 > p.sinks);
+      tmem_wait_ld();
+      if (some) {
+        const int keep = lim - k0;  // columns up to it are at or before the row's position
+        auto below = [](int i) { return i <= 0 ? 0u : i >= 32 ? 0xffffffffu : (1u << i) - 1; };
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t seen = below(keep + 1 - c);  // as bits
+          if constexpr (kWindowed)              // but for those between the sinks and the window
+            seen &= ~below(keep - p.window + 1 - c) | below(p.sinks - k0 - c);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(seen >> i & 1)) x[c + i] = masked;
+        }
+      }
+      float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      if (p.scale_log2 >= 0.f) {
+#pragma unroll
+        for (int i = 0; i < 64; i += 2)
+          a[(i >> 1) & 3] = fmax3(a[(i >> 1) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) a[i & 3] = fmaxf(a[i & 3], -__uint_as_float(x[i]));
+      }
+      // -inf stays -inf; two steps' worth of places: a warp may be a step ahead of the
+      // other's reading
+      swap[(b * 2 + half) * kRows] =
+          fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * fabsf(p.scale_log2);
+      offer();
+      return true;
+    };
+    // A piece whose output is still to be written. That is done when the next piece's first
+    // logits have been read: its last P.V runs meanwhile, and one exchange serves both.
+    struct Ended {
+      int slot, row, n_tok, head;
+      float m, l, lr;
+    } e = {};
+    bool ended = false;
+    auto finish = [&](int n) -> bool {  // e is piece n, its last step g - 1
+      // The next P.V, which overwrites O, waits for this warp's next P.
+      const int b = (g - 1) & 1;
+      if (!__all_sync(0xffffffffu, wait_(bar(kBarO + b), ((g - 1) >> 1) & 1, abort))) return false;
+      tc_fence_after();
+      const volatile float *sums = swap + (4 + (n & 1) * 4 + 1 - half) * kRows;
+      const float l = e.l + sums[0], lr = e.lr + sums[2 * kRows];
+      const int n_valid = min(32, (e.n_tok - tok0) << p.gqa_log2);
+      const float inv = e.slot < 0 ? 1.f / lr : 1.f;
+      const int64_t row0 = static_cast<int64_t>(e.row + tok0) * p.num_q_heads + (static_cast<int64_t>(e.head) << p.gqa_log2);
 #pragma unroll 1
       for (int c = 0; c < 64; c += 32) {
         uint32_t o[32];
@@ -866,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
         const int col = half * 64 + c;
-        if (d.slot < 0) {
+        if (e.slot < 0) {
           uint32_t y[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
@@ -876,18 +835,111 @@ __global__ void __launch_bounds__(kThreads, 1)
             return reinterpret_cast<uint8_t *>(p.out + at * kD + col);
           });
         } else {
-          float *dst = p.ws_o + (static_cast<int64_t>(d.slot) * kRows + quad * 32) * kD + col;
+          float *dst = p.ws_o + (static_cast<int64_t>(e.slot) * kRows + quad * 32) * kD + col;
           store_rows(o, scr, n_valid, lane, [&](int i) { return reinterpret_cast<uint8_t *>(dst + i * kD); });
           store_rows(o + 16, scr, n_valid, lane, [&](int i) { return reinterpret_cast<uint8_t *>(dst + i * kD + 16); });
         }
       }
-      if (live && half == 0) {
-        if (d.slot >= 0)
-          p.ws_ml[static_cast<int64_t>(d.slot) * kRows + r] = make_float4(m, l, lr, 0.f);
+      if (tok < e.n_tok && half == 0) {
+        if (e.slot >= 0)
+          p.ws_ml[static_cast<int64_t>(e.slot) * kRows + r] = make_float4(e.m, l, lr, 0.f);
         else if (p.lse != nullptr)
           p.lse[row0 + static_cast<int64_t>(lane >> p.gqa_log2) * p.num_q_heads + (lane & ((1 << p.gqa_log2) - 1))] =
-              (m + log2f(l)) * kLn2;
+              (e.m + log2f(l)) * kLn2;
       }
+      return true;
+    };
+#pragma unroll 1
+    for (int n = 0;; ++n) {
+      if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarDesc + n % kDescs), (n / kDescs) & 1, abort)))) break;
+      read_piece<kPieceInts>(n, smem, bars, lane, d);
+      const bool any = d.steps > 0 && tok0 < d.n_tok;  // some row of the warp is live
+      live = tok < d.n_tok;
+      lim = d.pos + tok;
+      if (any) {
+        if (!(good = logits(0, g))) break;
+      } else if (ended) {
+        offer();
+      }
+      if ((any || ended) && !(good = meet())) break;
+      if (ended && !(good = finish(n - 1))) break;
+      ended = any;
+      if (d.steps == 0) break;
+      if (!any) {
+        for (int j = 0; j < d.steps && good; ++j, ++g) {
+          good = __all_sync(0xffffffffu, wait_(bar(kBarS + (g & 1)), (g >> 1) & 1, abort));
+          if (lane == 0) mbar_arrive(bar(kBarP + (g & 1)));
+        }
+        if (!good) break;
+        continue;
+      }
+      float m = kFloor, l = 0.f, lr = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < d.steps; ++j, ++g) {
+        const int b = g & 1;
+        // The running maximum moves only where it is exceeded by more than 2^8: the
+        // warps then rescale O. A piece's first step always does.
+        const float mx = fmaxf(swap[b * 2 * kRows], swap[(b * 2 + 1) * kRows]);
+        if (__any_sync(0xffffffffu, live && !(mx <= m + kLazyMax))) {
+          const float m_new = fmaxf(m, mx);
+          if (j > 0) {
+            // O holds every step up to j - 1 once that P.V is complete
+            if (!(good = __all_sync(0xffffffffu, wait_(bar(kBarO + (b ^ 1)), ((g - 1) >> 1) & 1, abort)))) break;
+            tc_fence_after();
+            const float alpha = fast_exp2(m - m_new);
+#pragma unroll 1
+            for (int c = 0; c < 64; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(tO + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st16(tO + c, o);
+            }
+            l *= alpha;
+            lr *= alpha;
+          }
+          m = m_new;
+        }
+        // P = 2^(x * scale - m), packed two per column over the first columns of the
+        // thread's own half, and the sum of the fp32 values over eight chains.
+        uint32_t pk[32];
+        {
+          const uint32_t tP = tmem + b * kKeys + half * 64 + lane_off;
+          float s8[8] = {};
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            float e[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) e[i] = fast_exp2(fmaf(__uint_as_float(x[c + i]), p.scale_log2, -m));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[c / 2 + i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
+            tmem_st16(tP + c / 2, reinterpret_cast<uint32_t(&)[16]>(pk[c / 2]));
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s8[i & 7] += e[i];
+          }
+          l += ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + b));
+        const bool more = j + 1 < d.steps;
+        if (more && !(good = logits(j + 1, g + 1))) break;
+        // the sum of the rounded values, while the other half's maximum is on its way
+        {
+          float r8[8] = {};
+#pragma unroll
+          for (int i = 0; i < 32; ++i) add_bf16x2_to_f32(r8[2 * (i & 3)], r8[2 * (i & 3) + 1], pk[i]);
+          lr += ((r8[0] + r8[1]) + (r8[2] + r8[3])) + ((r8[4] + r8[5]) + (r8[6] + r8[7]));
+        }
+        if (more && !(good = meet())) break;
+      }
+      if (!good) break;
+      // (in the other piece's places the other warp may still be reading)
+      swap[(4 + (n & 1) * 4 + half) * kRows] = l;
+      swap[(6 + (n & 1) * 4 + half) * kRows] = lr;
+      e = {d.slot, d.row, d.n_tok, d.head, m, l, lr};
     }
     if (!good && lane == 0) fail();
   }
