@@ -714,7 +714,47 @@ pkv_status pkv_paged_chunk_attn(const void *q, const void *k_cache, const void *
   CUtensorMap qmap, kmap, vmap;
   const int64_t rows = num_blocks * block_size;
   const uint32_t G = static_cast<uint32_t>(num_q_heads / num_kv_heads);
-  const uint32_t box = static_cast<uint32_t>(pkv::prefill_box_rows(block_size));
+  const int32_t box_rows = pkv::prefill_box_rows(block_size);
+  const uint32_t box = static_cast<uint32_t>(box_rows);
+  // Long chunks that see every key before them are prefill's work: two row tiles pass each K/V
+  // tile there, where a CTA here has one, at the price of whole items per CTA. So they go there
+  // where each sequence alone has items for half of the SMs, however unequal their contexts
+  // are, and segments are about as long as the longest. Four of 2,048 tokens over 8,192 to 10,240
+  // keys take 450 us there and 536 here, 64 of 32 tokens over 736 keys 54 there and 45 here, two of
+  // 16 over 32,768 keys 362 there and 55 here.
+  const int64_t tiles = (static_cast<int64_t>(max_seqlen_q) + 127) / 128 * num_q_heads / 2;  // two an item
+  if (a.window == 0 && scale > 0.f && 2 * tiles >= sms && tiles * num_seqs <= pkv::kMaxPrefillItems &&
+      4 * static_cast<int64_t>(total_q) >= 3 * static_cast<int64_t>(num_seqs) * max_seqlen_q) {
+    pkv::PrefillArgs f;
+    f.cu_seqlens_q = cu_seqlens_q;
+    f.cu_seqlens_k = nullptr;
+    f.context_lens = context_lens;
+    f.block_tables = block_tables;
+    f.out = out;
+    f.lse = lse;
+    f.max_blocks = max_blocks_per_seq;
+    f.num_seqs = num_seqs;
+    f.total_q = total_q;
+    f.max_seqlen_q = max_seqlen_q;
+    f.max_seqlen_k = max_context_len;
+    f.total_k = -1;
+    f.num_q_heads = num_q_heads;
+    f.num_kv_heads = num_kv_heads;
+    f.head_dim = head_dim;
+    f.block_size = block_size;
+    f.num_blocks = static_cast<int32_t>(num_blocks);
+    f.window = 0;
+    f.box_rows = box_rows;
+    f.num_sms = sms;
+    f.scale_log2 = a.scale_log2;
+    if ((st = encode_rows_map(&qmap, q, total_q, num_q_heads, head_dim, 64, 1, 128, true)) != PKV_OK ||
+        (st = encode_rows_map(&kmap, k_cache, rows, num_kv_heads, head_dim, 64, 1, box, true)) != PKV_OK ||
+        (st = encode_rows_map(&vmap, v_cache, rows, num_kv_heads, head_dim, 64, 1, box, true)) != PKV_OK)
+      return st;
+    const cudaError_t e = pkv::launch_prefill(f, qmap, kmap, vmap, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+    return PKV_OK;
+  }
   if ((st = encode_rows_map(&qmap, q, total_q, num_q_heads, head_dim, 64, G, 128 / G, true)) != PKV_OK ||
       (st = encode_rows_map(&kmap, k_cache, rows, num_kv_heads, head_dim, 64, 1, box, true)) != PKV_OK ||
       (st = encode_rows_map(&vmap, v_cache, rows, num_kv_heads, head_dim, 64, 1, box, true)) != PKV_OK)

@@ -417,64 +417,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Wave *waves = reinterpret_cast<const Wave *>(smem + kWaveOff);
     volatile int *descs = reinterpret_cast<volatile int *>(smem + kDescOff);
     // the range: where it starts (s, head, i, first) and its length
-    int s = 0, head = 0, i = 0, n_tiles = 0, first = 0, rank, left;
+    const int64_t *starts = reinterpret_cast<const int64_t *>(smem + kShareOff);
+    auto start = [&](int c) { return shares.front ? starts[c] : min(c * shares.even, shares.U); };
+    auto rank_of = [&](int c) { return shares.front ? ranks[c] : c; };
+    const int64_t u_lo = start(cta);
+    const int rank = rank_of(cta);
+    int left = static_cast<int>(start(cta + 1) - u_lo);  // steps that no piece has yet
+    int s = 0, head = 0, i = 0, n_tiles = 0, first = 0;
     Seq q = {0, 0, 0};
-    {
-      const int64_t *starts = reinterpret_cast<const int64_t *>(smem + kShareOff);
-      auto start = [&](int c) { return shares.front ? starts[c] : min(c * shares.even, shares.U); };
+    if (left > 0) {
+      const int64_t *steps = reinterpret_cast<const int64_t *>(smem + kStepsOff);
+      s = find(steps, p.num_seqs, u_lo);  // it has steps
+      q = reinterpret_cast<const Seq *>(smem + kSeqOff)[s];
+      n_tiles = tiles_of(p, q);
+      int64_t skip = u_lo - steps[s];
+      const int64_t per_head = quotient(steps[s + 1] - steps[s], p.num_kv_heads);
+      head = static_cast<int>(quotient(skip, per_head));
+      skip -= head * per_head;
+      for (i = 0; n_tiles > 1; i += 32) {  // the tile that holds step `skip` of the head: 32 at a time
+        const int n = i + lane < n_tiles ? tile_of<kWindowed>(p, q, i + lane).steps() : 0;
+        int incl = n;  // 32 tiles have fewer than 2^31 steps
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += x;
+        }
+        const uint32_t beyond = __ballot_sync(0xffffffffu, incl > skip);
+        if (beyond != 0 || i + 32 >= n_tiles) {  // the step lies within the head: some lane is beyond it
+          const int at = max(__ffs(beyond) - 1, 0);
+          skip -= __shfl_sync(0xffffffffu, incl - n, at);
+          i += at;
+          break;
+        }
+        skip -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+      first = static_cast<int>(skip);
+    }
+    // The tile that the range's start cuts, if no range before does, for the joining kernel.
+    auto record_cut = [&](const Seq &sq, int at, int kv_head, int from) {
       auto owner = [&](int64_t u) {
         return shares.front ? find(starts, shares.W, u) : static_cast<int>(quotient(u, shares.even));
       };
-      auto rank_of = [&](int c) { return shares.front ? ranks[c] : c; };
-      const int64_t u_lo = start(cta);
-      rank = rank_of(cta);
-      left = static_cast<int>(start(cta + 1) - u_lo);  // steps that no piece has yet
-      if (left > 0) {
-        const int64_t *steps = reinterpret_cast<const int64_t *>(smem + kStepsOff);
-        s = find(steps, p.num_seqs, u_lo);  // it has steps
-        q = reinterpret_cast<const Seq *>(smem + kSeqOff)[s];
-        n_tiles = tiles_of(p, q);
-        int64_t skip = u_lo - steps[s];
-        const int64_t per_head = quotient(steps[s + 1] - steps[s], p.num_kv_heads);
-        head = static_cast<int>(quotient(skip, per_head));
-        skip -= head * per_head;
-        for (i = 0;; i += 32) {  // the tile that holds step `skip` of the head: 32 at a time
-          const int n = i + lane < n_tiles ? tile_of<kWindowed>(p, q, i + lane).steps() : 0;
-          int64_t incl = n;
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += x;
-          }
-          const uint32_t beyond = __ballot_sync(0xffffffffu, incl > skip);
-          if (beyond != 0 || i + 32 >= n_tiles) {  // the step lies within the head: some lane is beyond it
-            const int at = max(__ffs(beyond) - 1, 0);
-            skip -= __shfl_sync(0xffffffffu, incl - n, at);
-            i += at;
-            break;
-          }
-          skip -= __shfl_sync(0xffffffffu, incl, 31);
+      ChunkCut cut = {};
+      const int64_t P0 = u_lo - from;
+      if (from > 0) {
+        const int before = owner(u_lo - 1);  // the range before
+        if (start(before) <= P0) {
+          const Tile t = tile_of<kWindowed>(p, sq, at);
+          cut.pieces = rank_of(owner(P0 + t.steps() - 1)) - rank_of(before) + 1;
+          cut.slot0 = 2 * rank_of(before) + (start(before) < P0 ? 1 : 0);
+          cut.head = kv_head;
+          cut.row = sq.q0 + t.t0;
+          cut.n_tok = t.n_tok;
         }
-        first = static_cast<int>(skip);
-        // the tile that the range's start cuts, if no range before does
-        ChunkCut cut = {};
-        const int64_t P0 = u_lo - first;
-        if (first > 0) {
-          const int before = owner(u_lo - 1);  // the range before
-          if (start(before) <= P0) {
-            const Tile t = tile_of<kWindowed>(p, q, i);
-            cut.pieces = rank_of(owner(P0 + t.steps() - 1)) - rank_of(before) + 1;
-            cut.slot0 = 2 * rank_of(before) + (start(before) < P0 ? 1 : 0);
-            cut.head = head;
-            cut.row = q.q0 + t.t0;
-            cut.n_tok = t.n_tok;
-          }
-        }
-        if (lane == 0) p.cuts[rank] = cut;
       }
-      __syncwarp();
-      fence_proxy_async_smem();  // the copies overwrite the list
-    }
+      if (lane == 0) p.cuts[rank] = cut;
+    };
+    const Seq cut_q = q;
+    const int cut_tile = i, cut_head = head;
+    const bool in_a_range = left > 0;
     struct Work {  // a piece, as its copies need it
       Piece d;
       const int32_t *table;  // of its sequence
@@ -613,6 +614,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = sbase + kKOff + b * kTileBytes + lane * box_rows * 128;
           tma_load_3d(at, &k_map, bar(kBarK + b), 0, kv_head, row);
           tma_load_3d(at + kHalfBytes, &k_map, bar(kBarK + b), 64, kv_head, row);
+        }
+        if (g == 0) {
+          if (in_a_range) record_cut(cut_q, cut_tile, cut_head, first);
+          __syncwarp();
+          fence_proxy_async_smem();  // the copies of V overwrite the list
         }
         if (j == 0) {  // the next piece is known before the other warps are done with this one
           if (!(good = next_piece(next))) break;

@@ -109,6 +109,7 @@ cudaError_t decode_error_word(uint32_t **word);
 // ---------------------------------------------------------------- prefill
 struct PrefillArgs {
   const int32_t *cu_seqlens_q, *cu_seqlens_k;
+  const int32_t *context_lens = nullptr;  // without a window: in place of cu_seqlens_k
   const int32_t *block_tables;
   void *out;
   float *lse;

@@ -114,6 +114,7 @@ static_assert(kLazyBound == 256.0f && kLazyMax == 8.0f, "kLazyBound is 2^kLazyMa
 
 struct PrefillParams {
   const int32_t *cu_q, *cu_k, *block_tables;
+  const int32_t *lens;  // prefill_kernel: the sequences' keys in place of cu_k's, or null
   __nv_bfloat16 *out;
   float *lse;
   int32_t max_blocks, num_seqs, total_q, max_seqlen_q, max_seqlen_k;
@@ -315,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
 
   const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1];
-  const int Lq = q1 - q0, Lk = p.cu_k[s + 1] - p.cu_k[s];
+  const int Lq = q1 - q0, Lk = p.lens != nullptr ? p.lens[s] : p.cu_k[s + 1] - p.cu_k[s];
+  if (p.lens != nullptr && Lq == 0) return;  // its number of keys may be anything
   if (q0 < 0 || Lq < 0 || Lk < Lq || Lq > p.max_seqlen_q || Lk > p.max_seqlen_k ||
       q1 > p.total_q || (kBounded && Lq > 0 && beyond(p, s)) ||
       static_cast<int64_t>(Lk) > static_cast<int64_t>(p.max_blocks) * p.block_size) {
@@ -1357,6 +1359,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
   PrefillParams p;
   p.cu_q = a.cu_seqlens_q;
   p.cu_k = a.cu_seqlens_k;
+  p.lens = a.context_lens;
   p.block_tables = a.block_tables;
   p.out = static_cast<__nv_bfloat16 *>(a.out);
   p.lse = a.lse;

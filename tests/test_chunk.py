@@ -103,6 +103,27 @@ def test_shares_of_the_work(L, segments, Hq, H, window, sinks):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H", [(16, 8), (16, 16), (16, 4)])
+@pytest.mark.parametrize("bs", [16, 256])
+def test_long_chunks(L, Hq, H, bs):
+    # long enough that two row tiles pass a K/V tile; one segment is empty, its length nothing
+    keys, new = [1250, 1300, 0, 1501, 1280], [1250, 1153, 0, 1201, 1280]
+    b = Batch(keys, new, Hq, H, bs, 0, 0, seed=bs + H)
+    b.lens[2] = -7
+    b.check(*_run(b), rounded=True)
+    assert pkv.check_device_errors() == 0
+    # a length that is too short: refused by itself, its rows left as they were
+    b.lens[3] = 1200
+    out = torch.full_like(b.q, 7.0)
+    lse = torch.full((b.rows, Hq), 7.0, device=DEV)
+    _run(b, out=out, lse=lse)
+    assert pkv.check_device_errors() == pkv.DEVERR_SEQLENS
+    b.check(out, lse, rounded=True, skip=(3,))
+    rows = b.parts[3][0]
+    assert bool((out[rows] == 7).all()) and bool((lse[rows] == 7).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 1e-3, 2.0])
 def test_scales(L, scale):
     b = Batch([300, 90], [70, 4], 4, 2, 16, 100, 5, seed=2, scale=scale)
