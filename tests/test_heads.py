@@ -167,6 +167,7 @@ def _within(got, want_and_tol):
 @pytest.mark.parametrize("R,interleaved,norm,scaling", [(128, False, True, None), (128, True, False, "linear"),
                                                         (64, False, True, "yarn"), (96, True, True, "ntk"),
                                                         (8, False, False, None), (8, True, True, "yarn"),
+                                                        (40, False, True, "linear"), (104, False, False, None),
                                                         (0, False, True, None)])
 def test_norm_and_rotation(L, T, Hq, Hkv, R, interleaved, norm, scaling):
     (q, k, _), _ = _packed(T, Hq, Hkv, T + R)
@@ -263,6 +264,20 @@ def test_rows_of_zeros_nan_and_infinity_stay_their_own(L):
     fine = torch.isfinite(want)
     assert bool(((got.double().cpu() - want).abs()[fine] <= tol[fine]).all())
     assert not bool(torch.isfinite(got[3, 1, 7]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("R,interleaved", [(64, False), (40, False), (48, True), (72, True), (0, False)])
+def test_what_is_not_rotated_passes_as_it_is(L, R, interleaved):
+    (q, k, _), _ = _packed(5, 3, 1, 21)
+    q = q.clone()
+    q[..., R + (128 - R) // 2] = float("-inf")
+    q[1, 1, 127], q[2, 2, R] = float("nan"), -0.0
+    pos = torch.tensor([0, 1, 77, 4096, 100000], dtype=torch.int32, device=DEV)
+    got, _ = pkv.qk_norm_rope(q, k, pkv.rope(R, interleaved=interleaved), pos)
+    fine = torch.isnan(q[..., R:])
+    assert torch.equal(torch.isnan(got[..., R:]), fine)
+    assert torch.equal(_bits(got[..., R:])[~fine], _bits(q[..., R:])[~fine])
 
 
 def _cache(NB, bs, H):
