@@ -59,7 +59,7 @@ constexpr int kThreads = 384;
 constexpr int kMmaWarp = 1, kSoftmaxWarp0 = 4;
 constexpr int kDescs = 4;                   // pieces published ahead
 constexpr int kDescInts = 16;
-constexpr int kMaxWaves = 128;              // whole items a CTA, at most
+constexpr int kMaxWaves = 128;              // whole tiles a CTA, at most
 
 // barriers (8 bytes each): K and V landed, S complete (which frees its K), P written, P.V
 // complete (which frees its V), by the parity of the step; Q landed and free, by that of the
@@ -99,7 +99,9 @@ constexpr int kTilesOff = kStepsOff + 8 * (kChunkMaxSeqs + 2);            // int
 constexpr int kSeqOff = kTilesOff + 8 * (kChunkMaxSeqs + 2);              // Seq [S]
 constexpr int kShareOff = kSeqOff + static_cast<int>(sizeof(Seq)) * kChunkMaxSeqs;  // int64 [W + 1]: ranges' starts
 constexpr int kRankOff = kShareOff + 8 * (kChunkMaxCtas + 2);             // int [W + 1]: ranges before
-static_assert(kRankOff + 4 * (kChunkMaxCtas + 2) <= kEpiOff, "the list fits the V tiles");
+constexpr int kTotalOff = kRankOff + 4 * (kChunkMaxCtas + 2);             // int64 [warps]
+constexpr int kSumOff = kTotalOff + 8 * (kThreads / 32);                  // int [W]
+static_assert(kSumOff + 4 * kChunkMaxCtas <= kEpiOff && kTotalOff % 8 == 0, "the list fits the V tiles");
 static_assert(kChunkMaxCtas <= kThreads, "a thread for each CTA's share");
 
 constexpr uint32_t kTmemCols = 512;  // S (two), O: 128 columns each; a power of two
@@ -223,6 +225,8 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
   int64_t *starts = reinterpret_cast<int64_t *>(smem + kShareOff);
   int *ranks = reinterpret_cast<int *>(smem + kRankOff);
   Wave *list = reinterpret_cast<Wave *>(smem + kWaveOff);
+  int *sums = reinterpret_cast<int *>(smem + kSumOff);
+  int64_t *totals = reinterpret_cast<int64_t *>(smem + kTotalOff);
   const int lanes = 1 << p.lanes_log2, sub = tid & (lanes - 1);
   for (int base = 0; base < p.num_seqs; base += kThreads >> p.lanes_log2) {
     const int s = base + (tid >> p.lanes_log2);
@@ -264,18 +268,20 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
     return w;
   };
   // Whole tiles as far as no CTA gets more than its even share, and one more each is left
-  // to even out with.
-  int64_t mine = 0;  // thread c: steps of CTA c's whole tiles
+  // to even out with. (Fewer than 2^31 steps: at most kMaxWaves tiles of 2^23.)
+  int mine = 0;  // thread c: steps of CTA c's whole tiles
   for (r.waves = min(n_tiles / r.W - 1, kMaxWaves); r.waves > 0; r.waves >>= 1) {
-    mine = 0;
-    if (tid < r.W) {
-      int at = find(tiles, p.num_seqs, tid);
-      for (int w = 0; w < r.waves; ++w) {
-        const Wave x = locate(tid + w * r.W, at);
-        at = x.s;
-        mine += tile_of<kWindowed>(p, x.q, x.tile).steps();
-      }
+    if (tid < r.W) sums[tid] = 0;
+    __syncthreads();
+    int at = 0;
+    for (int i = tid; i < r.waves * r.W; i += kThreads) {
+      if (i == tid) at = find(tiles, p.num_seqs, tid);
+      const Wave x = locate(i, at);
+      at = x.s;
+      atomicAdd(&sums[i % r.W], tile_of<kWindowed>(p, x.q, x.tile).steps());
     }
+    __syncthreads();
+    mine = tid < r.W ? sums[tid] : 0;
     if (!__syncthreads_or(mine > r.even)) break;
   }
   if (r.waves <= 0) {
@@ -283,25 +289,32 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
     return r;
   }
   if (tid < r.waves) list[tid] = locate(cta + tid * r.W, find(tiles, p.num_seqs, cta + tid * r.W));
-  if (tid < r.W) starts[tid + 1] = r.even - mine;  // what CTA c may still take
-  __syncthreads();
-  if (warp == 0) {
-    // the whole tiles, all in front of the ranges, are `front` steps
-    scan(starts, r.W, lane);
-    const int64_t front = r.even * r.W - starts[r.W];
-    int before = 0;
-    for (int base = 0; base <= r.W; base += 32) {
-      const int c = base + lane;
-      const int64_t at = c <= r.W ? min(front + starts[c], U) : U;
-      const int64_t next = c < r.W ? min(front + starts[c + 1], U) : U;
-      const uint32_t some = __ballot_sync(0xffffffffu, next > at);
-      if (c <= r.W) ranks[c] = before + __popc(some & ((1u << lane) - 1));
-      before += __popc(some);
-      __syncwarp();
-      if (c <= r.W) starts[c] = at;
-      __syncwarp();
-    }
+  // the whole tiles are in front of the ranges, of which thread c's is what CTA c may still take
+  const int64_t rest = tid < r.W ? r.even - mine : 0;
+  int64_t before = rest;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += y;
   }
+  if (lane == 31) totals[warp] = before;
+  __syncthreads();
+  int64_t all = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += totals[w];
+    all += totals[w];
+  }
+  const int64_t front = r.even * r.W - all;
+  const int64_t start = min(front + before - rest, U), end = min(front + before, U);
+  const uint32_t some = __ballot_sync(0xffffffffu, tid < r.W && end > start);
+  if (lane == 0) sums[warp] = __popc(some);
+  if (tid < r.W) starts[tid] = start;
+  if (tid == r.W - 1) starts[r.W] = U;
+  __syncthreads();
+  int rank = __popc(some & ((1u << lane) - 1));
+  for (int w = 0; w < warp; ++w) rank += sums[w];
+  if (tid < r.W) ranks[tid] = rank;
+  if (tid == r.W - 1) ranks[r.W] = rank + (end > start ? 1 : 0);
   __syncthreads();
   r.front = 1;
   return r;
