@@ -975,8 +975,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // of the tile that the start of range k + 1 is the first to cut, a warp a row, four dims
 // a lane. Piece x > 0 is in slot 2 (range of piece 0 + x).
 constexpr int kJoinWarps = 4;
-constexpr int kJoinRows = 8;
-constexpr int kJoinLoads = 8;  // pieces whose outputs are in flight
+constexpr int kJoinRows = 4;
+// Pieces whose outputs are in flight: most tiles are cut once. With 4 and 8 the code for the
+// others costs more than their latency (23 ragged segments 66.0 and 67.7 us for 65.6; one tile
+// over every SM 37 and 33 for 35).
+constexpr int kJoinLoads = 2;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const ChunkParams p) {
   griddep_wait();
@@ -993,42 +996,38 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Chunk
       const int64_t slot = x == 0 ? cut.slot0 : 2 * (static_cast<int64_t>(cut.slot0 >> 1) + x);
       return slot * kRows + r;
     };
-    float M = kFloor;
-    for (int x = lane; x < cut.pieces; x += 32) M = fmaxf(M, p.ws_ml[at(x)].x);
+    float M = kFloor, l = 0.f, lr = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int base = 0; base < cut.pieces; base += kJoinLoads) {
+      float4 ml[kJoinLoads], o[kJoinLoads];
+      float top = M;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float l = 0.f, lr = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int base = 0; base < cut.pieces; base += 32) {
-      float f = 0.f;
-      if (base + lane < cut.pieces) {
-        const float4 ml = p.ws_ml[at(base + lane)];
-        f = fast_exp2(ml.x - M);
-        l = fmaf(ml.y, f, l);
-        lr = fmaf(ml.z, f, lr);
-      }
-      const int n = min(32, cut.pieces - base);
-      for (int x0 = 0; x0 < n; x0 += kJoinLoads) {
-        float4 o[kJoinLoads];
-#pragma unroll
-        for (int x = 0; x < kJoinLoads; ++x)
-          // of a piece without weight nothing is read: it may not have written its output
-          o[x] = __shfl_sync(0xffffffffu, f, (x0 + x) & 31) != 0.f && x0 + x < n
-                     ? reinterpret_cast<const float4 *>(p.ws_o + at(base + x0 + x) * kD)[lane]
-                     : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int x = 0; x < kJoinLoads; ++x) {
-          const float fx = __shfl_sync(0xffffffffu, f, (x0 + x) & 31);
-          acc[0] = fmaf(o[x].x, fx, acc[0]);
-          acc[1] = fmaf(o[x].y, fx, acc[1]);
-          acc[2] = fmaf(o[x].z, fx, acc[2]);
-          acc[3] = fmaf(o[x].w, fx, acc[3]);
+      for (int x = 0; x < kJoinLoads; ++x)
+        if (base + x < cut.pieces) {
+          ml[x] = p.ws_ml[at(base + x)];
+          o[x] = reinterpret_cast<const float4 *>(p.ws_o + at(base + x) * kD)[lane];
         }
-      }
-    }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, off);
-      lr += __shfl_xor_sync(0xffffffffu, lr, off);
+      for (int x = 0; x < kJoinLoads; ++x)
+        if (base + x < cut.pieces) top = fmaxf(top, ml[x].x);
+      auto add = [&](float f, float4 a, float b, float c) {
+        acc[0] = fmaf(a.x, f, acc[0]);
+        acc[1] = fmaf(a.y, f, acc[1]);
+        acc[2] = fmaf(a.z, f, acc[2]);
+        acc[3] = fmaf(a.w, f, acc[3]);
+        l = fmaf(b, f, l);
+        lr = fmaf(c, f, lr);
+      };
+      if (base > 0) {
+        const float f = fast_exp2(M - top);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] *= f;
+        l *= f;
+        lr *= f;
+      }
+      M = top;
+#pragma unroll
+      for (int x = 0; x < kJoinLoads; ++x)
+        if (base + x < cut.pieces) add(fast_exp2(ml[x].x - M), o[x], ml[x].y, ml[x].z);
     }
     const float inv = 1.f / lr;
     const int64_t row = static_cast<int64_t>(cut.row + (r >> p.gqa_log2)) * p.num_q_heads +
