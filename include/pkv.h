@@ -669,7 +669,8 @@ pkv_status pkv_rope_init_frequencies(pkv_rope *rope, int32_t rotary_dim, int32_t
  *   q_out, k_out  device bf16, written; strides as above, with rows that do not
  *              overlap (stride >= heads * 128). May be q and k themselves with
  *              their strides (in place); otherwise must not overlap an input.
- * num_tokens == 0 is a no-op; num_tokens * (H_q + H_kv) must be below 2^31.
+ * num_tokens == 0 is a no-op; num_tokens * (H_q + H_kv) must be below 2^31, and neither
+ * head count above 65535.
  */
 pkv_status pkv_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                             const void *q_weight, const void *k_weight, float eps,

@@ -36,6 +36,7 @@ pkv_status check_heads(const pkv::HeadsArgs &a, int32_t head_dim, int32_t kv_row
   if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q_weight) || !aligned16(a.k_weight) ||
       !aligned16(a.q_out) || !aligned16(a.k_out) || !aligned16(a.v_out))
     return PKV_ERR_INVALID_ARG;
+  if (a.num_q_heads > 65535 || a.num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
   const int64_t rows = static_cast<int64_t>(a.num_q_heads) + static_cast<int64_t>(kv_rows) * a.num_kv_heads;
   if (rows * a.num_tokens > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (a.num_tokens == 0 || rows == 0) {

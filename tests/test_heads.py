@@ -114,7 +114,8 @@ def test_calls_refuse(L, call):
     for kw in (dict(T=-1), dict(Hq=-1), dict(Hkv=-1), dict(eps=-1.0), dict(eps=float("nan")), dict(D=0),
                dict(rope=_rope_struct(magnitude=float("nan")))):
         assert call(L, **kw) == pkv.PKV_ERR_INVALID_ARG, kw
-    for kw in (dict(D=64), dict(rope=_rope_struct(12)), dict(rope=_rope_struct(136)), dict(T=1 << 30)):
+    for kw in (dict(D=64), dict(rope=_rope_struct(12)), dict(rope=_rope_struct(136)), dict(T=1 << 30),
+               dict(T=1, Hq=65536, qos=1 << 23), dict(T=1, Hkv=65536)):
         assert call(L, **kw) == pkv.PKV_ERR_UNSUPPORTED, kw
     assert call(L, T=0, q=None, k=None, pos=None, qo=None) == pkv.PKV_OK
 
