@@ -24,9 +24,11 @@
 // of the token's queries (or keys), so that a dim costs two products. No table of cosines is
 // read, whose rows would also be found only after the position has arrived.
 //
-// 32,768 tokens of 16 + 8 heads: 66 us, 6.1 TB/s, 91% of a plain copy's rate; with values,
-// norms and into the cache 89 us, 6.0 TB/s. 64 tokens 2.9 us, four 2.6, of which an empty
-// kernel takes about 2.
+// 32,768 tokens of 16 + 8 heads: 63 us, 6.35 TB/s, 95% of a plain copy's rate; with values,
+// norms and into the cache 86 us, 6.25 TB/s. 64 tokens 2.9 us, four 2.6, of which an empty
+// kernel takes about 2; 5,001 tokens of 12 rows 10.5 (floor 4.6): two tokens a warp, each some
+// 2 us of dependent instructions behind its position. (Weights read again for each token, from
+// the L1: 12.0.)
 #include <algorithm>
 
 #include "internal.h"
@@ -40,14 +42,10 @@ namespace {
 
 constexpr int kWarps = 4;
 // Blocks an SM, which the grid is limited to: 16 warps keep 64 KB of copies in flight. With 20
-// and 24 the registers run short: 32,768 tokens into the cache 94 and 104 us for 89.
+// and 24 the registers run short: 32,768 tokens into the cache 94 and 104 us where 16 took 89.
 constexpr int kBlocks = 4;
 constexpr int kRows = 4;    // rows a group
 constexpr int kStages = 4;  // groups whose copies a warp has in flight
-// Units an SM, at least, where tokens can be split. A unit computes its token's angles anew:
-// with 48, 5,001 tokens of 12 rows take 12.6 us for 12.0.
-constexpr int kWantUnits = 16;
-
 // How a lane's 16 dims lie in its row: pairs (i, i + R / 2) with R a multiple of 16, with R a
 // multiple of 8, and pairs (2 i, 2 i + 1).
 enum Layout { kHalf, kHalfNarrow, kInterleaved };
@@ -59,10 +57,11 @@ struct HeadsParams {
   const int32_t *positions, *slots;      // positions: null without a rotation; slots: null for k_out by token
   int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
   int64_t num_slots;
-  uint32_t num_units;              // parts of tokens, a warp each
+  uint32_t num_units;              // tokens, then parts of tokens, taken by the warps in turn
+  uint32_t whole;                  // the units that are tokens
   int32_t num_q, num_kv;           // heads
   int32_t k_group, v_group, num_groups;  // the first group of a token's keys, of its values; all
-  int32_t parts, part_groups;      // units a token, groups of each
+  int32_t parts, part_groups;      // units of each token behind those, groups of each
   int32_t rotary;
   float eps, magnitude;
   alignas(16) uint64_t turns[64];
@@ -73,10 +72,6 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool w
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void prefetch_l1(const void *at) {
-  asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
 }
 
 // Two bf16 values as fp32.
@@ -96,7 +91,8 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) heads_kernel(const __gri
   auto run = [&](int i) {
     if constexpr (kLayout == kInterleaved) return (i >> 1) * 64 + 8 * l + (i & 1) * 4;
     if constexpr (kLayout == kHalf)
-      return turned0 ? (i >> 1) * (p.rotary / 2) + 8 * l + (i & 1) * 4 : 16 * l + 4 * i;
+      return turned0 ? (i >> 1) * (p.rotary / 2) + 8 * l + (i & 1) * 4
+                     : p.rotary / 2 + (i >> 1) * (64 - p.rotary / 2) + 8 * l + (i & 1) * 4;
     return (i & 1 ? turned1 : turned0) ? (i >> 1) * (p.rotary / 2) + 8 * l + (i & 1) * 4
                                        : 16 * l + (i & 1) * 8 + (i >> 1) * 4;
   };
@@ -129,11 +125,14 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) heads_kernel(const __gri
     at.row = (at.group - (q ? 0 : k ? p.k_group : p.v_group)) * kRows + sub;
     at.rows = q ? p.num_q : p.num_kv;
   };
+  auto token_of = [&](uint32_t unit) {
+    return unit < p.whole || p.parts == 1 ? unit : p.whole + (unit - p.whole) / p.parts;
+  };
   auto enter = [&](At &at, uint32_t unit) {
     at.unit = unit;
-    at.token = p.parts == 1 ? unit : unit / p.parts;
-    at.group = (unit - at.token * p.parts) * p.part_groups;
-    at.last = min(at.group + p.part_groups, p.num_groups);
+    at.token = token_of(unit);
+    at.group = unit < p.whole ? 0 : (unit - p.whole - (at.token - p.whole) * p.parts) * p.part_groups;
+    at.last = unit < p.whole ? p.num_groups : min(at.group + p.part_groups, p.num_groups);
     enter_section(at);
   };
   At ahead = {};  // of the copies
@@ -173,14 +172,15 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) heads_kernel(const __gri
 
   At at;
   enter(at, unit0);
-  auto token_of = [&](uint32_t unit) {
-    unit = min(unit, p.num_units - 1);
-    return p.parts == 1 ? unit : unit / p.parts;
-  };
   int32_t next_slot = p.slots != nullptr ? p.slots[at.token] : 0;
   int32_t next_position = p.positions != nullptr ? p.positions[at.token] : 0;
-  if (p.q_weight != nullptr && sub == 0) prefetch_l1(p.q_weight + 16 * l);
-  if (p.k_weight != nullptr && sub == 1) prefetch_l1(p.k_weight + 16 * l);
+  uint2 wq[4] = {}, wk[4] = {};  // of the lane's dims
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at_run = i == 0 ? run0 : i == 1 ? run1 : i == 2 ? run2 : run3;
+    if (p.q_weight != nullptr) wq[i] = __ldg(reinterpret_cast<const uint2 *>(p.q_weight + at_run));
+    if (p.k_weight != nullptr) wk[i] = __ldg(reinterpret_cast<const uint2 *>(p.k_weight + at_run));
+  }
 #pragma unroll 1
   for (int i = 0; i < kStages; ++i) copy();
   int64_t slot = 0;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) heads_kernel(const __gri
     if (new_unit) {
       slot = next_slot;
       const int32_t position = next_position;
-      const uint32_t next = token_of(at.unit + stride);
+      const uint32_t next = token_of(min(at.unit + stride, p.num_units - 1));
       if (p.slots != nullptr) next_slot = p.slots[next];
       if (p.positions != nullptr) next_position = p.positions[next];
       if (slot < -1 || slot >= p.num_slots) {
@@ -222,15 +222,14 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks) heads_kernel(const __gri
       if (at.what > 0 && slot < 0) at.rows = 0;  // nothing is written
     }
     if (new_section && at.what < 2) {
-      const __nv_bfloat16 *weight = at.what == 0 ? p.q_weight : p.k_weight;
-      normed = weight != nullptr;
+      normed = (at.what == 0 ? p.q_weight : p.k_weight) != nullptr;
       float w[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) w[j] = 1.f;
       if (normed) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint2 u = __ldg(reinterpret_cast<const uint2 *>(weight + (i == 0 ? run0 : i == 1 ? run1 : i == 2 ? run2 : run3)));
+          const uint2 u = at.what == 0 ? wq[i] : wk[i];
           widen(u.x, w[4 * i], w[4 * i + 1]);
           widen(u.y, w[4 * i + 2], w[4 * i + 3]);
         }
@@ -337,15 +336,19 @@ cudaError_t launch_heads(const HeadsArgs &a, cudaStream_t stream) {
   p.eps = a.eps;
   p.magnitude = p.rotary > 0 ? a.rope->magnitude : 1.f;
   for (int i = 0; i < 64; ++i) p.turns[i] = p.rotary > 0 ? a.rope->turns[i] : 0;
-  // warps a token: one where there are tokens enough, more for few tokens
-  const int64_t want = kWantUnits * static_cast<int64_t>(a.num_sms);
+  // As many tokens as give every warp the same number are units; each of the tokens behind is
+  // split between as many warps as it has groups for and there are (of 5,001 tokens of 12 rows the
+  // last 137, between four warps each).
+  const int64_t warps = static_cast<int64_t>(kWarps * kBlocks) * a.num_sms;
+  p.whole = static_cast<uint32_t>(a.num_tokens / warps * warps);
+  const int64_t behind = a.num_tokens - p.whole;
   int32_t parts = 1;
-  while (parts < p.num_groups && static_cast<int64_t>(a.num_tokens) * parts < want) parts *= 2;
+  while (parts < p.num_groups && behind * parts * 2 <= warps) parts *= 2;
   p.part_groups = (p.num_groups + parts - 1) / parts;
   p.parts = (p.num_groups + p.part_groups - 1) / p.part_groups;
-  const int64_t units = static_cast<int64_t>(a.num_tokens) * p.parts;
-  p.num_units = static_cast<uint32_t>(units);
-  const int64_t blocks = std::min<int64_t>((units + kWarps - 1) / kWarps, kBlocks * static_cast<int64_t>(a.num_sms));
+  p.num_units = static_cast<uint32_t>(p.whole + behind * p.parts);
+  const int64_t blocks = std::min<int64_t>((static_cast<int64_t>(p.num_units) + kWarps - 1) / kWarps,
+                                           kBlocks * static_cast<int64_t>(a.num_sms));
   const auto kernel = p.rotary > 0 && a.rope->interleaved != 0 ? heads_kernel<kInterleaved>
                       : p.rotary % 16 == 0                     ? heads_kernel<kHalf>
                                                                : heads_kernel<kHalfNarrow>;
