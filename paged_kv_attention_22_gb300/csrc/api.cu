@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -723,7 +724,7 @@ pkv_status pkv_paged_chunk_attn(const void *q, const void *k_cache, const void *
   // keys take 450 us there and 536 here, 64 of 32 tokens over 736 keys 54 there and 45 here, two of
   // 16 over 32,768 keys 362 there and 55 here.
   const int64_t tiles = (static_cast<int64_t>(max_seqlen_q) + 127) / 128 * num_q_heads / 2;  // two an item
-  if (a.window == 0 && scale > 0.f && 2 * tiles >= sms && tiles * num_seqs <= pkv::kMaxPrefillItems &&
+  if (a.window == 0 && a.scale_log2 >= FLT_MIN && 2 * tiles >= sms && tiles * num_seqs <= pkv::kMaxPrefillItems &&
       4 * static_cast<int64_t>(total_q) >= 3 * static_cast<int64_t>(num_seqs) * max_seqlen_q) {
     pkv::PrefillArgs f;
     f.cu_seqlens_q = cu_seqlens_q;
