@@ -3,8 +3,8 @@
 The functions here have the names of the C entry points in ``include/pkv.h``
 and do argument marshalling only: they check dtypes and shapes of torch
 tensors, pass their device pointers and the current CUDA stream to the C ABI,
-and allocate outputs the caller did not supply. (For 4-bit caches, eviction and
-the calls on queries and keys before attention the checks are compiled, in the module
+and allocate outputs the caller did not supply. (For 4-bit caches, eviction, queries
+and keys before attention, sinks and chunks the checks are compiled, in the module
 ``_marshal`` beside the library, which only those calls load; they also want every
 tensor on the current device.) Every step of the computation
 runs in the library's CUDA kernels. There is no fallback: if libpkv.so has not

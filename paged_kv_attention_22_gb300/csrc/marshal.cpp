@@ -1,5 +1,6 @@
 // Argument marshalling of the Python binding for the calls on 4-bit caches, of
-// eviction, on queries and keys before attention, with sinks and on chunks: checks torch tensors (type, dtype, shape, device, layout), takes
+// eviction, on queries and keys before attention, with sinks and on chunks: checks
+// torch tensors (type, dtype, shape, device, layout), takes
 // their pointers and the current CUDA stream, and calls the C entries of
 // include/pkv.h. It computes nothing; a call costs about a microsecond here
 // where checks in Python cost ten to twenty, several times the launch itself.
