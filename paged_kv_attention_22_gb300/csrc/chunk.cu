@@ -786,8 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int lim = 0;  // last key this row sees
     uint32_t x[64];  // the thread's logits of the step
     // Reads those of the piece's step j, step h of the CTA, masked as -inf once scaled, and
-    // offers their maximum to the other half's warp. Blocks of 32 columns that every row of
-    // the warp sees are left alone.
+    // offers their maximum to the other half's warp.
     auto logits = [&](int j, int h) -> bool {
       const int b = h & 1;
       if (!__all_sync(0xffffffffu, wait_(bar(kBarS + b), (h >> 1) & 1, abort))) return false;
@@ -796,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tS, reinterpret_cast<uint32_t(&)[32]>(x[0]));
       tmem_ld32(tS + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
       const int k0 = d.key_tile(j) * kKeys + half * 64;  // the thread's first key
-      bool some = k0 + 63 > d.pos + tok0;
+      bool some = k0 + 63 > d.pos + tok0;  // some key is masked for some row of the warp
       if constexpr (kWindowed)  // the largest first key of the warp's rows
         some = some || (k0 <= d.pos + tok0 + (31 >> p.gqa_log2) - p.window && k0 + 64 > p.sinks);
       tmem_wait_ld();
