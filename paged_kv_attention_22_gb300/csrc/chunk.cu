@@ -50,6 +50,7 @@
 // probabilities, the weights that the products used; the lse comes from the fp32 sum.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -985,10 +986,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // a lane. Piece x > 0 is in slot 2 (range of piece 0 + x).
 constexpr int kJoinWarps = 4;
 constexpr int kJoinRows = 4;
-// Pieces whose outputs are in flight: most tiles are cut once. With 4 and 8 the code for the
-// others costs more than their latency (23 ragged segments 66.0 and 67.7 us for 65.6; one tile
-// over every SM 37 and 33 for 35).
-constexpr int kJoinLoads = 2;
+// Pieces whose outputs are in flight, where there are more than two (most tiles are cut once). 20
+// rows over 32,000 keys, one tile over every SM, take 25 us in all, with 4 of them 34; with 16
+// registers run short where there are many rows (23 ragged segments 71 us for 66). Few rows
+// split between a CTA's warps: 19 and 54 us on that tile and the two documents, here 25 and 52.
+constexpr int kJoinLoads = 8;
 
 __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const ChunkParams p) {
   griddep_wait();
@@ -1001,43 +1003,49 @@ __global__ void __launch_bounds__(kJoinWarps * 32) chunk_join_kernel(const Chunk
   const int rows = min(cut.n_tok << p.gqa_log2, kJoinRows * (static_cast<int>(blockIdx.y) + 1));
   if (cut.pieces == 0) return;
   for (int r = kJoinRows * blockIdx.y + warp; r < rows; r += kJoinWarps) {
-    auto at = [&](int x) {
-      const int64_t slot = x == 0 ? cut.slot0 : 2 * (static_cast<int64_t>(cut.slot0 >> 1) + x);
-      return slot * kRows + r;
-    };
+    // piece x > 0 is 2 x slots behind the even slot of piece 0's range
+    const int64_t even = static_cast<int64_t>(cut.slot0 & ~1) * kRows + r;
+    const float4 *ml0 = p.ws_ml + even, *o0 = reinterpret_cast<const float4 *>(p.ws_o + even * kD) + lane;
+    auto rows_on = [&](int x) { return x == 0 ? (cut.slot0 & 1) * kRows : 2 * x * kRows; };
     float M = kFloor, l = 0.f, lr = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int base = 0; base < cut.pieces; base += kJoinLoads) {
-      float4 ml[kJoinLoads], o[kJoinLoads];
+    // pieces base .. base + kLoads - 1, the loads of all in flight; past the last, that one
+    // again with no weight
+    auto join = [&](auto loads, int base) {
+      constexpr int kLoads = decltype(loads)::value;
+      float4 ml[kLoads], o[kLoads];
       float top = M;
 #pragma unroll
-      for (int x = 0; x < kJoinLoads; ++x)
-        if (base + x < cut.pieces) {
-          ml[x] = p.ws_ml[at(base + x)];
-          o[x] = reinterpret_cast<const float4 *>(p.ws_o + at(base + x) * kD)[lane];
-        }
-#pragma unroll
-      for (int x = 0; x < kJoinLoads; ++x)
-        if (base + x < cut.pieces) top = fmaxf(top, ml[x].x);
-      auto add = [&](float f, float4 a, float b, float c) {
-        acc[0] = fmaf(a.x, f, acc[0]);
-        acc[1] = fmaf(a.y, f, acc[1]);
-        acc[2] = fmaf(a.z, f, acc[2]);
-        acc[3] = fmaf(a.w, f, acc[3]);
-        l = fmaf(b, f, l);
-        lr = fmaf(c, f, lr);
-      };
-      if (base > 0) {
-        const float f = fast_exp2(M - top);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] *= f;
-        l *= f;
-        lr *= f;
+      for (int x = 0; x < kLoads; ++x) {
+        const int i = rows_on(min(base + x, cut.pieces - 1));
+        ml[x] = ml0[i];
+        o[x] = o0[i * (kD / 4)];
       }
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x) {
+        if (base + x >= cut.pieces) ml[x].x = -INFINITY;
+        top = fmaxf(top, ml[x].x);
+      }
+      const float old = fast_exp2(M - top);
       M = top;
 #pragma unroll
-      for (int x = 0; x < kJoinLoads; ++x)
-        if (base + x < cut.pieces) add(fast_exp2(ml[x].x - M), o[x], ml[x].y, ml[x].z);
-    }
+      for (int i = 0; i < 4; ++i) acc[i] *= old;
+      l *= old;
+      lr *= old;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x) {
+        const float f = fast_exp2(ml[x].x - M);
+        acc[0] = fmaf(o[x].x, f, acc[0]);
+        acc[1] = fmaf(o[x].y, f, acc[1]);
+        acc[2] = fmaf(o[x].z, f, acc[2]);
+        acc[3] = fmaf(o[x].w, f, acc[3]);
+        l = fmaf(ml[x].y, f, l);
+        lr = fmaf(ml[x].z, f, lr);
+      }
+    };
+    if (cut.pieces <= 2)
+      join(std::integral_constant<int, 2>{}, 0);
+    else
+      for (int base = 0; base < cut.pieces; base += kJoinLoads) join(std::integral_constant<int, kJoinLoads>{}, base);
     const float inv = 1.f / lr;
     const int64_t row = static_cast<int64_t>(cut.row + (r >> p.gqa_log2)) * p.num_q_heads +
                         (static_cast<int64_t>(cut.head) << p.gqa_log2) + (r & ((1 << p.gqa_log2) - 1));
