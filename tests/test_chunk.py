@@ -108,14 +108,17 @@ def test_shares_of_the_work(L, segments, Hq, H, window, sinks):
 def test_long_chunks(L, Hq, H, bs):
     # long enough that two row tiles pass a K/V tile; one segment is empty, its length nothing
     keys, new = [1250, 1300, 0, 1501, 1280], [1250, 1153, 0, 1201, 1280]
-    b = Batch(keys, new, Hq, H, bs, 0, 0, seed=bs + H)
+    b = Batch(keys, new, Hq, H, bs, 0, 0, seed=bs + H, extra_rows=40)
     b.lens[2] = -7
-    b.check(*_run(b), rounded=True)
+    out, lse = torch.full_like(b.q, 7.0), torch.full((b.q.shape[0], Hq), 7.0, device=DEV)
+    _run(b, out=out, lse=lse)
+    b.check(out, lse, rounded=True)
+    assert bool((out[b.rows:] == 7).all()) and bool((lse[b.rows:] == 7).all())
+    assert torch.equal(_run(b, with_lse=False)[0][:b.rows], out[:b.rows])
     assert pkv.check_device_errors() == 0
     # a length that is too short: refused by itself, its rows left as they were
     b.lens[3] = 1200
-    out = torch.full_like(b.q, 7.0)
-    lse = torch.full((b.rows, Hq), 7.0, device=DEV)
+    out, lse = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
     _run(b, out=out, lse=lse)
     assert pkv.check_device_errors() == pkv.DEVERR_SEQLENS
     b.check(out, lse, rounded=True, skip=(3,))
