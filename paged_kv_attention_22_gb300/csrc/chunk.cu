@@ -144,13 +144,14 @@ __device__ __forceinline__ bool wait_(uint32_t bar, uint32_t parity, const volat
   return mbar_wait(bar, parity, &g_chunk_errors, abort);
 }
 
-__device__ __forceinline__ Seq load_seq(const ChunkParams &p, int s, bool raise) {
+// Segment s, without rows if it is invalid, which sets `bad`.
+__device__ __forceinline__ Seq load_seq(const ChunkParams &p, int s, bool &bad) {
   const int q0 = p.cu_q[s], q1 = p.cu_q[s + 1], ctx = p.lens[s];
   Seq r = {q0, q1 - q0, ctx};
   if (q0 == q1) return r;
   if (q0 < 0 || q1 < q0 || q1 > p.total_q || r.Lq > p.max_seqlen_q || ctx < r.Lq || ctx > p.max_context_len ||
       ctx > static_cast<int64_t>(p.max_blocks) * p.block.d) {
-    if (raise) atomicOr(&g_chunk_errors, kErrSeqlens);
+    bad = true;
     r.Lq = 0;
   }
   return r;
@@ -226,9 +227,9 @@ struct Shares {
 };
 
 // Builds the list and the shares; the whole CTA. Afterwards this CTA's whole tiles are in
-// shared memory.
+// shared memory. No work if some thread says `skip`.
 template <bool kWindowed>
-__device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
+__device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem, bool skip) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   int64_t *steps = reinterpret_cast<int64_t *>(smem + kStepsOff);
   int64_t *tiles = reinterpret_cast<int64_t *>(smem + kTilesOff);
@@ -239,11 +240,12 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
   int *sums = reinterpret_cast<int *>(smem + kSumOff);
   int64_t *totals = reinterpret_cast<int64_t *>(smem + kTotalOff);
   const int lanes = 1 << p.lanes_log2, sub = tid & (lanes - 1);
+  bool bad = false;
   for (int base = 0; base < p.num_seqs; base += kThreads >> p.lanes_log2) {
     const int s = base + (tid >> p.lanes_log2);
     int64_t n = 0;
     if (s < p.num_seqs) {
-      const Seq q = load_seq(p, s, cta == 0 && sub == 0);
+      const Seq q = load_seq(p, s, bad);
       const int n_tiles = tiles_of(p, q);
       for (int i = sub; i < n_tiles; i += lanes) n += tile_of<kWindowed>(p, q, i).steps();
       if (sub == 0) {
@@ -254,7 +256,8 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem) {
     for (int off = lanes >> 1; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
     if (s < p.num_seqs && sub == 0) steps[s + 1] = n * p.num_kv_heads;
   }
-  __syncthreads();
+  if (__syncthreads_or(skip)) return Shares{};
+  if (bad && cta == 0 && sub == 0) atomicOr(&g_chunk_errors, kErrSeqlens);
   if (warp == 0) scan(steps, p.num_seqs, lane);
   if (warp == 1 && p.shared_keys) scan(tiles, p.num_seqs, lane);
   __syncthreads();
@@ -421,13 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   // a CTA gave up waiting (in this or an earlier launch): skip the work until the
   // error word is read and cleared; decided once per CTA
-  const bool skipped =
-      __syncthreads_or(tid == 0 && (*reinterpret_cast<volatile uint32_t *>(&g_chunk_errors) & kErrTimeout));
+  const Shares shares = build<kWindowed>(
+      p, smem, tid == 0 && (*reinterpret_cast<volatile uint32_t *>(&g_chunk_errors) & kErrTimeout));
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + kMiscOff);
   const int cta = blockIdx.x;
-  Shares shares = {};
-  if (!skipped) shares = build<kWindowed>(p, smem);
   const bool works = cta < shares.W;
   const int *ranks = reinterpret_cast<const int *>(smem + kRankOff);
   // ranges that no CTA has cut nothing
@@ -524,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             i = 0;
             if (++head == p.num_kv_heads) {
               head = 0;
-              do q = load_seq(p, ++s, false);  // steps are left, so a sequence has them
+              bool bad;
+              do q = load_seq(p, ++s, bad);  // steps are left, so a sequence has them
               while (q.Lq == 0);
               n_tiles = tiles_of(p, q);
             }
