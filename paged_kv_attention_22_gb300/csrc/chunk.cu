@@ -100,11 +100,13 @@ constexpr int kEpiOff = kVOff + 2 * kTileBytes;  // staging areas of the softmax
 constexpr int kBarOff = kEpiOff + 8 * kEpiWarpBytes;
 constexpr int kDescOff = kBarOff + (kNumBars * 8 + 15) / 16 * 16;
 constexpr int kMiscOff = kDescOff + kDescs * kDescInts * 4;  // TMEM address, abort flag, unseen rows of the V tiles
-constexpr int kSwapOff = kMiscOff + 16;                      // float [6][2][128] by half: maxima of two steps, two sums of two pieces
+constexpr int kAllOff = kMiscOff + 16;                       // int64: all steps, all tiles
+constexpr int kSwapOff = kAllOff + 16;                       // float [6][2][128] by half: maxima of two steps, two sums of two pieces
 constexpr int kWaveOff = kSwapOff + 6 * 2 * kRows * 4;       // Wave [kMaxWaves]
 constexpr int kSmemBytes = kWaveOff + kMaxWaves * static_cast<int>(sizeof(Wave)) + 1024;  // + slack for alignment
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
-// until the first copies, in the place of the V tiles: the list of sequences
+// until the first copies, in the place of the V tiles: the list of sequences. The producer's copy
+// of V(0) waits for no other warp, so behind build()'s last barrier only the producer reads here.
 constexpr int kStepsOff = kVOff;                                          // int64 [S + 1]: steps before
 constexpr int kTilesOff = kStepsOff + 8 * (kChunkMaxSeqs + 2);            // int64 [S + 1]: tiles before
 constexpr int kSeqOff = kTilesOff + 8 * (kChunkMaxSeqs + 2);              // Seq [S]
@@ -200,8 +202,8 @@ __device__ __forceinline__ int find(const int64_t *before, int n, int64_t x) {
   return lo;
 }
 
-// Inclusive prefix sums of a[1 .. n] in place, a[0] = 0; one warp.
-__device__ __forceinline__ void scan(int64_t *a, int n, int lane) {
+// Inclusive prefix sums of a[1 .. n] in place, a[0] = 0, and the last of them; one warp.
+__device__ __forceinline__ int64_t scan(int64_t *a, int n, int lane) {
   int64_t carry = 0;
   for (int base = 0; base < n; base += 32) {
     const int i = base + lane;
@@ -215,6 +217,7 @@ __device__ __forceinline__ void scan(int64_t *a, int n, int lane) {
     carry += __shfl_sync(0xffffffffu, x, 31);
   }
   if (lane == 0) a[0] = 0;
+  return carry;
 }
 
 // What the whole call comes to, as every thread knows it. Without whole tiles (front == 0)
@@ -239,6 +242,7 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem, boo
   Wave *list = reinterpret_cast<Wave *>(smem + kWaveOff);
   int *sums = reinterpret_cast<int *>(smem + kSumOff);
   int64_t *totals = reinterpret_cast<int64_t *>(smem + kTotalOff);
+  volatile int64_t *all_of = reinterpret_cast<volatile int64_t *>(smem + kAllOff);
   const int lanes = 1 << p.lanes_log2, sub = tid & (lanes - 1);
   bool bad = false;
   for (int base = 0; base < p.num_seqs; base += kThreads >> p.lanes_log2) {
@@ -258,10 +262,14 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem, boo
   }
   if (__syncthreads_or(skip)) return Shares{};
   if (bad && cta == 0 && sub == 0) atomicOr(&g_chunk_errors, kErrSeqlens);
-  if (warp == 0) scan(steps, p.num_seqs, lane);
-  if (warp == 1 && p.shared_keys) scan(tiles, p.num_seqs, lane);
+  if (warp == 0 || (warp == 1 && p.shared_keys)) {
+    const int64_t all = scan(warp == 0 ? steps : tiles, p.num_seqs, lane);
+    if (lane == 0) all_of[warp] = all;
+  }
   __syncthreads();
-  const int64_t U = steps[p.num_seqs];
+  // The ways out that pass no other barrier read no more of the list than this: a late warp may
+  // be here when V(0) lands there.
+  const int64_t U = all_of[0];
   Shares r;
   r.U = U;
   r.W = static_cast<int>(min(static_cast<int64_t>(gridDim.x), U));
@@ -270,7 +278,7 @@ __device__ __forceinline__ Shares build(const ChunkParams &p, uint8_t *smem, boo
   if (r.W == 0 || !p.shared_keys) return r;
   // Tile i of the list (the rows of q are fewer than 2^31, so are the tiles), found from
   // a sequence at or before it.
-  const int n_tiles = static_cast<int>(tiles[p.num_seqs]);
+  const int n_tiles = static_cast<int>(all_of[1]);
   auto locate = [&](int i, int from) {
     Wave w;
     w.s = from;
