@@ -905,6 +905,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ended = any;
       if (d.steps == 0) break;
       if (!any) {
+        tc_fence_before();  // finish() may have read O, which this piece's first P.V overwrites
+        __syncwarp();
         for (int j = 0; j < d.steps && good; ++j, ++g) {
           good = __all_sync(0xffffffffu, wait_(bar(kBarS + (g & 1)), (g >> 1) & 1, abort));
           if (lane == 0) mbar_arrive(bar(kBarP + (g & 1)));

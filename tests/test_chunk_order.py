@@ -73,6 +73,32 @@ def test_behind_the_list_only_the_producer_reads_it():
     assert reads and "tid == 0 && cta >=" in between[:reads[0]]  # of the producer's warp
 
 
+def test_what_was_read_from_tmem_is_ordered_before_the_next_product():
+    # A softmax warp's arrival on kBarP lets the MMA warp issue the P.V that overwrites O, and the S
+    # that overwrites the logits: between the warp's last access to TMEM (finish() reads O) and the
+    # arrival stands tcgen05.fence::before_thread_sync.
+    text = _source()
+    kernel = text[slice(*_block(text, "chunk_kernel(const __grid_constant__"))]
+    softmax = kernel[slice(*_block(kernel, "else if (warp >= kSoftmaxWarp0 && works)"))]
+    arrivals = [m.start() for m in re.finditer(r"mbar_arrive\(bar\(kBarP ", softmax)]
+    assert len(arrivals) == 2
+    for at in arrivals:
+        last = [m.end() for m in re.finditer(r"\b(tmem_\w+|finish|logits)\(", softmax[:at])][-1]
+        assert "tc_fence_before();" in softmax[last:at], softmax[last:at]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,H", [(1, 1), (4, 2)])
+def test_few_tokens_behind_a_full_tile(L, Hq, H):
+    # a CTA's softmax warps that have no row of the next tile still write the last one's output
+    segments = [(200, 128 * H // Hq), (40, 2), (300, 1)] * 150
+    keys, new = map(list, zip(*segments))
+    b = Batch(keys, new, Hq, H, 16, 0, 0, seed=23)
+    out, lse = pkv.paged_chunk_attn(b.q, b.kc, b.vc, b.cu, b.lens, b.bt, max(new), max(keys), b.scale)
+    b.check(out, lse, rounded=True)
+    assert pkv.check_device_errors() == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("segments,Hq,H,window,sinks", [
     ([(640, 5)] * 64, 16, 8, 0, 0),                         # one tile a sequence: no list of tiles
