@@ -332,16 +332,26 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
  * context_lens[s] positions, whose rows are in the cache (store them first). Query i,
  * at position p_i = context_lens[s] - Lq + i, sees the keys
  *   p <= p_i,  and with a window  p > p_i - sliding_window  or  p < num_sinks.
- * Output and lse as in decode, for every query row. A pkv_paged_prefill_attn with
- * context lengths in place of cu_seqlens_k, whose keys are shared out over all SMs
- * whatever the lengths, and joined by a second kernel.
+ * Output and lse as in decode, for every query row, but for the weights: as in prefill
+ * they are rounded to bf16 for the tensor cores, and the output is divided by the sum of
+ * the rounded ones (the lse is not), which leaves it within 2^-7 of the weighted mean of
+ * |v|. A batch of single tokens alone keeps fp32 weights in pkv_paged_decode_attn[_sinks].
+ * A pkv_paged_prefill_attn with context lengths in place of cu_seqlens_k, whose keys are
+ * shared out over all SMs and joined by a second kernel. Only a call without a window whose
+ * total_q and max_seqlen_q say that its segments are long and about as long as each other
+ * runs as prefill does, each 128 rows of two heads passing their keys on one SM. These host
+ * values choose, not the lengths on the device: a graph captured with wide bounds and
+ * replayed with a few tokens over long contexts stays there, at several times the chunk
+ * kernel's time. Capture such replays on their own, with tight bounds.
  *   q, out       device bf16 [total_q, num_q_heads, head_dim]
  *   lse          device float32 [total_q, num_q_heads], or NULL
  *   cu_seqlens_q device int32 [num_seqs + 1], non-decreasing, from 0; rows of q and
  *                out past its last value are not touched
  *   context_lens device int32 [num_seqs]; not looked at where Lq == 0
- *   max_seqlen_q, max_context_len  host ints: upper bounds, the latter at most 2^30
- *   workspace    device, >= pkv_chunk_workspace_size(...) bytes, 16-byte aligned
+ *   max_seqlen_q, max_context_len  host ints: upper bounds, the latter at most 2^30, the
+ *                former at most the latter (else PKV_ERR_INVALID_ARG)
+ *   workspace    device, >= pkv_chunk_workspace_size(...) bytes, 16-byte aligned; needs
+ *                no initialisation; calls that share one must be ordered (same stream)
  * num_seqs is at most 1024. Blocks with no key that a query of the segment sees are not
  * read (their entries may be -1), and keys that none sees may hold anything; keys that
  * some query of a segment sees must be finite, or that segment's rows may all be

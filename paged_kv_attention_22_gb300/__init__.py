@@ -638,7 +638,9 @@ def paged_chunk_attn(q, k_cache, v_cache, cu_seqlens_q, context_lens, block_tabl
                      stream=None, with_lse=True):
     """Attention of each sequence's last cu_seqlens_q[s + 1] - cu_seqlens_q[s] positions (their rows
     stored before) over its context_lens[s] keys in the paged cache, causal; with a window each query sees
-    the last sliding_window keys up to its own and the first num_sinks. Returns (out, lse)."""
+    the last sliding_window keys up to its own and the first num_sinks. Weights are rounded to bf16, as in
+    prefill (decode keeps them in fp32). The bounds choose between two kernels: pkv.h says how, and why a
+    graph that is replayed for short segments wants tight ones. Returns (out, lse)."""
     if out is None or workspace is None or (lse is None and with_lse):
         with _on(stream):
             out, lse = _decode_outputs(q, out, lse, with_lse)
