@@ -68,10 +68,11 @@ pkv_status pkv_rope_init_frequencies(pkv_rope *rope, int32_t rotary_dim, int32_t
   r.magnitude = magnitude;
   for (int32_t i = 0; i < rotary_dim / 2; ++i) {
     if (!std::isfinite(frequencies[i])) return PKV_ERR_INVALID_ARG;
-    const double turns = frequencies[i] / (2 * kPi);
-    // the fraction is below 1 but for the rounding of a tiny negative number
-    const double part = std::ldexp(turns - std::floor(turns), 64);
-    r.turns[i] = part < 0x1p64 ? static_cast<uint64_t>(part) : 0;
+    // The fraction of the size is exact; that of a small negative number would be a number
+    // near 1, rounded by 2^-54 of a turn. Negated as an integer, modulo 2^64.
+    const double turns = std::fabs(frequencies[i]) / (2 * kPi);
+    const uint64_t part = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));
+    r.turns[i] = std::signbit(frequencies[i]) ? 0 - part : part;
   }
   *rope = r;
   return PKV_OK;
