@@ -622,8 +622,11 @@ pkv_status pkv_evict_compact_q4(void *k_codes, void *k_params, void *v_codes, vo
  *   y = w x / sqrt(mean(x^2) + eps),
  *   (y_a, y_b) -> magnitude (y_a cos t - y_b sin t, y_b cos t + y_a sin t)
  * for the pairs (a, b) of the first rotary_dim dims and the angle t = position
- * * frequency of the pair; the other dims stay y. Computed in fp32, with the
- * angle exact to 2^-32 of a turn at any position, and rounded once, to bf16.
+ * * frequency of the pair; the other dims stay y. Computed in fp32 and rounded
+ * once, to bf16. (Sums of squares are fp32 too: values beyond some 2^60 overflow
+ * them, and their row comes out as zeros.) The angle is off by some 2^-26 of a turn,
+ * as fp32 holds it modulo a turn, whatever the position, and by |position| * frequency
+ * * 2^-54 of a turn, as 64 bits hold the frequency.
  */
 
 /*

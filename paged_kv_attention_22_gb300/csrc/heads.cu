@@ -16,10 +16,11 @@
 // which keeps enough bytes in flight without registers for them.
 //
 // The angle is taken in turns, modulo 1, in 64-bit integers: position times the
-// pair's 64-bit fraction of a turn wraps to the fraction of the angle exactly (to
-// 2^-64 of a turn a position), where fp32 angles of far positions have no digits
-// left, and without the 64-bit floating point that this GPU hardly has. Its top 32
-// bits go to sincospi. A lane computes two of a token's 64 and fetches those of its
+// pair's 64-bit fraction of a turn wraps to the fraction of the angle without a
+// rounding, where fp32 angles of far positions have no digits left, and without the
+// 64-bit floating point that this GPU hardly has. Its top 32 bits go to sincospi as fp32,
+// 2^-26 of a turn off at most; the fraction itself, from a 64-bit frequency, is off by
+// 2^-54 of the frequency a position. A lane computes two of a token's 64 and fetches those of its
 // pairs from the others; with the weights they make four factors a pair, the same for all
 // of the token's queries (or keys), so that a dim costs two products. No table of cosines is
 // read, whose rows would also be found only after the position has arrived.
