@@ -50,10 +50,12 @@
  * invalid value are undefined; nothing outside the given buffers is touched.
  *
  * Timeouts are sticky. Every wait inside a kernel is bounded; a kernel that
- * gives up raises PKV_DEVERR_TIMEOUT. From then on every later decode call
- * (fused store included) and prefill call on that device returns PKV_OK but
+ * gives up raises PKV_DEVERR_TIMEOUT. From then on every later call on that
+ * device that runs the kernel that gave up - bf16 decode (fused store, sinks and
+ * accumulated weights included), prefill, or chunks - returns PKV_OK but
  * skips all its work, leaving its outputs (and, for the fused call, the cache)
- * untouched, until the word is cleared by pkv_check_device_errors. An engine
+ * untouched, until the word is cleared by pkv_check_device_errors. (The bit
+ * raised by pkv_raise_device_errors stops all of them.) An engine
  * that runs these calls inside CUDA graphs and never synchronises should
  * append pkv_read_device_errors_async to its step and act on the bit.
  */
@@ -359,7 +361,7 @@ pkv_status pkv_paged_prefill_attn(const void *q, const void *k_cache, const void
  * total_q, or context_lens[s] above max_context_len or past the table raise
  * PKV_DEVERR_SEQLENS and are not written; an invalid table entry raises
  * PKV_DEVERR_BLOCK and makes its segment's rows undefined. After a PKV_DEVERR_TIMEOUT
- * the call does nothing, as the decode and prefill calls.
+ * of the kernel that it runs (see above) the call does nothing.
  */
 size_t pkv_chunk_workspace_size(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                 int32_t head_dim);
