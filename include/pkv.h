@@ -31,7 +31,8 @@
  * Memory and ownership. Every pointer is caller-owned device memory (except
  * the host pointer flags_out); the library allocates and frees nothing, keeps
  * no per-call state, and returns before the kernels finish. Device buffers
- * must be 16-byte aligned.
+ * must be 16-byte aligned. What a call writes (outputs, workspace) must not
+ * overlap its inputs or itself, except where the call says that it may.
  *
  * Streams. `stream` is a cudaStream_t passed as void* (NULL = the legacy
  * default stream). Every call only enqueues work on that stream and never
